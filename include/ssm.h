@@ -15,6 +15,8 @@
  *   ssd_chunked_bwd  gradient of ssd_chunked_fwd, tensor cores
  *   ssd_mamba3_bwd   gradient of ssd_mamba3_fwd (Mamba-3 SISO)
  *   ssd_mamba3_mimo_bwd  gradient of ssd_mamba3_mimo_fwd (Mamba-3 MIMO)
+ *   ssm_add_rmsnorm_fwd, _e4m3_fwd, _bwd  RMS norm with the residual's addition
+ *   ssm_linrec_fwd, _bwd  gated linear recurrence, one state per channel
  *
  * Conventions shared by every entry point
  *  - Pointers are DEVICE pointers unless stated otherwise, to dense row-major
@@ -731,16 +733,142 @@ ssm_status_t ssm_scan_fwd_host(const void* u, const void* delta, const float* A,
                                size_t workspace_bytes, void* stream);
 
 /*
+ * RMS norm with the residual's addition.
+ *   The pages run the mixer inside a residual block (pre-norm, mixer, residual
+ *   sum; "Mamba-3 NKI Kernels for AWS Neuron", section "How it works", norms B
+ *   and C the same way).  Per row, in fp32:
+ *     s = x + residual          (s = x where residual is NULL)
+ *     y = s / sqrt(mean(s^2) + eps) * weight
+ *   sum_out = s (rounded to res_dtype; the norm itself takes the unrounded s).
+ * Layouts: x, residual, y, sum_out (rows, dim); weight (dim,) fp32.
+ *   x in in_dtype, residual and sum_out in res_dtype, y in out_dtype.
+ * residual and sum_out may be NULL; sum_out may be residual itself (the
+ * residual stream updated in place).  A row of NaN gives NaN; rows == 0 does
+ * nothing.
+ * Supported: 1 <= dim <= 16384; any rows; res_dtype in_dtype or SSM_F32.
+ * Rows move in 16-byte units where dim is a multiple of 8.
+ */
+ssm_status_t ssm_add_rmsnorm_fwd(const void* x, const void* residual, const float* weight,
+                                 float eps, void* y, void* sum_out, int rows, int dim,
+                                 ssm_dtype_t in_dtype, ssm_dtype_t res_dtype,
+                                 ssm_dtype_t out_dtype, void* stream);
+
+/*
+ * The same norm with an 8-bit output: for each group of `group` consecutive
+ * values of a row's y (the last one may be shorter; group 0: the whole row),
+ *   amax = max |y|,  scale = amax / 448,  q = e4m3(y * (448 / amax))
+ * rounded to nearest even (q = 0 where amax is 0), so that y = q * scale to
+ * e4m3's 3 mantissa bits.
+ * Layouts: q (rows, dim) bytes holding e4m3 values; scales (rows, ceil(dim /
+ * group)) fp32 (rows, 1 for group 0); the rest as ssm_add_rmsnorm_fwd.
+ * Supported: group 0, 32, 64, 128 or 256; else as ssm_add_rmsnorm_fwd.
+ */
+ssm_status_t ssm_add_rmsnorm_e4m3_fwd(const void* x, const void* residual, const float* weight,
+                                      float eps, int group, void* q, float* scales,
+                                      void* sum_out, int rows, int dim, ssm_dtype_t in_dtype,
+                                      ssm_dtype_t res_dtype, void* stream);
+
+/* Bytes of device workspace ssm_add_rmsnorm_bwd needs (0 for invalid sizes). */
+size_t ssm_add_rmsnorm_bwd_workspace_bytes(int rows, int dim);
+
+/*
+ * Gradient of ssm_add_rmsnorm_fwd for the loss sum(dy * y) + sum(dsum *
+ * sum_out), taken at the kept sum: with n = sum / sqrt(mean(sum^2) + eps) and
+ * g = dy * weight,
+ *   d = (g - n mean(g n)) / sqrt(mean(sum^2) + eps) + dsum
+ *   dx = d (in_dtype),  dresidual = d (res_dtype),  dweight = sum over rows of dy n
+ * sum (rows, dim) is sum_out (or x, where there was no residual) in res_dtype;
+ * dy (rows, dim) in dy_dtype (y's type); dsum in res_dtype or NULL (0); dx or
+ * dresidual may be NULL, not both; dweight (dim,) fp32 is always written (0 for
+ * rows == 0).  The sums over rows are taken in a fixed order.
+ */
+ssm_status_t ssm_add_rmsnorm_bwd(const void* sum, const float* weight, float eps, const void* dy,
+                                 const void* dsum, void* dx, void* dresidual, float* dweight,
+                                 int rows, int dim, ssm_dtype_t in_dtype, ssm_dtype_t res_dtype,
+                                 ssm_dtype_t dy_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Bytes of the states ssm_linrec_fwd keeps for ssm_linrec_bwd: one fp32 state
+ * per channel every 64 steps, (ceil(seqlen / 64), batch, dim).
+ */
+size_t ssm_linrec_checkpoint_bytes(int batch, int seqlen, int dim);
+
+/* Bytes of device workspace ssm_linrec_fwd needs (0 for invalid sizes). */
+size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim);
+
+/*
+ * Gated linear recurrence, one state per channel.
+ *   The scan of ssm_scan_fwd with a scalar state whose decay is given directly
+ *   and whose input weight is its complement ("We brought Mamba to Trainium --
+ *   and mapped where custom kernels actually help", section "Mamba: bringing an
+ *   unsupported model to the chip, and writing its missing kernel": h_t = A_t
+ *   h_{t-1} + B_t x_t).  For every batch b, step t and channel d, in fp32:
+ *     a = sigmoid(f[b,t,d]);  h = a h + (1 - a) x[b,t,d]
+ *     y[b,t,d] = h * silu(z[b,t,d])        (y = h where z is NULL)
+ *   from h = initial_state[b,d] (or 0); final_state[b,d] = h after the last step.
+ * Masked steps: where f is +inf the state is held and x is not looked at (it
+ * may be NaN); where f is -inf (any f < -87) the state starts anew at x,
+ * whatever it was.
+ * Layouts: f, x, z (batch, seqlen, dim) in in_dtype with dim contiguous and
+ *   *_stride elements from one step to the next (the batches follow one
+ *   another: seqlen * stride apart), so that the three may be column ranges of
+ *   one projection; y (batch, seqlen, dim) in out_dtype; initial_state,
+ *   final_state (batch, dim) fp32, each may be NULL, and may be the same
+ *   buffer (a decode step updates its state in place with seqlen == 1);
+ *   checkpoints: NULL, or ssm_linrec_checkpoint_bytes for ssm_linrec_bwd.
+ * f, x and z need only the alignment of their element; rows whose addresses are
+ * multiples of 16 bytes move fastest.
+ * Supported: any batch, seqlen, dim >= 0 with batch * ceil(dim / 64) *
+ * ceil(seqlen / 64) < 2e9.  seqlen == 0 hands the state on.
+ * The sequence is cut into tiles chained by a decoupled look-back in the
+ * workspace (sequences of up to 16 steps are walked by one thread per channel
+ * pair); its bounded waits report through ssm_last_device_status.  The result
+ * does not depend on timing: runs are bit-equal.
+ */
+ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void* z, long long f_stride,
+                            long long x_stride, long long z_stride, const float* initial_state,
+                            void* y, float* final_state, float* checkpoints, int batch,
+                            int seqlen, int dim, ssm_dtype_t in_dtype, ssm_dtype_t out_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace ssm_linrec_bwd needs (0 for invalid sizes). */
+size_t ssm_linrec_bwd_workspace_bytes(int batch, int seqlen, int dim);
+
+/*
+ * Gradient of ssm_linrec_fwd for the loss sum(dy * y) + sum(dfinal_state *
+ * final_state): with mu_t the adjoint of h_{t-1}, backwards in time from
+ * dfinal_state (or 0),
+ *   lam_t = dy_t silu(z_t) + mu_{t+1};  mu_t = a_t lam_t
+ *   df_t = lam_t (h_{t-1} - x_t) a_t (1 - a_t);  dx_t = lam_t (1 - a_t)
+ *   dz_t = dy_t h_t silu'(z_t);  dinitial_state = mu at the first step
+ * f, x, z and their strides, initial_state as given to the forward; dy (batch,
+ * seqlen, dim) in in_dtype; df, dx, dz (batch, seqlen, dim) in grad_dtype (dz
+ * required with z, else not written); dfinal_state, dinitial_state (batch, dim)
+ * fp32, each may be NULL, and may be the same buffer; checkpoints: what the
+ * forward kept for the same inputs, or NULL (the forward recurrence is run
+ * again for its states).  The gradients of a step whose gate is infinite are 0
+ * (df, and dx where the state is held).
+ */
+ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void* z, long long f_stride,
+                            long long x_stride, long long z_stride, const float* initial_state,
+                            const void* dy, const float* dfinal_state, const float* checkpoints,
+                            void* df, void* dx, void* dz, float* dinitial_state, int batch,
+                            int seqlen, int dim, ssm_dtype_t in_dtype, ssm_dtype_t grad_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Waits for `stream` to drain, then returns the device-side status the last
- * ssm_scan_fwd that used `workspace` recorded (SSM_OK or SSM_ERR_TIMEOUT),
+ * ssm_scan_fwd (or ssm_linrec_fwd, _bwd) that used `workspace` recorded (SSM_OK or SSM_ERR_TIMEOUT),
  * or SSM_ERR_CUDA if the stream itself reports an error.
  */
 ssm_status_t ssm_last_device_status(const void* workspace, void* stream);
 
 /*
  * Test hook for the scan's bounded look-back waits (every entry point that
- * runs a scan kernel: ssm_scan_fwd, _ckpt, _noalloc, _host and the forward
- * inside ssm_scan_bwd).  The chained scan cuts the sequence into chunks when
+ * runs a scan kernel: ssm_scan_fwd, _ckpt, _noalloc, _host, the forward
+ * inside ssm_scan_bwd, and ssm_linrec_fwd and _bwd, whose tiles look back the
+ * same way).  The chained scan cuts the sequence into chunks when
  * the channel blocks outnumber the resident CTA slots, and chunk c of a block
  * polls the flag chunk c-1 publishes with its final state.  The
  * sequence-parallel scan always cuts it into 128-step chunks, and chunk c

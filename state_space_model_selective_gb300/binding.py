@@ -9,6 +9,7 @@ kernels.  There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -35,7 +36,10 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssd_chunked_checkpoint_bytes", "ssd_chunked_fwd_ckpt", "ssd_mamba3_bwd_workspace_bytes",
            "ssd_mamba3_bwd", "ssd_mamba3_mimo_bwd_workspace_bytes", "ssd_mamba3_mimo_bwd",
            "ssd_mamba3_fwd_ckpt", "ssd_mamba3_mimo_fwd_ckpt", "ssm_debug_set_lookback",
-           "ssm_debug_set_scan_path", "ssm_noalloc_last_status", "ssm_mamba3_rope"]
+           "ssm_debug_set_scan_path", "ssm_noalloc_last_status", "ssm_mamba3_rope",
+           "ssm_add_rmsnorm_fwd", "ssm_add_rmsnorm_e4m3_fwd", "ssm_add_rmsnorm_bwd_workspace_bytes",
+           "ssm_add_rmsnorm_bwd", "ssm_linrec_checkpoint_bytes", "ssm_linrec_workspace_bytes",
+           "ssm_linrec_fwd", "ssm_linrec_bwd_workspace_bytes", "ssm_linrec_bwd"]
 
 
 class SSMError(RuntimeError):
@@ -120,6 +124,23 @@ def lib() -> ctypes.CDLL:
         L.ssm_noalloc_last_status.argtypes = [vp]
         L.ssm_mamba3_rope.restype = i
         L.ssm_mamba3_rope.argtypes = [vp] * 8 + [i] * 7 + [vp]
+        ll, fl = ctypes.c_longlong, ctypes.c_float
+        L.ssm_add_rmsnorm_fwd.restype = i
+        L.ssm_add_rmsnorm_fwd.argtypes = [vp] * 3 + [fl] + [vp] * 2 + [i] * 5 + [vp]
+        L.ssm_add_rmsnorm_e4m3_fwd.restype = i
+        L.ssm_add_rmsnorm_e4m3_fwd.argtypes = [vp] * 3 + [fl, i] + [vp] * 3 + [i] * 4 + [vp]
+        L.ssm_add_rmsnorm_bwd_workspace_bytes.restype = sz
+        L.ssm_add_rmsnorm_bwd_workspace_bytes.argtypes = [i] * 2
+        L.ssm_add_rmsnorm_bwd.restype = i
+        L.ssm_add_rmsnorm_bwd.argtypes = [vp] * 2 + [fl] + [vp] * 5 + [i] * 5 + [vp, sz, vp]
+        for f in (L.ssm_linrec_checkpoint_bytes, L.ssm_linrec_workspace_bytes,
+                  L.ssm_linrec_bwd_workspace_bytes):
+            f.restype = sz
+            f.argtypes = [i] * 3
+        L.ssm_linrec_fwd.restype = i
+        L.ssm_linrec_fwd.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 4 + [i] * 5 + [vp, sz, vp]
+        L.ssm_linrec_bwd.restype = i
+        L.ssm_linrec_bwd.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 8 + [i] * 5 + [vp, sz, vp]
         _lib = L
     return _lib
 
@@ -951,3 +972,283 @@ def ssm_decode_step_mamba3_mimo(state, prev_B, prev_x, x, dt, lam, A, B, C, D=No
                                            headdim, dstate, ngroups, _DT[dt_], _stream(stream))
     _check(st, "ssm_decode_step_mamba3_mimo")
     return y
+
+
+# ---------------------------------------------------- norm, recurrence, loss
+#
+# Tensors a call allocates for itself (outputs, workspaces) belong to the
+# stream the call runs on, so that their memory is not handed out again before
+# the kernels there are done with it.
+
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _like(t, name, ref, dtype):
+    """Checks a given output against the tensor it has to be shaped like."""
+    _req(t, name, dtype)
+    _shape(t, name, ref)
+    return t
+
+
+def _norm_args(x, weight, residual):
+    _req(x, "x")
+    if x.dim() < 1 or x.dtype not in _DT:
+        raise TypeError("x must be a float32 or bfloat16 tensor of at least one dimension")
+    dim = x.shape[-1]
+    _req(weight, "weight", torch.float32)
+    _shape(weight, "weight", (dim,))
+    if residual is not None:
+        _req(residual, "residual")
+        _shape(residual, "residual", x.shape)
+        if residual.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"residual must be {x.dtype} or float32, got {residual.dtype}")
+    return x.numel() // dim if dim else 0, dim
+
+
+def ssm_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, sum_dtype=None, y=None,
+                        sum_out=None, return_sum=True, stream=None):
+    """RMS norm of x + residual over the last dimension.  x, residual: (..., dim);
+    weight: (dim,) fp32.  The sum is kept in ``sum_dtype`` (the residual's type, or
+    x's; float32 where the residual stream is kept in 32 bits).  ``sum_out`` may be
+    ``residual`` itself.  Returns (y, sum); sum is None with ``return_sum`` false
+    and no ``sum_out``."""
+    rows, dim = _norm_args(x, weight, residual)
+    out_dt = x.dtype if out_dtype is None else out_dtype
+    res_dt = _sum_dtype(x, residual, sum_dtype, sum_out)
+    with _on(stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dt, device=x.device)
+        if sum_out is None and return_sum:
+            sum_out = torch.empty(x.shape, dtype=res_dt, device=x.device)
+    _like(y, "y", x.shape, out_dt)
+    if sum_out is not None:
+        _like(sum_out, "sum_out", x.shape, res_dt)
+    st = lib().ssm_add_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(y),
+                                   _ptr(sum_out), rows, dim, _DT[x.dtype], _DT[res_dt],
+                                   _dt_code(out_dt, "out_dtype"), _stream(stream))
+    _check(st, "ssm_add_rmsnorm_fwd")
+    return y, sum_out
+
+
+def _dt_code(dt, name):
+    if dt not in _DT:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dt}")
+    return _DT[dt]
+
+
+def _sum_dtype(x, residual, sum_dtype, sum_out):
+    """The type the residual stream is kept in: the residual's where there is one."""
+    dt = (residual.dtype if residual is not None else
+          sum_out.dtype if sum_out is not None else
+          x.dtype if sum_dtype is None else sum_dtype)
+    if sum_dtype is not None and dt != sum_dtype:
+        raise TypeError(f"sum_dtype must be the residual's type {dt}, got {sum_dtype}")
+    if dt not in (x.dtype, torch.float32):
+        raise TypeError(f"the sum must be {x.dtype} or float32, got {dt}")
+    return dt
+
+
+def ssm_add_rmsnorm_e4m3_fwd(x, weight, residual=None, eps=1e-5, group=128, sum_dtype=None, q=None,
+                             scales=None, sum_out=None, return_sum=True, stream=None):
+    """ssm_add_rmsnorm_fwd with y in 8 bits: q (float8_e4m3fn, like x) and fp32
+    scales (..., ceil(dim / group)) with y = q * scale of its ``group`` of 32, 64, 128 or
+    256 consecutive values (group 0: one scale a row).  Returns (q, scales, sum)."""
+    rows, dim = _norm_args(x, weight, residual)
+    res_dt = _sum_dtype(x, residual, sum_dtype, sum_out)
+    group = int(group)
+    if group not in (0, 32, 64, 128, 256):
+        raise SSMError(5, "ssm_add_rmsnorm_e4m3_fwd")
+    sshape = tuple(x.shape[:-1]) + (1 if group == 0 else -(-dim // group),)
+    with _on(stream):
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
+        if sum_out is None and return_sum:
+            sum_out = torch.empty(x.shape, dtype=res_dt, device=x.device)
+    _like(q, "q", x.shape, torch.float8_e4m3fn)
+    _like(scales, "scales", sshape, torch.float32)
+    if sum_out is not None:
+        _like(sum_out, "sum_out", x.shape, res_dt)
+    st = lib().ssm_add_rmsnorm_e4m3_fwd(_ptr(x), _ptr(residual), _ptr(weight), float(eps), group,
+                                        _ptr(q), _ptr(scales), _ptr(sum_out), rows, dim,
+                                        _DT[x.dtype], _DT[res_dt], _stream(stream))
+    _check(st, "ssm_add_rmsnorm_e4m3_fwd")
+    return q, scales, sum_out
+
+
+def ssm_add_rmsnorm_bwd_workspace_bytes(rows, dim) -> int:
+    return int(lib().ssm_add_rmsnorm_bwd_workspace_bytes(rows, dim))
+
+
+def ssm_add_rmsnorm_bwd(dy, sum, weight, dsum=None, eps=1e-5, x_dtype=None, dx=None,
+                        dresidual=None, dweight=None, workspace=None, stream=None):
+    """Gradient of ``ssm_add_rmsnorm_fwd`` at the sum it returned.  dy: like y; dsum: the
+    gradient arriving at the sum itself, in its type, or None.  ``x_dtype``: the type of
+    x's gradient (dy's where the sum is fp32, else the sum's).  Returns a dict: dx,
+    dresidual (the same values in the sum's type; the same tensor as dx where the types
+    agree) and dweight (fp32)."""
+    _req(sum, "sum")
+    if sum.dim() < 1 or sum.dtype not in _DT:
+        raise TypeError("sum must be a float32 or bfloat16 tensor of at least one dimension")
+    dim = sum.shape[-1]
+    rows = sum.numel() // dim if dim else 0
+    _req(weight, "weight", torch.float32)
+    _shape(weight, "weight", (dim,))
+    _req(dy, "dy")
+    _shape(dy, "dy", sum.shape)
+    if dsum is not None:
+        _like(dsum, "dsum", sum.shape, sum.dtype)
+    dx_dt = x_dtype or (dx.dtype if dx is not None else
+                        dy.dtype if sum.dtype == torch.float32 else sum.dtype)
+    same = dx_dt == sum.dtype
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty(sum.shape, dtype=dx_dt, device=sum.device)
+        if dresidual is None and not same:
+            dresidual = torch.empty(sum.shape, dtype=sum.dtype, device=sum.device)
+        if dweight is None:
+            dweight = torch.empty(dim, dtype=torch.float32, device=sum.device)
+        if workspace is None:
+            need = ssm_add_rmsnorm_bwd_workspace_bytes(rows, dim)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=sum.device)
+    _like(dx, "dx", sum.shape, dx_dt)
+    if dresidual is not None:
+        _like(dresidual, "dresidual", sum.shape, sum.dtype)
+    _like(dweight, "dweight", (dim,), torch.float32)
+    _req(workspace, "workspace", torch.uint8)
+    st = lib().ssm_add_rmsnorm_bwd(_ptr(sum), _ptr(weight), float(eps), _ptr(dy), _ptr(dsum),
+                                   _ptr(dx), _ptr(dresidual), _ptr(dweight), rows, dim,
+                                   _dt_code(dx_dt, "x_dtype"), _DT[sum.dtype],
+                                   _dt_code(dy.dtype, "dy"), _ptr(workspace), workspace.numel(),
+                                   _stream(stream))
+    _check(st, "ssm_add_rmsnorm_bwd")
+    return {"dx": dx, "dresidual": dx if dresidual is None else dresidual, "dweight": dweight}
+
+
+def ssm_linrec_checkpoint_bytes(batch, seqlen, dim) -> int:
+    return int(lib().ssm_linrec_checkpoint_bytes(batch, seqlen, dim))
+
+
+def ssm_linrec_workspace_bytes(batch, seqlen, dim) -> int:
+    return int(lib().ssm_linrec_workspace_bytes(batch, seqlen, dim))
+
+
+def ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim) -> int:
+    return int(lib().ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim))
+
+
+def _steps(t, name, dtype, shape):
+    """Elements between the steps of a (batch, seqlen, dim) tensor whose channels are
+    contiguous and whose batches follow one another: a contiguous tensor, or a range
+    of the last dimension of one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    batch, seqlen, dim = shape
+    sb, st, sd = t.stride()
+    # a dimension of one element may carry any stride
+    step = st if seqlen > 1 else sb if batch > 1 else dim
+    if ((dim > 1 and sd != 1) or step < dim or
+            (batch > 1 and seqlen > 1 and sb != seqlen * st)):
+        raise ValueError(f"{name} must be contiguous, or a range of the last dimension of a "
+                         f"contiguous tensor")
+    return step
+
+
+def _linrec_args(f, x, z, initial_state):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DT:
+        raise TypeError("x must be a float32 or bfloat16 tensor")
+    if x.dim() != 3:
+        raise ValueError(f"x must have 3 dims, got {x.dim()}")
+    sx = _steps(x, "x", x.dtype, x.shape)
+    sf = _steps(f, "f", x.dtype, x.shape)
+    sz = 0 if z is None else _steps(z, "z", x.dtype, x.shape)
+    batch, seqlen, dim = x.shape
+    if initial_state is not None:
+        _like(initial_state, "initial_state", (batch, dim), torch.float32)
+    return sf, sx, sz
+
+
+def ssm_linrec_fwd(f, x, z=None, initial_state=None, out_dtype=None, y=None, final_state=None,
+                   checkpoints=None, workspace=None, return_final_state=True, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(f), and
+    y = h * silu(z) (y = h without z).  f, x, z: (batch, seqlen, dim), each contiguous or a
+    range of the last dimension of a contiguous tensor; initial_state, final_state:
+    (batch, dim) fp32, which may be the same tensor (a decode step in place).  With
+    ``checkpoints`` (a CUDA fp32 tensor of ssm_linrec_checkpoint_bytes bytes) the states
+    ssm_linrec_bwd needs are kept.  Returns (y, final_state)."""
+    sf, sx, sz = _linrec_args(f, x, z, initial_state)
+    batch, seqlen, dim = x.shape
+    out_dt = x.dtype if out_dtype is None else out_dtype
+    with _on(stream):
+        if y is None:
+            y = torch.empty((batch, seqlen, dim), dtype=out_dt, device=x.device)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((batch, dim), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            need = ssm_linrec_workspace_bytes(batch, seqlen, dim)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    _like(y, "y", (batch, seqlen, dim), out_dt)
+    if final_state is not None:
+        _like(final_state, "final_state", (batch, dim), torch.float32)
+    _req(workspace, "workspace", torch.uint8)
+    _kept(checkpoints, batch, seqlen, dim)
+    st = lib().ssm_linrec_fwd(_ptr(f), _ptr(x), _ptr(z), sf, sx, sz, _ptr(initial_state), _ptr(y),
+                              _ptr(final_state), _ptr(checkpoints), batch, seqlen, dim,
+                              _DT[x.dtype], _dt_code(out_dt, "out_dtype"), _ptr(workspace),
+                              workspace.numel(), _stream(stream))
+    _check(st, "ssm_linrec_fwd")
+    return y, final_state
+
+
+def _kept(checkpoints, batch, seqlen, dim):
+    if checkpoints is not None:
+        _req(checkpoints, "checkpoints", torch.float32)
+        if checkpoints.numel() * 4 < ssm_linrec_checkpoint_bytes(batch, seqlen, dim):
+            raise ValueError("checkpoints is smaller than ssm_linrec_checkpoint_bytes(...)")
+
+
+def ssm_linrec_bwd(f, x, dy, z=None, initial_state=None, dfinal_state=None, checkpoints=None,
+                   grad_dtype=None, workspace=None, want_dinitial_state=True, stream=None,
+                   out=None):
+    """Gradient of ``ssm_linrec_fwd`` for the loss sum(dy * y) + sum(dfinal_state *
+    final_state).  Inputs as for the forward; dy like x and contiguous; checkpoints: what
+    the forward kept, or None (its recurrence is run again).  Returns a dict: df, dx, dz
+    (None without z) in ``grad_dtype`` (x's type by default), dinitial_state fp32 (or
+    None).  ``out`` may map any of these names to a preallocated tensor to write."""
+    sf, sx, sz = _linrec_args(f, x, z, initial_state)
+    batch, seqlen, dim = x.shape
+    _like(dy, "dy", x.shape, x.dtype)
+    if dfinal_state is not None:
+        _like(dfinal_state, "dfinal_state", (batch, dim), torch.float32)
+    _kept(checkpoints, batch, seqlen, dim)
+    gd = x.dtype if grad_dtype is None else grad_dtype
+    names = ["df", "dx"] + ([] if z is None else ["dz"])
+    if want_dinitial_state or (out and "dinitial_state" in out):
+        names.append("dinitial_state")
+    g = dict.fromkeys(("df", "dx", "dz", "dinitial_state"))
+    out = out or {}
+    for k in out:
+        if k not in names:
+            raise ValueError(f"out[{k!r}] is not an output of this call")
+    with _on(stream):
+        for k in names:
+            shape, dt = ((batch, dim), torch.float32) if k == "dinitial_state" else (x.shape, gd)
+            g[k] = (torch.empty(shape, dtype=dt, device=x.device) if k not in out else
+                    _like(out[k], f"out[{k!r}]", shape, dt))
+        if workspace is None:
+            need = ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    _req(workspace, "workspace", torch.uint8)
+    st = lib().ssm_linrec_bwd(_ptr(f), _ptr(x), _ptr(z), sf, sx, sz, _ptr(initial_state), _ptr(dy),
+                              _ptr(dfinal_state), _ptr(checkpoints), _ptr(g["df"]), _ptr(g["dx"]),
+                              _ptr(g["dz"]), _ptr(g["dinitial_state"]), batch, seqlen, dim,
+                              _DT[x.dtype], _dt_code(gd, "grad_dtype"), _ptr(workspace),
+                              workspace.numel(), _stream(stream))
+    _check(st, "ssm_linrec_bwd")
+    return g

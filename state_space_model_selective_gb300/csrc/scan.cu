@@ -1206,6 +1206,12 @@ extern "C" ssm_status_t ssm_debug_set_scan_path(int path, int segments) {
     return SSM_OK;
 }
 
+void ssm_internal::lookback_setting(uint32_t* spin_limit, int* drop_first_publish) {
+    const uint32_t limit = g_flag_spin_limit.load(std::memory_order_relaxed);
+    *spin_limit = limit ? limit : ssm::kFlagSpinLimit;
+    *drop_first_publish = g_drop_first_publish.load(std::memory_order_relaxed);
+}
+
 extern "C" ssm_status_t ssm_debug_set_lookback(int drop_first_publish, unsigned int spin_limit) {
     g_flag_spin_limit.store(spin_limit, std::memory_order_relaxed);
     g_drop_first_publish.store(drop_first_publish ? 1 : 0, std::memory_order_relaxed);

@@ -74,6 +74,11 @@ ssm_status_t scan_seg_forward(const void* u, const void* delta, const float* A, 
                               int drop_first_publish, int ts, bool keep_status,
                               cudaStream_t stream);
 
+// The settings of ssm_debug_set_lookback, for every kernel that looks back:
+// polls before a wait gives up (the default resolved) and whether the first
+// chunk withholds its publish.
+void lookback_setting(uint32_t* spin_limit, int* drop_first_publish);
+
 // Test hook: force the segments per chunk (8, 16 or 32; 0 = planned).
 void scan_seg_debug_force_ts(int ts);
 
