@@ -17,6 +17,7 @@
  *   ssd_mamba3_mimo_bwd  gradient of ssd_mamba3_mimo_fwd (Mamba-3 MIMO)
  *   ssm_add_rmsnorm_fwd, _e4m3_fwd, _bwd  RMS norm with the residual's addition
  *   ssm_linrec_fwd, _bwd  gated linear recurrence, one state per channel
+ *   ssm_vocab_ce_fwd, _bwd  cross entropy over a vocabulary without the logits
  *
  * Conventions shared by every entry point
  *  - Pointers are DEVICE pointers unless stated otherwise, to dense row-major
@@ -858,8 +859,56 @@ ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void* z, long lo
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Bytes of device workspace ssm_vocab_ce_fwd needs (0 for sizes it does not
+ * take): a maximum and a sum per token and 128 columns of the vocabulary.
+ */
+size_t ssm_vocab_ce_workspace_bytes(int tokens, int dim, int vocab);
+
+/*
+ * Softmax cross entropy of the logits h W^T over a vocabulary, the logits
+ * never in memory.
+ *   The loss of the language models the pages' mixers run in (their heads are
+ *   out of the pages' scope).  Per token t, in fp32 from exact bf16 products:
+ *     lse[t]  = log sum_v exp(h[t,:] . W[v,:])
+ *     loss[t] = lse[t] - h[t,:] . W[targets[t],:]
+ * A token whose target is negative (-100, say) carries no loss: loss[t] = 0,
+ * lse[t] as for any.  A target of vocab or more gives loss[t] = NaN.
+ * Layouts: h (tokens, dim), W (vocab, dim) in in_dtype; targets (tokens,) 64-bit
+ * integers; loss, lse (tokens,) fp32; workspace of ssm_vocab_ce_workspace_bytes,
+ * whose status ssm_last_device_status reads.
+ * Supported: in_dtype SSM_BF16; dim a multiple of 8; any tokens >= 0, vocab >= 1
+ * (tokens * vocab below 6e13).  Runs are bit-equal.
+ */
+ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const long long* targets, float* loss,
+                              float* lse, int tokens, int dim, int vocab, ssm_dtype_t in_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of device workspace ssm_vocab_ce_bwd needs (0 for sizes it does not
+ * take): P of one piece of the vocabulary in bf16 (256 MB, or 4096 columns where
+ * those are more) and the fp32 sums of dh.
+ */
+size_t ssm_vocab_ce_bwd_workspace_bytes(int tokens, int dim, int vocab);
+
+/*
+ * Gradient of ssm_vocab_ce_fwd for the loss sum(dloss * loss):
+ *   P[t,v] = (exp(h[t,:] . W[v,:] - lse[t]) - [v == targets[t]]) dloss[t]
+ *   dh = P W  (tokens, dim),  dW = P^T h  (vocab, dim), both in grad_dtype
+ * lse is what the forward gave for the same h and W; dloss (tokens,) fp32 (the
+ * mean over n tokens that count: 1 / n).  A token without a target in [0,
+ * vocab) has P = 0; its h still has to be finite.  The vocabulary is taken in
+ * pieces: the logits of a piece again, P of the piece rounded to bf16, and its
+ * part of both products, summed in fp32.  tokens == 0 writes dW = 0.
+ * Supported as ssm_vocab_ce_fwd; grad_dtype either type.  Runs are bit-equal.
+ */
+ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const long long* targets,
+                              const float* lse, const float* dloss, void* dh, void* dW, int tokens,
+                              int dim, int vocab, ssm_dtype_t in_dtype, ssm_dtype_t grad_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Waits for `stream` to drain, then returns the device-side status the last
- * ssm_scan_fwd (or ssm_linrec_fwd, _bwd) that used `workspace` recorded (SSM_OK or SSM_ERR_TIMEOUT),
+ * ssm_scan_fwd (or ssm_linrec or ssm_vocab_ce call) that used `workspace` recorded (SSM_OK or SSM_ERR_TIMEOUT),
  * or SSM_ERR_CUDA if the stream itself reports an error.
  */
 ssm_status_t ssm_last_device_status(const void* workspace, void* stream);

@@ -7,7 +7,8 @@ Entry points (same names as in ``include/ssm.h``): ``ssm_scan_fwd``,
 ``ssm_scan_workspace_bytes``, ``ssm_scan_bwd_workspace_bytes``,
 ``ssm_last_device_status``; around the mixers: ``ssm_add_rmsnorm_fwd``,
 ``ssm_add_rmsnorm_e4m3_fwd``, ``ssm_add_rmsnorm_bwd`` (RMS norm with the residual's
-addition), ``ssm_linrec_fwd``, ``ssm_linrec_bwd`` (gated linear recurrence).  The library is loaded on first call; building it is
+addition), ``ssm_linrec_fwd``, ``ssm_linrec_bwd`` (gated linear recurrence), ``ssm_vocab_ce_fwd``,
+``ssm_vocab_ce_bwd`` (cross entropy over a vocabulary).  The library is loaded on first call; building it is
 ``state_space_model_selective_gb300.build.build()``.
 """
 from .binding import (EXPORTS, SSMError, lib, ssd_chunked_bwd,  # noqa: F401
@@ -22,4 +23,6 @@ from .binding import (EXPORTS, SSMError, lib, ssd_chunked_bwd,  # noqa: F401
                       ssm_last_device_status, ssm_scan_bwd, ssm_scan_bwd_workspace_bytes,
                       ssm_scan_checkpoint_bytes, ssm_scan_fwd, ssm_scan_fwd_host,
                       ssm_scan_fwd_host_workspace_bytes,
-                      ssm_scan_workspace_bytes, status_string)
+                      ssm_scan_workspace_bytes, ssm_vocab_ce_bwd,
+                      ssm_vocab_ce_bwd_workspace_bytes, ssm_vocab_ce_fwd,
+                      ssm_vocab_ce_workspace_bytes, status_string)

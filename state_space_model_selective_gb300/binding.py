@@ -39,7 +39,9 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssm_debug_set_scan_path", "ssm_noalloc_last_status", "ssm_mamba3_rope",
            "ssm_add_rmsnorm_fwd", "ssm_add_rmsnorm_e4m3_fwd", "ssm_add_rmsnorm_bwd_workspace_bytes",
            "ssm_add_rmsnorm_bwd", "ssm_linrec_checkpoint_bytes", "ssm_linrec_workspace_bytes",
-           "ssm_linrec_fwd", "ssm_linrec_bwd_workspace_bytes", "ssm_linrec_bwd"]
+           "ssm_linrec_fwd", "ssm_linrec_bwd_workspace_bytes", "ssm_linrec_bwd",
+           "ssm_vocab_ce_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd_workspace_bytes",
+           "ssm_vocab_ce_bwd"]
 
 
 class SSMError(RuntimeError):
@@ -134,13 +136,18 @@ def lib() -> ctypes.CDLL:
         L.ssm_add_rmsnorm_bwd.restype = i
         L.ssm_add_rmsnorm_bwd.argtypes = [vp] * 2 + [fl] + [vp] * 5 + [i] * 5 + [vp, sz, vp]
         for f in (L.ssm_linrec_checkpoint_bytes, L.ssm_linrec_workspace_bytes,
-                  L.ssm_linrec_bwd_workspace_bytes):
+                  L.ssm_linrec_bwd_workspace_bytes, L.ssm_vocab_ce_workspace_bytes,
+                  L.ssm_vocab_ce_bwd_workspace_bytes):
             f.restype = sz
             f.argtypes = [i] * 3
         L.ssm_linrec_fwd.restype = i
         L.ssm_linrec_fwd.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 4 + [i] * 5 + [vp, sz, vp]
         L.ssm_linrec_bwd.restype = i
         L.ssm_linrec_bwd.argtypes = [vp] * 3 + [ll] * 3 + [vp] * 8 + [i] * 5 + [vp, sz, vp]
+        L.ssm_vocab_ce_fwd.restype = i
+        L.ssm_vocab_ce_fwd.argtypes = [vp] * 5 + [i] * 4 + [vp, sz, vp]
+        L.ssm_vocab_ce_bwd.restype = i
+        L.ssm_vocab_ce_bwd.argtypes = [vp] * 7 + [i] * 5 + [vp, sz, vp]
         _lib = L
     return _lib
 
@@ -1251,4 +1258,74 @@ def ssm_linrec_bwd(f, x, dy, z=None, initial_state=None, dfinal_state=None, chec
                               _DT[x.dtype], _dt_code(gd, "grad_dtype"), _ptr(workspace),
                               workspace.numel(), _stream(stream))
     _check(st, "ssm_linrec_bwd")
+    return g
+
+
+def ssm_vocab_ce_workspace_bytes(tokens, dim, vocab) -> int:
+    return int(lib().ssm_vocab_ce_workspace_bytes(tokens, dim, vocab))
+
+
+def ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab) -> int:
+    return int(lib().ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab))
+
+
+def _ce_args(h, W, targets):
+    _req(h, "h", torch.bfloat16, 2)
+    _req(W, "W", torch.bfloat16, 2)
+    if W.shape[1] != h.shape[1]:
+        raise ValueError(f"W must have shape (vocab, {h.shape[1]}), got {tuple(W.shape)}")
+    _like(targets, "targets", (h.shape[0],), torch.int64)
+    return h.shape[0], h.shape[1], W.shape[0]
+
+
+def ssm_vocab_ce_fwd(h, W, targets, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits h W^T without the logits in memory.  h:
+    (tokens, dim), W: (vocab, dim) bf16, dim a multiple of 8; targets: (tokens,) int64, a
+    negative one for a token without loss.  Returns (loss, lse), (tokens,) fp32 each."""
+    tokens, dim, vocab = _ce_args(h, W, targets)
+    with _on(stream):
+        if loss is None:
+            loss = torch.empty(tokens, dtype=torch.float32, device=h.device)
+        if lse is None:
+            lse = torch.empty(tokens, dtype=torch.float32, device=h.device)
+        if workspace is None:
+            need = ssm_vocab_ce_workspace_bytes(tokens, dim, vocab)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=h.device)
+    _like(loss, "loss", (tokens,), torch.float32)
+    _like(lse, "lse", (tokens,), torch.float32)
+    _req(workspace, "workspace", torch.uint8)
+    st = lib().ssm_vocab_ce_fwd(_ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), tokens, dim,
+                                vocab, _DT[h.dtype], _ptr(workspace), workspace.numel(),
+                                _stream(stream))
+    _check(st, "ssm_vocab_ce_fwd")
+    return loss, lse
+
+
+def ssm_vocab_ce_bwd(h, W, targets, lse, dloss, grad_dtype=None, workspace=None, stream=None,
+                     out=None):
+    """Gradient of ``ssm_vocab_ce_fwd`` for the loss sum(dloss * loss), with the lse it
+    returned; dloss: (tokens,) fp32.  Returns a dict: dh, dW in ``grad_dtype`` (h's type by
+    default).  ``out`` may map either name to a preallocated tensor to write."""
+    tokens, dim, vocab = _ce_args(h, W, targets)
+    _like(lse, "lse", (tokens,), torch.float32)
+    _like(dloss, "dloss", (tokens,), torch.float32)
+    gd = h.dtype if grad_dtype is None else grad_dtype
+    code = _dt_code(gd, "grad_dtype")
+    out = out or {}
+    g = {}
+    for k in out:
+        if k not in ("dh", "dW"):
+            raise ValueError(f"out[{k!r}] is not an output of this call")
+    with _on(stream):
+        for k, t in (("dh", h), ("dW", W)):
+            g[k] = (torch.empty(t.shape, dtype=gd, device=h.device) if k not in out else
+                    _like(out[k], f"out[{k!r}]", t.shape, gd))
+        if workspace is None:
+            need = ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=h.device)
+    _req(workspace, "workspace", torch.uint8)
+    st = lib().ssm_vocab_ce_bwd(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss),
+                                _ptr(g["dh"]), _ptr(g["dW"]), tokens, dim, vocab, _DT[h.dtype], code,
+                                _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "ssm_vocab_ce_bwd")
     return g

@@ -1,0 +1,784 @@
+// vocab_ce.cu -- softmax cross entropy of the logits h W^T over a large
+// vocabulary, without the logits in memory: loss, and gradient.
+//
+//   l = h W^T,  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_t,target
+//   P_tv = (exp(l_tv - lse_t) - [v = target_t]) dloss_t
+//   dh = P W,  dW = P^T h
+//
+// Bound by the tensor cores: 2 tokens dim vocab multiply-adds a product, one
+// product for the loss and three for the gradient (the logits are computed
+// again, since the softmax needs the whole row's lse first).
+//
+// All four products run in one tcgen05 pipeline.  A cluster of two CTAs computes
+// 256 x 256 tiles (cta_group::2: each CTA holds 128 rows of A, 128 of B and the
+// 128 x 256 half of the accumulator that belongs to its rows of A), because a
+// pair loads 32 KB per CTA for what a single CTA's 128 x 256 tile needs 48 KB
+// for, and the loads go through L2.  Per CTA: one thread issues TMA loads into
+// a ring of six 64-deep stages, one thread of the first CTA issues the MMAs, and
+// eight warps empty the accumulators, of which there are two, so that a tile's
+// epilogue runs under the next tile's products.
+//  * logits, K-major h and W: the epilogue keeps each row's maximum and sum of
+//    exponentials of its 128 columns (fp32, base 2), and the target's logit; a
+//    small kernel joins them.
+//  * gradient, for a piece of the vocabulary at a time: the logits again, with
+//    P / max |dloss| as the epilogue, rounded to bf16, which the tensor cores'
+//    operands have to be, then dh += P W and dW = P^T h in one launch, where W, h
+//    and P are read as MN-major operands.  The rounding is at most 2^-9 of each
+//    value and independent from value to value, so the products' sums keep it
+//    below 2^-9; without the division by the largest dloss the targets' entries
+//    of a mean loss, which outweigh the rest, would all be off by the same
+//    rounding of 1 / n (0.25 % of the gradients at 1986 tokens, against 0.17 % for
+//    rounding the result to bf16).  The factor comes back in fp32 in dW's
+//    epilogue and dh's last sum.
+// The sum over pieces and over splits of one piece's vocabulary is kept in fp32
+// and taken in a fixed order: runs are bit-equal.
+#include <algorithm>
+
+#include "tcgen05.cuh"
+
+namespace {
+
+using namespace ssm;
+
+constexpr int kTile = 256;               // rows and columns of a pair's tile
+constexpr int kHalf = 128;               // rows of A and of B one CTA holds
+constexpr int kDepth = 64;               // K of one stage: 128 bytes of bf16
+constexpr int kStages = 6;
+constexpr uint32_t kBox = 64 * 128;      // a 64 x 64 box of bf16
+constexpr uint32_t kOperand = 2 * kBox;  // 128 x 64
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 2) * 32;  // + TMA warp, MMA warp
+constexpr uint32_t kTmemCols = 512;             // two accumulators of 256 columns
+constexpr int kGroupM = 32;  // token tiles whose h stays in L2 while W passes
+
+enum Mode { kLoss, kProb, kGrad };
+
+struct CeHeader {
+    uint32_t unused;
+    uint32_t status;
+    float scale;  // gradient: max |dloss| of the tokens that count
+    uint32_t pad[61];
+};
+static_assert(sizeof(CeHeader) == 256, "workspace header is 256 bytes");
+
+struct CeArgs {
+    int tokens, dim, vocab;
+    uint32_t* status;
+    const long long* targets;
+    // loss
+    float2* parts;       // [2 * vocab tiles][tokens]: maximum (base 2), sum
+    float* target_logit; // [tokens]
+    // gradient
+    const float* lse;
+    const float* dloss;
+    const float* scale;  // in the header
+    __nv_bfloat16* P;    // [tokens][ld], columns v0 .. v0 + width of the vocabulary
+    int ld, v0, width;   // width: what is left of the vocabulary, at most ld
+    float* dh_parts;     // [splits][tokens][dim]
+    int first_piece, splits, split_depth;  // stages of one split's K
+    void* dW;
+    int dw_bf16;
+};
+
+// ------------------------------------------------- pairs of CTAs (cta_group::2)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// the address of the first CTA's copy of a shared variable
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+                 : "memory");
+}
+
+// mbar_wait, acquiring what the other CTA's arrivals released
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    const uint32_t addr = smem_u32(bar);
+    for (uint32_t i = 0; i < kMbarSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity), "r"(1000u)
+            : "memory");
+        if (done) return true;
+    }
+    record_status(status, SSM_ERR_TIMEOUT);
+    return false;
+}
+
+// a box into this CTA's shared memory, its bytes counted on the first CTA's barrier
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                         int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// arrive on both CTAs' copies of `bar` once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ work
+
+// One tile of one product: operand origins, K range, and what it is for.
+struct Item {
+    bool dw;         // kGrad: dW's tile, else dh's
+    int m0, n0;      // rows and columns of the result
+    int k0, depth;   // first K, stages
+    int split;
+};
+
+// The pair's items, in order.  Loss and P: tiles round-robin, token tiles fastest
+// within groups of kGroupM, so that W passes once per group.  Gradient: dh's
+// (few, deep) tiles round-robin first; the pairs that have one less of them take
+// dW tiles for that time, then all take the rest in turn, so that at any time
+// the pairs work on neighbouring tiles and share them in L2.
+template <Mode MODE>
+struct Schedule {
+    int pairs, pair;
+    int mt, nt;                  // tiles of tokens, and of vocabulary (kGrad: of dim)
+    int n_dh, n_dw, dh_depth, dw_depth;
+    int own_dh, free_pairs, early, n_early;
+
+    __device__ Schedule(const CeArgs& a, int pairs_, int pair_) : pairs(pairs_), pair(pair_) {
+        mt = (a.tokens + kTile - 1) / kTile;
+        if constexpr (MODE == kGrad) {
+            nt = (a.dim + kTile - 1) / kTile;
+            n_dh = mt * nt * a.splits;
+            n_dw = (a.width + kTile - 1) / kTile * nt;
+            dh_depth = a.split_depth;
+            dw_depth = (a.tokens + kDepth - 1) / kDepth;
+            const int rest = n_dh % pairs;
+            own_dh = n_dh / pairs + (pair < rest ? 1 : 0);
+            free_pairs = rest ? pairs - rest : 0;
+            early = (dh_depth + dw_depth / 2) / dw_depth;  // dW tiles in the time of one of dh
+            n_early = (int)min((long long)n_dw, (long long)early * free_pairs);
+        } else {
+            nt = ((MODE == kProb ? a.width : a.vocab) + kTile - 1) / kTile;
+        }
+    }
+
+    __device__ bool get(const CeArgs& a, int i, Item& w) const {
+        if constexpr (MODE != kGrad) {
+            const long long t = (long long)i * pairs + pair;
+            if (t >= (long long)mt * nt) return false;
+            const int group = (int)(t / ((long long)kGroupM * nt));
+            const int gm = min(kGroupM, mt - group * kGroupM);
+            const int r = (int)(t - (long long)group * kGroupM * nt);
+            w.m0 = (group * kGroupM + r % gm) * kTile;
+            w.n0 = r / gm * kTile;
+            w.k0 = 0;
+            w.depth = (a.dim + kDepth - 1) / kDepth;
+            w.dw = false;
+            w.split = 0;
+            return true;
+        } else {
+            if (i < own_dh) {
+                const int t = i * pairs + pair;
+                w.dw = false;
+                w.split = t / (mt * nt);
+                const int r = t % (mt * nt);
+                w.m0 = r / nt * kTile;
+                w.n0 = r % nt * kTile;
+                const int all = (a.width + kDepth - 1) / kDepth;
+                w.k0 = w.split * dh_depth * kDepth;
+                w.depth = min(dh_depth, all - w.split * dh_depth);
+                return true;
+            }
+            i -= own_dh;
+            int t;
+            const bool is_free = free_pairs && pair >= pairs - free_pairs;
+            if (is_free) {
+                const int me = pair - (pairs - free_pairs);
+                const int mine = (n_early - me + free_pairs - 1) / free_pairs;
+                if (i < mine) {
+                    t = i * free_pairs + me;
+                } else {
+                    t = n_early + (i - mine) * pairs + pair;
+                }
+            } else {
+                t = n_early + i * pairs + pair;
+            }
+            if (t >= n_dw) return false;
+            w.dw = true;
+            w.split = 0;
+            w.m0 = t / nt * kTile;
+            w.n0 = t % nt * kTile;
+            w.k0 = 0;
+            w.depth = dw_depth;
+            return true;
+        }
+    }
+};
+
+// -------------------------------------------------------------- epilogues
+
+// maximum and sum of 2^(l - maximum) of a row's columns so far, base 2
+struct RowSum {
+    float m, s;
+    __device__ void add(const float* v, int n) {
+        float cm = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) cm = fmaxf(cm, v[j]);
+        cm = fmaxf(m, cm * kLog2e);
+        const float base = cm == -INFINITY ? 0.0f : cm;
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) t += ex2_approx(fmaf(v[j], kLog2e, -base));
+        s = fmaf(s, ex2_approx(m - base), t);
+        m = cm;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 columns of a row to memory, `n` of them (a multiple of 8)
+__device__ __forceinline__ void store_row(void* p, const float* v, int n, bool bf16) {
+    if (bf16) {
+        uint4* q = static_cast<uint4*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (8 * j < n)
+                q[j] = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]),
+                                  pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                  pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                                  pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+    } else {
+        float4* q = static_cast<float4*>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (4 * j < n)
+                q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+}
+
+// (the TMEM loads are warp-wide: lanes that took different branches meet before)
+// The half (128 columns) of one row of an accumulator that this thread empties:
+// taddr is its first column, row the row in the result, c0 the first column.
+template <Mode MODE>
+__device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_t taddr, int row,
+                                         int c0) {
+    float v[32];
+    if constexpr (MODE == kLoss) {
+        const bool in = row < a.tokens;
+        const long long target = in ? a.targets[row] : -1;
+        RowSum sum{-INFINITY, 0.0f};
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+            __syncwarp();
+            tmem_ld32(taddr + c, v);
+            tmem_wait_ld();
+            const int col = c0 + c;
+            if (col + 32 <= a.vocab) sum.add(v, 32);
+            else if (col < a.vocab) sum.add(v, a.vocab - col);
+            const long long at = target - col;
+            if (at >= 0 && at < 32 && target < a.vocab) {
+                float l = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j == (int)at) l = v[j];
+                a.target_logit[row] = l;
+            }
+        }
+        if (in) a.parts[(size_t)(c0 / kHalf) * a.tokens + row] = make_float2(sum.m, sum.s);
+    } else if constexpr (MODE == kProb) {
+        const bool in = row < a.tokens;
+        const long long target = in ? a.targets[row] : -1;
+        const bool counts = target >= 0 && target < a.vocab;
+        const float g = counts ? __fdiv_rn(a.dloss[row], *a.scale) : 0.0f;
+        const float lse2 = in ? a.lse[row] * kLog2e : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+            __syncwarp();
+            tmem_ld32(taddr + c, v);
+            tmem_wait_ld();
+            const int col = c0 + c;  // within the piece
+            const long long at = target - a.v0 - col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                float p = ex2_approx(fmaf(v[j], kLog2e, -lse2));
+                if (at == j) p -= 1.0f;
+                // a token without loss takes nothing, whatever its logits are; what
+                // lies past the vocabulary is K of the next products
+                v[j] = counts && col + j < a.width ? p * g : 0.0f;
+            }
+            if (in) store_row(a.P + (size_t)row * a.ld + col, v, 32, true);
+        }
+    } else {
+        const int rows = w.dw ? a.width : a.tokens;
+        const float scale = *a.scale;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+            __syncwarp();
+            tmem_ld32(taddr + c, v);
+            tmem_wait_ld();
+            const int col = c0 + c;
+            const int n = row < rows ? min(32, a.dim - col) : 0;
+            if (n <= 0) {
+                // nothing of this row here
+            } else if (w.dw) {
+                const size_t o = (size_t)(a.v0 + row) * a.dim + col;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= scale;
+                store_row(static_cast<uint8_t*>(a.dW) + o * (a.dw_bf16 ? 2 : 4), v, n, a.dw_bf16);
+            } else {
+                float* p = a.dh_parts + ((size_t)w.split * a.tokens + row) * a.dim + col;
+                if (!a.first_piece) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        if (j < n) {
+                            const float4 o = *reinterpret_cast<const float4*>(p + j);
+                            v[j] += o.x; v[j + 1] += o.y; v[j + 2] += o.z; v[j + 3] += o.w;
+                        }
+                    }
+                }
+                store_row(p, v, n, false);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- kernel
+
+// Tensor maps of 64 x 64 boxes: h (tokens x dim), W (vocab x dim), P (tokens x ld).
+template <Mode MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ce_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_W,
+              const __grid_constant__ CUtensorMap tm_P, const CeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t s_tmem;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const Schedule<MODE> sched(a, gridDim.x / 2, blockIdx.x / 2);
+    bool ok = true;
+
+    if (warp == kEpiWarps) {
+        // ---- loads: this CTA's half of A and of B
+        if (lane == 0) {
+            uint32_t n = 0;  // stages filled
+            Item w;
+            for (int i = 0; ok && sched.get(a, i, w); ++i) {
+                const int am = w.m0 + (int)rank * kHalf, bn = w.n0 + (int)rank * kHalf;
+                for (int kb = 0; kb < w.depth; ++kb, ++n) {
+                    const uint32_t s = n % kStages;
+                    if (!mbar_wait(&empty[s], ((n / kStages) & 1) ^ 1, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = first_cta(&full[s]);
+                    const uint32_t A = smem + s * kStageBytes, B = A + kOperand;
+                    const int k = w.k0 + kb * kDepth;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if constexpr (MODE != kGrad) {
+                            load_box(A + j * kBox, &tm_h, bar, k, am + 64 * j);
+                            load_box(B + j * kBox, &tm_W, bar, k, a.v0 + bn + 64 * j);
+                        } else if (w.dw) {
+                            load_box(A + j * kBox, &tm_P, bar, am + 64 * j, k);
+                            load_box(B + j * kBox, &tm_h, bar, bn + 64 * j, k);
+                        } else {
+                            load_box(A + j * kBox, &tm_P, bar, k, am + 64 * j);
+                            load_box(B + j * kBox, &tm_W, bar, bn + 64 * j, a.v0 + k);
+                        }
+                    }
+                }
+            }
+            // the MMAs' arrivals on this CTA's barriers are all in before it ends
+            for (uint32_t q = n > kStages ? n - kStages : 0; ok && q < n; ++q)
+                ok = mbar_wait(&empty[q % kStages], (q / kStages) & 1, a.status);
+        }
+    } else if (warp == kEpiWarps + 1) {
+        // ---- products, issued by the first CTA for both
+        if (lane == 0 && rank == 0) {
+            uint32_t n = 0;
+            Item w;
+            for (int i = 0; ok && sched.get(a, i, w); ++i) {
+                const uint32_t d = tmem + (i & 1) * kTile;
+                const bool a_mn = MODE == kGrad && w.dw, b_mn = MODE == kGrad;
+                const uint32_t idesc = idesc_bf16_f32(kTile, kTile) | (a_mn ? kIdescAMN : 0) |
+                                       (b_mn ? kIdescBMN : 0);
+                ok = wait_cluster(&acc_empty[i & 1], ((i >> 1) & 1) ^ 1, a.status);
+                tc_fence_after();
+                for (int kb = 0; ok && kb < w.depth; ++kb, ++n) {
+                    const uint32_t s = n % kStages;
+                    ok = wait_cluster(&full[s], (n / kStages) & 1, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t A = smem + s * kStageBytes, B = A + kOperand;
+                    // 16 of K: 32 bytes within a K-major row, 16 rows of an MN-major tile
+                    const uint64_t da = a_mn ? smem_desc_mn128(A, kBox) : smem_desc_k128(A);
+                    const uint64_t db = b_mn ? smem_desc_mn128(B, kBox) : smem_desc_k128(B);
+                    const uint32_t sa = a_mn ? 2048u >> 4 : 32u >> 4, sb = b_mn ? 2048u >> 4 : 32u >> 4;
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k)
+                        mma_pair(d, da + k * sa, db + k * sb, idesc, (uint32_t)(kb | k));
+                    commit_pair(&empty[s]);
+                }
+                if (ok) commit_pair(&acc_full[i & 1]);
+            }
+        }
+    } else {
+        // ---- epilogue: warp w of a quarter's two empties lanes 32 (w % 4) .. and
+        // the columns of its half
+        const int quarter = warp & 3, half = warp >> 2;
+        Item w;
+        for (int i = 0; sched.get(a, i, w); ++i) {
+            // every lane waits: each then acquires by itself
+            ok = mbar_wait(&acc_full[i & 1], (i >> 1) & 1, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (i & 1) * kTile +
+                                   half * kHalf;
+            epilogue<MODE>(a, w, taddr, w.m0 + (int)rank * kHalf + quarter * 32 + lane,
+                           w.n0 + half * kHalf);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(first_cta(&acc_empty[i & 1]));
+        }
+    }
+    // a wait ran out: leave the copies in flight time to land before the shared
+    // memory goes
+    if (!ok)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols)
+                     : "memory");
+}
+
+// Joins the column halves' maxima and sums: 8 warps take every eighth part of
+// 32 rows, then warp 0 joins the eight.
+__global__ void __launch_bounds__(256) ce_join_kernel(const float2* parts, int nparts,
+                                                      const float* target_logit,
+                                                      const long long* targets, int tokens,
+                                                      int vocab, float* loss, float* lse) {
+    __shared__ float2 sh[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.0f;
+    auto join = [&](float2 p) {
+        const float n = fmaxf(m, p.x), base = n == -INFINITY ? 0.0f : n;
+        s = s * ex2_approx(m - base) + p.y * ex2_approx(p.x - base);
+        m = n;
+    };
+    if (row < tokens)
+        for (int i = warp; i < nparts; i += 8) join(parts[(size_t)i * tokens + row]);
+    sh[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp == 0 && row < tokens) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) join(sh[i][lane]);
+        const float l = fmaf(m, 0.6931471805599453f, logf(s));
+        lse[row] = l;
+        const long long t = targets[row];
+        loss[row] = t < 0 ? 0.0f : t < vocab ? l - target_logit[row] : NAN;
+    }
+}
+
+// header of a gradient: max |dloss| over the tokens that count (1 where that is
+// no usable factor: 0, infinite or NaN)
+__global__ void __launch_bounds__(1024) ce_scale_kernel(const float* dloss,
+                                                        const long long* targets, int tokens,
+                                                        int vocab, CeHeader* head) {
+    __shared__ float sh[32];
+    float m = 0.0f;
+    for (int i = threadIdx.x; i < tokens; i += 1024) {
+        const long long t = targets[i];
+        if (t >= 0 && t < vocab) m = fmaxf(m, fabsf(dloss[i]));
+    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = sh[threadIdx.x];
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (threadIdx.x == 0) {
+            head->scale = m > 1e-30f && m < 1e30f ? m : 1.0f;
+            head->status = 0;
+        }
+    }
+}
+
+// dh = the factor times the sum of the splits' parts, in order
+template <typename T>
+__global__ void __launch_bounds__(256) ce_dh_kernel(const float* parts, int splits, size_t n,
+                                                    const float* scale, T* dh) {
+    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 t = *reinterpret_cast<const float4*>(parts + i);
+    for (int k = 1; k < splits; ++k) {
+        const float4 p = *reinterpret_cast<const float4*>(parts + k * n + i);
+        t.x += p.x; t.y += p.y; t.z += p.z; t.w += p.w;
+    }
+    const float f = *scale;
+    t.x *= f; t.y *= f; t.z *= f; t.w *= f;
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(dh + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+    else
+        *reinterpret_cast<float4*>(dh + i) = t;
+}
+
+// ------------------------------------------------------------------- host
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+int tiles(int n) { return (n + kTile - 1) / kTile; }
+
+// GB300 has 76 pairs of SMs; the plan may not depend on the device, since the
+// workspace size follows from it.
+constexpr int kPairs = 76;
+
+// The gradient's pieces: P takes tokens x piece bf16, at most 256 MB (which
+// spreads the launches' ends over enough work) but at least 4096 columns.
+constexpr size_t kPieceElements = size_t(1) << 27;
+
+struct Plan {
+    int piece;   // columns of one piece, a multiple of 256
+    int splits;  // of a piece's vocabulary in dh
+};
+
+Plan plan_grad(int tokens, int dim, int vocab) {
+    Plan p;
+    const size_t fit = std::max<size_t>(kPieceElements / std::max(tokens, 1) / kTile * kTile, 4096);
+    const int pieces = (int)(((size_t)vocab + fit - 1) / fit);
+    p.piece = tiles((vocab + pieces - 1) / pieces) * kTile;
+    // dh's tiles are as deep as the piece is wide: split them until they fit
+    // under an even share of the launch's work
+    const long long nt = tiles(dim), dh = tiles(tokens) * nt, dw = tiles(p.piece) * nt;
+    const long long dh_depth = p.piece / kDepth, dw_depth = (tokens + kDepth - 1) / kDepth;
+    const long long share = (dh * dh_depth + dw * dw_depth + kPairs - 1) / kPairs;
+    p.splits = 1;
+    while (p.splits < 32 &&
+           (dh * p.splits + kPairs - 1) / kPairs * ((dh_depth + p.splits - 1) / p.splits) >
+               share + share / 8)
+        ++p.splits;
+    return p;
+}
+
+bool sizes_fit(int tokens, int dim, int vocab) {
+    return dim % 8 == 0 && (double)tokens * vocab / (kTile * kTile) < 1e9;
+}
+
+template <Mode MODE>
+bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, const CeArgs& a,
+            cudaStream_t s) {
+    auto kernel = ce_kernel<MODE>;
+    int dev = 0, sms = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+            cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return false;
+    kernel<<<2 * std::max(1, sms / 2), kThreads, kSmemBytes, s>>>(h, W, P, a);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+struct Span { const void* p; size_t n; };
+
+}  // namespace
+
+extern "C" size_t ssm_vocab_ce_workspace_bytes(int tokens, int dim, int vocab) {
+    if (tokens < 0 || dim < 1 || vocab < 1 || !sizes_fit(tokens, dim, vocab)) return 0;
+    return 256 + round256((size_t)tokens * 4) + round256((size_t)2 * tiles(vocab) * tokens * 8);
+}
+
+extern "C" size_t ssm_vocab_ce_bwd_workspace_bytes(int tokens, int dim, int vocab) {
+    if (tokens < 0 || dim < 1 || vocab < 1 || !sizes_fit(tokens, dim, vocab)) return 0;
+    const Plan p = plan_grad(tokens, dim, vocab);
+    return 256 + round256((size_t)tokens * p.piece * 2) +
+           round256((size_t)p.splits * tokens * dim * 4);
+}
+
+static ssm_status_t ce_check(int tokens, int dim, int vocab) {
+    if (tokens < 0 || dim < 1 || vocab < 1) return SSM_ERR_SHAPE;
+    return sizes_fit(tokens, dim, vocab) ? SSM_OK : SSM_ERR_UNSUPPORTED;
+}
+
+extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const long long* targets,
+                                         float* loss, float* lse, int tokens, int dim, int vocab,
+                                         ssm_dtype_t in_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    using namespace ssm_host;
+    if (ssm_status_t st = ce_check(tokens, dim, vocab)) return st;
+    if (!dtype_ok(in_dtype)) return SSM_ERR_DTYPE;
+    if (in_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+    if (tokens == 0) return SSM_OK;
+    if (!h || !W || !targets || !loss || !lse) return SSM_ERR_NULL;
+    const size_t need = ssm_vocab_ce_workspace_bytes(tokens, dim, vocab);
+    if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
+    for (const void* p : {h, W, (const void*)targets, (const void*)loss, (const void*)lse,
+                          (const void*)workspace})
+        if (!aligned16(p)) return SSM_ERR_ALIGN;
+    const Span ins[] = {{h, (size_t)tokens * dim * 2}, {W, (size_t)vocab * dim * 2},
+                        {targets, (size_t)tokens * 8}};
+    const Span outs[] = {{loss, (size_t)tokens * 4}, {lse, (size_t)tokens * 4}, {workspace, need}};
+    for (const Span& o : outs)
+        for (const Span& i : ins)
+            if (overlaps(o.p, o.n, i.p, i.n)) return SSM_ERR_ALIAS;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SSM_ERR_ALIAS;
+
+    CUtensorMap mh, mw;
+    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
+        !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64))
+        return SSM_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CeArgs a{};
+    a.tokens = tokens; a.dim = dim; a.vocab = vocab; a.targets = targets;
+    a.status = &reinterpret_cast<CeHeader*>(ws)->status;
+    a.target_logit = reinterpret_cast<float*>(ws + 256);
+    a.parts = reinterpret_cast<float2*>(ws + 256 + round256((size_t)tokens * 4));
+    if (cudaMemsetAsync(ws, 0, 256, s) != cudaSuccess || !launch<kLoss>(mh, mw, mh, a, s))
+        return SSM_ERR_CUDA;
+    ce_join_kernel<<<(tokens + 31) / 32, 256, 0, s>>>(a.parts, 2 * tiles(vocab), a.target_logit,
+                                                      targets, tokens, vocab, loss, lse);
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const long long* targets,
+                                         const float* lse, const float* dloss, void* dh, void* dW,
+                                         int tokens, int dim, int vocab, ssm_dtype_t in_dtype,
+                                         ssm_dtype_t grad_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    using namespace ssm_host;
+    if (ssm_status_t st = ce_check(tokens, dim, vocab)) return st;
+    if (!dtype_ok(in_dtype) || !dtype_ok(grad_dtype)) return SSM_ERR_DTYPE;
+    if (in_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+    const size_t ge = dtype_size(grad_dtype);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!dW || (tokens > 0 && (!h || !W || !targets || !lse || !dloss || !dh))) return SSM_ERR_NULL;
+    if (!aligned16(dW)) return SSM_ERR_ALIGN;
+    if (tokens == 0)
+        return cudaMemsetAsync(dW, 0, (size_t)vocab * dim * ge, s) == cudaSuccess ? SSM_OK
+                                                                                  : SSM_ERR_CUDA;
+    const size_t need = ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab);
+    if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
+    for (const void* p : {h, W, (const void*)targets, (const void*)lse, (const void*)dloss,
+                          (const void*)dh, (const void*)workspace})
+        if (!aligned16(p)) return SSM_ERR_ALIGN;
+    const Span ins[] = {{h, (size_t)tokens * dim * 2}, {W, (size_t)vocab * dim * 2},
+                        {targets, (size_t)tokens * 8}, {lse, (size_t)tokens * 4},
+                        {dloss, (size_t)tokens * 4}};
+    const Span outs[] = {{dh, (size_t)tokens * dim * ge}, {dW, (size_t)vocab * dim * ge},
+                         {workspace, need}};
+    for (const Span& o : outs)
+        for (const Span& i : ins)
+            if (overlaps(o.p, o.n, i.p, i.n)) return SSM_ERR_ALIAS;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SSM_ERR_ALIAS;
+
+    const Plan plan = plan_grad(tokens, dim, vocab);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    CeArgs a{};
+    a.tokens = tokens; a.dim = dim; a.vocab = vocab; a.targets = targets;
+    a.status = &reinterpret_cast<CeHeader*>(ws)->status;
+    a.lse = lse; a.dloss = dloss; a.dW = dW; a.dw_bf16 = grad_dtype == SSM_BF16;
+    a.P = reinterpret_cast<__nv_bfloat16*>(ws + 256);
+    a.ld = plan.piece;
+    a.dh_parts = reinterpret_cast<float*>(ws + 256 + round256((size_t)tokens * plan.piece * 2));
+    CUtensorMap mh, mw, mp;
+    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
+        !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64) ||
+        !make_tmap_2d(&mp, a.P, SSM_BF16, tokens, plan.piece, 64, 64))
+        return SSM_ERR_CUDA;
+    CeHeader* head = reinterpret_cast<CeHeader*>(ws);
+    a.scale = &head->scale;
+    ce_scale_kernel<<<1, 1024, 0, s>>>(dloss, targets, tokens, vocab, head);
+    // a split is the same number of stages in every piece, so that the narrower
+    // last piece uses the first splits only
+    a.split_depth = (plan.piece / kDepth + plan.splits - 1) / plan.splits;
+    const int first_depth = (std::min(plan.piece, vocab) + kDepth - 1) / kDepth;
+    const int used = (first_depth + a.split_depth - 1) / a.split_depth;
+    for (int v0 = 0; v0 < vocab; v0 += plan.piece) {
+        a.v0 = v0;
+        a.width = std::min(plan.piece, vocab - v0);
+        a.first_piece = v0 == 0;
+        const int depth = (a.width + kDepth - 1) / kDepth;
+        a.splits = (depth + a.split_depth - 1) / a.split_depth;
+        if (!launch<kProb>(mh, mw, mp, a, s) || !launch<kGrad>(mh, mw, mp, a, s))
+            return SSM_ERR_CUDA;
+    }
+    const size_t n = (size_t)tokens * dim;
+    const unsigned grid = (unsigned)((n / 4 + 255) / 256);
+    if (grad_dtype == SSM_BF16)
+        ce_dh_kernel<<<grid, 256, 0, s>>>(a.dh_parts, used, n, a.scale,
+                                          static_cast<__nv_bfloat16*>(dh));
+    else
+        ce_dh_kernel<<<grid, 256, 0, s>>>(a.dh_parts, used, n, a.scale,
+                                          static_cast<float*>(dh));
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
