@@ -12,22 +12,31 @@
 // the state as h -> P h + q, and spans compose by (P1, q1) o (P2, q2) =
 // (P1 P2, P2 q1 + q2).
 //
-//  * A CTA takes a tile of 8 S steps by 64 channels; warp w takes S consecutive
-//    steps, a lane two neighbouring channels, so a warp's access to a step is
-//    one row segment of 64 channels.  Inputs come through a ring of shared
-//    memory tiles filled with cp.async, so the next tile's loads are in flight
-//    while this one waits for its predecessors.
+//  * A CTA takes a tile of 64 steps by 64 channels; each of its 8 (bf16) or 16
+//    (fp32) warps takes consecutive steps, a lane two neighbouring channels, so a
+//    warp's access to a step is one row segment of 64 channels.  Inputs come through a ring of shared
+//    memory tiles, by TMA where every row is 16-byte aligned (else cp.async or
+//    element loads), so the next tile's loads are in flight while this one waits
+//    for its predecessors; results go back in place and out by TMA.
 //  * Each warp scans its steps from zero, keeping a_t and b_t in registers;
 //    the warps' (P, q) meet in shared memory; tiles chain through a decoupled
-//    look-back (Merrill and Garland's single-pass prefix scan): a tile publishes
-//    its aggregate, or its inclusive state at once where its predecessor's is
-//    already there, and composes backwards to the newest inclusive state.
-//    Tiles are handed out in order by a ticket, so a predecessor is always
-//    running or done; every wait is bounded (SSM_ERR_TIMEOUT).
+//    look-back (Merrill and Garland's single-pass prefix scan).  The published
+//    values are their own flags (a pattern no result has means "not yet"), so a
+//    look-back is one round trip through L2 instead of two, and the warps look at
+//    the sixteen tiles before theirs at once.
+//    The grid is what the GPU holds at once (a cooperative launch) and CTA i
+//    takes tiles i, i + grid, ..., so that the tiles in work are always
+//    consecutive ones and a predecessor is running or done; every wait is bounded
+//    (SSM_ERR_TIMEOUT).  (Tiles drawn from a counter, two ahead for the loads,
+//    left gaps of drawn but unstarted tiles that everything behind waited for:
+//    786 us against 470 us for 65536 steps of 1536 channels.)
 //  * Each warp then replays its steps from its entry state and writes y.
+//  * Masked steps (below) cost comparisons at every step, 45 instructions an
+//    element in all; a warp whose gates all lie within |f| < 80, where no step can
+//    be masked, takes a path without them.
 // The gradient is the same scan of (a_t, a_t dh_t) in reverse order.  The states
-// it needs are not stored but taken again: the forward keeps the state every 64
-// steps in fp32, and each tile replays its own steps from there.
+// it needs are not stored but taken again: the forward keeps the state at every
+// tile's first step in fp32, and each tile replays its own steps from there.
 //
 // Masked steps: a gate of +inf holds the state whatever x is there (b_t = 0 where
 // 1 - a_t = 0), a gate of -inf restarts it whatever it was (a_t = 0 drops h, NaN
@@ -37,21 +46,20 @@
 
 #include "common.cuh"
 #include "scan_internal.h"
+#include "tcgen05.cuh"
 
 namespace {
 
 using namespace ssm;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kSteps = 64;      // steps per tile, and between kept states
 constexpr int kCh = 64;         // channels per tile, two per lane
-constexpr int kKeep = 64;       // steps between kept states
 constexpr int kWalkSteps = 16;  // sequences up to this long take one thread per channel pair
-
-enum : uint32_t { kFlagNone = 0, kFlagAgg = 1, kFlagInc = 2 };
+constexpr int kLook = 16;       // tiles one look-back sees
+constexpr float kFastGate = 80.0f;
 
 struct alignas(16) LinHeader {
-    uint32_t ticket;
+    uint32_t unused;
     uint32_t status;
     uint32_t pad[62];
 };
@@ -64,18 +72,20 @@ struct LinArgs {
     float* last;              // forward: final state; gradient: dinitial_state; may be NULL
     const float* first;       // gradient: the forward's initial state, may be NULL
     void* out[3];             // forward: y; gradient: df, dx, dz
-    float* keep;              // states entering each 64 steps [ceil(L / 64)][batch][dim]
-    LinHeader* head;          // NULL with one tile per sequence
+    float* keep;              // states entering every 64 steps [ceil(L / 64)][batch][dim]
     uint32_t* status;
-    uint32_t* flags;          // [tiles][blocks]
-    float* agg;               // [tiles][batch][dim][2]
-    float* inc;               // [tiles][batch][dim]
+    ulonglong2* agg;          // [tiles][blocks][32]: (P, q) of two channels
+    uint2* inc;               // [tiles][blocks][32]: the state after the tile
     int batch, seqlen, dim;
     int cblocks, blocks, tiles;  // channel blocks, channel blocks x batch, tiles per sequence
     uint32_t spin_limit;
     int drop_first_publish;
     int vec_out;              // dim even: two channels in one store
     int keep_status;          // the status word holds an earlier scan's result to keep
+};
+
+struct LinMaps {
+    CUtensorMap in[4], out[3];
 };
 
 // ------------------------------------------------------------- elements
@@ -160,16 +170,16 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A tile of STEPS x 64 channels of one input into shared memory [step][64];
+// A tile of 64 steps x 64 channels of one input into shared memory [step][64];
 // what lies past the sequence or the channels is filled with zeros.
-template <typename T, int STEPS, int BYTES>
+template <typename T, int BYTES>
 __device__ __forceinline__ void load_tile(void* dst, const void* src, long long stride, int b,
                                           int t0, int c0, int seqlen, int dim) {
     constexpr int kUnit = BYTES ? BYTES / (int)sizeof(T) : 1;  // elements per copy
     constexpr int kPerRow = kCh / kUnit;
     const T* base = static_cast<const T*>(src) + (long long)b * seqlen * stride + c0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < STEPS * kPerRow; i += kThreads) {
+    for (int i = threadIdx.x; i < kSteps * kPerRow; i += blockDim.x) {
         const int r = i / kPerRow, c = (i % kPerRow) * kUnit;
         const bool in = t0 + r < seqlen && c0 + c < dim;
         const T* p = in ? base + (long long)(t0 + r) * stride + c : static_cast<const T*>(src);
@@ -183,331 +193,489 @@ __device__ __forceinline__ void load_tile(void* dst, const void* src, long long 
 
 // ------------------------------------------------------------- look-back
 
-// Warp 0: given the tile's aggregate (P, q) of this lane's two channels, the
-// state that enters the tile, from the tiles before it (`seq` counts tiles in
-// the order of the scan).  Publishes the aggregate unless the predecessor's
-// inclusive state is already there, and the inclusive state unless the tile is
-// the last.
-__device__ __forceinline__ float2 look_back(const LinArgs& a, int seq, int blk, size_t chan,
-                                            bool valid, bool both, float2 P, float2 q) {
-    const int lane = threadIdx.x & 31;
-    const size_t stride = (size_t)a.batch * a.dim;
-    uint32_t* flags = a.flags + blk;
-    float2 h = make_float2(0.0f, 0.0f);
-    if (seq == 0) {
-        if (a.h0 && valid) h = load_state2(a.h0, chan, both);
-    } else {
-        int j_inc = -1;
-        uint32_t f0 = 0;
-        if (lane == 0) f0 = ld_acquire_gpu(flags + (size_t)(seq - 1) * a.blocks);
-        f0 = __shfl_sync(0xffffffffu, f0, 0);
-        bool ok = true;
-        if (f0 == kFlagInc) {
-            j_inc = seq - 1;
+constexpr uint32_t kNotYet = 0xffffffffu;  // a NaN pattern; results' NaNs are 0x7fffffff
+
+__device__ __forceinline__ uint32_t published(float v) {
+    return v != v ? 0x7fffffffu : __float_as_uint(v);
+}
+
+__device__ __forceinline__ void put_agg(ulonglong2* p, float2 P, float2 q) {
+    const unsigned long long u = (unsigned long long)published(q.x) << 32 | __float_as_uint(P.x);
+    const unsigned long long v = (unsigned long long)published(q.y) << 32 | __float_as_uint(P.y);
+    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(u), "l"(v) : "memory");
+}
+
+// (P.x, q.x, P.y, q.y); each channel's pair is one 64-bit access, so a q that is there
+// has its P
+__device__ __forceinline__ bool get_agg(const ulonglong2* p, float4& r) {
+    unsigned long long u, v;
+    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(u), "=l"(v) : "l"(p) : "memory");
+    r = make_float4(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)),
+                    __uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+    return (uint32_t)(u >> 32) != kNotYet && (uint32_t)(v >> 32) != kNotYet;
+}
+
+__device__ __forceinline__ void put_inc(uint2* p, float2 h) {
+    asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(published(h.x)),
+                 "r"(published(h.y))
+                 : "memory");
+}
+
+__device__ __forceinline__ bool get_inc(const uint2* p, float2& h) {
+    uint32_t u, v;
+    asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(u), "=r"(v) : "l"(p) : "memory");
+    h = make_float2(__uint_as_float(u), __uint_as_float(v));
+    return u != kNotYet && v != kNotYet;
+}
+
+struct Look {
+    float4 v[kLook][32];  // of the tile i + 1 before: its aggregate, or its state in x, z
+    int state[kLook];     // whether it is the state
+};
+
+// One warp's part of a look-back: waits until the tiles it looks at have
+// published something (every lane publishes, those past the channels too).
+template <int WARPS>
+__device__ __forceinline__ bool look(const LinArgs& a, Look& s, int seq, int blk, int warp, int lane) {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < kLook / WARPS; ++i) {
+        const int w = warp + i * WARPS, j = seq - 1 - w;
+        if (j < 0) {
+            if (lane == 0) s.state[w] = 0;
+            continue;
+        }
+        const size_t o = ((size_t)j * a.blocks + blk) * 32 + lane;
+        uint32_t polls = 0;
+        while (true) {
+            float2 h;
+            float4 r;
+            const bool inc = get_inc(a.inc + o, h), agg = get_agg(a.agg + o, r);
+            if (__all_sync(0xffffffffu, inc)) {
+                s.v[w][lane] = make_float4(h.x, 0.0f, h.y, 0.0f);
+                if (lane == 0) s.state[w] = 1;
+                break;
+            }
+            if (__all_sync(0xffffffffu, agg)) {
+                s.v[w][lane] = r;
+                if (lane == 0) s.state[w] = 0;
+                break;
+            }
+            if (++polls >= a.spin_limit) {
+                ok = false;
+                break;
+            }
+            if (polls > 4) __nanosleep(40);
+        }
+    }
+    return ok;
+}
+
+// ---------------------------------------------------- packed pairs of fp32
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// sigmoid(v) and the t = e^-v it comes from, for |v| < 80 or where an infinite t
+// gives the right 0
+__device__ __forceinline__ float2 sigmoid2(float2 v, float2& t) {
+    const float2 e = mul2(v, both(-kLog2e));
+    t = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+    const float2 d = add2(t, both(1.0f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// The arithmetic of a step for two channels.  FAST: gates within |f| < 80.
+template <bool FAST>
+struct Step {
+    __device__ static void gates(float2 f, float2& a, float2& om) {
+        if constexpr (FAST) {
+            float2 t;
+            a = sigmoid2(f, t);
+            om = mul2(t, a);
         } else {
-            if (valid) {
-                float* g = a.agg + ((size_t)seq * stride + chan) * 2;
-                __stcg(reinterpret_cast<float2*>(g), make_float2(P.x, q.x));
-                if (both) __stcg(reinterpret_cast<float2*>(g) + 1, make_float2(P.y, q.y));
-            }
-            __syncwarp();
-            if (lane == 0) st_release_gpu(flags + (size_t)seq * a.blocks, kFlagAgg);
-            int j_hi = seq - 1;
-            uint32_t polls = 0, ns = 20;
-            while (true) {
-                const int j = j_hi - lane;
-                uint32_t f = kFlagNone;
-                if (j >= 0) f = ld_acquire_gpu(flags + (size_t)j * a.blocks);
-                const uint32_t inc_mask = __ballot_sync(0xffffffffu, f == kFlagInc);
-                const uint32_t none_mask = __ballot_sync(0xffffffffu, f == kFlagNone);
-                const int first = inc_mask ? __ffs(inc_mask) - 1 : 32;
-                const uint32_t below = first >= 32 ? 0xffffffffu : ((1u << first) - 1u);
-                if ((none_mask & below) == 0) {
-                    if (first < 32) { j_inc = j_hi - first; break; }
-                    j_hi -= 32;  // 32 aggregates and no inclusive state: further back
-                    continue;
-                }
-                if (++polls >= a.spin_limit) { ok = false; break; }
-                __nanosleep(ns);
-                ns = ns < 160 ? ns * 2 : 160;
-            }
-            if (!ok && lane == 0) record_status(a.status, SSM_ERR_TIMEOUT);
-        }
-        __syncwarp();
-        if (ok && valid) {
-            const float* s = a.inc + (size_t)j_inc * stride + chan;
-            h.x = __ldcg(s);
-            if (both) h.y = __ldcg(s + 1);
-#pragma unroll 4
-            for (int j = j_inc + 1; j < seq; ++j) {
-                const float2* g =
-                    reinterpret_cast<const float2*>(a.agg + ((size_t)j * stride + chan) * 2);
-                const float2 u = __ldcg(g);
-                h.x = step(u.x, h.x, u.y);
-                if (both) {
-                    const float2 w = __ldcg(g + 1);
-                    h.y = step(w.x, h.y, w.y);
-                }
-            }
+            gate(f.x, a.x, om.x);
+            gate(f.y, a.y, om.y);
         }
     }
-    const float2 end = make_float2(step(P.x, h.x, q.x), step(P.y, h.y, q.y));
-    if (seq == a.tiles - 1) {
-        if (a.last && valid) {
-            a.last[chan] = end.x;
-            if (both) a.last[chan + 1] = end.y;
-        }
+    __device__ static float2 input(float2 om, float2 x) {  // (1 - a) x
+        if constexpr (FAST) return mul2(om, x);
+        return make_float2(input_term(om.x, x.x), input_term(om.y, x.y));
+    }
+    __device__ static float2 next(float2 a, float2 h, float2 b) {  // a h + b
+        if constexpr (FAST) return fma2(a, h, b);
+        return make_float2(step(a.x, h.x, b.x), step(a.y, h.y, b.y));
+    }
+    __device__ static float2 decay(float2 a, float2 h) {  // a h
+        if constexpr (FAST) return mul2(a, h);
+        return make_float2(step(a.x, h.x, 0.0f), step(a.y, h.y, 0.0f));
+    }
+    // lam (h - x) a (1 - a)
+    __device__ static float2 dgate(float2 a, float2 om, float2 lam, float2 h, float2 x) {
+        const float2 s = mul2(a, om);
+        const float2 d = mul2(mul2(lam, fma2(x, both(-1.0f), h)), s);
+        if constexpr (FAST) return d;
+        return make_float2(s.x == 0.0f ? 0.0f : d.x, s.y == 0.0f ? 0.0f : d.y);
+    }
+};
+
+// whether every one of a lane's raw gate pairs lies within |f| < 80
+template <typename T, int S>
+__device__ __forceinline__ bool all_fast(const void* const* rows) {
+    if constexpr (sizeof(T) == 2) {
+        __nv_bfloat162 m = __habs2(*static_cast<const __nv_bfloat162*>(rows[0]));
+#pragma unroll
+        for (int k = 1; k < S; ++k)
+            m = __hmax2_nan(m, __habs2(*static_cast<const __nv_bfloat162*>(rows[k])));
+        return __low2float(m) < kFastGate && __high2float(m) < kFastGate;
     } else {
-        if (valid) {
-            float* s = a.inc + (size_t)seq * stride + chan;
-            __stcg(s, end.x);
-            if (both) __stcg(s + 1, end.y);
+        bool ok = true;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const float2 f = *static_cast<const float2*>(rows[k]);
+            ok = ok && fabsf(f.x) < kFastGate && fabsf(f.y) < kFastGate;
         }
-        __syncwarp();
-        if (lane == 0 && !(a.drop_first_publish && seq == 0))
-            st_release_gpu(flags + (size_t)seq * a.blocks, kFlagInc);
+        return ok;
     }
-    return h;
 }
 
 // ---------------------------------------------------------- tile kernels
 
-// Shared memory of one CTA: the ring of input tiles, the warps' aggregates
-// (forward P, q; gradient also the reverse q) and the tile's entry state.
-template <typename T, int S, int NIN, int STAGES>
+template <typename T, int NIN>
 struct LinSmem {
-    static constexpr int kTile = kWarps * S * kCh * (int)sizeof(T);
+    static constexpr int kTile = kSteps * kCh * (int)sizeof(T);  // of one input
     static constexpr int kStage = NIN * kTile;
 };
 
 // GRAD false: inputs f, x[, z], output y.  GRAD true: inputs f, x, dy[, z],
-// outputs df, dx[, dz].
-template <typename T, typename TO, int S, int STAGES, int BYTES, bool GATED, bool GRAD>
-__global__ void __launch_bounds__(kThreads, 2) linrec_tile_kernel(const LinArgs a) {
+// outputs df, dx[, dz].  BYTES 16: TMA.
+template <typename T, typename TO, int WARPS, int STAGES, int BYTES, bool GATED, bool GRAD, int MINB>
+__global__ void __launch_bounds__(WARPS * 32, MINB)
+    linrec_tile_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
     constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
-    constexpr int STEPS = kWarps * S;
-    using SM = LinSmem<T, S, NIN, STAGES>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 s_P[kWarps][32], s_q[kWarps][32], s_r[GRAD ? kWarps : 1][32];
-    __shared__ float2 s_h[32];
-    __shared__ int s_item[STAGES + 1];
+    constexpr int S = kSteps / WARPS;
+    constexpr bool TMA = BYTES == 16;
+    // results of the inputs' size take their places in the tile
+    constexpr bool INPLACE = TMA && sizeof(T) == sizeof(TO);
+    using SM = LinSmem<T, NIN>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ float2 s_P[WARPS][32], s_q[WARPS][32], s_r[GRAD ? WARPS : 1][32];
+    __shared__ Look s_look;
+    __shared__ uint64_t full[STAGES];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int items = a.blocks * a.tiles;
-    int own = blockIdx.x;  // without tickets: blockIdx.x, + gridDim.x, ...
 
-    auto next_item = [&]() -> int {  // thread 0
-        if (a.head) return (int)min(atomicAdd(&a.head->ticket, 1u), 0x7fffffffu);
-        const int i = own;
-        own = own < items ? own + (int)gridDim.x : own;
-        return i;
+    auto place = [&](int item, int& seq, int& tile, int& b, int& c0) {
+        seq = item / a.blocks;
+        const int blk = item - seq * a.blocks;
+        tile = GRAD ? a.tiles - 1 - seq : seq;
+        b = blk / a.cblocks;
+        c0 = (blk - b * a.cblocks) * kCh;
+        return blk;
     };
-    auto fetch = [&](int item, int stage) {
+    // the tile `item` into `stage`: TMA by one thread, else by all
+    auto fetch = [&](long long item, int stage) {
         if (item < items) {
-            const int seq = item / a.blocks, blk = item % a.blocks;
-            const int tile = GRAD ? a.tiles - 1 - seq : seq;
-            const int b = blk / a.cblocks, c0 = (blk % a.cblocks) * kCh;
+            int seq, tile, b, c0;
+            place((int)item, seq, tile, b, c0);
+            uint8_t* dst = smem + stage * SM::kStage;
+            if constexpr (TMA) {
+                mbar_arrive_expect_tx(&full[stage], SM::kStage);
 #pragma unroll
-            for (int i = 0; i < NIN; ++i)
-                load_tile<T, STEPS, BYTES>(smem + stage * SM::kStage + i * SM::kTile, a.in[i],
-                                           a.stride[i], b, tile * STEPS, c0, a.seqlen, a.dim);
+                for (int i = 0; i < NIN; ++i)
+                    tma_load_3d(dst + i * SM::kTile, &maps.in[i], &full[stage], c0, tile * kSteps, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NIN; ++i)
+                    load_tile<T, BYTES>(dst + i * SM::kTile, a.in[i], a.stride[i], b,
+                                               tile * kSteps, c0, a.seqlen, a.dim);
+            }
         }
-        copy_commit();
+        if constexpr (!TMA) copy_commit();
+    };
+    // the results of a tile out of `stage` (one thread)
+    auto send = [&](int item, int stage) {
+        int seq, tile, b, c0;
+        place(item, seq, tile, b, c0);
+        uint8_t* src = smem + stage * SM::kStage;
+        if constexpr (!GRAD) {
+            if (a.out[0]) tma_store_3d(&maps.out[0], src, c0, tile * kSteps, b);
+        } else {
+            tma_store_3d(&maps.out[0], src, c0, tile * kSteps, b);
+            tma_store_3d(&maps.out[1], src + SM::kTile, c0, tile * kSteps, b);
+            if constexpr (GATED)
+                tma_store_3d(&maps.out[2], src + 3 * SM::kTile, c0, tile * kSteps, b);
+        }
     };
 
-    if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < STAGES; ++i) s_item[i] = next_item();
-        // one tile per sequence: no waits, so nothing else writes the status
-        if (!a.head && blockIdx.x == 0 && !a.keep_status) *a.status = 0;
+    // one tile per sequence: no waits, so nothing else writes the status
+    if (tid == 0 && a.tiles == 1 && blockIdx.x == 0 && !a.keep_status) *a.status = 0;
+    if constexpr (TMA) {
+        if (tid == 0) {
+            for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    int queue[STAGES];  // this tile and the ones being fetched
+    // tile i of this CTA is fetched at its tile i - (STAGES - 2), when the ring's
+    // place has been read out (two tiles back) and sent
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) queue[i] = s_item[i];
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fetch(queue[i], i);
+    for (int i = 0; i < STAGES - 2; ++i)
+        if (!TMA || tid == 0) fetch((long long)blockIdx.x + (long long)i * gridDim.x, i);
 
-    for (int turn = 0; queue[0] < items; ++turn) {
+    int turn = 0, before = -1;
+    bool ok = true;
+    for (int item = blockIdx.x; item < items; before = item, item += gridDim.x, ++turn) {
         const int stage = turn % STAGES;
-        copy_wait<STAGES - 2>();
-        __syncthreads();  // the tile is there; the previous one is done with
-        int ahead = 0;
-        if (tid == 0) ahead = next_item();  // read back after the next barriers
-        fetch(queue[STAGES - 1], (turn + STAGES - 1) % STAGES);
+        if constexpr (TMA) ok = mbar_wait(&full[stage], (turn / STAGES) & 1, a.status);
+        else copy_wait<STAGES - 3>();
+        // the tile is there, the previous one is done with
+        if (!__syncthreads_and(ok)) break;
+        if (!TMA || tid == 0) {
+            if constexpr (INPLACE) {
+                if (before >= 0) send(before, (turn - 1) % STAGES);
+                bulk_commit();
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            }
+            fetch((long long)item + (long long)(STAGES - 2) * gridDim.x,
+                  (turn + STAGES - 2) % STAGES);
+        }
 
-        const int seq = queue[0] / a.blocks, blk = queue[0] % a.blocks;
-        const int tile = GRAD ? a.tiles - 1 - seq : seq;
-        const int b = blk / a.cblocks, c = (blk % a.cblocks) * kCh + lane * 2;
-        const bool valid = c < a.dim, both = c + 1 < a.dim;
+        int seq, tile, b, c;
+        const int blk = place(item, seq, tile, b, c);
+        c += lane * 2;
+        const bool valid = c < a.dim, two = c + 1 < a.dim;
         const size_t chan = (size_t)b * a.dim + c;
-        const int t0 = tile * STEPS + warp * S;
-        const uint8_t* base = smem + stage * SM::kStage;
-        auto at = [&](int i, int k) -> const void* {
-            return base + i * SM::kTile + ((warp * S + k) * kCh + lane * 2) * (int)sizeof(T);
+        const int t0 = tile * kSteps + warp * S;
+        uint8_t* base = smem + stage * SM::kStage + (warp * S * kCh + lane * 2) * (int)sizeof(T);
+        auto at = [&](int i, int k) -> void* {
+            return base + i * SM::kTile + k * kCh * (int)sizeof(T);
         };
 
         // the state entering the tile, for the gradient's replay
         float2 hk = make_float2(0.0f, 0.0f);
         if constexpr (GRAD) {
             if (valid) {
-                if (tile * STEPS > 0)
-                    hk = load_state2(a.keep + (size_t)(tile * STEPS / kKeep) * a.batch * a.dim,
-                                     chan, both);
+                if (tile > 0)
+                    hk = load_state2(a.keep + (size_t)tile * a.batch * a.dim, chan, two);
                 else if (a.first)
-                    hk = load_state2(a.first, chan, both);
+                    hk = load_state2(a.first, chan, two);
             }
         }
 
+        const void* rows[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k) rows[k] = at(0, k);
+        const bool fast = __all_sync(0xffffffffu, all_fast<T, S>(rows) && t0 + S <= a.seqlen);
+
         // ---- the warp's steps from zero
         float2 ga[S], gb[S];  // a_t, and b_t (forward) or 1 - a_t (gradient)
-        float2 P = make_float2(1.0f, 1.0f), q = make_float2(0.0f, 0.0f);
-        float2 r = make_float2(0.0f, 0.0f);
+        float2 P = both(1.0f), q = both(0.0f);
+        auto scan = [&](auto fast_) {
+            constexpr bool F = decltype(fast_)::value;
 #pragma unroll
-        for (int k = 0; k < S; ++k) {
-            const float2 f = Pair<T>::get(at(0, k)), x = Pair<T>::get(at(1, k));
-            float2 om, bt;
-            gate(f.x, ga[k].x, om.x);
-            gate(f.y, ga[k].y, om.y);
-            if (t0 + k >= a.seqlen) {
-                ga[k] = make_float2(1.0f, 1.0f);
-                om = make_float2(0.0f, 0.0f);
+            for (int k = 0; k < S; ++k) {
+                const float2 x = Pair<T>::get(at(1, k));
+                float2 om;
+                Step<F>::gates(Pair<T>::get(at(0, k)), ga[k], om);
+                if (!F && t0 + k >= a.seqlen) {
+                    ga[k] = both(1.0f);
+                    om = both(0.0f);
+                }
+                const float2 bt = Step<F>::input(om, x);
+                gb[k] = GRAD ? om : bt;
+                q = Step<F>::next(ga[k], q, bt);
+                P = mul2(P, ga[k]);
             }
-            bt.x = input_term(om.x, x.x);
-            bt.y = input_term(om.y, x.y);
-            gb[k] = GRAD ? om : bt;
-            q.x = step(ga[k].x, q.x, bt.x);
-            q.y = step(ga[k].y, q.y, bt.y);
-            P.x *= ga[k].x;
-            P.y *= ga[k].y;
-        }
-        // dh_t = dy_t silu(z_t), 0 past the sequence (the tile is zero there)
-        auto grad_in = [&](int k) -> float2 {
-            float2 d = Pair<T>::get(at(2, k));
-            if constexpr (GATED) {
-                const float2 z = Pair<T>::get(at(3, k));
-                d.x *= silu_f(z.x);
-                d.y *= silu_f(z.y);
+            if constexpr (GRAD) {
+                // mu through the steps: dh_t = dy_t silu(z_t), 0 past the sequence
+                // (the tile is zero there)
+                float2 r = both(0.0f);
+#pragma unroll
+                for (int k = S - 1; k >= 0; --k) {
+                    float2 d = Pair<T>::get(at(2, k));
+                    if constexpr (GATED) {
+                        const float2 z = Pair<T>::get(at(3, k));
+                        float2 t;
+                        d = mul2(d, mul2(z, sigmoid2(z, t)));
+                    }
+                    r = Step<F>::decay(ga[k], add2(r, d));
+                }
+                s_r[warp][lane] = r;
             }
-            return d;
         };
-        if constexpr (GRAD) {
-#pragma unroll
-            for (int k = S - 1; k >= 0; --k) {
-                const float2 d = grad_in(k);
-                r.x = step(ga[k].x, r.x + d.x, 0.0f);
-                r.y = step(ga[k].y, r.y + d.y, 0.0f);
-            }
-            s_r[warp][lane] = r;
-        }
+        if (fast) scan(std::true_type{});
+        else scan(std::false_type{});
         s_P[warp][lane] = P;
         s_q[warp][lane] = q;
         __syncthreads();
 
-        // ---- across warps and tiles
+        // ---- across tiles: the state (gradient: mu) entering this one
+        float2 in = both(0.0f), TP = both(1.0f), tq = both(0.0f);
         if (warp == 0) {
-            float2 TP = make_float2(1.0f, 1.0f), tq = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const int w = GRAD ? kWarps - 1 - i : i;
-                const float2 p = s_P[w][lane], v = GRAD ? s_r[w][lane] : s_q[w][lane];
-                tq.x = step(p.x, tq.x, v.x);
-                tq.y = step(p.y, tq.y, v.y);
-                TP.x *= p.x;
-                TP.y *= p.y;
+            for (int i = 0; i < WARPS; ++i) {
+                const int w = GRAD ? WARPS - 1 - i : i;
+                tq = Step<false>::next(s_P[w][lane], tq, GRAD ? s_r[w][lane] : s_q[w][lane]);
+                TP = mul2(TP, s_P[w][lane]);
             }
-            s_h[lane] = look_back(a, seq, blk, chan, valid, both, TP, tq);
-            if (tid == 0) s_item[STAGES] = ahead;
         }
-        __syncthreads();
+        const size_t mine = ((size_t)seq * a.blocks + blk) * 32 + lane;
+        if (seq == 0) {
+            if (a.h0 && valid) in = load_state2(a.h0, chan, two);
+        } else {
+            // the last tile's values are nobody's to read
+            if (warp == 0 && seq < a.tiles - 1) put_agg(a.agg + mine, TP, tq);
+            while (true) {
+                const bool found = look<WARPS>(a, s_look, seq, blk, warp, lane);
+                const bool all = __syncthreads_and(found);
+                int w = 0;
+                while (w < kLook && !s_look.state[w]) ++w;
+                if (!all) {
+                    if (tid == 0) record_status(a.status, SSM_ERR_TIMEOUT);
+                    in = both(__int_as_float(0x7fffffff));
+                    break;
+                }
+                if (w < kLook) {
+                    // from the newest state through the aggregates after it, in
+                    // order: the same operations wherever the state was found
+                    const float4 h = s_look.v[w][lane];
+                    in = make_float2(h.x, h.z);
+                    for (--w; w >= 0; --w) {
+                        const float4 g = s_look.v[w][lane];
+                        in = Step<false>::next(make_float2(g.x, g.z), in, make_float2(g.y, g.w));
+                    }
+                    break;
+                }
+                __syncthreads();  // sixteen aggregates and no state: look again
+            }
+        }
+        if (warp == 0) {
+            const float2 end = Step<false>::next(TP, in, tq);
+            if (seq < a.tiles - 1) {
+                if (!(a.drop_first_publish && seq == 0)) put_inc(a.inc + mine, end);
+            } else if (a.last && valid) {
+                a.last[chan] = end.x;
+                if (two) a.last[chan + 1] = end.y;
+            }
+        }
 
+        // ---- the steps again from the warp's entry state
+        const size_t o = ((size_t)b * a.seqlen + t0) * a.dim + c;
         if constexpr (!GRAD) {
-            float2 h = s_h[lane];
-            for (int w = 0; w < warp; ++w) {
-                const float2 p = s_P[w][lane], v = s_q[w][lane];
-                h.x = step(p.x, h.x, v.x);
-                h.y = step(p.y, h.y, v.y);
-            }
-            if (a.keep && valid && t0 % kKeep == 0 && t0 < a.seqlen) {
-                float* s = a.keep + (size_t)(t0 / kKeep) * a.batch * a.dim + chan;
+            float2 h = in;
+            for (int w = 0; w < warp; ++w)
+                h = Step<false>::next(s_P[w][lane], h, s_q[w][lane]);
+            if (a.keep && warp == 0 && valid) {
+                float* s = a.keep + (size_t)tile * a.batch * a.dim + chan;
                 s[0] = h.x;
-                if (both) s[1] = h.y;
+                if (two) s[1] = h.y;
             }
-            if (a.out[0]) {
-                const size_t o = ((size_t)b * a.seqlen + t0) * a.dim + c;
+            auto replay = [&](auto fast_) {
+                constexpr bool F = decltype(fast_)::value;
 #pragma unroll
                 for (int k = 0; k < S; ++k) {
-                    h.x = step(ga[k].x, h.x, gb[k].x);
-                    h.y = step(ga[k].y, h.y, gb[k].y);
+                    h = Step<F>::next(ga[k], h, gb[k]);
                     float2 y = h;
                     if constexpr (GATED) {
                         const float2 z = Pair<T>::get(at(2, k));
-                        y.x *= silu_f(z.x);
-                        y.y *= silu_f(z.y);
+                        float2 t;
+                        y = mul2(y, mul2(z, sigmoid2(z, t)));
                     }
-                    if (valid && t0 + k < a.seqlen)
-                        put2<TO>(a.out[0], o + (size_t)k * a.dim, y, both, a.vec_out);
+                    if constexpr (INPLACE) Pair<TO>::put(at(0, k), y);
+                    else if (valid && t0 + k < a.seqlen)
+                        put2<TO>(a.out[0], o + (size_t)k * a.dim, y, two, a.vec_out);
                 }
+            };
+            if (a.out[0]) {
+                if (fast) replay(std::true_type{});
+                else replay(std::false_type{});
             }
         } else {
-            float2 h = hk, mu = s_h[lane];
-            for (int w = 0; w < warp; ++w) {
-                const float2 p = s_P[w][lane], v = s_q[w][lane];
-                h.x = step(p.x, h.x, v.x);
-                h.y = step(p.y, h.y, v.y);
-            }
-            for (int w = kWarps - 1; w > warp; --w) {
-                const float2 p = s_P[w][lane], v = s_r[w][lane];
-                mu.x = step(p.x, mu.x, v.x);
-                mu.y = step(p.y, mu.y, v.y);
-            }
-            float2 before[S];  // h_{t-1}
+            float2 h = hk, mu = in;
+            for (int w = 0; w < warp; ++w)
+                h = Step<false>::next(s_P[w][lane], h, s_q[w][lane]);
+            for (int w = WARPS - 1; w > warp; --w)
+                mu = Step<false>::next(s_P[w][lane], mu, s_r[w][lane]);
+            auto replay = [&](auto fast_) {
+                constexpr bool F = decltype(fast_)::value;
+                float2 prev[S];  // h_{t-1}
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
-                const float2 x = Pair<T>::get(at(1, k));
-                before[k] = h;
-                h.x = step(ga[k].x, h.x, input_term(gb[k].x, x.x));
-                h.y = step(ga[k].y, h.y, input_term(gb[k].y, x.y));
-            }
-            const size_t o = ((size_t)b * a.seqlen + t0) * a.dim + c;
+                for (int k = 0; k < S; ++k) {
+                    prev[k] = h;
+                    h = Step<F>::next(ga[k], h, Step<F>::input(gb[k], Pair<T>::get(at(1, k))));
+                }
 #pragma unroll
-            for (int k = S - 1; k >= 0; --k) {
-                const bool in = valid && t0 + k < a.seqlen;
-                const size_t ok = o + (size_t)k * a.dim;
-                const float2 x = Pair<T>::get(at(1, k));
-                float2 d = Pair<T>::get(at(2, k));
-                if constexpr (GATED) {
-                    const float2 z = Pair<T>::get(at(3, k));
-                    float2 dz;
-                    float sg = rcp_approx(1.0f + ex2_approx(z.x * -kLog2e));
-                    dz.x = d.x * h.x * sg * fmaf(z.x, 1.0f - sg, 1.0f);
-                    d.x *= z.x * sg;
-                    sg = rcp_approx(1.0f + ex2_approx(z.y * -kLog2e));
-                    dz.y = d.y * h.y * sg * fmaf(z.y, 1.0f - sg, 1.0f);
-                    d.y *= z.y * sg;
-                    if (in) put2<TO>(a.out[2], ok, dz, both, a.vec_out);
+                for (int k = S - 1; k >= 0; --k) {
+                    [[maybe_unused]] const bool inside = valid && t0 + k < a.seqlen;
+                    [[maybe_unused]] const size_t ok_ = o + (size_t)k * a.dim;
+                    const float2 x = Pair<T>::get(at(1, k));
+                    float2 d = Pair<T>::get(at(2, k));
+                    if constexpr (GATED) {
+                        const float2 z = Pair<T>::get(at(3, k));
+                        float2 t;
+                        const float2 sg = sigmoid2(z, t);
+                        const float2 si = mul2(z, sg);
+                        // silu' = sg (1 + z (1 - sg)) = sg + si - si sg
+                        const float2 ds = fma2(mul2(si, both(-1.0f)), sg, add2(sg, si));
+                        const float2 dz = mul2(mul2(d, h), ds);
+                        d = mul2(d, si);
+                        if constexpr (INPLACE) Pair<TO>::put(at(3, k), dz);
+                        else if (inside) put2<TO>(a.out[2], ok_, dz, two, a.vec_out);
+                    }
+                    const float2 lam = add2(d, mu);
+                    const float2 df = Step<F>::dgate(ga[k], gb[k], lam, prev[k], x);
+                    const float2 dx = Step<F>::input(gb[k], lam);
+                    if constexpr (INPLACE) {
+                        Pair<TO>::put(at(0, k), df);
+                        Pair<TO>::put(at(1, k), dx);
+                    } else if (inside) {
+                        put2<TO>(a.out[0], ok_, df, two, a.vec_out);
+                        put2<TO>(a.out[1], ok_, dx, two, a.vec_out);
+                    }
+                    mu = Step<F>::decay(ga[k], lam);
+                    h = prev[k];
                 }
-                const float2 lam = make_float2(d.x + mu.x, d.y + mu.y);
-                float2 df, dx;
-                dx.x = gb[k].x == 0.0f ? 0.0f : lam.x * gb[k].x;
-                dx.y = gb[k].y == 0.0f ? 0.0f : lam.y * gb[k].y;
-                const float sx = ga[k].x * gb[k].x, sy = ga[k].y * gb[k].y;
-                df.x = sx == 0.0f ? 0.0f : lam.x * (before[k].x - x.x) * sx;
-                df.y = sy == 0.0f ? 0.0f : lam.y * (before[k].y - x.y) * sy;
-                if (in) {
-                    put2<TO>(a.out[0], ok, df, both, a.vec_out);
-                    put2<TO>(a.out[1], ok, dx, both, a.vec_out);
-                }
-                mu.x = step(ga[k].x, lam.x, 0.0f);
-                mu.y = step(ga[k].y, lam.y, 0.0f);
-                h = before[k];
-            }
+            };
+            if (fast) replay(std::true_type{});
+            else replay(std::false_type{});
         }
-#pragma unroll
-        for (int i = 0; i + 1 < STAGES; ++i) queue[i] = queue[i + 1];
-        queue[STAGES - 1] = s_item[STAGES];
+        if constexpr (INPLACE) fence_proxy_async_smem();
     }
-    copy_wait<0>();
+    if constexpr (INPLACE) {
+        __syncthreads();
+        if (tid == 0 && ok && before >= 0) {
+            send(before, (turn + STAGES - 1) % STAGES);
+            bulk_commit();
+        }
+        if (tid == 0) bulk_wait_all();
+    }
+    if constexpr (!TMA) copy_wait<0>();
+    // a load that never came: leave what is in flight time to land
+    if (!ok)
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // -------------------------------------------------------- short sequences
@@ -521,18 +689,18 @@ __global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
     if (i == 0 && !a.keep_status) *a.status = 0;
     if (i >= (long long)a.batch * pairs) return;
     const int b = (int)(i / pairs), c = (int)(i % pairs) * 2;
-    const bool both = c + 1 < a.dim;
+    const bool two = c + 1 < a.dim;
     const size_t chan = (size_t)b * a.dim + c;
     auto get = [&](int k, int t) -> float2 {
         const T* p = static_cast<const T*>(a.in[k]) + ((long long)b * a.seqlen + t) * a.stride[k] + c;
         if constexpr (VEC) return Pair<T>::get(p);
-        return make_float2(to_f32(p[0]), both ? to_f32(p[1]) : 0.0f);
+        return make_float2(to_f32(p[0]), two ? to_f32(p[1]) : 0.0f);
     };
     float2 h = make_float2(0.0f, 0.0f);
-    if (a.h0) h = load_state2(a.h0, chan, both);
+    if (a.h0) h = load_state2(a.h0, chan, two);
     if (a.keep && a.seqlen > 0) {
         a.keep[chan] = h.x;
-        if (both) a.keep[chan + 1] = h.y;
+        if (two) a.keep[chan + 1] = h.y;
     }
 #pragma unroll 2
     for (int t = 0; t < a.seqlen; ++t) {
@@ -549,11 +717,11 @@ __global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
             y.y *= silu_f(z.y);
         }
         if (a.out[0])
-            put2<TO>(a.out[0], ((size_t)b * a.seqlen + t) * a.dim + c, y, both, a.vec_out);
+            put2<TO>(a.out[0], ((size_t)b * a.seqlen + t) * a.dim + c, y, two, a.vec_out);
     }
     if (a.last) {
         a.last[chan] = h.x;
-        if (both) a.last[chan + 1] = h.y;
+        if (two) a.last[chan + 1] = h.y;
     }
 }
 
@@ -561,94 +729,98 @@ __global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Steps of a forward tile by type: 128 of bf16 or 64 of fp32 are 16 KB of one
-// input; the gradient keeps three values per step in registers, so 64.
-constexpr int kFwdStepsBf16 = 128, kFwdStepsF32 = 64, kBwdSteps = 64;
+int tiles_of(int seqlen) { return seqlen / kSteps + (seqlen % kSteps != 0); }
 
-int tiles_of(int seqlen, int steps) { return (seqlen + steps - 1) / steps; }
-
-// header, flags, aggregates and inclusive states of `tiles` tiles
+// header, aggregates and inclusive states of `tiles` tiles
 size_t scan_bytes(int batch, int dim, int tiles) {
     const size_t blocks = (size_t)batch * ((dim + kCh - 1) / kCh);
-    return 256 + (tiles > 1 ? round256((size_t)tiles * blocks * 4) +
-                                  round256((size_t)tiles * batch * dim * 8) +
-                                  round256((size_t)tiles * batch * dim * 4)
-                            : 0);
+    return sizeof(LinHeader) + (tiles > 1 ? (size_t)tiles * blocks * 32 * 24 : 0);
 }
 
 bool sizes_ok(int batch, int seqlen, int dim) { return batch >= 0 && seqlen >= 0 && dim >= 0; }
 
-// one int counts the tiles of all blocks, with room for the tickets past the end
+// one int counts the tiles of all blocks
 bool sizes_fit(int batch, int seqlen, int dim) {
     const double blocks = (double)batch * ((dim + kCh - 1) / kCh);
-    return blocks * tiles_of(seqlen, 64) < 2.0e9 && (double)batch * dim < 2.0e9;
+    return blocks * tiles_of(seqlen) < 2.0e9 && (double)batch * dim < 2.0e9;
 }
 
-// Fills in the work area of one scan; returns the bytes it takes.
-size_t place(LinArgs& a, uint8_t* ws, int tiles) {
+// Fills in the work area of one scan.
+void place(LinArgs& a, uint8_t* ws, int tiles) {
     a.cblocks = (a.dim + kCh - 1) / kCh;
     a.blocks = a.batch * a.cblocks;
     a.tiles = tiles;
     a.status = reinterpret_cast<uint32_t*>(ws) + 1;
-    const size_t need = scan_bytes(a.batch, a.dim, tiles);
-    if (tiles > 1) {
-        a.head = reinterpret_cast<LinHeader*>(ws);
-        size_t o = 256;
-        a.flags = reinterpret_cast<uint32_t*>(ws + o);
-        o += round256((size_t)tiles * a.blocks * 4);
-        a.agg = reinterpret_cast<float*>(ws + o);
-        o += round256((size_t)tiles * a.batch * a.dim * 8);
-        a.inc = reinterpret_cast<float*>(ws + o);
-    }
-    return need;
+    a.agg = reinterpret_cast<ulonglong2*>(ws + sizeof(LinHeader));
+    a.inc = reinterpret_cast<uint2*>(a.agg + (size_t)tiles * a.blocks * 32);
 }
 
-bool set_smem(const void* kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+// (batch, seqlen, dim) with rows `stride` elements apart, boxes of a tile
+bool make_map(CUtensorMap* map, const void* base, size_t es, long long stride, const LinArgs& a) {
+    auto fn = ssm_host::encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.seqlen, (cuuint64_t)a.batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * es, (cuuint64_t)stride * es * a.seqlen};
+    const cuuint32_t box[3] = {(cuuint32_t)kCh, (cuuint32_t)kSteps, 1}, one[3] = {1, 1, 1};
+    return fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+              const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, typename TO, int BYTES, bool GATED, bool GRAD>
+bool launch_tile(LinArgs& a, cudaStream_t s) {
+    constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
+    // 16 warps an SM, and as many stages as fit in its shared memory
+    constexpr int WARPS = sizeof(T) == 2 ? 8 : 16, MINB = 16 / WARPS;
+    constexpr int kStage = LinSmem<T, NIN>::kStage;
+    constexpr int STAGES = 96 * 1024 * WARPS / 8 / kStage;
+    static_assert(STAGES >= 3, "one tile being read out, one at work, one coming in");
+    constexpr int smem = STAGES * kStage;
+    auto kernel = linrec_tile_kernel<T, TO, WARPS, STAGES, BYTES, GATED, GRAD, MINB>;
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    int dev = 0, sms = 0, per_sm = 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, WARPS * 32, smem) !=
+            cudaSuccess ||
+        per_sm < 1)
+        return false;
+    LinMaps maps{};
+    if constexpr (BYTES == 16) {
+        for (int i = 0; i < NIN; ++i)
+            if (!make_map(&maps.in[i], a.in[i], sizeof(T), a.stride[i], a)) return false;
+        for (int i = 0; i < 3 && sizeof(T) == sizeof(TO); ++i)
+            if (a.out[i] && !make_map(&maps.out[i], a.out[i], sizeof(TO), a.dim, a))
+                return false;
+    }
+    const long long items = (long long)a.blocks * a.tiles;
+    const unsigned grid = (unsigned)std::min<long long>(items, (long long)per_sm * sms);
+    if (a.tiles == 1) {
+        kernel<<<grid, WARPS * 32, smem, s>>>(maps, a);
+        return cudaGetLastError() == cudaSuccess;
+    }
+    if ((!a.keep_status && cudaMemsetAsync(a.status, 0, 4, s) != cudaSuccess) ||
+        cudaMemsetAsync(a.agg, 0xff, (size_t)items * 32 * 24, s) != cudaSuccess)
+        return false;
+    void* args[] = {&maps, &a};
+    return cudaLaunchCooperativeKernel(fn, dim3(grid), dim3(WARPS * 32), args, smem, s) ==
            cudaSuccess;
 }
 
-template <typename T, typename TO, int S, int BYTES, bool GATED, bool GRAD>
-bool launch_tile(const LinArgs& a, cudaStream_t s) {
-    constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
-    // the ring fills about half of an SM's shared memory
-    constexpr int kTile = LinSmem<T, S, NIN, 1>::kStage;
-    constexpr int STAGES = BYTES == 0 ? 2 : kTile * 3 <= 100 * 1024 ? 3 : 2;
-    constexpr int smem = STAGES * kTile;
-    auto kernel = linrec_tile_kernel<T, TO, S, STAGES, BYTES, GATED, GRAD>;
-    if (!set_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return false;
-    const long long items = (long long)a.blocks * a.tiles;
-    const unsigned grid = (unsigned)std::min<long long>(items, 2ll * sms);
-    if (a.head) {
-        // header and flags are neighbours; an earlier scan's status stays
-        const size_t flags = round256((size_t)a.tiles * a.blocks * 4);
-        if (a.keep_status) {
-            if (cudaMemsetAsync(&a.head->ticket, 0, sizeof(uint32_t), s) != cudaSuccess ||
-                cudaMemsetAsync(a.flags, 0, flags, s) != cudaSuccess)
-                return false;
-        } else if (cudaMemsetAsync(a.head, 0, sizeof(LinHeader) + flags, s) != cudaSuccess) {
-            return false;
-        }
-    }
-    kernel<<<grid, kThreads, smem, s>>>(a);
-    return cudaGetLastError() == cudaSuccess;
-}
-
-template <typename T, typename TO, int S, bool GRAD>
-bool launch_by(const LinArgs& a, int bytes, bool gated, cudaStream_t s) {
+template <typename T, typename TO, bool GRAD>
+bool launch_by(LinArgs& a, int bytes, bool gated, cudaStream_t s) {
     if (bytes == 16)
-        return gated ? launch_tile<T, TO, S, 16, true, GRAD>(a, s)
-                     : launch_tile<T, TO, S, 16, false, GRAD>(a, s);
+        return gated ? launch_tile<T, TO, 16, true, GRAD>(a, s)
+                     : launch_tile<T, TO, 16, false, GRAD>(a, s);
     if (bytes == 4)
-        return gated ? launch_tile<T, TO, S, 4, true, GRAD>(a, s)
-                     : launch_tile<T, TO, S, 4, false, GRAD>(a, s);
+        return gated ? launch_tile<T, TO, 4, true, GRAD>(a, s)
+                     : launch_tile<T, TO, 4, false, GRAD>(a, s);
     if constexpr (sizeof(T) == 2)
-        return gated ? launch_tile<T, TO, S, 0, true, GRAD>(a, s)
-                     : launch_tile<T, TO, S, 0, false, GRAD>(a, s);
+        return gated ? launch_tile<T, TO, 0, true, GRAD>(a, s)
+                     : launch_tile<T, TO, 0, false, GRAD>(a, s);
     return false;
 }
 
@@ -698,15 +870,11 @@ bool run_forward(LinArgs& a, ssm_dtype_t in, ssm_dtype_t out, bool gated, cudaSt
                       a.stride[i] % 2 == 0;
             return launch_walk<T, TO>(a, vec, gated, s);
         }
-        constexpr int S = (sizeof(T) == 2 ? kFwdStepsBf16 : kFwdStepsF32) / kWarps;
-        return launch_by<T, TO, S, false>(a, copy_bytes(a, nin, es), gated, s);
+        return launch_by<T, TO, false>(a, copy_bytes(a, nin, es), gated, s);
     });
 }
 
-int fwd_tiles(int seqlen, ssm_dtype_t in) {
-    return seqlen <= kWalkSteps ? 1
-                                : tiles_of(seqlen, in == SSM_BF16 ? kFwdStepsBf16 : kFwdStepsF32);
-}
+int fwd_tiles(int seqlen) { return seqlen <= kWalkSteps ? 1 : tiles_of(seqlen); }
 
 struct Span { const void* p; size_t n; };
 
@@ -719,17 +887,17 @@ size_t strided_bytes(long long steps, int dim, long long stride, size_t es) {
 
 extern "C" size_t ssm_linrec_checkpoint_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim)) return 0;
-    return (size_t)tiles_of(seqlen, kKeep) * batch * dim * 4;
+    return (size_t)tiles_of(seqlen) * batch * dim * 4;
 }
 
 extern "C" size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim) || !sizes_fit(batch, seqlen, dim)) return 0;
-    return scan_bytes(batch, dim, tiles_of(seqlen, 64));
+    return scan_bytes(batch, dim, tiles_of(seqlen));
 }
 
 extern "C" size_t ssm_linrec_bwd_workspace_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim) || !sizes_fit(batch, seqlen, dim)) return 0;
-    return scan_bytes(batch, dim, tiles_of(seqlen, 64)) +
+    return scan_bytes(batch, dim, tiles_of(seqlen)) +
            round256(ssm_linrec_checkpoint_bytes(batch, seqlen, dim));
 }
 
@@ -783,7 +951,7 @@ extern "C" ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void*
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
     a.vec_out = dim % 2 == 0;
     ssm_internal::lookback_setting(&a.spin_limit, &a.drop_first_publish);
-    place(a, static_cast<uint8_t*>(workspace), fwd_tiles(seqlen, in_dtype));
+    place(a, static_cast<uint8_t*>(workspace), fwd_tiles(seqlen));
     return run_forward(a, in_dtype, out_dtype, z != nullptr, static_cast<cudaStream_t>(stream))
                ? SSM_OK : SSM_ERR_CUDA;
 }
@@ -848,8 +1016,8 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
         // the forward again, states only
         LinArgs w = a;
         w.h0 = initial_state;
-        w.keep = reinterpret_cast<float*>(ws + scan_bytes(batch, dim, tiles_of(seqlen, 64)));
-        place(w, ws, fwd_tiles(seqlen, in_dtype));
+        w.keep = reinterpret_cast<float*>(ws + scan_bytes(batch, dim, tiles_of(seqlen)));
+        place(w, ws, fwd_tiles(seqlen));
         if (!run_forward(w, in_dtype, in_dtype, false, s)) return SSM_ERR_CUDA;
         checkpoints = w.keep;
         a.keep_status = 1;
@@ -867,12 +1035,11 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
                          : cudaMemsetAsync(dinitial_state, 0, states * 4, s);
         return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
     }
-    place(a, ws, tiles_of(seqlen, kBwdSteps));
+    place(a, ws, tiles_of(seqlen));
     const bool ok = by_types(in_dtype, grad_dtype, [&](auto ti, auto to) -> bool {
         using T = decltype(ti);
         using TO = decltype(to);
-        return launch_by<T, TO, kBwdSteps / kWarps, true>(a, copy_bytes(a, z ? 4 : 3, es),
-                                                          z != nullptr, s);
+        return launch_by<T, TO, true>(a, copy_bytes(a, z ? 4 : 3, es), z != nullptr, s);
     });
     return ok ? SSM_OK : SSM_ERR_CUDA;
 }
