@@ -12,9 +12,9 @@
 // the state as h -> P h + q, and spans compose by (P1, q1) o (P2, q2) =
 // (P1 P2, P2 q1 + q2).
 //
-//  * A CTA takes a tile of 64 steps by 64 channels; each of its 8 (bf16) or 16
-//    (fp32) warps takes consecutive steps, a lane two neighbouring channels, so a
-//    warp's access to a step is one row segment of 64 channels.  Inputs come through a ring of shared
+//  * A CTA takes a tile of 128 steps (gradient: 64) by 64 channels; each of its 8
+//    (bf16) or 16 (fp32) warps takes consecutive steps, a lane two neighbouring
+//    channels, so a warp's access to a step is one row segment of 64 channels.  Inputs come through a ring of shared
 //    memory tiles, by TMA where every row is 16-byte aligned (else cp.async or
 //    element loads), so the next tile's loads are in flight while this one waits
 //    for its predecessors; results go back in place and out by TMA.
@@ -23,7 +23,7 @@
 //    look-back (Merrill and Garland's single-pass prefix scan).  The published
 //    values are their own flags (a pattern no result has means "not yet"), so a
 //    look-back is one round trip through L2 instead of two, and the warps look at
-//    the sixteen tiles before theirs at once.
+//    the 7 to 15 tiles before theirs at once.
 //    The grid is what the GPU holds at once (a cooperative launch) and CTA i
 //    takes tiles i, i + grid, ..., so that the tiles in work are always
 //    consecutive ones and a predecessor is running or done; every wait is bounded
@@ -52,10 +52,9 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kSteps = 64;      // steps per tile, and between kept states
+constexpr int kKeep = 64;       // steps between kept states, and of a gradient's tile
 constexpr int kCh = 64;         // channels per tile, two per lane
 constexpr int kWalkSteps = 16;  // sequences up to this long take one thread per channel pair
-constexpr int kLook = 16;       // tiles one look-back sees
 constexpr float kFastGate = 80.0f;
 
 struct alignas(16) LinHeader {
@@ -78,6 +77,7 @@ struct LinArgs {
     uint2* inc;               // [tiles][blocks][32]: the state after the tile
     int batch, seqlen, dim;
     int cblocks, blocks, tiles;  // channel blocks, channel blocks x batch, tiles per sequence
+    uint32_t cblocks_inv;        // 2^32 / cblocks, rounded up
     uint32_t spin_limit;
     int drop_first_publish;
     int vec_out;              // dim even: two channels in one store
@@ -170,16 +170,16 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A tile of 64 steps x 64 channels of one input into shared memory [step][64];
+// A tile of STEPS x 64 channels of one input into shared memory [step][64];
 // what lies past the sequence or the channels is filled with zeros.
-template <typename T, int BYTES>
+template <typename T, int STEPS, int BYTES>
 __device__ __forceinline__ void load_tile(void* dst, const void* src, long long stride, int b,
                                           int t0, int c0, int seqlen, int dim) {
     constexpr int kUnit = BYTES ? BYTES / (int)sizeof(T) : 1;  // elements per copy
     constexpr int kPerRow = kCh / kUnit;
     const T* base = static_cast<const T*>(src) + (long long)b * seqlen * stride + c0;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < kSteps * kPerRow; i += blockDim.x) {
+    for (int i = threadIdx.x; i < STEPS * kPerRow; i += blockDim.x) {
         const int r = i / kPerRow, c = (i % kPerRow) * kUnit;
         const bool in = t0 + r < seqlen && c0 + c < dim;
         const T* p = in ? base + (long long)(t0 + r) * stride + c : static_cast<const T*>(src);
@@ -205,13 +205,13 @@ __device__ __forceinline__ void put_agg(ulonglong2* p, float2 P, float2 q) {
     asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(u), "l"(v) : "memory");
 }
 
-// (P.x, q.x, P.y, q.y); each channel's pair is one 64-bit access, so a q that is there
+// (P.x, P.y, q.x, q.y); each channel's pair is one 64-bit access, so a q that is there
 // has its P
 __device__ __forceinline__ bool get_agg(const ulonglong2* p, float4& r) {
     unsigned long long u, v;
     asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(u), "=l"(v) : "l"(p) : "memory");
-    r = make_float4(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)(u >> 32)),
-                    __uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+    r = make_float4(__uint_as_float((uint32_t)u), __uint_as_float((uint32_t)v),
+                    __uint_as_float((uint32_t)(u >> 32)), __uint_as_float((uint32_t)(v >> 32)));
     return (uint32_t)(u >> 32) != kNotYet && (uint32_t)(v >> 32) != kNotYet;
 }
 
@@ -228,47 +228,64 @@ __device__ __forceinline__ bool get_inc(const uint2* p, float2& h) {
     return u != kNotYet && v != kNotYet;
 }
 
+// What the tiles before a tile have published.
+template <int WARPS, int PER>
 struct Look {
-    float4 v[kLook][32];  // of the tile i + 1 before: its aggregate, or its state in x, z
-    int state[kLook];     // whether it is the state
+    static constexpr int kTiles = (WARPS - 1) * PER;  // warp 0 has the aggregate to make
+    float4 v[kTiles][32];  // of the tile i + 1 before: its aggregate, or its state in x, y
+    int state[kTiles];     // whether it is the state
 };
 
-// One warp's part of a look-back: waits until the tiles it looks at have
-// published something (every lane publishes, those past the channels too).
-template <int WARPS>
-__device__ __forceinline__ bool look(const LinArgs& a, Look& s, int seq, int blk, int warp, int lane) {
-    bool ok = true;
+// A warp's part of a look-back: waits until each of its tiles has published
+// something, or a nearer one its state (every lane publishes, those past the
+// channels too).
+template <int WARPS, int N>
+__device__ __forceinline__ bool look(const LinArgs& a, Look<WARPS, N>& s, int seq, int blk,
+                                     int warp, int lane) {
+    const size_t step = (size_t)a.blocks * 32;
+    const int first = seq - warp;  // tiles seq - warp, then WARPS - 1 further back
+    uint32_t polls = 0;
+    bool done[N];
 #pragma unroll
-    for (int i = 0; i < kLook / WARPS; ++i) {
-        const int w = warp + i * WARPS, j = seq - 1 - w;
-        if (j < 0) {
-            if (lane == 0) s.state[w] = 0;
-            continue;
-        }
-        const size_t o = ((size_t)j * a.blocks + blk) * 32 + lane;
-        uint32_t polls = 0;
-        while (true) {
-            float2 h;
-            float4 r;
-            const bool inc = get_inc(a.inc + o, h), agg = get_agg(a.agg + o, r);
-            if (__all_sync(0xffffffffu, inc)) {
-                s.v[w][lane] = make_float4(h.x, 0.0f, h.y, 0.0f);
-                if (lane == 0) s.state[w] = 1;
-                break;
-            }
-            if (__all_sync(0xffffffffu, agg)) {
-                s.v[w][lane] = r;
-                if (lane == 0) s.state[w] = 0;
-                break;
-            }
-            if (++polls >= a.spin_limit) {
-                ok = false;
-                break;
-            }
-            if (polls > 4) __nanosleep(40);
-        }
+    for (int i = 0; i < N; ++i) {
+        done[i] = first - i * (WARPS - 1) < 0;
+        if (done[i] && lane == 0) s.state[warp - 1 + i * (WARPS - 1)] = 0;
     }
-    return ok;
+    while (true) {
+        float2 h[N];
+        float4 r[N];
+        bool inc[N], agg[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            inc[i] = agg[i] = false;
+            if (!done[i]) {
+                const size_t o = (size_t)(first - i * (WARPS - 1)) * step + blk * 32 + lane;
+                inc[i] = get_inc(a.inc + o, h[i]);
+                agg[i] = get_agg(a.agg + o, r[i]);
+            }
+        }
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (done[i]) continue;
+            const int w = warp - 1 + i * (WARPS - 1);
+            if (__all_sync(0xffffffffu, inc[i])) {
+                s.v[w][lane] = make_float4(h[i].x, h[i].y, 0.0f, 0.0f);
+                if (lane == 0) s.state[w] = 1;
+                // nothing further back is needed
+                for (int k = i; k < N; ++k) done[k] = true;
+            } else if (__all_sync(0xffffffffu, agg[i])) {
+                s.v[w][lane] = r[i];
+                if (lane == 0) s.state[w] = 0;
+                done[i] = true;
+            } else {
+                all = false;
+            }
+        }
+        if (all) return true;
+        if (++polls >= a.spin_limit) return false;
+        if (polls > 4) __nanosleep(40);
+    }
 }
 
 // ---------------------------------------------------- packed pairs of fp32
@@ -362,9 +379,11 @@ __device__ __forceinline__ bool all_fast(const void* const* rows) {
 
 // ---------------------------------------------------------- tile kernels
 
-template <typename T, int NIN>
+__host__ __device__ constexpr int tile_steps(bool grad) { return grad ? kKeep : 2 * kKeep; }
+
+template <typename T, int NIN, bool GRAD>
 struct LinSmem {
-    static constexpr int kTile = kSteps * kCh * (int)sizeof(T);  // of one input
+    static constexpr int kTile = tile_steps(GRAD) * kCh * (int)sizeof(T);  // of one input
     static constexpr int kStage = NIN * kTile;
 };
 
@@ -374,60 +393,86 @@ template <typename T, typename TO, int WARPS, int STAGES, int BYTES, bool GATED,
 __global__ void __launch_bounds__(WARPS * 32, MINB)
     linrec_tile_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
     constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
-    constexpr int S = kSteps / WARPS;
+    constexpr int STEPS = tile_steps(GRAD), S = STEPS / WARPS;
     constexpr bool TMA = BYTES == 16;
     // results of the inputs' size take their places in the tile
     constexpr bool INPLACE = TMA && sizeof(T) == sizeof(TO);
-    using SM = LinSmem<T, NIN>;
+    using SM = LinSmem<T, NIN, GRAD>;
     extern __shared__ __align__(1024) uint8_t smem[];
+    // the warps' (P, q), gradient also the reverse q; each q is replaced by that of
+    // all that stands before its warp in the scan's order (for the gradient's q: in
+    // time), whose P is beside
     __shared__ float2 s_P[WARPS][32], s_q[WARPS][32], s_r[GRAD ? WARPS : 1][32];
-    __shared__ Look s_look;
+    __shared__ float2 s_preP[WARPS][32], s_timeP[GRAD ? WARPS : 1][32];
+    // a gradient's CTAs, two of which share an SM, have no room for more than seven
+    using L = Look<WARPS, WARPS == 8 && !GRAD ? 2 : 1>;
+    __shared__ L s_look;
     __shared__ uint64_t full[STAGES];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int items = a.blocks * a.tiles;
+    const bool copies = TMA ? tid == WARPS * 32 - 32 : true;  // the TMA thread, or all
 
-    auto place = [&](int item, int& seq, int& tile, int& b, int& c0) {
-        seq = item / a.blocks;
-        const int blk = item - seq * a.blocks;
-        tile = GRAD ? a.tiles - 1 - seq : seq;
-        b = blk / a.cblocks;
-        c0 = (blk - b * a.cblocks) * kCh;
-        return blk;
+    // a tile of this CTA: its place in the scan and its channel block, moved on by
+    // the grid without divisions
+    struct At {
+        int seq, blk;
     };
-    // the tile `item` into `stage`: TMA by one thread, else by all
-    auto fetch = [&](long long item, int stage) {
-        if (item < items) {
-            int seq, tile, b, c0;
-            place((int)item, seq, tile, b, c0);
+    const int dseq = gridDim.x / a.blocks, dblk = gridDim.x % a.blocks;
+    auto next = [&](At t) {
+        t.seq += dseq;
+        t.blk += dblk;
+        if (t.blk >= a.blocks) {
+            t.blk -= a.blocks;
+            ++t.seq;
+        }
+        return t;
+    };
+    auto where = [&](At t, int& tile, int& b, int& c0) {
+        tile = GRAD ? a.tiles - 1 - t.seq : t.seq;
+        b = __umulhi((uint32_t)t.blk, a.cblocks_inv);  // at most one off
+        int r = t.blk - b * a.cblocks;
+        if (r < 0) {
+            --b;
+            r += a.cblocks;
+        } else if (r >= a.cblocks) {
+            ++b;
+            r -= a.cblocks;
+        }
+        c0 = r * kCh;
+    };
+    auto fetch = [&](At t, int stage) {
+        if (t.seq < a.tiles) {
+            int tile, b, c0;
+            where(t, tile, b, c0);
             uint8_t* dst = smem + stage * SM::kStage;
             if constexpr (TMA) {
                 mbar_arrive_expect_tx(&full[stage], SM::kStage);
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
-                    tma_load_3d(dst + i * SM::kTile, &maps.in[i], &full[stage], c0, tile * kSteps, b);
+                    tma_load_3d(dst + i * SM::kTile, &maps.in[i], &full[stage], c0, tile * STEPS, b);
             } else {
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
-                    load_tile<T, BYTES>(dst + i * SM::kTile, a.in[i], a.stride[i], b,
-                                               tile * kSteps, c0, a.seqlen, a.dim);
+                    load_tile<T, STEPS, BYTES>(dst + i * SM::kTile, a.in[i], a.stride[i], b,
+                                               tile * STEPS, c0, a.seqlen, a.dim);
             }
         }
         if constexpr (!TMA) copy_commit();
     };
-    // the results of a tile out of `stage` (one thread)
-    auto send = [&](int item, int stage) {
-        int seq, tile, b, c0;
-        place(item, seq, tile, b, c0);
+    // the results of a tile out of `stage`
+    auto send = [&](At t, int stage) {
+        int tile, b, c0;
+        where(t, tile, b, c0);
         uint8_t* src = smem + stage * SM::kStage;
         if constexpr (!GRAD) {
-            if (a.out[0]) tma_store_3d(&maps.out[0], src, c0, tile * kSteps, b);
+            if (a.out[0]) tma_store_3d(&maps.out[0], src, c0, tile * STEPS, b);
         } else {
-            tma_store_3d(&maps.out[0], src, c0, tile * kSteps, b);
-            tma_store_3d(&maps.out[1], src + SM::kTile, c0, tile * kSteps, b);
+            tma_store_3d(&maps.out[0], src, c0, tile * STEPS, b);
+            tma_store_3d(&maps.out[1], src + SM::kTile, c0, tile * STEPS, b);
             if constexpr (GATED)
-                tma_store_3d(&maps.out[2], src + 3 * SM::kTile, c0, tile * kSteps, b);
+                tma_store_3d(&maps.out[2], src + 3 * SM::kTile, c0, tile * STEPS, b);
         }
+        bulk_commit();
     };
 
     // one tile per sequence: no waits, so nothing else writes the status
@@ -439,36 +484,33 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         }
         __syncthreads();
     }
-    // tile i of this CTA is fetched at its tile i - (STAGES - 2), when the ring's
-    // place has been read out (two tiles back) and sent
+    // tile i + STAGES - 1 of this CTA is fetched during its tile i, once the ring's
+    // place, tile i - 1's, has been sent
+    At cur{(int)blockIdx.x / a.blocks, (int)blockIdx.x % a.blocks}, ahead = cur, before = cur;
 #pragma unroll
-    for (int i = 0; i < STAGES - 2; ++i)
-        if (!TMA || tid == 0) fetch((long long)blockIdx.x + (long long)i * gridDim.x, i);
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (copies) fetch(ahead, i);
+        ahead = next(ahead);
+    }
 
-    int turn = 0, before = -1;
+    int turn = 0, stage = 0, last_stage = STAGES - 1;
+    uint32_t parity = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < items; before = item, item += gridDim.x, ++turn) {
-        const int stage = turn % STAGES;
-        if constexpr (TMA) ok = mbar_wait(&full[stage], (turn / STAGES) & 1, a.status);
-        else copy_wait<STAGES - 3>();
+    for (; cur.seq < a.tiles; before = cur, cur = next(cur), ++turn) {
+        if constexpr (TMA) ok = mbar_wait(&full[stage], parity, a.status);
+        else copy_wait<STAGES - 2>();
         // the tile is there, the previous one is done with
         if (!__syncthreads_and(ok)) break;
-        if (!TMA || tid == 0) {
-            if constexpr (INPLACE) {
-                if (before >= 0) send(before, (turn - 1) % STAGES);
-                bulk_commit();
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            }
-            fetch((long long)item + (long long)(STAGES - 2) * gridDim.x,
-                  (turn + STAGES - 2) % STAGES);
-        }
+        if constexpr (INPLACE)
+            if (copies && turn > 0) send(before, last_stage);
 
-        int seq, tile, b, c;
-        const int blk = place(item, seq, tile, b, c);
+        const int seq = cur.seq, blk = cur.blk;
+        int tile, b, c;
+        where(cur, tile, b, c);
         c += lane * 2;
         const bool valid = c < a.dim, two = c + 1 < a.dim;
         const size_t chan = (size_t)b * a.dim + c;
-        const int t0 = tile * kSteps + warp * S;
+        const int t0 = tile * STEPS + warp * S;
         uint8_t* base = smem + stage * SM::kStage + (warp * S * kCh + lane * 2) * (int)sizeof(T);
         auto at = [&](int i, int k) -> void* {
             return base + i * SM::kTile + k * kCh * (int)sizeof(T);
@@ -532,44 +574,63 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         s_q[warp][lane] = q;
         __syncthreads();
 
-        // ---- across tiles: the state (gradient: mu) entering this one
+        if (copies) {
+            if constexpr (INPLACE) bulk_wait_read_all();
+            fetch(ahead, last_stage);
+        }
+
+        // ---- across warps and tiles: the state (gradient: mu) entering this one
         float2 in = both(0.0f), TP = both(1.0f), tq = both(0.0f);
+        const size_t mine = ((size_t)seq * a.blocks + blk) * 32 + lane;
         if (warp == 0) {
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) {
                 const int w = GRAD ? WARPS - 1 - i : i;
-                tq = Step<false>::next(s_P[w][lane], tq, GRAD ? s_r[w][lane] : s_q[w][lane]);
-                TP = mul2(TP, s_P[w][lane]);
+                float2& q_ = GRAD ? s_r[w][lane] : s_q[w][lane];
+                const float2 own = q_, p = s_P[w][lane];
+                q_ = tq;
+                s_preP[w][lane] = TP;
+                tq = Step<false>::next(p, tq, own);
+                TP = mul2(TP, p);
+            }
+            // the first tile has its state at once, the last one's is nobody's to read
+            if (seq > 0 && seq < a.tiles - 1) put_agg(a.agg + mine, TP, tq);
+        } else if (GRAD && warp == 1) {
+            float2 fP = both(1.0f), fq = both(0.0f);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 own = s_q[w][lane], p = s_P[w][lane];
+                s_q[w][lane] = fq;
+                s_timeP[w][lane] = fP;
+                fq = Step<false>::next(p, fq, own);
+                fP = mul2(fP, p);
             }
         }
-        const size_t mine = ((size_t)seq * a.blocks + blk) * 32 + lane;
         if (seq == 0) {
             if (a.h0 && valid) in = load_state2(a.h0, chan, two);
+            __syncthreads();
         } else {
-            // the last tile's values are nobody's to read
-            if (warp == 0 && seq < a.tiles - 1) put_agg(a.agg + mine, TP, tq);
             while (true) {
-                const bool found = look<WARPS>(a, s_look, seq, blk, warp, lane);
-                const bool all = __syncthreads_and(found);
-                int w = 0;
-                while (w < kLook && !s_look.state[w]) ++w;
-                if (!all) {
+                const bool found = warp == 0 || look(a, s_look, seq, blk, warp, lane);
+                if (!__syncthreads_and(found)) {
                     if (tid == 0) record_status(a.status, SSM_ERR_TIMEOUT);
                     in = both(__int_as_float(0x7fffffff));
                     break;
                 }
-                if (w < kLook) {
+                int w = 0;
+                while (w < L::kTiles && !s_look.state[w]) ++w;
+                if (w < L::kTiles) {
                     // from the newest state through the aggregates after it, in
                     // order: the same operations wherever the state was found
                     const float4 h = s_look.v[w][lane];
-                    in = make_float2(h.x, h.z);
+                    in = make_float2(h.x, h.y);
                     for (--w; w >= 0; --w) {
                         const float4 g = s_look.v[w][lane];
-                        in = Step<false>::next(make_float2(g.x, g.z), in, make_float2(g.y, g.w));
+                        in = Step<false>::next(make_float2(g.x, g.y), in, make_float2(g.z, g.w));
                     }
                     break;
                 }
-                __syncthreads();  // sixteen aggregates and no state: look again
+                __syncthreads();  // aggregates and no state yet: look again
             }
         }
         if (warp == 0) {
@@ -581,15 +642,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 if (two) a.last[chan + 1] = end.y;
             }
         }
+        in = Step<false>::next(s_preP[warp][lane], in, GRAD ? s_r[warp][lane] : s_q[warp][lane]);
 
         // ---- the steps again from the warp's entry state
         const size_t o = ((size_t)b * a.seqlen + t0) * a.dim + c;
         if constexpr (!GRAD) {
             float2 h = in;
-            for (int w = 0; w < warp; ++w)
-                h = Step<false>::next(s_P[w][lane], h, s_q[w][lane]);
-            if (a.keep && warp == 0 && valid) {
-                float* s = a.keep + (size_t)tile * a.batch * a.dim + chan;
+            if (a.keep && warp % (WARPS / 2) == 0 && valid && t0 < a.seqlen) {
+                float* s = a.keep + (size_t)(t0 / kKeep) * a.batch * a.dim + chan;
                 s[0] = h.x;
                 if (two) s[1] = h.y;
             }
@@ -614,11 +674,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 else replay(std::false_type{});
             }
         } else {
-            float2 h = hk, mu = in;
-            for (int w = 0; w < warp; ++w)
-                h = Step<false>::next(s_P[w][lane], h, s_q[w][lane]);
-            for (int w = WARPS - 1; w > warp; --w)
-                mu = Step<false>::next(s_P[w][lane], mu, s_r[w][lane]);
+            float2 mu = in, h = Step<false>::next(s_timeP[warp][lane], hk, s_q[warp][lane]);
             auto replay = [&](auto fast_) {
                 constexpr bool F = decltype(fast_)::value;
                 float2 prev[S];  // h_{t-1}
@@ -663,14 +719,19 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             else replay(std::false_type{});
         }
         if constexpr (INPLACE) fence_proxy_async_smem();
+        ahead = next(ahead);
+        last_stage = stage;
+        if (++stage == STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
     }
     if constexpr (INPLACE) {
         __syncthreads();
-        if (tid == 0 && ok && before >= 0) {
-            send(before, (turn + STAGES - 1) % STAGES);
-            bulk_commit();
+        if (copies) {
+            if (ok && turn > 0) send(before, last_stage);
+            bulk_wait_all();
         }
-        if (tid == 0) bulk_wait_all();
     }
     if constexpr (!TMA) copy_wait<0>();
     // a load that never came: leave what is in flight time to land
@@ -729,7 +790,7 @@ __global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-int tiles_of(int seqlen) { return seqlen / kSteps + (seqlen % kSteps != 0); }
+int tiles_of(int seqlen, int steps) { return seqlen / steps + (seqlen % steps != 0); }
 
 // header, aggregates and inclusive states of `tiles` tiles
 size_t scan_bytes(int batch, int dim, int tiles) {
@@ -742,12 +803,13 @@ bool sizes_ok(int batch, int seqlen, int dim) { return batch >= 0 && seqlen >= 0
 // one int counts the tiles of all blocks
 bool sizes_fit(int batch, int seqlen, int dim) {
     const double blocks = (double)batch * ((dim + kCh - 1) / kCh);
-    return blocks * tiles_of(seqlen) < 2.0e9 && (double)batch * dim < 2.0e9;
+    return blocks * tiles_of(seqlen, kKeep) < 2.0e9 && (double)batch * dim < 2.0e9;
 }
 
 // Fills in the work area of one scan.
 void place(LinArgs& a, uint8_t* ws, int tiles) {
     a.cblocks = (a.dim + kCh - 1) / kCh;
+    a.cblocks_inv = (uint32_t)std::min<uint64_t>(0xffffffffu, (uint64_t(1) << 32) / a.cblocks + 1);
     a.blocks = a.batch * a.cblocks;
     a.tiles = tiles;
     a.status = reinterpret_cast<uint32_t*>(ws) + 1;
@@ -756,12 +818,13 @@ void place(LinArgs& a, uint8_t* ws, int tiles) {
 }
 
 // (batch, seqlen, dim) with rows `stride` elements apart, boxes of a tile
-bool make_map(CUtensorMap* map, const void* base, size_t es, long long stride, const LinArgs& a) {
+bool make_map(CUtensorMap* map, const void* base, size_t es, long long stride, const LinArgs& a,
+              int steps) {
     auto fn = ssm_host::encode_tiled_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.seqlen, (cuuint64_t)a.batch};
     const cuuint64_t strides[2] = {(cuuint64_t)stride * es, (cuuint64_t)stride * es * a.seqlen};
-    const cuuint32_t box[3] = {(cuuint32_t)kCh, (cuuint32_t)kSteps, 1}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)kCh, (cuuint32_t)steps, 1}, one[3] = {1, 1, 1};
     return fn(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
               const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -773,9 +836,9 @@ bool launch_tile(LinArgs& a, cudaStream_t s) {
     constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
     // 16 warps an SM, and as many stages as fit in its shared memory
     constexpr int WARPS = sizeof(T) == 2 ? 8 : 16, MINB = 16 / WARPS;
-    constexpr int kStage = LinSmem<T, NIN>::kStage;
+    constexpr int kStage = LinSmem<T, NIN, GRAD>::kStage;
     constexpr int STAGES = 96 * 1024 * WARPS / 8 / kStage;
-    static_assert(STAGES >= 3, "one tile being read out, one at work, one coming in");
+    static_assert(STAGES >= 2, "one tile at work, one coming in");
     constexpr int smem = STAGES * kStage;
     auto kernel = linrec_tile_kernel<T, TO, WARPS, STAGES, BYTES, GATED, GRAD, MINB>;
     const void* fn = reinterpret_cast<const void*>(kernel);
@@ -791,9 +854,10 @@ bool launch_tile(LinArgs& a, cudaStream_t s) {
     LinMaps maps{};
     if constexpr (BYTES == 16) {
         for (int i = 0; i < NIN; ++i)
-            if (!make_map(&maps.in[i], a.in[i], sizeof(T), a.stride[i], a)) return false;
+            if (!make_map(&maps.in[i], a.in[i], sizeof(T), a.stride[i], a, tile_steps(GRAD))) return false;
         for (int i = 0; i < 3 && sizeof(T) == sizeof(TO); ++i)
-            if (a.out[i] && !make_map(&maps.out[i], a.out[i], sizeof(TO), a.dim, a))
+            if (a.out[i] && !make_map(&maps.out[i], a.out[i], sizeof(TO), a.dim, a,
+                                       tile_steps(GRAD)))
                 return false;
     }
     const long long items = (long long)a.blocks * a.tiles;
@@ -874,7 +938,7 @@ bool run_forward(LinArgs& a, ssm_dtype_t in, ssm_dtype_t out, bool gated, cudaSt
     });
 }
 
-int fwd_tiles(int seqlen) { return seqlen <= kWalkSteps ? 1 : tiles_of(seqlen); }
+int fwd_tiles(int seqlen) { return seqlen <= kWalkSteps ? 1 : tiles_of(seqlen, tile_steps(false)); }
 
 struct Span { const void* p; size_t n; };
 
@@ -887,17 +951,17 @@ size_t strided_bytes(long long steps, int dim, long long stride, size_t es) {
 
 extern "C" size_t ssm_linrec_checkpoint_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim)) return 0;
-    return (size_t)tiles_of(seqlen) * batch * dim * 4;
+    return (size_t)tiles_of(seqlen, kKeep) * batch * dim * 4;
 }
 
 extern "C" size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim) || !sizes_fit(batch, seqlen, dim)) return 0;
-    return scan_bytes(batch, dim, tiles_of(seqlen));
+    return scan_bytes(batch, dim, tiles_of(seqlen, kKeep));
 }
 
 extern "C" size_t ssm_linrec_bwd_workspace_bytes(int batch, int seqlen, int dim) {
     if (!sizes_ok(batch, seqlen, dim) || !sizes_fit(batch, seqlen, dim)) return 0;
-    return scan_bytes(batch, dim, tiles_of(seqlen)) +
+    return scan_bytes(batch, dim, tiles_of(seqlen, kKeep)) +
            round256(ssm_linrec_checkpoint_bytes(batch, seqlen, dim));
 }
 
@@ -1016,7 +1080,7 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
         // the forward again, states only
         LinArgs w = a;
         w.h0 = initial_state;
-        w.keep = reinterpret_cast<float*>(ws + scan_bytes(batch, dim, tiles_of(seqlen)));
+        w.keep = reinterpret_cast<float*>(ws + scan_bytes(batch, dim, tiles_of(seqlen, kKeep)));
         place(w, ws, fwd_tiles(seqlen));
         if (!run_forward(w, in_dtype, in_dtype, false, s)) return SSM_ERR_CUDA;
         checkpoints = w.keep;
@@ -1035,7 +1099,7 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
                          : cudaMemsetAsync(dinitial_state, 0, states * 4, s);
         return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
     }
-    place(a, ws, tiles_of(seqlen));
+    place(a, ws, tiles_of(seqlen, tile_steps(true)));
     const bool ok = by_types(in_dtype, grad_dtype, [&](auto ti, auto to) -> bool {
         using T = decltype(ti);
         using TO = decltype(to);
