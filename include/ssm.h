@@ -824,7 +824,7 @@ size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim);
  * ceil(seqlen / 64) < 2e9.  seqlen == 0 hands the state on.
  * The sequence is cut into tiles chained by a decoupled look-back in the
  * workspace (sequences of up to 16 steps are walked by one thread per channel
- * pair); its bounded waits report through ssm_last_device_status.  The result
+ * pair, and need no workspace: it may be NULL); its bounded waits report through ssm_last_device_status.  The result
  * does not depend on timing: runs are bit-equal.
  */
 ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void* z, long long f_stride,

@@ -987,8 +987,22 @@ def ssm_decode_step_mamba3_mimo(state, prev_B, prev_x, x, dt, lam, A, B, C, D=No
 # stream the call runs on, so that their memory is not handed out again before
 # the kernels there are done with it.
 
+_NULL = contextlib.nullcontext()
+
+
 def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NULL if stream is None else torch.cuda.stream(stream)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw(stream, t):
+    """The stream's handle: the given one's, or the current one's of t's device (without
+    the Stream object, whose making takes half as long as a kernel launch)."""
+    return (torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else
+            stream.cuda_stream)
 
 
 def _like(t, name, ref, dtype):
@@ -1031,9 +1045,9 @@ def ssm_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, sum_
     _like(y, "y", x.shape, out_dt)
     if sum_out is not None:
         _like(sum_out, "sum_out", x.shape, res_dt)
-    st = lib().ssm_add_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(y),
-                                   _ptr(sum_out), rows, dim, _DT[x.dtype], _DT[res_dt],
-                                   _dt_code(out_dt, "out_dtype"), _stream(stream))
+    st = lib().ssm_add_rmsnorm_fwd(_p(x), _p(residual), _p(weight), float(eps), _p(y),
+                                   _p(sum_out), rows, dim, _DT[x.dtype], _DT[res_dt],
+                                   _dt_code(out_dt, "out_dtype"), _raw(stream, x))
     _check(st, "ssm_add_rmsnorm_fwd")
     return y, sum_out
 
@@ -1078,9 +1092,9 @@ def ssm_add_rmsnorm_e4m3_fwd(x, weight, residual=None, eps=1e-5, group=128, sum_
     _like(scales, "scales", sshape, torch.float32)
     if sum_out is not None:
         _like(sum_out, "sum_out", x.shape, res_dt)
-    st = lib().ssm_add_rmsnorm_e4m3_fwd(_ptr(x), _ptr(residual), _ptr(weight), float(eps), group,
-                                        _ptr(q), _ptr(scales), _ptr(sum_out), rows, dim,
-                                        _DT[x.dtype], _DT[res_dt], _stream(stream))
+    st = lib().ssm_add_rmsnorm_e4m3_fwd(_p(x), _p(residual), _p(weight), float(eps), group,
+                                        _p(q), _p(scales), _p(sum_out), rows, dim,
+                                        _DT[x.dtype], _DT[res_dt], _raw(stream, x))
     _check(st, "ssm_add_rmsnorm_e4m3_fwd")
     return q, scales, sum_out
 
@@ -1125,11 +1139,11 @@ def ssm_add_rmsnorm_bwd(dy, sum, weight, dsum=None, eps=1e-5, x_dtype=None, dx=N
         _like(dresidual, "dresidual", sum.shape, sum.dtype)
     _like(dweight, "dweight", (dim,), torch.float32)
     _req(workspace, "workspace", torch.uint8)
-    st = lib().ssm_add_rmsnorm_bwd(_ptr(sum), _ptr(weight), float(eps), _ptr(dy), _ptr(dsum),
-                                   _ptr(dx), _ptr(dresidual), _ptr(dweight), rows, dim,
+    st = lib().ssm_add_rmsnorm_bwd(_p(sum), _p(weight), float(eps), _p(dy), _p(dsum),
+                                   _p(dx), _p(dresidual), _p(dweight), rows, dim,
                                    _dt_code(dx_dt, "x_dtype"), _DT[sum.dtype],
-                                   _dt_code(dy.dtype, "dy"), _ptr(workspace), workspace.numel(),
-                                   _stream(stream))
+                                   _dt_code(dy.dtype, "dy"), _p(workspace), workspace.numel(),
+                                   _raw(stream, sum))
     _check(st, "ssm_add_rmsnorm_bwd")
     return {"dx": dx, "dresidual": dx if dresidual is None else dresidual, "dweight": dweight}
 
@@ -1197,18 +1211,18 @@ def ssm_linrec_fwd(f, x, z=None, initial_state=None, out_dtype=None, y=None, fin
             y = torch.empty((batch, seqlen, dim), dtype=out_dt, device=x.device)
         if final_state is None and return_final_state:
             final_state = torch.empty((batch, dim), dtype=torch.float32, device=x.device)
-        if workspace is None:
+        if workspace is None and seqlen > 16:  # shorter sequences run without one
             need = ssm_linrec_workspace_bytes(batch, seqlen, dim)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
     _like(y, "y", (batch, seqlen, dim), out_dt)
     if final_state is not None:
         _like(final_state, "final_state", (batch, dim), torch.float32)
-    _req(workspace, "workspace", torch.uint8)
+    _opt(workspace, "workspace", torch.uint8)
     _kept(checkpoints, batch, seqlen, dim)
-    st = lib().ssm_linrec_fwd(_ptr(f), _ptr(x), _ptr(z), sf, sx, sz, _ptr(initial_state), _ptr(y),
-                              _ptr(final_state), _ptr(checkpoints), batch, seqlen, dim,
-                              _DT[x.dtype], _dt_code(out_dt, "out_dtype"), _ptr(workspace),
-                              workspace.numel(), _stream(stream))
+    st = lib().ssm_linrec_fwd(_p(f), _p(x), _p(z), sf, sx, sz, _p(initial_state), _p(y),
+                              _p(final_state), _p(checkpoints), batch, seqlen, dim,
+                              _DT[x.dtype], _dt_code(out_dt, "out_dtype"), _p(workspace),
+                              0 if workspace is None else workspace.numel(), _raw(stream, x))
     _check(st, "ssm_linrec_fwd")
     return y, final_state
 
@@ -1252,11 +1266,11 @@ def ssm_linrec_bwd(f, x, dy, z=None, initial_state=None, dfinal_state=None, chec
             need = ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
     _req(workspace, "workspace", torch.uint8)
-    st = lib().ssm_linrec_bwd(_ptr(f), _ptr(x), _ptr(z), sf, sx, sz, _ptr(initial_state), _ptr(dy),
-                              _ptr(dfinal_state), _ptr(checkpoints), _ptr(g["df"]), _ptr(g["dx"]),
-                              _ptr(g["dz"]), _ptr(g["dinitial_state"]), batch, seqlen, dim,
-                              _DT[x.dtype], _dt_code(gd, "grad_dtype"), _ptr(workspace),
-                              workspace.numel(), _stream(stream))
+    st = lib().ssm_linrec_bwd(_p(f), _p(x), _p(z), sf, sx, sz, _p(initial_state), _p(dy),
+                              _p(dfinal_state), _p(checkpoints), _p(g["df"]), _p(g["dx"]),
+                              _p(g["dz"]), _p(g["dinitial_state"]), batch, seqlen, dim,
+                              _DT[x.dtype], _dt_code(gd, "grad_dtype"), _p(workspace),
+                              workspace.numel(), _raw(stream, x))
     _check(st, "ssm_linrec_bwd")
     return g
 
@@ -1294,9 +1308,9 @@ def ssm_vocab_ce_fwd(h, W, targets, loss=None, lse=None, workspace=None, stream=
     _like(loss, "loss", (tokens,), torch.float32)
     _like(lse, "lse", (tokens,), torch.float32)
     _req(workspace, "workspace", torch.uint8)
-    st = lib().ssm_vocab_ce_fwd(_ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), tokens, dim,
-                                vocab, _DT[h.dtype], _ptr(workspace), workspace.numel(),
-                                _stream(stream))
+    st = lib().ssm_vocab_ce_fwd(_p(h), _p(W), _p(targets), _p(loss), _p(lse), tokens, dim,
+                                vocab, _DT[h.dtype], _p(workspace), workspace.numel(),
+                                _raw(stream, h))
     _check(st, "ssm_vocab_ce_fwd")
     return loss, lse
 
@@ -1324,8 +1338,8 @@ def ssm_vocab_ce_bwd(h, W, targets, lse, dloss, grad_dtype=None, workspace=None,
             need = ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab)
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=h.device)
     _req(workspace, "workspace", torch.uint8)
-    st = lib().ssm_vocab_ce_bwd(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss),
-                                _ptr(g["dh"]), _ptr(g["dW"]), tokens, dim, vocab, _DT[h.dtype], code,
-                                _ptr(workspace), workspace.numel(), _stream(stream))
+    st = lib().ssm_vocab_ce_bwd(_p(h), _p(W), _p(targets), _p(lse), _p(dloss),
+                                _p(g["dh"]), _p(g["dW"]), tokens, dim, vocab, _DT[h.dtype], code,
+                                _p(workspace), workspace.numel(), _raw(stream, h))
     _check(st, "ssm_vocab_ce_bwd")
     return g

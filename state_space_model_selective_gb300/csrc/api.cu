@@ -39,6 +39,32 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, ssm_dtype_t dtype, uint64_
     return r == CUDA_SUCCESS;
 }
 
+int sm_count() {
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+int resident_ctas(const void* kernel, int threads, int smem, std::atomic<int>* cache) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess)
+            return 0;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 }  // namespace ssm_host
 
 extern "C" int ssm_abi_version(void) { return 4; }
@@ -67,5 +93,6 @@ extern "C" ssm_status_t ssm_last_device_status(const void* workspace, void* stre
     if (cudaMemcpyAsync(hdr, workspace, sizeof(hdr), cudaMemcpyDeviceToHost, s) != cudaSuccess)
         return SSM_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return SSM_ERR_CUDA;
-    return hdr[1] == 0 ? SSM_OK : static_cast<ssm_status_t>(hdr[1]);
+    // 0 or, where the header was cleared with the look-back's values, all ones: none
+    return hdr[1] == 0 || hdr[1] == 0xffffffffu ? SSM_OK : static_cast<ssm_status_t>(hdr[1]);
 }

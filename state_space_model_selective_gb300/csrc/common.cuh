@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ssm.h"
 
 namespace ssm {
@@ -211,6 +213,16 @@ inline bool overlaps(const void* a, size_t abytes, const void* b, size_t bbytes)
 inline size_t dtype_size(ssm_dtype_t t) { return t == SSM_BF16 ? 2 : 4; }
 
 inline bool dtype_ok(ssm_dtype_t t) { return t == SSM_F32 || t == SSM_BF16; }
+
+// Multiprocessors of the current device (0 if it cannot be told), kept per device.
+int sm_count();
+
+// The CTAs of `kernel` one multiprocessor of the current device holds with this
+// many threads and bytes of dynamic shared memory, which the kernel is first
+// allowed to use (0 on an error).  Kept per device in `cache`, one static array
+// to a kernel: the two runtime calls cost about as much as a launch.
+constexpr int kMaxDevices = 64;
+int resident_ctas(const void* kernel, int threads, int smem, std::atomic<int>* cache);
 
 // cuTensorMapEncodeTiled, fetched from the driver through the runtime so the
 // library has no link-time dependency on libcuda.

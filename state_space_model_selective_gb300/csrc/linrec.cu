@@ -193,7 +193,9 @@ __device__ __forceinline__ void load_tile(void* dst, const void* src, long long 
 
 // ------------------------------------------------------------- look-back
 
-constexpr uint32_t kNotYet = 0xffffffffu;  // a NaN pattern; results' NaNs are 0x7fffffff
+// What the work area is filled with before a scan: a NaN pattern no result has
+// (results' NaNs are 0x7fffffff), and the status word's "nothing recorded".
+constexpr uint32_t kNotYet = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t published(float v) {
     return v != v ? 0x7fffffffu : __float_as_uint(v);
@@ -475,8 +477,6 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         bulk_commit();
     };
 
-    // one tile per sequence: no waits, so nothing else writes the status
-    if (tid == 0 && a.tiles == 1 && blockIdx.x == 0 && !a.keep_status) *a.status = 0;
     if constexpr (TMA) {
         if (tid == 0) {
             for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
@@ -497,10 +497,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
     uint32_t parity = 0;
     bool ok = true;
     for (; cur.seq < a.tiles; before = cur, cur = next(cur), ++turn) {
-        if constexpr (TMA) ok = mbar_wait(&full[stage], parity, a.status);
+        if constexpr (TMA) ok = mbar_wait(&full[stage], parity, nullptr);
         else copy_wait<STAGES - 2>();
         // the tile is there, the previous one is done with
-        if (!__syncthreads_and(ok)) break;
+        if (!__syncthreads_and(ok)) {
+            if (tid == 0) atomicCAS(a.status, kNotYet, SSM_ERR_TIMEOUT);
+            ok = false;
+            break;
+        }
         if constexpr (INPLACE)
             if (copies && turn > 0) send(before, last_stage);
 
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             while (true) {
                 const bool found = warp == 0 || look(a, s_look, seq, blk, warp, lane);
                 if (!__syncthreads_and(found)) {
-                    if (tid == 0) record_status(a.status, SSM_ERR_TIMEOUT);
+                    if (tid == 0) atomicCAS(a.status, kNotYet, SSM_ERR_TIMEOUT);
                     in = both(__int_as_float(0x7fffffff));
                     break;
                 }
@@ -747,7 +751,7 @@ template <typename T, typename TO, bool VEC, bool GATED>
 __global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
     const int pairs = (a.dim + 1) / 2;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
-    if (i == 0 && !a.keep_status) *a.status = 0;
+    if (i == 0 && a.status && !a.keep_status) *a.status = 0;
     if (i >= (long long)a.batch * pairs) return;
     const int b = (int)(i / pairs), c = (int)(i % pairs) * 2;
     const bool two = c + 1 < a.dim;
@@ -812,6 +816,7 @@ void place(LinArgs& a, uint8_t* ws, int tiles) {
     a.cblocks_inv = (uint32_t)std::min<uint64_t>(0xffffffffu, (uint64_t(1) << 32) / a.cblocks + 1);
     a.blocks = a.batch * a.cblocks;
     a.tiles = tiles;
+    if (!ws) return;  // a walked sequence
     a.status = reinterpret_cast<uint32_t*>(ws) + 1;
     a.agg = reinterpret_cast<ulonglong2*>(ws + sizeof(LinHeader));
     a.inc = reinterpret_cast<uint2*>(a.agg + (size_t)tiles * a.blocks * 32);
@@ -842,15 +847,10 @@ bool launch_tile(LinArgs& a, cudaStream_t s) {
     constexpr int smem = STAGES * kStage;
     auto kernel = linrec_tile_kernel<T, TO, WARPS, STAGES, BYTES, GATED, GRAD, MINB>;
     const void* fn = reinterpret_cast<const void*>(kernel);
-    int dev = 0, sms = 0, per_sm = 0;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, WARPS * 32, smem) !=
-            cudaSuccess ||
-        per_sm < 1)
-        return false;
+    static std::atomic<int> cache[ssm_host::kMaxDevices];
+    const int slots =
+        ssm_host::sm_count() * ssm_host::resident_ctas(fn, WARPS * 32, smem, cache);
+    if (slots < 1) return false;
     LinMaps maps{};
     if constexpr (BYTES == 16) {
         for (int i = 0; i < NIN; ++i)
@@ -861,13 +861,18 @@ bool launch_tile(LinArgs& a, cudaStream_t s) {
                 return false;
     }
     const long long items = (long long)a.blocks * a.tiles;
-    const unsigned grid = (unsigned)std::min<long long>(items, (long long)per_sm * sms);
+    const unsigned grid = (unsigned)std::min<long long>(items, slots);
     if (a.tiles == 1) {
+        // no look-back: only the status is cleared
+        if (!a.keep_status && cudaMemsetAsync(a.status, 0xff, 4, s) != cudaSuccess) return false;
         kernel<<<grid, WARPS * 32, smem, s>>>(maps, a);
         return cudaGetLastError() == cudaSuccess;
     }
-    if ((!a.keep_status && cudaMemsetAsync(a.status, 0, 4, s) != cudaSuccess) ||
-        cudaMemsetAsync(a.agg, 0xff, (size_t)items * 32 * 24, s) != cudaSuccess)
+    // header and published values are neighbours; an earlier scan's status stays
+    uint8_t* from = reinterpret_cast<uint8_t*>(a.agg) - (a.keep_status ? 0 : sizeof(LinHeader));
+    if (cudaMemsetAsync(from, 0xff,
+                        (size_t)items * 32 * 24 + (a.keep_status ? 0 : sizeof(LinHeader)),
+                        s) != cudaSuccess)
         return false;
     void* args[] = {&maps, &a};
     return cudaLaunchCooperativeKernel(fn, dim3(grid), dim3(WARPS * 32), args, smem, s) ==
@@ -980,7 +985,10 @@ extern "C" ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void*
     const size_t states = (size_t)batch * dim;
     if (states == 0) return SSM_OK;
     if (seqlen > 0 && (!f || !x || !y)) return SSM_ERR_NULL;
-    if (!workspace || workspace_bytes < ssm_linrec_workspace_bytes(batch, seqlen, dim))
+    // a walked sequence waits for nothing: it runs without a workspace too
+    const bool walked = seqlen <= kWalkSteps && !workspace;
+    if (!walked &&
+        (!workspace || workspace_bytes < ssm_linrec_workspace_bytes(batch, seqlen, dim)))
         return SSM_ERR_WORKSPACE;
     const size_t es = dtype_size(in_dtype);
     for (const void* p : {(const void*)initial_state, (const void*)y, (const void*)final_state,

@@ -634,12 +634,11 @@ template <Mode MODE>
 bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, const CeArgs& a,
             cudaStream_t s) {
     auto kernel = ce_kernel<MODE>;
-    int dev = 0, sms = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
-            cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    static std::atomic<int> cache[ssm_host::kMaxDevices];
+    if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kThreads, kSmemBytes, cache) <
+        1)
         return false;
+    const int sms = ssm_host::sm_count();
     kernel<<<2 * std::max(1, sms / 2), kThreads, kSmemBytes, s>>>(h, W, P, a);
     return cudaGetLastError() == cudaSuccess;
 }
