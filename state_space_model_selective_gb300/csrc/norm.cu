@@ -16,10 +16,11 @@
 // (dim a multiple of 8) a lane holds 8 consecutive elements, moved with 16-byte
 // accesses; else lane l holds elements l, 32 + l, ... of the block, so that the
 // element-wise accesses of a warp are contiguous.  Rows of up to 256 elements
-// take one warp each, several to a CTA; longer rows take one CTA of up to 32
-// warps.
+// take one warp each, several to a CTA; longer rows take one CTA of up to
+// 32 warps of one block or 16 of four.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -28,8 +29,10 @@ namespace {
 using namespace ssm;
 
 constexpr int kBlock = 256;      // elements of a row one warp owns at a time
-constexpr int kMaxDim = 16384;   // 32 warps of 2 blocks
+constexpr int kMaxDim = 16384;   // 16 warps of 4 blocks
 constexpr float kE4m3Max = 448.0f;
+constexpr int kBwdThreads = 640;
+constexpr int kFwdThreads = 1024;  // of the forward on an SM at a time
 
 struct NormArgs {
     const void* x;         // forward: x; gradient: the kept sum
@@ -47,35 +50,41 @@ struct NormArgs {
     int group, ngroups;    // 8-bit only; group 0 = the whole row
 };
 
-// The 8 elements a lane holds of block `blk` of the row at `p`; elements past
-// `dim` read as 0.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* p, int blk, int lane, int dim, float* v) {
-    if constexpr (VEC) {
-        const int i = blk * kBlock + lane * 8;
-        if (i < dim) {
-            if constexpr (sizeof(T) == 2) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p + i));
-                v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
-                v[4] = bf16lo(w.z); v[5] = bf16hi(w.z); v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
-            } else {
-                const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
-                const float4 b = __ldcs(reinterpret_cast<const float4*>(p + i + 4));
-                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            }
+// The 8 elements a lane holds of block `blk` of a row, as they come from memory:
+// loaded a row ahead of their use.  Elements past `dim` read as 0.
+template <typename T, bool VEC>
+struct Raw {
+    static constexpr int kWords = VEC ? (int)sizeof(T) / 2 : 8;
+    using Word = std::conditional_t<VEC, uint4, float>;
+    Word w[kWords];
+
+    __device__ void load(const T* p, int blk, int lane, int dim) {
+        if constexpr (VEC) {
+            const int i = blk * kBlock + lane * 8;
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+                w[j] = i < dim ? __ldcs(reinterpret_cast<const uint4*>(p + i) + j)
+                               : make_uint4(0, 0, 0, 0);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = blk * kBlock + j * 32 + lane;
-            v[j] = i < dim ? to_f32(p[i]) : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const int i = blk * kBlock + j * 32 + lane;
+                w[j] = i < dim ? to_f32(p[i]) : 0.0f;
+            }
         }
     }
-}
+    __device__ float get(int j) const {  // j a constant
+        if constexpr (!VEC) return w[j];
+        else if constexpr (sizeof(T) == 2) {
+            const uint32_t u = (j >> 1) == 0 ? w[0].x : (j >> 1) == 1 ? w[0].y
+                             : (j >> 1) == 2 ? w[0].z : w[0].w;
+            return j & 1 ? bf16hi(u) : bf16lo(u);
+        } else {
+            const uint4& q = w[j >> 2];
+            return __uint_as_float((j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w);
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -117,7 +126,11 @@ __device__ __forceinline__ void load_weight(const float* p, int blk, int lane, i
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
-        load8<false>(p, blk, lane, dim, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = blk * kBlock + j * 32 + lane;
+            v[j] = i < dim ? __ldg(p + i) : 0.0f;
+        }
     }
 }
 
@@ -160,176 +173,210 @@ __device__ __forceinline__ float quant_value(float y, float factor) {
 
 enum Out { kPlain, kE4m3 };
 
-// ------------------------------------------------------------- forward
-
-template <typename TX, typename TR, typename TY, int NV, bool VEC, Out OUT>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
-    __shared__ float red[2][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wr = warp % a.warps_per_row;  // the warp within its row
-    const long long row = (long long)blockIdx.x * a.rows_per_cta + warp / a.warps_per_row;
-    if (row >= a.rows) return;  // whole CTA or, with one warp to a row, whole warps
-    const size_t base = (size_t)row * a.dim;
-
-    float v[NV][8];
-    float ss = 0.0f;
-    {
-        float rv[NV][8];
+// The 8-bit output of a row: v is its y.
+template <int NV, bool VEC>
+__device__ __forceinline__ void quantise(const NormArgs& a, long long row, float (*v)[8], int wr,
+                                         int lane, int warp, float* red) {
+    uint8_t* q = static_cast<uint8_t*>(a.y) + (size_t)row * a.dim;
+    float* scales = a.scales + (size_t)row * a.ngroups;
+    float row_amax = 0.0f;
+    if (a.group == 0) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
-            load8<VEC>(static_cast<const TX*>(a.x) + base, blk, lane, a.dim, v[k]);
-            if (a.residual)
-                load8<VEC>(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim, rv[k]);
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) row_amax = max_nan(row_amax, fabsf(v[k][j]));
+        row_amax = lanes_max(row_amax, 32);
+        if (a.warps_per_row > 1) {
+            if (lane == 0) red[warp] = row_amax;
+            __syncthreads();
+            row_amax = lanes_max(lane < a.warps_per_row ? red[lane] : 0.0f, 32);
         }
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
-            if (a.residual) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[k][j] += rv[k][j];
-            }
-            if (a.sum) store8<VEC>(static_cast<TR*>(a.sum) + base, blk, lane, a.dim, v[k]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
-        }
+        if (wr == 0 && lane == 0) scales[0] = __fdiv_rn(row_amax, kE4m3Max);
     }
-    ss = warp_sum(ss);
-    if (a.warps_per_row > 1) {
-        if (lane == 0) red[0][warp] = ss;
-        __syncthreads();
-        ss = warp_sum(lane < a.warps_per_row ? red[0][lane] : 0.0f);
-    }
-    const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
-
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int blk = wr + k * a.warps_per_row;
-        float w[8];
-        load_weight<VEC>(a.weight, blk, lane, a.dim, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * w[j];
-        if constexpr (OUT == kPlain)
-            store8<VEC>(static_cast<TY*>(a.y) + base, blk, lane, a.dim, v[k]);
-    }
-
-    if constexpr (OUT == kE4m3) {
-        uint8_t* q = static_cast<uint8_t*>(a.y) + base;
-        float* scales = a.scales + (size_t)row * a.ngroups;
-        float row_amax = 0.0f;
+        float amax[8];  // VEC: one group per lane, in amax[0]
         if (a.group == 0) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+            for (int j = 0; j < 8; ++j) amax[j] = row_amax;
+        } else if constexpr (VEC) {
+            float m = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) row_amax = max_nan(row_amax, fabsf(v[k][j]));
-            row_amax = lanes_max(row_amax, 32);
-            if (a.warps_per_row > 1) {
-                if (lane == 0) red[1][warp] = row_amax;
-                __syncthreads();
-                row_amax = lanes_max(lane < a.warps_per_row ? red[1][lane] : 0.0f, 32);
+            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[k][j]));
+            const int width = a.group >> 3;
+            amax[0] = lanes_max(m, width);
+            const int i = blk * kBlock + lane * 8;
+            if ((lane & (width - 1)) == 0 && i < a.dim)
+                scales[i / a.group] = __fdiv_rn(amax[0], kE4m3Max);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax[j] = lanes_max(fabsf(v[k][j]), 32);
+            // a group is group / 32 consecutive rows of 32 lanes
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                if (o * 32 < a.group) {
+                    float t[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) t[j] = max_nan(amax[j], amax[j ^ o]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) amax[j] = t[j];
+                }
             }
-            if (wr == 0 && lane == 0) scales[0] = __fdiv_rn(row_amax, kE4m3Max);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = blk * kBlock + j * 32;
+                if (lane == 0 && i % a.group == 0 && i < a.dim)
+                    scales[i / a.group] = __fdiv_rn(amax[j], kE4m3Max);
+            }
         }
+        if constexpr (VEC) {
+            const float f = quant_factor(amax[0]);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
-            float amax[8];  // VEC: one group per lane, in amax[0]
-            if (a.group == 0) {
+            for (int j = 0; j < 8; ++j) v[k][j] = quant_value(v[k][j], f);
+            const int i = blk * kBlock + lane * 8;
+            if (i < a.dim)
+                *reinterpret_cast<uint2*>(q + i) =
+                    make_uint2(e4m3x2(v[k][0], v[k][1]) | e4m3x2(v[k][2], v[k][3]) << 16,
+                               e4m3x2(v[k][4], v[k][5]) | e4m3x2(v[k][6], v[k][7]) << 16);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) amax[j] = row_amax;
-            } else if constexpr (VEC) {
-                float m = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[k][j]));
-                const int width = a.group >> 3;
-                amax[0] = lanes_max(m, width);
-                const int i = blk * kBlock + lane * 8;
-                if ((lane & (width - 1)) == 0 && i < a.dim)
-                    scales[i / a.group] = __fdiv_rn(amax[0], kE4m3Max);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax[j] = lanes_max(fabsf(v[k][j]), 32);
-                // a group is group / 32 consecutive rows of 32 lanes
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) {
-                    if (o * 32 < a.group) {
-                        float t[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) t[j] = max_nan(amax[j], amax[j ^ o]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) amax[j] = t[j];
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = blk * kBlock + j * 32;
-                    if (lane == 0 && i % a.group == 0 && i < a.dim)
-                        scales[i / a.group] = __fdiv_rn(amax[j], kE4m3Max);
-                }
-            }
-            if constexpr (VEC) {
-                const float f = quant_factor(amax[0]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[k][j] = quant_value(v[k][j], f);
-                const int i = blk * kBlock + lane * 8;
+            for (int j = 0; j < 8; ++j) {
+                const int i = blk * kBlock + j * 32 + lane;
                 if (i < a.dim)
-                    *reinterpret_cast<uint2*>(q + i) =
-                        make_uint2(e4m3x2(v[k][0], v[k][1]) | e4m3x2(v[k][2], v[k][3]) << 16,
-                                   e4m3x2(v[k][4], v[k][5]) | e4m3x2(v[k][6], v[k][7]) << 16);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = blk * kBlock + j * 32 + lane;
-                    if (i < a.dim)
-                        q[i] = (uint8_t)e4m3x2(quant_value(v[k][j], quant_factor(amax[j])), 0.0f);
-                }
+                    q[i] = (uint8_t)e4m3x2(quant_value(v[k][j], quant_factor(amax[j])), 0.0f);
             }
         }
     }
 }
 
+// ------------------------------------------------------------- forward
+
+// A CTA (with one warp to a row: each warp) walks rows, the next row's loads in
+// flight while this one is reduced and written: one row to a CTA, and CTAs that
+// come and go, left the memory idle during each CTA's reductions (4.7 TB/s at
+// 16384 rows of 2048 with an 8-bit output, against @Q8@ TB/s).
+template <typename TX, typename TR, typename TY, int NV, bool VEC, Out OUT>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_fwd_kernel(const NormArgs a) {
+    __shared__ float red[2][2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wr = warp % a.warps_per_row;  // the warp within its row
+    const bool has_res = a.residual != nullptr;
+    long long row = (long long)blockIdx.x * a.rows_per_cta + warp / a.warps_per_row;
+    const long long step = (long long)gridDim.x * a.rows_per_cta;
+
+    Raw<TX, VEC> x[NV];
+    Raw<TR, VEC> res[NV];
+    auto load = [&](long long r) {
+        const size_t base = (size_t)r * a.dim;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int blk = wr + k * a.warps_per_row;
+            x[k].load(static_cast<const TX*>(a.x) + base, blk, lane, a.dim);
+            if (has_res) res[k].load(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim);
+        }
+    };
+    if (row < a.rows) load(row);
+    // `row` is the same in a CTA, or the warps do not meet
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        const size_t base = (size_t)row * a.dim;
+        float v[NV][8];
+        float ss = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[k][j] = x[k].get(j);
+                if (has_res) v[k][j] += res[k].get(j);
+            }
+        if (row + step < a.rows) load(row + step);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int blk = wr + k * a.warps_per_row;
+            if (a.sum) store8<VEC>(static_cast<TR*>(a.sum) + base, blk, lane, a.dim, v[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
+        }
+        ss = warp_sum(ss);
+        if (a.warps_per_row > 1) {
+            // two buffers: a warp may write the next row's sums while another still
+            // reads this row's
+            if (lane == 0) red[0][turn][warp] = ss;
+            __syncthreads();
+            ss = warp_sum(lane < a.warps_per_row ? red[0][turn][lane] : 0.0f);
+        }
+        const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int blk = wr + k * a.warps_per_row;
+            float w[8];
+            load_weight<VEC>(a.weight, blk, lane, a.dim, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * w[j];
+            if constexpr (OUT == kPlain)
+                store8<VEC>(static_cast<TY*>(a.y) + base, blk, lane, a.dim, v[k]);
+        }
+        if constexpr (OUT == kE4m3) quantise<NV, VEC>(a, row, v, wr, lane, warp, red[1][turn]);
+    }
+}
+
 // ------------------------------------------------------------ gradient
 
-// CTAs walk rows blockIdx, blockIdx + gridDim, ..., each thread keeping the
-// weight's gradient of its columns in registers; norm_dw_kernel adds the CTAs'
-// sums in order.
-template <typename TX, typename TR, typename TY, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
-    __shared__ float2 red[2][32];
+// CTAs walk rows as the forward's do, each thread keeping the weight's gradient of
+// its columns in registers; norm_dw_kernel adds the CTAs' sums in order.  AHEAD:
+// the next row's loads are in flight while this one is reduced (three inputs of
+// two blocks a warp are as much as the registers hold).
+template <typename TX, typename TR, typename TY, int NV, bool VEC, bool AHEAD>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
+    __shared__ float2 red[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool has_add = a.residual != nullptr;
     float dw[NV][8];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
-    int turn = 0;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const size_t base = (size_t)row * a.dim;
-        float s[NV][8], dy[NV][8], add[NV][8];
+    Raw<TR, VEC> rs[NV], radd[NV];
+    Raw<TY, VEC> rdy[NV];
+    auto load = [&](long long r) {
+        const size_t base = (size_t)r * a.dim;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int blk = warp + k * a.warps_per_row;
-            load8<VEC>(static_cast<const TR*>(a.x) + base, blk, lane, a.dim, s[k]);
-            load8<VEC>(static_cast<const TY*>(a.dy) + base, blk, lane, a.dim, dy[k]);
-            if (a.residual)
-                load8<VEC>(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim, add[k]);
+            rs[k].load(static_cast<const TR*>(a.x) + base, blk, lane, a.dim);
+            rdy[k].load(static_cast<const TY*>(a.dy) + base, blk, lane, a.dim);
+            if (has_add) radd[k].load(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim);
         }
-        float ss = 0.0f, sg = 0.0f;
-        float w[NV][8];
+    };
+    int turn = 0;
+    if (AHEAD && blockIdx.x < a.rows) load(blockIdx.x);
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const size_t base = (size_t)row * a.dim;
+        if constexpr (!AHEAD) load(row);
+        Raw<TR, VEC> s[NV], add[NV];
+        Raw<TY, VEC> dy[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            load_weight<VEC>(a.weight, warp + k * a.warps_per_row, lane, a.dim, w[k]);
+            s[k] = rs[k];
+            dy[k] = rdy[k];
+            if (has_add) add[k] = radd[k];
+        }
+        if (AHEAD && row + gridDim.x < a.rows) load(row + gridDim.x);
+        float ss = 0.0f, sg = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float w[8];
+            load_weight<VEC>(a.weight, warp + k * a.warps_per_row, lane, a.dim, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fmaf(s[k][j], s[k][j], ss);
-                sg = fmaf(s[k][j], dy[k][j] * w[k][j], sg);
+                ss = fmaf(s[k].get(j), s[k].get(j), ss);
+                sg = fmaf(s[k].get(j), dy[k].get(j) * w[j], sg);
             }
         }
         ss = warp_sum(ss);
         sg = warp_sum(sg);
         if (a.warps_per_row > 1) {
-            // two buffers: a warp may write the next row's sums while another
-            // still reads this row's
             if (lane == 0) red[turn][warp] = make_float2(ss, sg);
             __syncthreads();
             const float2 t = lane < a.warps_per_row ? red[turn][lane] : make_float2(0.f, 0.f);
@@ -341,12 +388,14 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int blk = warp + k * a.warps_per_row;
-            float d[8];
+            float w[8], d[8];
+            load_weight<VEC>(a.weight, blk, lane, a.dim, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                d[j] = r * fmaf(-s[k][j], c, dy[k][j] * w[k][j]);
-                if (a.residual) d[j] += add[k][j];
-                dw[k][j] = fmaf(dy[k][j], s[k][j] * r, dw[k][j]);
+                const float sj = s[k].get(j), g = dy[k].get(j);
+                d[j] = r * fmaf(-sj, c, g * w[j]);
+                if (has_add) d[j] += add[k].get(j);
+                dw[k][j] = fmaf(g, sj * r, dw[k][j]);
             }
             if (a.y) store8<VEC>(static_cast<TX*>(a.y) + base, blk, lane, a.dim, d);
             if (a.sum) store8<VEC>(static_cast<TR*>(a.sum) + base, blk, lane, a.dim, d);
@@ -379,8 +428,8 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int 
 
 // -------------------------------------------------------------- launch
 
-// CTAs of the gradient per row count: the CTAs' sums of dw are written and read
-// once more, so they are kept well below the rows.
+// The most CTAs a gradient takes: their sums of dw are written and read once more.
+// (The workspace's size follows from it, so it does not depend on the device.)
 constexpr int kBwdCtas = 152 * 4;
 
 template <typename F>
@@ -396,12 +445,8 @@ bool by_types(ssm_dtype_t x, ssm_dtype_t r, ssm_dtype_t y, F&& f) {
     return true;
 }
 
-// blocks of 256 elements -> warps and blocks per warp
-void plan(int dim, int* nv, int* warps) {
-    const int blocks = (dim + kBlock - 1) / kBlock;
-    *nv = blocks <= 32 ? 1 : 2;
-    *warps = (blocks + *nv - 1) / *nv;
-}
+// blocks of 256 elements -> warps of a row, with NV blocks to a warp
+int row_warps(int dim, int nv) { return ((dim + kBlock - 1) / kBlock + nv - 1) / nv; }
 
 struct Span { const void* p; size_t n; };
 
@@ -451,12 +496,15 @@ static ssm_status_t norm_fwd(const void* x, const void* residual, const float* w
     a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.sum = sum; a.scales = scales;
     a.eps = eps; a.inv_dim = 1.0f / (float)dim; a.rows = rows; a.dim = dim;
     a.group = group; a.ngroups = ngroups;
-    int nv, warps;
-    plan(dim, &nv, &warps);
+    const int nv = dim <= 32 * kBlock ? 1 : 4, warps = row_warps(dim, nv);
     a.warps_per_row = warps;
     a.rows_per_cta = warps == 1 ? 4 : 1;
-    const unsigned grid = (unsigned)(((long long)rows + a.rows_per_cta - 1) / a.rows_per_cta);
-    const unsigned threads = 32u * warps * a.rows_per_cta;
+    const int threads = 32 * warps * a.rows_per_cta;
+    // as many CTAs as are resident: @THREADS@ threads to an SM
+    const int resident = ssm_host::sm_count() * std::max(1, kFwdThreads / threads);
+    const unsigned grid = (unsigned)std::min<long long>(
+        ((long long)rows + a.rows_per_cta - 1) / a.rows_per_cta, resident);
+    if (grid == 0) return SSM_ERR_CUDA;
     const bool vec = dim % 8 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     by_types(in, res, e4m3 ? SSM_F32 : out, [&](auto tx, auto tr, auto ty) {
@@ -468,15 +516,15 @@ static ssm_status_t norm_fwd(const void* x, const void* residual, const float* w
             if (e4m3) {
                 if (nv == 1) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, kE4m3>)
                                  : go(norm_fwd_kernel<TX, TR, TY, 1, false, kE4m3>);
-                else vec ? go(norm_fwd_kernel<TX, TR, TY, 2, true, kE4m3>)
-                         : go(norm_fwd_kernel<TX, TR, TY, 2, false, kE4m3>);
+                else vec ? go(norm_fwd_kernel<TX, TR, TY, 4, true, kE4m3>)
+                         : go(norm_fwd_kernel<TX, TR, TY, 4, false, kE4m3>);
                 return;
             }
         }
         if (nv == 1) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, kPlain>)
                          : go(norm_fwd_kernel<TX, TR, TY, 1, false, kPlain>);
-        else vec ? go(norm_fwd_kernel<TX, TR, TY, 2, true, kPlain>)
-                 : go(norm_fwd_kernel<TX, TR, TY, 2, false, kPlain>);
+        else vec ? go(norm_fwd_kernel<TX, TR, TY, 4, true, kPlain>)
+                 : go(norm_fwd_kernel<TX, TR, TY, 4, false, kPlain>);
     });
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
@@ -541,21 +589,25 @@ extern "C" ssm_status_t ssm_add_rmsnorm_bwd(const void* sum, const float* weight
     a.x = sum; a.residual = dsum; a.weight = weight; a.dy = dy; a.y = dx; a.sum = dresidual;
     a.partial = static_cast<float*>(workspace);
     a.eps = eps; a.inv_dim = 1.0f / (float)dim; a.rows = rows; a.dim = dim;
-    int nv, warps;
-    plan(dim, &nv, &warps);
+    const int nv = dim <= 16 * kBlock ? 1 : dim <= 32 * kBlock ? 2 : 4;
+    const int warps = row_warps(dim, nv);
     a.warps_per_row = warps;
     a.rows_per_cta = 1;
-    const unsigned grid = (unsigned)std::min(rows, kBwdCtas);
+    const unsigned grid = (unsigned)std::min(
+        rows, std::min(kBwdCtas, ssm_host::sm_count() * std::max(1, kBwdThreads / (32 * warps))));
+    if (grid == 0) return SSM_ERR_CUDA;
     const bool vec = dim % 8 == 0;
     by_types(in_dtype, res_dtype, dy_dtype, [&](auto tx, auto tr, auto ty) {
         using TX = decltype(tx);
         using TR = decltype(tr);
         using TY = decltype(ty);
         auto go = [&](auto kernel) { kernel<<<grid, 32u * warps, 0, s>>>(a); };
-        if (nv == 1) vec ? go(norm_bwd_kernel<TX, TR, TY, 1, true>)
-                         : go(norm_bwd_kernel<TX, TR, TY, 1, false>);
-        else vec ? go(norm_bwd_kernel<TX, TR, TY, 2, true>)
-                 : go(norm_bwd_kernel<TX, TR, TY, 2, false>);
+        if (nv == 1) vec ? go(norm_bwd_kernel<TX, TR, TY, 1, true, true>)
+                         : go(norm_bwd_kernel<TX, TR, TY, 1, false, true>);
+        else if (nv == 2) vec ? go(norm_bwd_kernel<TX, TR, TY, 2, true, true>)
+                              : go(norm_bwd_kernel<TX, TR, TY, 2, false, true>);
+        else vec ? go(norm_bwd_kernel<TX, TR, TY, 4, true, false>)
+                 : go(norm_bwd_kernel<TX, TR, TY, 4, false, false>);
     });
     norm_dw_kernel<<<(dim + 31) / 32, 256, 0, s>>>(a.partial, (int)grid, dim, dweight);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
