@@ -155,21 +155,21 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // max over the `width` consecutive lanes (a power of two) this lane is among
 __device__ __forceinline__ float lanes_max(float v, int width) {
-    for (int o = width >> 1; o > 0; o >>= 1)
-        v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        if (o < width) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// amax -> 448 / amax, the factor q takes (0 for a group of zeros; kept finite
-// so that a zero beside denormals stays zero)
+// amax -> 448 / amax, the factor q takes, within 2 ulp (an exact division costs as
+// much as the rest of the quantisation).  0 for a group of zeros, and for one whose
+// amax is infinite or NaN, where the factor leaves NaN in the places it came from;
+// kept finite so that a zero beside denormals stays zero.
 __device__ __forceinline__ float quant_factor(float amax) {
-    return amax > 0.0f ? fminf(__fdiv_rn(kE4m3Max, amax), FLT_MAX) : 0.0f;
+    return amax > 0.0f ? fminf(kE4m3Max * rcp_approx(amax), FLT_MAX) : 0.0f;
 }
 
-// y * factor with the group's NaN or zero amax giving 0
-__device__ __forceinline__ float quant_value(float y, float factor) {
-    return factor != 0.0f ? y * factor : (y - y == 0.0f ? 0.0f : y * 0.0f);
-}
+__device__ __forceinline__ float quant_scale(float amax) { return amax * (1.0f / kE4m3Max); }
 
 enum Out { kPlain, kE4m3 };
 
@@ -191,7 +191,7 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
             __syncthreads();
             row_amax = lanes_max(lane < a.warps_per_row ? red[lane] : 0.0f, 32);
         }
-        if (wr == 0 && lane == 0) scales[0] = __fdiv_rn(row_amax, kE4m3Max);
+        if (wr == 0 && lane == 0) scales[0] = quant_scale(row_amax);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -208,7 +208,7 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
             amax[0] = lanes_max(m, width);
             const int i = blk * kBlock + lane * 8;
             if ((lane & (width - 1)) == 0 && i < a.dim)
-                scales[i / a.group] = __fdiv_rn(amax[0], kE4m3Max);
+                scales[i / a.group] = quant_scale(amax[0]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) amax[j] = lanes_max(fabsf(v[k][j]), 32);
@@ -227,13 +227,13 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
             for (int j = 0; j < 8; ++j) {
                 const int i = blk * kBlock + j * 32;
                 if (lane == 0 && i % a.group == 0 && i < a.dim)
-                    scales[i / a.group] = __fdiv_rn(amax[j], kE4m3Max);
+                    scales[i / a.group] = quant_scale(amax[j]);
             }
         }
         if constexpr (VEC) {
             const float f = quant_factor(amax[0]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = quant_value(v[k][j], f);
+            for (int j = 0; j < 8; ++j) v[k][j] *= f;
             const int i = blk * kBlock + lane * 8;
             if (i < a.dim)
                 *reinterpret_cast<uint2*>(q + i) =
@@ -244,7 +244,7 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
             for (int j = 0; j < 8; ++j) {
                 const int i = blk * kBlock + j * 32 + lane;
                 if (i < a.dim)
-                    q[i] = (uint8_t)e4m3x2(quant_value(v[k][j], quant_factor(amax[j])), 0.0f);
+                    q[i] = (uint8_t)e4m3x2(v[k][j] * quant_factor(amax[j]), 0.0f);
             }
         }
     }
@@ -277,6 +277,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_fwd_kernel(const No
         }
     };
     if (row < a.rows) load(row);
+    float w1[8];  // the weight, kept where a lane has one block of it
+    if constexpr (NV == 1) load_weight<VEC>(a.weight, wr, lane, a.dim, w1);
     // `row` is the same in a CTA, or the warps do not meet
     for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
         const size_t base = (size_t)row * a.dim;
@@ -311,9 +313,9 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_fwd_kernel(const No
         for (int k = 0; k < NV; ++k) {
             const int blk = wr + k * a.warps_per_row;
             float w[8];
-            load_weight<VEC>(a.weight, blk, lane, a.dim, w);
+            if constexpr (NV > 1) load_weight<VEC>(a.weight, blk, lane, a.dim, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * w[j];
+            for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * (NV > 1 ? w[j] : w1[j]);
             if constexpr (OUT == kPlain)
                 store8<VEC>(static_cast<TY*>(a.y) + base, blk, lane, a.dim, v[k]);
         }
@@ -415,8 +417,17 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.0f;
-    if (c < dim)
-        for (int i = warp; i < parts; i += 8) t += partial[(size_t)i * dim + c];
+    if (c < dim) {
+        int i = warp;
+        for (; i + 56 < parts; i += 64) {  // eight loads at a time
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = partial[(size_t)(i + 8 * k) * dim + c];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t += v[k];
+        }
+        for (; i < parts; i += 8) t += partial[(size_t)i * dim + c];
+    }
     acc[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < dim) {
