@@ -68,6 +68,7 @@ struct CeArgs {
     uint32_t* status;
     const long long* targets;
     // loss
+    uint32_t* failed;    // [CTAs]: whether a wait ran out
     float2* parts;       // [2 * vocab tiles][tokens]: maximum (base 2), sum
     float* target_logit; // [tokens]
     // gradient
@@ -388,12 +389,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const __grid_constant__ CUtensorMap tm_P, const CeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_failed;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
     if (threadIdx.x == 0) {
+        s_failed = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -506,40 +508,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     // a wait ran out: leave the copies in flight time to land before the shared
     // memory goes
-    if (!ok)
+    if (!ok) {
+        s_failed = 1;
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
     __syncwarp();
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    if (MODE == kLoss && threadIdx.x == 0) a.failed[blockIdx.x] = s_failed;
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
 }
 
-// Joins the column halves' maxima and sums: 8 warps take every eighth part of
-// 32 rows, then warp 0 joins the eight.
-__global__ void __launch_bounds__(256) ce_join_kernel(const float2* parts, int nparts,
-                                                      const float* target_logit,
-                                                      const long long* targets, int tokens,
-                                                      int vocab, float* loss, float* lse) {
-    __shared__ float2 sh[8][32];
+// Joins the column halves' maxima and sums: 32 warps take every 32nd part of 32
+// rows, eight reads ahead (a warp that waited for each read took 30 us for 8
+// tokens' 394 parts), then warp 0 joins the 32.  The first CTA also tells the
+// status, from what the loss kernel's CTAs left.
+__global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int nparts,
+                                                       const float* target_logit,
+                                                       const long long* targets, int tokens,
+                                                       int vocab, float* loss, float* lse,
+                                                       const uint32_t* failed, int nctas,
+                                                       uint32_t* status) {
+    __shared__ float2 sh[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
+    if (blockIdx.x == 0) {
+        uint32_t f = 0;
+        for (int i = threadIdx.x; i < nctas; i += 1024) f |= failed[i];
+        f = __syncthreads_or((int)f);
+        if (threadIdx.x == 0) *status = f ? SSM_ERR_TIMEOUT : SSM_OK;
+    }
     float m = -INFINITY, s = 0.0f;
     auto join = [&](float2 p) {
         const float n = fmaxf(m, p.x), base = n == -INFINITY ? 0.0f : n;
         s = s * ex2_approx(m - base) + p.y * ex2_approx(p.x - base);
         m = n;
     };
-    if (row < tokens)
-        for (int i = warp; i < nparts; i += 8) join(parts[(size_t)i * tokens + row]);
+    if (row < tokens) {
+        for (int i = warp; i < nparts; i += 256) {
+            float2 p[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                p[k] = i + 32 * k < nparts ? parts[(size_t)(i + 32 * k) * tokens + row]
+                                           : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) join(p[k]);
+        }
+    }
     sh[warp][lane] = make_float2(m, s);
     __syncthreads();
     if (warp == 0 && row < tokens) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) join(sh[i][lane]);
+        for (int i = 1; i < 32; ++i) join(sh[i][lane]);
         const float l = fmaf(m, 0.6931471805599453f, logf(s));
         lse[row] = l;
         const long long t = targets[row];
@@ -630,6 +654,9 @@ bool sizes_fit(int tokens, int dim, int vocab) {
     return dim % 8 == 0 && (double)tokens * vocab / (kTile * kTile) < 1e9;
 }
 
+constexpr int kMaxCtas = 1024;  // room for their flags
+int grid_ctas() { return 2 * std::min(std::max(1, ssm_host::sm_count() / 2), kMaxCtas / 2); }
+
 template <Mode MODE>
 bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, const CeArgs& a,
             cudaStream_t s) {
@@ -638,8 +665,7 @@ bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, co
     if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kThreads, kSmemBytes, cache) <
         1)
         return false;
-    const int sms = ssm_host::sm_count();
-    kernel<<<2 * std::max(1, sms / 2), kThreads, kSmemBytes, s>>>(h, W, P, a);
+    kernel<<<grid_ctas(), kThreads, kSmemBytes, s>>>(h, W, P, a);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -649,7 +675,8 @@ struct Span { const void* p; size_t n; };
 
 extern "C" size_t ssm_vocab_ce_workspace_bytes(int tokens, int dim, int vocab) {
     if (tokens < 0 || dim < 1 || vocab < 1 || !sizes_fit(tokens, dim, vocab)) return 0;
-    return 256 + round256((size_t)tokens * 4) + round256((size_t)2 * tiles(vocab) * tokens * 8);
+    return 256 + kMaxCtas * 4 + round256((size_t)tokens * 4) +
+           round256((size_t)2 * tiles(vocab) * tokens * 8);
 }
 
 extern "C" size_t ssm_vocab_ce_bwd_workspace_bytes(int tokens, int dim, int vocab) {
@@ -697,13 +724,13 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CeArgs a{};
     a.tokens = tokens; a.dim = dim; a.vocab = vocab; a.targets = targets;
-    a.status = &reinterpret_cast<CeHeader*>(ws)->status;
-    a.target_logit = reinterpret_cast<float*>(ws + 256);
-    a.parts = reinterpret_cast<float2*>(ws + 256 + round256((size_t)tokens * 4));
-    if (cudaMemsetAsync(ws, 0, 256, s) != cudaSuccess || !launch<kLoss>(mh, mw, mh, a, s))
-        return SSM_ERR_CUDA;
-    ce_join_kernel<<<(tokens + 31) / 32, 256, 0, s>>>(a.parts, 2 * tiles(vocab), a.target_logit,
-                                                      targets, tokens, vocab, loss, lse);
+    a.failed = reinterpret_cast<uint32_t*>(ws + 256);
+    a.target_logit = reinterpret_cast<float*>(ws + 256 + kMaxCtas * 4);
+    a.parts = reinterpret_cast<float2*>(ws + 256 + kMaxCtas * 4 + round256((size_t)tokens * 4));
+    if (!launch<kLoss>(mh, mw, mh, a, s)) return SSM_ERR_CUDA;
+    ce_join_kernel<<<(tokens + 31) / 32, 1024, 0, s>>>(
+        a.parts, 2 * tiles(vocab), a.target_logit, targets, tokens, vocab, loss, lse, a.failed,
+        grid_ctas(), &reinterpret_cast<CeHeader*>(ws)->status);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
