@@ -523,6 +523,173 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      : "memory");
 }
 
+// ------------------------------------------------------------- few tokens
+
+// Up to 64 tokens the loss is bound by reading W once, and the pair's 256 rows of
+// tokens would be mostly empty (8 tokens of dim 1536, vocabulary 50280: 49 us with
+// them, @FEW@ here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
+// is the MMA's rows and the tokens its columns: each CTA takes one contiguous,
+// evenly cut range of the vocabulary in 128-row tiles (the last one as many rows as
+// are left, in boxes of 16, so that no CTA reads more than 15 rows beyond its share),
+// and keeps each row's and token's running maximum and sum in registers until its
+// range is through.
+constexpr int kFewTokens = 64;
+constexpr int kFewStages = 8;
+constexpr uint32_t kFewBox = 16 * 128;           // 16 rows x 64 of K
+constexpr uint32_t kFewW = 128 * 128;            // a stage's W
+constexpr int kFewThreads = 192;                 // 4 epilogue warps, TMA, MMA
+
+template <int N>
+__host__ __device__ constexpr uint32_t few_stage() { return kFewW + N * 128; }
+
+template <int N>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    ce_few_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_W,
+                  const CeArgs a, int share) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t s_tmem, s_failed;
+    __shared__ int s_target[N];
+    __shared__ float2 s_join[4][N];
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r0 = (int)min((long long)blockIdx.x * share, (long long)a.vocab);
+    const int r1 = (int)min((long long)r0 + share, (long long)a.vocab);
+    const int ntiles = (r1 - r0 + 127) / 128, depth = (a.dim + kDepth - 1) / kDepth;
+    constexpr uint32_t kCols = 2 * N < 32 ? 32 : 2 * N;
+
+    if (tid == 0) {
+        s_failed = 0;
+        for (int i = 0; i < kFewStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        fence_mbar_init();
+    }
+    for (int i = tid; i < N; i += kFewThreads) {
+        const long long t = i < a.tokens ? a.targets[i] : -1;
+        s_target[i] = t >= r0 && t < r1 ? (int)t : -1;
+    }
+    if (warp == 0) tmem_alloc(&s_tmem, kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            for (int t = 0; ok && t < ntiles; ++t) {
+                const int row = r0 + t * 128, boxes = min(8, (r1 - row + 15) / 16);
+                for (int kb = 0; kb < depth; ++kb, ++n) {
+                    const uint32_t s = n % kFewStages;
+                    ok = mbar_wait(&empty[s], ((n / kFewStages) & 1) ^ 1, nullptr);
+                    if (!ok) break;
+                    uint8_t* W = smem_raw + (smem - smem_u32(smem_raw)) + s * few_stage<N>();
+                    mbar_arrive_expect_tx(&full[s], boxes * kFewBox + N * 128);
+                    for (int j = 0; j < boxes; ++j)
+                        tma_load_2d(W + j * kFewBox, &tm_W, &full[s], kb * kDepth, row + j * 16);
+                    tma_load_2d(W + kFewW, &tm_h, &full[s], kb * kDepth, 0);
+                }
+            }
+            for (uint32_t q = n > kFewStages ? n - kFewStages : 0; ok && q < n; ++q)
+                ok = mbar_wait(&empty[q % kFewStages], (q / kFewStages) & 1, nullptr);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            for (int t = 0; ok && t < ntiles; ++t) {
+                ok = mbar_wait(&acc_empty[t & 1], ((t >> 1) & 1) ^ 1, nullptr);
+                tc_fence_after();
+                for (int kb = 0; ok && kb < depth; ++kb, ++n) {
+                    const uint32_t s = n % kFewStages;
+                    ok = mbar_wait(&full[s], (n / kFewStages) & 1, nullptr);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t W = smem + s * few_stage<N>();
+                    const uint64_t da = smem_desc_k128(W), db = smem_desc_k128(W + kFewW);
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k)
+                        mma_bf16(tmem + (t & 1) * N, da + 2 * k, db + 2 * k, idesc_bf16_f32(128, N),
+                                 (uint32_t)(kb | k));
+                    mma_commit(&empty[s]);
+                }
+                if (ok) mma_commit(&acc_full[t & 1]);
+            }
+        }
+    } else {
+        // rows' running maxima and sums, base 2, by token
+        float m[N], sum[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            m[j] = -INFINITY;
+            sum[j] = 0.0f;
+        }
+        for (int t = 0; t < ntiles; ++t) {
+            ok = mbar_wait(&acc_full[t & 1], (t >> 1) & 1, nullptr);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int row = r0 + t * 128 + warp * 32 + lane;
+            float v[N];
+#pragma unroll
+            for (int c = 0; c < N; c += 16)
+                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (t & 1) * N + c, v + c);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[t & 1]);
+            if (row < r1) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (s_target[j] == row) a.target_logit[j] = v[j];
+                    const float l = v[j] * kLog2e, n = fmaxf(m[j], l);
+                    // n is -inf only where every logit so far is
+                    const float base = n == -INFINITY ? 0.0f : n;
+                    sum[j] = fmaf(sum[j], ex2_approx(m[j] - base), ex2_approx(l - base));
+                    m[j] = n;
+                }
+            }
+        }
+        // over the warp's rows, then the four warps
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float mx = m[j];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            float sj = sum[j] * ex2_approx(m[j] - (mx == -INFINITY ? 0.0f : mx));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sj += __shfl_xor_sync(0xffffffffu, sj, o);
+            if (lane == 0) s_join[warp][j] = make_float2(mx, sj);
+        }
+    }
+    if (!ok) {
+        s_failed = 1;
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid < a.tokens) {
+        float mx = -INFINITY, sj = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_join[w][tid].x);
+        const float base = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            sj = fmaf(s_join[w][tid].y, ex2_approx(s_join[w][tid].x - base), sj);
+        a.parts[(size_t)blockIdx.x * a.tokens + tid] = make_float2(mx, sj);
+    }
+    if (tid == 0) a.failed[blockIdx.x] = s_failed;
+    if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
 // Joins the column halves' maxima and sums: 32 warps take every 32nd part of 32
 // rows, eight reads ahead (a warp that waited for each read took 30 us for 8
 // tokens' 394 parts), then warp 0 joins the 32.  The first CTA also tells the
@@ -561,13 +728,22 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
     }
     sh[warp][lane] = make_float2(m, s);
     __syncthreads();
-    if (warp == 0 && row < tokens) {
+    // warp w joins the 32 parts of row w of the CTA's rows
+    {
+        const float2 p = sh[lane][warp];
+        float mx = p.x;
 #pragma unroll
-        for (int i = 1; i < 32; ++i) join(sh[i][lane]);
-        const float l = fmaf(m, 0.6931471805599453f, logf(s));
-        lse[row] = l;
-        const long long t = targets[row];
-        loss[row] = t < 0 ? 0.0f : t < vocab ? l - target_logit[row] : NAN;
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float t = p.y * ex2_approx(p.x - (mx == -INFINITY ? 0.0f : mx));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        const int r = blockIdx.x * 32 + warp;
+        if (lane == 0 && r < tokens) {
+            const float l = fmaf(mx, 0.6931471805599453f, logf(t));
+            lse[r] = l;
+            const long long at = targets[r];
+            loss[r] = at < 0 ? 0.0f : at < vocab ? l - target_logit[r] : NAN;
+        }
     }
 }
 
@@ -669,6 +845,20 @@ bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, co
     return cudaGetLastError() == cudaSuccess;
 }
 
+// the vocabulary of one CTA of the few-token kernel, whole boxes of 16 rows
+int few_share(int vocab) { return ((vocab + grid_ctas() - 1) / grid_ctas() + 15) / 16 * 16; }
+
+template <int N>
+bool launch_few(const CUtensorMap& h, const CUtensorMap& W, const CeArgs& a, cudaStream_t s) {
+    auto kernel = ce_few_kernel<N>;
+    constexpr int smem = kFewStages * few_stage<N>() + 1024;
+    static std::atomic<int> cache[ssm_host::kMaxDevices];
+    if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kFewThreads, smem, cache) < 1)
+        return false;
+    kernel<<<grid_ctas(), kFewThreads, smem, s>>>(h, W, a, few_share(a.vocab));
+    return cudaGetLastError() == cudaSuccess;
+}
+
 struct Span { const void* p; size_t n; };
 
 }  // namespace
@@ -676,7 +866,8 @@ struct Span { const void* p; size_t n; };
 extern "C" size_t ssm_vocab_ce_workspace_bytes(int tokens, int dim, int vocab) {
     if (tokens < 0 || dim < 1 || vocab < 1 || !sizes_fit(tokens, dim, vocab)) return 0;
     return 256 + kMaxCtas * 4 + round256((size_t)tokens * 4) +
-           round256((size_t)2 * tiles(vocab) * tokens * 8);
+           round256((size_t)std::max(2 * tiles(vocab), tokens <= kFewTokens ? kMaxCtas : 0) * tokens *
+                    8);
 }
 
 extern "C" size_t ssm_vocab_ce_bwd_workspace_bytes(int tokens, int dim, int vocab) {
@@ -716,9 +907,11 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
         for (int j = 0; j < i; ++j)
             if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SSM_ERR_ALIAS;
 
+    const bool few = tokens <= kFewTokens;
+    const int cols = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;  // of the few-token kernel
     CUtensorMap mh, mw;
-    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
-        !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64))
+    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, few ? cols : 64, 64) ||
+        !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, few ? 16 : 64, 64))
         return SSM_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -727,9 +920,13 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
     a.failed = reinterpret_cast<uint32_t*>(ws + 256);
     a.target_logit = reinterpret_cast<float*>(ws + 256 + kMaxCtas * 4);
     a.parts = reinterpret_cast<float2*>(ws + 256 + kMaxCtas * 4 + round256((size_t)tokens * 4));
-    if (!launch<kLoss>(mh, mw, mh, a, s)) return SSM_ERR_CUDA;
+    const bool ok = !few      ? launch<kLoss>(mh, mw, mh, a, s)
+                    : cols == 16 ? launch_few<16>(mh, mw, a, s)
+                    : cols == 32 ? launch_few<32>(mh, mw, a, s)
+                                 : launch_few<64>(mh, mw, a, s);
+    if (!ok) return SSM_ERR_CUDA;
     ce_join_kernel<<<(tokens + 31) / 32, 1024, 0, s>>>(
-        a.parts, 2 * tiles(vocab), a.target_logit, targets, tokens, vocab, loss, lse, a.failed,
+        a.parts, few ? grid_ctas() : 2 * tiles(vocab), a.target_logit, targets, tokens, vocab, loss, lse, a.failed,
         grid_ctas(), &reinterpret_cast<CeHeader*>(ws)->status);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

@@ -192,3 +192,16 @@ def test_writes_stay_inside_the_outputs():
             assert not v.isnan().any(), k
     for v, b in zip((h, W, t, d), before):
         assert torch.equal(v, b)
+
+
+# few tokens: the columns of the vocabulary-major kernel (16, 32 or 64, full and not)
+# and the first size past it; vocabularies cut among the CTAs into whole tiles, part
+# of a tile, part of a box of 16 rows, and into fewer pieces than there are CTAs
+@pytest.mark.parametrize("tokens", [1, 15, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("dim,vocab", [(64, 15), (520, 2433), (72, 20011), (136, 60000)])
+def test_few_tokens(tokens, dim, vocab):
+    h, W, t, d = _inputs(tokens, dim, vocab, tokens + vocab)
+    loss, lse = binding.ssm_vocab_ce_fwd(h.cuda(), W.cuda(), t.cuda())
+    loss_ref, lse_ref = P.ce_fwd(to64(h), to64(W), t.numpy())
+    _check_loss(lse, lse_ref, lse_ref)
+    _check_loss(loss, loss_ref, lse_ref)
