@@ -382,7 +382,8 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_
 
 // ----------------------------------------------------------------- kernel
 
-// Tensor maps of 64 x 64 boxes: h (tokens x dim), W (vocab x dim), P (tokens x ld).
+// Tensor maps of h (tokens x dim), W (vocab x dim) and P (tokens x ld): boxes of 64
+// of K by a CTA's 128 rows (loss and P), or 64 x 64 (gradient).
 template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_W,
@@ -437,17 +438,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t A = smem + s * kStageBytes, B = A + kOperand;
                     const int k = w.k0 + kb * kDepth;
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    if constexpr (MODE != kGrad) {
+                        load_box(A, &tm_h, bar, k, am);
+                        load_box(B, &tm_W, bar, k, a.v0 + bn);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if constexpr (MODE != kGrad) {
-                            load_box(A + j * kBox, &tm_h, bar, k, am + 64 * j);
-                            load_box(B + j * kBox, &tm_W, bar, k, a.v0 + bn + 64 * j);
-                        } else if (w.dw) {
-                            load_box(A + j * kBox, &tm_P, bar, am + 64 * j, k);
-                            load_box(B + j * kBox, &tm_h, bar, bn + 64 * j, k);
-                        } else {
-                            load_box(A + j * kBox, &tm_P, bar, k, am + 64 * j);
-                            load_box(B + j * kBox, &tm_W, bar, bn + 64 * j, a.v0 + k);
+                        for (int j = 0; j < 2; ++j) {
+                            if (w.dw) {
+                                load_box(A + j * kBox, &tm_P, bar, am + 64 * j, k);
+                                load_box(B + j * kBox, &tm_h, bar, bn + 64 * j, k);
+                            } else {
+                                load_box(A + j * kBox, &tm_P, bar, k, am + 64 * j);
+                                load_box(B + j * kBox, &tm_W, bar, bn + 64 * j, a.v0 + k);
+                            }
                         }
                     }
                 }
@@ -530,12 +533,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // them, @FEW@ here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
 // is the MMA's rows and the tokens its columns: each CTA takes one contiguous,
 // evenly cut range of the vocabulary in 128-row tiles (the last one as many rows as
-// are left, in boxes of 16, so that no CTA reads more than 15 rows beyond its share),
-// and keeps each row's and token's running maximum and sum in registers until its
+// are left, in boxes of 64 and 16, so that no CTA reads more than 15 rows beyond its
+// share; all of it in boxes of 16 was bound by one thread's issue of nine loads a
+// stage: 37 us), and keeps each row's and token's running maximum and sum in registers until its
 // range is through.
 constexpr int kFewTokens = 64;
-constexpr int kFewStages = 8;
-constexpr uint32_t kFewBox = 16 * 128;           // 16 rows x 64 of K
 constexpr uint32_t kFewW = 128 * 128;            // a stage's W
 constexpr int kFewThreads = 192;                 // 4 epilogue warps, TMA, MMA
 
@@ -543,9 +545,15 @@ template <int N>
 __host__ __device__ constexpr uint32_t few_stage() { return kFewW + N * 128; }
 
 template <int N>
+__host__ __device__ constexpr int few_stages() { return 216 * 1024 / few_stage<N>(); }
+
+template <int N>
 __global__ void __launch_bounds__(kFewThreads, 1)
-    ce_few_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_W,
-                  const CeArgs a, int share) {
+    ce_few_kernel(const __grid_constant__ CUtensorMap tm_h,
+                  const __grid_constant__ CUtensorMap tm_W128,
+                  const __grid_constant__ CUtensorMap tm_W64,
+                  const __grid_constant__ CUtensorMap tm_W16, const CeArgs a, int share) {
+    constexpr uint32_t kFewStages = few_stages<N>();
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t s_tmem, s_failed;
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     if (tid == 0) {
         s_failed = 0;
-        for (int i = 0; i < kFewStages; ++i) {
+        for (uint32_t i = 0; i < kFewStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -581,19 +589,30 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const uint32_t tmem = s_tmem;
     bool ok = true;
 
+    // the join may take its place beside this kernel's CTAs
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 4) {
         if (lane == 0) {
             uint32_t n = 0;
             for (int t = 0; ok && t < ntiles; ++t) {
-                const int row = r0 + t * 128, boxes = min(8, (r1 - row + 15) / 16);
+                const int row = r0 + t * 128, rows = min(128, (r1 - row + 15) / 16 * 16);
                 for (int kb = 0; kb < depth; ++kb, ++n) {
                     const uint32_t s = n % kFewStages;
                     ok = mbar_wait(&empty[s], ((n / kFewStages) & 1) ^ 1, nullptr);
                     if (!ok) break;
                     uint8_t* W = smem_raw + (smem - smem_u32(smem_raw)) + s * few_stage<N>();
-                    mbar_arrive_expect_tx(&full[s], boxes * kFewBox + N * 128);
-                    for (int j = 0; j < boxes; ++j)
-                        tma_load_2d(W + j * kFewBox, &tm_W, &full[s], kb * kDepth, row + j * 16);
+                    mbar_arrive_expect_tx(&full[s], (rows + N) * 128);
+                    if (rows == 128) {
+                        tma_load_2d(W, &tm_W128, &full[s], kb * kDepth, row);
+                    } else {
+                        int j = 0;
+                        if (rows >= 64) {
+                            tma_load_2d(W, &tm_W64, &full[s], kb * kDepth, row);
+                            j = 64;
+                        }
+                        for (; j < rows; j += 16)
+                            tma_load_2d(W + j * 128, &tm_W16, &full[s], kb * kDepth, row + j);
+                    }
                     tma_load_2d(W + kFewW, &tm_h, &full[s], kb * kDepth, 0);
                 }
             }
@@ -703,6 +722,8 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
     __shared__ float2 sh[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
+    // launched beside the loss kernel's end: wait for all it wrote
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0) {
         uint32_t f = 0;
         for (int i = threadIdx.x; i < nctas; i += 1024) f |= failed[i];
@@ -849,13 +870,13 @@ bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, co
 int few_share(int vocab) { return ((vocab + grid_ctas() - 1) / grid_ctas() + 15) / 16 * 16; }
 
 template <int N>
-bool launch_few(const CUtensorMap& h, const CUtensorMap& W, const CeArgs& a, cudaStream_t s) {
+bool launch_few(const CUtensorMap& h, const CUtensorMap* W, const CeArgs& a, cudaStream_t s) {
     auto kernel = ce_few_kernel<N>;
-    constexpr int smem = kFewStages * few_stage<N>() + 1024;
+    constexpr int smem = few_stages<N>() * few_stage<N>() + 1024;
     static std::atomic<int> cache[ssm_host::kMaxDevices];
     if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kFewThreads, smem, cache) < 1)
         return false;
-    kernel<<<grid_ctas(), kFewThreads, smem, s>>>(h, W, a, few_share(a.vocab));
+    kernel<<<grid_ctas(), kFewThreads, smem, s>>>(h, W[0], W[1], W[2], a, few_share(a.vocab));
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -909,9 +930,11 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
 
     const bool few = tokens <= kFewTokens;
     const int cols = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;  // of the few-token kernel
-    CUtensorMap mh, mw;
-    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, few ? cols : 64, 64) ||
-        !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, few ? 16 : 64, 64))
+    CUtensorMap mh, mw[3];
+    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, few ? cols : kHalf, 64) ||
+        !make_tmap_2d(&mw[0], W, SSM_BF16, vocab, dim, kHalf, 64) ||
+        (few && (!make_tmap_2d(&mw[1], W, SSM_BF16, vocab, dim, 64, 64) ||
+                 !make_tmap_2d(&mw[2], W, SSM_BF16, vocab, dim, 16, 64))))
         return SSM_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -920,15 +943,26 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
     a.failed = reinterpret_cast<uint32_t*>(ws + 256);
     a.target_logit = reinterpret_cast<float*>(ws + 256 + kMaxCtas * 4);
     a.parts = reinterpret_cast<float2*>(ws + 256 + kMaxCtas * 4 + round256((size_t)tokens * 4));
-    const bool ok = !few      ? launch<kLoss>(mh, mw, mh, a, s)
+    const bool ok = !few      ? launch<kLoss>(mh, mw[0], mh, a, s)
                     : cols == 16 ? launch_few<16>(mh, mw, a, s)
                     : cols == 32 ? launch_few<32>(mh, mw, a, s)
                                  : launch_few<64>(mh, mw, a, s);
     if (!ok) return SSM_ERR_CUDA;
-    ce_join_kernel<<<(tokens + 31) / 32, 1024, 0, s>>>(
-        a.parts, few ? grid_ctas() : 2 * tiles(vocab), a.target_logit, targets, tokens, vocab, loss, lse, a.failed,
+    // launched as the loss kernel's CTAs end, which saves the gap between the two
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((tokens + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, ce_join_kernel, (const float2*)a.parts, few ? grid_ctas() : 2 * tiles(vocab),
+        (const float*)a.target_logit, targets, tokens, vocab, loss, lse, (const uint32_t*)a.failed,
         grid_ctas(), &reinterpret_cast<CeHeader*>(ws)->status);
-    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+    return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const long long* targets,
@@ -973,10 +1007,12 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
     a.P = reinterpret_cast<__nv_bfloat16*>(ws + 256);
     a.ld = plan.piece;
     a.dh_parts = reinterpret_cast<float*>(ws + 256 + round256((size_t)tokens * plan.piece * 2));
-    CUtensorMap mh, mw, mp;
+    CUtensorMap mh, mw, mp, mh2, mw2;
     if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
         !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64) ||
-        !make_tmap_2d(&mp, a.P, SSM_BF16, tokens, plan.piece, 64, 64))
+        !make_tmap_2d(&mp, a.P, SSM_BF16, tokens, plan.piece, 64, 64) ||
+        !make_tmap_2d(&mh2, h, SSM_BF16, tokens, dim, kHalf, 64) ||
+        !make_tmap_2d(&mw2, W, SSM_BF16, vocab, dim, kHalf, 64))
         return SSM_ERR_CUDA;
     CeHeader* head = reinterpret_cast<CeHeader*>(ws);
     a.scale = &head->scale;
@@ -992,7 +1028,7 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
         a.first_piece = v0 == 0;
         const int depth = (a.width + kDepth - 1) / kDepth;
         a.splits = (depth + a.split_depth - 1) / a.split_depth;
-        if (!launch<kProb>(mh, mw, mp, a, s) || !launch<kGrad>(mh, mw, mp, a, s))
+        if (!launch<kProb>(mh2, mw2, mp, a, s) || !launch<kGrad>(mh, mw, mp, a, s))
             return SSM_ERR_CUDA;
     }
     const size_t n = (size_t)tokens * dim;
