@@ -47,8 +47,9 @@ constexpr int kStages = 6;
 constexpr uint32_t kBox = 64 * 128;      // a 64 x 64 box of bf16
 constexpr uint32_t kOperand = 2 * kBox;  // 128 x 64
 constexpr uint32_t kStageBytes = 2 * kOperand;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;
 constexpr int kEpiWarps = 8;
+constexpr uint32_t kOutBox = 32 * 128;   // a warp's 32 rows by 128 bytes on their way out
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBox + 1024;
 constexpr int kThreads = (kEpiWarps + 2) * 32;  // + TMA warp, MMA warp
 constexpr uint32_t kTmemCols = 512;             // two accumulators of 256 columns
 constexpr int kGroupM = 32;  // token tiles whose h stays in L2 while W passes
@@ -269,39 +270,104 @@ struct RowSum {
     }
 };
 
+// v[at], as 32 selections: indexed, the array would live in local memory, written
+// for every tile
+__device__ __forceinline__ float pick(const float* v, int at) {
+    float l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.eq.s32 p, %1, %2;\n\t"
+            "selp.f32 %0, %3, %0, p;\n\t}"
+            : "+f"(l)
+            : "r"(at), "r"(j), "f"(v[j]));
+    return l;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 columns of a row to memory, `n` of them (a multiple of 8)
-__device__ __forceinline__ void store_row(void* p, const float* v, int n, bool bf16) {
-    if (bf16) {
-        uint4* q = static_cast<uint4*>(p);
+// A warp's 32 rows (one to a lane) go out 128 bytes of each at a time: into shared
+// memory in the 128-byte swizzle (16-byte pieces XORed with row mod 8), from there by
+// TMA, which clips them at the tensor's end.  (Rows written by their lanes, 16 bytes at
+// 32 places at a time, made dW of 8 tokens take @DWOLD@.)
+struct OutBox {
+    uint32_t smem;  // the warp's 4 KB
+    int lane;
+
+    __device__ void ready() const {  // the last box has been read out
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+    }
+    __device__ void put(int piece, uint4 w) const {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         smem + lane * 128 + ((piece ^ (lane & 7)) << 4)),
+                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                     : "memory");
+    }
+    __device__ void put_bf16(int piece0, const float* v) const {  // 32 values
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (8 * j < n)
-                q[j] = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]),
-                                  pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                  pack_bf16(v[8 * j + 4], v[8 * j + 5]),
-                                  pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-    } else {
-        float4* q = static_cast<float4*>(p);
+            put(piece0 + j, make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]),
+                                       pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                       pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                                       pack_bf16(v[8 * j + 6], v[8 * j + 7])));
+    }
+    __device__ void put_f32(const float* v) const {  // 32 values
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (4 * j < n)
-                q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            put(j, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                              __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
     }
-}
+    __device__ void send(const CUtensorMap* map, int c0, int c1) const {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                    reinterpret_cast<uint64_t>(map)),
+                "r"(smem), "r"(c0), "r"(c1)
+                : "memory");
+            bulk_commit();
+        }
+    }
+    // ADD: onto what is there, in fp32
+    template <bool ADD>
+    __device__ void send3(const CUtensorMap* map, int c0, int c1, int c2) const {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (ADD)
+                asm volatile(
+                    "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group "
+                    "[%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                    "r"(smem), "r"(c0), "r"(c1), "r"(c2)
+                    : "memory");
+            else
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group "
+                    "[%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                    "r"(smem), "r"(c0), "r"(c1), "r"(c2)
+                    : "memory");
+            bulk_commit();
+        }
+    }
+};
 
-// (the TMEM loads are warp-wide: lanes that took different branches meet before)
 // The half (128 columns) of one row of an accumulator that this thread empties:
-// taddr is its first column, row the row in the result, c0 the first column.
-template <Mode MODE>
-__device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_t taddr, int row,
-                                         int c0) {
-    float v[32];
+// taddr is its first column, row0 the warp's first row in the result, c0 the first
+// column.  `release` is called once the accumulator has been read.  (The TMEM loads
+// are warp-wide: lanes that took different branches meet before.)
+template <Mode MODE, typename F>
+__device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_t taddr, int row0,
+                                         int c0, const OutBox& out, const CUtensorMap* map_dh,
+                                         const CUtensorMap* map_out, F&& release) {
+    const int row = row0 + out.lane;
     if constexpr (MODE == kLoss) {
+        float v[32];
         const bool in = row < a.tokens;
         const long long target = in ? a.targets[row] : -1;
         RowSum sum{-INFINITY, 0.0f};
@@ -310,71 +376,82 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_
             __syncwarp();
             tmem_ld32(taddr + c, v);
             tmem_wait_ld();
+            if (c + 32 == kHalf) release();
             const int col = c0 + c;
             if (col + 32 <= a.vocab) sum.add(v, 32);
             else if (col < a.vocab) sum.add(v, a.vocab - col);
             const long long at = target - col;
-            if (at >= 0 && at < 32 && target < a.vocab) {
-                float l = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j == (int)at) l = v[j];
-                a.target_logit[row] = l;
-            }
+            if (at >= 0 && at < 32 && target < a.vocab) a.target_logit[row] = pick(v, (int)at);
         }
         if (in) a.parts[(size_t)(c0 / kHalf) * a.tokens + row] = make_float2(sum.m, sum.s);
     } else if constexpr (MODE == kProb) {
+        float v[32];
         const bool in = row < a.tokens;
         const long long target = in ? a.targets[row] : -1;
         const bool counts = target >= 0 && target < a.vocab;
         const float g = counts ? __fdiv_rn(a.dloss[row], *a.scale) : 0.0f;
         const float lse2 = in ? a.lse[row] * kLog2e : 0.0f;
+        // the target's column in the piece, -1 where it is in none of it
+        const long long rel = target - a.v0;
+        const int tcol = counts && rel >= 0 && rel < a.width ? (int)rel : -1;
 #pragma unroll 1
         for (int c = 0; c < kHalf; c += 32) {
             __syncwarp();
             tmem_ld32(taddr + c, v);
             tmem_wait_ld();
+            if (c + 32 == kHalf) release();
             const int col = c0 + c;  // within the piece
-            const long long at = target - a.v0 - col;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 float p = ex2_approx(fmaf(v[j], kLog2e, -lse2));
-                if (at == j) p -= 1.0f;
-                // a token without loss takes nothing, whatever its logits are; what
-                // lies past the vocabulary is K of the next products
-                v[j] = counts && col + j < a.width ? p * g : 0.0f;
+                if (tcol == col + j) p -= 1.0f;
+                v[j] = p * g;
             }
-            if (in) store_row(a.P + (size_t)row * a.ld + col, v, 32, true);
+            // a token without loss takes nothing, whatever its logits are
+            if (!counts) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            }
+            // what lies past the vocabulary is K of the next products
+            if (col + 32 > a.width) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (col + j >= a.width) v[j] = 0.0f;
+            }
+            if ((c & 32) == 0) out.ready();
+            out.put_bf16((c & 32) / 8, v);
+            if ((c & 32) && row0 < a.tokens) out.send(map_out, col - 32, row0);
         }
     } else {
-        const int rows = w.dw ? a.width : a.tokens;
+        float v[32];
         const float scale = *a.scale;
 #pragma unroll 1
         for (int c = 0; c < kHalf; c += 32) {
             __syncwarp();
             tmem_ld32(taddr + c, v);
             tmem_wait_ld();
+            if (c + 32 == kHalf) release();
             const int col = c0 + c;
-            const int n = row < rows ? min(32, a.dim - col) : 0;
-            if (n <= 0) {
-                // nothing of this row here
-            } else if (w.dw) {
-                const size_t o = (size_t)(a.v0 + row) * a.dim + col;
+            if (w.dw) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] *= scale;
-                store_row(static_cast<uint8_t*>(a.dW) + o * (a.dw_bf16 ? 2 : 4), v, n, a.dw_bf16);
-            } else {
-                float* p = a.dh_parts + ((size_t)w.split * a.tokens + row) * a.dim + col;
-                if (!a.first_piece) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        if (j < n) {
-                            const float4 o = *reinterpret_cast<const float4*>(p + j);
-                            v[j] += o.x; v[j + 1] += o.y; v[j + 2] += o.z; v[j + 3] += o.w;
-                        }
-                    }
+                if (a.dw_bf16) {
+                    if ((c & 32) == 0) out.ready();
+                    out.put_bf16((c & 32) / 8, v);
+                    if ((c & 32) && col - 32 < a.dim && row0 < a.width)
+                        out.send(map_out, col - 32, a.v0 + row0);
+                } else {
+                    out.ready();
+                    out.put_f32(v);
+                    if (col < a.dim && row0 < a.width) out.send(map_out, col, a.v0 + row0);
                 }
-                store_row(p, v, n, false);
+            } else {
+                out.ready();
+                out.put_f32(v);
+                if (col < a.dim && row0 < a.tokens) {
+                    if (a.first_piece) out.send3<false>(map_dh, col, row0, w.split);
+                    else out.send3<true>(map_dh, col, row0, w.split);
+                }
             }
         }
     }
@@ -387,7 +464,8 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_
 template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ce_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_W,
-              const __grid_constant__ CUtensorMap tm_P, const CeArgs a) {
+              const __grid_constant__ CUtensorMap tm_P, const __grid_constant__ CUtensorMap tm_dh,
+              const __grid_constant__ CUtensorMap tm_out, const CeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t s_tmem, s_failed;
@@ -493,6 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- epilogue: warp w of a quarter's two empties lanes 32 (w % 4) .. and
         // the columns of its half
         const int quarter = warp & 3, half = warp >> 2;
+        const OutBox out{smem + kStages * kStageBytes + warp * kOutBox, lane};
         Item w;
         for (int i = 0; sched.get(a, i, w); ++i) {
             // every lane waits: each then acquires by itself
@@ -502,12 +581,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (i & 1) * kTile +
                                    half * kHalf;
-            epilogue<MODE>(a, w, taddr, w.m0 + (int)rank * kHalf + quarter * 32 + lane,
-                           w.n0 + half * kHalf);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_remote(first_cta(&acc_empty[i & 1]));
+            epilogue<MODE>(a, w, taddr, w.m0 + (int)rank * kHalf + quarter * 32,
+                           w.n0 + half * kHalf, out, &tm_dh, &tm_out, [&] {
+                               tc_fence_before();
+                               __syncwarp();
+                               if (lane == 0) arrive_remote(first_cta(&acc_empty[i & 1]));
+                           });
         }
+        if (MODE != kLoss && lane == 0) bulk_wait_all();
     }
     // a wait ran out: leave the copies in flight time to land before the shared
     // memory goes
@@ -855,14 +936,14 @@ constexpr int kMaxCtas = 1024;  // room for their flags
 int grid_ctas() { return 2 * std::min(std::max(1, ssm_host::sm_count() / 2), kMaxCtas / 2); }
 
 template <Mode MODE>
-bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P, const CeArgs& a,
-            cudaStream_t s) {
+bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P,
+            const CUtensorMap& dh, const CUtensorMap& out, const CeArgs& a, cudaStream_t s) {
     auto kernel = ce_kernel<MODE>;
     static std::atomic<int> cache[ssm_host::kMaxDevices];
     if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kThreads, kSmemBytes, cache) <
         1)
         return false;
-    kernel<<<grid_ctas(), kThreads, kSmemBytes, s>>>(h, W, P, a);
+    kernel<<<grid_ctas(), kThreads, kSmemBytes, s>>>(h, W, P, dh, out, a);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -878,6 +959,19 @@ bool launch_few(const CUtensorMap& h, const CUtensorMap* W, const CeArgs& a, cud
         return false;
     kernel<<<grid_ctas(), kFewThreads, smem, s>>>(h, W[0], W[1], W[2], a, few_share(a.vocab));
     return cudaGetLastError() == cudaSuccess;
+}
+
+// dh's fp32 sums, (splits, tokens, dim): clipped at each split's tokens
+bool make_parts_map(CUtensorMap* map, const float* base, int dim, int tokens, int splits) {
+    auto fn = ssm_host::encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)tokens, (cuuint64_t)splits};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 4, (cuuint64_t)dim * 4 * tokens};
+    const cuuint32_t box[3] = {32, 32, 1}, one[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box,
+              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 struct Span { const void* p; size_t n; };
@@ -943,7 +1037,7 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
     a.failed = reinterpret_cast<uint32_t*>(ws + 256);
     a.target_logit = reinterpret_cast<float*>(ws + 256 + kMaxCtas * 4);
     a.parts = reinterpret_cast<float2*>(ws + 256 + kMaxCtas * 4 + round256((size_t)tokens * 4));
-    const bool ok = !few      ? launch<kLoss>(mh, mw[0], mh, a, s)
+    const bool ok = !few      ? launch<kLoss>(mh, mw[0], mh, mh, mh, a, s)
                     : cols == 16 ? launch_few<16>(mh, mw, a, s)
                     : cols == 32 ? launch_few<32>(mh, mw, a, s)
                                  : launch_few<64>(mh, mw, a, s);
@@ -1007,12 +1101,16 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
     a.P = reinterpret_cast<__nv_bfloat16*>(ws + 256);
     a.ld = plan.piece;
     a.dh_parts = reinterpret_cast<float*>(ws + 256 + round256((size_t)tokens * plan.piece * 2));
-    CUtensorMap mh, mw, mp, mh2, mw2;
+    CUtensorMap mh, mw, mp, mh2, mw2, mdh, mdw, mpo;
     if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
         !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64) ||
         !make_tmap_2d(&mp, a.P, SSM_BF16, tokens, plan.piece, 64, 64) ||
         !make_tmap_2d(&mh2, h, SSM_BF16, tokens, dim, kHalf, 64) ||
-        !make_tmap_2d(&mw2, W, SSM_BF16, vocab, dim, kHalf, 64))
+        !make_tmap_2d(&mw2, W, SSM_BF16, vocab, dim, kHalf, 64) ||
+        // what the epilogues write: boxes of 32 rows by 128 bytes
+        !make_tmap_2d(&mpo, a.P, SSM_BF16, tokens, plan.piece, 32, 64) ||
+        !make_tmap_2d(&mdw, dW, grad_dtype, vocab, dim, 32, 128 / (int)ge) ||
+        !make_parts_map(&mdh, a.dh_parts, dim, tokens, plan.splits))
         return SSM_ERR_CUDA;
     CeHeader* head = reinterpret_cast<CeHeader*>(ws);
     a.scale = &head->scale;
@@ -1028,7 +1126,8 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
         a.first_piece = v0 == 0;
         const int depth = (a.width + kDepth - 1) / kDepth;
         a.splits = (depth + a.split_depth - 1) / a.split_depth;
-        if (!launch<kProb>(mh2, mw2, mp, a, s) || !launch<kGrad>(mh, mw, mp, a, s))
+        if (!launch<kProb>(mh2, mw2, mp, mdh, mpo, a, s) ||
+            !launch<kGrad>(mh, mw, mp, mdh, mdw, a, s))
             return SSM_ERR_CUDA;
     }
     const size_t n = (size_t)tokens * dim;
