@@ -52,6 +52,7 @@ constexpr uint32_t kOutBox = 32 * 128;   // a warp's 32 rows by 128 bytes on the
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBox + 1024;
 constexpr int kThreads = (kEpiWarps + 2) * 32;  // + TMA warp, MMA warp
 constexpr uint32_t kTmemCols = 512;             // two accumulators of 256 columns
+constexpr int kEpilogue = 6;  // stages in whose time a tile's epilogue runs (2 us)
 constexpr int kGroupM = 32;  // token tiles whose h stays in L2 while W passes
 
 enum Mode { kLoss, kProb, kGrad };
@@ -189,7 +190,10 @@ struct Schedule {
             const int rest = n_dh % pairs;
             own_dh = n_dh / pairs + (pair < rest ? 1 : 0);
             free_pairs = rest ? pairs - rest : 0;
-            early = (dh_depth + dw_depth / 2) / dw_depth;  // dW tiles in the time of one of dh
+            // dW tiles in the time of one of dh: a tile takes its products' time or its
+            // epilogue's
+            const int dw_cost = max(dw_depth, kEpilogue);
+            early = (max(dh_depth, kEpilogue) + dw_cost / 2) / dw_cost;
             n_early = (int)min((long long)n_dw, (long long)early * free_pairs);
         } else {
             nt = ((MODE == kProb ? a.width : a.vocab) + kTile - 1) / kTile;
@@ -412,15 +416,10 @@ __device__ __forceinline__ void epilogue(const CeArgs& a, const Item& w, uint32_
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             }
-            // what lies past the vocabulary is K of the next products
-            if (col + 32 > a.width) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (col + j >= a.width) v[j] = 0.0f;
-            }
             if ((c & 32) == 0) out.ready();
             out.put_bf16((c & 32) / 8, v);
-            if ((c & 32) && row0 < a.tokens) out.send(map_out, col - 32, row0);
+            if ((c & 32) && col - 32 < a.width && row0 < a.tokens)
+                out.send(map_out, col - 32, row0);
         }
     } else {
         float v[32];
@@ -628,7 +627,9 @@ __host__ __device__ constexpr uint32_t few_stage() { return kFewW + N * 128; }
 template <int N>
 __host__ __device__ constexpr int few_stages() { return 216 * 1024 / few_stage<N>(); }
 
-template <int N>
+// PROB: the epilogue is P instead (bf16, a token's 32 neighbouring columns to a warp's
+// store).
+template <int N, bool PROB>
 __global__ void __launch_bounds__(kFewThreads, 1)
     ce_few_kernel(const __grid_constant__ CUtensorMap tm_h,
                   const __grid_constant__ CUtensorMap tm_W128,
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t s_tmem, s_failed;
     __shared__ int s_target[N];
-    __shared__ float2 s_join[4][N];
+    __shared__ float2 s_join[4][N];  // PROB: of [0], a token's lse (base 2) and dloss / scale
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = (int)min((long long)blockIdx.x * share, (long long)a.vocab);
@@ -662,6 +663,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int i = tid; i < N; i += kFewThreads) {
         const long long t = i < a.tokens ? a.targets[i] : -1;
         s_target[i] = t >= r0 && t < r1 ? (int)t : -1;
+        if constexpr (PROB) {
+            const bool counts = t >= 0 && t < a.vocab;
+            s_join[0][i] = counts ? make_float2(a.lse[i] * kLog2e, __fdiv_rn(a.dloss[i], *a.scale))
+                                  : make_float2(0.0f, 0.0f);
+            s_join[1][i].x = counts ? 1.0f : 0.0f;
+        }
     }
     if (warp == 0) tmem_alloc(&s_tmem, kCols);
     tc_fence_before();
@@ -744,7 +751,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[t & 1]);
-            if (row < r1) {
+            if constexpr (PROB) {
+                if (row < r1) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        if (j >= a.tokens) break;
+                        const float2 g = s_join[0][j];
+                        float p = ex2_approx(fmaf(v[j], kLog2e, -g.x));
+                        if (s_target[j] == row) p -= 1.0f;
+                        // a token without loss takes nothing, whatever its logits are
+                        p = s_join[1][j].x != 0.0f ? p * g.y : 0.0f;
+                        a.P[(size_t)j * a.ld + row] = __float2bfloat16_rn(p);
+                    }
+                }
+            } else if (row < r1) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     if (s_target[j] == row) a.target_logit[j] = v[j];
@@ -758,7 +778,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         // over the warp's rows, then the four warps
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < (PROB ? 0 : N); ++j) {
             float mx = m[j];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -776,7 +796,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid < a.tokens) {
+    if (!PROB && tid < a.tokens) {
         float mx = -INFINITY, sj = 0.0f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) mx = fmaxf(mx, s_join[w][tid].x);
@@ -786,23 +806,30 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             sj = fmaf(s_join[w][tid].y, ex2_approx(s_join[w][tid].x - base), sj);
         a.parts[(size_t)blockIdx.x * a.tokens + tid] = make_float2(mx, sj);
     }
-    if (tid == 0) a.failed[blockIdx.x] = s_failed;
+    if (tid == 0) {
+        if (!PROB) a.failed[blockIdx.x] = s_failed;
+        else if (s_failed) record_status(a.status, SSM_ERR_TIMEOUT);
+    }
     if (warp == 0) tmem_dealloc(tmem, kCols);
 }
 
-// Joins the column halves' maxima and sums: 32 warps take every 32nd part of 32
-// rows, eight reads ahead (a warp that waited for each read took 30 us for 8
-// tokens' 394 parts), then warp 0 joins the 32.  The first CTA also tells the
-// status, from what the loss kernel's CTAs left.
+// Joins the column halves' maxima and sums: a CTA takes 8 rows, 128 threads to a row
+// every 128th part, eight reads ahead; then warp w joins the 128 of row w.  (Threads
+// that waited for each read took 30 us for 8 tokens' 394 parts, 32 rows to a CTA 22 us
+// for 300 tokens' 1000.)  The first CTA also tells the status, from what the loss
+// kernel's CTAs left.
+constexpr int kJoinRows = 8, kJoinLanes = 128;
+
 __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int nparts,
                                                        const float* target_logit,
                                                        const long long* targets, int tokens,
                                                        int vocab, float* loss, float* lse,
                                                        const uint32_t* failed, int nctas,
                                                        uint32_t* status) {
-    __shared__ float2 sh[32][32];
+    __shared__ float2 sh[kJoinLanes][kJoinRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane;
+    const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
+    const int row = blockIdx.x * kJoinRows + r;
     // launched beside the loss kernel's end: wait for all it wrote
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0) {
@@ -818,33 +845,36 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
         m = n;
     };
     if (row < tokens) {
-        for (int i = warp; i < nparts; i += 256) {
+        for (int i = q; i < nparts; i += 8 * kJoinLanes) {
             float2 p[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                p[k] = i + 32 * k < nparts ? parts[(size_t)(i + 32 * k) * tokens + row]
-                                           : make_float2(-INFINITY, 0.0f);
+                p[k] = i + kJoinLanes * k < nparts
+                           ? parts[(size_t)(i + kJoinLanes * k) * tokens + row]
+                           : make_float2(-INFINITY, 0.0f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) join(p[k]);
         }
     }
-    sh[warp][lane] = make_float2(m, s);
+    sh[q][r] = make_float2(m, s);
     __syncthreads();
-    // warp w joins the 32 parts of row w of the CTA's rows
-    {
-        const float2 p = sh[lane][warp];
-        float mx = p.x;
+    if (warp < kJoinRows) {
+        m = -INFINITY;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kJoinLanes / 32; ++k) join(sh[lane + 32 * k][warp]);
+        float mx = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        float t = p.y * ex2_approx(p.x - (mx == -INFINITY ? 0.0f : mx));
+        float t = s * ex2_approx(m - (mx == -INFINITY ? 0.0f : mx));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const int r = blockIdx.x * 32 + warp;
-        if (lane == 0 && r < tokens) {
+        const int w = blockIdx.x * kJoinRows + warp;
+        if (lane == 0 && w < tokens) {
             const float l = fmaf(mx, 0.6931471805599453f, logf(t));
-            lse[r] = l;
-            const long long at = targets[r];
-            loss[r] = at < 0 ? 0.0f : at < vocab ? l - target_logit[r] : NAN;
+            lse[w] = l;
+            const long long at = targets[w];
+            loss[w] = at < 0 ? 0.0f : at < vocab ? l - target_logit[w] : NAN;
         }
     }
 }
@@ -918,8 +948,9 @@ Plan plan_grad(int tokens, int dim, int vocab) {
     // dh's tiles are as deep as the piece is wide: split them until they fit
     // under an even share of the launch's work
     const long long nt = tiles(dim), dh = tiles(tokens) * nt, dw = tiles(p.piece) * nt;
-    const long long dh_depth = p.piece / kDepth, dw_depth = (tokens + kDepth - 1) / kDepth;
-    const long long share = (dh * dh_depth + dw * dw_depth + kPairs - 1) / kPairs;
+    const long long dh_depth = p.piece / kDepth;
+    const long long dw_cost = std::max((tokens + kDepth - 1) / kDepth, kEpilogue);
+    const long long share = (dh * dh_depth + dw * dw_cost + kPairs - 1) / kPairs;
     p.splits = 1;
     while (p.splits < 32 &&
            (dh * p.splits + kPairs - 1) / kPairs * ((dh_depth + p.splits - 1) / p.splits) >
@@ -950,15 +981,50 @@ bool launch(const CUtensorMap& h, const CUtensorMap& W, const CUtensorMap& P,
 // the vocabulary of one CTA of the few-token kernel, whole boxes of 16 rows
 int few_share(int vocab) { return ((vocab + grid_ctas() - 1) / grid_ctas() + 15) / 16 * 16; }
 
-template <int N>
-bool launch_few(const CUtensorMap& h, const CUtensorMap* W, const CeArgs& a, cudaStream_t s) {
-    auto kernel = ce_few_kernel<N>;
+template <int N, bool PROB>
+bool launch_few_as(const CUtensorMap& h, const CUtensorMap* W, const CeArgs& a, cudaStream_t s) {
+    auto kernel = ce_few_kernel<N, PROB>;
     constexpr int smem = few_stages<N>() * few_stage<N>() + 1024;
     static std::atomic<int> cache[ssm_host::kMaxDevices];
     if (ssm_host::resident_ctas(reinterpret_cast<const void*>(kernel), kFewThreads, smem, cache) < 1)
         return false;
     kernel<<<grid_ctas(), kFewThreads, smem, s>>>(h, W[0], W[1], W[2], a, few_share(a.vocab));
     return cudaGetLastError() == cudaSuccess;
+}
+
+// columns of the few-token kernel
+int few_cols(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
+
+// W: its maps of 128, 64 and 16 rows
+template <bool PROB>
+bool launch_few(const CUtensorMap& h, const CUtensorMap* W, const CeArgs& a, cudaStream_t s) {
+    const int cols = few_cols(a.tokens);
+    return cols == 16   ? launch_few_as<16, PROB>(h, W, a, s)
+           : cols == 32 ? launch_few_as<32, PROB>(h, W, a, s)
+                        : launch_few_as<64, PROB>(h, W, a, s);
+}
+
+bool few_maps(CUtensorMap* mh, CUtensorMap* mw, const void* h, const void* W, int tokens, int dim,
+              int vocab) {
+    using ssm_host::make_tmap_2d;
+    return make_tmap_2d(mh, h, SSM_BF16, tokens, dim, few_cols(tokens), 64) &&
+           make_tmap_2d(&mw[0], W, SSM_BF16, vocab, dim, kHalf, 64) &&
+           make_tmap_2d(&mw[1], W, SSM_BF16, vocab, dim, 64, 64) &&
+           make_tmap_2d(&mw[2], W, SSM_BF16, vocab, dim, 16, 64);
+}
+
+// P, (tokens, width) with rows ld apart: past its width it reads as 0, whatever the
+// rows hold there
+bool make_p_map(CUtensorMap* map, const CeArgs& a, int box_rows) {
+    auto fn = ssm_host::encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.width, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.P, dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 // dh's fp32 sums, (splits, tokens, dim): clipped at each split's tokens
@@ -1023,12 +1089,10 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
             if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SSM_ERR_ALIAS;
 
     const bool few = tokens <= kFewTokens;
-    const int cols = tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;  // of the few-token kernel
     CUtensorMap mh, mw[3];
-    if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, few ? cols : kHalf, 64) ||
-        !make_tmap_2d(&mw[0], W, SSM_BF16, vocab, dim, kHalf, 64) ||
-        (few && (!make_tmap_2d(&mw[1], W, SSM_BF16, vocab, dim, 64, 64) ||
-                 !make_tmap_2d(&mw[2], W, SSM_BF16, vocab, dim, 16, 64))))
+    if (few ? !few_maps(&mh, mw, h, W, tokens, dim, vocab)
+            : !make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, kHalf, 64) ||
+                  !make_tmap_2d(&mw[0], W, SSM_BF16, vocab, dim, kHalf, 64))
         return SSM_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1037,14 +1101,12 @@ extern "C" ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const lon
     a.failed = reinterpret_cast<uint32_t*>(ws + 256);
     a.target_logit = reinterpret_cast<float*>(ws + 256 + kMaxCtas * 4);
     a.parts = reinterpret_cast<float2*>(ws + 256 + kMaxCtas * 4 + round256((size_t)tokens * 4));
-    const bool ok = !few      ? launch<kLoss>(mh, mw[0], mh, mh, mh, a, s)
-                    : cols == 16 ? launch_few<16>(mh, mw, a, s)
-                    : cols == 32 ? launch_few<32>(mh, mw, a, s)
-                                 : launch_few<64>(mh, mw, a, s);
+    const bool ok = few ? launch_few<false>(mh, mw, a, s)
+                        : launch<kLoss>(mh, mw[0], mh, mh, mh, a, s);
     if (!ok) return SSM_ERR_CUDA;
     // launched as the loss kernel's CTAs end, which saves the gap between the two
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((tokens + 31) / 32);
+    cfg.gridDim = dim3((tokens + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -1101,16 +1163,18 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
     a.P = reinterpret_cast<__nv_bfloat16*>(ws + 256);
     a.ld = plan.piece;
     a.dh_parts = reinterpret_cast<float*>(ws + 256 + round256((size_t)tokens * plan.piece * 2));
-    CUtensorMap mh, mw, mp, mh2, mw2, mdh, mdw, mpo;
+    // products of the gradient: boxes of 64 x 64; of the logits: as the forward; what
+    // the epilogues write: boxes of 32 rows by 128 bytes
+    const bool few = tokens <= kFewTokens && plan.piece >= vocab;
+    CUtensorMap mh, mw, mp, mdh, mdw, mpo, lh, lw[3];
     if (!make_tmap_2d(&mh, h, SSM_BF16, tokens, dim, 64, 64) ||
         !make_tmap_2d(&mw, W, SSM_BF16, vocab, dim, 64, 64) ||
-        !make_tmap_2d(&mp, a.P, SSM_BF16, tokens, plan.piece, 64, 64) ||
-        !make_tmap_2d(&mh2, h, SSM_BF16, tokens, dim, kHalf, 64) ||
-        !make_tmap_2d(&mw2, W, SSM_BF16, vocab, dim, kHalf, 64) ||
-        // what the epilogues write: boxes of 32 rows by 128 bytes
-        !make_tmap_2d(&mpo, a.P, SSM_BF16, tokens, plan.piece, 32, 64) ||
         !make_tmap_2d(&mdw, dW, grad_dtype, vocab, dim, 32, 128 / (int)ge) ||
         !make_parts_map(&mdh, a.dh_parts, dim, tokens, plan.splits))
+        return SSM_ERR_CUDA;
+    if (few ? !few_maps(&lh, lw, h, W, tokens, dim, vocab)
+            : !make_tmap_2d(&lh, h, SSM_BF16, tokens, dim, kHalf, 64) ||
+                  !make_tmap_2d(&lw[0], W, SSM_BF16, vocab, dim, kHalf, 64))
         return SSM_ERR_CUDA;
     CeHeader* head = reinterpret_cast<CeHeader*>(ws);
     a.scale = &head->scale;
@@ -1126,7 +1190,9 @@ extern "C" ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const lon
         a.first_piece = v0 == 0;
         const int depth = (a.width + kDepth - 1) / kDepth;
         a.splits = (depth + a.split_depth - 1) / a.split_depth;
-        if (!launch<kProb>(mh2, mw2, mp, mdh, mpo, a, s) ||
+        if (!make_p_map(&mp, a, 64) || !make_p_map(&mpo, a, 32) ||
+            !(few ? launch_few<true>(lh, lw, a, s)
+                  : launch<kProb>(lh, lw[0], mp, mdh, mpo, a, s)) ||
             !launch<kGrad>(mh, mw, mp, mdh, mdw, a, s))
             return SSM_ERR_CUDA;
     }
