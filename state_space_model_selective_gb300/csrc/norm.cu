@@ -10,14 +10,22 @@
 // Bound by memory: about ten FP32 operations per element against 6 to 20
 // bytes, so the row is read once into registers, reduced, and written once.
 //
-// Layout of the work: a warp owns blocks of 256 consecutive elements of a row
-// (block k of warp w starts at 256 (w + k warps)), so that a quantisation group
-// of up to 256 elements never leaves a warp.  Where rows are 16-byte aligned
-// (dim a multiple of 8) a lane holds 8 consecutive elements, moved with 16-byte
-// accesses; else lane l holds elements l, 32 + l, ... of the block, so that the
-// element-wise accesses of a warp are contiguous.  Rows of up to 256 elements
-// take one warp each, several to a CTA; longer rows take one CTA of up to
-// 32 warps of one block or 16 of four.
+// Layout of the work: a lane holds 8 neighbouring elements, a warp 32 such chunks, so
+// that a quantisation group of up to 256 elements never leaves a warp.  Rows of up
+// to 64 (128) elements take 8 (16) lanes each, rows of up to 256 one warp, longer rows
+// one CTA of up to 32 warps with one chunk a lane or 17 with four.  CTAs (with one
+// warp or less to a row: their warps) walk rows, the next row's loads in flight while
+// this one is reduced and written: one row to a CTA, and CTAs that come and go, left
+// the memory idle during each CTA's reductions (461 us against 394 us for forward and
+// gradient of 16384 rows of 5120, bf16 with an fp32 residual).
+//
+// Widths that are no multiple of 8: chunks are cut at multiples of 8 of the tensor's
+// flat index, where every type is 16-byte aligned, so that a row's first and last
+// chunk may be shared with its neighbours; only those are written element by element.
+// A row's shift against the chunks is row * dim mod 8, and CTAs step by multiples of 8
+// rows, so a lane's columns, and with them its weights and its sum of dw, stay the
+// same.  (Element-wise accesses took 34.8 us for 10000 rows of 1001, bf16 with 8-bit
+// output, against 23 us.)
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -28,11 +36,12 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kBlock = 256;      // elements of a row one warp owns at a time
-constexpr int kMaxDim = 16384;   // 16 warps of 4 blocks
+constexpr int kMaxDim = 16384;
 constexpr float kE4m3Max = 448.0f;
-constexpr int kBwdThreads = 640;
 constexpr int kFwdThreads = 1024;  // of the forward on an SM at a time
+constexpr int kBwdThreads = 640;   // of the gradient, bound by registers
+constexpr int kMaxGroups = kMaxDim / 32;
+constexpr int kSmallWarps = 8;     // of a CTA whose warps take rows by themselves
 
 struct NormArgs {
     const void* x;         // forward: x; gradient: the kept sum
@@ -46,42 +55,103 @@ struct NormArgs {
     float eps, inv_dim;
     long long rows;
     int dim;
-    int warps_per_row, rows_per_cta;
+    int warps_per_row;     // 1: a warp takes 32 / lanes rows at a time
+    int lanes;             // of a row's first warp: 8, 16 or 32
+    int rows_per_cta;
     int group, ngroups;    // 8-bit only; group 0 = the whole row
 };
 
-// The 8 elements a lane holds of block `blk` of a row, as they come from memory:
-// loaded a row ahead of their use.  Elements past `dim` read as 0.
-template <typename T, bool VEC>
-struct Raw {
-    static constexpr int kWords = VEC ? (int)sizeof(T) / 2 : 8;
-    using Word = std::conditional_t<VEC, uint4, float>;
-    Word w[kWords];
+// ------------------------------------------------------------------ chunks
 
-    __device__ void load(const T* p, int blk, int lane, int dim) {
-        if constexpr (VEC) {
-            const int i = blk * kBlock + lane * 8;
+// A lane's 8 elements of a row, i0 .. i0 + 7; those outside 0 .. dim - 1 are a
+// neighbouring row's.
+struct Chunk {
+    int i0;
+    bool any, full;
+};
+
+template <bool ALIGNED>
+__device__ __forceinline__ Chunk chunk_at(int c, int shift, int dim, bool valid) {
+    Chunk k;
+    k.i0 = 8 * c - (ALIGNED ? 0 : shift);
+    k.any = valid && k.i0 < dim;
+    k.full = k.any && (ALIGNED || (k.i0 >= 0 && k.i0 + 8 <= dim));
+    return k;
+}
+
+// 16 bytes read once, or zeros.  Volatile, so that the compiler leaves the next row's
+// loads before this row's barrier instead of moving them to where they save registers
+// (a few percent of forward and
+// gradient of 16384 rows of 5120).
+__device__ __forceinline__ uint4 load16(const void* p, bool in) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)in)
+        : "memory");
+    return v;
+}
+
+// The 8 elements as they come from memory: loaded a row ahead of their use.
+template <typename T, bool ALIGNED>
+struct Raw {
+    static constexpr int kWords = (int)sizeof(T) / 2;
+    uint4 w[kWords];
+
+    // `at`: the chunk's first element in the tensor of `total` elements, a multiple of 8
+    __device__ void load(const void* base, long long at, long long total, bool any) {
+        const T* p = static_cast<const T*>(base) + at;
+        const bool whole = any && (ALIGNED || at + 8 <= total);
 #pragma unroll
-            for (int j = 0; j < kWords; ++j)
-                w[j] = i < dim ? __ldcs(reinterpret_cast<const uint4*>(p + i) + j)
-                               : make_uint4(0, 0, 0, 0);
-        } else {
+        for (int j = 0; j < kWords; ++j)
+            w[j] = load16(reinterpret_cast<const uint4*>(p) + j, whole);
+        if (!ALIGNED && any && !whole) {  // the tensor's last elements
+            uint32_t u[4 * kWords] = {};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int i = blk * kBlock + j * 32 + lane;
-                w[j] = i < dim ? to_f32(p[i]) : 0.0f;
+                if (at + j >= total) continue;
+                if constexpr (sizeof(T) == 2)
+                    u[j >> 1] |= (uint32_t)__bfloat16_as_ushort(p[j]) << (16 * (j & 1));
+                else
+                    u[j] = __float_as_uint(p[j]);
             }
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+                w[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
         }
     }
     __device__ float get(int j) const {  // j a constant
-        if constexpr (!VEC) return w[j];
-        else if constexpr (sizeof(T) == 2) {
+        if constexpr (sizeof(T) == 2) {
             const uint32_t u = (j >> 1) == 0 ? w[0].x : (j >> 1) == 1 ? w[0].y
                              : (j >> 1) == 2 ? w[0].z : w[0].w;
             return j & 1 ? bf16hi(u) : bf16lo(u);
         } else {
             const uint4& q = w[j >> 2];
             return __uint_as_float((j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w);
+        }
+    }
+    // zeros in the places of the neighbouring rows
+    __device__ void mask(const Chunk& k, int dim) {
+        if constexpr (!ALIGNED) {
+            if (k.any && !k.full) {
+                uint32_t u[4 * kWords] = {w[0].x, w[0].y, w[0].z, w[0].w};
+                if constexpr (kWords == 2) {
+                    u[4] = w[1].x; u[5] = w[1].y; u[6] = w[1].z; u[7] = w[1].w;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (k.i0 + j >= 0 && k.i0 + j < dim) continue;
+                    if constexpr (sizeof(T) == 2) u[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+                    else u[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < kWords; ++j)
+                    w[j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+            }
         }
     }
 };
@@ -91,46 +161,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* p, int blk, int lane, int dim, const float* v) {
-    if constexpr (VEC) {
-        const int i = blk * kBlock + lane * 8;
-        if (i >= dim) return;
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store8(void* base, long long at, const Chunk& k, int dim,
+                                       const float* v) {
+    T* p = static_cast<T*>(base) + at;
+    if (k.full) {
         if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(p + i) =
+            *reinterpret_cast<uint4*>(p) =
                 make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                            pack_bf16(v[6], v[7]));
         } else {
-            *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
         }
-    } else {
+    } else if (!ALIGNED && k.any) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = blk * kBlock + j * 32 + lane;
-            if (i < dim) p[i] = from_f32<T>(v[j]);
-        }
+        for (int j = 0; j < 8; ++j)
+            if (k.i0 + j >= 0 && k.i0 + j < dim) p[j] = from_f32<T>(v[j]);
     }
 }
 
-// weight, read by every row: cached
-template <bool VEC>
-__device__ __forceinline__ void load_weight(const float* p, int blk, int lane, int dim, float* v) {
-    if constexpr (VEC) {
-        const int i = blk * kBlock + lane * 8;
+template <bool ALIGNED>
+__device__ __forceinline__ void load_weight(const float* p, const Chunk& k, int dim, float* v) {
+    if (ALIGNED) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (i < dim) {
-            a = __ldg(reinterpret_cast<const float4*>(p + i));
-            b = __ldg(reinterpret_cast<const float4*>(p + i + 4));
+        if (k.any) {
+            a = __ldg(reinterpret_cast<const float4*>(p + k.i0));
+            b = __ldg(reinterpret_cast<const float4*>(p + k.i0 + 4));
         }
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = blk * kBlock + j * 32 + lane;
-            v[j] = i < dim ? __ldg(p + i) : 0.0f;
-        }
+        for (int j = 0; j < 8; ++j)
+            v[j] = k.any && k.i0 + j >= 0 && k.i0 + j < dim ? __ldg(p + k.i0 + j) : 0.0f;
     }
 }
 
@@ -147,13 +211,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// over the `width` consecutive lanes (a power of two) this lane is among
+__device__ __forceinline__ float lanes_sum(float v, int width) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < 32; o <<= 1)
+        if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// max over the `width` consecutive lanes (a power of two) this lane is among
 __device__ __forceinline__ float lanes_max(float v, int width) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -173,240 +238,340 @@ __device__ __forceinline__ float quant_scale(float amax) { return amax * (1.0f /
 
 enum Out { kPlain, kE4m3 };
 
-// The 8-bit output of a row: v is its y.
-template <int NV, bool VEC>
-__device__ __forceinline__ void quantise(const NormArgs& a, long long row, float (*v)[8], int wr,
-                                         int lane, int warp, float* red) {
-    uint8_t* q = static_cast<uint8_t*>(a.y) + (size_t)row * a.dim;
-    float* scales = a.scales + (size_t)row * a.ngroups;
-    float row_amax = 0.0f;
+// The 8-bit output of a row: v is its y (0 in the neighbouring rows' places).
+template <int NV, bool ALIGNED, bool SMALL>
+__device__ __forceinline__ void quantise(const NormArgs& a, long long row, float (*v)[8],
+                                         const Chunk* ks, int lane, int warp, int wr, float* red,
+                                         uint32_t* s_amax) {
+    const long long base = row * a.dim;
+    uint8_t* q = static_cast<uint8_t*>(a.y);
+    constexpr bool small = SMALL;
+    const int lanes = SMALL ? a.lanes : 32;
+    float factor[NV][2];  // of the chunk's group, and of the next one's where it spans two
+    int cut[NV];          // first element of that
     if (a.group == 0) {
+        float amax = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) row_amax = max_nan(row_amax, fabsf(v[k][j]));
-        row_amax = lanes_max(row_amax, 32);
-        if (a.warps_per_row > 1) {
-            if (lane == 0) red[warp] = row_amax;
+            for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[k][j]));
+        amax = lanes_max(amax, lanes);
+        if (!small) {
+            if (lane == 0) red[warp] = amax;
             __syncthreads();
-            row_amax = lanes_max(lane < a.warps_per_row ? red[lane] : 0.0f, 32);
+            amax = lanes_max(lane < a.warps_per_row ? red[lane] : 0.0f, 32);
         }
-        if (wr == 0 && lane == 0) scales[0] = quant_scale(row_amax);
+        if (wr == 0 && (lane & (lanes - 1)) == 0 && row < a.rows) a.scales[row] = quant_scale(amax);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            factor[k][0] = quant_factor(amax);
+            cut[k] = 8;
+        }
+    } else if constexpr (ALIGNED) {
+        const int width = min(a.group >> 3, lanes);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[k][j]));
+            amax = lanes_max(amax, width);
+            if ((lane & (width - 1)) == 0 && ks[k].any)
+                a.scales[row * a.ngroups + ks[k].i0 / a.group] = quant_scale(amax);
+            factor[k][0] = quant_factor(amax);
+            cut[k] = 8;
+        }
+    } else {
+        // groups are cut in the row, chunks in the tensor: the maxima meet in shared
+        // memory (magnitudes are ordered as their bits are, NaN above all)
+        const int sub = small ? (threadIdx.x / lanes) * 8 : 0;
+        const int me = small ? lane & (lanes - 1) : (int)threadIdx.x;
+        const int all = small ? lanes : (int)blockDim.x;
+        auto sync = [&] {
+            if (small) __syncwarp();
+            else __syncthreads();
+        };
+        for (int g = me; g < a.ngroups; g += all) s_amax[sub + g] = 0;
+        sync();
+        int first[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            first[k] = max(ks[k].i0, 0) / a.group;
+            cut[k] = min(8, (first[k] + 1) * a.group - ks[k].i0);
+            if (ks[k].any) {
+                float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j < cut[k]) m0 = max_nan(m0, fabsf(v[k][j]));
+                    else m1 = max_nan(m1, fabsf(v[k][j]));
+                }
+                atomicMax(&s_amax[sub + first[k]], __float_as_uint(m0));
+                if (cut[k] < 8 && first[k] + 1 < a.ngroups)
+                    atomicMax(&s_amax[sub + first[k] + 1], __float_as_uint(m1));
+            }
+        }
+        sync();
+        if (row < a.rows)
+            for (int g = me; g < a.ngroups; g += all)
+                a.scales[row * a.ngroups + g] = quant_scale(__uint_as_float(s_amax[sub + g]));
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            factor[k][0] = factor[k][1] = 0.0f;
+            if (ks[k].any) {
+                factor[k][0] = quant_factor(__uint_as_float(s_amax[sub + first[k]]));
+                if (cut[k] < 8 && first[k] + 1 < a.ngroups)
+                    factor[k][1] = quant_factor(__uint_as_float(s_amax[sub + first[k] + 1]));
+            }
+        }
+        sync();  // before the next row's zeros
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int blk = wr + k * a.warps_per_row;
-        float amax[8];  // VEC: one group per lane, in amax[0]
-        if (a.group == 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax[j] = row_amax;
-        } else if constexpr (VEC) {
-            float m = 0.0f;
+        for (int j = 0; j < 8; ++j)
+            v[k][j] *= ALIGNED || j < cut[k] ? factor[k][0] : factor[k][1];
+        const uint2 w = make_uint2(e4m3x2(v[k][0], v[k][1]) | e4m3x2(v[k][2], v[k][3]) << 16,
+                                   e4m3x2(v[k][4], v[k][5]) | e4m3x2(v[k][6], v[k][7]) << 16);
+        uint8_t* p = q + base + ks[k].i0;
+        if (ks[k].full) {
+            *reinterpret_cast<uint2*>(p) = w;
+        } else if (!ALIGNED && ks[k].any) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[k][j]));
-            const int width = a.group >> 3;
-            amax[0] = lanes_max(m, width);
-            const int i = blk * kBlock + lane * 8;
-            if ((lane & (width - 1)) == 0 && i < a.dim)
-                scales[i / a.group] = quant_scale(amax[0]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax[j] = lanes_max(fabsf(v[k][j]), 32);
-            // a group is group / 32 consecutive rows of 32 lanes
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                if (o * 32 < a.group) {
-                    float t[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) t[j] = max_nan(amax[j], amax[j ^ o]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) amax[j] = t[j];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = blk * kBlock + j * 32;
-                if (lane == 0 && i % a.group == 0 && i < a.dim)
-                    scales[i / a.group] = quant_scale(amax[j]);
-            }
-        }
-        if constexpr (VEC) {
-            const float f = quant_factor(amax[0]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] *= f;
-            const int i = blk * kBlock + lane * 8;
-            if (i < a.dim)
-                *reinterpret_cast<uint2*>(q + i) =
-                    make_uint2(e4m3x2(v[k][0], v[k][1]) | e4m3x2(v[k][2], v[k][3]) << 16,
-                               e4m3x2(v[k][4], v[k][5]) | e4m3x2(v[k][6], v[k][7]) << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = blk * kBlock + j * 32 + lane;
-                if (i < a.dim)
-                    q[i] = (uint8_t)e4m3x2(v[k][j] * quant_factor(amax[j]), 0.0f);
-            }
+            for (int j = 0; j < 8; ++j)
+                if (ks[k].i0 + j >= 0 && ks[k].i0 + j < a.dim)
+                    p[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
         }
     }
 }
 
 // ------------------------------------------------------------- forward
 
-// A CTA (with one warp to a row: each warp) walks rows, the next row's loads in
-// flight while this one is reduced and written: one row to a CTA, and CTAs that
-// come and go, left the memory idle during each CTA's reductions (4.7 TB/s at
-// 16384 rows of 2048 with an 8-bit output, against @Q8@ TB/s).
-template <typename TX, typename TR, typename TY, int NV, bool VEC, Out OUT>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_fwd_kernel(const NormArgs a) {
+// SMALL: a row takes one warp or less.
+template <typename TX, typename TR, typename TY, int NV, bool ALIGNED, bool SMALL, Out OUT>
+__global__ void __launch_bounds__(SMALL ? 256 : !ALIGNED ? 544 : NV == 1 ? 1024 : 512)
+    norm_fwd_kernel(const NormArgs a) {
     __shared__ float red[2][2][32];
+    __shared__ uint32_t s_amax[OUT == kE4m3 && !ALIGNED ? kMaxGroups : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wr = warp % a.warps_per_row;  // the warp within its row
+    constexpr bool small = SMALL;
+    const int lanes = SMALL ? a.lanes : 32;
+    const int wr = small ? 0 : warp;  // the warp within its row
+    const int c = small ? lane & (lanes - 1) : warp * 32 + lane;
     const bool has_res = a.residual != nullptr;
-    long long row = (long long)blockIdx.x * a.rows_per_cta + warp / a.warps_per_row;
-    const long long step = (long long)gridDim.x * a.rows_per_cta;
+    const long long total = a.rows * a.dim, step = (long long)gridDim.x * a.rows_per_cta;
+    // the warp's first row, and this lane's
+    long long first = (long long)blockIdx.x * a.rows_per_cta + (small ? warp * (32 / lanes) : 0);
+    const int sub = small ? lane / lanes : 0;
+    const int shift = (int)((first + sub) * a.dim & 7);
 
-    Raw<TX, VEC> x[NV];
-    Raw<TR, VEC> res[NV];
-    auto load = [&](long long r) {
-        const size_t base = (size_t)r * a.dim;
+    Chunk ks[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        ks[k] = chunk_at<ALIGNED>(c + k * 32 * a.warps_per_row, shift, a.dim, true);
+    Raw<TX, ALIGNED> x[NV];
+    Raw<TR, ALIGNED> res[NV];
+    auto load = [&](long long row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
-            x[k].load(static_cast<const TX*>(a.x) + base, blk, lane, a.dim);
-            if (has_res) res[k].load(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim);
+            const long long at = row * a.dim + ks[k].i0;
+            const bool any = ks[k].any && (!SMALL || row < a.rows);
+            x[k].load(a.x, at, total, any);
+            if (has_res) res[k].load(a.residual, at, total, any);
         }
     };
-    if (row < a.rows) load(row);
-    float w1[8];  // the weight, kept where a lane has one block of it
-    if constexpr (NV == 1) load_weight<VEC>(a.weight, wr, lane, a.dim, w1);
-    // `row` is the same in a CTA, or the warps do not meet
-    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-        const size_t base = (size_t)row * a.dim;
+    if (first < a.rows) load(first + sub);
+    float w1[8];  // the weight, kept where a lane has one chunk
+    if constexpr (NV == 1) load_weight<ALIGNED>(a.weight, ks[0], a.dim, w1);
+    // `first` is the same in a CTA, or its warps do not meet
+    for (int turn = 0; first < a.rows; first += step, turn ^= 1) {
+        const long long row = first + sub;
+        Chunk now[NV];
         float v[NV][8];
         float ss = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+            now[k] = ks[k];
+            if constexpr (SMALL) {  // the warp's other rows may be past the last one
+                now[k].any = ks[k].any && row < a.rows;
+                now[k].full = ks[k].full && row < a.rows;
+            }
+            x[k].mask(now[k], a.dim);
+            if (has_res) res[k].mask(now[k], a.dim);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[k][j] = x[k].get(j);
                 if (has_res) v[k][j] += res[k].get(j);
             }
-        if (row + step < a.rows) load(row + step);
+        }
+        if (first + step < a.rows) load(row + step);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
-            if (a.sum) store8<VEC>(static_cast<TR*>(a.sum) + base, blk, lane, a.dim, v[k]);
+            if (a.sum) store8<TR, ALIGNED>(a.sum, row * a.dim + now[k].i0, now[k], a.dim, v[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
         }
-        ss = warp_sum(ss);
-        if (a.warps_per_row > 1) {
+        ss = lanes_sum(ss, lanes);
+        if (!small) {
             // two buffers: a warp may write the next row's sums while another still
             // reads this row's
             if (lane == 0) red[0][turn][warp] = ss;
             __syncthreads();
-            ss = warp_sum(lane < a.warps_per_row ? red[0][turn][lane] : 0.0f);
+            ss = lanes_sum(lane < a.warps_per_row ? red[0][turn][lane] : 0.0f, 32);
         }
         const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
 
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int blk = wr + k * a.warps_per_row;
             float w[8];
-            if constexpr (NV > 1) load_weight<VEC>(a.weight, blk, lane, a.dim, w);
+            if constexpr (NV > 1) load_weight<ALIGNED>(a.weight, ks[k], a.dim, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * (NV > 1 ? w[j] : w1[j]);
             if constexpr (OUT == kPlain)
-                store8<VEC>(static_cast<TY*>(a.y) + base, blk, lane, a.dim, v[k]);
+                store8<TY, ALIGNED>(a.y, row * a.dim + now[k].i0, now[k], a.dim, v[k]);
         }
-        if constexpr (OUT == kE4m3) quantise<NV, VEC>(a, row, v, wr, lane, warp, red[1][turn]);
+        if constexpr (OUT == kE4m3)
+            quantise<NV, ALIGNED, SMALL>(a, row, v, now, lane, warp, wr, red[1][turn], s_amax);
     }
 }
 
 // ------------------------------------------------------------ gradient
 
-// CTAs walk rows as the forward's do, each thread keeping the weight's gradient of
-// its columns in registers; norm_dw_kernel adds the CTAs' sums in order.  AHEAD:
-// the next row's loads are in flight while this one is reduced (three inputs of
-// two blocks a warp are as much as the registers hold).
-template <typename TX, typename TR, typename TY, int NV, bool VEC, bool AHEAD>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
-    __shared__ float2 red[2][16];
+// CTAs walk rows as the forward's do, each lane keeping the weight's gradient of its
+// columns in registers; norm_dw_kernel adds the CTAs' sums in order.  AHEAD: the next
+// row's loads are in flight while this one is reduced (three inputs of two chunks a
+// lane are as much as the registers hold).
+template <typename TX, typename TR, typename TY, int NV, bool ALIGNED, bool SMALL, bool AHEAD>
+__global__ void __launch_bounds__(SMALL ? 256 : ALIGNED ? 512 : 544)
+    norm_bwd_kernel(const NormArgs a) {
+    __shared__ float2 red[2][32];
+    __shared__ float s_dw[SMALL ? 256 : 1];  // of a CTA whose warps take rows by themselves
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr bool small = SMALL;
+    const int lanes = SMALL ? a.lanes : 32;
+    const int c = small ? lane & (lanes - 1) : warp * 32 + lane;
     const bool has_add = a.residual != nullptr;
+    const long long total = a.rows * a.dim, step = (long long)gridDim.x * a.rows_per_cta;
+    long long first = (long long)blockIdx.x * a.rows_per_cta + (small ? warp * (32 / lanes) : 0);
+    const int sub = small ? lane / lanes : 0;
+    const int shift = (int)((first + sub) * a.dim & 7);
+    Chunk ks[NV];
     float dw[NV][8];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        ks[k] = chunk_at<ALIGNED>(c + k * 32 * a.warps_per_row, shift, a.dim, true);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
-    Raw<TR, VEC> rs[NV], radd[NV];
-    Raw<TY, VEC> rdy[NV];
-    auto load = [&](long long r) {
-        const size_t base = (size_t)r * a.dim;
+    }
+    float w1[8];  // the weight, kept where a lane has one chunk
+    if constexpr (NV == 1) load_weight<ALIGNED>(a.weight, ks[0], a.dim, w1);
+    struct In {
+        Raw<TR, ALIGNED> s[NV], add[NV];
+        Raw<TY, ALIGNED> dy[NV];
+    };
+    auto load = [&](In& in, long long row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int blk = warp + k * a.warps_per_row;
-            rs[k].load(static_cast<const TR*>(a.x) + base, blk, lane, a.dim);
-            rdy[k].load(static_cast<const TY*>(a.dy) + base, blk, lane, a.dim);
-            if (has_add) radd[k].load(static_cast<const TR*>(a.residual) + base, blk, lane, a.dim);
+            const long long at = row * a.dim + ks[k].i0;
+            const bool any = ks[k].any && (!SMALL || row < a.rows);
+            in.s[k].load(a.x, at, total, any);
+            in.dy[k].load(a.dy, at, total, any);
+            if (has_add) in.add[k].load(a.residual, at, total, any);
         }
     };
     int turn = 0;
-    if (AHEAD && blockIdx.x < a.rows) load(blockIdx.x);
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const size_t base = (size_t)row * a.dim;
-        if constexpr (!AHEAD) load(row);
-        Raw<TR, VEC> s[NV], add[NV];
-        Raw<TY, VEC> dy[NV];
+    // the row `first`, held in `in`; the next one's loads into `ahead`
+    auto row_of = [&](In& in, In& ahead) {
+        const long long row = first + sub;
+        Chunk now[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            s[k] = rs[k];
-            dy[k] = rdy[k];
-            if (has_add) add[k] = radd[k];
+            now[k] = ks[k];
+            if constexpr (SMALL) {
+                now[k].any = ks[k].any && row < a.rows;
+                now[k].full = ks[k].full && row < a.rows;
+            }
         }
-        if (AHEAD && row + gridDim.x < a.rows) load(row + gridDim.x);
+        if constexpr (!AHEAD) load(in, row);
+        else if (first + step < a.rows) load(ahead, row + step);
         float ss = 0.0f, sg = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float w[8];
-            load_weight<VEC>(a.weight, warp + k * a.warps_per_row, lane, a.dim, w);
+            in.s[k].mask(now[k], a.dim);
+            in.dy[k].mask(now[k], a.dim);
+            if constexpr (NV > 1) load_weight<ALIGNED>(a.weight, ks[k], a.dim, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = fmaf(s[k].get(j), s[k].get(j), ss);
-                sg = fmaf(s[k].get(j), dy[k].get(j) * w[j], sg);
+                const float sj = in.s[k].get(j);
+                ss = fmaf(sj, sj, ss);
+                sg = fmaf(sj, in.dy[k].get(j) * (NV > 1 ? w[j] : w1[j]), sg);
             }
         }
-        ss = warp_sum(ss);
-        sg = warp_sum(sg);
-        if (a.warps_per_row > 1) {
+        ss = lanes_sum(ss, lanes);
+        sg = lanes_sum(sg, lanes);
+        if (!small) {
             if (lane == 0) red[turn][warp] = make_float2(ss, sg);
             __syncthreads();
             const float2 t = lane < a.warps_per_row ? red[turn][lane] : make_float2(0.f, 0.f);
-            ss = warp_sum(t.x);
-            sg = warp_sum(t.y);
+            ss = lanes_sum(t.x, 32);
+            sg = lanes_sum(t.y, 32);
         }
         const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
-        const float c = sg * a.inv_dim * r * r;  // mean(g n) r, so that n mean(g n) = s c
+        const float c_ = sg * a.inv_dim * r * r;  // mean(g n) r, so that n mean(g n) = s c
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int blk = warp + k * a.warps_per_row;
+            const long long at = row * a.dim + now[k].i0;
             float w[8], d[8];
-            load_weight<VEC>(a.weight, blk, lane, a.dim, w);
+            if constexpr (NV > 1) load_weight<ALIGNED>(a.weight, ks[k], a.dim, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float sj = s[k].get(j), g = dy[k].get(j);
-                d[j] = r * fmaf(-sj, c, g * w[j]);
-                if (has_add) d[j] += add[k].get(j);
+                const float sj = in.s[k].get(j), g = in.dy[k].get(j);
+                d[j] = r * fmaf(-sj, c_, g * (NV > 1 ? w[j] : w1[j]));
+                if (has_add) d[j] += in.add[k].get(j);
                 dw[k][j] = fmaf(g, sj * r, dw[k][j]);
             }
-            if (a.y) store8<VEC>(static_cast<TX*>(a.y) + base, blk, lane, a.dim, d);
-            if (a.sum) store8<VEC>(static_cast<TR*>(a.sum) + base, blk, lane, a.dim, d);
+            if (a.y) store8<TX, ALIGNED>(a.y, at, now[k], a.dim, d);
+            if (a.sum) store8<TR, ALIGNED>(a.sum, at, now[k], a.dim, d);
+        }
+        first += step;
+        turn ^= 1;
+    };
+    // One chunk a lane: two sets of inputs in turn, so that none is copied.  With two
+    // chunks the two unrolled rows spill (419 us against 377 us for forward and
+    // gradient of 16384 rows of 5120).
+    In in0, in1;
+    if (AHEAD && first < a.rows) load(in0, first + sub);
+    while (first < a.rows) {
+        if constexpr (AHEAD && NV == 1) {
+            row_of(in0, in1);
+            if (first >= a.rows) break;
+            row_of(in1, in0);
+        } else {
+            in1 = in0;
+            row_of(in1, in0);
         }
     }
+    float* out = a.partial + (size_t)blockIdx.x * a.dim;
+    if constexpr (SMALL) {
+        // the rows' lane groups one after another, so that the order is fixed
+        for (int i = threadIdx.x; i < a.dim; i += blockDim.x) s_dw[i] = 0.0f;
+        for (int g = 0; g < a.rows_per_cta; ++g) {
+            __syncthreads();
+            if ((int)threadIdx.x / lanes == g && ks[0].any) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        store8<VEC>(a.partial + (size_t)blockIdx.x * a.dim, warp + k * a.warps_per_row, lane,
-                    a.dim, dw[k]);
+                for (int j = 0; j < 8; ++j)
+                    if (ks[0].i0 + j >= 0 && ks[0].i0 + j < a.dim) s_dw[ks[0].i0 + j] += dw[0][j];
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.dim; i += blockDim.x) out[i] = s_dw[i];
+    } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (ks[k].any && ks[k].i0 + j >= 0 && ks[k].i0 + j < a.dim)
+                    out[ks[k].i0 + j] = dw[k][j];
+    }
 }
 
 // dw[c] = sum of the CTAs' partial[i][c] in a fixed order: 8 warps take every
@@ -418,15 +583,14 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int 
     const int c = blockIdx.x * 32 + lane;
     float t = 0.0f;
     if (c < dim) {
-        int i = warp;
-        for (; i + 56 < parts; i += 64) {  // eight loads at a time
+        for (int i = warp; i < parts; i += 64) {  // eight loads at a time
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = partial[(size_t)(i + 8 * k) * dim + c];
+            for (int k = 0; k < 8; ++k)
+                v[k] = partial[(size_t)min(i + 8 * k, parts - 1) * dim + c];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t += v[k];
+            for (int k = 0; k < 8; ++k) t += i + 8 * k < parts ? v[k] : 0.0f;
         }
-        for (; i < parts; i += 8) t += partial[(size_t)i * dim + c];
     }
     acc[warp][lane] = t;
     __syncthreads();
@@ -438,10 +602,6 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int 
 }
 
 // -------------------------------------------------------------- launch
-
-// The most CTAs a gradient takes: their sums of dw are written and read once more.
-// (The workspace's size follows from it, so it does not depend on the device.)
-constexpr int kBwdCtas = 152 * 4;
 
 template <typename F>
 bool by_types(ssm_dtype_t x, ssm_dtype_t r, ssm_dtype_t y, F&& f) {
@@ -456,8 +616,41 @@ bool by_types(ssm_dtype_t x, ssm_dtype_t r, ssm_dtype_t y, F&& f) {
     return true;
 }
 
-// blocks of 256 elements -> warps of a row, with NV blocks to a warp
-int row_warps(int dim, int nv) { return ((dim + kBlock - 1) / kBlock + nv - 1) / nv; }
+// Chunks of a row: at a shift it reaches into one more.
+int row_chunks(int dim) { return (dim + 7) / 8 + (dim % 8 ? 1 : 0); }
+
+// Lanes and warps of a row with nv chunks to a lane.
+void row_plan(int dim, int nv, int* lanes, int* warps) {
+    const int n = row_chunks(dim);
+    *lanes = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+    *warps = (n + 32 * nv - 1) / (32 * nv);
+}
+
+// The gradient's chunks per lane, its CTA and the most CTAs: their sums of dw are
+// written and read once more.  (The workspace's size follows from it, so it does not
+// depend on the device: a GB300 has 152 SMs.)
+struct BwdPlan {
+    int nv, lanes, warps, rows_per_cta, threads, most;
+};
+
+BwdPlan bwd_plan(int dim) {
+    BwdPlan p;
+    const int n = row_chunks(dim);
+    p.nv = n <= 512 ? 1 : n <= 1024 ? 2 : 4;  // up to 16 (17) warps
+    row_plan(dim, p.nv, &p.lanes, &p.warps);
+    const bool small = p.warps == 1 && p.nv == 1;
+    p.rows_per_cta = small ? kSmallWarps * (32 / p.lanes) : 1;
+    p.threads = 32 * (small ? kSmallWarps : p.warps);
+    p.most = 152 * std::max(1, kBwdThreads / p.threads);
+    return p;
+}
+
+// CTAs step by multiples of 8 rows, so that a lane's columns stay the same
+unsigned whole_grid(long long rows, int rows_per_cta, long long most, bool aligned) {
+    long long g = std::min((rows + rows_per_cta - 1) / rows_per_cta, most);
+    if (!aligned) g = std::max<long long>(8, g / 8 * 8);
+    return (unsigned)g;
+}
 
 struct Span { const void* p; size_t n; };
 
@@ -507,35 +700,41 @@ static ssm_status_t norm_fwd(const void* x, const void* residual, const float* w
     a.x = x; a.residual = residual; a.weight = weight; a.y = y; a.sum = sum; a.scales = scales;
     a.eps = eps; a.inv_dim = 1.0f / (float)dim; a.rows = rows; a.dim = dim;
     a.group = group; a.ngroups = ngroups;
-    const int nv = dim <= 32 * kBlock ? 1 : 4, warps = row_warps(dim, nv);
-    a.warps_per_row = warps;
-    a.rows_per_cta = warps == 1 ? 4 : 1;
-    const int threads = 32 * warps * a.rows_per_cta;
-    // as many CTAs as are resident: @THREADS@ threads to an SM
-    const int resident = ssm_host::sm_count() * std::max(1, kFwdThreads / threads);
-    const unsigned grid = (unsigned)std::min<long long>(
-        ((long long)rows + a.rows_per_cta - 1) / a.rows_per_cta, resident);
-    if (grid == 0) return SSM_ERR_CUDA;
     const bool vec = dim % 8 == 0;
+    // one chunk a lane up to 32 warps, or the 17 that unaligned rows' registers allow
+    const int nv = row_chunks(dim) <= (vec ? 1024 : 544) ? 1 : 4;
+    int warps;
+    row_plan(dim, nv, &a.lanes, &warps);
+    a.warps_per_row = warps;
+    const bool small = warps == 1;
+    a.rows_per_cta = small ? kSmallWarps * (32 / a.lanes) : 1;
+    const int threads = 32 * (small ? kSmallWarps : warps);
+    const int sms = ssm_host::sm_count();
+    if (sms == 0) return SSM_ERR_CUDA;
+    const unsigned grid =
+        whole_grid(rows, a.rows_per_cta, (long long)sms * std::max(1, kFwdThreads / threads), vec);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     by_types(in, res, e4m3 ? SSM_F32 : out, [&](auto tx, auto tr, auto ty) {
         using TX = decltype(tx);
         using TR = decltype(tr);
         using TY = decltype(ty);
         auto go = [&](auto kernel) { kernel<<<grid, threads, 0, s>>>(a); };
+        auto pick = [&](auto out) {
+            constexpr Out O = decltype(out)::value;
+            if (small) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, true, O>)
+                           : go(norm_fwd_kernel<TX, TR, TY, 1, false, true, O>);
+            else if (nv == 1) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, false, O>)
+                                  : go(norm_fwd_kernel<TX, TR, TY, 1, false, false, O>);
+            else vec ? go(norm_fwd_kernel<TX, TR, TY, 4, true, false, O>)
+                     : go(norm_fwd_kernel<TX, TR, TY, 4, false, false, O>);
+        };
         if constexpr (sizeof(TY) == 4) {
             if (e4m3) {
-                if (nv == 1) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, kE4m3>)
-                                 : go(norm_fwd_kernel<TX, TR, TY, 1, false, kE4m3>);
-                else vec ? go(norm_fwd_kernel<TX, TR, TY, 4, true, kE4m3>)
-                         : go(norm_fwd_kernel<TX, TR, TY, 4, false, kE4m3>);
+                pick(std::integral_constant<Out, kE4m3>{});
                 return;
             }
         }
-        if (nv == 1) vec ? go(norm_fwd_kernel<TX, TR, TY, 1, true, kPlain>)
-                         : go(norm_fwd_kernel<TX, TR, TY, 1, false, kPlain>);
-        else vec ? go(norm_fwd_kernel<TX, TR, TY, 4, true, kPlain>)
-                 : go(norm_fwd_kernel<TX, TR, TY, 4, false, kPlain>);
+        pick(std::integral_constant<Out, kPlain>{});
     });
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
@@ -560,7 +759,8 @@ extern "C" ssm_status_t ssm_add_rmsnorm_e4m3_fwd(const void* x, const void* resi
 
 extern "C" size_t ssm_add_rmsnorm_bwd_workspace_bytes(int rows, int dim) {
     if (rows < 0 || dim < 1 || dim > kMaxDim) return 0;
-    return 256 + (size_t)std::min(rows, kBwdCtas) * dim * 4;
+    const BwdPlan p = bwd_plan(dim);
+    return 256 + (size_t)whole_grid(rows, p.rows_per_cta, p.most, dim % 8 == 0) * dim * 4;
 }
 
 extern "C" ssm_status_t ssm_add_rmsnorm_bwd(const void* sum, const float* weight, float eps,
@@ -600,25 +800,28 @@ extern "C" ssm_status_t ssm_add_rmsnorm_bwd(const void* sum, const float* weight
     a.x = sum; a.residual = dsum; a.weight = weight; a.dy = dy; a.y = dx; a.sum = dresidual;
     a.partial = static_cast<float*>(workspace);
     a.eps = eps; a.inv_dim = 1.0f / (float)dim; a.rows = rows; a.dim = dim;
-    const int nv = dim <= 16 * kBlock ? 1 : dim <= 32 * kBlock ? 2 : 4;
-    const int warps = row_warps(dim, nv);
-    a.warps_per_row = warps;
-    a.rows_per_cta = 1;
-    const unsigned grid = (unsigned)std::min(
-        rows, std::min(kBwdCtas, ssm_host::sm_count() * std::max(1, kBwdThreads / (32 * warps))));
-    if (grid == 0) return SSM_ERR_CUDA;
+    const BwdPlan p = bwd_plan(dim);
+    a.lanes = p.lanes;
+    a.warps_per_row = p.warps;
+    a.rows_per_cta = p.rows_per_cta;
     const bool vec = dim % 8 == 0;
+    const int sms = ssm_host::sm_count();
+    if (sms == 0) return SSM_ERR_CUDA;
+    const unsigned grid = whole_grid(
+        rows, p.rows_per_cta, std::min(p.most, sms * std::max(1, kBwdThreads / p.threads)), vec);
     by_types(in_dtype, res_dtype, dy_dtype, [&](auto tx, auto tr, auto ty) {
         using TX = decltype(tx);
         using TR = decltype(tr);
         using TY = decltype(ty);
-        auto go = [&](auto kernel) { kernel<<<grid, 32u * warps, 0, s>>>(a); };
-        if (nv == 1) vec ? go(norm_bwd_kernel<TX, TR, TY, 1, true, true>)
-                         : go(norm_bwd_kernel<TX, TR, TY, 1, false, true>);
-        else if (nv == 2) vec ? go(norm_bwd_kernel<TX, TR, TY, 2, true, true>)
-                              : go(norm_bwd_kernel<TX, TR, TY, 2, false, true>);
-        else vec ? go(norm_bwd_kernel<TX, TR, TY, 4, true, false>)
-                 : go(norm_bwd_kernel<TX, TR, TY, 4, false, false>);
+        auto go = [&](auto kernel) { kernel<<<grid, p.threads, 0, s>>>(a); };
+        if (p.rows_per_cta > 1) vec ? go(norm_bwd_kernel<TX, TR, TY, 1, true, true, true>)
+                                    : go(norm_bwd_kernel<TX, TR, TY, 1, false, true, true>);
+        else if (p.nv == 1) vec ? go(norm_bwd_kernel<TX, TR, TY, 1, true, false, true>)
+                                : go(norm_bwd_kernel<TX, TR, TY, 1, false, false, true>);
+        else if (p.nv == 2) vec ? go(norm_bwd_kernel<TX, TR, TY, 2, true, false, true>)
+                                : go(norm_bwd_kernel<TX, TR, TY, 2, false, false, true>);
+        else vec ? go(norm_bwd_kernel<TX, TR, TY, 4, true, false, false>)
+                 : go(norm_bwd_kernel<TX, TR, TY, 4, false, false, false>);
     });
     norm_dw_kernel<<<(dim + 31) / 32, 256, 0, s>>>(a.partial, (int)grid, dim, dweight);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
