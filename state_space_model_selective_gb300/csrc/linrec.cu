@@ -150,15 +150,10 @@ __device__ __forceinline__ float2 load_state2(const float* p, size_t i, bool bot
 
 // --------------------------------------------------------------- loading
 
-// BYTES per asynchronous copy (16 or 4), or 0: element loads through registers
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t n) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-                     : "memory");
+// 16 bytes of which the first n come from memory, the rest are zeros
+__device__ __forceinline__ void copy_async(uint32_t dst, uintptr_t src, uint32_t n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
 }
 
 __device__ __forceinline__ void copy_commit() {
@@ -170,24 +165,92 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A tile of STEPS x 64 channels of one input into shared memory [step][64];
-// what lies past the sequence or the channels is filled with zeros.
-template <typename T, int STEPS, int BYTES>
-__device__ __forceinline__ void load_tile(void* dst, const void* src, long long stride, int b,
-                                          int t0, int c0, int seqlen, int dim) {
-    constexpr int kUnit = BYTES ? BYTES / (int)sizeof(T) : 1;  // elements per copy
-    constexpr int kPerRow = kCh / kUnit;
-    const T* base = static_cast<const T*>(src) + (long long)b * seqlen * stride + c0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < STEPS * kPerRow; i += blockDim.x) {
-        const int r = i / kPerRow, c = (i % kPerRow) * kUnit;
-        const bool in = t0 + r < seqlen && c0 + c < dim;
-        const T* p = in ? base + (long long)(t0 + r) * stride + c : static_cast<const T*>(src);
-        T* d = static_cast<T*>(dst) + r * kCh + c;
-        // a unit lies wholly inside the row or wholly outside: dim is a
-        // multiple of it
-        if constexpr (BYTES) copy_async<BYTES>(smem_u32(d), p, in ? BYTES : 0);
-        else *d = in ? *p : from_f32<T>(0.0f);
+// Rows that are not 16-byte aligned: a tile's row is copied from the 16-byte boundary
+// before it, in 16-byte pieces (16 bytes with their part of the row are
+// always memory of the tensor's own), and lies in shared memory at the offset
+// it has from that boundary.  (4-byte copies took 99 us, element loads 324 us for the
+// forward of batch 8, 2048 steps, 1500 and 1501 channels of bf16 with a gate, against
+// 85 us and 89 us.)
+template <typename T>
+constexpr int kShiftedRow = kCh * (int)sizeof(T) + 16;
+template <typename T>
+constexpr int kPieces = kShiftedRow<T> / 16;
+
+// where a row's 64 channels start behind the boundary
+__device__ __forceinline__ uint32_t shift_of(const void* base, long long at, int es) {
+    return (uint32_t)(reinterpret_cast<uintptr_t>(base) + at * es) & 15u;
+}
+
+template <typename T, int STEPS, int THREADS>
+__device__ __forceinline__ void load_shifted(void* dst, const void* src, long long stride, int b,
+                                             int t0, int c0, int seqlen, int dim) {
+    const long long first = (long long)b * seqlen * stride + c0;
+    const uint32_t bytes = min(kCh, dim - c0) * (int)sizeof(T);
+    // THREADS / STEPS neighbouring threads to a row, every so many-th piece each
+    constexpr int PER = THREADS / STEPS;
+    const int r = threadIdx.x / PER, q = threadIdx.x % PER;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src) +
+                         (first + (long long)(t0 + r) * stride) * (long long)sizeof(T);
+    const uintptr_t from = at & ~uintptr_t(15);
+    // bytes behind the boundary, none past the sequence
+    const int end = t0 + r < seqlen ? (int)((uint32_t)(at & 15) + bytes) : 0;
+    const uint32_t to = smem_u32(static_cast<uint8_t*>(dst) + r * kShiftedRow<T>);
+#pragma unroll
+    for (int j0 = 0; j0 < kPieces<T>; j0 += PER) {
+        const int j = j0 + q, n = max(0, min(16, end - j * 16));
+        if (j < kPieces<T>)
+            copy_async(to + j * 16, n > 0 ? from + j * 16 : reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15), n);
+    }
+}
+
+// two neighbouring channels at a byte offset that is a multiple of the element's size
+template <typename T>
+__device__ __forceinline__ float2 get_shifted(const uint8_t* row, uint32_t off) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (off >> 2);
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t v = __funnelshift_r(w[0], w[1], (off & 2) * 8);
+        return make_float2(bf16lo(v), bf16hi(v));
+    } else {
+        return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void put_shifted(uint8_t* row, uint32_t off, float2 v) {
+    T* p = reinterpret_cast<T*>(row + off);
+    p[0] = from_f32<T>(v.x);
+    p[1] = from_f32<T>(v.y);
+}
+
+// A warp's `rows` rows (of S) of results out of shared memory (row r at its own offset behind
+// the 16-byte boundary before its place): whole 16 bytes where they are the row's, else
+// element by element.
+template <typename T, int S>
+__device__ __forceinline__ void send_shifted(const uint8_t* smem, void* out, size_t first, int dim,
+                                             int rows, int channels, int lane) {
+    // 32 / S neighbouring lanes to a row: its whole pieces, then the elements before
+    // the first and after the last
+    constexpr int PER = 32 / S, ES = (int)sizeof(T), kEdge = 16 / ES;
+    const int r = lane / PER, q = lane % PER;
+    if (r >= rows) return;
+    uint8_t* p = reinterpret_cast<uint8_t*>(static_cast<T*>(out) + first + (size_t)r * dim);
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), end = off + channels * ES;
+    p -= off;
+    const uint8_t* s = smem + r * kShiftedRow<T>;
+#pragma unroll
+    for (int j0 = 0; j0 < kPieces<T>; j0 += PER) {
+        const int j = (j0 + q) * 16;
+        if (j >= off && j + 16 <= end)
+            *reinterpret_cast<uint4*>(p + j) = *reinterpret_cast<const uint4*>(s + j);
+    }
+    // up to kEdge - 1 elements at either end
+    const int head = min((off + 15) & ~15, end), tail = max(end & ~15, head);
+#pragma unroll
+    for (int e0 = 0; e0 < kEdge; e0 += PER) {
+        const int e = (e0 + q) * ES;
+        if (off + e < head)
+            *reinterpret_cast<T*>(p + off + e) = *reinterpret_cast<const T*>(s + off + e);
+        if (tail + e < end)
+            *reinterpret_cast<T*>(p + tail + e) = *reinterpret_cast<const T*>(s + tail + e);
     }
 }
 
@@ -381,25 +444,28 @@ __device__ __forceinline__ bool all_fast(const void* const* rows) {
 
 // ---------------------------------------------------------- tile kernels
 
-__host__ __device__ constexpr int tile_steps(bool grad) { return grad ? kKeep : 2 * kKeep; }
+__host__ __device__ constexpr int tile_steps(bool grad, bool tma) {
+    return grad || !tma ? kKeep : 2 * kKeep;
+}
 
-template <typename T, int NIN, bool GRAD>
+template <typename T, int NIN, bool GRAD, bool TMA>
 struct LinSmem {
-    static constexpr int kTile = tile_steps(GRAD) * kCh * (int)sizeof(T);  // of one input
+    static constexpr int kRow = TMA ? kCh * (int)sizeof(T) : kShiftedRow<T>;
+    static constexpr int kTile = tile_steps(GRAD, TMA) * kRow;  // of one input
     static constexpr int kStage = NIN * kTile;
 };
 
 // GRAD false: inputs f, x[, z], output y.  GRAD true: inputs f, x, dy[, z],
-// outputs df, dx[, dz].  BYTES 16: TMA.
-template <typename T, typename TO, int WARPS, int STAGES, int BYTES, bool GATED, bool GRAD, int MINB>
+// outputs df, dx[, dz].  TMA: every row 16-byte aligned; else shifted rows.
+template <typename T, typename TO, int WARPS, int STAGES, bool TMA, bool GATED, bool GRAD, int MINB>
 __global__ void __launch_bounds__(WARPS * 32, MINB)
     linrec_tile_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
     constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
-    constexpr int STEPS = tile_steps(GRAD), S = STEPS / WARPS;
-    constexpr bool TMA = BYTES == 16;
-    // results of the inputs' size take their places in the tile
-    constexpr bool INPLACE = TMA && sizeof(T) == sizeof(TO);
-    using SM = LinSmem<T, NIN, GRAD>;
+    constexpr int STEPS = tile_steps(GRAD, TMA), S = STEPS / WARPS;
+    // results of the inputs' size take their places in the tile, and leave by TMA or,
+    // where rows are shifted, by their warps
+    constexpr bool STAGED = sizeof(T) == sizeof(TO), INPLACE = TMA && STAGED;
+    using SM = LinSmem<T, NIN, GRAD, TMA>;
     extern __shared__ __align__(1024) uint8_t smem[];
     // the warps' (P, q), gradient also the reverse q; each q is replaced by that of
     // all that stands before its warp in the scan's order (for the gradient's q: in
@@ -455,8 +521,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             } else {
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
-                    load_tile<T, STEPS, BYTES>(dst + i * SM::kTile, a.in[i], a.stride[i], b,
-                                               tile * STEPS, c0, a.seqlen, a.dim);
+                    load_shifted<T, STEPS, WARPS * 32>(dst + i * SM::kTile, a.in[i], a.stride[i], b,
+                                                       tile * STEPS, c0, a.seqlen, a.dim);
             }
         }
         if constexpr (!TMA) copy_commit();
@@ -515,9 +581,45 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         const bool valid = c < a.dim, two = c + 1 < a.dim;
         const size_t chan = (size_t)b * a.dim + c;
         const int t0 = tile * STEPS + warp * S;
-        uint8_t* base = smem + stage * SM::kStage + (warp * S * kCh + lane * 2) * (int)sizeof(T);
-        auto at = [&](int i, int k) -> void* {
-            return base + i * SM::kTile + k * kCh * (int)sizeof(T);
+        uint8_t* base = smem + stage * SM::kStage + warp * S * SM::kRow;
+        const long long row0 = (long long)b * a.seqlen + t0;
+        // where the warp's first row starts behind its 16-byte boundary, and how far that
+        // moves from a row to the next
+        uint32_t sh_in[NIN], d_in[NIN], sh_out[3] = {}, d_out = 0;
+        if constexpr (!TMA) {
+#pragma unroll
+            for (int i = 0; i < NIN; ++i) {
+                sh_in[i] = shift_of(a.in[i], row0 * a.stride[i] + c - lane * 2, sizeof(T));
+                d_in[i] = (uint32_t)(a.stride[i] * (long long)sizeof(T)) & 15;
+            }
+#pragma unroll
+            for (int i = 0; i < (GRAD ? (GATED ? 3 : 2) : 1); ++i)
+                sh_out[i] = shift_of(a.out[i], row0 * a.dim + c - lane * 2, sizeof(TO));
+            d_out = (uint32_t)a.dim * (uint32_t)sizeof(TO) & 15;
+        }
+        // this lane's two channels of input i at the warp's step k
+        auto get = [&](int i, int k) -> float2 {
+            const uint8_t* row = base + i * SM::kTile + k * SM::kRow;
+            if constexpr (TMA) return Pair<T>::get(row + lane * 2 * sizeof(T));
+            else return get_shifted<T>(row, ((sh_in[i] + k * d_in[i]) & 15) + lane * 2 * sizeof(T));
+        };
+        // a result into the place of input i (shifted rows: at its own offset there)
+        const size_t o = (size_t)row0 * a.dim + c;
+        auto put = [&](int i, int k, int result, float2 v) {
+            uint8_t* row = base + i * SM::kTile + k * SM::kRow;
+            if constexpr (INPLACE)
+                Pair<TO>::put(row + lane * 2 * sizeof(T), v);
+            else if constexpr (STAGED)
+                put_shifted<TO>(row, ((sh_out[result] + k * d_out) & 15) + lane * 2 * sizeof(TO), v);
+            else if (valid && t0 + k < a.seqlen)
+                put2<TO>(a.out[result], o + (size_t)k * a.dim, v, two, a.vec_out);
+        };
+        auto send_rows = [&](int i, int result) {
+            if constexpr (!TMA && STAGED) {
+                __syncwarp();
+                send_shifted<TO, S>(base + i * SM::kTile, a.out[result], o - lane * 2, a.dim,
+                                 min(S, a.seqlen - t0), min(kCh, a.dim - (c - lane * 2)), lane);
+            }
         };
 
         // the state entering the tile, for the gradient's replay
@@ -531,21 +633,38 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             }
         }
 
-        const void* rows[S];
+        float2 ga[S], gb[S];  // a_t, and b_t (forward) or 1 - a_t (gradient)
+        // warps whose steps are all past the sequence have nothing to do; a warp whose
+        // gates all lie within |f| < 80 needs no comparisons
+        const bool live = t0 < a.seqlen;
+        bool fast = false;
+        if (live) {
+            if constexpr (TMA) {
+                const void* rows[S];
 #pragma unroll
-        for (int k = 0; k < S; ++k) rows[k] = at(0, k);
-        const bool fast = __all_sync(0xffffffffu, all_fast<T, S>(rows) && t0 + S <= a.seqlen);
+                for (int k = 0; k < S; ++k) rows[k] = base + k * SM::kRow + lane * 2 * sizeof(T);
+                fast = all_fast<T, S>(rows);
+            } else {
+                fast = true;
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const float2 f = get(0, k);
+                    ga[k] = f;  // read once: the gate takes its place
+                    fast = fast && fabsf(f.x) < kFastGate && fabsf(f.y) < kFastGate;
+                }
+            }
+            fast = __all_sync(0xffffffffu, fast && t0 + S <= a.seqlen);
+        }
 
         // ---- the warp's steps from zero
-        float2 ga[S], gb[S];  // a_t, and b_t (forward) or 1 - a_t (gradient)
         float2 P = both(1.0f), q = both(0.0f);
         auto scan = [&](auto fast_) {
             constexpr bool F = decltype(fast_)::value;
 #pragma unroll
             for (int k = 0; k < S; ++k) {
-                const float2 x = Pair<T>::get(at(1, k));
+                const float2 x = get(1, k);
                 float2 om;
-                Step<F>::gates(Pair<T>::get(at(0, k)), ga[k], om);
+                Step<F>::gates(TMA ? get(0, k) : ga[k], ga[k], om);
                 if (!F && t0 + k >= a.seqlen) {
                     ga[k] = both(1.0f);
                     om = both(0.0f);
@@ -561,9 +680,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 float2 r = both(0.0f);
 #pragma unroll
                 for (int k = S - 1; k >= 0; --k) {
-                    float2 d = Pair<T>::get(at(2, k));
+                    float2 d = get(2, k);
                     if constexpr (GATED) {
-                        const float2 z = Pair<T>::get(at(3, k));
+                        const float2 z = get(3, k);
                         float2 t;
                         d = mul2(d, mul2(z, sigmoid2(z, t)));
                     }
@@ -573,7 +692,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             }
         };
         if (fast) scan(std::true_type{});
-        else scan(std::false_type{});
+        else if (live) scan(std::false_type{});
+        else if (GRAD) s_r[GRAD ? warp : 0][lane] = both(0.0f);
         s_P[warp][lane] = P;
         s_q[warp][lane] = q;
         __syncthreads();
@@ -649,10 +769,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         in = Step<false>::next(s_preP[warp][lane], in, GRAD ? s_r[warp][lane] : s_q[warp][lane]);
 
         // ---- the steps again from the warp's entry state
-        const size_t o = ((size_t)b * a.seqlen + t0) * a.dim + c;
         if constexpr (!GRAD) {
             float2 h = in;
-            if (a.keep && warp % (WARPS / 2) == 0 && valid && t0 < a.seqlen) {
+            if (a.keep && t0 % kKeep == 0 && valid && live) {
                 float* s = a.keep + (size_t)(t0 / kKeep) * a.batch * a.dim + chan;
                 s[0] = h.x;
                 if (two) s[1] = h.y;
@@ -664,18 +783,17 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                     h = Step<F>::next(ga[k], h, gb[k]);
                     float2 y = h;
                     if constexpr (GATED) {
-                        const float2 z = Pair<T>::get(at(2, k));
+                        const float2 z = get(2, k);
                         float2 t;
                         y = mul2(y, mul2(z, sigmoid2(z, t)));
                     }
-                    if constexpr (INPLACE) Pair<TO>::put(at(0, k), y);
-                    else if (valid && t0 + k < a.seqlen)
-                        put2<TO>(a.out[0], o + (size_t)k * a.dim, y, two, a.vec_out);
+                    put(0, k, 0, y);
                 }
             };
-            if (a.out[0]) {
+            if (a.out[0] && live) {
                 if (fast) replay(std::true_type{});
                 else replay(std::false_type{});
+                send_rows(0, 0);
             }
         } else {
             float2 mu = in, h = Step<false>::next(s_timeP[warp][lane], hk, s_q[warp][lane]);
@@ -685,16 +803,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
 #pragma unroll
                 for (int k = 0; k < S; ++k) {
                     prev[k] = h;
-                    h = Step<F>::next(ga[k], h, Step<F>::input(gb[k], Pair<T>::get(at(1, k))));
+                    h = Step<F>::next(ga[k], h, Step<F>::input(gb[k], get(1, k)));
                 }
 #pragma unroll
                 for (int k = S - 1; k >= 0; --k) {
-                    [[maybe_unused]] const bool inside = valid && t0 + k < a.seqlen;
-                    [[maybe_unused]] const size_t ok_ = o + (size_t)k * a.dim;
-                    const float2 x = Pair<T>::get(at(1, k));
-                    float2 d = Pair<T>::get(at(2, k));
+                    const float2 x = get(1, k);
+                    float2 d = get(2, k);
                     if constexpr (GATED) {
-                        const float2 z = Pair<T>::get(at(3, k));
+                        const float2 z = get(3, k);
                         float2 t;
                         const float2 sg = sigmoid2(z, t);
                         const float2 si = mul2(z, sg);
@@ -702,25 +818,26 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                         const float2 ds = fma2(mul2(si, both(-1.0f)), sg, add2(sg, si));
                         const float2 dz = mul2(mul2(d, h), ds);
                         d = mul2(d, si);
-                        if constexpr (INPLACE) Pair<TO>::put(at(3, k), dz);
-                        else if (inside) put2<TO>(a.out[2], ok_, dz, two, a.vec_out);
+                        if constexpr (!TMA) __syncwarp();  // the row is read before it is replaced
+                        put(3, k, 2, dz);
                     }
                     const float2 lam = add2(d, mu);
                     const float2 df = Step<F>::dgate(ga[k], gb[k], lam, prev[k], x);
                     const float2 dx = Step<F>::input(gb[k], lam);
-                    if constexpr (INPLACE) {
-                        Pair<TO>::put(at(0, k), df);
-                        Pair<TO>::put(at(1, k), dx);
-                    } else if (inside) {
-                        put2<TO>(a.out[0], ok_, df, two, a.vec_out);
-                        put2<TO>(a.out[1], ok_, dx, two, a.vec_out);
-                    }
+                    if constexpr (!TMA && !GATED) __syncwarp();
+                    put(0, k, 0, df);
+                    put(1, k, 1, dx);
                     mu = Step<F>::decay(ga[k], lam);
                     h = prev[k];
                 }
             };
-            if (fast) replay(std::true_type{});
-            else replay(std::false_type{});
+            if (live) {
+                if (fast) replay(std::true_type{});
+                else replay(std::false_type{});
+                send_rows(0, 0);
+                send_rows(1, 1);
+                if constexpr (GATED) send_rows(3, 2);
+            }
         }
         if constexpr (INPLACE) fence_proxy_async_smem();
         ahead = next(ahead);
@@ -745,49 +862,107 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
 
 // -------------------------------------------------------- short sequences
 
-// One thread walks the steps of two channels: a decode step (one token) is a
-// single pass over the states.
-template <typename T, typename TO, bool VEC, bool GATED>
-__global__ void __launch_bounds__(128) linrec_walk_kernel(const LinArgs a) {
-    const int pairs = (a.dim + 1) / 2;
-    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+// One thread walks the steps of CPT channels (two where every pair of them is aligned),
+// eight steps' loads in flight: a decode step (one token) is a single pass over the
+// states, and many sequences fill the GPU by themselves.
+constexpr int kWalkThreads = 128, kWalkAhead = 8;
+
+template <typename T, int CPT>
+__device__ __forceinline__ float2 walk_get(const void* base, long long at) {
+    const T* p = static_cast<const T*>(base) + at;
+    if constexpr (CPT == 2) return Pair<T>::get(p);
+    return make_float2(to_f32(*p), 0.0f);
+}
+
+template <typename T, int CPT>
+__device__ __forceinline__ void walk_put(void* base, long long at, float2 v) {
+    T* p = static_cast<T*>(base) + at;
+    if constexpr (CPT == 2) Pair<T>::put(p, v);
+    else *p = from_f32<T>(v.x);
+}
+
+template <typename T, typename TO, int CPT, bool GATED>
+__global__ void __launch_bounds__(kWalkThreads) linrec_walk_kernel(const LinArgs a) {
+    const int per = a.dim / CPT;
+    const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
     if (i == 0 && a.status && !a.keep_status) *a.status = 0;
-    if (i >= (long long)a.batch * pairs) return;
-    const int b = (int)(i / pairs), c = (int)(i % pairs) * 2;
-    const bool two = c + 1 < a.dim;
-    const size_t chan = (size_t)b * a.dim + c;
-    auto get = [&](int k, int t) -> float2 {
-        const T* p = static_cast<const T*>(a.in[k]) + ((long long)b * a.seqlen + t) * a.stride[k] + c;
-        if constexpr (VEC) return Pair<T>::get(p);
-        return make_float2(to_f32(p[0]), two ? to_f32(p[1]) : 0.0f);
-    };
+    if (i >= (long long)a.batch * per) return;
+    const int b = (int)(i / per), c = (int)(i % per) * CPT;
+    const long long chan = (long long)b * a.dim + c, row0 = (long long)b * a.seqlen;
     float2 h = make_float2(0.0f, 0.0f);
-    if (a.h0) h = load_state2(a.h0, chan, two);
-    if (a.keep && a.seqlen > 0) {
-        a.keep[chan] = h.x;
-        if (two) a.keep[chan + 1] = h.y;
-    }
-#pragma unroll 2
-    for (int t = 0; t < a.seqlen; ++t) {
-        const float2 f = get(0, t), x = get(1, t);
-        float2 g, om, y;
-        gate(f.x, g.x, om.x);
-        gate(f.y, g.y, om.y);
-        h.x = step(g.x, h.x, input_term(om.x, x.x));
-        h.y = step(g.y, h.y, input_term(om.y, x.y));
-        y = h;
-        if constexpr (GATED) {
-            const float2 z = get(2, t);
-            y.x *= silu_f(z.x);
-            y.y *= silu_f(z.y);
+    if (a.h0) h = walk_get<float, CPT>(a.h0, chan);
+    for (int t0 = 0; t0 < a.seqlen; t0 += kWalkAhead) {
+        float2 f[kWalkAhead], x[kWalkAhead], z[kWalkAhead];
+#pragma unroll
+        for (int k = 0; k < kWalkAhead; ++k) {
+            if (t0 + k >= a.seqlen) break;
+            const long long t = row0 + t0 + k;
+            f[k] = walk_get<T, CPT>(a.in[0], t * a.stride[0] + c);
+            x[k] = walk_get<T, CPT>(a.in[1], t * a.stride[1] + c);
+            if constexpr (GATED) z[k] = walk_get<T, CPT>(a.in[2], t * a.stride[2] + c);
         }
-        if (a.out[0])
-            put2<TO>(a.out[0], ((size_t)b * a.seqlen + t) * a.dim + c, y, two, a.vec_out);
+        if (a.keep && t0 % kKeep == 0)
+            walk_put<float, CPT>(a.keep, (long long)(t0 / kKeep) * a.batch * a.dim + chan, h);
+#pragma unroll
+        for (int k = 0; k < kWalkAhead; ++k) {
+            if (t0 + k >= a.seqlen) break;
+            float2 g, om, u;
+            Step<false>::gates(f[k], g, om);
+            h = Step<false>::next(g, h, Step<false>::input(om, x[k]));
+            float2 y = h;
+            if constexpr (GATED) y = mul2(y, mul2(z[k], sigmoid2(z[k], u)));
+            if (a.out[0]) walk_put<TO, CPT>(a.out[0], (row0 + t0 + k) * a.dim + c, y);
+        }
     }
-    if (a.last) {
-        a.last[chan] = h.x;
-        if (two) a.last[chan + 1] = h.y;
+    if (a.last) walk_put<float, CPT>(a.last, chan, h);
+}
+
+// The gradient of a sequence of up to kWalkSteps steps: forwards keeping each step's
+// state, then backwards.
+template <typename T, typename TO, int CPT, bool GATED>
+__global__ void __launch_bounds__(kWalkThreads) linrec_walk_bwd_kernel(const LinArgs a) {
+    const int per = a.dim / CPT;
+    const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
+    if (i == 0 && !a.keep_status) *a.status = 0;
+    if (i >= (long long)a.batch * per) return;
+    const int b = (int)(i / per), c = (int)(i % per) * CPT;
+    const long long chan = (long long)b * a.dim + c, row0 = (long long)b * a.seqlen;
+    float2 h = make_float2(0.0f, 0.0f), mu = h;
+    if (a.first) h = walk_get<float, CPT>(a.first, chan);
+    if (a.h0) mu = walk_get<float, CPT>(a.h0, chan);
+    float2 prev[kWalkSteps];  // h_{t-1}
+#pragma unroll
+    for (int k = 0; k < kWalkSteps; ++k) {
+        if (k >= a.seqlen) break;
+        float2 g, om;
+        Step<false>::gates(walk_get<T, CPT>(a.in[0], (row0 + k) * a.stride[0] + c), g, om);
+        prev[k] = h;
+        h = Step<false>::next(
+            g, h, Step<false>::input(om, walk_get<T, CPT>(a.in[1], (row0 + k) * a.stride[1] + c)));
     }
+#pragma unroll
+    for (int k = kWalkSteps - 1; k >= 0; --k) {
+        if (k >= a.seqlen) continue;
+        const long long t = row0 + k, at = t * a.dim + c;
+        float2 g, om;  // again: the lines are in the cache
+        Step<false>::gates(walk_get<T, CPT>(a.in[0], t * a.stride[0] + c), g, om);
+        const float2 x = walk_get<T, CPT>(a.in[1], t * a.stride[1] + c);
+        float2 d = walk_get<T, CPT>(a.in[2], t * a.stride[2] + c);
+        if constexpr (GATED) {
+            const float2 z = walk_get<T, CPT>(a.in[3], t * a.stride[3] + c);
+            float2 u;
+            const float2 sg = sigmoid2(z, u), si = mul2(z, sg);
+            const float2 ds = fma2(mul2(si, both(-1.0f)), sg, add2(sg, si));
+            walk_put<TO, CPT>(a.out[2], at, mul2(mul2(d, h), ds));
+            d = mul2(d, si);
+        }
+        const float2 lam = add2(d, mu);
+        walk_put<TO, CPT>(a.out[0], at, Step<false>::dgate(g, om, lam, prev[k], x));
+        walk_put<TO, CPT>(a.out[1], at, Step<false>::input(om, lam));
+        mu = Step<false>::decay(g, lam);
+        h = prev[k];
+    }
+    if (a.last) walk_put<float, CPT>(a.last, chan, mu);
 }
 
 // ---------------------------------------------------------------- launch
@@ -836,28 +1011,29 @@ bool make_map(CUtensorMap* map, const void* base, size_t es, long long stride, c
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, typename TO, int BYTES, bool GATED, bool GRAD>
-bool launch_tile(LinArgs& a, cudaStream_t s) {
+template <typename T, typename TO, bool TMA, bool GATED, bool GRAD>
+bool launch_tile(LinArgs& a, uint8_t* ws, cudaStream_t s) {
     constexpr int NIN = (GRAD ? 3 : 2) + (GATED ? 1 : 0);
     // 16 warps an SM, and as many stages as fit in its shared memory
     constexpr int WARPS = sizeof(T) == 2 ? 8 : 16, MINB = 16 / WARPS;
-    constexpr int kStage = LinSmem<T, NIN, GRAD>::kStage;
+    constexpr int kStage = LinSmem<T, NIN, GRAD, TMA>::kStage;
     constexpr int STAGES = 96 * 1024 * WARPS / 8 / kStage;
     static_assert(STAGES >= 2, "one tile at work, one coming in");
     constexpr int smem = STAGES * kStage;
-    auto kernel = linrec_tile_kernel<T, TO, WARPS, STAGES, BYTES, GATED, GRAD, MINB>;
+    auto kernel = linrec_tile_kernel<T, TO, WARPS, STAGES, TMA, GATED, GRAD, MINB>;
+    place(a, ws, tiles_of(a.seqlen, tile_steps(GRAD, TMA)));
     const void* fn = reinterpret_cast<const void*>(kernel);
     static std::atomic<int> cache[ssm_host::kMaxDevices];
     const int slots =
         ssm_host::sm_count() * ssm_host::resident_ctas(fn, WARPS * 32, smem, cache);
     if (slots < 1) return false;
     LinMaps maps{};
-    if constexpr (BYTES == 16) {
+    if constexpr (TMA) {
         for (int i = 0; i < NIN; ++i)
-            if (!make_map(&maps.in[i], a.in[i], sizeof(T), a.stride[i], a, tile_steps(GRAD))) return false;
+            if (!make_map(&maps.in[i], a.in[i], sizeof(T), a.stride[i], a, tile_steps(GRAD, TMA))) return false;
         for (int i = 0; i < 3 && sizeof(T) == sizeof(TO); ++i)
             if (a.out[i] && !make_map(&maps.out[i], a.out[i], sizeof(TO), a.dim, a,
-                                       tile_steps(GRAD)))
+                                       tile_steps(GRAD, TMA)))
                 return false;
     }
     const long long items = (long long)a.blocks * a.tiles;
@@ -879,41 +1055,58 @@ bool launch_tile(LinArgs& a, cudaStream_t s) {
            cudaSuccess;
 }
 
+// Whether TMA can take the inputs' rows and bring the results' home.
+bool rows_aligned(const LinArgs& a, int n, size_t es, size_t out_es) {
+    bool ok = a.dim * es % 16 == 0 && a.dim * out_es % 16 == 0;
+    for (int i = 0; i < n; ++i)
+        ok = ok && reinterpret_cast<uintptr_t>(a.in[i]) % 16 == 0 &&
+             (size_t)a.stride[i] * es % 16 == 0;
+    return ok;
+}
+
 template <typename T, typename TO, bool GRAD>
-bool launch_by(LinArgs& a, int bytes, bool gated, cudaStream_t s) {
-    if (bytes == 16)
-        return gated ? launch_tile<T, TO, 16, true, GRAD>(a, s)
-                     : launch_tile<T, TO, 16, false, GRAD>(a, s);
-    if (bytes == 4)
-        return gated ? launch_tile<T, TO, 4, true, GRAD>(a, s)
-                     : launch_tile<T, TO, 4, false, GRAD>(a, s);
-    if constexpr (sizeof(T) == 2)
-        return gated ? launch_tile<T, TO, 0, true, GRAD>(a, s)
-                     : launch_tile<T, TO, 0, false, GRAD>(a, s);
-    return false;
+bool launch_by(LinArgs& a, uint8_t* ws, bool gated, cudaStream_t s) {
+    const int nin = (GRAD ? 3 : 2) + (gated ? 1 : 0);
+    if (rows_aligned(a, nin, sizeof(T), sizeof(TO)))
+        return gated ? launch_tile<T, TO, true, true, GRAD>(a, ws, s)
+                     : launch_tile<T, TO, true, false, GRAD>(a, ws, s);
+    return gated ? launch_tile<T, TO, false, true, GRAD>(a, ws, s)
+                 : launch_tile<T, TO, false, false, GRAD>(a, ws, s);
 }
 
-// The widest copy every row of every input allows: 16 bytes, 4, or elements.
-int copy_bytes(const LinArgs& a, int n, size_t es) {
-    for (int unit : {16, 4}) {
-        bool ok = (size_t)a.dim * es % unit == 0;
-        for (int i = 0; i < n; ++i)
-            ok = ok && reinterpret_cast<uintptr_t>(a.in[i]) % unit == 0 &&
-                 (size_t)a.stride[i] * es % unit == 0;
-        if (ok) return unit;
+// Sequences of up to kWalkSteps steps, and (forward) of up to twice that where the
+// channels are so many that a thread to each pair of them fills the GPU, are walked
+// (batch 256, 2560 channels of bf16 with a gate: 34 us against 74 us for the tiles at 17
+// steps; batch 200: 83 us against 75 us at 60).
+constexpr long long kWalkChannels = 262144;
+
+bool walks(int batch, int seqlen, int dim) {
+    return seqlen <= kWalkSteps ||
+           (seqlen <= 2 * kWalkSteps && (long long)batch * dim >= kWalkChannels);
+}
+
+template <typename T, typename TO, bool GRAD>
+bool launch_walk(const LinArgs& a, bool gated, cudaStream_t s) {
+    // two channels in one access to each input and result
+    const int nin = (GRAD ? 3 : 2) + (gated ? 1 : 0);
+    bool pairs = a.dim % 2 == 0;
+    for (int i = 0; i < nin; ++i)
+        pairs = pairs && reinterpret_cast<uintptr_t>(a.in[i]) % (2 * sizeof(T)) == 0 &&
+                a.stride[i] % 2 == 0;
+    const long long n = (long long)a.batch * (pairs ? a.dim / 2 : a.dim);
+    const unsigned grid = (unsigned)((n + kWalkThreads - 1) / kWalkThreads);
+    auto go = [&](auto kernel) { kernel<<<grid, kWalkThreads, 0, s>>>(a); };
+    if constexpr (GRAD) {
+        if (pairs) gated ? go(linrec_walk_bwd_kernel<T, TO, 2, true>)
+                         : go(linrec_walk_bwd_kernel<T, TO, 2, false>);
+        else gated ? go(linrec_walk_bwd_kernel<T, TO, 1, true>)
+                   : go(linrec_walk_bwd_kernel<T, TO, 1, false>);
+    } else {
+        if (pairs) gated ? go(linrec_walk_kernel<T, TO, 2, true>)
+                         : go(linrec_walk_kernel<T, TO, 2, false>);
+        else gated ? go(linrec_walk_kernel<T, TO, 1, true>)
+                   : go(linrec_walk_kernel<T, TO, 1, false>);
     }
-    return 0;
-}
-
-template <typename T, typename TO>
-bool launch_walk(const LinArgs& a, bool vec, bool gated, cudaStream_t s) {
-    const long long n = (long long)a.batch * ((a.dim + 1) / 2);
-    const unsigned grid = (unsigned)((n + 127) / 128);
-    auto go = [&](auto kernel) { kernel<<<grid, 128, 0, s>>>(a); };
-    if (vec) gated ? go(linrec_walk_kernel<T, TO, true, true>)
-                   : go(linrec_walk_kernel<T, TO, true, false>);
-    else gated ? go(linrec_walk_kernel<T, TO, false, true>)
-               : go(linrec_walk_kernel<T, TO, false, false>);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -925,25 +1118,15 @@ bool by_types(ssm_dtype_t in, ssm_dtype_t out, F&& f) {
 }
 
 // The forward scan (a.out[0] may be NULL: states only).
-bool run_forward(LinArgs& a, ssm_dtype_t in, ssm_dtype_t out, bool gated, cudaStream_t s) {
-    const size_t es = ssm_host::dtype_size(in);
-    const int nin = gated ? 3 : 2;
+bool run_forward(LinArgs& a, uint8_t* ws, ssm_dtype_t in, ssm_dtype_t out, bool gated,
+                 cudaStream_t s) {
     return by_types(in, out, [&](auto ti, auto to) -> bool {
         using T = decltype(ti);
         using TO = decltype(to);
-        if (a.seqlen <= kWalkSteps) {
-            // two channels in one load: 2 * es bytes
-            bool vec = a.dim % 2 == 0;
-            for (int i = 0; i < nin; ++i)
-                vec = vec && reinterpret_cast<uintptr_t>(a.in[i]) % (2 * es) == 0 &&
-                      a.stride[i] % 2 == 0;
-            return launch_walk<T, TO>(a, vec, gated, s);
-        }
-        return launch_by<T, TO, false>(a, copy_bytes(a, nin, es), gated, s);
+        if (walks(a.batch, a.seqlen, a.dim)) return launch_walk<T, TO, false>(a, gated, s);
+        return launch_by<T, TO, false>(a, ws, gated, s);
     });
 }
-
-int fwd_tiles(int seqlen) { return seqlen <= kWalkSteps ? 1 : tiles_of(seqlen, tile_steps(false)); }
 
 struct Span { const void* p; size_t n; };
 
@@ -1023,8 +1206,9 @@ extern "C" ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void*
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
     a.vec_out = dim % 2 == 0;
     ssm_internal::lookback_setting(&a.spin_limit, &a.drop_first_publish);
-    place(a, static_cast<uint8_t*>(workspace), fwd_tiles(seqlen));
-    return run_forward(a, in_dtype, out_dtype, z != nullptr, static_cast<cudaStream_t>(stream))
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    place(a, ws, 1);
+    return run_forward(a, ws, in_dtype, out_dtype, z != nullptr, static_cast<cudaStream_t>(stream))
                ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -1084,13 +1268,13 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
     a.vec_out = dim % 2 == 0;
     ssm_internal::lookback_setting(&a.spin_limit, &a.drop_first_publish);
-    if (!checkpoints && seqlen > 0) {
+    if (!checkpoints && seqlen > kWalkSteps) {  // walked ones are short enough to keep them
         // the forward again, states only
         LinArgs w = a;
         w.h0 = initial_state;
         w.keep = reinterpret_cast<float*>(ws + scan_bytes(batch, dim, tiles_of(seqlen, kKeep)));
-        place(w, ws, fwd_tiles(seqlen));
-        if (!run_forward(w, in_dtype, in_dtype, false, s)) return SSM_ERR_CUDA;
+        place(w, ws, 1);
+        if (!run_forward(w, ws, in_dtype, in_dtype, false, s)) return SSM_ERR_CUDA;
         checkpoints = w.keep;
         a.keep_status = 1;
     }
@@ -1107,11 +1291,12 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
                          : cudaMemsetAsync(dinitial_state, 0, states * 4, s);
         return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
     }
-    place(a, ws, tiles_of(seqlen, tile_steps(true)));
+    place(a, ws, 1);
     const bool ok = by_types(in_dtype, grad_dtype, [&](auto ti, auto to) -> bool {
         using T = decltype(ti);
         using TO = decltype(to);
-        return launch_by<T, TO, true>(a, copy_bytes(a, z ? 4 : 3, es), z != nullptr, s);
+        if (seqlen <= kWalkSteps) return launch_walk<T, TO, true>(a, z != nullptr, s);
+        return launch_by<T, TO, true>(a, ws, z != nullptr, s);
     });
     return ok ? SSM_OK : SSM_ERR_CUDA;
 }
