@@ -9,7 +9,6 @@ kernels.  There is no fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -987,11 +986,22 @@ def ssm_decode_step_mamba3_mimo(state, prev_B, prev_x, x, dt, lam, A, B, C, D=No
 # stream the call runs on, so that their memory is not handed out again before
 # the kernels there are done with it.
 
-_NULL = contextlib.nullcontext()
+def _new(like, shape, dtype, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _on(stream):
-    return _NULL if stream is None else torch.cuda.stream(stream)
+def _out(t, name, like, shape, dtype, stream):
+    """The given output, checked, or a new one."""
+    return _new(like, shape, dtype, stream) if t is None else _like(t, name, shape, dtype)
+
+
+def _work(t, like, need, stream):
+    """The given workspace, or a new one."""
+    return (_new(like, max(need, 256), torch.uint8, stream) if t is None else
+            _req(t, "workspace", torch.uint8))
 
 
 def _p(t):
@@ -1037,14 +1047,9 @@ def ssm_add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, sum_
     rows, dim = _norm_args(x, weight, residual)
     out_dt = x.dtype if out_dtype is None else out_dtype
     res_dt = _sum_dtype(x, residual, sum_dtype, sum_out)
-    with _on(stream):
-        if y is None:
-            y = torch.empty(x.shape, dtype=out_dt, device=x.device)
-        if sum_out is None and return_sum:
-            sum_out = torch.empty(x.shape, dtype=res_dt, device=x.device)
-    _like(y, "y", x.shape, out_dt)
-    if sum_out is not None:
-        _like(sum_out, "sum_out", x.shape, res_dt)
+    y = _out(y, "y", x, x.shape, out_dt, stream)
+    if sum_out is not None or return_sum:
+        sum_out = _out(sum_out, "sum_out", x, x.shape, res_dt, stream)
     st = lib().ssm_add_rmsnorm_fwd(_p(x), _p(residual), _p(weight), float(eps), _p(y),
                                    _p(sum_out), rows, dim, _DT[x.dtype], _DT[res_dt],
                                    _dt_code(out_dt, "out_dtype"), _raw(stream, x))
@@ -1081,17 +1086,10 @@ def ssm_add_rmsnorm_e4m3_fwd(x, weight, residual=None, eps=1e-5, group=128, sum_
     if group not in (0, 32, 64, 128, 256):
         raise SSMError(5, "ssm_add_rmsnorm_e4m3_fwd")
     sshape = tuple(x.shape[:-1]) + (1 if group == 0 else -(-dim // group),)
-    with _on(stream):
-        if q is None:
-            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        if scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
-        if sum_out is None and return_sum:
-            sum_out = torch.empty(x.shape, dtype=res_dt, device=x.device)
-    _like(q, "q", x.shape, torch.float8_e4m3fn)
-    _like(scales, "scales", sshape, torch.float32)
-    if sum_out is not None:
-        _like(sum_out, "sum_out", x.shape, res_dt)
+    q = _out(q, "q", x, x.shape, torch.float8_e4m3fn, stream)
+    scales = _out(scales, "scales", x, sshape, torch.float32, stream)
+    if sum_out is not None or return_sum:
+        sum_out = _out(sum_out, "sum_out", x, x.shape, res_dt, stream)
     st = lib().ssm_add_rmsnorm_e4m3_fwd(_p(x), _p(residual), _p(weight), float(eps), group,
                                         _p(q), _p(scales), _p(sum_out), rows, dim,
                                         _DT[x.dtype], _DT[res_dt], _raw(stream, x))
@@ -1124,21 +1122,11 @@ def ssm_add_rmsnorm_bwd(dy, sum, weight, dsum=None, eps=1e-5, x_dtype=None, dx=N
     dx_dt = x_dtype or (dx.dtype if dx is not None else
                         dy.dtype if sum.dtype == torch.float32 else sum.dtype)
     same = dx_dt == sum.dtype
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty(sum.shape, dtype=dx_dt, device=sum.device)
-        if dresidual is None and not same:
-            dresidual = torch.empty(sum.shape, dtype=sum.dtype, device=sum.device)
-        if dweight is None:
-            dweight = torch.empty(dim, dtype=torch.float32, device=sum.device)
-        if workspace is None:
-            need = ssm_add_rmsnorm_bwd_workspace_bytes(rows, dim)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=sum.device)
-    _like(dx, "dx", sum.shape, dx_dt)
-    if dresidual is not None:
-        _like(dresidual, "dresidual", sum.shape, sum.dtype)
-    _like(dweight, "dweight", (dim,), torch.float32)
-    _req(workspace, "workspace", torch.uint8)
+    dx = _out(dx, "dx", sum, sum.shape, dx_dt, stream)
+    if dresidual is not None or not same:
+        dresidual = _out(dresidual, "dresidual", sum, sum.shape, sum.dtype, stream)
+    dweight = _out(dweight, "dweight", sum, (dim,), torch.float32, stream)
+    workspace = _work(workspace, sum, ssm_add_rmsnorm_bwd_workspace_bytes(rows, dim), stream)
     st = lib().ssm_add_rmsnorm_bwd(_p(sum), _p(weight), float(eps), _p(dy), _p(dsum),
                                    _p(dx), _p(dresidual), _p(dweight), rows, dim,
                                    _dt_code(dx_dt, "x_dtype"), _DT[sum.dtype],
@@ -1206,18 +1194,11 @@ def ssm_linrec_fwd(f, x, z=None, initial_state=None, out_dtype=None, y=None, fin
     sf, sx, sz = _linrec_args(f, x, z, initial_state)
     batch, seqlen, dim = x.shape
     out_dt = x.dtype if out_dtype is None else out_dtype
-    with _on(stream):
-        if y is None:
-            y = torch.empty((batch, seqlen, dim), dtype=out_dt, device=x.device)
-        if final_state is None and return_final_state:
-            final_state = torch.empty((batch, dim), dtype=torch.float32, device=x.device)
-        if workspace is None and seqlen > 16:  # shorter sequences run without one
-            need = ssm_linrec_workspace_bytes(batch, seqlen, dim)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    _like(y, "y", (batch, seqlen, dim), out_dt)
-    if final_state is not None:
-        _like(final_state, "final_state", (batch, dim), torch.float32)
-    _opt(workspace, "workspace", torch.uint8)
+    y = _out(y, "y", x, x.shape, out_dt, stream)
+    if final_state is not None or return_final_state:
+        final_state = _out(final_state, "final_state", x, (batch, dim), torch.float32, stream)
+    if workspace is not None or seqlen > 16:  # shorter sequences run without one
+        workspace = _work(workspace, x, ssm_linrec_workspace_bytes(batch, seqlen, dim), stream)
     _kept(checkpoints, batch, seqlen, dim)
     st = lib().ssm_linrec_fwd(_p(f), _p(x), _p(z), sf, sx, sz, _p(initial_state), _p(y),
                               _p(final_state), _p(checkpoints), batch, seqlen, dim,
@@ -1257,15 +1238,10 @@ def ssm_linrec_bwd(f, x, dy, z=None, initial_state=None, dfinal_state=None, chec
     for k in out:
         if k not in names:
             raise ValueError(f"out[{k!r}] is not an output of this call")
-    with _on(stream):
-        for k in names:
-            shape, dt = ((batch, dim), torch.float32) if k == "dinitial_state" else (x.shape, gd)
-            g[k] = (torch.empty(shape, dtype=dt, device=x.device) if k not in out else
-                    _like(out[k], f"out[{k!r}]", shape, dt))
-        if workspace is None:
-            need = ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    _req(workspace, "workspace", torch.uint8)
+    for k in names:
+        shape, dt = ((batch, dim), torch.float32) if k == "dinitial_state" else (x.shape, gd)
+        g[k] = _out(out.get(k), f"out[{k!r}]", x, shape, dt, stream)
+    workspace = _work(workspace, x, ssm_linrec_bwd_workspace_bytes(batch, seqlen, dim), stream)
     st = lib().ssm_linrec_bwd(_p(f), _p(x), _p(z), sf, sx, sz, _p(initial_state), _p(dy),
                               _p(dfinal_state), _p(checkpoints), _p(g["df"]), _p(g["dx"]),
                               _p(g["dz"]), _p(g["dinitial_state"]), batch, seqlen, dim,
@@ -1297,17 +1273,9 @@ def ssm_vocab_ce_fwd(h, W, targets, loss=None, lse=None, workspace=None, stream=
     (tokens, dim), W: (vocab, dim) bf16, dim a multiple of 8; targets: (tokens,) int64, a
     negative one for a token without loss.  Returns (loss, lse), (tokens,) fp32 each."""
     tokens, dim, vocab = _ce_args(h, W, targets)
-    with _on(stream):
-        if loss is None:
-            loss = torch.empty(tokens, dtype=torch.float32, device=h.device)
-        if lse is None:
-            lse = torch.empty(tokens, dtype=torch.float32, device=h.device)
-        if workspace is None:
-            need = ssm_vocab_ce_workspace_bytes(tokens, dim, vocab)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=h.device)
-    _like(loss, "loss", (tokens,), torch.float32)
-    _like(lse, "lse", (tokens,), torch.float32)
-    _req(workspace, "workspace", torch.uint8)
+    loss = _out(loss, "loss", h, (tokens,), torch.float32, stream)
+    lse = _out(lse, "lse", h, (tokens,), torch.float32, stream)
+    workspace = _work(workspace, h, ssm_vocab_ce_workspace_bytes(tokens, dim, vocab), stream)
     st = lib().ssm_vocab_ce_fwd(_p(h), _p(W), _p(targets), _p(loss), _p(lse), tokens, dim,
                                 vocab, _DT[h.dtype], _p(workspace), workspace.numel(),
                                 _raw(stream, h))
@@ -1330,14 +1298,9 @@ def ssm_vocab_ce_bwd(h, W, targets, lse, dloss, grad_dtype=None, workspace=None,
     for k in out:
         if k not in ("dh", "dW"):
             raise ValueError(f"out[{k!r}] is not an output of this call")
-    with _on(stream):
-        for k, t in (("dh", h), ("dW", W)):
-            g[k] = (torch.empty(t.shape, dtype=gd, device=h.device) if k not in out else
-                    _like(out[k], f"out[{k!r}]", t.shape, gd))
-        if workspace is None:
-            need = ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=h.device)
-    _req(workspace, "workspace", torch.uint8)
+    for k, t in (("dh", h), ("dW", W)):
+        g[k] = _out(out.get(k), f"out[{k!r}]", h, t.shape, gd, stream)
+    workspace = _work(workspace, h, ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab), stream)
     st = lib().ssm_vocab_ce_bwd(_p(h), _p(W), _p(targets), _p(lse), _p(dloss),
                                 _p(g["dh"]), _p(g["dW"]), tokens, dim, vocab, _DT[h.dtype], code,
                                 _p(workspace), workspace.numel(), _raw(stream, h))

@@ -543,6 +543,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         bulk_commit();
     };
 
+    // one tile per sequence: nothing was cleared before the launch, and only a load
+    // that never comes, seconds later, writes the status too
+    if (tid == 0 && a.tiles == 1 && blockIdx.x == 0 && !a.keep_status) *a.status = kNotYet;
     if constexpr (TMA) {
         if (tid == 0) {
             for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
@@ -1039,8 +1042,6 @@ bool launch_tile(LinArgs& a, uint8_t* ws, cudaStream_t s) {
     const long long items = (long long)a.blocks * a.tiles;
     const unsigned grid = (unsigned)std::min<long long>(items, slots);
     if (a.tiles == 1) {
-        // no look-back: only the status is cleared
-        if (!a.keep_status && cudaMemsetAsync(a.status, 0xff, 4, s) != cudaSuccess) return false;
         kernel<<<grid, WARPS * 32, smem, s>>>(maps, a);
         return cudaGetLastError() == cudaSuccess;
     }
