@@ -12,12 +12,14 @@
 // the state as h -> P h + q, and spans compose by (P1, q1) o (P2, q2) =
 // (P1 P2, P2 q1 + q2).
 //
-//  * A CTA takes a tile of 128 steps (gradient: 64) by 64 channels; each of its 8
-//    (bf16) or 16 (fp32) warps takes consecutive steps, a lane two neighbouring
-//    channels, so a warp's access to a step is one row segment of 64 channels.  Inputs come through a ring of shared
-//    memory tiles, by TMA where every row is 16-byte aligned (else cp.async or
-//    element loads), so the next tile's loads are in flight while this one waits
-//    for its predecessors; results go back in place and out by TMA.
+//  * A CTA takes a tile of 128 steps (gradient, and rows that are not 16-byte
+//    aligned: 64) by 64 channels; each of its 8 (bf16) or 16 (fp32) warps takes
+//    consecutive steps, a lane two neighbouring channels, so a warp's access to a
+//    step is one row segment of 64 channels.  Inputs come through a ring of shared
+//    memory tiles, by TMA where every row is 16-byte aligned, else by cp.async in
+//    16-byte pieces at each row's own shift, so the next tile's loads are in
+//    flight while this one waits for its predecessors; results go back in place
+//    and out by TMA, or by their warps.
 //  * Each warp scans its steps from zero, keeping a_t and b_t in registers;
 //    the warps' (P, q) meet in shared memory; tiles chain through a decoupled
 //    look-back (Merrill and Garland's single-pass prefix scan).  The published
@@ -35,8 +37,8 @@
 //    element in all; a warp whose gates all lie within |f| < 80, where no step can
 //    be masked, takes a path without them.
 // The gradient is the same scan of (a_t, a_t dh_t) in reverse order.  The states
-// it needs are not stored but taken again: the forward keeps the state at every
-// tile's first step in fp32, and each tile replays its own steps from there.
+// it needs are not stored but taken again: the forward keeps the state before every
+// 64th step in fp32, and each tile replays its own steps from there.
 //
 // Masked steps: a gate of +inf holds the state whatever x is there (b_t = 0 where
 // 1 - a_t = 0), a gate of -inf restarts it whatever it was (a_t = 0 drops h, NaN
@@ -73,6 +75,7 @@ struct LinArgs {
     void* out[3];             // forward: y; gradient: df, dx, dz
     float* keep;              // states entering every 64 steps [ceil(L / 64)][batch][dim]
     uint32_t* status;
+    uint32_t* clear;          // the status word, if the tile kernel has to clear it
     ulonglong2* agg;          // [tiles][blocks][32]: (P, q) of two channels
     uint2* inc;               // [tiles][blocks][32]: the state after the tile
     int batch, seqlen, dim;
@@ -544,12 +547,16 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
     };
 
     // one tile per sequence: nothing was cleared before the launch, and only a load
-    // that never comes, seconds later, writes the status too
-    if (tid == 0 && a.tiles == 1 && blockIdx.x == 0 && !a.keep_status) *a.status = kNotYet;
+    // that never comes, seconds later, writes the status too.  (The tile count and the
+    // flag tested here instead of by the host: 142 us against 133 us for 65536 steps of
+    // 1536 channels, as the forward kernel uses every register it may have.)
+    if constexpr (!TMA)
+        if (tid == 0 && a.clear && blockIdx.x == 0) *a.clear = kNotYet;
     if constexpr (TMA) {
         if (tid == 0) {
             for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
             fence_mbar_init();
+            if (a.clear && blockIdx.x == 0) *a.clear = kNotYet;
         }
         __syncthreads();
     }
@@ -584,7 +591,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         const bool valid = c < a.dim, two = c + 1 < a.dim;
         const size_t chan = (size_t)b * a.dim + c;
         const int t0 = tile * STEPS + warp * S;
-        uint8_t* base = smem + stage * SM::kStage + warp * S * SM::kRow;
+        // the warp's first row; aligned rows: this lane's channels of it
+        uint8_t* base = smem + stage * SM::kStage + warp * S * SM::kRow +
+                        (TMA ? lane * 2 * (int)sizeof(T) : 0);
         const long long row0 = (long long)b * a.seqlen + t0;
         // where the warp's first row starts behind its 16-byte boundary, and how far that
         // moves from a row to the next
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         // this lane's two channels of input i at the warp's step k
         auto get = [&](int i, int k) -> float2 {
             const uint8_t* row = base + i * SM::kTile + k * SM::kRow;
-            if constexpr (TMA) return Pair<T>::get(row + lane * 2 * sizeof(T));
+            if constexpr (TMA) return Pair<T>::get(row);
             else return get_shifted<T>(row, ((sh_in[i] + k * d_in[i]) & 15) + lane * 2 * sizeof(T));
         };
         // a result into the place of input i (shifted rows: at its own offset there)
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         auto put = [&](int i, int k, int result, float2 v) {
             uint8_t* row = base + i * SM::kTile + k * SM::kRow;
             if constexpr (INPLACE)
-                Pair<TO>::put(row + lane * 2 * sizeof(T), v);
+                Pair<TO>::put(row, v);
             else if constexpr (STAGED)
                 put_shifted<TO>(row, ((sh_out[result] + k * d_out) & 15) + lane * 2 * sizeof(TO), v);
             else if (valid && t0 + k < a.seqlen)
@@ -637,15 +646,17 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         }
 
         float2 ga[S], gb[S];  // a_t, and b_t (forward) or 1 - a_t (gradient)
-        // warps whose steps are all past the sequence have nothing to do; a warp whose
-        // gates all lie within |f| < 80 needs no comparisons
-        const bool live = t0 < a.seqlen;
+        // shifted rows: warps whose steps are all past the sequence have nothing to do
+        // (aligned rows are zeros there, and the branch costs registers that the kernel
+        // does not have: 116 us became 118 us for the gradient of 8 x 2048 x 1536); a warp
+        // whose gates all lie within |f| < 80 needs no comparisons
+        const bool live = TMA || t0 < a.seqlen;
         bool fast = false;
         if (live) {
             if constexpr (TMA) {
                 const void* rows[S];
 #pragma unroll
-                for (int k = 0; k < S; ++k) rows[k] = base + k * SM::kRow + lane * 2 * sizeof(T);
+                for (int k = 0; k < S; ++k) rows[k] = base + k * SM::kRow;
                 fast = all_fast<T, S>(rows);
             } else {
                 fast = true;
@@ -774,7 +785,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         // ---- the steps again from the warp's entry state
         if constexpr (!GRAD) {
             float2 h = in;
-            if (a.keep && t0 % kKeep == 0 && valid && live) {
+            if (a.keep && warp * S % kKeep == 0 && valid && t0 < a.seqlen) {
                 float* s = a.keep + (size_t)(t0 / kKeep) * a.batch * a.dim + chan;
                 s[0] = h.x;
                 if (two) s[1] = h.y;
@@ -866,8 +877,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
 // -------------------------------------------------------- short sequences
 
 // One thread walks the steps of CPT channels (two where every pair of them is aligned),
-// eight steps' loads in flight: a decode step (one token) is a single pass over the
-// states, and many sequences fill the GPU by themselves.
+// AHEAD steps' loads in flight: eight, and one where there is one, which then fetches less
+// code (batch 128, 2560 channels: 2.4 us against 2.6 us).  A decode step (one token) is a
+// single pass over the states, and many sequences fill the GPU by themselves.
 constexpr int kWalkThreads = 128, kWalkAhead = 8;
 
 template <typename T, int CPT>
@@ -884,7 +896,7 @@ __device__ __forceinline__ void walk_put(void* base, long long at, float2 v) {
     else *p = from_f32<T>(v.x);
 }
 
-template <typename T, typename TO, int CPT, bool GATED>
+template <typename T, typename TO, int CPT, int AHEAD, bool GATED>
 __global__ void __launch_bounds__(kWalkThreads) linrec_walk_kernel(const LinArgs a) {
     const int per = a.dim / CPT;
     const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
@@ -894,10 +906,10 @@ __global__ void __launch_bounds__(kWalkThreads) linrec_walk_kernel(const LinArgs
     const long long chan = (long long)b * a.dim + c, row0 = (long long)b * a.seqlen;
     float2 h = make_float2(0.0f, 0.0f);
     if (a.h0) h = walk_get<float, CPT>(a.h0, chan);
-    for (int t0 = 0; t0 < a.seqlen; t0 += kWalkAhead) {
-        float2 f[kWalkAhead], x[kWalkAhead], z[kWalkAhead];
+    for (int t0 = 0; t0 < a.seqlen; t0 += AHEAD) {
+        float2 f[AHEAD], x[AHEAD], z[AHEAD];
 #pragma unroll
-        for (int k = 0; k < kWalkAhead; ++k) {
+        for (int k = 0; k < AHEAD; ++k) {
             if (t0 + k >= a.seqlen) break;
             const long long t = row0 + t0 + k;
             f[k] = walk_get<T, CPT>(a.in[0], t * a.stride[0] + c);
@@ -907,7 +919,7 @@ __global__ void __launch_bounds__(kWalkThreads) linrec_walk_kernel(const LinArgs
         if (a.keep && t0 % kKeep == 0)
             walk_put<float, CPT>(a.keep, (long long)(t0 / kKeep) * a.batch * a.dim + chan, h);
 #pragma unroll
-        for (int k = 0; k < kWalkAhead; ++k) {
+        for (int k = 0; k < AHEAD; ++k) {
             if (t0 + k >= a.seqlen) break;
             float2 g, om, u;
             Step<false>::gates(f[k], g, om);
@@ -1042,6 +1054,7 @@ bool launch_tile(LinArgs& a, uint8_t* ws, cudaStream_t s) {
     const long long items = (long long)a.blocks * a.tiles;
     const unsigned grid = (unsigned)std::min<long long>(items, slots);
     if (a.tiles == 1) {
+        a.clear = a.keep_status ? nullptr : a.status;
         kernel<<<grid, WARPS * 32, smem, s>>>(maps, a);
         return cudaGetLastError() == cudaSuccess;
     }
@@ -1103,10 +1116,15 @@ bool launch_walk(const LinArgs& a, bool gated, cudaStream_t s) {
         else gated ? go(linrec_walk_bwd_kernel<T, TO, 1, true>)
                    : go(linrec_walk_bwd_kernel<T, TO, 1, false>);
     } else {
-        if (pairs) gated ? go(linrec_walk_kernel<T, TO, 2, true>)
-                         : go(linrec_walk_kernel<T, TO, 2, false>);
-        else gated ? go(linrec_walk_kernel<T, TO, 1, true>)
-                   : go(linrec_walk_kernel<T, TO, 1, false>);
+        auto by = [&](auto ahead) {
+            constexpr int A = decltype(ahead)::value;
+            if (pairs) gated ? go(linrec_walk_kernel<T, TO, 2, A, true>)
+                             : go(linrec_walk_kernel<T, TO, 2, A, false>);
+            else gated ? go(linrec_walk_kernel<T, TO, 1, A, true>)
+                       : go(linrec_walk_kernel<T, TO, 1, A, false>);
+        };
+        if (a.seqlen == 1) by(std::integral_constant<int, 1>{});
+        else by(std::integral_constant<int, kWalkAhead>{});
     }
     return cudaGetLastError() == cudaSuccess;
 }
