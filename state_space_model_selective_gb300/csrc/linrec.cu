@@ -83,7 +83,6 @@ struct LinArgs {
     uint32_t cblocks_inv;        // 2^32 / cblocks, rounded up
     uint32_t spin_limit;
     int drop_first_publish;
-    int vec_out;              // dim even: two channels in one store
     int keep_status;          // the status word holds an earlier scan's result to keep
 };
 
@@ -135,20 +134,15 @@ template <> struct Pair<float> {
     __device__ static void put(void* p, float2 v) { *static_cast<float2*>(p) = v; }
 };
 
-// two channels of a row in global memory, the second only where it exists
-template <typename T>
-__device__ __forceinline__ void put2(void* base, size_t i, float2 v, bool both, bool vec) {
-    T* p = static_cast<T*>(base) + i;
-    if (vec && both) {
-        Pair<T>::put(p, v);
-    } else {
-        p[0] = from_f32<T>(v.x);
-        if (both) p[1] = from_f32<T>(v.y);
-    }
-}
-
+// a lane's two channels of a state, APART elements apart, the second only where it exists
+template <int APART>
 __device__ __forceinline__ float2 load_state2(const float* p, size_t i, bool both) {
-    return make_float2(p[i], both ? p[i + 1] : 0.0f);
+    return make_float2(p[i], both ? p[i + APART] : 0.0f);
+}
+template <int APART>
+__device__ __forceinline__ void store_state2(float* p, size_t i, float2 v, bool both) {
+    p[i] = v.x;
+    if (both) p[i + APART] = v.y;
 }
 
 // --------------------------------------------------------------- loading
@@ -170,10 +164,12 @@ __device__ __forceinline__ void copy_wait() {
 
 // Rows that are not 16-byte aligned: a tile's row is copied from the 16-byte boundary
 // before it, in 16-byte pieces (16 bytes with their part of the row are
-// always memory of the tensor's own), and lies in shared memory at the offset
-// it has from that boundary.  (4-byte copies took 99 us, element loads 324 us for the
-// forward of batch 8, 2048 steps, 1500 and 1501 channels of bf16 with a gate, against
-// 85 us and 89 us.)
+// always memory of the tensor's own).  From a row to the next its start moves by d, the
+// stride's bytes mod 16, against the boundaries; rows lie kShiftedRow + d apart, so that
+// pieces stay on boundaries and a step's address is linear in it.  A lane has channels
+// lane and lane + 32: neighbours would straddle words.  (4-byte copies took 99 us, element
+// loads 324 us for the forward of batch 8, 2048 steps, 1500 and 1501 channels of bf16 with
+// a gate; rows kShiftedRow apart and neighbouring channels 88 us; this 82 us.)
 template <typename T>
 constexpr int kShiftedRow = kCh * (int)sizeof(T) + 16;
 template <typename T>
@@ -187,17 +183,18 @@ __device__ __forceinline__ uint32_t shift_of(const void* base, long long at, int
 template <typename T, int STEPS, int THREADS>
 __device__ __forceinline__ void load_shifted(void* dst, const void* src, long long stride, int b,
                                              int t0, int c0, int seqlen, int dim) {
-    const long long first = (long long)b * seqlen * stride + c0;
+    const uintptr_t first = reinterpret_cast<uintptr_t>(src) +
+                            (((long long)b * seqlen + t0) * stride + c0) * (long long)sizeof(T);
     const uint32_t bytes = min(kCh, dim - c0) * (int)sizeof(T);
     // THREADS / STEPS neighbouring threads to a row, every so many-th piece each
     constexpr int PER = THREADS / STEPS;
     const int r = threadIdx.x / PER, q = threadIdx.x % PER;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(src) +
-                         (first + (long long)(t0 + r) * stride) * (long long)sizeof(T);
+    const uintptr_t at = first + r * stride * (long long)sizeof(T);
     const uintptr_t from = at & ~uintptr_t(15);
     // bytes behind the boundary, none past the sequence
     const int end = t0 + r < seqlen ? (int)((uint32_t)(at & 15) + bytes) : 0;
-    const uint32_t to = smem_u32(static_cast<uint8_t*>(dst) + r * kShiftedRow<T>);
+    const uint32_t d = (uint32_t)(stride * (long long)sizeof(T)) & 15;
+    const uint32_t to = smem_u32(dst) + r * kShiftedRow<T> + (((uint32_t)(first & 15) + r * d) & ~15u);
 #pragma unroll
     for (int j0 = 0; j0 < kPieces<T>; j0 += PER) {
         const int j = j0 + q, n = max(0, min(16, end - j * 16));
@@ -206,30 +203,27 @@ __device__ __forceinline__ void load_shifted(void* dst, const void* src, long lo
     }
 }
 
-// two neighbouring channels at a byte offset that is a multiple of the element's size
+// channels lane and lane + 32 of a row
 template <typename T>
-__device__ __forceinline__ float2 get_shifted(const uint8_t* row, uint32_t off) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (off >> 2);
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t v = __funnelshift_r(w[0], w[1], (off & 2) * 8);
-        return make_float2(bf16lo(v), bf16hi(v));
-    } else {
-        return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-    }
+__device__ __forceinline__ float2 get_shifted(const uint8_t* at) {
+    const T* p = reinterpret_cast<const T*>(at);
+    return make_float2(to_f32(p[0]), to_f32(p[32]));
 }
 template <typename T>
-__device__ __forceinline__ void put_shifted(uint8_t* row, uint32_t off, float2 v) {
-    T* p = reinterpret_cast<T*>(row + off);
+__device__ __forceinline__ void put_shifted(uint8_t* at, float2 v) {
+    T* p = reinterpret_cast<T*>(at);
     p[0] = from_f32<T>(v.x);
-    p[1] = from_f32<T>(v.y);
+    p[32] = from_f32<T>(v.y);
 }
 
-// A warp's `rows` rows (of S) of results out of shared memory (row r at its own offset behind
-// the 16-byte boundary before its place): whole 16 bytes where they are the row's, else
+// A warp's `rows` rows (of S) of results out of shared memory (row r in the place of an
+// input's row, whose start moved by `d` from `shift`, at its own offset behind the 16-byte
+// boundary before its place in memory): whole 16 bytes where they are the row's, else
 // element by element.
 template <typename T, int S>
-__device__ __forceinline__ void send_shifted(const uint8_t* smem, void* out, size_t first, int dim,
-                                             int rows, int channels, int lane) {
+__device__ __forceinline__ void send_shifted(const uint8_t* smem, uint32_t shift, uint32_t d,
+                                             void* out, size_t first, int dim, int rows,
+                                             int channels, int lane) {
     // 32 / S neighbouring lanes to a row: its whole pieces, then the elements before
     // the first and after the last
     constexpr int PER = 32 / S, ES = (int)sizeof(T), kEdge = 16 / ES;
@@ -238,7 +232,7 @@ __device__ __forceinline__ void send_shifted(const uint8_t* smem, void* out, siz
     uint8_t* p = reinterpret_cast<uint8_t*>(static_cast<T*>(out) + first + (size_t)r * dim);
     const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), end = off + channels * ES;
     p -= off;
-    const uint8_t* s = smem + r * kShiftedRow<T>;
+    const uint8_t* s = smem + r * kShiftedRow<T> + ((shift + r * d) & ~15u);
 #pragma unroll
     for (int j0 = 0; j0 < kPieces<T>; j0 += PER) {
         const int j = (j0 + q) * 16;
@@ -454,7 +448,7 @@ __host__ __device__ constexpr int tile_steps(bool grad, bool tma) {
 template <typename T, int NIN, bool GRAD, bool TMA>
 struct LinSmem {
     static constexpr int kRow = TMA ? kCh * (int)sizeof(T) : kShiftedRow<T>;
-    static constexpr int kTile = tile_steps(GRAD, TMA) * kRow;  // of one input
+    static constexpr int kTile = tile_steps(GRAD, TMA) * (kRow + (TMA ? 0 : 16));  // of one input
     static constexpr int kStage = NIN * kTile;
 };
 
@@ -469,6 +463,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
     // where rows are shifted, by their warps
     constexpr bool STAGED = sizeof(T) == sizeof(TO), INPLACE = TMA && STAGED;
     using SM = LinSmem<T, NIN, GRAD, TMA>;
+    constexpr int APART = TMA ? 1 : 32;  // a lane's channels are neighbours, or not
     extern __shared__ __align__(1024) uint8_t smem[];
     // the warps' (P, q), gradient also the reverse q; each q is replaced by that of
     // all that stands before its warp in the scan's order (for the gradient's q: in
@@ -587,50 +582,65 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         const int seq = cur.seq, blk = cur.blk;
         int tile, b, c;
         where(cur, tile, b, c);
-        c += lane * 2;
-        const bool valid = c < a.dim, two = c + 1 < a.dim;
+        const int c0 = c;
+        c += lane * (TMA ? 2 : 1);
+        const bool valid = c < a.dim, two = c + APART < a.dim;
         const size_t chan = (size_t)b * a.dim + c;
         const int t0 = tile * STEPS + warp * S;
-        // the warp's first row; aligned rows: this lane's channels of it
-        uint8_t* base = smem + stage * SM::kStage + warp * S * SM::kRow +
-                        (TMA ? lane * 2 * (int)sizeof(T) : 0);
+        // aligned rows: this lane's channels of the warp's first row
+        uint8_t* base = smem + stage * SM::kStage +
+                        (TMA ? warp * S * SM::kRow + lane * 2 * (int)sizeof(T) : 0);
         const long long row0 = (long long)b * a.seqlen + t0;
-        // where the warp's first row starts behind its 16-byte boundary, and how far that
-        // moves from a row to the next
-        uint32_t sh_in[NIN], d_in[NIN], sh_out[3] = {}, d_out = 0;
+        // shifted rows: the same of each input, the distance of its rows, where the warp's
+        // first row starts behind its 16-byte boundary, and how far that moves from a row
+        // to the next
+        uint32_t in_at[NIN], in_row[NIN], sh_in[NIN], d_in[NIN], sh_out[3] = {}, d_out = 0;
         if constexpr (!TMA) {
 #pragma unroll
             for (int i = 0; i < NIN; ++i) {
-                sh_in[i] = shift_of(a.in[i], row0 * a.stride[i] + c - lane * 2, sizeof(T));
                 d_in[i] = (uint32_t)(a.stride[i] * (long long)sizeof(T)) & 15;
+                in_row[i] = SM::kRow + d_in[i];
+                // of the tile's first row, then of the warp's
+                sh_in[i] = shift_of(a.in[i], (row0 - warp * S) * a.stride[i] + c0, sizeof(T)) +
+                           warp * S * d_in[i];
+                in_at[i] = i * SM::kTile + warp * S * SM::kRow + sh_in[i] + lane * (int)sizeof(T);
             }
 #pragma unroll
             for (int i = 0; i < (GRAD ? (GATED ? 3 : 2) : 1); ++i)
-                sh_out[i] = shift_of(a.out[i], row0 * a.dim + c - lane * 2, sizeof(TO));
+                sh_out[i] = shift_of(a.out[i], row0 * a.dim + c0, sizeof(TO));
             d_out = (uint32_t)a.dim * (uint32_t)sizeof(TO) & 15;
         }
         // this lane's two channels of input i at the warp's step k
         auto get = [&](int i, int k) -> float2 {
-            const uint8_t* row = base + i * SM::kTile + k * SM::kRow;
-            if constexpr (TMA) return Pair<T>::get(row);
-            else return get_shifted<T>(row, ((sh_in[i] + k * d_in[i]) & 15) + lane * 2 * sizeof(T));
+            if constexpr (TMA) return Pair<T>::get(base + i * SM::kTile + k * SM::kRow);
+            else return get_shifted<T>(base + in_at[i] + k * in_row[i]);
         };
         // a result into the place of input i (shifted rows: at its own offset there)
         const size_t o = (size_t)row0 * a.dim + c;
         auto put = [&](int i, int k, int result, float2 v) {
-            uint8_t* row = base + i * SM::kTile + k * SM::kRow;
-            if constexpr (INPLACE)
-                Pair<TO>::put(row, v);
-            else if constexpr (STAGED)
-                put_shifted<TO>(row, ((sh_out[result] + k * d_out) & 15) + lane * 2 * sizeof(TO), v);
-            else if (valid && t0 + k < a.seqlen)
-                put2<TO>(a.out[result], o + (size_t)k * a.dim, v, two, a.vec_out);
+            if constexpr (INPLACE) {
+                Pair<TO>::put(base + i * SM::kTile + k * SM::kRow, v);
+            } else if constexpr (STAGED) {
+                put_shifted<TO>(base + i * SM::kTile + (warp * S + k) * SM::kRow +
+                                    ((sh_in[i] + k * d_in[i]) & ~15u) +
+                                    ((sh_out[result] + k * d_out) & 15) + lane * (int)sizeof(TO),
+                                v);
+            } else if (valid && t0 + k < a.seqlen) {
+                TO* p = static_cast<TO*>(a.out[result]) + o + (size_t)k * a.dim;
+                if constexpr (TMA) {
+                    Pair<TO>::put(p, v);
+                } else {
+                    p[0] = from_f32<TO>(v.x);
+                    if (two) p[APART] = from_f32<TO>(v.y);
+                }
+            }
         };
         auto send_rows = [&](int i, int result) {
             if constexpr (!TMA && STAGED) {
                 __syncwarp();
-                send_shifted<TO, S>(base + i * SM::kTile, a.out[result], o - lane * 2, a.dim,
-                                 min(S, a.seqlen - t0), min(kCh, a.dim - (c - lane * 2)), lane);
+                send_shifted<TO, S>(base + i * SM::kTile + warp * S * SM::kRow, sh_in[i], d_in[i],
+                                    a.out[result], o - lane, a.dim, min(S, a.seqlen - t0),
+                                    min(kCh, a.dim - c0), lane);
             }
         };
 
@@ -639,9 +649,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         if constexpr (GRAD) {
             if (valid) {
                 if (tile > 0)
-                    hk = load_state2(a.keep + (size_t)tile * a.batch * a.dim, chan, two);
+                    hk = load_state2<APART>(a.keep + (size_t)tile * a.batch * a.dim, chan, two);
                 else if (a.first)
-                    hk = load_state2(a.first, chan, two);
+                    hk = load_state2<APART>(a.first, chan, two);
             }
         }
 
@@ -712,9 +722,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
         s_q[warp][lane] = q;
         __syncthreads();
 
-        if (copies) {
-            if constexpr (INPLACE) bulk_wait_read_all();
-            fetch(ahead, last_stage);
+        if constexpr (TMA) {
+            if (copies) {
+                if constexpr (INPLACE) bulk_wait_read_all();
+                fetch(ahead, last_stage);
+            }
         }
 
         // ---- across warps and tiles: the state (gradient: mu) entering this one
@@ -744,8 +756,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 fP = mul2(fP, p);
             }
         }
+        // every thread's copies: once the aggregate is out (before it: 84 us for the 82 us
+        // above)
+        if constexpr (!TMA) fetch(ahead, last_stage);
         if (seq == 0) {
-            if (a.h0 && valid) in = load_state2(a.h0, chan, two);
+            if (a.h0 && valid) in = load_state2<APART>(a.h0, chan, two);
             __syncthreads();
         } else {
             while (true) {
@@ -776,8 +791,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             if (seq < a.tiles - 1) {
                 if (!(a.drop_first_publish && seq == 0)) put_inc(a.inc + mine, end);
             } else if (a.last && valid) {
-                a.last[chan] = end.x;
-                if (two) a.last[chan + 1] = end.y;
+                store_state2<APART>(a.last, chan, end, two);
             }
         }
         in = Step<false>::next(s_preP[warp][lane], in, GRAD ? s_r[warp][lane] : s_q[warp][lane]);
@@ -787,8 +801,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             float2 h = in;
             if (a.keep && warp * S % kKeep == 0 && valid && t0 < a.seqlen) {
                 float* s = a.keep + (size_t)(t0 / kKeep) * a.batch * a.dim + chan;
-                s[0] = h.x;
-                if (two) s[1] = h.y;
+                store_state2<APART>(s, 0, h, two);
             }
             auto replay = [&](auto fast_) {
                 constexpr bool F = decltype(fast_)::value;
@@ -1223,7 +1236,6 @@ extern "C" ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void*
     a.stride[0] = f_stride; a.stride[1] = x_stride; a.stride[2] = z_stride;
     a.h0 = initial_state; a.last = final_state; a.keep = checkpoints; a.out[0] = y;
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
-    a.vec_out = dim % 2 == 0;
     ssm_internal::lookback_setting(&a.spin_limit, &a.drop_first_publish);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     place(a, ws, 1);
@@ -1285,7 +1297,6 @@ extern "C" ssm_status_t ssm_linrec_bwd(const void* f, const void* x, const void*
     a.in[0] = f; a.in[1] = x;
     a.stride[0] = f_stride; a.stride[1] = x_stride;
     a.batch = batch; a.seqlen = seqlen; a.dim = dim;
-    a.vec_out = dim % 2 == 0;
     ssm_internal::lookback_setting(&a.spin_limit, &a.drop_first_publish);
     if (!checkpoints && seqlen > kWalkSteps) {  // walked ones are short enough to keep them
         // the forward again, states only
