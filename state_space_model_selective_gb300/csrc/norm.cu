@@ -81,8 +81,7 @@ __device__ __forceinline__ Chunk chunk_at(int c, int shift, int dim, bool valid)
 
 // 16 bytes read once, or zeros.  Volatile, so that the compiler leaves the next row's
 // loads before this row's barrier instead of moving them to where they save registers
-// (a few percent of forward and
-// gradient of 16384 rows of 5120).
+// (a few percent of forward and gradient of 16384 rows of 5120).
 __device__ __forceinline__ uint4 load16(const void* p, bool in) {
     uint4 v;
     asm volatile(
@@ -574,29 +573,31 @@ __global__ void __launch_bounds__(SMALL ? 256 : ALIGNED ? 512 : 544)
     }
 }
 
-// dw[c] = sum of the CTAs' partial[i][c] in a fixed order: 8 warps take every
-// eighth partial row, then warp 0 adds the 8 sums.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int parts, int dim,
-                                                      float* dw) {
-    __shared__ float acc[8][32];
+// dw[c] = sum of the CTAs' partial[i][c] in a fixed order: each warp takes every 32nd
+// partial row, ten of them (a GB300's grid) in flight, then warp 0 adds the warps' sums.
+constexpr int kDwWarps = 32, kDwAhead = 10;
+
+__global__ void __launch_bounds__(kDwWarps * 32) norm_dw_kernel(const float* partial, int parts,
+                                                               int dim, float* dw) {
+    __shared__ float acc[kDwWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float t = 0.0f;
     if (c < dim) {
-        for (int i = warp; i < parts; i += 64) {  // eight loads at a time
-            float v[8];
+        for (int i = warp; i < parts; i += kDwWarps * kDwAhead) {
+            float v[kDwAhead];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = partial[(size_t)min(i + 8 * k, parts - 1) * dim + c];
+            for (int k = 0; k < kDwAhead; ++k)
+                v[k] = i + kDwWarps * k < parts ? partial[(size_t)(i + kDwWarps * k) * dim + c] : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t += i + 8 * k < parts ? v[k] : 0.0f;
+            for (int k = 0; k < kDwAhead; ++k) t += v[k];
         }
     }
     acc[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < dim) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += acc[i][lane];
+        for (int i = 1; i < kDwWarps; ++i) t += acc[i][lane];
         dw[c] = t;
     }
 }
@@ -823,6 +824,6 @@ extern "C" ssm_status_t ssm_add_rmsnorm_bwd(const void* sum, const float* weight
         else vec ? go(norm_bwd_kernel<TX, TR, TY, 4, true, false, false>)
                  : go(norm_bwd_kernel<TX, TR, TY, 4, false, false, false>);
     });
-    norm_dw_kernel<<<(dim + 31) / 32, 256, 0, s>>>(a.partial, (int)grid, dim, dweight);
+    norm_dw_kernel<<<(dim + 31) / 32, kDwWarps * 32, 0, s>>>(a.partial, (int)grid, dim, dweight);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
