@@ -125,6 +125,22 @@ def test_slices_of_one_projection(n, dim, dtype):
         _check(d, dev)
 
 
+@pytest.mark.parametrize("pad", [0, 1, 7])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_rows_that_move_against_alignment(pad, dtype, out):
+    """Several tiles of several channel blocks in every direction, where inputs (ranges of
+    a padded projection) and outputs step by different bytes against 16-byte boundaries."""
+    for dim, gated in ((131, True), (201, False)):
+        d = _inputs(2, 333, dim, dtype, dim + pad, gated)
+        order = "fxz" if gated else "xf"
+        packed = torch.cat([torch.zeros(2, 333, pad, dtype=dtype)] + [d[k] for k in order],
+                           -1).cuda()
+        dev = _dev(d)
+        for i, k in enumerate(order):
+            dev[k] = packed[..., pad + i * dim:pad + (i + 1) * dim]
+        _check(d, dev, out, out)
+
+
 @pytest.mark.parametrize("n", [12, 300])
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_masked_steps(n, dtype):
