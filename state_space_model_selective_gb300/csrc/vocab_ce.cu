@@ -610,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Up to 64 tokens the loss is bound by reading W once, and the pair's 256 rows of
 // tokens would be mostly empty (8 tokens of dim 1536, vocabulary 50280: 49 us with
-// them, 33 us here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
+// them, 31 us here; a read of W at the card's copy rate: 23 us).  Here the vocabulary
 // is the MMA's rows and the tokens its columns: each CTA takes one contiguous,
 // evenly cut range of the vocabulary in 128-row tiles (the last one as many rows as
 // are left, in boxes of 64 and 16, so that no CTA reads more than 15 rows beyond its
@@ -648,7 +648,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int ntiles = (r1 - r0 + 127) / 128, depth = (a.dim + kDepth - 1) / kDepth;
     constexpr uint32_t kCols = 2 * N < 32 ? 32 : 2 * N;
 
-    if (tid == 0) {
+    // the n-th stage's loads: tile t's depths from kb on
+    uint32_t n = 0;
+    int t = 0, kb = 0;
+    auto load_next = [&] {
+        const uint32_t s = n % kFewStages;
+        const int row = r0 + t * 128, rows = min(128, (r1 - row + 15) / 16 * 16);
+        uint8_t* W = smem_raw + (smem - smem_u32(smem_raw)) + s * few_stage<N>();
+        mbar_arrive_expect_tx(&full[s], (rows + N) * 128);
+        if (rows == 128) {
+            tma_load_2d(W, &tm_W128, &full[s], kb * kDepth, row);
+        } else {
+            int j = 0;
+            if (rows >= 64) {
+                tma_load_2d(W, &tm_W64, &full[s], kb * kDepth, row);
+                j = 64;
+            }
+            for (; j < rows; j += 16)
+                tma_load_2d(W + j * 128, &tm_W16, &full[s], kb * kDepth, row + j);
+        }
+        tma_load_2d(W + kFewW, &tm_h, &full[s], kb * kDepth, 0);
+        ++n;
+        if (++kb == depth) {
+            kb = 0;
+            ++t;
+        }
+    };
+    if (warp == 4 && lane == 0) {
         s_failed = 0;
         for (uint32_t i = 0; i < kFewStages; ++i) {
             mbar_init(&full[i], 1);
@@ -659,6 +685,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mbar_init(&acc_empty[i], 4);
         }
         fence_mbar_init();
+        // the ring's first filling does not wait for the other warps' preparations (with
+        // the join's reads all at its start: 33 us became 31 us)
+        while (t < ntiles && n < kFewStages) load_next();
     }
     for (int i = tid; i < N; i += kFewThreads) {
         const long long t = i < a.tokens ? a.targets[i] : -1;
@@ -681,28 +710,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 4) {
         if (lane == 0) {
-            uint32_t n = 0;
-            for (int t = 0; ok && t < ntiles; ++t) {
-                const int row = r0 + t * 128, rows = min(128, (r1 - row + 15) / 16 * 16);
-                for (int kb = 0; kb < depth; ++kb, ++n) {
-                    const uint32_t s = n % kFewStages;
-                    ok = mbar_wait(&empty[s], ((n / kFewStages) & 1) ^ 1, nullptr);
-                    if (!ok) break;
-                    uint8_t* W = smem_raw + (smem - smem_u32(smem_raw)) + s * few_stage<N>();
-                    mbar_arrive_expect_tx(&full[s], (rows + N) * 128);
-                    if (rows == 128) {
-                        tma_load_2d(W, &tm_W128, &full[s], kb * kDepth, row);
-                    } else {
-                        int j = 0;
-                        if (rows >= 64) {
-                            tma_load_2d(W, &tm_W64, &full[s], kb * kDepth, row);
-                            j = 64;
-                        }
-                        for (; j < rows; j += 16)
-                            tma_load_2d(W + j * 128, &tm_W16, &full[s], kb * kDepth, row + j);
-                    }
-                    tma_load_2d(W + kFewW, &tm_h, &full[s], kb * kDepth, 0);
-                }
+            while (t < ntiles) {
+                ok = mbar_wait(&empty[n % kFewStages], ((n / kFewStages) & 1) ^ 1, nullptr);
+                if (!ok) break;
+                load_next();
             }
             for (uint32_t q = n > kFewStages ? n - kFewStages : 0; ok && q < n; ++q)
                 ok = mbar_wait(&empty[q % kFewStages], (q / kFewStages) & 1, nullptr);
@@ -830,14 +841,16 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
     const int row = blockIdx.x * kJoinRows + r;
+    // what a row's warp needs at the end is read here, so that reads wait only once
+    const int mine = blockIdx.x * kJoinRows + warp;
+    const bool last = warp < kJoinRows && lane == 0 && mine < tokens;
+    const long long at = last ? targets[mine] : -1;
     // launched beside the loss kernel's end: wait for all it wrote
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0) {
-        uint32_t f = 0;
+    const float logit = at >= 0 && at < vocab ? target_logit[mine] : 0.0f;
+    uint32_t f = 0;
+    if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < nctas; i += 1024) f |= failed[i];
-        f = __syncthreads_or((int)f);
-        if (threadIdx.x == 0) *status = f ? SSM_ERR_TIMEOUT : SSM_OK;
-    }
     float m = -INFINITY, s = 0.0f;
     auto join = [&](float2 p) {
         const float n = fmaxf(m, p.x), base = n == -INFINITY ? 0.0f : n;
@@ -857,7 +870,8 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
         }
     }
     sh[q][r] = make_float2(m, s);
-    __syncthreads();
+    f = __syncthreads_or((int)f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = f ? SSM_ERR_TIMEOUT : SSM_OK;
     if (warp < kJoinRows) {
         m = -INFINITY;
         s = 0.0f;
@@ -869,12 +883,10 @@ __global__ void __launch_bounds__(1024) ce_join_kernel(const float2* parts, int 
         float t = s * ex2_approx(m - (mx == -INFINITY ? 0.0f : mx));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        const int w = blockIdx.x * kJoinRows + warp;
-        if (lane == 0 && w < tokens) {
+        if (last) {
             const float l = fmaf(mx, 0.6931471805599453f, logf(t));
-            lse[w] = l;
-            const long long at = targets[w];
-            loss[w] = at < 0 ? 0.0f : at < vocab ? l - target_logit[w] : NAN;
+            lse[mine] = l;
+            loss[mine] = at < 0 ? 0.0f : at < vocab ? l - logit : NAN;
         }
     }
 }
