@@ -42,7 +42,8 @@
 //
 // Masked steps: a gate of +inf holds the state whatever x is there (b_t = 0 where
 // 1 - a_t = 0), a gate of -inf restarts it whatever it was (a_t = 0 drops h, NaN
-// and infinities too); their gradients are 0.
+// and infinities too); their gradients are 0.  A span's decay is 0 only where one of its
+// gates is.
 #include <algorithm>
 #include <type_traits>
 
@@ -376,6 +377,21 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+// The decay of a span of steps, the product of their gates, is 0 only where one of them
+// restarts the state.  A product that fell below every number counts as the least one, so
+// that a NaN or an infinity outlasts the span as it outlasts each step; a finite state h is
+// off by at most 2^-149 |h|.  While it grows, -0 says that a gate was 0.
+__device__ __forceinline__ float2 longer_span(float2 product, float2 a) {
+    const float2 p = mul2(product, a);
+    return make_float2(a.x == 0.0f ? -0.0f : p.x, a.y == 0.0f ? -0.0f : p.y);
+}
+__device__ __forceinline__ float span_decay(float product) {
+    return __float_as_int(product) < 0 ? 0.0f : fmaxf(product, __int_as_float(1));
+}
+__device__ __forceinline__ float2 span_decay(float2 product) {
+    return make_float2(span_decay(product.x), span_decay(product.y));
+}
+
 // sigmoid(v) and the t = e^-v it comes from, for |v| < 80 or where an infinite t
 // gives the right 0
 __device__ __forceinline__ float2 sigmoid2(float2 v, float2& t) {
@@ -696,8 +712,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 const float2 bt = Step<F>::input(om, x);
                 gb[k] = GRAD ? om : bt;
                 q = Step<F>::next(ga[k], q, bt);
-                P = mul2(P, ga[k]);
+                P = F ? mul2(P, ga[k]) : longer_span(P, ga[k]);
             }
+            P = span_decay(P);
             if constexpr (GRAD) {
                 // mu through the steps: dh_t = dy_t silu(z_t), 0 past the sequence
                 // (the tile is zero there)
@@ -739,10 +756,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 float2& q_ = GRAD ? s_r[w][lane] : s_q[w][lane];
                 const float2 own = q_, p = s_P[w][lane];
                 q_ = tq;
-                s_preP[w][lane] = TP;
+                s_preP[w][lane] = span_decay(TP);
                 tq = Step<false>::next(p, tq, own);
-                TP = mul2(TP, p);
+                TP = longer_span(TP, p);
             }
+            TP = span_decay(TP);
             // the first tile has its state at once, the last one's is nobody's to read
             if (seq > 0 && seq < a.tiles - 1) put_agg(a.agg + mine, TP, tq);
         } else if (GRAD && warp == 1) {
@@ -751,9 +769,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             for (int w = 0; w < WARPS; ++w) {
                 const float2 own = s_q[w][lane], p = s_P[w][lane];
                 s_q[w][lane] = fq;
-                s_timeP[w][lane] = fP;
+                s_timeP[w][lane] = span_decay(fP);
                 fq = Step<false>::next(p, fq, own);
-                fP = mul2(fP, p);
+                fP = longer_span(fP, p);
             }
         }
         // every thread's copies: once the aggregate is out (before it: 84 us for the 82 us

@@ -320,3 +320,37 @@ def test_writes_stay_inside_the_outputs(n, dim, dtype):
         assert not t.isnan().any(), k
     for k, v in before.items():
         assert torch.equal(d[k], v), k
+
+
+@pytest.mark.parametrize("n", [12, 300, 1500])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_what_is_not_finite_outlasts_a_span_that_forgets(n, dtype):
+    """Gates around sigmoid(-1.5), so that the product of a tile's gates lies below every
+    fp32 number, but none that restarts the state: NaN and infinities in x, in the
+    initial state, in dy and in dfinal_state stay to the sequence's end (or its start), as
+    they do step by step; a restart behind one ends it."""
+    for dim in (70, 64):
+        d = _inputs(4, n, dim, dtype, n + dim)
+        d["f"] = (-1.5 + 0.3 * (d["f"].float() - 2)).to(dtype)
+        d["x"][0, 5, 3], d["x"][1, 6, 9], d["x"][1, 6, 10] = float("nan"), float("inf"), -float("inf")
+        d["x"][0, 5, 40], d["f"][0, n // 2, 40] = float("nan"), float("-inf")
+        d["h0"][2, 4], d["h0"][2, 5], d["h0"][2, 41] = float("inf"), float("nan"), -float("inf")
+        d["f"][2, n // 2, 41] = float("-inf")
+        d["dy"][3, n - 3, 20] = float("nan")
+        d["dfin"][3, 7], d["dfin"][3, 8] = float("nan"), float("inf")
+        dev, r = _dev(d), _n64(d)
+        kept = torch.empty(binding.ssm_linrec_checkpoint_bytes(4, n, dim) // 4, device="cuda")
+        y, fin = binding.ssm_linrec_fwd(dev["f"], dev["x"], dev["z"], initial_state=dev["h0"],
+                                        checkpoints=kept)
+        y_ref, fin_ref, _ = P.linrec_fwd(r["f"], r["x"], r["z"], r["h0"])
+        assert np.isnan(fin_ref[0, 3]) and np.isfinite(fin_ref[0, 40]) and fin_ref[2, 4] == np.inf
+        _near(fin, fin_ref, "final", 1e-5)
+        _near(y, y_ref, "y", 1e-5)
+        refs = P.linrec_bwd(r["f"], r["x"], r["dy"], r["z"], r["h0"], r["dfin"])
+        assert np.isnan(refs[3][3, 7]) and refs[3][3, 8] == np.inf and np.isnan(refs[3][3, 20])
+        for c in (kept, None):
+            g = binding.ssm_linrec_bwd(dev["f"], dev["x"], dev["dy"], dev["z"],
+                                       initial_state=dev["h0"], dfinal_state=dev["dfin"],
+                                       checkpoints=c)
+            for k, ref in zip(("df", "dx", "dz", "dinitial_state"), refs):
+                _near(g[k], ref, k, 2e-5)
