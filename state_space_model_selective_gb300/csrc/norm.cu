@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(SMALL ? 256 : ALIGNED ? 512 : 544)
             ss = lanes_sum(t.x, 32);
             sg = lanes_sum(t.y, 32);
         }
-        const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+        // a row past the last one is zeros: with eps 0 its r would be infinite and reach dw
+        const float r = !SMALL || row < a.rows ? rsqrtf(fmaf(ss, a.inv_dim, a.eps)) : 0.0f;
         const float c_ = sg * a.inv_dim * r * r;  // mean(g n) r, so that n mean(g n) = s c
 #pragma unroll
         for (int k = 0; k < NV; ++k) {

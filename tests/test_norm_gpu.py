@@ -162,3 +162,17 @@ def test_runs_are_bit_equal_and_on_another_stream():
     torch.cuda.synchronize()
     for g in again:
         assert torch.equal(g["dx"], first["dx"]) and torch.equal(g["dweight"], first["dweight"])
+
+
+@pytest.mark.parametrize("dim", [7, 64, 96, 128, 200, 520])
+@pytest.mark.parametrize("rows", [1, 3, 5, 33])
+def test_gradient_without_eps(dim, rows):
+    """eps = 0: rows of values are well defined, and what a warp holds in the place of rows
+    past the last one does not reach dweight."""
+    x, res, w, dy, ds = _inputs(rows, dim, F32, F32, rows + dim)
+    y, s = binding.ssm_add_rmsnorm_fwd(x.cuda(), w.cuda(), res.cuda(), eps=0.0)
+    _near(y, P.norm_fwd(to64(x), to64(res), to64(w), 0.0)[0], F32, "y")
+    g = binding.ssm_add_rmsnorm_bwd(dy.cuda(), s, w.cuda(), dsum=ds.cuda(), eps=0.0)
+    dx_ref, dw_ref = P.norm_bwd(to64(s), to64(w), 0.0, to64(dy), to64(ds))
+    _near(g["dx"], dx_ref, F32, "dx")
+    _near(g["dweight"], dw_ref, F32, "dweight", 1e-5)
