@@ -27,7 +27,6 @@
 // same.  (Element-wise accesses took 34.8 us for 10000 rows of 1001, bf16 with 8-bit
 // output, against 23 us.)
 #include <algorithm>
-#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -225,12 +224,20 @@ __device__ __forceinline__ float lanes_max(float v, int width) {
     return v;
 }
 
-// amax -> 448 / amax, the factor q takes, within 2 ulp (an exact division costs as
-// much as the rest of the quantisation).  0 for a group of zeros, and for one whose
-// amax is infinite or NaN, where the factor leaves NaN in the places it came from;
-// kept finite so that a zero beside denormals stays zero.
-__device__ __forceinline__ float quant_factor(float amax) {
-    return amax > 0.0f ? fminf(kE4m3Max * rcp_approx(amax), FLT_MAX) : 0.0f;
+// 448 / amax, the factor q takes, within 2 ulp (an exact division costs as much as the rest
+// of the quantisation) for an amax within 2^-100 .. 2^100.
+__device__ __forceinline__ float quant_factor(float amax) { return kE4m3Max * rcp_approx(amax); }
+
+// Whether amax is outside of that, where it or the factor may have no normal reciprocal: one
+// comparison of the bits, which zeros, infinities and NaN fail too.
+__device__ __forceinline__ bool quant_far(float amax) {
+    constexpr uint32_t kLow = 0x0d800000u, kHigh = 0x71800000u;
+    return __float_as_uint(amax) - kLow > kHigh - kLow;
+}
+
+// The power of two by which such a group comes nearer before it is quantised.
+__device__ __forceinline__ float quant_nearer(float amax) {
+    return !quant_far(amax) ? 1.0f : amax < 1.0f ? 0x1p64f : 0x1p-64f;
 }
 
 __device__ __forceinline__ float quant_scale(float amax) { return amax * (1.0f / kE4m3Max); }
@@ -246,8 +253,8 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
     uint8_t* q = static_cast<uint8_t*>(a.y);
     constexpr bool small = SMALL;
     const int lanes = SMALL ? a.lanes : 32;
-    float factor[NV][2];  // of the chunk's group, and of the next one's where it spans two
-    int cut[NV];          // first element of that
+    float amax_of[NV][2];  // of the chunk's group, and of the next one's where it spans two
+    int cut[NV];           // first element of that
     if (a.group == 0) {
         float amax = 0.0f;
 #pragma unroll
@@ -263,7 +270,7 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
         if (wr == 0 && (lane & (lanes - 1)) == 0 && row < a.rows) a.scales[row] = quant_scale(amax);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            factor[k][0] = quant_factor(amax);
+            amax_of[k][0] = amax_of[k][1] = amax;
             cut[k] = 8;
         }
     } else if constexpr (ALIGNED) {
@@ -276,7 +283,7 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
             amax = lanes_max(amax, width);
             if ((lane & (width - 1)) == 0 && ks[k].any)
                 a.scales[row * a.ngroups + ks[k].i0 / a.group] = quant_scale(amax);
-            factor[k][0] = quant_factor(amax);
+            amax_of[k][0] = amax_of[k][1] = amax;
             cut[k] = 8;
         }
     } else {
@@ -314,20 +321,39 @@ __device__ __forceinline__ void quantise(const NormArgs& a, long long row, float
                 a.scales[row * a.ngroups + g] = quant_scale(__uint_as_float(s_amax[sub + g]));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            factor[k][0] = factor[k][1] = 0.0f;
+            amax_of[k][0] = amax_of[k][1] = 1.0f;
             if (ks[k].any) {
-                factor[k][0] = quant_factor(__uint_as_float(s_amax[sub + first[k]]));
+                amax_of[k][0] = __uint_as_float(s_amax[sub + first[k]]);
                 if (cut[k] < 8 && first[k] + 1 < a.ngroups)
-                    factor[k][1] = quant_factor(__uint_as_float(s_amax[sub + first[k] + 1]));
+                    amax_of[k][1] = __uint_as_float(s_amax[sub + first[k] + 1]);
             }
         }
         sync();  // before the next row's zeros
     }
+    bool far = false;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        far = far || quant_far(amax_of[k][0]) || (!ALIGNED && quant_far(amax_of[k][1]));
+    if (__builtin_expect(far, 0)) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[k][j] *= quant_nearer(ALIGNED || j < cut[k] ? amax_of[k][0] : amax_of[k][1]);
+            // factor 0 for a group of zeros, and for one whose amax is infinite or NaN, where
+            // it leaves NaN in the places that came from
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                amax_of[k][i] = amax_of[k][i] > 0.0f ? amax_of[k][i] * quant_nearer(amax_of[k][i])
+                                                     : INFINITY;
+        }
+    }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+        const float f0 = quant_factor(amax_of[k][0]);
+        const float f1 = ALIGNED ? f0 : quant_factor(amax_of[k][1]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[k][j] *= ALIGNED || j < cut[k] ? factor[k][0] : factor[k][1];
+        for (int j = 0; j < 8; ++j) v[k][j] *= ALIGNED || j < cut[k] ? f0 : f1;
         const uint2 w = make_uint2(e4m3x2(v[k][0], v[k][1]) | e4m3x2(v[k][2], v[k][3]) << 16,
                                    e4m3x2(v[k][4], v[k][5]) | e4m3x2(v[k][6], v[k][7]) << 16);
         uint8_t* p = q + base + ks[k].i0;

@@ -176,3 +176,24 @@ def test_gradient_without_eps(dim, rows):
     dx_ref, dw_ref = P.norm_bwd(to64(s), to64(w), 0.0, to64(dy), to64(ds))
     _near(g["dx"], dx_ref, F32, "dx")
     _near(g["dweight"], dw_ref, F32, "dweight", 1e-5)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("dim", [40, 300, 512, 9001])
+@pytest.mark.parametrize("exponent", [127, 126, 119, 60, -60, -119, -121, -125, -140])
+def test_e4m3_of_extreme_groups(dim, group, exponent):
+    """Groups whose largest magnitude is near either end of fp32's range are scaled like any:
+    q = e4m3(y * (448 / amax)) for every amax.  y itself is rounded to a multiple of 2^-149
+    down there, which q may show, and so may the scale."""
+    g = torch.Generator().manual_seed(dim + group)
+    x = torch.where(torch.rand(5, dim, generator=g) < 0.5, -1.0, 1.0)  # y = x * w
+    w = ((2 * torch.rand(dim, generator=g).double() - 1) * 1.9 * 2.0 ** exponent).float()
+    q, scales, _ = binding.ssm_add_rmsnorm_e4m3_fwd(x.cuda(), w.cuda(), eps=0.0, group=group)
+    y_ref, _ = P.norm_fwd(to64(x), None, to64(w), 0.0)
+    amax = P.group_amax(y_ref, group)
+    np.testing.assert_allclose(to64(scales), amax / 448.0, rtol=4e-6, atol=2.0 ** -148)
+    full = np.repeat(amax, group or dim, 1)[:, :dim]
+    v = y_ref * (448.0 / full)
+    off = 1e-5 * np.abs(v) + 2 * 448.0 * 2.0 ** -149 / full
+    got = to64(q.float())
+    assert np.all((got >= P.e4m3_round(v - off)) & (got <= P.e4m3_round(v + off)))
