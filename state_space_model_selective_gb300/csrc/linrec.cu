@@ -305,7 +305,8 @@ struct Look {
 template <int WARPS, int N>
 __device__ __forceinline__ bool look(const LinArgs& a, Look<WARPS, N>& s, int seq, int blk,
                                      int warp, int lane) {
-    const size_t step = (size_t)a.blocks * 32;
+    // (blocks reach past 2^26, of 32 entries each)
+    const size_t step = (size_t)a.blocks * 32, at = (size_t)blk * 32 + lane;
     const int first = seq - warp;  // tiles seq - warp, then WARPS - 1 further back
     uint32_t polls = 0;
     bool done[N];
@@ -322,7 +323,7 @@ __device__ __forceinline__ bool look(const LinArgs& a, Look<WARPS, N>& s, int se
         for (int i = 0; i < N; ++i) {
             inc[i] = agg[i] = false;
             if (!done[i]) {
-                const size_t o = (size_t)(first - i * (WARPS - 1)) * step + blk * 32 + lane;
+                const size_t o = (size_t)(first - i * (WARPS - 1)) * step + at;
                 inc[i] = get_inc(a.inc + o, h[i]);
                 agg[i] = get_agg(a.agg + o, r[i]);
             }

@@ -354,3 +354,36 @@ def test_what_is_not_finite_outlasts_a_span_that_forgets(n, dtype):
                                        checkpoints=c)
             for k, ref in zip(("df", "dx", "dz", "dinitial_state"), refs):
                 _near(g[k], ref, k, 2e-5)
+
+
+def test_more_than_two_to_the_26_channel_blocks():
+    """Sequences of two tiles, so many that an entry's number in the work area passes 31
+    bits: the last ones' states come from their own first tiles, forwards and backwards."""
+    batch, n = 2 ** 26 + 64, 65
+    need = binding.ssm_linrec_bwd_workspace_bytes(batch, n, 1)
+    if torch.cuda.mem_get_info()[0] < need + 9 * batch * n * 2:
+        pytest.skip("needs about 180 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(16)
+
+    def randn(*shape, dtype=BF16):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=dtype)
+
+    f = randn(batch, n, 1).mul_(1.5).add_(2)
+    x, dy, h0 = randn(batch, n, 1), randn(batch, n, 1), randn(batch, 1, dtype=F32)
+    kept = torch.empty(binding.ssm_linrec_checkpoint_bytes(batch, n, 1) // 4, device="cuda")
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    y, fin = binding.ssm_linrec_fwd(f, x, initial_state=h0, checkpoints=kept, workspace=ws)
+    assert binding.ssm_last_device_status(ws) == OK
+    grads = binding.ssm_linrec_bwd(f, x, dy, initial_state=h0, checkpoints=kept, workspace=ws)
+    assert binding.ssm_last_device_status(ws) == OK
+    for at in (slice(0, 40), slice(2 ** 25 - 20, 2 ** 25 + 20), slice(2 ** 26 - 40, batch)):
+        c = [to64(t[at]) for t in (f, x, dy, h0)]
+        y_ref, fin_ref, _ = P.linrec_fwd(c[0], c[1], None, c[3])
+        _near(y[at], y_ref, "y", 1e-5)
+        _near(fin[at], fin_ref, "final", 1e-5)
+        refs = P.linrec_bwd(c[0], c[1], c[2], None, c[3])
+        for k, ref in zip(("df", "dx", "dz", "dinitial_state"), refs):
+            if ref is not None:
+                _near(grads[k][at], ref, k, 2e-5)
+    del f, x, dy, h0, kept, ws, y, fin, grads
+    torch.cuda.empty_cache()
