@@ -382,12 +382,13 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // restarts the state.  A product that fell below every number counts as the least one, so
 // that a NaN or an infinity outlasts the span as it outlasts each step; a finite state h is
 // off by at most 2^-149 |h|.  While it grows, -0 says that a gate was 0.
+constexpr float kLeast = 0x1p-149f;
 __device__ __forceinline__ float2 longer_span(float2 product, float2 a) {
     const float2 p = mul2(product, a);
     return make_float2(a.x == 0.0f ? -0.0f : p.x, a.y == 0.0f ? -0.0f : p.y);
 }
 __device__ __forceinline__ float span_decay(float product) {
-    return __float_as_int(product) < 0 ? 0.0f : fmaxf(product, __int_as_float(1));
+    return __float_as_int(product) < 0 ? 0.0f : fmaxf(product, kLeast);
 }
 __device__ __forceinline__ float2 span_decay(float2 product) {
     return make_float2(span_decay(product.x), span_decay(product.y));
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 q = Step<F>::next(ga[k], q, bt);
                 P = F ? mul2(P, ga[k]) : longer_span(P, ga[k]);
             }
-            P = span_decay(P);
+            P = F ? make_float2(fmaxf(P.x, kLeast), fmaxf(P.y, kLeast)) : span_decay(P);
             if constexpr (GRAD) {
                 // mu through the steps: dh_t = dy_t silu(z_t), 0 past the sequence
                 // (the tile is zero there)
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 float2& q_ = GRAD ? s_r[w][lane] : s_q[w][lane];
                 const float2 own = q_, p = s_P[w][lane];
                 q_ = tq;
-                s_preP[w][lane] = span_decay(TP);
+                s_preP[w][lane] = TP;
                 tq = Step<false>::next(p, tq, own);
                 TP = longer_span(TP, p);
             }
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
             for (int w = 0; w < WARPS; ++w) {
                 const float2 own = s_q[w][lane], p = s_P[w][lane];
                 s_q[w][lane] = fq;
-                s_timeP[w][lane] = span_decay(fP);
+                s_timeP[w][lane] = fP;
                 fq = Step<false>::next(p, fq, own);
                 fP = longer_span(fP, p);
             }
@@ -813,7 +814,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 store_state2<APART>(a.last, chan, end, two);
             }
         }
-        in = Step<false>::next(s_preP[warp][lane], in, GRAD ? s_r[warp][lane] : s_q[warp][lane]);
+        in = Step<false>::next(span_decay(s_preP[warp][lane]), in,
+                               GRAD ? s_r[warp][lane] : s_q[warp][lane]);
 
         // ---- the steps again from the warp's entry state
         if constexpr (!GRAD) {
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 send_rows(0, 0);
             }
         } else {
-            float2 mu = in, h = Step<false>::next(s_timeP[warp][lane], hk, s_q[warp][lane]);
+            float2 mu = in, h = Step<false>::next(span_decay(s_timeP[warp][lane]), hk, s_q[warp][lane]);
             auto replay = [&](auto fast_) {
                 constexpr bool F = decltype(fast_)::value;
                 float2 prev[S];  // h_{t-1}
