@@ -934,7 +934,8 @@ template <typename T, typename TO, int CPT, int AHEAD, bool GATED>
 __global__ void __launch_bounds__(kWalkThreads) linrec_walk_kernel(const LinArgs a) {
     const int per = a.dim / CPT;
     const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
-    if (i == 0 && a.status && !a.keep_status) *a.status = 0;
+    // nothing recorded: a gradient's tiles, which may follow, record over that word only
+    if (i == 0 && a.status && !a.keep_status) *a.status = kNotYet;
     if (i >= (long long)a.batch * per) return;
     const int b = (int)(i / per), c = (int)(i % per) * CPT;
     const long long chan = (long long)b * a.dim + c, row0 = (long long)b * a.seqlen;
@@ -972,7 +973,7 @@ template <typename T, typename TO, int CPT, bool GATED>
 __global__ void __launch_bounds__(kWalkThreads) linrec_walk_bwd_kernel(const LinArgs a) {
     const int per = a.dim / CPT;
     const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
-    if (i == 0 && !a.keep_status) *a.status = 0;
+    if (i == 0 && !a.keep_status) *a.status = kNotYet;
     if (i >= (long long)a.batch * per) return;
     const int b = (int)(i / per), c = (int)(i % per) * CPT;
     const long long chan = (long long)b * a.dim + c, row0 = (long long)b * a.seqlen;

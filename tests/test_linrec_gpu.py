@@ -387,3 +387,16 @@ def test_more_than_two_to_the_26_channel_blocks():
                 _near(grads[k][at], ref, k, 2e-5)
     del f, x, dy, h0, kept, ws, y, fin, grads
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n,dim", [(24, 262144), (300, 64), (9, 64)])
+def test_a_gradient_can_report_whatever_forward_it_ran(n, dim):
+    """A gradient without kept states runs its forward first (24 steps of many channels by
+    the walk) and keeps its status.  What both leave is the word over which a wait that runs
+    out is recorded, all ones, and it reads as OK."""
+    d = _dev(_inputs(1, n, dim, BF16, 17, gated=False, state=False))
+    ws = torch.zeros(binding.ssm_linrec_bwd_workspace_bytes(1, n, dim), dtype=torch.uint8,
+                     device="cuda")
+    binding.ssm_linrec_bwd(d["f"], d["x"], d["dy"], workspace=ws)
+    assert binding.ssm_last_device_status(ws) == OK
+    assert int(ws[:8].view(torch.int32)[1]) == -1
