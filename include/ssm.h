@@ -876,8 +876,8 @@ size_t ssm_vocab_ce_workspace_bytes(int tokens, int dim, int vocab);
  * Layouts: h (tokens, dim), W (vocab, dim) in in_dtype; targets (tokens,) 64-bit
  * integers; loss, lse (tokens,) fp32; workspace of ssm_vocab_ce_workspace_bytes,
  * whose status ssm_last_device_status reads.
- * Supported: in_dtype SSM_BF16; dim a multiple of 8; any tokens >= 0, vocab >= 1
- * (tokens * vocab below 6e13).  Runs are bit-equal.
+ * Supported: in_dtype SSM_BF16; dim a multiple of 8; any tokens >= 0, vocab >= 1, each of
+ * the three up to 2^30 (tokens * vocab below 6e13).  Runs are bit-equal.
  */
 ssm_status_t ssm_vocab_ce_fwd(const void* h, const void* W, const long long* targets, float* loss,
                               float* lse, int tokens, int dim, int vocab, ssm_dtype_t in_dtype,

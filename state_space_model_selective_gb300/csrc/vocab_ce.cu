@@ -971,8 +971,11 @@ Plan plan_grad(int tokens, int dim, int vocab) {
     return p;
 }
 
+// (all three are counted in ints, whole tiles, pieces and CTAs' shares too)
+constexpr int kMost = 1 << 30;
 bool sizes_fit(int tokens, int dim, int vocab) {
-    return dim % 8 == 0 && (double)tokens * vocab / (kTile * kTile) < 1e9;
+    return dim % 8 == 0 && tokens <= kMost && dim <= kMost && vocab <= kMost &&
+           (double)tokens * vocab / (kTile * kTile) < 1e9;
 }
 
 constexpr int kMaxCtas = 1024;  // room for their flags

@@ -207,3 +207,19 @@ def test_step_strides_of_slices():
     for bad in (big.transpose(0, 1), big[:, :, ::2], big[:, ::2], big[:, 1:], big[:, :, :1].expand(3, 5, 9)):
         with pytest.raises(ValueError):
             steps(bad)
+
+
+def test_vocab_ce_sizes_near_two_to_the_31(L):
+    """All three sizes are counted in ints: what would pass them once rounded up to tiles
+    or pieces is refused, before the workspace is looked at."""
+    most = 2 ** 31 - 1
+    for sizes in ({"tokens": most, "vocab": 1}, {"tokens": most - 255, "vocab": 1},
+                  {"tokens": 1, "vocab": most}, {"tokens": 2 ** 30 + 1, "vocab": 1},
+                  {"tokens": 1, "vocab": 1, "dim": 2 ** 31 - 8}):
+        sizes = {"dim": 8, **sizes}
+        assert ce(L, n=0, **sizes) == UNSUP and ce_bwd(L, n=0, **sizes) == UNSUP
+        three = sizes["tokens"], sizes["dim"], sizes["vocab"]
+        assert binding.ssm_vocab_ce_workspace_bytes(*three) == 0
+        assert binding.ssm_vocab_ce_bwd_workspace_bytes(*three) == 0
+    assert ce(L, tokens=2 ** 30, vocab=1, dim=8, n=0) == WS
+    assert ce(L, tokens=1, vocab=2 ** 30, dim=8, n=0) == WS
