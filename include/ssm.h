@@ -821,7 +821,8 @@ size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim);
  * f, x and z need only the alignment of their element; rows whose addresses are
  * multiples of 16 bytes move fastest.
  * Supported: any batch, seqlen, dim >= 0 with batch * ceil(dim / 64) *
- * ceil(seqlen / 64) < 2e9.  seqlen == 0 hands the state on.
+ * ceil(seqlen / 64) < 2e9, batch * dim < 2e9 and seqlen < 2^31 - 128.  seqlen == 0 hands
+ * the state on.
  * The sequence is cut into tiles chained by a decoupled look-back in the
  * workspace (sequences of up to 16 steps are walked by one thread per channel
  * pair, and need no workspace: it may be NULL); its bounded waits report through ssm_last_device_status.  The result

@@ -1019,6 +1019,8 @@ __global__ void __launch_bounds__(kWalkThreads) linrec_walk_bwd_kernel(const Lin
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
+constexpr int kMostSteps = 0x7fffffff - 2 * kKeep;
+
 int tiles_of(int seqlen, int steps) { return seqlen / steps + (seqlen % steps != 0); }
 
 // header, aggregates and inclusive states of `tiles` tiles
@@ -1029,8 +1031,10 @@ size_t scan_bytes(int batch, int dim, int tiles) {
 
 bool sizes_ok(int batch, int seqlen, int dim) { return batch >= 0 && seqlen >= 0 && dim >= 0; }
 
-// one int counts the tiles of all blocks
+// one int counts the tiles of all blocks, one a sequence's steps to the end of its last tile,
+// one the channels
 bool sizes_fit(int batch, int seqlen, int dim) {
+    if (seqlen > kMostSteps || dim > 2000000000) return false;
     const double blocks = (double)batch * ((dim + kCh - 1) / kCh);
     return blocks * tiles_of(seqlen, kKeep) < 2.0e9 && (double)batch * dim < 2.0e9;
 }

@@ -223,3 +223,16 @@ def test_vocab_ce_sizes_near_two_to_the_31(L):
         assert binding.ssm_vocab_ce_bwd_workspace_bytes(*three) == 0
     assert ce(L, tokens=2 ** 30, vocab=1, dim=8, n=0) == WS
     assert ce(L, tokens=1, vocab=2 ** 30, dim=8, n=0) == WS
+
+
+def test_linrec_sizes_near_two_to_the_31(L):
+    """The steps to the end of a sequence's last tile are counted in an int: sequences whose
+    last tile would pass it are refused, before the workspace is looked at."""
+    for n in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 128):
+        sizes = {"batch": 1, "n": n, "dim": 1, "sf": 1, "sx": 1, "sz": 1, "nb": 0}
+        assert linrec(L, **sizes) == UNSUP and linrec_bwd(L, **sizes) == UNSUP
+        assert binding.ssm_linrec_workspace_bytes(1, n, 1) == 0
+        assert binding.ssm_linrec_bwd_workspace_bytes(1, n, 1) == 0
+    assert linrec(L, batch=1, n=2 ** 31 - 129, dim=1, nb=0) == WS
+    wide = 2 ** 31 - 1
+    assert linrec(L, batch=0, n=1, dim=wide, sf=wide, sx=wide, sz=wide, nb=0) == UNSUP
