@@ -1264,6 +1264,15 @@ def ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab) -> int:
     return int(lib().ssm_vocab_ce_bwd_workspace_bytes(tokens, dim, vocab))
 
 
+def _vector(t, stream):
+    """t, or a copy of it where it starts off a 16-byte boundary: the labels shifted by one
+    (``labels[1:]``) are contiguous and 8-byte aligned."""
+    if t.data_ptr() % 16 == 0:
+        return t
+    with torch.cuda.stream(stream):  # no other stream for None
+        return t.clone()
+
+
 def _ce_args(h, W, targets):
     _req(h, "h", torch.bfloat16, 2)
     _req(W, "W", torch.bfloat16, 2)
@@ -1278,6 +1287,7 @@ def ssm_vocab_ce_fwd(h, W, targets, loss=None, lse=None, workspace=None, stream=
     (tokens, dim), W: (vocab, dim) bf16, dim a multiple of 8; targets: (tokens,) int64, a
     negative one for a token without loss.  Returns (loss, lse), (tokens,) fp32 each."""
     tokens, dim, vocab = _ce_args(h, W, targets)
+    targets = _vector(targets, stream)
     loss = _out(loss, "loss", h, (tokens,), torch.float32, stream)
     lse = _out(lse, "lse", h, (tokens,), torch.float32, stream)
     workspace = _work(workspace, h, ssm_vocab_ce_workspace_bytes(tokens, dim, vocab), stream)
@@ -1296,6 +1306,7 @@ def ssm_vocab_ce_bwd(h, W, targets, lse, dloss, grad_dtype=None, workspace=None,
     tokens, dim, vocab = _ce_args(h, W, targets)
     _like(lse, "lse", (tokens,), torch.float32)
     _like(dloss, "dloss", (tokens,), torch.float32)
+    targets, lse, dloss = (_vector(t, stream) for t in (targets, lse, dloss))
     gd = h.dtype if grad_dtype is None else grad_dtype
     code = _dt_code(gd, "grad_dtype")
     out = out or {}

@@ -205,3 +205,22 @@ def test_few_tokens(tokens, dim, vocab):
     loss_ref, lse_ref = P.ce_fwd(to64(h), to64(W), t.numpy())
     _check_loss(lse, lse_ref, lse_ref)
     _check_loss(loss, loss_ref, lse_ref)
+
+
+@pytest.mark.parametrize("tokens", [9, 131])
+def test_vectors_off_a_16_byte_boundary(tokens):
+    """Targets, lse and dloss as ranges that start at the second element (a program's labels
+    shifted by one): the same results, on the current stream and on another."""
+    h, W, t, d = (v.cuda() for v in _inputs(tokens, 72, 300, 12))
+    loss, lse = binding.ssm_vocab_ce_fwd(h, W, t)
+    g = binding.ssm_vocab_ce_bwd(h, W, t, lse, d)
+    shifted = [torch.cat([v.new_zeros(1), v])[1:] for v in (t, lse, d)]
+    assert all(v.data_ptr() % 16 and v.is_contiguous() for v in shifted)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        a, b = binding.ssm_vocab_ce_fwd(h, W, shifted[0], stream=stream)
+        r = binding.ssm_vocab_ce_bwd(h, W, *shifted, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(a, loss) and torch.equal(b, lse)
+        assert torch.equal(r["dh"], g["dh"]) and torch.equal(r["dW"], g["dW"])
