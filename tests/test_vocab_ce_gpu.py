@@ -224,3 +224,20 @@ def test_vectors_off_a_16_byte_boundary(tokens):
         torch.cuda.synchronize()
         assert torch.equal(a, loss) and torch.equal(b, lse)
         assert torch.equal(r["dh"], g["dh"]) and torch.equal(r["dW"], g["dW"])
+
+
+@pytest.mark.parametrize("tokens", [1, 6, 15, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("dim,vocab", [(64, 15), (520, 2433), (72, 20011), (136, 60000)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_few_tokens_gradient(tokens, dim, vocab, dtype):
+    """The gradient's own kernel of few tokens, in each of its widths, full and not, and the
+    first size past it; every fourth target lies outside the vocabulary, on either side."""
+    h, W, t, d = _inputs(tokens, dim, vocab, tokens + vocab, skip=0)
+    counts = torch.arange(tokens) % 4 != 2
+    t[~counts] = torch.where(torch.arange(tokens) % 8 == 2, -1, vocab)[~counts]
+    hc, Wc, tc, dc = h.cuda(), W.cuda(), t.cuda(), d.cuda()
+    _, lse = binding.ssm_vocab_ce_fwd(hc, Wc, tc)
+    g = binding.ssm_vocab_ce_bwd(hc, Wc, tc, lse, dc, grad_dtype=dtype)
+    assert not g["dh"][~counts.cuda()].any()
+    t[~counts] = -1
+    _check_grads(g, h, W, t, d, dtype)
