@@ -400,3 +400,29 @@ def test_a_gradient_can_report_whatever_forward_it_ran(n, dim):
     binding.ssm_linrec_bwd(d["f"], d["x"], d["dy"], workspace=ws)
     assert binding.ssm_last_device_status(ws) == OK
     assert int(ws[:8].view(torch.int32)[1]) == -1
+
+
+@pytest.mark.parametrize("n", [9, 24, 20000])
+@pytest.mark.parametrize("dim", [8, 7])
+def test_long_memory(n, dim):
+    """Constant gates close to 1, a channel to each f.  A gate and each update carry fp32
+    roundings of up to 2^-22 of the state, which a channel remembers for 1 / (1 - a) = 1 +
+    e^f steps: the state is within 2^-22 min(1 + e^f, n), and 1 - a, whose exponent is rounded
+    once, within (|f| + 8) 2^-24, of the channel's largest.  The gradients multiply two such
+    quantities."""
+    f0 = torch.tensor([2.0, 4.0, 6.0, 8.0, 10.0, 12.0, 14.0, 16.0][:dim])
+    d = _inputs(2, n, dim, F32, n + dim, gated=False)
+    d["f"], d["x"] = f0.expand(2, n, dim).contiguous(), 1 + d["x"]
+    dev, r = _dev(d), _n64(d)
+    y, fin = binding.ssm_linrec_fwd(dev["f"], dev["x"], initial_state=dev["h0"])
+    g = binding.ssm_linrec_bwd(dev["f"], dev["x"], dev["dy"], initial_state=dev["h0"],
+                               dfinal_state=dev["dfin"])
+    y_ref, fin_ref, _ = P.linrec_fwd(r["f"], r["x"], None, r["h0"])
+    df, dx, _, dh0 = P.linrec_bwd(r["f"], r["x"], r["dy"], None, r["h0"], r["dfin"])
+    for c in range(dim):
+        v = float(f0[c])
+        tol = 2.0 ** -22 * min(1 + np.exp(v), n) + (v + 8) * 2.0 ** -24
+        for name, got, ref, k in (("y", y, y_ref, 1), ("final", fin, fin_ref, 1),
+                                  ("df", g["df"], df, 2), ("dx", g["dx"], dx, 2),
+                                  ("dinitial_state", g["dinitial_state"], dh0, 2)):
+            _near(got[..., c], ref[..., c], (name, v), k * tol)
