@@ -826,9 +826,11 @@ size_t ssm_linrec_workspace_bytes(int batch, int seqlen, int dim);
  * ceil(seqlen / 64) < 2e9, batch * dim < 2e9 and seqlen < 2^31 - 128.  seqlen == 0 hands
  * the state on.
  * The sequence is cut into tiles chained by a decoupled look-back in the
- * workspace (sequences of up to 16 steps are walked by one thread per channel
- * pair, and need no workspace: it may be NULL); its bounded waits report through ssm_last_device_status.  The result
- * does not depend on timing: runs are bit-equal.
+ * workspace, whose bounded waits report through ssm_last_device_status.
+ * Sequences of up to 16 steps, and of up to 32 where batch * dim is 65536 or
+ * more, are walked by one thread per channel or pair of channels instead; those
+ * of up to 16 need no workspace: it may be NULL.  The result does not depend on
+ * timing: runs are bit-equal.
  */
 ssm_status_t ssm_linrec_fwd(const void* f, const void* x, const void* z, long long f_stride,
                             long long x_stride, long long z_stride, const float* initial_state,

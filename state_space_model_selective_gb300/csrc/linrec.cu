@@ -1134,11 +1134,19 @@ bool launch_by(LinArgs& a, uint8_t* ws, bool gated, cudaStream_t s) {
                  : launch_tile<T, TO, false, false, GRAD>(a, ws, s);
 }
 
-// Sequences of up to kWalkSteps steps, and (forward) of up to twice that where the
-// channels are so many that a thread to each pair of them fills the GPU, are walked
-// (batch 256, 2560 channels of bf16 with a gate: 34 us against 74 us for the tiles at 17
-// steps; batch 200: 83 us against 75 us at 60).
-constexpr long long kWalkChannels = 262144;
+// Sequences of up to kWalkSteps steps, and (forward) of up to twice that where a thread to
+// each channel or pair of them gives the GPU enough warps, are walked.  Walk and tiles, us,
+// with a gate:
+//   channels    bf16: 17 steps   32 steps   48 steps   fp32: 17 steps   32 steps
+//   10240             5    6      8    6     12    5         3    8      5    7
+//   40960             5   10      9   10     12   10         4   16      5   15
+//   81920             6   17      9   17     13   17         5   26      7   26
+//   655360           35  123     64  123     93  117        30  184     51  175
+// (A tile is mostly empty at these lengths; of unaligned bf16 rows 41041 channels, 32 steps
+// take 9 us against 8.  In fp32 the walk stays ahead for longer: 655360 channels, 128 steps
+// 191 us against 218 us, 40960 channels 26 us against 21 us; in bf16 it is behind at 64
+// steps: 124 us against 106 us.)
+constexpr long long kWalkChannels = 65536;
 
 bool walks(int batch, int seqlen, int dim) {
     return seqlen <= kWalkSteps ||

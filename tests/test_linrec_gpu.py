@@ -426,3 +426,12 @@ def test_long_memory(n, dim):
                                   ("df", g["df"], df, 2), ("dx", g["dx"], dx, 2),
                                   ("dinitial_state", g["dinitial_state"], dh0, 2)):
             _near(got[..., c], ref[..., c], (name, v), k * tol)
+
+
+@pytest.mark.parametrize("n", [16, 17, 24, 31, 32, 33])
+@pytest.mark.parametrize("batch,dim", [(26, 2560), (66, 1001), (1, 65535)])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_short_sequences_of_many_channels(n, batch, dim, dtype):
+    """The lengths and channels where the forward's walk ends and the tiles begin, with pairs
+    of channels and single ones to a thread."""
+    _check(_inputs(batch, n, dim, dtype, n + dim))
