@@ -721,7 +721,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB)
                 const float2 bt = Step<F>::input(om, x);
                 gb[k] = GRAD ? om : bt;
                 q = Step<F>::next(ga[k], q, bt);
-                P = F ? mul2(P, ga[k]) : longer_span(P, ga[k]);
+                // (a NaN gate is NaN in q: left out here, so that a restart before it counts)
+                P = F ? mul2(P, ga[k])
+                      : longer_span(P, make_float2(fminf(ga[k].x, 1.0f), fminf(ga[k].y, 1.0f)));
             }
             P = F ? make_float2(fmaxf(P.x, kLeast), fmaxf(P.y, kLeast)) : span_decay(P);
             if constexpr (GRAD) {

@@ -435,3 +435,28 @@ def test_short_sequences_of_many_channels(n, batch, dim, dtype):
     """The lengths and channels where the forward's walk ends and the tiles begin, with pairs
     of channels and single ones to a thread."""
     _check(_inputs(batch, n, dim, dtype, n + dim))
+
+
+@pytest.mark.parametrize("n", [12, 300])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_a_restart_ends_what_lies_behind_a_nan_gate(n, dtype):
+    """A restart with a NaN gate after it in the same warp's steps, and a NaN gradient further
+    on: nothing of it reaches the steps before the restart, nor the other way round."""
+    d = _inputs(1, n, 70, dtype, n + 3)
+    t = n // 2
+    d["f"][0, t, 30], d["f"][0, t + 1, 30] = float("-inf"), float("nan")
+    d["f"][0, t, 31], d["f"][0, t - 1, 31] = float("-inf"), float("nan")
+    for c in (30, 31, 32):
+        d["dy"][0, n - 1, c] = float("nan")
+    dev, r = _dev(d), _n64(d)
+    y, fin = binding.ssm_linrec_fwd(dev["f"], dev["x"], dev["z"], initial_state=dev["h0"])
+    y_ref, fin_ref, _ = P.linrec_fwd(r["f"], r["x"], r["z"], r["h0"])
+    _near(y, y_ref, "y", 1e-5)
+    _near(fin, fin_ref, "final", 1e-5)
+    refs = P.linrec_bwd(r["f"], r["x"], r["dy"], r["z"], r["h0"], r["dfin"])
+    assert np.isfinite(refs[3][0, 30]) and np.isfinite(fin_ref[0, 31])
+    assert np.isnan(refs[3][0, 31]) and np.isnan(refs[3][0, 32])
+    g = binding.ssm_linrec_bwd(dev["f"], dev["x"], dev["dy"], dev["z"], initial_state=dev["h0"],
+                               dfinal_state=dev["dfin"])
+    for k, ref in zip(("df", "dx", "dz", "dinitial_state"), refs):
+        _near(g[k], ref, k, 2e-5)
