@@ -747,7 +747,8 @@ ssm_status_t ssm_scan_fwd_host(const void* u, const void* delta, const float* A,
  * residual stream updated in place).  A row of NaN gives NaN; rows == 0 does
  * nothing.
  * Supported: 1 <= dim <= 16384; any rows; res_dtype in_dtype or SSM_F32.
- * Rows move in 16-byte units where dim is a multiple of 8.
+ * Rows move in 16-byte units at any dim; a dim that is a multiple of 8 moves
+ * fastest, as no unit is shared by two rows.
  */
 ssm_status_t ssm_add_rmsnorm_fwd(const void* x, const void* residual, const float* weight,
                                  float eps, void* y, void* sum_out, int rows, int dim,
@@ -903,7 +904,9 @@ size_t ssm_vocab_ce_bwd_workspace_bytes(int tokens, int dim, int vocab);
  * mean over n tokens that count: 1 / n).  A token without a target in [0,
  * vocab) has P = 0; its h still has to be finite.  The vocabulary is taken in
  * pieces: the logits of a piece again, P of the piece rounded to bf16, and its
- * part of both products, summed in fp32.  tokens == 0 writes dW = 0.
+ * part of both products, summed in fp32.  The rounding of P is what an fp32
+ * dh or dW is off by: about 1e-3 of it (2-norm), as much as a bf16 one is off by
+ * its own rounding.  tokens == 0 writes dW = 0.
  * Supported as ssm_vocab_ce_fwd; grad_dtype either type.  Runs are bit-equal.
  */
 ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const long long* targets,
