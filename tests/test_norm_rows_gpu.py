@@ -95,3 +95,48 @@ def test_e4m3_walks(dim, group, xt):
     got = to64(q.float())
     assert np.all((got == P.e4m3_round(v)) | (got == P.e4m3_round(v * (1 - 1e-5))) |
                   (got == P.e4m3_round(v * (1 + 1e-5))))
+
+
+@pytest.mark.parametrize("dim", [7, 100, 257, 1097, 5001])
+@pytest.mark.parametrize("xt,rt", [(F32, F32), (BF16, F32), (BF16, BF16)],
+                         ids=["f32", "bf16-f32", "bf16"])
+def test_sum_in_the_residuals_place_at_odd_widths(dim, xt, rt):
+    """Rows share 16-byte units with their neighbours, which other CTAs replace meanwhile."""
+    rows = 2 * _fwd_rows(dim) + 3
+    x, res, w, _, _ = (t.cuda() for t in _inputs(rows, dim, xt, rt, dim + 2))
+    y, s = binding.ssm_add_rmsnorm_fwd(x, w, res, eps=EPS)
+    q, scales, _ = binding.ssm_add_rmsnorm_e4m3_fwd(x, w, res, eps=EPS, group=32)
+    for _ in range(3):
+        stream = res.clone()
+        y2, _ = binding.ssm_add_rmsnorm_fwd(x, w, stream, eps=EPS, sum_out=stream)
+        assert torch.equal(y2, y) and torch.equal(stream, s)
+        stream = res.clone()
+        q2, scales2, _ = binding.ssm_add_rmsnorm_e4m3_fwd(x, w, stream, eps=EPS, group=32,
+                                                          sum_out=stream)
+        assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8))
+        assert torch.equal(scales2, scales) and torch.equal(stream, s)
+
+
+@pytest.mark.parametrize("dim", [7, 100, 257, 1097, 5001])
+@pytest.mark.parametrize("xt", [F32, BF16], ids=["f32", "bf16"])
+def test_rows_of_nan_and_infinities_between_others(dim, xt):
+    """Every third row is NaN, every fifth infinite in one place: the rows beside them, which
+    share units with them, are what they are without."""
+    rows = 45
+    x, res, w, dy, ds = _inputs(rows, dim, xt, xt, dim + 3)
+    dy = dy.to(xt)
+    bad = torch.zeros(rows, dtype=torch.bool)
+    bad[::3], bad[1::5] = True, True
+    x2, dy2 = x.clone(), dy.clone()
+    x2[::3], dy2[::3] = float("nan"), float("nan")
+    x2[1::5, dim - 1], x2[1::5, 0] = float("inf"), float("-inf")
+
+    def all_of(x, dy):
+        y, s = binding.ssm_add_rmsnorm_fwd(x.cuda(), w.cuda(), res.cuda(), eps=EPS)
+        q, sc, _ = binding.ssm_add_rmsnorm_e4m3_fwd(x.cuda(), w.cuda(), res.cuda(), eps=EPS, group=32)
+        g = binding.ssm_add_rmsnorm_bwd(dy.cuda(), s, w.cuda(), dsum=ds.cuda(), eps=EPS)
+        return y, s, q.float(), sc, g["dx"]
+
+    for a, b in zip(all_of(x2, dy2), all_of(x, dy)):
+        a, b = a.cpu(), b.cpu()
+        assert torch.equal(a[~bad], b[~bad]) and not a[bad].isfinite().all()
