@@ -18,6 +18,7 @@
  *   ssm_add_rmsnorm_fwd, _e4m3_fwd, _bwd  RMS norm with the residual's addition
  *   ssm_linrec_fwd, _bwd  gated linear recurrence, one state per channel
  *   ssm_vocab_ce_fwd, _bwd  cross entropy over a vocabulary without the logits
+ *   ssm_qk_norm_rope_fwd, _bwd  norms of query and key heads with the rotation by position
  *
  * Conventions shared by every entry point
  *  - Pointers are DEVICE pointers unless stated otherwise, to dense row-major
@@ -913,6 +914,62 @@ ssm_status_t ssm_vocab_ce_bwd(const void* h, const void* W, const long long* tar
                               const float* lse, const float* dloss, void* dh, void* dW, int tokens,
                               int dim, int vocab, ssm_dtype_t in_dtype, ssm_dtype_t grad_dtype,
                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm of every query and key head, and the rotation by position, in one pass.
+ *   "Mamba-3 NKI Kernels for AWS Neuron", section "How it works", norms B and C (the
+ *   keys and queries) before they are rotated; ssm_mamba3_rope has that page's
+ *   rotation, by angles that the data sums up.  This is the rotation by a token's
+ *   place, as a mixer with a plain state (ssm_gated_delta_fwd) or attention takes it.
+ * For every token t, every head x of q and of k, in fp32:
+ *   n = x / sqrt(mean(x^2) + eps) * weight          (the head's own columns)
+ *   the pairs (a, b) of the first rot_dim columns, a = i, b = i + rot_dim / 2, or with
+ *   `interleaved` a = 2 i, b = 2 i + 1, at angle = positions[t] * inv_freq[i]:
+ *     (out_a, out_b) = (n_a cos - n_b sin, n_a sin + n_b cos);  out = n behind them
+ * A weight of 1 / sqrt(headdim) gives heads of length one (the delta rule's keys).
+ * The angle's fraction of a turn is exact to 2^-52 |positions[t] inv_freq[i]| turns at
+ * any position.
+ * Layouts: q (tokens, qheads, headdim), k (tokens, kheads, headdim) in in_dtype, heads
+ *   contiguous, *_stride elements from one token to the next, so that both may be
+ *   column ranges of one projection; q_out, k_out contiguous in out_dtype; q_weight,
+ *   k_weight (headdim,) fp32, each may be NULL (ones); positions (tokens,) 64-bit
+ *   integers, inv_freq (rot_dim / 2,) fp64 and finite: both needed with rot_dim > 0.
+ * q and k need only the alignment of their element (16-byte rows move fastest),
+ * positions 8 bytes.
+ * Supported: headdim a multiple of 8 up to 256; rot_dim even, 0 to headdim; up to 4096
+ * heads each (0: that tensor is not looked at) and 2^40 tokens.  tokens == 0 does nothing.
+ */
+ssm_status_t ssm_qk_norm_rope_fwd(const void* q, const void* k, long long q_stride,
+                                  long long k_stride, const float* q_weight,
+                                  const float* k_weight, const long long* positions,
+                                  const double* inv_freq, float eps, int rot_dim, int interleaved,
+                                  void* q_out, void* k_out, long long tokens, int qheads,
+                                  int kheads, int headdim, ssm_dtype_t in_dtype,
+                                  ssm_dtype_t out_dtype, void* stream);
+
+/* Bytes of device workspace ssm_qk_norm_rope_bwd needs for the weights' gradients (0 for
+ * sizes it does not take). */
+size_t ssm_qk_norm_rope_bwd_workspace_bytes(long long tokens, int qheads, int kheads,
+                                            int headdim);
+
+/*
+ * Gradient of ssm_qk_norm_rope_fwd for the loss sum(dq_out * q_out) + sum(dk_out *
+ * k_out): with g = dy turned back by the token's angles, r = 1 / sqrt(mean(x^2) + eps),
+ *   dx = r (g w - n mean(g w n)),  n = x r;   dw = sum over tokens and heads of g n
+ * q, k, strides, weights, positions and inv_freq as given to the forward; dq_out, dk_out
+ * contiguous in out_dtype; dq, dk contiguous in in_dtype; dq_weight, dk_weight (headdim,)
+ * fp32, each may be NULL (the workspace is only needed for them).  Both are written
+ * whenever given (0 without tokens or heads).  Runs are bit-equal.
+ */
+ssm_status_t ssm_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                  const void* k, long long q_stride, long long k_stride,
+                                  const float* q_weight, const float* k_weight,
+                                  const long long* positions, const double* inv_freq, float eps,
+                                  int rot_dim, int interleaved, void* dq, void* dk,
+                                  float* dq_weight, float* dk_weight, long long tokens, int qheads,
+                                  int kheads, int headdim, ssm_dtype_t in_dtype,
+                                  ssm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 /*
  * Waits for `stream` to drain, then returns the device-side status the last

@@ -40,7 +40,8 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssm_add_rmsnorm_bwd", "ssm_linrec_checkpoint_bytes", "ssm_linrec_workspace_bytes",
            "ssm_linrec_fwd", "ssm_linrec_bwd_workspace_bytes", "ssm_linrec_bwd",
            "ssm_vocab_ce_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd_workspace_bytes",
-           "ssm_vocab_ce_bwd"]
+           "ssm_vocab_ce_bwd", "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd_workspace_bytes",
+           "ssm_qk_norm_rope_bwd"]
 
 
 class SSMError(RuntimeError):
@@ -147,6 +148,14 @@ def lib() -> ctypes.CDLL:
         L.ssm_vocab_ce_fwd.argtypes = [vp] * 5 + [i] * 4 + [vp, sz, vp]
         L.ssm_vocab_ce_bwd.restype = i
         L.ssm_vocab_ce_bwd.argtypes = [vp] * 7 + [i] * 5 + [vp, sz, vp]
+        L.ssm_qk_norm_rope_fwd.restype = i
+        L.ssm_qk_norm_rope_fwd.argtypes = ([vp] * 2 + [ll] * 2 + [vp] * 4 + [fl, i, i] + [vp] * 2 +
+                                           [ll] + [i] * 5 + [vp])
+        L.ssm_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        L.ssm_qk_norm_rope_bwd_workspace_bytes.argtypes = [ll] + [i] * 3
+        L.ssm_qk_norm_rope_bwd.restype = i
+        L.ssm_qk_norm_rope_bwd.argtypes = ([vp] * 4 + [ll] * 2 + [vp] * 4 + [fl, i, i] + [vp] * 4 +
+                                           [ll] + [i] * 5 + [vp, sz, vp])
         _lib = L
     return _lib
 
@@ -1321,4 +1330,141 @@ def ssm_vocab_ce_bwd(h, W, targets, lse, dloss, grad_dtype=None, workspace=None,
                                 _p(g["dh"]), _p(g["dW"]), tokens, dim, vocab, _DT[h.dtype], code,
                                 _p(workspace), workspace.numel(), _raw(stream, h))
     _check(st, "ssm_vocab_ce_bwd")
+    return g
+
+
+# ------------------------------- query and key heads, gated delta rule
+
+def _token_step(t, name, dtype, shape):
+    """Elements between the tokens of a (batch, seqlen, heads, dim) tensor whose heads are
+    contiguous and whose batches follow one another: a contiguous tensor, or a range of
+    the columns of a projection."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    batch, seqlen, heads, dim = shape
+    if t.is_contiguous():
+        return heads * dim
+    sb, st, sh, sd = t.stride()
+    # a dimension of one element may carry any stride
+    step = st if seqlen > 1 else sb if batch > 1 else heads * dim
+    if ((dim > 1 and sd != 1) or (heads > 1 and sh != dim) or step < heads * dim or
+            (batch > 1 and seqlen > 1 and sb != seqlen * st)):
+        raise ValueError(f"{name} must be contiguous, or a range of the columns of a "
+                         f"contiguous projection")
+    return step
+
+
+def _one_device(first, *others):
+    for t in others:
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError("all tensors must be on one device")
+
+
+def _qk_args(q, k, q_weight, k_weight, positions, inv_freq):
+    """(q, its step, k's step, tokens, heads of both, headdim, rot_dim)."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DT:
+        raise TypeError("q must be a float32 or bfloat16 tensor")
+    if q.dim() != 4:
+        raise ValueError(f"q must have 4 dims, got {q.dim()}")
+    batch, seqlen, qheads, dim = q.shape
+    sq = _token_step(q, "q", q.dtype, q.shape)
+    kheads = sk = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise TypeError("k must be a CUDA tensor of 4 dims")
+        kheads = k.shape[2]
+        sk = _token_step(k, "k", q.dtype, (batch, seqlen, kheads, dim))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _like(w, name, (dim,), torch.float32)
+    rot = 0
+    if inv_freq is not None and inv_freq.numel():
+        _req(inv_freq, "inv_freq", torch.float64, 1)
+        rot = 2 * inv_freq.numel()
+        if rot > dim:
+            raise ValueError(f"inv_freq must have at most {dim // 2} elements, got {rot // 2}")
+        if positions is None:
+            raise ValueError("positions are needed with inv_freq")
+        _like(positions, "positions", (batch, seqlen), torch.int64)
+    _one_device(q, k, q_weight, k_weight, positions if rot else None, inv_freq if rot else None)
+    return sq, sk, batch * seqlen, qheads, kheads, dim, rot
+
+
+def ssm_qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                         eps=1e-5, interleaved=False, out_dtype=None, q_out=None, k_out=None,
+                         stream=None):
+    """RMS norm of every head of q (batch, seqlen, qheads, headdim) and k (batch, seqlen,
+    kheads, headdim) over its own columns, and the rotation by position, in one pass.  q
+    and k may be ranges of the columns of one projection; k may be None.  weights:
+    (headdim,) fp32 or None (ones; 1 / sqrt(headdim) gives heads of length one).
+    positions: (batch, seqlen) int64; inv_freq: (rot_dim / 2,) fp64, or None for no
+    rotation; pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) with ``interleaved``.
+    Returns (q_out, k_out), contiguous, in ``out_dtype`` (q's type by default)."""
+    sq, sk, tokens, qheads, kheads, dim, rot = _qk_args(q, k, q_weight, k_weight, positions,
+                                                        inv_freq)
+    out_dt = q.dtype if out_dtype is None else out_dtype
+    code = _dt_code(out_dt, "out_dtype")
+    q_out = _out(q_out, "q_out", q, q.shape, out_dt, stream)
+    if k is not None:
+        k_out = _out(k_out, "k_out", q, k.shape, out_dt, stream)
+        _one_device(q, q_out, k_out)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    st = lib().ssm_qk_norm_rope_fwd(_p(q), _p(k), sq, sk, _p(q_weight), _p(k_weight),
+                                    _p(positions) if rot else None, _p(inv_freq) if rot else None,
+                                    float(eps), rot, int(bool(interleaved)), _p(q_out), _p(k_out),
+                                    tokens, qheads, kheads, dim, _DT[q.dtype], code,
+                                    _raw(stream, q))
+    _check(st, "ssm_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def ssm_qk_norm_rope_bwd_workspace_bytes(tokens, qheads, kheads, headdim) -> int:
+    return int(lib().ssm_qk_norm_rope_bwd_workspace_bytes(tokens, qheads, kheads, headdim))
+
+
+def ssm_qk_norm_rope_bwd(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None, positions=None,
+                         inv_freq=None, eps=1e-5, interleaved=False, workspace=None, stream=None,
+                         out=None):
+    """Gradient of ``ssm_qk_norm_rope_fwd`` for the loss sum(dq_out * q_out) + sum(dk_out *
+    k_out), dq_out and dk_out contiguous and of the outputs' type; the other arguments as
+    given to the forward.  Returns a dict: dq, dk in q's type, contiguous, and dq_weight,
+    dk_weight fp32 (None where there was no weight).  ``out`` may map any of these names
+    to a preallocated tensor to write."""
+    sq, sk, tokens, qheads, kheads, dim, rot = _qk_args(q, k, q_weight, k_weight, positions,
+                                                        inv_freq)
+    _req(dq_out, "dq_out")
+    code = _dt_code(dq_out.dtype, "dq_out")
+    _like(dq_out, "dq_out", q.shape, dq_out.dtype)
+    wants = {"dq": (q.shape, q.dtype)}
+    if k is not None:
+        _like(dk_out, "dk_out", k.shape, dq_out.dtype)
+        wants["dk"] = (k.shape, q.dtype)
+    if q_weight is not None:
+        wants["dq_weight"] = ((dim,), torch.float32)
+    if k is not None and k_weight is not None:
+        wants["dk_weight"] = ((dim,), torch.float32)
+    out = out or {}
+    for name in out:
+        if name not in wants:
+            raise ValueError(f"out[{name!r}] is not an output of this call")
+    g = dict.fromkeys(("dq", "dk", "dq_weight", "dk_weight"))
+    for name, (shape, dt) in wants.items():
+        g[name] = _out(out.get(name), f"out[{name!r}]", q, shape, dt, stream)
+    if g["dq_weight"] is not None or g["dk_weight"] is not None or workspace is not None:
+        workspace = _work(workspace, q, ssm_qk_norm_rope_bwd_workspace_bytes(tokens, qheads, kheads,
+                                                                             dim), stream)
+    _one_device(q, dq_out, dk_out if k is not None else None, workspace, *g.values())
+    st = lib().ssm_qk_norm_rope_bwd(_p(dq_out), _p(dk_out) if k is not None else None, _p(q), _p(k),
+                                    sq, sk, _p(q_weight), _p(k_weight),
+                                    _p(positions) if rot else None, _p(inv_freq) if rot else None,
+                                    float(eps), rot, int(bool(interleaved)), _p(g["dq"]),
+                                    _p(g["dk"]), _p(g["dq_weight"]), _p(g["dk_weight"]), tokens,
+                                    qheads, kheads, dim, _DT[q.dtype], code, _p(workspace),
+                                    0 if workspace is None else workspace.numel(), _raw(stream, q))
+    _check(st, "ssm_qk_norm_rope_bwd")
     return g

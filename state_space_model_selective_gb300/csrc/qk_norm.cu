@@ -1,0 +1,645 @@
+// qk_norm.cu -- RMS norm of every query and key head over its own columns, and
+// the rotation by position, in one pass; and the gradient.
+//
+//   n = x / sqrt(mean(x^2) + eps),  t = n w,
+//   (y_a, y_b) = (t_a cos - t_b sin, t_a sin + t_b cos)  for the pairs (a, b) of the
+//   first rot columns, at the angle position * inv_freq[pair];  y = t behind them
+//   gradient: g = dy turned back, dx = r (g w - n mean(g w n)),
+//             dw = sum over tokens and heads of g n
+//
+// Bound by memory: 8 (gradient: 26) FP32 operations an element against 4 to 16 bytes,
+// so a head's row is read once into registers, reduced by shuffles, turned and
+// written.  What costs beside the bytes is the angles: a token's rot / 2 sines and
+// cosines are shared by its heads, so a CTA takes a few tokens with all their heads
+// and puts them into shared memory first.
+//
+// Angles of far positions: position * inv_freq is a phase in turns whose whole part
+// does not matter, so inv_freq / 2 pi is taken as a 64-bit binary fraction and
+// multiplied by the (whole) position modulo 2^64: the fraction of a turn comes out to
+// 2^-52 * position, in four integer instructions.  (An fp32 product is off by 0.06 rad
+// at position 10^6; a product in fp64 runs at one 64th of fp32's rate here.)
+//
+// Layout of the work: a lane holds two 8-element chunks of a row -- chunk p of the
+// first and of the second half of the rotated columns, so that both partners of a
+// rotation are in one lane -- and a row takes 1 to 16 lanes.  Rotations whose halves
+// are no multiples of 8 columns exchange partners through shared memory.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace {
+
+using namespace ssm;
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 256;
+constexpr int kTable = 2048;      // sines and cosines a CTA holds (pairs x tokens)
+constexpr int kFwdCtas = 6;       // of the forward on an SM
+constexpr int kBwdMost = 152 * 3; // CTAs of the gradient, whose sums of dw are joined
+
+// How a row's columns are paired.
+enum Pairs {
+    kHalves,      // (i, i + rot / 2), rot / 2 a multiple of 8: partners in one lane
+    kNeighbours,  // (2 i, 2 i + 1)
+    kShared       // (i, i + rot / 2), any rot: partners through shared memory
+};
+
+struct QkArgs {
+    const void* x[2];          // q, k
+    const void* dy[2];         // gradient only
+    void* y[2];                // outputs; gradient: dq, dk
+    const float* w[2];         // may be NULL (ones)
+    long long stride[2];       // of x, elements between tokens
+    int heads[2];
+    const long long* pos;
+    const double* freq;
+    float* partial;            // gradient: [gridDim.x][2][dim]
+    long long tokens;
+    float eps, inv_dim;
+    int dim, rot, lanes;       // lanes of a row, a power of two
+    int tile;                  // tokens a CTA takes at a time
+    int vec[2];                // x's rows are 16-byte aligned
+    int join;                  // gradient: dw is wanted
+};
+
+// The first column of a lane's two chunks (dim where it has none).
+template <int MODE>
+__device__ __forceinline__ void lane_columns(const QkArgs& a, int p, int& c0, int& c1) {
+    const int half = MODE == kHalves ? a.rot / 16 : 0;
+    if (p < half) {
+        c0 = 8 * p;
+        c1 = 8 * (p + half);
+    } else {
+        c0 = 8 * (2 * p);  // behind 2 * half chunks: 2 half + 2 (p - half)
+        c1 = c0 + 8;
+    }
+    c0 = min(c0, a.dim);
+    c1 = min(c1, a.dim);
+}
+
+__device__ __forceinline__ void unpack(uint4 v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16lo(w[i]);
+        f[2 * i + 1] = bf16hi(w[i]);
+    }
+}
+
+// 8 consecutive elements as loaded: raw bits, converted when they are used, so that
+// loads in flight take few registers.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        v = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void load_each(const __nv_bfloat16* p) {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = u[2 * i] | ((uint32_t)u[2 * i + 1] << 16);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float* f) const { unpack(v, f); }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void load_each(const float* p) {
+        a = make_float4(p[0], p[1], p[2], p[3]);
+        b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float* f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(Raw<T>& r, const T* row, int c, int dim, bool vec) {
+    if (c >= dim) r.zero();
+    else if (vec) r.load(row + c);
+    else r.load_each(row + c);
+}
+
+__device__ __forceinline__ void store8(float* p, const float* f) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Sum over the `lanes` lanes of a row (all lanes of the warp take part).
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1)
+        if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The 64-bit fraction of a turn that one position is worth.
+__device__ __forceinline__ unsigned long long turn_of(double freq) {
+    const double t = freq * 0.15915494309189533577;  // 1 / (2 pi)
+    return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+
+// Sines and cosines of the tile's tokens, [token][pair]; rot / 2 pairs.
+__device__ __forceinline__ void make_table(const QkArgs& a, long long t0, int n, float2* cs) {
+    const int half = a.rot / 2;
+    if (half == 0) return;
+    // a thread keeps its pair where it can, and with it the pair's fraction
+    const int per = half <= kThreads ? kThreads / half : 1;
+    for (int e = threadIdx.x; e < half * per; e += kThreads) {
+        const int pair = e % half;
+        const unsigned long long f = turn_of(a.freq[pair]);
+        for (int t = e / half; t < n; t += per) {
+            const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * f;
+            // in half turns, -1 to 1
+            const float r = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
+            float s, c;
+            sincospif(r, &s, &c);
+            cs[t * half + pair] = make_float2(c, s);
+        }
+    }
+}
+
+// t turned by the token's angles (BACK: turned back), in place.  `buf`: this row's dim
+// floats of shared memory (kShared).
+template <int MODE, bool BACK>
+__device__ __forceinline__ void turn(const QkArgs& a, const float2* cs, int p, int c0, int c1,
+                                     float* u, float* v, float* buf) {
+    const int half = a.rot / 2;
+    if constexpr (MODE == kHalves) {
+        if (p < a.rot / 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 k = cs[c0 + i];
+                const float s = BACK ? -k.y : k.y;
+                const float x = u[i], z = v[i];
+                u[i] = fmaf(x, k.x, -z * s);
+                v[i] = fmaf(x, s, z * k.x);
+            }
+        }
+    } else if constexpr (MODE == kNeighbours) {
+        auto both = [&](float* x, int c) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const int pair = (c + i) >> 1;
+                if (pair < half) {
+                    const float2 k = cs[pair];
+                    const float s = BACK ? -k.y : k.y;
+                    const float e = x[i], o = x[i + 1];
+                    x[i] = fmaf(e, k.x, -o * s);
+                    x[i + 1] = fmaf(e, s, o * k.x);
+                }
+            }
+        };
+        both(u, c0);
+        both(v, c1);
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c0 < a.dim) buf[c0 + i] = u[i];
+            if (c1 < a.dim) buf[c1 + i] = v[i];
+        }
+        __syncwarp();
+        auto each = [&](float* x, int c) {
+            if (c >= a.dim) return;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int col = c + i;
+                if (col >= a.rot) continue;
+                const bool first = col < half;
+                const float2 k = cs[first ? col : col - half];
+                const float s = BACK ? -k.y : k.y;
+                const float other = buf[first ? col + half : col - half];
+                x[i] = fmaf(x[i], k.x, first ? -other * s : other * s);
+            }
+        };
+        each(u, c0);
+        each(v, c1);
+    }
+}
+
+__device__ __forceinline__ void load_weights(const float* w, int c0, int c1, int dim, float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[i] = w && c0 < dim ? w[c0 + i] : 1.0f;
+        f[8 + i] = w && c1 < dim ? w[c1 + i] : 1.0f;
+    }
+}
+
+// A row group's shared memory for kShared.
+template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 1;
+
+template <typename TI, typename TO, int MODE>
+__global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
+    __shared__ float2 table[kTable];
+    __shared__ float bufs[kBufFloats<MODE>];
+    const int lanes = a.lanes, groups = kThreads / lanes;
+    const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
+    int c0, c1;
+    lane_columns<MODE>(a, p, c0, c1);
+    float* buf = MODE == kShared ? bufs + group * (16 * lanes) : nullptr;
+    const int half = a.rot / 2;
+
+    for (long long t0 = (long long)blockIdx.x * a.tile; t0 < a.tokens;
+         t0 += (long long)gridDim.x * a.tile) {
+        const int n = (int)min((long long)a.tile, a.tokens - t0);
+        make_table(a, t0, n, table);
+        bool ready = false;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const TI* x = static_cast<const TI*>(a.x[which]);
+            TO* y = static_cast<TO*>(a.y[which]);
+            const int heads = a.heads[which], rows = n * heads;
+            const bool vec = a.vec[which] != 0;
+            float w[16];
+            load_weights(a.w[which], c0, c1, a.dim, w);
+            // rows beyond the last are loaded as zeros and not stored: every lane of a
+            // warp takes part in the shuffles
+            Raw<TI> r0, r1;
+            auto fetch = [&](int row) {
+                if (row < rows) {
+                    const TI* src = x + (t0 + row / heads) * a.stride[which] +
+                                    (long long)(row % heads) * a.dim;
+                    load8(r0, src, c0, a.dim, vec);
+                    load8(r1, src, c1, a.dim, vec);
+                } else {
+                    r0.zero();
+                    r1.zero();
+                }
+            };
+            fetch(group);
+            if (!ready) {
+                __syncthreads();
+                ready = true;
+            }
+            for (int base = 0; base < rows; base += groups) {
+                const int row = base + group;
+                float u[8], v[8];
+                r0.get(u);
+                r1.get(v);
+                if (base + groups < rows) fetch(row + groups);
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(u[i], u[i], fmaf(v[i], v[i], s));
+                s = row_sum(s, lanes);
+                const float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    u[i] *= r * w[i];
+                    v[i] *= r * w[8 + i];
+                }
+                const int t = min(row / heads, n - 1);
+                turn<MODE, false>(a, table + t * half, p, c0, c1, u, v, buf);
+                if (row < rows) {
+                    TO* dst = y + ((t0 + t) * heads + row % heads) * (long long)a.dim;
+                    if (c0 < a.dim) store8(dst + c0, u);
+                    if (c1 < a.dim) store8(dst + c1, v);
+                }
+            }
+        }
+        __syncthreads();  // the table is read before it is made anew
+    }
+}
+
+// TI: the type of x and dx, TO: of dy.
+template <typename TI, typename TO, int MODE>
+__global__ void __launch_bounds__(kThreads, 3) qk_bwd_kernel(const QkArgs a) {
+    __shared__ float2 table[kTable];
+    __shared__ float bufs[kBufFloats<MODE>];
+    __shared__ float sums[kThreads * 16];
+    const int lanes = a.lanes, groups = kThreads / lanes;
+    const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
+    int c0, c1;
+    lane_columns<MODE>(a, p, c0, c1);
+    float* buf = MODE == kShared ? bufs + group * (16 * lanes) : nullptr;
+    const int half = a.rot / 2;
+
+    // q's rows over all tiles, then k's, so that one set of sums is kept at a time
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const TI* x = static_cast<const TI*>(a.x[which]);
+        const TO* dy = static_cast<const TO*>(a.dy[which]);
+        TI* dx = static_cast<TI*>(a.y[which]);
+        const int heads = a.heads[which];
+        const bool vec = a.vec[which] != 0;
+        float w[16], dw[16];
+        load_weights(a.w[which], c0, c1, a.dim, w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+        for (long long t0 = (long long)blockIdx.x * a.tile; heads > 0 && t0 < a.tokens;
+             t0 += (long long)gridDim.x * a.tile) {
+            const int n = (int)min((long long)a.tile, a.tokens - t0), rows = n * heads;
+            Raw<TI> x0, x1;
+            Raw<TO> d0, d1;
+            auto fetch = [&](int row) {
+                if (row < rows) {
+                    const int t = row / heads, h = row % heads;
+                    const TI* src = x + (t0 + t) * a.stride[which] + (long long)h * a.dim;
+                    load8(x0, src, c0, a.dim, vec);
+                    load8(x1, src, c1, a.dim, vec);
+                    const TO* up = dy + ((t0 + t) * heads + h) * (long long)a.dim;
+                    load8(d0, up, c0, a.dim, true);
+                    load8(d1, up, c1, a.dim, true);
+                } else {
+                    x0.zero(); x1.zero(); d0.zero(); d1.zero();
+                }
+            };
+            fetch(group);
+            __syncthreads();  // the table's readers are done
+            make_table(a, t0, n, table);
+            __syncthreads();
+            for (int base = 0; base < rows; base += groups) {
+                const int row = base + group;
+                float u[8], v[8], g[8], q[8];
+                x0.get(u);
+                x1.get(v);
+                d0.get(g);
+                d1.get(q);
+                if (base + groups < rows) fetch(row + groups);
+                const int t = min(row / heads, n - 1);
+                turn<MODE, true>(a, table + t * half, p, c0, c1, g, q, buf);
+                float s = 0.0f, m = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s = fmaf(u[i], u[i], fmaf(v[i], v[i], s));
+                    m = fmaf(g[i] * w[i], u[i], fmaf(q[i] * w[8 + i], v[i], m));
+                }
+                s = row_sum(s, lanes);
+                m = row_sum(m, lanes);
+                if (row >= rows) continue;  // uniform over a row; no shuffles behind this
+                const float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));
+                const float mr = m * a.inv_dim * r * r;  // mean(g w n) r, per x
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dw[i] = fmaf(g[i], u[i] * r, dw[i]);
+                    dw[8 + i] = fmaf(q[i], v[i] * r, dw[8 + i]);
+                    g[i] = r * fmaf(-mr, u[i], g[i] * w[i]);
+                    q[i] = r * fmaf(-mr, v[i], q[i] * w[8 + i]);
+                }
+                TI* dst = dx + ((t0 + t) * heads + row % heads) * (long long)a.dim;
+                if (c0 < a.dim) store8(dst + c0, g);
+                if (c1 < a.dim) store8(dst + c1, q);
+            }
+        }
+        if (!a.join) continue;
+        // the CTA's sum over its groups, in their order
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c0 < a.dim) sums[group * a.dim + c0 + i] = dw[i];
+            if (c1 < a.dim) sums[group * a.dim + c1 + i] = dw[8 + i];
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.dim; c += kThreads) {
+            float s = 0.0f;
+            for (int j = 0; j < groups; ++j) s += sums[j * a.dim + c];
+            a.partial[((long long)blockIdx.x * 2 + which) * a.dim + c] = s;
+        }
+        __syncthreads();
+    }
+}
+
+// dw of q and k (columns 0 .. 2 dim - 1) from the CTAs' sums: a warp's lanes take 32
+// columns, 32 warps every 32nd CTA, joined in their order.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* partial, int ctas, int dim,
+                                                     float* dwq, float* dwk) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < 2 * dim)
+        for (int j = warp; j < ctas; j += 32) s += partial[(long long)j * 2 * dim + c];
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < 2 * dim) {
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) t += part[j][lane];
+        float* out = c < dim ? dwq : dwk;
+        if (out) out[c < dim ? c : c - dim] = t;
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+struct Span { const void* p; size_t n; };
+
+size_t strided_bytes(long long rows, long long width, long long stride, size_t es) {
+    return rows > 0 ? ((size_t)(rows - 1) * stride + width) * es : 0;
+}
+
+bool sizes_ok(long long tokens, int qheads, int kheads, int dim) {
+    return tokens >= 0 && qheads >= 0 && kheads >= 0 && dim >= 1;
+}
+
+// heads and tokens that an int can count together, heads of 8 to 256 columns
+bool sizes_fit(long long tokens, int qheads, int kheads, int dim) {
+    return dim % 8 == 0 && dim <= kMaxDim && qheads <= 4096 && kheads <= 4096 &&
+           tokens <= (1LL << 40);
+}
+
+// Lanes of a row, tokens of a tile.
+void plan(QkArgs& a, int mode, long long slots) {
+    const int chunks = a.dim / 8;
+    const int need = mode == kHalves ? a.rot / 16 + (chunks - a.rot / 8 + 1) / 2 : (chunks + 1) / 2;
+    a.lanes = 1;
+    while (a.lanes < need) a.lanes *= 2;
+    // rows for four rounds of the CTA's groups, no more tokens than the table holds, and
+    // few enough that all the CTAs have some
+    const int groups = kThreads / a.lanes, heads = std::max(1, a.heads[0] + a.heads[1]);
+    long long t = (4 * groups + heads - 1) / heads;
+    if (a.rot > 0) t = std::min<long long>(t, kTable / (a.rot / 2));
+    t = std::min(t, (a.tokens + slots - 1) / slots);
+    a.tile = (int)std::max(1LL, t);
+}
+
+template <typename F>
+bool by_types(ssm_dtype_t in, ssm_dtype_t out, F&& f) {
+    using B = __nv_bfloat16;
+    if (in == SSM_F32) return out == SSM_F32 ? f(float{}, float{}) : f(float{}, B{});
+    return out == SSM_F32 ? f(B{}, float{}) : f(B{}, B{});
+}
+
+template <typename F>
+void by_mode(int mode, F&& f) {
+    if (mode == kHalves) f(std::integral_constant<int, kHalves>{});
+    else if (mode == kNeighbours) f(std::integral_constant<int, kNeighbours>{});
+    else f(std::integral_constant<int, kShared>{});
+}
+
+ssm_status_t check_sizes(const QkArgs& a, int interleaved, ssm_dtype_t in, ssm_dtype_t out) {
+    using namespace ssm_host;
+    if (!sizes_ok(a.tokens, a.heads[0], a.heads[1], a.dim) || a.rot < 0 || a.rot > a.dim ||
+        a.rot % 2 || (interleaved != 0 && interleaved != 1))
+        return SSM_ERR_SHAPE;
+    for (int i = 0; i < 2; ++i)
+        if (a.heads[i] > 0 && a.stride[i] < (long long)a.heads[i] * a.dim) return SSM_ERR_SHAPE;
+    if (!dtype_ok(in) || !dtype_ok(out)) return SSM_ERR_DTYPE;
+    if (!sizes_fit(a.tokens, a.heads[0], a.heads[1], a.dim)) return SSM_ERR_UNSUPPORTED;
+    return SSM_OK;
+}
+
+int mode_of(const QkArgs& a, int interleaved) {
+    return interleaved ? kNeighbours : a.rot % 16 == 0 ? kHalves : kShared;
+}
+
+// Fills what the forward and the gradient share and checks the inputs they share.
+ssm_status_t shared_args(QkArgs& a, ssm_dtype_t in) {
+    using namespace ssm_host;
+    for (int i = 0; i < 2; ++i) {
+        if (a.heads[i] == 0) continue;
+        if (!a.x[i]) return SSM_ERR_NULL;
+        if (reinterpret_cast<uintptr_t>(a.x[i]) % dtype_size(in)) return SSM_ERR_ALIGN;
+        if (a.w[i] && !aligned16(a.w[i])) return SSM_ERR_ALIGN;
+        a.vec[i] = aligned16(a.x[i]) && a.stride[i] * dtype_size(in) % 16 == 0;
+    }
+    if (a.rot > 0 && (!a.pos || !a.freq)) return SSM_ERR_NULL;
+    if (a.rot > 0 && (reinterpret_cast<uintptr_t>(a.pos) % 8 || !aligned16(a.freq)))
+        return SSM_ERR_ALIGN;
+    a.inv_dim = 1.0f / (float)a.dim;
+    return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" ssm_status_t ssm_qk_norm_rope_fwd(
+    const void* q, const void* k, long long q_stride, long long k_stride, const float* q_weight,
+    const float* k_weight, const long long* positions, const double* inv_freq, float eps,
+    int rot_dim, int interleaved, void* q_out, void* k_out, long long tokens, int qheads,
+    int kheads, int headdim, ssm_dtype_t in_dtype, ssm_dtype_t out_dtype, void* stream) {
+    using namespace ssm_host;
+    QkArgs a{};
+    a.x[0] = q; a.x[1] = k; a.stride[0] = q_stride; a.stride[1] = k_stride;
+    a.w[0] = q_weight; a.w[1] = k_weight; a.pos = positions; a.freq = inv_freq;
+    a.eps = eps; a.rot = rot_dim; a.tokens = tokens; a.heads[0] = qheads; a.heads[1] = kheads;
+    a.dim = headdim; a.y[0] = q_out; a.y[1] = k_out;
+    if (ssm_status_t st = check_sizes(a, interleaved, in_dtype, out_dtype)) return st;
+    if (tokens == 0 || qheads + kheads == 0) return SSM_OK;
+    if (ssm_status_t st = shared_args(a, in_dtype)) return st;
+    size_t xb[2], yb[2];
+    for (int i = 0; i < 2; ++i) {
+        const long long width = (long long)a.heads[i] * headdim;
+        xb[i] = width ? strided_bytes(tokens, width, a.stride[i], dtype_size(in_dtype)) : 0;
+        yb[i] = (size_t)tokens * width * dtype_size(out_dtype);
+        if (width && !a.y[i]) return SSM_ERR_NULL;
+        if (width && !aligned16(a.y[i])) return SSM_ERR_ALIGN;
+    }
+    const Span ins[] = {{q, xb[0]}, {k, xb[1]}, {q_weight, (size_t)headdim * 4},
+                        {k_weight, (size_t)headdim * 4},
+                        {positions, rot_dim ? (size_t)tokens * 8 : 0},
+                        {inv_freq, (size_t)rot_dim * 4}};
+    for (const Span& i : ins)
+        for (int o = 0; o < 2; ++o)
+            if (overlaps(a.y[o], yb[o], i.p, i.n)) return SSM_ERR_ALIAS;
+    if (overlaps(q_out, yb[0], k_out, yb[1])) return SSM_ERR_ALIAS;
+
+    const int sms = sm_count();
+    if (sms == 0) return SSM_ERR_CUDA;
+    const int mode = mode_of(a, interleaved);
+    plan(a, mode, (long long)sms * kFwdCtas);
+    // every CTA takes one tile where the grid allows
+    const unsigned grid =
+        (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, 1 << 30);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
+        by_mode(mode, [&](auto m) {
+            qk_fwd_kernel<decltype(ti), decltype(to), decltype(m)::value>
+                <<<grid, kThreads, 0, s>>>(a);
+        });
+        return true;
+    });
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+extern "C" size_t ssm_qk_norm_rope_bwd_workspace_bytes(long long tokens, int qheads, int kheads,
+                                                       int headdim) {
+    if (!sizes_ok(tokens, qheads, kheads, headdim) || !sizes_fit(tokens, qheads, kheads, headdim))
+        return 0;
+    return 256 + (size_t)std::min<long long>(tokens, kBwdMost) * 2 * headdim * 4;
+}
+
+extern "C" ssm_status_t ssm_qk_norm_rope_bwd(
+    const void* dq_out, const void* dk_out, const void* q, const void* k, long long q_stride,
+    long long k_stride, const float* q_weight, const float* k_weight, const long long* positions,
+    const double* inv_freq, float eps, int rot_dim, int interleaved, void* dq, void* dk,
+    float* dq_weight, float* dk_weight, long long tokens, int qheads, int kheads, int headdim,
+    ssm_dtype_t in_dtype, ssm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+    void* stream) {
+    using namespace ssm_host;
+    QkArgs a{};
+    a.x[0] = q; a.x[1] = k; a.stride[0] = q_stride; a.stride[1] = k_stride;
+    a.w[0] = q_weight; a.w[1] = k_weight; a.pos = positions; a.freq = inv_freq;
+    a.eps = eps; a.rot = rot_dim; a.tokens = tokens; a.heads[0] = qheads; a.heads[1] = kheads;
+    a.dim = headdim; a.dy[0] = dq_out; a.dy[1] = dk_out; a.y[0] = dq; a.y[1] = dk;
+    a.join = dq_weight || dk_weight;
+    if (ssm_status_t st = check_sizes(a, interleaved, in_dtype, out_dtype)) return st;
+    float* dws[2] = {dq_weight, dk_weight};
+    for (float* d : dws)
+        if (d && !aligned16(d)) return SSM_ERR_ALIGN;
+    const size_t wb = (size_t)headdim * 4;
+    if (overlaps(dq_weight, wb, dk_weight, wb)) return SSM_ERR_ALIAS;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tokens == 0 || qheads + kheads == 0) {
+        for (float* d : dws)
+            if (d && cudaMemsetAsync(d, 0, wb, s) != cudaSuccess) return SSM_ERR_CUDA;
+        return SSM_OK;
+    }
+    if (ssm_status_t st = shared_args(a, in_dtype)) return st;
+    size_t xb[2], yb[2], gb[2];
+    for (int i = 0; i < 2; ++i) {
+        const long long width = (long long)a.heads[i] * headdim;
+        xb[i] = width ? strided_bytes(tokens, width, a.stride[i], dtype_size(in_dtype)) : 0;
+        yb[i] = (size_t)tokens * width * dtype_size(out_dtype);
+        gb[i] = (size_t)tokens * width * dtype_size(in_dtype);
+        if (width && (!a.dy[i] || !a.y[i])) return SSM_ERR_NULL;
+        if (width && (!aligned16(a.dy[i]) || !aligned16(a.y[i]))) return SSM_ERR_ALIGN;
+    }
+    const size_t need = ssm_qk_norm_rope_bwd_workspace_bytes(tokens, qheads, kheads, headdim);
+    if (a.join && (!workspace || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
+    if (a.join && !aligned16(workspace)) return SSM_ERR_ALIGN;
+    const Span ins[] = {{q, xb[0]}, {k, xb[1]}, {dq_out, yb[0]}, {dk_out, yb[1]}, {q_weight, wb},
+                        {k_weight, wb}, {positions, rot_dim ? (size_t)tokens * 8 : 0},
+                        {inv_freq, (size_t)rot_dim * 4}};
+    const Span outs[] = {{dq, gb[0]}, {dk, gb[1]}, {dq_weight, wb}, {dk_weight, wb},
+                         {workspace, a.join ? need : 0}};
+    for (const Span& o : outs)
+        for (const Span& i : ins)
+            if (overlaps(o.p, o.n, i.p, i.n)) return SSM_ERR_ALIAS;
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return SSM_ERR_ALIAS;
+
+    const int mode = mode_of(a, interleaved);
+    plan(a, mode, kBwdMost);
+    const unsigned grid = (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, kBwdMost);
+    a.partial = static_cast<float*>(workspace);
+    by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
+        by_mode(mode, [&](auto m) {
+            qk_bwd_kernel<decltype(ti), decltype(to), decltype(m)::value>
+                <<<grid, kThreads, 0, s>>>(a);
+        });
+        return true;
+    });
+    if (a.join)
+        qk_dw_kernel<<<(2 * headdim + 31) / 32, 1024, 0, s>>>(a.partial, (int)grid, headdim,
+                                                              dq_weight, dk_weight);
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
