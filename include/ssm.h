@@ -19,6 +19,7 @@
  *   ssm_linrec_fwd, _bwd  gated linear recurrence, one state per channel
  *   ssm_vocab_ce_fwd, _bwd  cross entropy over a vocabulary without the logits
  *   ssm_qk_norm_rope_fwd, _bwd  norms of query and key heads with the rotation by position
+ *   ssm_gated_delta_fwd, _bwd  gated delta rule, chunked and step by step
  *
  * Conventions shared by every entry point
  *  - Pointers are DEVICE pointers unless stated otherwise, to dense row-major
@@ -970,6 +971,59 @@ ssm_status_t ssm_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const 
                                   int kheads, int headdim, ssm_dtype_t in_dtype,
                                   ssm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/*
+ * Bytes of what ssm_gated_delta_fwd keeps for ssm_gated_delta_bwd (0 for sizes it does not
+ * take): per 64 steps and head the chunk's products of q, k and the gates, its entering
+ * state and its steps' errors (104 KB at dstate = headdim = 128).
+ */
+size_t ssm_gated_delta_checkpoint_bytes(int batch, int seqlen, int nheads, int dstate,
+                                        int headdim);
+
+/* Bytes of device workspace ssm_gated_delta_fwd needs (0 for sizes it does not take); 1024 are
+ * enough with checkpoints, and none are needed for a sequence that is walked. */
+size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int dstate, int headdim);
+
+/*
+ * Gated delta rule.
+ *   The scalar-decay state of ssd_chunked_fwd ("Mamba-3 NKI Kernels for AWS Neuron",
+ *   section "Kernel details": S = exp(dt A) S + dt B x^T, y = C S), with k for B, q for C
+ *   and v for x, whose input first takes out what the state already answers to k.
+ * For every batch b, head h (group = h / (nheads / ngroups)) and step t, S (headdim x
+ * dstate) from initial_state[b,h] (or 0):
+ *   S = exp(g) S;   u = beta (v - S k);   S = S + u k^T;   y = S q
+ *   final_state[b,h] = S after the last step.
+ * Keys are meant to have length one or less (ssm_qk_norm_rope_fwd makes such): with beta in
+ * (0, 1) and g <= 0 no step then makes a state grow.
+ * Masked steps: where beta is 0 neither k nor v is looked at (they may be NaN) and
+ * the state only decays; where g is -inf (any g < -207) the state starts anew, and at a
+ * sequence's first step so it does whatever initial_state holds.
+ * Layouts: q, k (batch, seqlen, ngroups, dstate) and v (batch, seqlen, nheads, headdim) in
+ *   in_dtype, heads contiguous and *_stride elements from one step to the next (the
+ *   batches follow one another), so that the three may be column ranges of one
+ *   projection; g, beta (batch, seqlen, nheads) in gate_dtype; y (batch, seqlen, nheads,
+ *   headdim) in out_dtype; initial_state, final_state (batch, nheads, headdim, dstate) fp32,
+ *   each may be NULL, and may be the same buffer; checkpoints: NULL, or
+ *   ssm_gated_delta_checkpoint_bytes bytes for ssm_gated_delta_bwd.
+ * q, k, v and their strides: multiples of 16 bytes (SSM_ERR_ALIGN); g and beta: their
+ * element's alignment.
+ * Supported: dstate a multiple of 8 up to 128, headdim a multiple of 8 up to 256, nheads a
+ * multiple of ngroups, seqlen < 2^30, batch * nheads * ceil(seqlen / 64) < 2^30; in_dtype
+ * SSM_BF16, or SSM_F32 without checkpoints.  seqlen == 0 hands the state on.
+ * fp32 sequences, and bf16 ones of up to 16 steps without checkpoints (a decode step: one),
+ * are walked step by step in fp32 and need no workspace.  Others are taken in chunks of
+ * 64 steps on the tensor cores; what enters their products beside q and k is held as the
+ * sum of two bf16, so y and the state are within about 1e-5 (2-norm) of the definition.
+ * Runs are bit-equal.  Bounded waits report through ssm_last_device_status.
+ */
+ssm_status_t ssm_gated_delta_fwd(const void* q, const void* k, const void* v, long long q_stride,
+                                 long long k_stride, long long v_stride, const void* g,
+                                 const void* beta, const float* initial_state, void* y,
+                                 float* final_state, void* checkpoints, int batch, int seqlen,
+                                 int nheads, int ngroups, int dstate, int headdim,
+                                 ssm_dtype_t in_dtype, ssm_dtype_t gate_dtype,
+                                 ssm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
 
 /*
  * Waits for `stream` to drain, then returns the device-side status the last

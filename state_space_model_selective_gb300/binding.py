@@ -41,7 +41,8 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssm_linrec_fwd", "ssm_linrec_bwd_workspace_bytes", "ssm_linrec_bwd",
            "ssm_vocab_ce_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd_workspace_bytes",
            "ssm_vocab_ce_bwd", "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd_workspace_bytes",
-           "ssm_qk_norm_rope_bwd"]
+           "ssm_qk_norm_rope_bwd", "ssm_gated_delta_checkpoint_bytes",
+           "ssm_gated_delta_workspace_bytes", "ssm_gated_delta_fwd"]
 
 
 class SSMError(RuntimeError):
@@ -156,6 +157,12 @@ def lib() -> ctypes.CDLL:
         L.ssm_qk_norm_rope_bwd.restype = i
         L.ssm_qk_norm_rope_bwd.argtypes = ([vp] * 4 + [ll] * 2 + [vp] * 4 + [fl, i, i] + [vp] * 4 +
                                            [ll] + [i] * 5 + [vp, sz, vp])
+        for f in (L.ssm_gated_delta_checkpoint_bytes, L.ssm_gated_delta_workspace_bytes):
+            f.restype = sz
+            f.argtypes = [i] * 5
+        L.ssm_gated_delta_fwd.restype = i
+        L.ssm_gated_delta_fwd.argtypes = ([vp] * 3 + [ll] * 3 + [vp] * 6 + [i] * 9 +
+                                          [vp, sz, vp])
         _lib = L
     return _lib
 
@@ -1468,3 +1475,78 @@ def ssm_qk_norm_rope_bwd(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None
                                     0 if workspace is None else workspace.numel(), _raw(stream, q))
     _check(st, "ssm_qk_norm_rope_bwd")
     return g
+
+
+def ssm_gated_delta_checkpoint_bytes(batch, seqlen, nheads, dstate, headdim) -> int:
+    return int(lib().ssm_gated_delta_checkpoint_bytes(batch, seqlen, nheads, dstate, headdim))
+
+
+def ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim) -> int:
+    return int(lib().ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim))
+
+
+_WALKED = 16  # steps a bf16 sequence is walked up to, without a workspace
+
+
+def _delta_args(q, k, v, g, beta, initial_state):
+    """(steps of q, k, v; batch, seqlen, nheads, ngroups, dstate, headdim)."""
+    for t, name in ((q, "q"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _DT:
+            raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
+    batch, seqlen, ngroups, dstate = q.shape
+    nheads, headdim = v.shape[2], v.shape[3]
+    if (nheads % ngroups if ngroups else nheads) != 0:
+        raise ValueError(f"nheads {nheads} must be a multiple of ngroups {ngroups}")
+    sq = _token_step(q, "q", q.dtype, q.shape)
+    sk = _token_step(k, "k", q.dtype, q.shape)
+    sv = _token_step(v, "v", q.dtype, (batch, seqlen, nheads, headdim))
+    _req(g, "g")
+    _dt_code(g.dtype, "g")
+    _like(g, "g", (batch, seqlen, nheads), g.dtype)
+    _like(beta, "beta", (batch, seqlen, nheads), g.dtype)
+    if initial_state is not None:
+        _like(initial_state, "initial_state", (batch, nheads, headdim, dstate), torch.float32)
+    return sq, sk, sv, batch, seqlen, nheads, ngroups, dstate, headdim
+
+
+def _delta_kept(checkpoints, *sizes):
+    if checkpoints is not None:
+        _req(checkpoints, "checkpoints", torch.uint8)
+        if checkpoints.numel() < ssm_gated_delta_checkpoint_bytes(*sizes):
+            raise ValueError("checkpoints is smaller than ssm_gated_delta_checkpoint_bytes(...)")
+
+
+def ssm_gated_delta_fwd(q, k, v, g, beta, initial_state=None, out_dtype=None, y=None,
+                        final_state=None, checkpoints=None, workspace=None,
+                        return_final_state=True, stream=None):
+    """Gated delta rule S = exp(g) S; u = beta (v - S k); S += u k^T; y = S q per head.  q,
+    k: (batch, seqlen, ngroups, dstate), v: (batch, seqlen, nheads, headdim), each contiguous
+    or a range of the columns of a projection; g, beta: (batch, seqlen, nheads) fp32 or
+    bf16; initial_state, final_state: (batch, nheads, headdim, dstate) fp32, which may be
+    the same tensor (a decode step in place).  A beta of 0 masks a step, a g of -inf starts
+    the state anew.  With ``checkpoints`` (a CUDA uint8 tensor of
+    ssm_gated_delta_checkpoint_bytes bytes) what ssm_gated_delta_bwd needs is kept.
+    Returns (y, final_state)."""
+    sq, sk, sv, *sizes = _delta_args(q, k, v, g, beta, initial_state)
+    batch, seqlen, nheads, ngroups, dstate, headdim = sizes
+    out_dt = q.dtype if out_dtype is None else out_dtype
+    code = _dt_code(out_dt, "out_dtype")
+    y = _out(y, "y", v, v.shape, out_dt, stream)
+    if final_state is not None or return_final_state:
+        final_state = _out(final_state, "final_state", v, (batch, nheads, headdim, dstate),
+                           torch.float32, stream)
+    five = batch, seqlen, nheads, dstate, headdim
+    _delta_kept(checkpoints, *five)
+    if workspace is not None or (q.dtype == torch.bfloat16 and
+                                 (checkpoints is not None or seqlen > _WALKED)):
+        need = 1024 if checkpoints is not None else ssm_gated_delta_workspace_bytes(*five)
+        workspace = _work(workspace, q, need, stream)
+    _one_device(q, k, v, g, beta, initial_state, y, final_state, checkpoints, workspace)
+    st = lib().ssm_gated_delta_fwd(_p(q), _p(k), _p(v), sq, sk, sv, _p(g), _p(beta),
+                                   _p(initial_state), _p(y), _p(final_state), _p(checkpoints),
+                                   *sizes, _DT[q.dtype], _DT[g.dtype], code, _p(workspace),
+                                   0 if workspace is None else workspace.numel(), _raw(stream, q))
+    _check(st, "ssm_gated_delta_fwd")
+    return y, final_state
