@@ -996,7 +996,7 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * Keys are meant to have length one or less (ssm_qk_norm_rope_fwd makes such): with beta in
  * (0, 1) and g <= 0 no step then makes a state grow.
  * Masked steps: where beta is 0 neither k nor v is looked at (they may be NaN) and
- * the state only decays; where g is -inf (any g < -207) the state starts anew, and at a
+ * the state only decays; where g is -inf (any g < -88) the state starts anew, and at a
  * sequence's first step so it does whatever initial_state holds.
  * Layouts: q, k (batch, seqlen, ngroups, dstate) and v (batch, seqlen, nheads, headdim) in
  *   in_dtype, heads contiguous and *_stride elements from one step to the next (the
@@ -1023,6 +1023,45 @@ ssm_status_t ssm_gated_delta_fwd(const void* q, const void* k, const void* v, lo
                                  int nheads, int ngroups, int dstate, int headdim,
                                  ssm_dtype_t in_dtype, ssm_dtype_t gate_dtype,
                                  ssm_dtype_t out_dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Bytes of device workspace ssm_gated_delta_bwd needs with checkpoints (0 for sizes it does
+ * not take); without them add ssm_gated_delta_checkpoint_bytes.
+ */
+size_t ssm_gated_delta_bwd_workspace_bytes(int batch, int seqlen, int nheads, int dstate,
+                                           int headdim);
+
+/*
+ * Gradient of ssm_gated_delta_fwd for the loss sum(dy * y) + sum(dfinal_state *
+ * final_state): with L the adjoint of S behind step t (from dfinal_state, or 0, backwards)
+ * and S the state the decay has left, e = v - S k,
+ *   L += dy q^T;  dq = S_t^T dy;  dbeta = (L k) . e;  dv = beta L k;
+ *   dk = beta L^T e - S^T dv;  L -= dv k^T;  dg = sum(L * S);  L = exp(g) L
+ *   dinitial_state = L before the first step.
+ * q, k, v and their strides, g, beta and initial_state as given to the forward; dy
+ * (batch, seqlen, nheads, headdim) in in_dtype, contiguous; dq, dk (batch, seqlen, ngroups,
+ * dstate; summed over the group's heads) and dv (batch, seqlen, nheads, headdim) in
+ * grad_dtype, contiguous; dg, dbeta (batch, seqlen, nheads) in gate_dtype; dfinal_state,
+ * dinitial_state (batch, nheads, headdim, dstate) fp32, each may be NULL, and may be the
+ * same buffer; checkpoints: what the forward kept for the same inputs, or NULL (the forward
+ * runs again, in a workspace that much larger).
+ * The gradients of a masked step (beta 0) with respect to k, v and beta are 0, and so is
+ * dg where g is -inf.  A key may only be NaN where all heads of its group mask the step.
+ * The adjoint of the state, dv and dinitial_state are as exact as the forward; dq, dk, dg
+ * and dbeta come from products of operands rounded to bf16 (summed in fp32): within about
+ * 3e-3 (2-norm), as far as their own rounding to bf16.
+ * Supported as ssm_gated_delta_fwd, in_dtype SSM_BF16.  Runs are bit-equal: sums over
+ * heads and steps have a fixed order.
+ */
+ssm_status_t ssm_gated_delta_bwd(const void* q, const void* k, const void* v, long long q_stride,
+                                 long long k_stride, long long v_stride, const void* g,
+                                 const void* beta, const float* initial_state, const void* dy,
+                                 const float* dfinal_state, const void* checkpoints, void* dq,
+                                 void* dk, void* dv, void* dg, void* dbeta, float* dinitial_state,
+                                 int batch, int seqlen, int nheads, int ngroups, int dstate,
+                                 int headdim, ssm_dtype_t in_dtype, ssm_dtype_t gate_dtype,
+                                 ssm_dtype_t grad_dtype, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
 /*

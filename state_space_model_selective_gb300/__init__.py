@@ -23,6 +23,7 @@ from .binding import (EXPORTS, SSMError, lib, ssd_chunked_bwd,  # noqa: F401
                       ssd_chunked_bwd_workspace_bytes, ssd_chunked_fwd, ssd_mamba3_fwd,
                       ssd_mamba3_mimo_fwd, ssm_abi_version, ssm_decode_step,
                       ssm_decode_step_mamba3, ssm_decode_step_mamba3_mimo,
+                      ssm_gated_delta_bwd, ssm_gated_delta_bwd_workspace_bytes,
                       ssm_gated_delta_checkpoint_bytes, ssm_gated_delta_fwd,
                       ssm_gated_delta_workspace_bytes,
                       ssm_last_device_status, ssm_qk_norm_rope_bwd,

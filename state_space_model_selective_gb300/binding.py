@@ -42,7 +42,8 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssm_vocab_ce_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd_workspace_bytes",
            "ssm_vocab_ce_bwd", "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd_workspace_bytes",
            "ssm_qk_norm_rope_bwd", "ssm_gated_delta_checkpoint_bytes",
-           "ssm_gated_delta_workspace_bytes", "ssm_gated_delta_fwd"]
+           "ssm_gated_delta_workspace_bytes", "ssm_gated_delta_fwd",
+           "ssm_gated_delta_bwd_workspace_bytes", "ssm_gated_delta_bwd"]
 
 
 class SSMError(RuntimeError):
@@ -157,11 +158,15 @@ def lib() -> ctypes.CDLL:
         L.ssm_qk_norm_rope_bwd.restype = i
         L.ssm_qk_norm_rope_bwd.argtypes = ([vp] * 4 + [ll] * 2 + [vp] * 4 + [fl, i, i] + [vp] * 4 +
                                            [ll] + [i] * 5 + [vp, sz, vp])
-        for f in (L.ssm_gated_delta_checkpoint_bytes, L.ssm_gated_delta_workspace_bytes):
+        for f in (L.ssm_gated_delta_checkpoint_bytes, L.ssm_gated_delta_workspace_bytes,
+                  L.ssm_gated_delta_bwd_workspace_bytes):
             f.restype = sz
             f.argtypes = [i] * 5
         L.ssm_gated_delta_fwd.restype = i
         L.ssm_gated_delta_fwd.argtypes = ([vp] * 3 + [ll] * 3 + [vp] * 6 + [i] * 9 +
+                                          [vp, sz, vp])
+        L.ssm_gated_delta_bwd.restype = i
+        L.ssm_gated_delta_bwd.argtypes = ([vp] * 3 + [ll] * 3 + [vp] * 12 + [i] * 9 +
                                           [vp, sz, vp])
         _lib = L
     return _lib
@@ -1550,3 +1555,52 @@ def ssm_gated_delta_fwd(q, k, v, g, beta, initial_state=None, out_dtype=None, y=
                                    0 if workspace is None else workspace.numel(), _raw(stream, q))
     _check(st, "ssm_gated_delta_fwd")
     return y, final_state
+
+
+def ssm_gated_delta_bwd_workspace_bytes(batch, seqlen, nheads, dstate, headdim) -> int:
+    return int(lib().ssm_gated_delta_bwd_workspace_bytes(batch, seqlen, nheads, dstate, headdim))
+
+
+def ssm_gated_delta_bwd(q, k, v, g, beta, dy, initial_state=None, dfinal_state=None,
+                        checkpoints=None, grad_dtype=None, workspace=None,
+                        want_dinitial_state=True, stream=None, out=None):
+    """Gradient of ``ssm_gated_delta_fwd`` for the loss sum(dy * y) + sum(dfinal_state *
+    final_state), bf16 inputs.  Inputs as for the forward; dy like v and contiguous;
+    checkpoints: what the forward kept, or None (it is run again).  Returns a dict: dq, dk, dv
+    in ``grad_dtype`` (q's type by default), dg, dbeta in g's type, dinitial_state fp32 (or
+    None).  ``out`` may map any of these names to a preallocated tensor to write."""
+    sq, sk, sv, *sizes = _delta_args(q, k, v, g, beta, initial_state)
+    batch, seqlen, nheads, ngroups, dstate, headdim = sizes
+    _like(dy, "dy", v.shape, q.dtype)
+    if dfinal_state is not None:
+        _like(dfinal_state, "dfinal_state", (batch, nheads, headdim, dstate), torch.float32)
+    five = batch, seqlen, nheads, dstate, headdim
+    _delta_kept(checkpoints, *five)
+    gd = q.dtype if grad_dtype is None else grad_dtype
+    code = _dt_code(gd, "grad_dtype")
+    out = out or {}
+    wants = {"dq": (q.shape, gd), "dk": (q.shape, gd), "dv": (v.shape, gd),
+             "dg": (g.shape, g.dtype), "dbeta": (g.shape, g.dtype)}
+    if want_dinitial_state or "dinitial_state" in out:
+        wants["dinitial_state"] = ((batch, nheads, headdim, dstate), torch.float32)
+    for name in out:
+        if name not in wants:
+            raise ValueError(f"out[{name!r}] is not an output of this call")
+    grads = {"dinitial_state": None}
+    for name, (shape, dt) in wants.items():
+        grads[name] = _out(out.get(name), f"out[{name!r}]", q, shape, dt, stream)
+    need = ssm_gated_delta_bwd_workspace_bytes(*five)
+    if checkpoints is None:
+        need += ssm_gated_delta_checkpoint_bytes(*five)
+    workspace = _work(workspace, q, need, stream)
+    _one_device(q, k, v, g, beta, initial_state, dy, dfinal_state, checkpoints, workspace,
+                *grads.values())
+    st = lib().ssm_gated_delta_bwd(_p(q), _p(k), _p(v), sq, sk, sv, _p(g), _p(beta),
+                                   _p(initial_state), _p(dy), _p(dfinal_state), _p(checkpoints),
+                                   _p(grads["dq"]), _p(grads["dk"]), _p(grads["dv"]),
+                                   _p(grads["dg"]), _p(grads["dbeta"]),
+                                   _p(grads["dinitial_state"]), *sizes, _DT[q.dtype],
+                                   _DT[g.dtype], code, _p(workspace), workspace.numel(),
+                                   _raw(stream, q))
+    _check(st, "ssm_gated_delta_bwd")
+    return grads

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssm.so")
 SOURCES = ["scan.cu", "scan_seg.cu", "rope.cu", "scan_bwd.cu", "scan_host.cu", "decode.cu", "ssd.cu", "ssd_bwd.cu",
-           "norm.cu", "linrec.cu", "vocab_ce.cu", "qk_norm.cu", "gated_delta.cu", "api.cu"]
+           "norm.cu", "linrec.cu", "vocab_ce.cu", "qk_norm.cu", "gated_delta.cu",
+           "gated_delta_bwd.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                      "-Xptxas", "-v"]
