@@ -32,11 +32,6 @@ struct WalkArgs {
     int batch, seqlen, heads, groups, dk, dv, gates_bf16;
 };
 
-__device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-                : static_cast<const float*>(p)[i];
-}
-
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     const uint2 w = *reinterpret_cast<const uint2*>(p);
@@ -142,15 +137,18 @@ constexpr int kPitch = 68;  // floats between the rows of the triangle
 
 template <int DK> struct RecSmem {
     static constexpr uint32_t kq = 0;                    // panels of [K 64 rows | Q 64 rows]
-    static constexpr uint32_t p_hi = (DK / 64) * 2 * kTile;
-    static constexpr uint32_t p_lo = p_hi + kTile;
-    static constexpr uint32_t t_hi = p_lo + kTile;       // T', rows i, columns j
+    static constexpr uint32_t t_hi = kq_bytes(DK);       // T', rows i, columns j
     static constexpr uint32_t t_lo = t_hi + kTile;
     static constexpr uint32_t w_hi = t_lo + kTile;       // diag(w) T'
     static constexpr uint32_t w_lo = w_hi + kTile;
-    static constexpr uint32_t tri = w_lo + kTile;        // A, then T (fp32)
-    static constexpr uint32_t misc = tri + kC * kPitch * 4;
+    static constexpr uint32_t p_hi = w_lo + kTile;       // (Q K^T) D
+    static constexpr uint32_t p_lo = p_hi + kTile;
+    static constexpr uint32_t gates = p_lo + kTile;      // as the record has them
+    static constexpr uint32_t misc = gates + kGateBytes;
     static constexpr uint32_t bytes = misc + 1024;
+    // A, then T (fp32), in the place of T' and its w's first tile; H and P leave from there too
+    static constexpr uint32_t tri = t_hi;
+    static constexpr uint32_t tmp = w_lo;
 };
 
 struct RecArgs {
@@ -158,23 +156,32 @@ struct RecArgs {
     uint8_t* records;
     uint32_t* status;
     Dims d;
+    long long count;  // of chunks and heads
     int gates_bf16;
-    int keep_t;      // T' is wanted (training)
+    int keep_t;       // T' is wanted (training)
 };
 
 // T = (1 + A)^-1 in place, A strictly lower 64 x 64 (zeros above).  The four 16 x 16
 // blocks on the diagonal by substitution, a thread to a column, then blocks joined in
 // pairs: the lower left of [[X, 0], [L, Z]]^-1 is -Z^-1 L X^-1.  `tmp`: 32 x 36 floats.
+// In fp32: what is lost here no later product gives back.
 __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid) {
     if (tid < 64) {
         const int b = (tid >> 4) * 16, c = tid & 15;
+        const float* base = m + b * kPitch + b;
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            float s = r == c ? 1.0f : 0.0f;
+            float s = r == c ? 1.0f : 0.0f, s2 = 0.0f;
 #pragma unroll
-            for (int j = 0; j < r; ++j) s = fmaf(-m[(b + r) * kPitch + b + j], x[j], s);
-            x[r] = s;
+            for (int j = 0; j < r; j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(base + r * kPitch + j);
+                s = fmaf(-l.x, x[j], s);
+                if (j + 1 < r) s2 = fmaf(-l.y, x[j + 1], s2);
+                if (j + 2 < r) s = fmaf(-l.z, x[j + 2], s);
+                if (j + 3 < r) s2 = fmaf(-l.w, x[j + 3], s2);
+            }
+            x[r] = s + s2;
         }
         __syncwarp();  // a block's columns are read and written by one half warp
 #pragma unroll
@@ -183,61 +190,76 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
     __syncthreads();
     // joins of 16: blocks (1, 0) and (3, 2); two elements to a thread
     {
-        const int pair = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2;
-        const float* L = m + (pair * 32 + 16) * kPitch + pair * 32;
-        const float* X = m + pair * 32 * kPitch + pair * 32;
-        const float* Z = X + 16 * kPitch + 16;
+        const int two = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2;
+        const float* X = m + two * 32 * kPitch + two * 32;
+        const float* L = X + 16 * kPitch;
+        const float* Z = L + 16;
         float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float l = L[r * kPitch + j];
-            a0 = fmaf(l, X[j * kPitch + c], a0);
-            a1 = fmaf(l, X[j * kPitch + c + 1], a1);
+        for (int j = 0; j < 16; j += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(L + r * kPitch + j);
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = *reinterpret_cast<const float2*>(X + (j + e) * kPitch + c);
+                a0 = fmaf(lv[e], x.x, a0);
+                a1 = fmaf(lv[e], x.y, a1);
+            }
         }
-        float* t = tmp + (pair * 16 + r) * 36 + c;
-        t[0] = a0;
-        t[1] = a1;
+        *reinterpret_cast<float2*>(tmp + (two * 16 + r) * 36 + c) = make_float2(a0, a1);
         __syncthreads();
         a0 = a1 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float z = Z[r * kPitch + j];
-            a0 = fmaf(-z, tmp[(pair * 16 + j) * 36 + c], a0);
-            a1 = fmaf(-z, tmp[(pair * 16 + j) * 36 + c + 1], a1);
+        for (int j = 0; j < 16; j += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(Z + r * kPitch + j);
+            const float zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = *reinterpret_cast<const float2*>(tmp + (two * 16 + j + e) * 36 + c);
+                a0 = fmaf(-zv[e], x.x, a0);
+                a1 = fmaf(-zv[e], x.y, a1);
+            }
         }
-        float* o = m + (pair * 32 + 16 + r) * kPitch + pair * 32 + c;
-        o[0] = a0;
-        o[1] = a1;
+        *reinterpret_cast<float2*>(m + (two * 32 + 16 + r) * kPitch + two * 32 + c) = make_float2(a0, a1);
     }
     __syncthreads();
     // join of 32: four elements to a thread
     {
         const int r = tid >> 3, c = (tid & 7) * 4;
-        const float* L = m + 32 * kPitch;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) {
-            const float l = L[r * kPitch + j];
-            const float4 x = *reinterpret_cast<const float4*>(m + j * kPitch + c);
-            s.x = fmaf(l, x.x, s.x); s.y = fmaf(l, x.y, s.y);
-            s.z = fmaf(l, x.z, s.z); s.w = fmaf(l, x.w, s.w);
+        const float* L = m + (32 + r) * kPitch;
+        f2 s0 = 0, s1 = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(L + j);
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(m + (j + e) * kPitch + c);
+                s0 = fma2(pair(lv[e], lv[e]), x.x, s0);
+                s1 = fma2(pair(lv[e], lv[e]), x.y, s1);
+            }
         }
-        *reinterpret_cast<float4*>(tmp + r * 36 + c) = s;
+        *reinterpret_cast<ulonglong2*>(tmp + r * 36 + c) = make_ulonglong2(s0, s1);
         __syncthreads();
-        s = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float* Z = m + 32 * kPitch + 32;
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) {
-            const float z = -Z[r * kPitch + j];
-            const float4 x = *reinterpret_cast<const float4*>(tmp + j * 36 + c);
-            s.x = fmaf(z, x.x, s.x); s.y = fmaf(z, x.y, s.y);
-            s.z = fmaf(z, x.z, s.z); s.w = fmaf(z, x.w, s.w);
+        s0 = s1 = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(L + 32 + j);
+            const float zv[4] = {-z.x, -z.y, -z.z, -z.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(tmp + (j + e) * 36 + c);
+                s0 = fma2(pair(zv[e], zv[e]), x.x, s0);
+                s1 = fma2(pair(zv[e], zv[e]), x.y, s1);
+            }
         }
-        *reinterpret_cast<float4*>(m + (32 + r) * kPitch + c) = s;
+        *reinterpret_cast<ulonglong2*>(m + (32 + r) * kPitch + c) = make_ulonglong2(s0, s1);
     }
     __syncthreads();
 }
 
+// CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
+// this one's H and P leave.
 template <int DK>
 __global__ void __launch_bounds__(kRecThreads, 2)
     records_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -245,201 +267,327 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = RecSmem<DK>;
     constexpr int NP = DK / 64;
-    constexpr uint32_t kTmX = 0, kTmH = 64, kTmP = 128, kTmCols = 256;
+    // tensor memory: [K; Q] K^T, then H (hi and lo columns); P (hi and lo columns)
+    constexpr uint32_t kTmX = 0, kTmH = 0, kTmP = 128, kTmCols = 256;
     const uint32_t sb = smem_u32(smem);
     float* tri = reinterpret_cast<float*>(smem + M::tri);
-    float* tmp = reinterpret_cast<float*>(smem + M::t_hi);  // before T' is written there
-    float* s_hi = reinterpret_cast<float*>(smem + M::misc);
-    float* s_lo = s_hi + kC;
-    float* s_beta = s_lo + kC;
-    long long* s_sum = reinterpret_cast<long long*>(s_beta + kC);
-    uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);  // masked, NaN (two words each)
+    float* tmp = reinterpret_cast<float*>(smem + M::tmp);
+    Gates* gates = reinterpret_cast<Gates*>(smem + M::gates);
+    float* s_beta = reinterpret_cast<float*>(smem + M::misc);
+    float* s_most = s_beta + kC;                                  // [2][8]
+    long long* s_sum = reinterpret_cast<long long*>(s_most + 16);
+    uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN (two words each)
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 4);
     uint64_t* bar_mma = bar_in + 1;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mma + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
-    const long long ch = blockIdx.x;
-    const int c = (int)(ch % a.d.chunks);
-    const long long bh = ch / a.d.chunks;
-    const int b = (int)(bh / a.d.heads), h = (int)(bh % a.d.heads);
-    const int group = h / (a.d.heads / a.d.groups), t0 = c * kC;
-    uint8_t* rec = a.records + ch * rec_bytes(DK);
+    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane, i = row & 63;
+    const bool is_q = row >= kC;
 
+    auto load = [&](long long ch) {  // K and Q of a chunk (one thread)
+        const int c = (int)(ch % a.d.chunks);
+        const long long bh = ch / a.d.chunks;
+        const int b = (int)(bh / a.d.heads), group = (int)(bh % a.d.heads) / (a.d.heads / a.d.groups);
+        mbar_arrive_expect_tx(bar_in, kq_bytes(DK));
+        for (int p = 0; p < NP; ++p) {
+            tma_load_4d(smem + M::kq + p * 2 * kTile, &tm_k, bar_in, 64 * p, group, c * kC, b);
+            tma_load_4d(smem + M::kq + p * 2 * kTile + kTile, &tm_q, bar_in, 64 * p, group, c * kC, b);
+        }
+    };
+    float g = 0.0f, beta = 0.0f;  // of step tid, one chunk ahead
+    auto fetch = [&](long long ch) {
+        if (tid >= kC) return;
+        const int t = (int)(ch % a.d.chunks) * kC + tid;
+        const long long bh = ch / a.d.chunks;
+        const long long at = ((bh / a.d.heads) * a.d.seqlen + t) * a.d.heads + bh % a.d.heads;
+        const bool in = t < a.d.seqlen;
+        g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
+        beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
+    };
+    if ((long long)blockIdx.x < a.count) fetch(blockIdx.x);
     if (warp == 0) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
         mbar_init(bar_in, 1);
         mbar_init(bar_mma, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(bar_in, NP * 2 * kTile);
-        for (int p = 0; p < NP; ++p) {
-            tma_load_4d(smem + M::kq + p * 2 * kTile, &tm_k, bar_in, 64 * p, group, t0, b);
-            tma_load_4d(smem + M::kq + p * 2 * kTile + kTile, &tm_q, bar_in, 64 * p, group, t0, b);
-        }
-    }
-    // the gates: base-2 logarithms summed as integers of 2^-32, so that differences of far
-    // sums are as exact as near ones (a decay of 2^-300 and less is 0 all the same)
-    long long sum = 0;
-    if (tid < kC) {
-        const int t = t0 + tid;
-        const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + h;
-        const bool in = t < a.d.seqlen;
-        const float g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
-        const float beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
-        s_beta[tid] = beta;
-        const float g2 = fminf(fmaxf(g * kLog2e, -300.0f), 300.0f);
-        sum = __float2ll_rn(g2 * 4294967296.0f);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
-        }
-        const uint32_t off = __ballot_sync(0xffffffffu, beta == 0.0f);
-        const uint32_t bad = __ballot_sync(0xffffffffu, isnan(g));
-        if (lane == 0) {
-            s_flags[warp] = off;
-            s_flags[2 + warp] = bad;
-        }
-        if (tid == 31) *s_sum = sum;
+        if ((long long)blockIdx.x < a.count) load(blockIdx.x);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-    const unsigned long long masked = (unsigned long long)s_flags[1] << 32 | s_flags[0];
-    if (tid < kC) {
-        if (warp == 1) sum += *s_sum;
-        const unsigned long long bad = (unsigned long long)s_flags[3] << 32 | s_flags[2];
-        float hi = (float)sum;
-        const float lo = (float)(sum - (long long)hi) * 2.3283064365386963e-10f;  // 2^-32
-        hi *= 2.3283064365386963e-10f;
-        if (bad & (~0ull >> (63 - tid))) hi = __int_as_float(0x7fc00000);
-        s_hi[tid] = hi;
-        s_lo[tid] = lo;
-        Gates* gates = reinterpret_cast<Gates*>(rec + hp_bytes(DK) + kTile);
-        gates->hi[tid] = hi;
-        gates->lo[tid] = lo;
-        if (tid == 0) gates->masked = masked;
-    }
-    bool ok = warp_wait(bar_in, 0, a.status);
-    if (masked) {  // steps that learn nothing: their keys are not looked at
-        if (ok)
-            for (int e = tid; e < NP * kC * 8; e += kRecThreads) {
-                const int r = (e >> 3) & 63;
-                if (masked >> r & 1)
-                    *reinterpret_cast<uint4*>(smem + M::kq + (e >> 9) * 2 * kTile + r * 128 +
-                                              (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-        fence_proxy_async_smem();
-    }
-    ok = __syncthreads_and(ok);
+    bool ok = true;
+    bool landing = false;  // (thread 0) a load is on its way
+    uint32_t mma_phase = 0, in_phase = 0;
 
-    // ---- [K; Q] K^T
-    if (tid == 0 && ok) {
+    for (long long ch = blockIdx.x; ch < a.count && ok; ch += gridDim.x) {
+        uint8_t* rec = a.records + ch * rec_bytes(DK);
+        const bool more = ch + gridDim.x < a.count;
+        // ---- the gates: base-2 logarithms summed as integers of 2^-32, so that differences
+        // of far sums are as exact as near ones (a decay of 2^-300 and less is 0 all the same)
+        long long sum = 0;
+        if (tid < kC) {
+            s_beta[tid] = beta;
+            const float g2 = fminf(fmaxf(g * kLog2e, -300.0f), 300.0f);
+            sum = __float2ll_rn(g2 * 4294967296.0f);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += u;
+            }
+            const uint32_t off = __ballot_sync(0xffffffffu, beta == 0.0f);
+            const uint32_t bad = __ballot_sync(0xffffffffu, isnan(g));
+            if (lane == 0) {
+                s_flags[warp] = off;
+                s_flags[2 + warp] = bad;
+            }
+            if (tid == 31) *s_sum = sum;
+        }
+        if (tid == 0) bulk_wait_read_all();  // the last chunk's stores have left shared memory
+        __syncthreads();
+        const unsigned long long masked = (unsigned long long)s_flags[1] << 32 | s_flags[0];
+        if (tid < kC) {
+            if (warp == 1) sum += *s_sum;
+            const unsigned long long bad = (unsigned long long)s_flags[3] << 32 | s_flags[2];
+            float hi = (float)sum;
+            const float lo = (float)(sum - (long long)hi) * 2.3283064365386963e-10f;  // 2^-32
+            hi *= 2.3283064365386963e-10f;
+            if (bad & (~0ull >> (63 - tid))) hi = __int_as_float(0x7fc00000);
+            gates->hi[tid] = hi;
+            gates->lo[tid] = lo;
+            if (tid == 0) gates->masked = masked;
+            const float e = ex2_approx(hi + lo);
+            const float m = warp_most<2>((const float[2]){e, 0.0f});
+            if (lane == 0) s_most[8 + warp] = m;
+        }
+        if (more) fetch(ch + gridDim.x);
+
+        // ---- K and Q to fp16, in place, under one factor.  Steps that learn nothing: their
+        // keys are not looked at
+        ok = warp_wait(bar_in, in_phase, a.status);
+        in_phase ^= 1;
+        landing = false;
+        uint4 raw[NP * 4];
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < NP * 4; ++e) {
+            const int at = tid + kRecThreads * e, r = (at >> 3) & 127;
+            raw[e] = *reinterpret_cast<const uint4*>(smem + M::kq + at * 16);
+            if (r < kC && (masked >> r & 1)) raw[e] = make_uint4(0, 0, 0, 0);
+            float x[8];
+            unpack8_bf16(raw[e], x);
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) most = fmaxf(most, fmaxf(fabsf(x[k]), fabsf(x[k + 1])));
+        }
+        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+        if (lane == 0) s_most[warp] = most;
+        ok = __syncthreads_and(ok);
+        float s_kq;
+        const float kq_scale = tile_scale(most_of<8>(s_most), kTop, s_kq);
+#pragma unroll
+        for (int e = 0; e < NP * 4; ++e) {
+            float x[8];
+            uint32_t w[4];
+            unpack8_bf16(raw[e], x);
+            round_to<8>(x, kq_scale, w);
+            *reinterpret_cast<uint4*>(smem + M::kq + (tid + kRecThreads * e) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (tid == 0) {
+            gates->s_kq = s_kq;
+            gates->e_max = fmaxf(s_most[8], s_most[9]);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+
+        // ---- [K; Q] K^T
+        if (tid == 0 && ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < DK / 16; ++kk)
+                mma_f16(tmem + kTmX, kdesc<128>(sb + M::kq, kk), kdesc<128>(sb + M::kq, kk),
+                        idesc_f16(128, 64), kk > 0);
+            mma_commit(bar_mma);
+            bulk_store(rec + rec_kq(DK), smem + M::kq, kq_bytes(DK));
+            bulk_commit();
+        }
+        ok = warp_wait(bar_mma, mma_phase, a.status) && ok;
+        mma_phase ^= 1;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk)
-            mma_bf16(tmem + kTmX, kdesc<128>(sb + M::kq, kk), kdesc<128>(sb + M::kq, kk),
-                     idesc_bf16_f32(128, 64), kk > 0);
-        mma_commit(bar_mma);
-    }
-    ok = __syncthreads_and(ok && warp_wait(bar_mma, 0, a.status));
-    tc_fence_after();
-    {
         float x[32];
-        tmem_ld32(t_lane + kTmX + 32 * part, x);
-        tmem_wait_ld();
-        const int i = row & 63;
-        const bool is_q = row >= kC;
-        const float hi = s_hi[i], lo = s_lo[i], beta = is_q ? 1.0f : s_beta[i];
-        const int last = is_q ? i : i - 1;  // of the columns that count
+        if (ok) {
+            tmem_ld32(t_lane + kTmX + 32 * part, x);
+            tmem_wait_ld();
+            const float hi = gates->hi[i], lo = gates->lo[i];
+            const float f = s_kq * s_kq * (is_q ? 1.0f : s_beta[i]);
+            const int last = is_q ? i : i - 1;  // of the columns that count
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const int j = 32 * part + e;
-            x[e] = j <= last ? beta * x[e] * decay(hi, lo, s_hi[j], s_lo[j]) : 0.0f;
+            for (int e = 0; e < 32; e += 4) {
+                const int j = 32 * part + e;
+                const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
+                const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
+                x[e] = j <= last ? f * x[e] * decay(hi, lo, h4.x, l4.x) : 0.0f;
+                x[e + 1] = j + 1 <= last ? f * x[e + 1] * decay(hi, lo, h4.y, l4.y) : 0.0f;
+                x[e + 2] = j + 2 <= last ? f * x[e + 2] * decay(hi, lo, h4.z, l4.z) : 0.0f;
+                x[e + 3] = j + 3 <= last ? f * x[e + 3] * decay(hi, lo, h4.w, l4.w) : 0.0f;
+            }
+            if (!is_q)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(tri + i * kPitch + 32 * part + e) =
+                        make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        }
+        most = warp_most<32>(x);
+        if (lane == 0 && is_q) s_most[(quarter & 1) * 2 + part] = most;
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        float s_p;  // of the operand (Q K^T) D
+        const float p_scale = tile_scale(most_of<4>(s_most), kTop, s_p);
+        if (is_q) {
+            uint32_t hw[16], lw[16];
+            split<32>(x, p_scale, hw, lw);
+            put32(smem + M::p_hi, i, 4 * part, hw);
+            put32(smem + M::p_lo, i, 4 * part, lw);
+        }
+        invert_unit_lower(tri, tmp, tid);
+
+        // ---- T' and diag(w) T' as operands: row r = tid / 4, 16 columns
+        float s_t, s_w;
+        {
+            const int r = tid >> 2, j0 = (tid & 3) * 16;
+            const float w = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[r], gates->lo[r]);
+            float t[16], wt[16];
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 m4 = *reinterpret_cast<const float4*>(tri + r * kPitch + j0 + e);
+                const float4 b4 = *reinterpret_cast<const float4*>(s_beta + j0 + e);
+                t[e] = m4.x * b4.x; t[e + 1] = m4.y * b4.y;
+                t[e + 2] = m4.z * b4.z; t[e + 3] = m4.w * b4.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) wt[e] = w * t[e];
+            const float mt = warp_most<16>(t), mw = warp_most<16>(wt);
+            if (lane == 0) {
+                s_most[warp] = mt;
+                s_most[8 + warp] = mw;
+            }
+            __syncthreads();  // (the triangle has been read)
+            const float t_scale = tile_scale(most_of<8>(s_most), kTop, s_t);
+            const float w_scale = tile_scale(most_of<8>(s_most + 8), kTop, s_w);
+            uint32_t th[8], tl[8], wh[8], wl[8];
+            split<16>(t, t_scale, th, tl);
+            split<16>(wt, w_scale, wh, wl);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint32_t off = piece(r, (j0 >> 3) + s);
+                auto put = [&](uint32_t tile, const uint32_t* v) {
+                    *reinterpret_cast<uint4*>(smem + tile + off) =
+                        make_uint4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+                };
+                put(M::t_hi, th);
+                put(M::t_lo, tl);
+                put(M::w_hi, wh);
+                put(M::w_lo, wl);
+            }
+            if (tid == 0) gates->s_t = s_t;
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+
+        // ---- H = K^T diag(w) T' (rows of dstate) and P T' (rows 64 to 127: the tile of 128
+        // rows starts one tile early, its first half is not read); columns 64 to 127: the
+        // right operand's lo part
+        if (tid == 0 && ok) {
+            tc_fence_after();
+            constexpr uint32_t idH = idesc_f16(128, 128) | kIdescAMN | kIdescBMN;
+            constexpr uint32_t idP = idesc_f16(128, 128) | kIdescBMN;
+            constexpr uint32_t idP64 = idesc_f16(128, 64) | kIdescBMN;
+            // of 64 columns of dstate the second block of rows is not read either
+            constexpr uint32_t lbo = NP > 1 ? 2 * kTile : kTile;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16(tmem + kTmH, mdesc(sb + M::kq, kk, lbo), mdesc(sb + M::w_hi, kk, kTile), idH, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_hi - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
+                        idP, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
+                        idP64, 1);
+            mma_commit(bar_mma);
+            if (a.keep_t) {
+                bulk_store(rec + rec_t(DK), smem + M::t_hi, kTile);
+                bulk_commit();
+            }
+        }
+        ok = warp_wait(bar_mma, mma_phase, a.status) && ok;
+        mma_phase ^= 1;
+        tc_fence_after();
+        if (tid == 0 && ok) {
+            bulk_wait_read_all();   // K, Q and T' have left
+            if (more) load(ch + gridDim.x);
+            landing = more;
+        }
+        float hx[32], px[32];
+        if (ok) {
+            float y[32];
+            if (row < DK) {
+                tmem_ld32(t_lane + kTmH + 32 * part, hx);
+                tmem_ld32(t_lane + kTmH + 64 + 32 * part, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) hx[e] += y[e];
+            }
+            if (is_q) {
+                tmem_ld32(t_lane + kTmP + 32 * part, px);
+                tmem_ld32(t_lane + kTmP + 64 + 32 * part, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) px[e] += y[e];
+            }
+        }
+        const float mh = row < DK ? warp_most<32>(hx) : 0.0f;
+        const float mp = is_q ? warp_most<32>(px) : 0.0f;
+        if (lane == 0) {
+            s_most[warp] = mh;
+            s_most[8 + warp] = mp;
+        }
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        float s_h2, s_p2;
+        const float h_scale = tile_scale(most_of<8>(s_most), kTop, s_h2);
+        const float p2_scale = tile_scale(most_of<8>(s_most + 8), kTop, s_p2);
+        uint32_t hw[16], lw[16];
+        if (row < DK) {
+            split<32>(hx, h_scale, hw, lw);
+            put32(smem + M::t_hi, row, 4 * part, hw);
+            put32(smem + M::t_hi + h_bytes(DK), row, 4 * part, lw);
         }
         if (is_q) {
-            put32_split(smem + M::p_hi, smem + M::p_lo, i, 4 * part, x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(tri + i * kPitch + 32 * part + e) =
-                    make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            split<32>(px, p2_scale, hw, lw);
+            put32(smem + M::p_hi, i, 4 * part, hw);
+            put32(smem + M::p_lo, i, 4 * part, lw);
+        }
+        if (tid == 0) {
+            gates->s_h = s_h2 * s_kq * s_w;
+            gates->s_p = s_p2 * s_p * s_t;
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_store(rec, smem + M::gates, kGateBytes);
+            bulk_store(rec + rec_h(DK), smem + M::t_hi, 2 * h_bytes(DK));
+            bulk_store(rec + rec_p(DK), smem + M::p_hi, 2 * kTile);
+            bulk_commit();
         }
     }
-    __syncthreads();
-    invert_unit_lower(tri, tmp, tid);
-
-    // ---- T' and diag(w) T' as operands: row i = tid / 4, 16 columns
-    {
-        const int i = tid >> 2, j0 = (tid & 3) * 16;
-        const float w = decay(s_hi[kC - 1], s_lo[kC - 1], s_hi[i], s_lo[i]);
-        uint32_t th[8], tl[8], wh[8], wl[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const int j = j0 + e;
-            const float x = tri[i * kPitch + j] * s_beta[j];
-            const float y = tri[i * kPitch + j + 1] * s_beta[j + 1];
-            split2(x, y, th[e >> 1], tl[e >> 1]);
-            split2(w * x, w * y, wh[e >> 1], wl[e >> 1]);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const uint32_t off = piece(i, (j0 >> 3) + s);
-            const uint4 hi4 = make_uint4(th[4 * s], th[4 * s + 1], th[4 * s + 2], th[4 * s + 3]);
-            *reinterpret_cast<uint4*>(smem + M::t_hi + off) = hi4;
-            *reinterpret_cast<uint4*>(smem + M::t_lo + off) =
-                make_uint4(tl[4 * s], tl[4 * s + 1], tl[4 * s + 2], tl[4 * s + 3]);
-            *reinterpret_cast<uint4*>(smem + M::w_hi + off) =
-                make_uint4(wh[4 * s], wh[4 * s + 1], wh[4 * s + 2], wh[4 * s + 3]);
-            *reinterpret_cast<uint4*>(smem + M::w_lo + off) =
-                make_uint4(wl[4 * s], wl[4 * s + 1], wl[4 * s + 2], wl[4 * s + 3]);
-            if (a.keep_t) *reinterpret_cast<uint4*>(rec + hp_bytes(DK) + off) = hi4;
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-
-    // ---- H = K^T diag(w) T' (rows of dstate) and P T' (rows 64 to 127: the tile of 128
-    // rows starts one tile early, its first half is not read)
-    if (tid == 0 && ok) {
-        tc_fence_after();
-        constexpr uint32_t idH = idesc_bf16_f32(128, 64) | kIdescAMN | kIdescBMN;
-        constexpr uint32_t idP = idesc_bf16_f32(128, 64) | kIdescBMN;
-        // of 64 columns of dstate the second block of rows is not read either
-        constexpr uint32_t lbo = NP > 1 ? 2 * kTile : kTile;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            mma_bf16(tmem + kTmH, mdesc(sb + M::kq, kk, lbo), mdesc(sb + M::w_hi, kk, kTile), idH, kk > 0);
-            mma_bf16(tmem + kTmH, mdesc(sb + M::kq, kk, lbo), mdesc(sb + M::w_lo, kk, kTile), idH, 1);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ph = kdesc<128>(sb + M::p_hi - kTile, kk);
-            const uint64_t pl = kdesc<128>(sb + M::p_lo - kTile, kk);
-            mma_bf16(tmem + kTmP, ph, mdesc(sb + M::t_hi, kk, kTile), idP, kk > 0);
-            mma_bf16(tmem + kTmP, ph, mdesc(sb + M::t_lo, kk, kTile), idP, 1);
-            mma_bf16(tmem + kTmP, pl, mdesc(sb + M::t_hi, kk, kTile), idP, 1);
-        }
-        mma_commit(bar_mma);
-    }
-    ok = ok && warp_wait(bar_mma, 1, a.status);
-    tc_fence_after();
-    if (ok) {
-        float x[32];
-        if (row < DK) {
-            tmem_ld32(t_lane + kTmH + 32 * part, x);
-            tmem_wait_ld();
-            put32_split(rec, rec + h_bytes(DK), row, 4 * part, x);
-        }
-        if (row >= kC) {
-            tmem_ld32(t_lane + kTmP + 32 * part, x);
-            tmem_wait_ld();
-            put32_split(rec + 2 * h_bytes(DK), rec + 2 * h_bytes(DK) + kTile, row - kC, 4 * part, x);
-        }
+    if (tid == 0) {
+        bulk_wait_all();
+        if (landing) (void)mbar_wait(bar_in, in_phase, a.status);  // never leave with one landing
     }
     tc_fence_before();
     __syncthreads();
@@ -450,20 +598,24 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 constexpr int kChainThreads = 288;  // 8 warps on rows, one that loads and multiplies
 
-template <int DK> struct ChainSmem {
-    static constexpr uint32_t kq = 0;                              // of a stage
-    static constexpr uint32_t hp = (DK / 64) * 2 * kTile;
-    static constexpr uint32_t stage = hp + hp_bytes(DK);
+// PLO: P's lo part is multiplied too (y in fp32)
+template <int DK, bool PLO> struct ChainSmem {
+    // of a stage: the record up to P, then the tile of v (one box)
+    static constexpr uint32_t kq = rec_kq(DK);
+    static constexpr uint32_t h = rec_h(DK);
+    static constexpr uint32_t p = rec_p(DK);
+    static constexpr uint32_t rec = p + (PLO ? 2 : 1) * kTile;
+    static constexpr uint32_t v = rec;
+    static constexpr uint32_t stage = v + kTile;
     static constexpr uint32_t s_hi = 2 * stage;                    // S0, rows of dstate
     static constexpr uint32_t s_lo = s_hi + h_bytes(DK);
     static constexpr uint32_t r_hi = s_lo + h_bytes(DK);           // R, rows of steps
     static constexpr uint32_t r_lo = r_hi + kTile;
     static constexpr uint32_t misc = r_lo + kTile;
-    static constexpr uint32_t bytes = misc + 128;
+    static constexpr uint32_t bytes = misc + 512;
 };
 
 struct ChainArgs {
-    const __nv_bfloat16* v;
     const uint8_t* records;
     uint8_t* kept;
     const float* h0;
@@ -471,22 +623,28 @@ struct ChainArgs {
     void* y;
     uint32_t* status;
     Dims d;
-    long long v_step;
 };
 
 // One head and 64 columns of headdim, chunk after chunk.  Rows of products are lanes of
 // tensor memory: of K S0 and Q S0 the steps (0 to 63 and 64 to 127), of H R the state's
 // rows, of P R the steps (64 to 127).  Two warpgroups take 32 columns each.  The state stays
-// in registers (a row of dstate to a lane) and goes through shared memory as the sum of
-// two bf16 each chunk, as R does.
+// in registers (a row of dstate to a lane) and goes through shared memory as hi + lo each
+// chunk, as R does.  Right operands are [hi | lo] side by side, 128 columns to an
+// instruction: it reads 4 KB of A either way, and at 64 columns that reading bounds it (55
+// cycles an instruction against 64 for twice the columns).
+//
+// The factors of S and R have to be known before they are written, and a reduction over
+// the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
+// |S1| <= e_63 |S| + |H|_1 |R|, with the measured maxima of V and S, found while products
+// run.  A bound 2^20 too large would still leave 20 bits.
 template <int DK, typename TO>
 __global__ void __launch_bounds__(kChainThreads, 1)
-    chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const ChainArgs a) {
+    chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using M = ChainSmem<DK>;
-    constexpr int NP = DK / 64;
-    constexpr uint32_t kTmX = 0, kTmH = 64, kTmY = 128, kTmCols = 256;
+    constexpr bool PLO = sizeof(TO) == 4;
+    using M = ChainSmem<DK, PLO>;
+    // tensor memory, hi and lo columns each: [K; Q] S0, H R, P R
+    constexpr uint32_t kTmX = 0, kTmH = 128, kTmY = 256, kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // a stage has come in
     uint64_t* bar_x = full + 2;   // [K; Q] S0 done
@@ -495,25 +653,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_s = full + 5;   // S0 is in shared memory
     uint64_t* bar_r = full + 6;   // R is
     uint64_t* bar_o = full + 7;   // P R has been read
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 8);
+    uint64_t* bar_m = full + 8;   // the largest values of S0 and V are known
+    float* s_most = reinterpret_cast<float*>(full + 9);  // [2 chunks][8 warps of S, 4 of V]
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pan = blockIdx.x % a.d.pans;
     const long long bh = blockIdx.x / a.d.pans;
     const int b = (int)(bh / a.d.heads), h = (int)(bh % a.d.heads);
     const int nc = a.d.chunks;
-    const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        mbar_init(full, 1);
-        mbar_init(full + 1, 1);
-        mbar_init(bar_x, 1);
-        mbar_init(bar_h, 1);
-        mbar_init(bar_y, 1);
+        for (int n = 0; n < 5; ++n) mbar_init(full + n, 1);
         mbar_init(bar_s, 8);
         mbar_init(bar_r, 4);
         mbar_init(bar_o, 4);
+        mbar_init(bar_m, 8);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -523,22 +679,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            const int group = h / (a.d.heads / a.d.groups);
+            const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             int loads = 0;
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
-                uint64_t* bar = full + (c & 1);
-                mbar_arrive_expect_tx(bar, M::stage);
-                for (int p = 0; p < NP; ++p) {
-                    tma_load_4d(st + M::kq + p * 2 * kTile, &tm_k, bar, 64 * p, group, c * kC, b);
-                    tma_load_4d(st + M::kq + p * 2 * kTile + kTile, &tm_q, bar, 64 * p, group, c * kC, b);
-                }
-                bulk_load(st + M::hp, rec0 + (long long)c * rec_bytes(DK), hp_bytes(DK), bar);
+                mbar_arrive_expect_tx(full + (c & 1), M::stage);
+                bulk_load(st, rec0 + (long long)c * rec_bytes(DK), M::rec, full + (c & 1));
+                tma_load_4d(st + M::v, &tm_v, full + (c & 1), pan * kPan, h, c * kC, b);
                 ++loads;
             };
             load(0);
             if (nc > 1) load(1);
-            constexpr uint32_t id = idesc_bf16_f32(128, 64) | kIdescBMN;
+            constexpr uint32_t id = idesc_f16(128, 128) | kIdescBMN;
+            constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescBMN;
             int waited = 0;
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
@@ -547,29 +700,32 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (!mbar_wait(bar_s, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) {
-                    mma_bf16(tmem + kTmX, kdesc<128>(st + M::kq, kk), mdesc(sb + M::s_hi, kk, kTile), id, kk > 0);
-                    mma_bf16(tmem + kTmX, kdesc<128>(st + M::kq, kk), mdesc(sb + M::s_lo, kk, kTile), id, 1);
-                }
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmX, kdesc<128>(st + M::kq, kk), mdesc(sb + M::s_hi, kk, h_bytes(DK)),
+                            id, kk > 0);
                 mma_commit(bar_x);
                 if (!mbar_wait(bar_r, ph, a.status)) break;
                 tc_fence_after();
-                const uint32_t hh = st + M::hp, hl = hh + h_bytes(DK), pp = hl + h_bytes(DK);
+                const uint32_t hh = st + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
+                // (of 64 rows of H the 64 behind them are not read)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
-                    mma_bf16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r_lo, kk, kTile), id, 1);
-                    mma_bf16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r_hi, kk, kTile), id, 1);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r_hi, kk, kTile), id64, 1);
                 mma_commit(bar_h);
                 if (c > 0 && !mbar_wait(bar_o, ph ^ 1, a.status)) break;
                 tc_fence_after();
+                // P in rows 64 to 127: its tile of 128 rows starts one tile early
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
-                    mma_bf16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r_lo, kk, kTile), id, 1);
-                    mma_bf16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r_hi, kk, kTile), id, 1);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r_hi, kk, kTile),
+                            PLO ? id : id64, kk > 0);
+                if constexpr (PLO)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r_hi, kk, kTile), id64, 1);
                 mma_commit(bar_y);
                 if (c + 2 < nc) {
                     if (!mbar_wait(bar_y, ph, a.status)) break;
@@ -591,100 +747,177 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int e = 0; e < 32; ++e)
             S[e] = a.h0 && row < a.d.dk && col0 + e < a.d.dv
                        ? a.h0[(bh * a.d.dv + col0 + e) * a.d.dk + row] : 0.0f;
+        // what a chunk's rows take from its gates, read before the stage can be refilled
+        float f_row = 0.0f, e_end = 0.0f, k_bound = 0.0f, h_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        bool off = true, cut = false;
+        auto gates_of = [&](int c) {
+            const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status);
+            const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
+            const float e = ex2_approx(g->hi[i] + g->lo[i]);
+            cut = e == 0.0f;  // the chunk starts anew before this row, whatever S0 is
+            f_row = e * g->s_kq;
+            e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
+            off = g->masked >> i & 1;
+            s_h = g->s_h;
+            s_p = g->s_p;
+            // bounds of e |K|_1 and |H|_1 over a row, in units of the largest S and R
+            k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
+            h_bound = kC * 2 * kTopValue * s_h;
+            return in;
+        };
+        // the largest values of S (all warps) and of the next V (the warps on Q rows), for
+        // the factors of chunk c
+        auto maxima = [&](int c) {
+            const float m = warp_most<32>(S);
+            if (lane == 0) s_most[12 * (c & 1) + warp] = m;
+            if (!on_k) {
+                float v = 0.0f;
+                const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    float x[8];
+                    unpack8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p)), x);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) v = fmaxf(v, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
+                }
+                if (off) v = 0.0f;
+                v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+                if (lane == 0) s_most[12 * (c & 1) + 8 + (quarter & 1) * 2 + part] = v;
+            }
+            warp_arrive(bar_m);
+        };
         // S0 of chunk c as an operand, and kept
-        auto put_state = [&](int c) {
+        float s_s = 0.0f;  // S0's factor, undone
+        auto put_state = [&](int c, float bound) {
+            const float scale = tile_scale(bound, kBoundTop, s_s);
+            uint32_t hw[16], lw[16];
             if (row < DK) {
-                put32_split(smem + M::s_hi, smem + M::s_lo, row, 4 * part, S);
-                if (a.kept)
-                    put32(a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK) + kTile, row,
-                          4 * part, S);
+                split<32>(S, scale, hw, lw);
+                put32(smem + M::s_hi, row, 4 * part, hw);
+                put32(smem + M::s_lo, row, 4 * part, lw);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(bar_s);
+            if (a.kept) {
+                uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
+                if (row < DK) put32(k + kTile, row, 4 * part, hw);
+                if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK) + 4) = s_s;
+            }
         };
-        put_state(0);
-        // what a chunk's rows take from global memory, read one chunk ahead
-        uint4 v[4];
-        float e_row = 0.0f, e_end = 0.0f;
-        bool off = true;
-        auto fetch = [&](int c) {
-            const Gates* g = reinterpret_cast<const Gates*>(rec0 + (long long)c * rec_bytes(DK) +
-                                                            hp_bytes(DK) + kTile);
-            e_row = ex2_approx(g->hi[i] + g->lo[i]);
-            e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
-            off = g->masked >> i & 1;
-            const long long t = (long long)b * a.d.seqlen + c * kC + i;
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                v[p] = on_k && !off && col0 + 8 * p < a.d.dv
-                           ? *reinterpret_cast<const uint4*>(a.v + t * a.v_step + (long long)h * a.d.dv +
-                                                             col0 + 8 * p)
-                           : make_uint4(0, 0, 0, 0);
-        };
-        fetch(0);
-        for (int c = 0; c < nc; ++c) {
+        {   // the first chunk: its largest values are measured
+            const float m = warp_most<32>(S);
+            if (lane == 0) s_most[12 + warp] = m;
+            named_bar_sync(1, 256);
+            put_state(0, most_of<8>(s_most + 12));
+        }
+        bool ok = gates_of(0);
+        if (ok) maxima(0);
+        for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
-            const float er = e_row, ee = e_end;
+            const float fs = f_row * s_s, ee = e_end, sp = s_p, sh = s_h, hb = h_bound;
+            const bool none = cut;
             float x[32];
-            if (!warp_wait(bar_x, ph, a.status)) break;
+            ok = warp_wait(bar_m, ph, a.status) && warp_wait(bar_x, ph, a.status);
+            if (!ok) break;
             tc_fence_after();
+            const float s_max = most_of<8>(s_most + 12 * ph);
+            const float r_bound = fmaf(k_bound, s_max, most_of<4>(s_most + 12 * ph + 8));
+            float s_r;
+            const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
             tmem_ld32(t_lane + kTmX, x);
-            tmem_wait_ld();
+            if (on_k || PLO) {
+                float y[32];
+                tmem_ld32(t_lane + kTmX + 64, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] += y[e];
+            } else {
+                tmem_wait_ld();
+            }
             if (on_k) {
                 // (the products that read R before are done: bar_x follows them)
+                const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    float vv[8];
-                    unpack8(v[p], vv);
+                    float v[8];
+                    unpack8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p)), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float carried = er == 0.0f ? 0.0f : er * x[8 * p + e];
-                        x[8 * p + e] = off ? 0.0f : vv[e] - carried;
-                    }
+                    for (int e = 0; e < 8; ++e) x[8 * p + e] = none ? v[e] : fmaf(-fs, x[8 * p + e], v[e]);
                 }
-                put32_split(smem + M::r_hi, smem + M::r_lo, i, 4 * part, x);
+                if (off)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0.0f;
+                uint32_t hw[16], lw[16];
+                split<32>(x, r_scale, hw, lw);
+                put32(smem + M::r_hi, i, 4 * part, hw);
+                put32(smem + M::r_lo, i, 4 * part, lw);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(bar_r);
-                if (a.kept)
-                    put32(a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK), i, 4 * part, x);
+                if (a.kept) {
+                    uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
+                    put32(k, i, 4 * part, hw);
+                    if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK)) = s_r;
+                }
             }
-            if (c + 1 < nc) fetch(c + 1);
-            float z[32];
-            if (!warp_wait(bar_h, ph, a.status)) break;
+            ok = warp_wait(bar_h, ph, a.status);
+            if (!ok) break;
             tc_fence_after();
-            tmem_ld32(t_lane + kTmH, z);
-            tmem_wait_ld();
+            if (ee == 0.0f)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) S[e] = ee == 0.0f ? z[e] : fmaf(ee, S[e], z[e]);
-            if (c + 1 < nc) put_state(c + 1);
-            if (!on_k) {
-                if (!warp_wait(bar_y, ph, a.status)) break;
-                tc_fence_after();
-                tmem_ld32(t_lane + kTmY, z);
+                for (int e = 0; e < 32; ++e) S[e] = 0.0f;
+#pragma unroll
+            for (int e0 = 0; e0 < 32; e0 += 16) {
+                const f2 f = pair(sh * s_r, sh * s_r), e2 = pair(ee, ee);
+                float z[16], y[16];
+                tmem_ld16(t_lane + kTmH + e0, z);
+                tmem_ld16(t_lane + kTmH + 64 + e0, y);
                 tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const f2 hr = add2(pair(z[e], z[e + 1]), pair(y[e], y[e + 1]));
+                    unpair(fma2(e2, pair(S[e0 + e], S[e0 + e + 1]), mul2(f, hr)), S[e0 + e], S[e0 + e + 1]);
+                }
+            }
+            if (c + 1 < nc) {
+                put_state(c + 1, fmaf(ee, s_max, hb * r_bound));
+                ok = gates_of(c + 1);
+                if (!ok) break;
+                maxima(c + 1);
+            }
+            if (!on_k) {
+                ok = warp_wait(bar_y, ph, a.status);
+                if (!ok) break;
+                tc_fence_after();
+                float z[32];
+                tmem_ld32(t_lane + kTmY, z);
+                if constexpr (PLO) {
+                    float y[32];
+                    tmem_ld32(t_lane + kTmY + 64, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) z[e] += y[e];
+                } else {
+                    tmem_wait_ld();
+                }
                 tc_fence_before();
                 warp_arrive(bar_o);
                 const int t = c * kC + i;
                 if (a.y && t < a.d.seqlen) {
                     TO* y = static_cast<TO*>(a.y) +
                             (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
+                    const float f = sp * s_r;
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         if (col0 + 8 * p >= a.d.dv) break;
                         float o[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            o[e] = er == 0.0f ? z[8 * p + e] : fmaf(er, x[8 * p + e], z[8 * p + e]);
-                        if constexpr (sizeof(TO) == 4) {
-                            *reinterpret_cast<float4*>(y + 8 * p) = make_float4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<float4*>(y + 8 * p + 4) = make_float4(o[4], o[5], o[6], o[7]);
-                        } else {
-                            *reinterpret_cast<uint4*>(y + 8 * p) =
-                                make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
-                                           pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+                        for (int e = 0; e < 8; ++e) {
+                            const float own = f * z[8 * p + e];
+                            o[e] = none ? own : fmaf(fs, x[8 * p + e], own);
                         }
+                        store8(y + 8 * p, o);
                     }
                 }
             }
@@ -709,30 +942,34 @@ bool allow_smem(K kernel, uint32_t bytes) {
 
 template <int DK>
 ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
-    CUtensorMap mq, mk;
+    CUtensorMap mq, mk, mv;
     if (!gdn_host::make_map(&mq, f.q, f.batch, f.seqlen, f.groups, f.dk, f.q_step) ||
-        !gdn_host::make_map(&mk, f.k, f.batch, f.seqlen, f.groups, f.dk, f.k_step))
+        !gdn_host::make_map(&mk, f.k, f.batch, f.seqlen, f.groups, f.dk, f.k_step) ||
+        !gdn_host::make_map(&mv, f.v, f.batch, f.seqlen, f.heads, f.dv, f.v_step))
         return SSM_ERR_CUDA;
+    const int sms = ssm_host::sm_count();
+    if (sms == 0) return SSM_ERR_CUDA;
     Dims d{f.batch, f.seqlen, f.heads, f.groups, f.dk, f.dv, (f.seqlen + kC - 1) / kC,
            (f.dv + kPan - 1) / kPan};
     RecArgs r{};
     r.g = f.g; r.beta = f.beta; r.records = f.records; r.status = f.status; r.d = d;
     r.gates_bf16 = f.gate_dtype == SSM_BF16;
     r.keep_t = f.kept != nullptr;
-    const unsigned chs = (unsigned)((long long)f.batch * f.heads * d.chunks);
+    r.count = (long long)f.batch * f.heads * d.chunks;
     if (!allow_smem(records_kernel<DK>, RecSmem<DK>::bytes)) return SSM_ERR_CUDA;
-    records_kernel<DK><<<chs, kRecThreads, RecSmem<DK>::bytes, s>>>(mq, mk, r);
+    records_kernel<DK><<<(unsigned)std::min<long long>(r.count, 2 * sms), kRecThreads,
+                         RecSmem<DK>::bytes, s>>>(mq, mk, r);
     ChainArgs a{};
-    a.v = static_cast<const __nv_bfloat16*>(f.v); a.records = f.records; a.kept = f.kept;
-    a.h0 = f.initial_state; a.last = f.final_state; a.y = f.y; a.status = f.status; a.d = d;
-    a.v_step = f.v_step;
+    a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;
+    a.y = f.y; a.status = f.status; a.d = d;
     const unsigned grid = (unsigned)((long long)f.batch * f.heads * d.pans);
-    auto go = [&](auto kernel) {
-        if (!allow_smem(kernel, ChainSmem<DK>::bytes)) return false;
-        kernel<<<grid, kChainThreads, ChainSmem<DK>::bytes, s>>>(mq, mk, a);
+    auto go = [&](auto kernel, uint32_t bytes) {
+        if (!allow_smem(kernel, bytes)) return false;
+        kernel<<<grid, kChainThreads, bytes, s>>>(mv, a);
         return true;
     };
-    if (!(f.out_dtype == SSM_F32 ? go(chain_kernel<DK, float>) : go(chain_kernel<DK, __nv_bfloat16>)))
+    if (!(f.out_dtype == SSM_F32 ? go(chain_kernel<DK, float>, ChainSmem<DK, true>::bytes)
+                                 : go(chain_kernel<DK, __nv_bfloat16>, ChainSmem<DK, false>::bytes)))
         return SSM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

@@ -12,7 +12,14 @@
 //   S1 = e_63 S0 + H R,  H = K^T diag(w) T'
 // P and H depend on q, k and the gates alone, so one kernel makes them for all chunks at
 // once, and the chain over the chunks is two products deep: K S0 and H R.
+//
+// Operands are fp16 under one power of two per tile, chosen from the tile's largest value
+// or a bound of it: bf16 inputs are exact in it down to 2^-30 of that, a value as the sum
+// of two fp16 (hi + lo) is to 2^-22, where two bf16 leave 2^-17 and cost the same products.
+// (With bf16 the state of 1000 steps was 5e-6 off, 2-norm.)
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "tcgen05.cuh"
@@ -21,73 +28,155 @@ namespace gdn {
 
 using namespace ssm;
 
-constexpr int kC = 64;          // steps of a chunk
-constexpr int kPan = 64;        // columns of headdim that one chain takes
-constexpr uint32_t kTile = 8192;  // a 64 x 64 bf16 tile: 64 rows of 128 bytes
-
-// The record of one chunk and head (bytes): H hi | H lo (dstate rows each) | P hi |
-// P lo | T' | the gates.  Tiles are stored as they lie in shared memory: rows of 128
-// bytes whose 16-byte pieces are XORed with (row mod 8), so that one bulk copy
-// brings H and P in.  hi + lo: a value as the sum of two bf16, 2^-17 of it off.
-constexpr uint32_t kGateBytes = 1024;
-__host__ __device__ constexpr uint32_t h_bytes(int dk) { return (uint32_t)dk * 128u; }
-__host__ __device__ constexpr uint32_t hp_bytes(int dk) { return 2 * h_bytes(dk) + 2 * kTile; }
-__host__ __device__ constexpr uint32_t rec_bytes(int dk) {
-    return hp_bytes(dk) + kTile + kGateBytes;
-}
-// What training keeps for each chunk, head and 64 columns of headdim: R | S0 (forward),
-// dR | dS1 (gradient), rounded to bf16: only products whose results are rounded to bf16
-// themselves read them.
-__host__ __device__ constexpr uint32_t kept_bytes(int dk) { return kTile + h_bytes(dk); }
+constexpr int kC = 64;            // steps of a chunk
+constexpr int kPan = 64;          // columns of headdim that one chain takes
+constexpr uint32_t kTile = 8192;  // a 64 x 64 fp16 tile: 64 rows of 128 bytes
 
 // The gates of a record: base-2 logarithms of the decay from the chunk's start as the
-// sum of two floats, and a bit for every step that learns nothing.
+// sum of two floats, a bit for every step that learns nothing, and what the tiles have to
+// be multiplied with.
 struct Gates {
     float hi[kC], lo[kC];
     unsigned long long masked;
+    float s_kq, s_h, s_p, s_t;
+    float e_max;   // the largest decay from the chunk's start to a step
 };
+constexpr uint32_t kGateBytes = 1024;
 static_assert(sizeof(Gates) <= kGateBytes, "gates fit their place");
+
+// The record of one chunk and head (bytes): gates | panels of K and Q (64 columns of
+// dstate: 64 rows each) | H hi | H lo (dstate rows) | P hi | P lo | T'.  Tiles are stored as
+// they lie in shared memory: rows of 128 bytes whose 16-byte pieces are XORed with (row mod
+// 8), so that one bulk copy brings in what the chain needs.
+__host__ __device__ constexpr uint32_t h_bytes(int dk) { return (uint32_t)dk * 128u; }
+__host__ __device__ constexpr uint32_t kq_bytes(int dk) { return (uint32_t)(dk / 64) * 2 * kTile; }
+__host__ __device__ constexpr uint32_t rec_kq(int) { return kGateBytes; }
+__host__ __device__ constexpr uint32_t rec_h(int dk) { return kGateBytes + kq_bytes(dk); }
+__host__ __device__ constexpr uint32_t rec_p(int dk) { return rec_h(dk) + 2 * h_bytes(dk); }
+__host__ __device__ constexpr uint32_t rec_t(int dk) { return rec_p(dk) + 2 * kTile; }
+__host__ __device__ constexpr uint32_t rec_bytes(int dk) { return rec_t(dk) + kTile; }
+// What training keeps for each chunk, head and 64 columns of headdim, rounded to one fp16:
+// R | S0 | their factors (forward), dR | dY | L | their factors (gradient).  Only products
+// whose results are rounded to bf16 read them.
+constexpr uint32_t kFactorBytes = 128;
+__host__ __device__ constexpr uint32_t kept_bytes(int dk) { return kTile + h_bytes(dk) + kFactorBytes; }
+__host__ __device__ constexpr uint32_t adjoint_bytes(int dk) { return 2 * kTile + h_bytes(dk) + kFactorBytes; }
 
 __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
     return ex2_approx((hi_i - hi_j) + (lo_i - lo_j));
 }
 
+// ------------------------------------------------- two floats to an instruction
+
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// ------------------------------------------------------------------ rounding
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// (a, b) = hi + lo, each a pair of bf16.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hp, uint32_t& lp) {
-    hp = pack_bf16(a, b);
-    lp = pack_bf16(a - bf16lo(hp), b - bf16hi(hp));
+// n values times `scale` as hi + lo, pairs.
+template <int N>
+__device__ __forceinline__ void split(const float* v, float scale, uint32_t* hi, uint32_t* lo) {
+    const f2 s = pair(scale, scale);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+        float a, b;
+        const f2 x = mul2(pair(v[2 * e], v[2 * e + 1]), s);
+        unpair(x, a, b);
+        hi[e] = pack_f16(a, b);
+        const float2 h = unpack_f16(hi[e]);
+        unpair(add2(x, pair(-h.x, -h.y)), a, b);
+        lo[e] = pack_f16(a, b);
+    }
 }
+template <int N>
+__device__ __forceinline__ void round_to(const float* v, float scale, uint32_t* hi) {
+    const f2 s = pair(scale, scale);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+        float a, b;
+        unpair(mul2(pair(v[2 * e], v[2 * e + 1]), s), a, b);
+        hi[e] = pack_f16(a, b);
+    }
+}
+
+// A tile's factor: a power of two that brings `most` (the largest magnitude, or a bound of
+// it) to 2^top or less than twice that; `back` undoes it.  Infinities and NaN stay what
+// they are, values below 2^-100 count as that.
+__device__ __forceinline__ float tile_scale(float most, int top, float& back) {
+    const uint32_t e = min(max(__float_as_uint(most) >> 23 & 0xffu, 27u), 254u);
+    const uint32_t f = 254u + (uint32_t)top - e;   // 127 + top - (e - 127)
+    const uint32_t g = min(f, 253u);
+    back = __uint_as_float((254u - g) << 23);
+    return __uint_as_float(g << 23);
+}
+constexpr int kTop = 12;    // of a measured maximum
+constexpr int kBoundTop = 14;  // of a bound
+// The largest stored magnitude of a tile scaled by its maximum.
+constexpr float kTopValue = 8192.0f;
+
+// The largest magnitude of n values over a warp (NaN aside).
+template <int N>
+__device__ __forceinline__ float warp_most(const float* v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) m = fmaxf(m, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+template <int N>
+__device__ __forceinline__ float most_of(const float* s) {
+    float m = s[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) m = fmaxf(m, s[e]);
+    return m;
+}
+
+// -------------------------------------------------------------------- tiles
 
 // Byte offset of 16-byte piece c of row r of a tile of 128-byte rows.
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
 }
-
-// 32 values as the 4 pieces c0 .. c0 + 3 of row r, split into a hi and a lo tile.
-__device__ __forceinline__ void put32_split(uint8_t* hi, uint8_t* lo, int r, int c0, const float* v) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split2(v[8 * c + 2 * e], v[8 * c + 2 * e + 1], h[e], l[e]);
-        const uint32_t off = piece(r, c0 + c);
-        *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-}
-// The same, rounded to one tile.
-__device__ __forceinline__ void put32(uint8_t* tile, int r, int c0, const float* v) {
+// 32 values (16 packed pairs) as pieces c0 .. c0 + 3 of row r.
+__device__ __forceinline__ void put32(uint8_t* tile, int r, int c0, const uint32_t* w) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         *reinterpret_cast<uint4*>(tile + piece(r, c0 + c)) =
-            make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                       pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
-__device__ __forceinline__ void unpack8(uint4 w, float* f) {
+__device__ __forceinline__ void unpack8_bf16(uint4 w, float* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -95,13 +184,43 @@ __device__ __forceinline__ void unpack8(uint4 w, float* f) {
         f[2 * e + 1] = bf16hi(u[e]);
     }
 }
+__device__ __forceinline__ void unpack8_f16(uint4 w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 h = unpack_f16(u[e]);
+        f[2 * e] = h.x;
+        f[2 * e + 1] = h.y;
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float* o) {
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* o) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                              pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+}
+__device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+                : static_cast<const float*>(p)[i];
+}
 
-// K-major operand (rows of 64 bf16 along the contraction) of R rows, k-step kk.
+// Instruction descriptor, kind::f16 with fp16 operands and fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+    mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);  // the types are the descriptor's
+}
+
+// K-major operand (rows of 64 values along the contraction) of R rows, k-step kk.
 template <int R>
 __device__ __forceinline__ uint64_t kdesc(uint32_t tile, int kk) {
     return smem_desc_k128(tile + (uint32_t)((kk >> 2) * (R * 128) + (kk & 3) * 32));
 }
-// MN-major operand (one row of 64 bf16 per step of the contraction), k-step kk;
+// MN-major operand (one row of 64 values per step of the contraction), k-step kk;
 // further blocks of 64 `lbo` bytes apart.
 __device__ __forceinline__ uint64_t mdesc(uint32_t tile, int kk, uint32_t lbo) {
     return smem_desc_mn128(tile + (uint32_t)kk * 2048u, lbo);
@@ -114,6 +233,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
             smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+// `bytes` (a multiple of 16) of shared memory to global memory, in the thread's bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
 }
 
 // One arrival of a warp whose lanes have all come this far.
@@ -172,6 +298,10 @@ inline size_t records_bytes(int batch, int seqlen, int heads, int dk) {
 }
 inline size_t keep_bytes(int batch, int seqlen, int heads, int dk, int dv) {
     return chunk_count(batch, seqlen, heads) * ((dv + 63) / 64) * gdn::kept_bytes(dk_tile(dk));
+}
+
+inline size_t adjoints_bytes(int batch, int seqlen, int heads, int dk, int dv) {
+    return chunk_count(batch, seqlen, heads) * ((dv + 63) / 64) * gdn::adjoint_bytes(dk_tile(dk));
 }
 
 struct Span { const void* p; size_t n; };

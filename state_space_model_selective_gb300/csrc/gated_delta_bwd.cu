@@ -21,49 +21,38 @@ namespace {
 
 using namespace gdn;
 
-__device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-                : static_cast<const float*>(p)[i];
-}
 __device__ __forceinline__ void put_gate(void* p, long long i, int bf16, float v) {
     if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
     else static_cast<float*>(p)[i] = v;
 }
-__device__ __forceinline__ void store8(float* p, const float* o) {
-    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* o) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
-                                              pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-}
-
 // ------------------------------------------------------------------ chain
 
 constexpr int kChainThreads = 288;
 
 template <int DK> struct ChainSmem {
     static constexpr uint32_t k_bytes = (DK / 64) * kTile;
-    // a stage: K panels, H hi | lo
-    static constexpr uint32_t stage = k_bytes + 2 * h_bytes(DK);
+    // a stage: gates, K panels, H hi | lo
+    static constexpr uint32_t k = kGateBytes;
+    static constexpr uint32_t h = k + k_bytes;
+    static constexpr uint32_t stage = h + 2 * h_bytes(DK);
     static constexpr uint32_t q = 2 * stage;
-    static constexpr uint32_t p = q + k_bytes;               // P hi | lo, dY
-    static constexpr uint32_t dy = p + 2 * kTile;
-    static constexpr uint32_t l_hi = dy + kTile;             // L, rows of dstate
+    static constexpr uint32_t p = q + k_bytes;               // P hi | lo
+    static constexpr uint32_t l_hi = p + 2 * kTile;          // L, rows of dstate
     static constexpr uint32_t l_lo = l_hi + h_bytes(DK);
-    static constexpr uint32_t o_hi = l_lo + h_bytes(DK);     // e dY, rows of steps
+    static constexpr uint32_t dy = l_lo + h_bytes(DK);       // dY, rows of steps
+    static constexpr uint32_t o_hi = dy + kTile;             // e dY
     static constexpr uint32_t o_lo = o_hi + kTile;
     static constexpr uint32_t r_hi = o_lo + kTile;           // -e dR
     static constexpr uint32_t r_lo = r_hi + kTile;
     static constexpr uint32_t xch = r_lo + kTile;            // 64 x 64 fp32, columns first
     static constexpr uint32_t misc = xch + 64 * 64 * 4;
-    static constexpr uint32_t bytes = misc + 128;
+    static constexpr uint32_t bytes = misc + 512;
 };
 
 struct ChainArgs {
     const __nv_bfloat16* dy;
     const uint8_t* records;
-    uint8_t* kept;          // dR | L
+    uint8_t* kept;          // dR | dY | L
     const float* dlast;
     float* dh0;
     void* dv;
@@ -71,28 +60,32 @@ struct ChainArgs {
     Dims d;
 };
 
-// Products with a hi and a lo operand on the left put both into the 128 rows of one
-// instruction: rows 64 to 127 of dR's tensor memory are its lo part, added through shared
-// memory.
+// One head and 64 columns of headdim, backwards; laid out as the forward's chain.  H^T L and
+// P^T dY have 64 rows, so both parts of the left operand go into the 128 rows of one
+// instruction: rows 64 to 127 are their lo part, added through shared memory.  The warps on
+// those rows also make dY and e dY of the chunk before, while the others work on dR.  The
+// factors come from bounds as the forward's do, with the largest values of L and dY measured.
 template <int DK, typename TG>
 __global__ void __launch_bounds__(kChainThreads, 1)
-    chain_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
-                     const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_dy, const ChainArgs a) {
+    chain_bwd_kernel(const ChainArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = ChainSmem<DK>;
     constexpr int NP = DK / 64;
-    constexpr uint32_t kTmR = 0, kTmL = 64, kTmCols = 128;
+    // tensor memory: P^T dY; hi and lo columns of H^T L, of Q^T e dY and of -K^T e dR
+    constexpr uint32_t kTmP = 0, kTmX = 64, kTmQ = 192, kTmK = 320, kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // K and H of a stage
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // gates, K and H of a stage
     uint64_t* full_q = full + 2;
-    uint64_t* full_p = full + 3;   // P and dY
-    uint64_t* bar_x = full + 4;    // dR done
-    uint64_t* bar_l = full + 5;    // L0's products done
-    uint64_t* bar_s = full + 6;    // L is in shared memory
-    uint64_t* bar_o = full + 7;    // e dY is
-    uint64_t* bar_r = full + 8;    // -e dR is
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 9);
+    uint64_t* full_p = full + 3;
+    uint64_t* bar_x = full + 4;    // P^T dY and H^T L done
+    uint64_t* bar_q = full + 5;    // Q^T e dY done
+    uint64_t* bar_l = full + 6;    // K^T e dR done
+    uint64_t* bar_s = full + 7;    // L is in shared memory
+    uint64_t* bar_o = full + 8;    // dY and e dY are
+    uint64_t* bar_r = full + 9;    // -e dR is
+    uint64_t* bar_m = full + 10;   // the largest values of L are known
+    float* s_most = reinterpret_cast<float*>(full + 11);  // [2 chunks][8 warps of L, 4 of dY]
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pan = blockIdx.x % a.d.pans;
@@ -103,10 +96,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int i = 0; i < 6; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < 7; ++i) mbar_init(full + i, 1);
         mbar_init(bar_s, 8);
         mbar_init(bar_o, 4);
         mbar_init(bar_r, 4);
+        mbar_init(bar_m, 8);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -116,85 +110,75 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            const int group = h / (a.d.heads / a.d.groups);
             int kh_loads = 0, q_loads = 0, p_loads = 0;
+            auto rec_of = [&](int it) { return rec0 + (long long)(nc - 1 - it) * rec_bytes(DK); };
             auto load_kh = [&](int it) {
-                const int c = nc - 1 - it;
                 uint8_t* st = smem + (it & 1) * M::stage;
-                mbar_arrive_expect_tx(full + (it & 1), M::stage);
+                uint64_t* bar = full + (it & 1);
+                mbar_arrive_expect_tx(bar, M::stage);
+                bulk_load(st, rec_of(it), kGateBytes, bar);
                 for (int p = 0; p < NP; ++p)
-                    tma_load_4d(st + p * kTile, &tm_k, full + (it & 1), 64 * p, group, c * kC, b);
-                bulk_load(st + M::k_bytes, rec0 + (long long)c * rec_bytes(DK), 2 * h_bytes(DK),
-                          full + (it & 1));
+                    bulk_load(st + M::k + p * kTile, rec_of(it) + rec_kq(DK) + p * 2 * kTile, kTile, bar);
+                bulk_load(st + M::h, rec_of(it) + rec_h(DK), 2 * h_bytes(DK), bar);
                 ++kh_loads;
             };
             auto load_q = [&](int it) {
                 mbar_arrive_expect_tx(full_q, M::k_bytes);
                 for (int p = 0; p < NP; ++p)
-                    tma_load_4d(smem + M::q + p * kTile, &tm_q, full_q, 64 * p, group,
-                                (nc - 1 - it) * kC, b);
+                    bulk_load(smem + M::q + p * kTile, rec_of(it) + rec_kq(DK) + p * 2 * kTile + kTile,
+                              kTile, full_q);
                 ++q_loads;
             };
             auto load_p = [&](int it) {
-                const int c = nc - 1 - it;
-                mbar_arrive_expect_tx(full_p, 3 * kTile);
-                bulk_load(smem + M::p, rec0 + (long long)c * rec_bytes(DK) + 2 * h_bytes(DK),
-                          2 * kTile, full_p);
-                tma_load_4d(smem + M::dy, &tm_dy, full_p, pan * kPan, h, c * kC, b);
+                mbar_arrive_expect_tx(full_p, 2 * kTile);
+                bulk_load(smem + M::p, rec_of(it) + rec_p(DK), 2 * kTile, full_p);
                 ++p_loads;
             };
-            load_p(0);
             load_kh(0);
+            load_p(0);
             load_q(0);
             if (nc > 1) load_kh(1);
             int kh_seen = 0, q_seen = 0, p_seen = 0;
-            constexpr uint32_t id = idesc_bf16_f32(128, 64) | kIdescAMN | kIdescBMN;
-            // (of 64 columns of dstate the second block of rows is not read)
-            constexpr uint32_t lbo = kTile;
+            constexpr uint32_t id = idesc_f16(128, 128) | kIdescAMN | kIdescBMN;
+            constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescAMN | kIdescBMN;
             for (int it = 0; it < nc; ++it) {
                 const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
                 if (!mbar_wait(full_p, ph, a.status)) break;
                 ++p_seen;
+                if (!mbar_wait(bar_o, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16(tmem + kTmR, mdesc(sb + M::p, kk, kTile), mdesc(sb + M::dy, kk, kTile),
-                             id, kk > 0);
+                    mma_f16(tmem + kTmP, mdesc(sb + M::p, kk, kTile), mdesc(sb + M::dy, kk, kTile),
+                            id64, kk > 0);
                 if (!mbar_wait(full + (it & 1), (it >> 1) & 1, a.status)) break;
                 ++kh_seen;
                 if (!mbar_wait(bar_s, ph, a.status)) break;
                 tc_fence_after();
-                const uint32_t hh = st + M::k_bytes;
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) {
-                    mma_bf16(tmem + kTmR, mdesc(hh, kk, h_bytes(DK)), mdesc(sb + M::l_hi, kk, kTile), id, 1);
-                    mma_bf16(tmem + kTmR, mdesc(hh, kk, h_bytes(DK)), mdesc(sb + M::l_lo, kk, kTile), id, 1);
-                }
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmX, mdesc(st + M::h, kk, h_bytes(DK)),
+                            mdesc(sb + M::l_hi, kk, h_bytes(DK)), id, kk > 0);
                 mma_commit(bar_x);
                 if (!mbar_wait(full_q, ph, a.status)) break;
                 ++q_seen;
-                if (!mbar_wait(bar_o, ph, a.status)) break;
                 tc_fence_after();
+                // (of 64 columns of dstate the second block of rows is not read)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16(tmem + kTmL, mdesc(sb + M::q, kk, lbo), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
-                    mma_bf16(tmem + kTmL, mdesc(sb + M::q, kk, lbo), mdesc(sb + M::o_lo, kk, kTile), id, 1);
-                }
-                if (it + 1 < nc) {
-                    if (!mbar_wait(bar_x, ph, a.status)) break;
-                    load_p(it + 1);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmQ, mdesc(sb + M::q, kk, kTile), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
+                mma_commit(bar_q);
                 if (!mbar_wait(bar_r, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16(tmem + kTmL, mdesc(st, kk, lbo), mdesc(sb + M::r_hi, kk, kTile), id, 1);
-                    mma_bf16(tmem + kTmL, mdesc(st, kk, lbo), mdesc(sb + M::r_lo, kk, kTile), id, 1);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmK, mdesc(st + M::k, kk, kTile), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
                 mma_commit(bar_l);
                 if (it + 1 < nc) {
-                    if (!mbar_wait(bar_l, ph, a.status)) break;
+                    if (!mbar_wait(bar_q, ph, a.status)) break;  // (it follows bar_x)
+                    load_p(it + 1);
                     load_q(it + 1);
+                    if (!mbar_wait(bar_l, ph, a.status)) break;
                     if (it + 2 < nc) load_kh(it + 2);
                 }
             }
@@ -208,7 +192,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * part;
         const int col0 = pan * kPan + 32 * part;
-        const bool upper = row >= kC;   // these rows make e dY
+        const bool upper = row >= kC;   // these rows make dY and e dY
         const int i = row & 63;
         float* xch = reinterpret_cast<float*>(smem + M::xch) + 32 * part * 64 + i;
         float L[32];
@@ -216,25 +200,43 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int e = 0; e < 32; ++e)
             L[e] = a.dlast && row < a.d.dk && col0 + e < a.d.dv
                        ? a.dlast[(bh * a.d.dv + col0 + e) * a.d.dk + row] : 0.0f;
-        auto put_state = [&](int c) {
+        auto kept_of = [&](int c) {
+            return a.kept + ((bh * nc + c) * a.d.pans + pan) * adjoint_bytes(DK);
+        };
+        // what a chunk's rows take from its gates, read before the stage can be refilled
+        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_kq = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        auto gates_of = [&](int it) {
+            const bool in = warp_wait(full + (it & 1), (it >> 1) & 1, a.status);
+            const Gates* g = reinterpret_cast<const Gates*>(smem + (it & 1) * M::stage);
+            e_row = ex2_approx(g->hi[i] + g->lo[i]);
+            e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
+            e_max = fmaxf(g->e_max, 1.0f);
+            s_kq = g->s_kq;
+            s_h = g->s_h;
+            s_p = g->s_p;
+            return in;
+        };
+        float s_l = 0.0f;  // L's factor, undone
+        auto put_state = [&](int it, float bound) {
+            const float scale = tile_scale(bound, kBoundTop, s_l);
+            uint32_t hw[16], lw[16];
             if (row < DK) {
-                put32_split(smem + M::l_hi, smem + M::l_lo, row, 4 * part, L);
-                put32(a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK) + kTile, row,
-                      4 * part, L);
+                split<32>(L, scale, hw, lw);
+                put32(smem + M::l_hi, row, 4 * part, hw);
+                put32(smem + M::l_lo, row, 4 * part, lw);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(bar_s);
+            const float m = warp_most<32>(L);
+            if (lane == 0) s_most[12 * (it & 1) + warp] = m;
+            warp_arrive(bar_m);
+            uint8_t* k = kept_of(nc - 1 - it);
+            if (row < DK) put32(k + 2 * kTile, row, 4 * part, hw);
+            if (tid == 0) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[2] = s_l;
         };
         uint4 dy[4];
-        float e_row = 0.0f, e_end = 0.0f;
-        bool off = true;
         auto fetch = [&](int c) {
-            const Gates* g = reinterpret_cast<const Gates*>(rec0 + (long long)c * rec_bytes(DK) +
-                                                            hp_bytes(DK) + kTile);
-            e_row = ex2_approx(g->hi[i] + g->lo[i]);
-            e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
-            off = g->masked >> i & 1;
             const int t = c * kC + i;
 #pragma unroll
             for (int p = 0; p < 4; ++p)
@@ -244,39 +246,94 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                   col0 + 8 * p)
                             : make_uint4(0, 0, 0, 0);
         };
-        put_state(nc - 1);
+        // (upper warps) dY and e dY of step `it` as operands, dY kept
+        float s_dy = 0.0f, s_o = 0.0f;
+        auto put_dy = [&](int it, float e) {
+            float x[32];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) unpack8_bf16(dy[p], x + 8 * p);
+            const float m = warp_most<32>(x);
+            float* most = s_most + 12 * (it & 1) + 8;
+            if (lane == 0) most[(quarter & 1) * 2 + part] = m;
+            named_bar_sync(2, 128);
+            const float all = most_of<4>(most);
+            uint32_t hw[16], lw[16];
+            round_to<32>(x, tile_scale(all, kTop, s_dy), hw);
+            put32(smem + M::dy, i, 4 * part, hw);
+            uint8_t* k = kept_of(nc - 1 - it);
+            put32(k + kTile, i, 4 * part, hw);
+            if (tid == 64) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[1] = s_dy;
+#pragma unroll
+            for (int n = 0; n < 32; ++n) x[n] *= e;
+            split<32>(x, tile_scale(all * e_max, kBoundTop, s_o), hw, lw);
+            put32(smem + M::o_hi, i, 4 * part, hw);
+            put32(smem + M::o_lo, i, 4 * part, lw);
+            fence_proxy_async_smem();
+            warp_arrive(bar_o);
+        };
+        {   // the last chunk: its largest values are measured
+            const float m = warp_most<32>(L);
+            if (lane == 0) s_most[12 + warp] = m;
+            named_bar_sync(1, 256);
+            const float all = most_of<8>(s_most + 12);
+            named_bar_sync(1, 256);
+            put_state(0, all);
+        }
+        bool ok = gates_of(0);  // the same for all lanes of a warp
         fetch(nc - 1);
-        bool ok = true;  // the same for all lanes of a warp
+        if (upper) put_dy(0, e_row);
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
-            const float er = e_row, ee = e_end;
-            const bool masked = off;
-            float x[32];
-            if (upper) {  // (the products that read e dY before are done: bar_l follows them)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) unpack8(dy[p], x + 8 * p);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] *= er;
-                put32_split(smem + M::o_hi, smem + M::o_lo, i, 4 * part, x);
-                fence_proxy_async_smem();
-                warp_arrive(bar_o);
-            }
+            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h;
             if (c > 0) fetch(c - 1);
-            ok = ok && warp_wait(bar_x, ph, a.status);
+            float x[32];
+            ok = ok && warp_wait(bar_m, ph, a.status) && warp_wait(bar_o, ph, a.status) &&
+                 warp_wait(bar_x, ph, a.status);
             tc_fence_after();
+            // bounds: of L and dY measured, of dR from them
+            const float l_max = most_of<8>(s_most + 12 * ph);
+            const float dy_max = most_of<4>(s_most + 12 * ph + 8);
+            const float dr_bound = kC * kTopValue * s_p * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
+            float s_od;  // e dY's factor, undone (the upper warps' own s_dy and s_o)
+            (void)tile_scale(dy_max * em, kBoundTop, s_od);
+            float s_dyd;
+            (void)tile_scale(dy_max, kTop, s_dyd);
+            float s_r, s_g;
+            const float r_scale = tile_scale(dr_bound, kBoundTop, s_r);
+            const float g_scale = tile_scale(dr_bound * em, kBoundTop, s_g);
             if (ok) {
-                tmem_ld32(t_lane + kTmR, x);
+                const float fp = s_p * s_dyd, fx = sh * s_l;
+                float z[32];
+                tmem_ld32(t_lane + kTmP, x);
+                tmem_ld32(t_lane + kTmX, z);
                 tmem_wait_ld();
-                if (upper)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = fmaf(fp, x[e], fx * z[e]);
+                if (upper) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) xch[64 * e] = x[e];
+                } else {
+                    tmem_ld32(t_lane + kTmX + 64, z);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = fmaf(fx, z[e], x[e]);
+                }
             }
             tc_fence_before();
             if (!named_bar_and(1, 256, ok)) break;  // all eight warps leave together
             if (!upper) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] += xch[64 * e];
+                uint32_t hw[16], lw[16];
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = -er * x[e];
+                split<32>(y, g_scale, hw, lw);
+                put32(smem + M::r_hi, i, 4 * part, hw);
+                put32(smem + M::r_lo, i, 4 * part, lw);
+                fence_proxy_async_smem();
+                warp_arrive(bar_r);
                 const int t = c * kC + i;
                 if (t < a.d.seqlen) {
                     TG* dv = static_cast<TG*>(a.dv) +
@@ -285,30 +342,44 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     for (int p = 0; p < 4; ++p)
                         if (col0 + 8 * p < a.d.dv) store8(dv + 8 * p, x + 8 * p);
                 }
-                put32(a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK), i, 4 * part, x);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] *= -er;
-                put32_split(smem + M::r_hi, smem + M::r_lo, i, 4 * part, x);
-                if (masked && part < NP) {
-                    // a masked step's key is not looked at: its dR is 0, but 0 NaN is not
-                    (void)mbar_wait(full + (it & 1), (it >> 1) & 1, a.status);
-#pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        *reinterpret_cast<uint4*>(smem + (it & 1) * M::stage + part * kTile + i * 128 +
-                                                  16 * p) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                warp_arrive(bar_r);
+                round_to<32>(x, r_scale, hw);
+                uint8_t* k = kept_of(c);
+                put32(k, i, 4 * part, hw);
+                if (tid == 0) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[0] = s_r;
             }
-            float z[32];
-            ok = warp_wait(bar_l, ph, a.status);
+            // ---- L0 = e_63 L + Q^T e dY - K^T e dR
+            ok = warp_wait(bar_q, ph, a.status);
+            tc_fence_after();
+            if (ee == 0.0f)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) L[e] = 0.0f;
+            auto add = [&](uint32_t at, float factor, float keep) {
+                const f2 f = pair(factor, factor), k2 = pair(keep, keep);
+#pragma unroll
+                for (int e0 = 0; e0 < 32; e0 += 16) {
+                    float z[16], y[16];
+                    tmem_ld16(t_lane + at + e0, z);
+                    tmem_ld16(t_lane + at + 64 + e0, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const f2 s = add2(pair(z[e], z[e + 1]), pair(y[e], y[e + 1]));
+                        unpair(fma2(k2, pair(L[e0 + e], L[e0 + e + 1]), mul2(f, s)), L[e0 + e], L[e0 + e + 1]);
+                    }
+                }
+            };
+            if (ok) add(kTmQ, skq * s_od, ee);
+            if (c > 0) {
+                ok = ok && gates_of(it + 1);
+                // (the products that read dY and e dY are done: bar_q follows them)
+                if (upper) put_dy(it + 1, e_row);
+            }
+            ok = ok && warp_wait(bar_l, ph, a.status);
             tc_fence_after();
             if (ok) {
-                tmem_ld32(t_lane + kTmL, z);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) L[e] = ee == 0.0f ? z[e] : fmaf(ee, L[e], z[e]);
-                if (c > 0) put_state(c - 1);
+                add(kTmK, skq * s_g, 1.0f);
+                const float qk = kC * kTopValue * 2.0f * skq;
+                if (c > 0) put_state(it + 1, fmaf(ee, l_max, qk * em * (dy_max + dr_bound)));
             }
         }
         if (a.dh0 && row < a.d.dk)
@@ -323,54 +394,59 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
 // ------------------------------------------------------------------ grads
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 288;  // 8 warps on rows, one that loads
 
 template <int DK> struct GradSmem {
-    static constexpr uint32_t kq = 0;                        // panels of [K | Q]
-    static constexpr uint32_t rdo = 0;                       // of a stage: dR, dY
-    static constexpr uint32_t s0 = 2 * kTile;
-    static constexpr uint32_t l = s0 + h_bytes(DK);
-    static constexpr uint32_t t = l + h_bytes(DK);           // T', then R
-    static constexpr uint32_t r = t + kTile;
-    static constexpr uint32_t stage = r + kTile;
-    static constexpr uint32_t stages = (DK / 64) * 2 * kTile;
-    static constexpr uint32_t u = stages + 2 * stage;        // U, then W (rows 64 to 127 of
-    static constexpr uint32_t w = u + kTile;                 // U's operand are not read)
-    static constexpr uint32_t sums = w + 3 * kTile;          // floats (W^T's second block reads
-                                                             // one tile past W)
-    static constexpr uint32_t n_sums = 128 * 2 + 4 * 64 + 64 * 2 + 64 * 2 + 8 + 64 * 2 + 64;
-    static constexpr uint32_t misc = sums + n_sums * 4;
-    static constexpr uint32_t bytes = misc + 128;
+    // of a head (two in turn): gates, panels of [K | Q], T' (64 rows; the 64 behind them in its
+    // operand are not read)
+    static constexpr uint32_t kq = kGateBytes;
+    static constexpr uint32_t t = kq + kq_bytes(DK);
+    static constexpr uint32_t head = t + kTile;
+    // of a head's 64 columns of headdim (two in turn): R, S0, then [dR; dY], L
+    static constexpr uint32_t r = 0;
+    static constexpr uint32_t s0 = kTile;
+    static constexpr uint32_t rdo = s0 + h_bytes(DK);
+    static constexpr uint32_t l = rdo + 2 * kTile;
+    static constexpr uint32_t stage = l + h_bytes(DK);
+    static constexpr uint32_t stages = 2 * head;
+    static constexpr uint32_t u = stages + 2 * stage;   // U, then W (rows 64 to 127 of U's
+    static constexpr uint32_t w = u + kTile;            // operand are not read)
+    static constexpr uint32_t sums = w + 2 * kTile;     // (W^T's second block, not read either)
+    static constexpr uint32_t misc = sums + 4096;
+    static constexpr uint32_t factors = misc + 256;     // [2][8] floats
+    static constexpr uint32_t bytes = w + 3 * kTile;
+    static_assert(factors + 64 <= bytes, "sums fit behind W");
 };
 
 struct GradArgs {
     const uint8_t* records;
     const uint8_t* kept;     // R | S0
-    const uint8_t* adjoint;  // dR | L
+    const uint8_t* adjoint;  // dR | dY | L
     const void *g, *beta;
     void *dq, *dk, *dg, *dbeta;
     uint32_t* status;
     Dims d;
+    long long count;         // of chunks and groups
     int gates_bf16;
 };
 
-// 8 products of a row's 16-byte pieces of two tiles, summed.
+// Products of a row's 16-byte pieces of two tiles, summed.
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
     float x[8], y[8], s = 0.0f;
-    unpack8(a, x);
-    unpack8(b, y);
+    unpack8_f16(a, x);
+    unpack8_f16(b, y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
     return s;
 }
 
+// CTAs walk the chunks and groups of heads; a warp brings in what comes next.  Rows of
+// products are lanes: steps as k rows (0 to 63) and as q rows (64 to 127).
 template <int DK, typename TG>
-__global__ void __launch_bounds__(kGradThreads, 1)
-    grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_dy, const GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = GradSmem<DK>;
-    constexpr int NP = DK / 64, CW = DK / 2;  // columns of dstate a thread holds
+    constexpr int CW = DK / 2;  // columns of dstate a thread holds
     // tensor memory: F, F2; [dA'; dP'], [K; Q] K^T and U until W is made, then W K and W^T [K; Q]
     constexpr uint32_t kTmF = 0, kTmF2 = 128, kTmA = 256, kTmX = 320, kTmU = 384, kTmW = 384,
                        kTmV = 256, kTmCols = 512;
@@ -380,306 +456,361 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     float* s_dec = s_col + 256;                               // [64][2]
     float* s_db = s_dec + 128;                                // [64][2]
     float* s_c = s_db + 128;                                  // [8]
-    float* s_hi = s_c + 8;
-    float* s_lo = s_hi + 64;
-    float* s_scan = s_lo + 64;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);
-    uint64_t* bar_kq = full + 2;
-    uint64_t* bar_u = full + 3;
-    uint64_t* bar_f = full + 4;
-    uint64_t* bar_w = full + 5;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 6);
+    float* s_most = s_c + 8;                                  // [8]
+    float* s_scan = s_most + 8;                               // [2]
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // [2] columns are in
+    uint64_t* empty = full + 2;                                    // [2] and have been read
+    uint64_t* full_h = full + 4;                                   // [2] a head is in
+    uint64_t* empty_h = full + 6;                                  // [2]
+    uint64_t* bar_u = full + 8;
+    uint64_t* bar_f = full + 9;
+    uint64_t* bar_w = full + 10;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 11);
+    float* factors = reinterpret_cast<float*>(smem + M::factors);  // [2][8]: R, S0, dR, dY, L
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
-    const bool is_q = row >= kC;
-    const int i = row & 63;
-    const int nc = a.d.chunks, ratio = a.d.heads / a.d.groups;
-    const int c = blockIdx.x % nc;
-    const int bg = blockIdx.x / nc, b = bg / a.d.groups, group = bg % a.d.groups;
-    const int t0 = c * kC;
-    const int steps = ratio * a.d.pans;
-    auto chunk_of = [&](int n) {  // index of the chunk and head of step n
-        return ((long long)b * a.d.heads + group * ratio + n / a.d.pans) * nc + c;
-    };
+    const int nc = a.d.chunks, ratio = a.d.heads / a.d.groups, pans = a.d.pans;
+    const int steps = ratio * pans;  // of an item (a chunk and a group)
 
-    if (warp == 0) tmem_alloc(s_tmem, kTmCols);
-    int loads = 0;
-    auto load = [&](int n) {
-        uint8_t* st = smem + M::stages + (n & 1) * M::stage;
-        uint64_t* bar = full + (n & 1);
-        const long long ch = chunk_of(n), at = (ch * a.d.pans + n % a.d.pans) * kept_bytes(DK);
-        mbar_arrive_expect_tx(bar, M::stage);
-        bulk_load(st + M::rdo, a.adjoint + at, kTile, bar);
-        tma_load_4d(st + M::rdo + kTile, &tm_dy, bar, (n % a.d.pans) * kPan,
-                    group * ratio + n / a.d.pans, t0, b);
-        bulk_load(st + M::s0, a.kept + at + kTile, h_bytes(DK), bar);
-        bulk_load(st + M::l, a.adjoint + at + kTile, h_bytes(DK), bar);
-        bulk_load(st + M::t, a.records + ch * rec_bytes(DK) + hp_bytes(DK), kTile, bar);
-        bulk_load(st + M::r, a.kept + at, kTile, bar);
-        ++loads;
-    };
+    if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int n = 0; n < 6; ++n) mbar_init(full + n, 1);
+        for (int n = 0; n < 11; ++n) mbar_init(full + n, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(bar_kq, NP * 2 * kTile);
-        for (int p = 0; p < NP; ++p) {
-            tma_load_4d(smem + M::kq + p * 2 * kTile, &tm_k, bar_kq, 64 * p, group, t0, b);
-            tma_load_4d(smem + M::kq + p * 2 * kTile + kTile, &tm_q, bar_kq, 64 * p, group, t0, b);
-        }
-        load(0);
-        if (steps > 1) load(1);
     }
-    // keys that no head of the group looks at
-    unsigned long long unseen = ~0ull;
-    for (int n = 0; n < steps; n += a.d.pans)
-        unseen &= reinterpret_cast<const Gates*>(a.records + chunk_of(n) * rec_bytes(DK) +
-                                                 hp_bytes(DK) + kTile)->masked;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-    bool ok = warp_wait(bar_kq, 0, a.status);
-    if (unseen) {
-        if (ok)
-            for (int e = tid; e < NP * kC * 8; e += kGradThreads) {
-                const int r = (e >> 3) & 63;
-                if (unseen >> r & 1)
-                    *reinterpret_cast<uint4*>(smem + M::kq + (e >> 9) * 2 * kTile + r * 128 +
-                                              (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-        fence_proxy_async_smem();
-    }
-    ok = __syncthreads_and(ok);
 
-    float acc[CW];  // of dK (rows 0 to 63) or dQ
-#pragma unroll
-    for (int e = 0; e < CW; ++e) acc[e] = 0.0f;
-    float hi_i = 0.0f, lo_i = 0.0f, beta_sum = 0.0f, ls = 0.0f;
-    bool off = false;
-
-    for (int n = 0; n < steps && ok; ++n) {
-        const int p = n % a.d.pans, h = group * ratio + n / a.d.pans;
-        const uint32_t st = sb + M::stages + (n & 1) * M::stage;
-        const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
-        const long long ch = chunk_of(n);
-        const Gates* gates = reinterpret_cast<const Gates*>(a.records + ch * rec_bytes(DK) +
-                                                            hp_bytes(DK) + kTile);
-        if (p == 0) {  // a head begins
-            hi_i = gates->hi[i];
-            lo_i = gates->lo[i];
-            off = gates->masked >> i & 1;
-            if (tid < kC) {
-                s_hi[tid] = hi_i;
-                s_lo[tid] = lo_i;
-            }
-            beta_sum = ls = 0.0f;
-        }
-        // ---- U = T' R, and with a head's first columns [K; Q] K^T
-        if (tid == 0) {
-            const bool in = mbar_wait(full + (n & 1), (n >> 1) & 1, a.status);
-            tc_fence_after();
-            if (in) {
-                if (p == 0)
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk)
-                        mma_bf16(tmem + kTmX, kdesc<128>(sb + M::kq, kk), kdesc<128>(sb + M::kq, kk),
-                                 idesc_bf16_f32(128, 64), kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16(tmem + kTmU, kdesc<128>(st + M::t, kk), mdesc(st + M::r, kk, kTile),
-                             idesc_bf16_f32(128, 64) | kIdescBMN, kk > 0);
-                mma_commit(bar_u);
-            }
-        }
-        ok = warp_wait(full + (n & 1), (n >> 1) & 1, a.status);
-        // sums over this panel's columns: dR . R, and L . S0
-        if (ok) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t off4 = piece(row, 4 * part + q);
-                if (!is_q)
-                    beta_sum += dot8(*reinterpret_cast<const uint4*>(sg + M::rdo + off4),
-                                     *reinterpret_cast<const uint4*>(sg + M::r + off4));
-                if (row < DK)
-                    ls += dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + off4),
-                               *reinterpret_cast<const uint4*>(sg + M::l + off4));
-            }
-        }
-        ok = ok && warp_wait(bar_u, n & 1, a.status);
-        tc_fence_after();
-        if (ok && !is_q) {
-            float x[32];
-            tmem_ld32(t_lane + kTmU + 32 * part, x);
-            tmem_wait_ld();
-            put32(smem + M::u, i, 4 * part, x);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        ok = __syncthreads_and(ok);
-        if (!ok) break;
-        if (tid == 0) {
-            tc_fence_after();
-            constexpr uint32_t id64 = idesc_bf16_f32(128, 64), idk = idesc_bf16_f32(128, DK);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t more = p > 0 || kk > 0;
-                mma_bf16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, more);
-                mma_bf16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, more);
-                mma_bf16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk, more);
-            }
-            mma_commit(bar_f);
-        }
-        ok = warp_wait(bar_f, n & 1, a.status);
-        tc_fence_after();
-        if (tid == 0 && ok && n + 2 < steps) load(n + 2);
-        ok = __syncthreads_and(ok);
-        if (!ok || p + 1 < a.d.pans) continue;
-
-        // ---- the head's last columns are in: W = [dKK; dQK], and its sums with [KK; QK]
-        float rsum = 0.0f;
-        {
-            float x[32], m[32];
-            tmem_ld32(t_lane + kTmA + 32 * part, x);
-            tmem_ld32(t_lane + kTmX + 32 * part, m);
-            tmem_wait_ld();
-            const int last = is_q ? i : i - 1;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int j = 32 * part + e;
-                x[e] = j <= last ? (is_q ? x[e] : -x[e]) * decay(hi_i, lo_i, s_hi[j], s_lo[j]) : 0.0f;
-                m[e] = j <= last ? m[e] * x[e] : 0.0f;
-                rsum += m[e];
-            }
-            put32(smem + M::w, row, 4 * part, x);
-            // sums over the warp's 32 rows: lane l ends with column l
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-                for (int k = 0; k < o; ++k) {
-                    const bool up = lane & o;
-                    const float send = up ? m[k] : m[k + o];
-                    m[k] = (up ? m[k + o] : m[k]) + __shfl_xor_sync(0xffffffffu, send, o);
+    if (warp == 8) {
+        if (lane == 0) {
+            int n = 0, hn = 0;  // columns and heads loaded
+            bool ok = true;
+            for (long long item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+                const long long bg = item / nc;
+                const long long head0 = (bg / a.d.groups) * a.d.heads + (bg % a.d.groups) * ratio;
+                for (int hh = 0; hh < ratio && ok; ++hh, ++hn) {
+                    const long long ch = (head0 + hh) * nc + item % nc;
+                    if (hn >= 2) ok = mbar_wait(empty_h + (hn & 1), ((hn >> 1) - 1) & 1, a.status);
+                    if (!ok) break;
+                    uint8_t* hd = smem + (hn & 1) * M::head;
+                    const uint8_t* rec = a.records + ch * rec_bytes(DK);
+                    mbar_arrive_expect_tx(full_h + (hn & 1), M::head);
+                    bulk_load(hd, rec, kGateBytes + kq_bytes(DK), full_h + (hn & 1));
+                    bulk_load(hd + M::t, rec + rec_t(DK), kTile, full_h + (hn & 1));
+                    for (int p = 0; p < pans; ++p, ++n) {
+                        if (n >= 2) ok = mbar_wait(empty + (n & 1), ((n >> 1) - 1) & 1, a.status);
+                        if (!ok) break;
+                        uint8_t* st = smem + M::stages + (n & 1) * M::stage;
+                        uint64_t* bar = full + (n & 1);
+                        const uint8_t* kept = a.kept + (ch * pans + p) * kept_bytes(DK);
+                        const uint8_t* adj = a.adjoint + (ch * pans + p) * adjoint_bytes(DK);
+                        mbar_arrive_expect_tx(bar, M::stage + 32);
+                        bulk_load(st + M::r, kept, kTile + h_bytes(DK), bar);
+                        bulk_load(st + M::rdo, adj, 2 * kTile + h_bytes(DK), bar);
+                        bulk_load(factors + 8 * (n & 1), kept + kTile + h_bytes(DK), 16, bar);
+                        bulk_load(factors + 8 * (n & 1) + 4, adj + 2 * kTile + h_bytes(DK), 16, bar);
+                    }
                 }
-            s_col[quarter * 64 + 32 * part + lane] = m[0];
+            }
+            // never leave with a load still landing
+            for (int k = max(0, n - 2); k < n; ++k) (void)mbar_wait(full + (k & 1), (k >> 1) & 1, a.status);
+            for (int k = max(0, hn - 2); k < hn; ++k)
+                (void)mbar_wait(full_h + (k & 1), (k >> 1) & 1, a.status);
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tc_fence_after();
-            constexpr uint32_t idW = idesc_bf16_f32(128, DK) | kIdescBMN;
-            constexpr uint32_t idV = idesc_bf16_f32(128, DK) | kIdescAMN | kIdescBMN;
+    } else {
+        const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const bool is_q = row >= kC;
+        const int i = row & 63;
+        int n = 0, hn = 0;
+        bool ok = true;
+        for (long long item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+            const int c = (int)(item % nc), t0 = c * kC;
+            const long long bg = item / nc;
+            const int b = (int)(bg / a.d.groups), group = (int)(bg % a.d.groups);
+            float acc[CW];  // of dK (rows 0 to 63) or dQ
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(sb + M::kq, kk, 2 * kTile), idW, kk > 0);
-            // (rows 64 to 127 of W^T [K; Q] are not read)
+            for (int e = 0; e < CW; ++e) acc[e] = 0.0f;
+            float own[32];  // of [dA'; dP']
+            float beta_sum = 0.0f, ls = 0.0f, into = 0.0f, outof = 0.0f;
+            float er = 0.0f, wr = 0.0f, skq = 0.0f, s_t = 0.0f;
+            for (int step = 0; step < steps; ++step, ++n) {
+                const int p = step % pans;
+                const uint32_t st = sb + M::stages + (n & 1) * M::stage;
+                const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
+                const uint32_t hd = sb + (hn & 1) * M::head;
+                const uint8_t* hg = smem + (hn & 1) * M::head;
+                const Gates* gates = reinterpret_cast<const Gates*>(hg);
+                const float* fac = factors + 8 * (n & 1);
+                // ---- U = T' R, and with a head's first columns [K; Q] K^T
+                if (tid == 0) {
+                    bool in = true;
+                    if (p == 0) in = mbar_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
+                    in = mbar_wait(full + (n & 1), (n >> 1) & 1, a.status) && in;
+                    tc_fence_after();
+                    if (in) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16(tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(sb + M::kq, kk, 2 * kTile), idV, kk > 0);
-            mma_commit(bar_w);
-        }
-        // ---- the state's parts
-        const float er = ex2_approx(hi_i + lo_i);
-        const float wr = decay(s_hi[kC - 1], s_lo[kC - 1], hi_i, lo_i);
-        float into = 0.0f, outof = 0.0f;
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kTmU, kdesc<128>(hd + M::t, kk), mdesc(st + M::r, kk, kTile),
+                                    idesc_f16(128, 64) | kIdescBMN, kk > 0);
+                        mma_commit(bar_u);
+                        if (p == 0)
 #pragma unroll
-        for (int b8 = 0; b8 < CW; b8 += 16) {
-            const int c0 = CW * part + b8;
-            float f[16], f2[16], x[16];
-            tmem_ld16(t_lane + kTmF + c0, f);
-            if (!is_q) tmem_ld16(t_lane + kTmF2 + c0, f2);
-            tmem_wait_ld();
+                            for (int kk = 0; kk < DK / 16; ++kk)
+                                mma_f16(tmem + kTmX, kdesc<128>(hd + M::kq, kk), kdesc<128>(hd + M::kq, kk),
+                                        idesc_f16(128, 64), kk > 0);
+                    }
+                }
+                bool here = true;
+                if (p == 0) here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
+                here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
+                const float s_r = fac[0], s_s = fac[1], s_dr = fac[4], s_dy = fac[5], s_l = fac[6];
+                if (p == 0) {  // a head begins
+                    er = ex2_approx(gates->hi[i] + gates->lo[i]);
+                    wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
+                    skq = gates->s_kq;
+                    s_t = gates->s_t;
+                    beta_sum = ls = into = outof = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                unpack8(*reinterpret_cast<const uint4*>(
-                            smem + M::kq + (c0 >> 6) * 2 * kTile + piece(row, ((c0 & 63) >> 3) + q)),
-                        x + 8 * q);
+                    for (int e = 0; e < 32; ++e) own[e] = 0.0f;
+                }
+                // sums over these columns: dR . R, and L . S0
+                {
+                    float dr = 0.0f, dl = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                into = fmaf(x[e], f[e], into);
-                acc[b8 + e] = fmaf(is_q ? er : -er, f[e], acc[b8 + e]);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t off4 = piece(row, 4 * part + q);
+                        if (!is_q)
+                            dr += dot8(*reinterpret_cast<const uint4*>(sg + M::rdo + off4),
+                                       *reinterpret_cast<const uint4*>(sg + M::r + off4));
+                        if (row < DK)
+                            dl += dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + off4),
+                                       *reinterpret_cast<const uint4*>(sg + M::l + off4));
+                    }
+                    beta_sum = fmaf(s_dr * s_r, dr, beta_sum);
+                    ls = fmaf(s_s * s_l, dl, ls);
+                }
+                here = warp_wait(bar_u, n & 1, a.status) && here;
+                tc_fence_after();
+                // U's factor: at most 64 products of 2^13 and 2^15, down to 2^15
+                constexpr float kDown = 1.0f / 524288.0f;
+                const float s_u = s_t * s_r / kDown;
+                if (here && !is_q) {
+                    float x[32];
+                    uint32_t hw[16];
+                    tmem_ld32(t_lane + kTmU + 32 * part, x);
+                    tmem_wait_ld();
+                    round_to<32>(x, kDown, hw);
+                    put32(smem + M::u, i, 4 * part, hw);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                ok = named_bar_and(1, 256, here);
+                if (!ok) break;
+                if (tid == 0) {
+                    tc_fence_after();
+                    constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk, kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
+                    mma_commit(bar_f);
+                }
+                here = warp_wait(bar_f, n & 1, a.status);
+                tc_fence_after();
+                if (here) {  // the state's parts, and these columns' part of [dA'; dP']
+                    const float f1 = (is_q ? s_dy : s_dr) * s_s, f2_ = s_u * s_l;
+                    const float fa = (is_q ? s_dy : -s_dr) * s_u;
+                    const float g1 = is_q ? er * f1 : -er * f1, g2 = wr * f2_;
+                    float in1 = 0.0f, out1 = 0.0f;
+#pragma unroll
+                    for (int b8 = 0; b8 < CW; b8 += 16) {
+                        const int c0 = CW * part + b8;
+                        float f[16], x[16];
+                        tmem_ld16(t_lane + kTmF + c0, f);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            unpack8_f16(*reinterpret_cast<const uint4*>(
+                                            hg + M::kq + (c0 >> 6) * 2 * kTile +
+                                            piece(row, ((c0 & 63) >> 3) + q)), x + 8 * q);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            in1 = fmaf(x[e], f[e], in1);
+                            acc[b8 + e] = fmaf(g1, f[e], acc[b8 + e]);
+                        }
+                        if (!is_q) {
+                            tmem_ld16(t_lane + kTmF2 + c0, f);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                out1 = fmaf(x[e], f[e], out1);
+                                acc[b8 + e] = fmaf(g2, f[e], acc[b8 + e]);
+                            }
+                        }
+                    }
+                    into = fmaf(g1 * skq, in1, into);
+                    outof = fmaf(g2 * skq, out1, outof);
+                    float x[32];
+                    tmem_ld32(t_lane + kTmA + 32 * part, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) own[e] = fmaf(fa, x[e], own[e]);
+                }
+                tc_fence_before();
+                if (p + 1 < pans) {
+                    ok = named_bar_and(1, 256, here);
+                    if (!ok) break;
+                    if (tid == 0) mbar_arrive(empty + (n & 1));
+                    continue;
+                }
+
+                // ---- the head's last columns are in: W = [dKK; dQK], and its sums with [KK; QK]
+                const int h = group * ratio + step / pans;
+                float rsum = 0.0f;
+                if (here) {
+                    const float hi = gates->hi[i], lo = gates->lo[i], kk2 = skq * skq;
+                    const int last = is_q ? i : i - 1;
+                    float m[32];
+                    tmem_ld32(t_lane + kTmX + 32 * part, m);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const int j = 32 * part + e;
+                        const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
+                        const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
+                        const float hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool in = j + k <= last;
+                            own[e + k] = in ? own[e + k] * decay(hi, lo, hv[k], lv[k]) : 0.0f;
+                            m[e + k] = in ? kk2 * m[e + k] * own[e + k] : 0.0f;
+                            rsum += m[e + k];
+                        }
+                    }
+                    // sums over the warp's 32 rows: lane l ends with column l
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < o; ++k) {
+                            const bool up = lane & o;
+                            const float send = up ? m[k] : m[k + o];
+                            m[k] = (up ? m[k + o] : m[k]) + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                    s_col[quarter * 64 + 32 * part + lane] = m[0];
+                }
+                const float most = warp_most<32>(own);
+                if (lane == 0) s_most[warp] = most;
+                tc_fence_before();
+                ok = named_bar_and(1, 256, here);
+                if (!ok) break;
+                if (tid == 0) mbar_arrive(empty + (n & 1));  // these columns have been read
+                float s_w;
+                const float w_scale = tile_scale(most_of<8>(s_most), kTop, s_w);
+                {
+                    uint32_t hw[16];
+                    round_to<32>(own, w_scale, hw);
+                    put32(smem + M::w, row, 4 * part, hw);
+                }
+                s_row[2 * row + part] = rsum + into;
                 if (!is_q) {
-                    outof = fmaf(x[e], f2[e], outof);
-                    acc[b8 + e] = fmaf(wr, f2[e], acc[b8 + e]);
+                    s_dec[2 * i + part] = outof;
+                    s_db[2 * i + part] = beta_sum + rsum;
                 }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+                if (lane == 0) s_c[warp] = ls;
+                fence_proxy_async_smem();
+                named_bar_sync(1, 256);
+                if (tid == 0) {
+                    tc_fence_after();
+                    constexpr uint32_t idW = idesc_f16(128, DK) | kIdescBMN;
+                    constexpr uint32_t idV = idesc_f16(128, DK) | kIdescAMN | kIdescBMN;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(hd + M::kq, kk, 2 * kTile),
+                                idW, kk > 0);
+                    // (rows 64 to 127 of W^T [K; Q] are not read)
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16(tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(hd + M::kq, kk, 2 * kTile),
+                                idV, kk > 0);
+                    mma_commit(bar_w);
+                }
+                // ---- the gates
+                if (tid < kC) {
+                    const int t = t0 + i;
+                    const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + h;
+                    float up = s_row[2 * i] + s_row[2 * i + 1] + s_row[128 + 2 * i] + s_row[129 + 2 * i];
+                    for (int q = 0; q < 4; ++q) up -= s_col[q * 64 + i];
+                    float down = s_dec[2 * i] + s_dec[2 * i + 1];
+                    const float self = down;
+                    // sums of `up` from here on, of `down` before here
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float u = __shfl_down_sync(0xffffffffu, up, o);
+                        const float d = __shfl_up_sync(0xffffffffu, down, o);
+                        if (lane + o < 32) up += u;
+                        if (lane >= o) down += d;
+                    }
+                    if (tid == 32) s_scan[0] = up;
+                    if (tid == 31) s_scan[1] = down;
+                    named_bar_sync(2, 64);
+                    if (warp == 0) up += s_scan[0];
+                    if (warp == 1) down += s_scan[1];
+                    float all = 0.0f;
+                    for (int q = 0; q < 8; ++q) all += s_c[q];
+                    if (t < a.d.seqlen) {
+                        const float e_end = ex2_approx(gates->hi[kC - 1] + gates->lo[kC - 1]);
+                        // a gate of -inf cuts the past off: its gradient is 0
+                        const bool cut = ex2_approx(gate_at(a.g, at, a.gates_bf16) * kLog2e) == 0.0f;
+                        const bool off = gates->masked >> i & 1;
+                        put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - self) + e_end * all);
+                        put_gate(a.dbeta, at, a.gates_bf16,
+                                 off ? 0.0f : (s_db[2 * i] + s_db[2 * i + 1]) / gate_at(a.beta, at, a.gates_bf16));
+                    }
+                }
+                // ---- the products with W
+                here = warp_wait(bar_w, hn & 1, a.status);
+                tc_fence_after();
+                if (here) {
+                    const float f1 = s_w * skq;
+#pragma unroll
+                    for (int b8 = 0; b8 < CW; b8 += 16) {
+                        const int c0 = CW * part + b8;
+                        float f[16], f2_[16];
+                        tmem_ld16(t_lane + kTmW + c0, f);
+                        if (!is_q) tmem_ld16(t_lane + kTmV + c0, f2_);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            acc[b8 + e] = fmaf(f1, is_q ? f[e] : f[e] + f2_[e], acc[b8 + e]);
+                    }
+                }
+                tc_fence_before();
+                ok = named_bar_and(1, 256, here);  // sums and tensor memory are free for the next head
+                if (!ok) break;
+                if (tid == 0) mbar_arrive(empty_h + (hn & 1));
+                ++hn;
+            }
+            if (ok && t0 + i < a.d.seqlen) {
+                TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
+                          (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + CW * part;
+#pragma unroll
+                for (int e = 0; e < CW; e += 8)
+                    if (CW * part + e < a.d.dk) store8(out + e, acc + e);
             }
         }
-        s_row[2 * row + part] = rsum + (is_q ? er * into : -er * into);
-        if (!is_q) {
-            s_dec[2 * i + part] = wr * outof;
-            s_db[2 * i + part] = beta_sum + rsum;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-        if (lane == 0) s_c[warp] = ls;
-        __syncthreads();
-        // ---- the gates
-        if (tid < kC) {
-            const int t = t0 + i;
-            const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + h;
-            float up = s_row[2 * i] + s_row[2 * i + 1] + s_row[128 + 2 * i] + s_row[129 + 2 * i];
-            for (int q = 0; q < 4; ++q) up -= s_col[q * 64 + i];
-            float down = s_dec[2 * i] + s_dec[2 * i + 1];
-            const float own = down;
-            // sums of `up` from here on, of `down` before here
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_down_sync(0xffffffffu, up, o);
-                const float d = __shfl_up_sync(0xffffffffu, down, o);
-                if (lane + o < 32) up += u;
-                if (lane >= o) down += d;
-            }
-            if (tid == 32) s_scan[0] = up;
-            if (tid == 31) s_scan[1] = down;
-            named_bar_sync(2, 64);
-            if (warp == 0) up += s_scan[0];
-            if (warp == 1) down += s_scan[1];
-            float all = 0.0f;
-            for (int q = 0; q < 8; ++q) all += s_c[q];
-            if (t < a.d.seqlen) {
-                const float e_end = ex2_approx(s_hi[kC - 1] + s_lo[kC - 1]);
-                // a gate of -inf cuts the past off: its gradient is 0
-                const bool cut = ex2_approx(gate_at(a.g, at, a.gates_bf16) * kLog2e) == 0.0f;
-                put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - own) + e_end * all);
-                put_gate(a.dbeta, at, a.gates_bf16,
-                         off ? 0.0f : (s_db[2 * i] + s_db[2 * i + 1]) / gate_at(a.beta, at, a.gates_bf16));
-            }
-        }
-        // ---- the products with W
-        ok = warp_wait(bar_w, (n / a.d.pans) & 1, a.status);
-        tc_fence_after();
-        if (ok) {
-#pragma unroll
-            for (int b8 = 0; b8 < CW; b8 += 16) {
-                const int c0 = CW * part + b8;
-                float f[16], f2[16];
-                tmem_ld16(t_lane + kTmW + c0, f);
-                if (!is_q) tmem_ld16(t_lane + kTmV + c0, f2);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[b8 + e] += is_q ? f[e] : f[e] + f2[e];
-            }
-        }
-        tc_fence_before();
-        ok = __syncthreads_and(ok);  // sums and tensor memory are free for the next head
-    }
-    if (ok && t0 + i < a.d.seqlen) {
-        TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
-                  (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + CW * part;
-#pragma unroll
-        for (int e = 0; e < CW; e += 8)
-            if (CW * part + e < a.d.dk) store8(out + e, acc + e);
-    }
-    if (tid == 0 && !ok) {  // never leave with a load still landing
-        if (loads > 0) (void)mbar_wait(full + ((loads - 1) & 1), ((loads - 1) >> 1) & 1, a.status);
-        if (loads > 1) (void)mbar_wait(full + (loads & 1), ((loads - 2) >> 1) & 1, a.status);
-        (void)mbar_wait(bar_kq, 0, a.status);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, kTmCols);
+    if (warp == 8) tmem_dealloc(tmem, kTmCols);
 }
 
 // ------------------------------------------------------------------- host
@@ -690,28 +821,18 @@ bool allow_smem(K kernel, uint32_t bytes) {
            cudaSuccess;
 }
 
-struct Backward {
-    const void *q, *k, *dy;
-    long long q_step, k_step;
-    ChainArgs chain;
-    GradArgs grads;
-};
-
 template <int DK, typename TG>
-ssm_status_t run_backward(const Backward& w, cudaStream_t s) {
-    const Dims& d = w.chain.d;
-    CUtensorMap mq, mk, my;
-    if (!gdn_host::make_map(&mq, w.q, d.batch, d.seqlen, d.groups, d.dk, w.q_step) ||
-        !gdn_host::make_map(&mk, w.k, d.batch, d.seqlen, d.groups, d.dk, w.k_step) ||
-        !gdn_host::make_map(&my, w.dy, d.batch, d.seqlen, d.heads, d.dv, (long long)d.heads * d.dv))
-        return SSM_ERR_CUDA;
-    if (!allow_smem(chain_bwd_kernel<DK, TG>, ChainSmem<DK>::bytes) ||
+ssm_status_t run_backward(const ChainArgs& chain, GradArgs grads, cudaStream_t s) {
+    const Dims& d = chain.d;
+    const int sms = ssm_host::sm_count();
+    if (sms == 0 || !allow_smem(chain_bwd_kernel<DK, TG>, ChainSmem<DK>::bytes) ||
         !allow_smem(grads_kernel<DK, TG>, GradSmem<DK>::bytes))
         return SSM_ERR_CUDA;
     chain_bwd_kernel<DK, TG><<<(unsigned)((long long)d.batch * d.heads * d.pans), kChainThreads,
-                               ChainSmem<DK>::bytes, s>>>(mq, mk, my, w.chain);
-    grads_kernel<DK, TG><<<(unsigned)((long long)d.batch * d.groups * d.chunks), kGradThreads,
-                           GradSmem<DK>::bytes, s>>>(mq, mk, my, w.grads);
+                               ChainSmem<DK>::bytes, s>>>(chain);
+    grads.count = (long long)d.batch * d.groups * d.chunks;
+    grads_kernel<DK, TG><<<(unsigned)std::min<long long>(grads.count, sms), kGradThreads,
+                           GradSmem<DK>::bytes, s>>>(grads);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -723,7 +844,7 @@ extern "C" size_t ssm_gated_delta_bwd_workspace_bytes(int batch, int seqlen, int
     if (!sizes_ok(batch, seqlen, nheads, nheads, dstate, headdim) ||
         !sizes_fit(batch, seqlen, nheads, dstate, headdim))
         return 0;
-    return 1024 + keep_bytes(batch, seqlen, nheads, dstate, headdim);
+    return 1024 + adjoints_bytes(batch, seqlen, nheads, dstate, headdim);
 }
 
 extern "C" ssm_status_t ssm_gated_delta_bwd(
@@ -801,20 +922,17 @@ extern "C" ssm_status_t ssm_gated_delta_bwd(
         if (ssm_status_t st = gdn_internal::chunked_forward(f, s)) return st;
         records = f.records;
     }
-    Backward w{};
-    w.q = q; w.k = k; w.dy = dy; w.q_step = q_stride; w.k_step = k_stride;
     const Dims d{batch, seqlen, nheads, ngroups, dstate, headdim, (seqlen + kC - 1) / kC,
                  (headdim + kPan - 1) / kPan};
-    w.chain.dy = static_cast<const __nv_bfloat16*>(dy);
-    w.chain.records = records;
-    w.chain.kept = ws + 1024;
-    w.chain.dlast = dfinal_state; w.chain.dh0 = dinitial_state; w.chain.dv = dv;
-    w.chain.status = status; w.chain.d = d;
-    w.grads.records = records; w.grads.kept = records + rb; w.grads.adjoint = ws + 1024;
-    w.grads.g = g; w.grads.beta = beta;
-    w.grads.dq = dq; w.grads.dk = dk; w.grads.dg = dg; w.grads.dbeta = dbeta;
-    w.grads.status = status; w.grads.d = d; w.grads.gates_bf16 = gate_dtype == SSM_BF16;
+    ChainArgs c{};
+    c.dy = static_cast<const __nv_bfloat16*>(dy);
+    c.records = records; c.kept = ws + 1024; c.dlast = dfinal_state; c.dh0 = dinitial_state;
+    c.dv = dv; c.status = status; c.d = d;
+    GradArgs w{};
+    w.records = records; w.kept = records + rb; w.adjoint = ws + 1024; w.g = g; w.beta = beta;
+    w.dq = dq; w.dk = dk; w.dg = dg; w.dbeta = dbeta; w.status = status; w.d = d;
+    w.gates_bf16 = gate_dtype == SSM_BF16;
     const bool small = gdn_host::dk_tile(dstate) == 64;
-    if (grad_dtype == SSM_F32) return small ? run_backward<64, float>(w, s) : run_backward<128, float>(w, s);
-    return small ? run_backward<64, __nv_bfloat16>(w, s) : run_backward<128, __nv_bfloat16>(w, s);
+    if (grad_dtype == SSM_F32) return small ? run_backward<64, float>(c, w, s) : run_backward<128, float>(c, w, s);
+    return small ? run_backward<64, __nv_bfloat16>(c, w, s) : run_backward<128, __nv_bfloat16>(c, w, s);
 }
