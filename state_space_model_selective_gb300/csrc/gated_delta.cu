@@ -156,106 +156,80 @@ struct RecArgs {
     uint8_t* records;
     uint32_t* status;
     Dims d;
-    long long count;  // of chunks and heads
+    unsigned count;   // of chunks and heads
     int gates_bf16;
     int keep_t;       // T' is wanted (training)
 };
 
-// T = (1 + A)^-1 in place, A strictly lower 64 x 64 (zeros above).  The four 16 x 16
+// Joins pairs of inverted blocks of N rows: of the lower left of [[X, 0], [L, Z]]^-1 =
+// -Z^-1 L X^-1, element (r, c .. c + V - 1) of the pair at (at, at).  In two steps, the
+// first product through `tmp` (rows of 36 floats; row `t` is this thread's).
+template <int N, int V>
+__device__ __forceinline__ void join_blocks(float* m, float* tmp, int at, int t0, int r, int c) {
+    const float* X = m + at * kPitch + at;
+    const float* L = X + N * kPitch;
+    const float* Z = L + N;
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(L + r * kPitch + j);
+        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = fmaf(lv[e], X[(j + e) * kPitch + c + v], s[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) tmp[(t0 + r) * 36 + c + v] = s[v];
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        const float4 z = *reinterpret_cast<const float4*>(Z + r * kPitch + j);
+        const float zv[4] = {-z.x, -z.y, -z.z, -z.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = fmaf(zv[e], tmp[(t0 + j + e) * 36 + c + v], s[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) m[(at + N + r) * kPitch + at + c + v] = s[v];
+    __syncthreads();
+}
+
+// T = (1 + A)^-1 in place, A strictly lower 64 x 64 (zeros above).  The eight 8 x 8
 // blocks on the diagonal by substitution, a thread to a column, then blocks joined in
-// pairs: the lower left of [[X, 0], [L, Z]]^-1 is -Z^-1 L X^-1.  `tmp`: 32 x 36 floats.
-// In fp32: what is lost here no later product gives back.
+// pairs three times.  `tmp`: 32 x 36 floats.  In fp32: what is lost here no later product
+// gives back.
 __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid) {
     if (tid < 64) {
-        const int b = (tid >> 4) * 16, c = tid & 15;
+        const int b = (tid >> 3) * 8, c = tid & 7;
         const float* base = m + b * kPitch + b;
-        float x[16];
+        float x[8];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float s = r == c ? 1.0f : 0.0f, s2 = 0.0f;
+        for (int r = 0; r < 8; ++r) {
+            float s = r == c ? 1.0f : 0.0f;
 #pragma unroll
             for (int j = 0; j < r; j += 4) {
                 const float4 l = *reinterpret_cast<const float4*>(base + r * kPitch + j);
                 s = fmaf(-l.x, x[j], s);
-                if (j + 1 < r) s2 = fmaf(-l.y, x[j + 1], s2);
+                if (j + 1 < r) s = fmaf(-l.y, x[j + 1], s);
                 if (j + 2 < r) s = fmaf(-l.z, x[j + 2], s);
-                if (j + 3 < r) s2 = fmaf(-l.w, x[j + 3], s2);
+                if (j + 3 < r) s = fmaf(-l.w, x[j + 3], s);
             }
-            x[r] = s + s2;
+            x[r] = s;
         }
-        __syncwarp();  // a block's columns are read and written by one half warp
+        __syncwarp();  // a block's columns are read and written by one quarter of a warp
 #pragma unroll
-        for (int r = 0; r < 16; ++r) m[(b + r) * kPitch + b + c] = x[r];
+        for (int r = 0; r < 8; ++r) m[(b + r) * kPitch + b + c] = x[r];
     }
     __syncthreads();
-    // joins of 16: blocks (1, 0) and (3, 2); two elements to a thread
-    {
-        const int two = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2;
-        const float* X = m + two * 32 * kPitch + two * 32;
-        const float* L = X + 16 * kPitch;
-        const float* Z = L + 16;
-        float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(L + r * kPitch + j);
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = *reinterpret_cast<const float2*>(X + (j + e) * kPitch + c);
-                a0 = fmaf(lv[e], x.x, a0);
-                a1 = fmaf(lv[e], x.y, a1);
-            }
-        }
-        *reinterpret_cast<float2*>(tmp + (two * 16 + r) * 36 + c) = make_float2(a0, a1);
-        __syncthreads();
-        a0 = a1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(Z + r * kPitch + j);
-            const float zv[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = *reinterpret_cast<const float2*>(tmp + (two * 16 + j + e) * 36 + c);
-                a0 = fmaf(-zv[e], x.x, a0);
-                a1 = fmaf(-zv[e], x.y, a1);
-            }
-        }
-        *reinterpret_cast<float2*>(m + (two * 32 + 16 + r) * kPitch + two * 32 + c) = make_float2(a0, a1);
-    }
-    __syncthreads();
-    // join of 32: four elements to a thread
-    {
-        const int r = tid >> 3, c = (tid & 7) * 4;
-        const float* L = m + (32 + r) * kPitch;
-        f2 s0 = 0, s1 = 0;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(L + j);
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(m + (j + e) * kPitch + c);
-                s0 = fma2(pair(lv[e], lv[e]), x.x, s0);
-                s1 = fma2(pair(lv[e], lv[e]), x.y, s1);
-            }
-        }
-        *reinterpret_cast<ulonglong2*>(tmp + r * 36 + c) = make_ulonglong2(s0, s1);
-        __syncthreads();
-        s0 = s1 = 0;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(L + 32 + j);
-            const float zv[4] = {-z.x, -z.y, -z.z, -z.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(tmp + (j + e) * 36 + c);
-                s0 = fma2(pair(zv[e], zv[e]), x.x, s0);
-                s1 = fma2(pair(zv[e], zv[e]), x.y, s1);
-            }
-        }
-        *reinterpret_cast<ulonglong2*>(m + (32 + r) * kPitch + c) = make_ulonglong2(s0, s1);
-    }
-    __syncthreads();
+    join_blocks<8, 1>(m, tmp, (tid >> 6) * 16, (tid >> 6) * 8, (tid >> 3) & 7, tid & 7);
+    join_blocks<16, 2>(m, tmp, (tid >> 7) * 32, (tid >> 7) * 16, (tid >> 3) & 15, (tid & 7) * 2);
+    join_blocks<32, 4>(m, tmp, 0, 0, tid >> 3, (tid & 7) * 4);
 }
 
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
@@ -274,10 +248,11 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     float* tmp = reinterpret_cast<float*>(smem + M::tmp);
     Gates* gates = reinterpret_cast<Gates*>(smem + M::gates);
     float* s_beta = reinterpret_cast<float*>(smem + M::misc);
-    float* s_most = s_beta + kC;                                  // [2][8]
+    float* s_dec = s_beta + kC;                                   // [32]: decays to step 31
+    float* s_most = s_dec + 32;                                   // [2][8]
     long long* s_sum = reinterpret_cast<long long*>(s_most + 16);
-    uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN (two words each)
-    uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 4);
+    uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
+    uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
     uint64_t* bar_mma = bar_in + 1;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mma + 1);
 
@@ -285,33 +260,33 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane, i = row & 63;
     const bool is_q = row >= kC;
 
-    auto load = [&](long long ch) {  // K and Q of a chunk (one thread)
-        const int c = (int)(ch % a.d.chunks);
-        const long long bh = ch / a.d.chunks;
-        const int b = (int)(bh / a.d.heads), group = (int)(bh % a.d.heads) / (a.d.heads / a.d.groups);
+    const unsigned chunks = a.d.chunks, heads = a.d.heads, ratio = heads / a.d.groups;
+    auto load = [&](unsigned ch) {  // K and Q of a chunk (one thread)
+        const unsigned bh = ch / chunks, b = bh / heads;
+        const int t0 = (int)(ch - bh * chunks) * kC, group = (int)((bh - b * heads) / ratio);
         mbar_arrive_expect_tx(bar_in, kq_bytes(DK));
         for (int p = 0; p < NP; ++p) {
-            tma_load_4d(smem + M::kq + p * 2 * kTile, &tm_k, bar_in, 64 * p, group, c * kC, b);
-            tma_load_4d(smem + M::kq + p * 2 * kTile + kTile, &tm_q, bar_in, 64 * p, group, c * kC, b);
+            tma_load_4d(smem + M::kq + p * 2 * kTile, &tm_k, bar_in, 64 * p, group, t0, b);
+            tma_load_4d(smem + M::kq + p * 2 * kTile + kTile, &tm_q, bar_in, 64 * p, group, t0, b);
         }
     };
     float g = 0.0f, beta = 0.0f;  // of step tid, one chunk ahead
-    auto fetch = [&](long long ch) {
+    auto fetch = [&](unsigned ch) {
         if (tid >= kC) return;
-        const int t = (int)(ch % a.d.chunks) * kC + tid;
-        const long long bh = ch / a.d.chunks;
-        const long long at = ((bh / a.d.heads) * a.d.seqlen + t) * a.d.heads + bh % a.d.heads;
+        const unsigned bh = ch / chunks, b = bh / heads;
+        const int t = (int)(ch - bh * chunks) * kC + tid;
+        const long long at = ((long long)b * a.d.seqlen + t) * heads + (bh - b * heads);
         const bool in = t < a.d.seqlen;
         g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
         beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
     };
-    if ((long long)blockIdx.x < a.count) fetch(blockIdx.x);
+    if (blockIdx.x < a.count) fetch(blockIdx.x);
     if (warp == 0) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
         mbar_init(bar_in, 1);
         mbar_init(bar_mma, 1);
         fence_mbar_init();
-        if ((long long)blockIdx.x < a.count) load(blockIdx.x);
+        if (blockIdx.x < a.count) load(blockIdx.x);
     }
     tc_fence_before();
     __syncthreads();
@@ -322,8 +297,8 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     bool landing = false;  // (thread 0) a load is on its way
     uint32_t mma_phase = 0, in_phase = 0;
 
-    for (long long ch = blockIdx.x; ch < a.count && ok; ch += gridDim.x) {
-        uint8_t* rec = a.records + ch * rec_bytes(DK);
+    for (unsigned ch = blockIdx.x; ch < a.count && ok; ch += gridDim.x) {
+        uint8_t* rec = a.records + (size_t)ch * rec_bytes(DK);
         const bool more = ch + gridDim.x < a.count;
         // ---- the gates: base-2 logarithms summed as integers of 2^-32, so that differences
         // of far sums are as exact as near ones (a decay of 2^-300 and less is 0 all the same)
@@ -339,15 +314,18 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             }
             const uint32_t off = __ballot_sync(0xffffffffu, beta == 0.0f);
             const uint32_t bad = __ballot_sync(0xffffffffu, isnan(g));
+            const uint32_t grows = __ballot_sync(0xffffffffu, !(g <= 0.0f));
             if (lane == 0) {
                 s_flags[warp] = off;
                 s_flags[2 + warp] = bad;
+                s_flags[4 + warp] = grows;
             }
             if (tid == 31) *s_sum = sum;
         }
         if (tid == 0) bulk_wait_read_all();  // the last chunk's stores have left shared memory
         __syncthreads();
         const unsigned long long masked = (unsigned long long)s_flags[1] << 32 | s_flags[0];
+        const bool grows = s_flags[4] | s_flags[5];
         if (tid < kC) {
             if (warp == 1) sum += *s_sum;
             const unsigned long long bad = (unsigned long long)s_flags[3] << 32 | s_flags[2];
@@ -359,7 +337,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             gates->lo[tid] = lo;
             if (tid == 0) gates->masked = masked;
             const float e = ex2_approx(hi + lo);
-            const float m = warp_most<2>((const float[2]){e, 0.0f});
+            const float m = warp_most(e);
             if (lane == 0) s_most[8 + warp] = m;
         }
         if (more) fetch(ch + gridDim.x);
@@ -376,25 +354,24 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             const int at = tid + kRecThreads * e, r = (at >> 3) & 127;
             raw[e] = *reinterpret_cast<const uint4*>(smem + M::kq + at * 16);
             if (r < kC && (masked >> r & 1)) raw[e] = make_uint4(0, 0, 0, 0);
-            float x[8];
-            unpack8_bf16(raw[e], x);
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) most = fmaxf(most, fmaxf(fabsf(x[k]), fabsf(x[k + 1])));
+            most = fmaxf(most, most8_bf16(raw[e]));
         }
-        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+        most = warp_most(most);
         if (lane == 0) s_most[warp] = most;
         ok = __syncthreads_and(ok);
         float s_kq;
         const float kq_scale = tile_scale(most_of<8>(s_most), kTop, s_kq);
 #pragma unroll
         for (int e = 0; e < NP * 4; ++e) {
-            float x[8];
+            f2 x[4];
             uint32_t w[4];
             unpack8_bf16(raw[e], x);
-            round_to<8>(x, kq_scale, w);
+            scaled<4>(x, kq_scale, x);
+            round_to<4>(x, w);
             *reinterpret_cast<uint4*>(smem + M::kq + (tid + kRecThreads * e) * 16) =
                 make_uint4(w[0], w[1], w[2], w[3]);
         }
+        if (tid < 32) s_dec[tid] = decay(gates->hi[31], gates->lo[31], gates->hi[tid], gates->lo[tid]);
         if (tid == 0) {
             gates->s_kq = s_kq;
             gates->e_max = fmaxf(s_most[8], s_most[9]);
@@ -416,38 +393,63 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         ok = warp_wait(bar_mma, mma_phase, a.status) && ok;
         mma_phase ^= 1;
         tc_fence_after();
-        float x[32];
-        if (ok) {
+        f2 x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0;
+        // rows 0 to 31 have nothing in columns 32 to 63
+        const bool any = !(part == 1 && (quarter & 1) == 0);
+        if (ok && any) {
             tmem_ld32(t_lane + kTmX + 32 * part, x);
             tmem_wait_ld();
             const float hi = gates->hi[i], lo = gates->lo[i];
             const float f = s_kq * s_kq * (is_q ? 1.0f : s_beta[i]);
-            const int last = is_q ? i : i - 1;  // of the columns that count
+            const int j0 = 32 * part;
+            if (part == 0 && (quarter & 1) && !grows) {
+                // rows behind 32, columns before it: the decay from step 31 to the row times
+                // that from the column to step 31, neither above 1
+                const float e_i = f * decay(hi, lo, gates->hi[31], gates->lo[31]);
+                const f2 e2 = pair(e_i, e_i);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const int j = 32 * part + e;
-                const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
-                const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
-                x[e] = j <= last ? f * x[e] * decay(hi, lo, h4.x, l4.x) : 0.0f;
-                x[e + 1] = j + 1 <= last ? f * x[e + 1] * decay(hi, lo, h4.y, l4.y) : 0.0f;
-                x[e + 2] = j + 2 <= last ? f * x[e + 2] * decay(hi, lo, h4.z, l4.z) : 0.0f;
-                x[e + 3] = j + 3 <= last ? f * x[e + 3] * decay(hi, lo, h4.w, l4.w) : 0.0f;
+                for (int e = 0; e < 16; e += 2) {
+                    const float4 d4 = *reinterpret_cast<const float4*>(s_dec + 2 * e);
+                    x[e] = mul2(x[e], mul2(e2, pair(d4.x, d4.y)));
+                    x[e + 1] = mul2(x[e + 1], mul2(e2, pair(d4.z, d4.w)));
+                }
+            } else {
+                const int last = is_q ? i : i - 1;  // of the columns that count
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const int j = j0 + 2 * e;
+                    const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
+                    const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
+                    const float d0 = j <= last ? f * decay(hi, lo, h4.x, l4.x) : 0.0f;
+                    const float d1 = j + 1 <= last ? f * decay(hi, lo, h4.y, l4.y) : 0.0f;
+                    const float d2 = j + 2 <= last ? f * decay(hi, lo, h4.z, l4.z) : 0.0f;
+                    const float d3 = j + 3 <= last ? f * decay(hi, lo, h4.w, l4.w) : 0.0f;
+                    // (columns past the row may hold a q that is not finite)
+                    float a0, a1, a2, a3;
+                    unpair(x[e], a0, a1);
+                    unpair(x[e + 1], a2, a3);
+                    x[e] = pair(j <= last ? a0 * d0 : 0.0f, j + 1 <= last ? a1 * d1 : 0.0f);
+                    x[e + 1] = pair(j + 2 <= last ? a2 * d2 : 0.0f, j + 3 <= last ? a3 * d3 : 0.0f);
+                }
             }
-            if (!is_q)
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(tri + i * kPitch + 32 * part + e) =
-                        make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
-        most = warp_most<32>(x);
+        if (!is_q)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+                *reinterpret_cast<ulonglong2*>(tri + i * kPitch + 32 * part + 2 * e) =
+                    make_ulonglong2(x[e], x[e + 1]);
+        most = warp_most<16>(x);
         if (lane == 0 && is_q) s_most[(quarter & 1) * 2 + part] = most;
         tc_fence_before();
         ok = __syncthreads_and(ok);
         float s_p;  // of the operand (Q K^T) D
         const float p_scale = tile_scale(most_of<4>(s_most), kTop, s_p);
+        uint32_t hw[16], lw[16];
         if (is_q) {
-            uint32_t hw[16], lw[16];
-            split<32>(x, p_scale, hw, lw);
+            scaled<16>(x, p_scale, x);
+            split<16>(x, hw, lw);
             put32(smem + M::p_hi, i, 4 * part, hw);
             put32(smem + M::p_lo, i, 4 * part, lw);
         }
@@ -458,17 +460,16 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         {
             const int r = tid >> 2, j0 = (tid & 3) * 16;
             const float w = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[r], gates->lo[r]);
-            float t[16], wt[16];
+            f2 t[8], wt[8];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4 m4 = *reinterpret_cast<const float4*>(tri + r * kPitch + j0 + e);
-                const float4 b4 = *reinterpret_cast<const float4*>(s_beta + j0 + e);
-                t[e] = m4.x * b4.x; t[e + 1] = m4.y * b4.y;
-                t[e + 2] = m4.z * b4.z; t[e + 3] = m4.w * b4.w;
+            for (int e = 0; e < 8; e += 2) {
+                const ulonglong2 m2 = *reinterpret_cast<const ulonglong2*>(tri + r * kPitch + j0 + 2 * e);
+                const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(s_beta + j0 + 2 * e);
+                t[e] = mul2(m2.x, b2.x);
+                t[e + 1] = mul2(m2.y, b2.y);
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) wt[e] = w * t[e];
-            const float mt = warp_most<16>(t), mw = warp_most<16>(wt);
+            scaled<8>(t, w, wt);
+            const float mt = warp_most<8>(t), mw = warp_most<8>(wt);
             if (lane == 0) {
                 s_most[warp] = mt;
                 s_most[8 + warp] = mw;
@@ -477,8 +478,10 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             const float t_scale = tile_scale(most_of<8>(s_most), kTop, s_t);
             const float w_scale = tile_scale(most_of<8>(s_most + 8), kTop, s_w);
             uint32_t th[8], tl[8], wh[8], wl[8];
-            split<16>(t, t_scale, th, tl);
-            split<16>(wt, w_scale, wh, wl);
+            scaled<8>(t, t_scale, t);
+            scaled<8>(wt, w_scale, wt);
+            split<8>(t, th, tl);
+            split<8>(wt, wh, wl);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const uint32_t off = piece(r, (j0 >> 3) + s);
@@ -531,26 +534,25 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             if (more) load(ch + gridDim.x);
             landing = more;
         }
-        float hx[32], px[32];
+        f2 hx[16], px[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hx[e] = px[e] = 0;
         if (ok) {
-            float y[32];
-            if (row < DK) {
-                tmem_ld32(t_lane + kTmH + 32 * part, hx);
-                tmem_ld32(t_lane + kTmH + 64 + 32 * part, y);
-                tmem_wait_ld();
+            auto both = [&](uint32_t at, f2* v) {  // columns of the hi and the lo part
 #pragma unroll
-                for (int e = 0; e < 32; ++e) hx[e] += y[e];
-            }
-            if (is_q) {
-                tmem_ld32(t_lane + kTmP + 32 * part, px);
-                tmem_ld32(t_lane + kTmP + 64 + 32 * part, y);
-                tmem_wait_ld();
+                for (int e0 = 0; e0 < 16; e0 += 8) {
+                    f2 y[8];
+                    tmem_ld16(t_lane + at + 2 * e0, v + e0);
+                    tmem_ld16(t_lane + at + 64 + 2 * e0, y);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) px[e] += y[e];
-            }
+                    for (int e = 0; e < 8; ++e) v[e0 + e] = add2(v[e0 + e], y[e]);
+                }
+            };
+            if (row < DK) both(kTmH + 32 * part, hx);
+            if (is_q) both(kTmP + 32 * part, px);
         }
-        const float mh = row < DK ? warp_most<32>(hx) : 0.0f;
-        const float mp = is_q ? warp_most<32>(px) : 0.0f;
+        const float mh = warp_most<16>(hx), mp = warp_most<16>(px);
         if (lane == 0) {
             s_most[warp] = mh;
             s_most[8 + warp] = mp;
@@ -561,14 +563,15 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         float s_h2, s_p2;
         const float h_scale = tile_scale(most_of<8>(s_most), kTop, s_h2);
         const float p2_scale = tile_scale(most_of<8>(s_most + 8), kTop, s_p2);
-        uint32_t hw[16], lw[16];
         if (row < DK) {
-            split<32>(hx, h_scale, hw, lw);
+            scaled<16>(hx, h_scale, hx);
+            split<16>(hx, hw, lw);
             put32(smem + M::t_hi, row, 4 * part, hw);
             put32(smem + M::t_hi + h_bytes(DK), row, 4 * part, lw);
         }
         if (is_q) {
-            split<32>(px, p2_scale, hw, lw);
+            scaled<16>(px, p2_scale, px);
+            split<16>(px, hw, lw);
             put32(smem + M::p_hi, i, 4 * part, hw);
             put32(smem + M::p_lo, i, 4 * part, lw);
         }
@@ -742,57 +745,44 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int col0 = pan * kPan + 32 * part;      // first column of headdim
         const bool on_k = row < kC;                   // of [K; Q] S0
         const int i = row & 63;
-        float S[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            S[e] = a.h0 && row < a.d.dk && col0 + e < a.d.dv
-                       ? a.h0[(bh * a.d.dv + col0 + e) * a.d.dk + row] : 0.0f;
+        f2 S[16];          // times its operand's factor; s_s undoes it
+        float s_s = 0.0f;
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float f_row = 0.0f, e_end = 0.0f, k_bound = 0.0f, h_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
-        bool off = true, cut = false;
+        float f_row = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        bool off = true;
         auto gates_of = [&](int c) {
             const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
-            const float e = ex2_approx(g->hi[i] + g->lo[i]);
-            cut = e == 0.0f;  // the chunk starts anew before this row, whatever S0 is
-            f_row = e * g->s_kq;
+            f_row = ex2_approx(g->hi[i] + g->lo[i]) * g->s_kq;
             e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
             off = g->masked >> i & 1;
             s_h = g->s_h;
             s_p = g->s_p;
-            // bounds of e |K|_1 and |H|_1 over a row, in units of the largest S and R
+            // of e |K|_1 over a row, in units of the largest S
             k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
-            h_bound = kC * 2 * kTopValue * s_h;
             return in;
         };
-        // the largest values of S (all warps) and of the next V (the warps on Q rows), for
-        // the factors of chunk c
+        // the largest values of S (all warps) and of V (the warps on Q rows), for the
+        // factors of chunk c
         auto maxima = [&](int c) {
-            const float m = warp_most<32>(S);
+            const float m = warp_most<16>(S) * s_s;
             if (lane == 0) s_most[12 * (c & 1) + warp] = m;
             if (!on_k) {
                 float v = 0.0f;
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    float x[8];
-                    unpack8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p)), x);
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) v = fmaxf(v, fmaxf(fabsf(x[e]), fabsf(x[e + 1])));
-                }
-                if (off) v = 0.0f;
-                v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+                for (int p = 0; p < 4; ++p)
+                    v = fmaxf(v, most8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p))));
+                v = warp_most(off ? 0.0f : v);
                 if (lane == 0) s_most[12 * (c & 1) + 8 + (quarter & 1) * 2 + part] = v;
             }
             warp_arrive(bar_m);
         };
         // S0 of chunk c as an operand, and kept
-        float s_s = 0.0f;  // S0's factor, undone
-        auto put_state = [&](int c, float bound) {
-            const float scale = tile_scale(bound, kBoundTop, s_s);
+        auto put_state = [&](int c) {
             uint32_t hw[16], lw[16];
             if (row < DK) {
-                split<32>(S, scale, hw, lw);
+                split<16>(S, hw, lw);
                 put32(smem + M::s_hi, row, 4 * part, hw);
                 put32(smem + M::s_lo, row, 4 * part, lw);
             }
@@ -805,51 +795,65 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK) + 4) = s_s;
             }
         };
-        {   // the first chunk: its largest values are measured
-            const float m = warp_most<32>(S);
+        bool ok = gates_of(0);
+        {   // the first chunk: its largest values are measured.  A state that the first step
+            // starts anew is not looked at
+            const Gates* g = reinterpret_cast<const Gates*>(smem);
+            const bool given = a.h0 && row < a.d.dk && ex2_approx(g->hi[0] + g->lo[0]) != 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float* at = a.h0 + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
+                // (columns come in eights)
+                const bool in = given && col0 + 2 * e < a.d.dv;
+                S[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
+            }
+            const float m = warp_most<16>(S);
             if (lane == 0) s_most[12 + warp] = m;
             named_bar_sync(1, 256);
-            put_state(0, most_of<8>(s_most + 12));
+            scaled<16>(S, tile_scale(most_of<8>(s_most + 12), kBoundTop, s_s), S);
+            put_state(0);
         }
-        bool ok = gates_of(0);
         if (ok) maxima(0);
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
-            const float fs = f_row * s_s, ee = e_end, sp = s_p, sh = s_h, hb = h_bound;
-            const bool none = cut;
-            float x[32];
-            ok = warp_wait(bar_m, ph, a.status) && warp_wait(bar_x, ph, a.status);
+            const float fs = f_row * s_s, ee = e_end, sp = s_p, sh = s_h;
+            f2 x[16];
+            ok = warp_wait(bar_m, ph, a.status);
             if (!ok) break;
-            tc_fence_after();
             const float s_max = most_of<8>(s_most + 12 * ph);
             const float r_bound = fmaf(k_bound, s_max, most_of<4>(s_most + 12 * ph + 8));
-            float s_r;
+            float s_r, s_next;
             const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
+            // |H|_1 over a row is at most 64 times its largest value
+            const float next = tile_scale(fmaf(ee, s_max, kC * 2 * kTopValue * sh * r_bound), kBoundTop, s_next);
+            ok = warp_wait(bar_x, ph, a.status);
+            if (!ok) break;
+            tc_fence_after();
             tmem_ld32(t_lane + kTmX, x);
-            if (on_k || PLO) {
-                float y[32];
-                tmem_ld32(t_lane + kTmX + 64, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] += y[e];
-            } else {
-                tmem_wait_ld();
-            }
             if (on_k) {
                 // (the products that read R before are done: bar_x follows them)
+                f2 y[16];
+                tmem_ld32(t_lane + kTmX + 64, y);
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
+                uint4 v[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    float v[8];
-                    unpack8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p)), v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[8 * p + e] = none ? v[e] : fmaf(-fs, x[8 * p + e], v[e]);
+                    v[p] = make_uint4(0, 0, 0, 0);
+                    // a masked step's value is not looked at (its row of K is 0)
+                    if (!off) v[p] = *reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p));
                 }
-                if (off)
+                const f2 f = pair(-fs * r_scale, -fs * r_scale), rs = pair(r_scale, r_scale);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = 0.0f;
+                for (int p = 0; p < 4; ++p) {
+                    f2 w[4];
+                    unpack8_bf16(v[p], w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[4 * p + e] = fma2(f, add2(x[4 * p + e], y[4 * p + e]), mul2(w[e], rs));
+                }
                 uint32_t hw[16], lw[16];
-                split<32>(x, r_scale, hw, lw);
+                split<16>(x, hw, lw);
                 put32(smem + M::r_hi, i, 4 * part, hw);
                 put32(smem + M::r_lo, i, 4 * part, lw);
                 fence_proxy_async_smem();
@@ -860,28 +864,34 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     put32(k, i, 4 * part, hw);
                     if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK)) = s_r;
                 }
+            } else {
+                if constexpr (PLO) {
+                    f2 y[16];
+                    tmem_ld32(t_lane + kTmX + 64, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = add2(x[e], y[e]);
+                } else {
+                    tmem_wait_ld();
+                }
             }
+            const float decayed = ee * s_s * next, added = sh * s_r * next;
+            const f2 a2 = pair(added, added);
+            scaled<16>(S, decayed, S);
             ok = warp_wait(bar_h, ph, a.status);
             if (!ok) break;
             tc_fence_after();
-            if (ee == 0.0f)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[e] = 0.0f;
-#pragma unroll
-            for (int e0 = 0; e0 < 32; e0 += 16) {
-                const f2 f = pair(sh * s_r, sh * s_r), e2 = pair(ee, ee);
-                float z[16], y[16];
-                tmem_ld16(t_lane + kTmH + e0, z);
-                tmem_ld16(t_lane + kTmH + 64 + e0, y);
+            {
+                f2 z[16], y[16];
+                tmem_ld32(t_lane + kTmH, z);
+                tmem_ld32(t_lane + kTmH + 64, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const f2 hr = add2(pair(z[e], z[e + 1]), pair(y[e], y[e + 1]));
-                    unpair(fma2(e2, pair(S[e0 + e], S[e0 + e + 1]), mul2(f, hr)), S[e0 + e], S[e0 + e + 1]);
-                }
+                for (int e = 0; e < 16; ++e) S[e] = fma2(a2, add2(z[e], y[e]), S[e]);
             }
+            s_s = s_next;
             if (c + 1 < nc) {
-                put_state(c + 1, fmaf(ee, s_max, hb * r_bound));
+                put_state(c + 1);
                 ok = gates_of(c + 1);
                 if (!ok) break;
                 maxima(c + 1);
@@ -890,14 +900,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 ok = warp_wait(bar_y, ph, a.status);
                 if (!ok) break;
                 tc_fence_after();
-                float z[32];
+                f2 z[16];
                 tmem_ld32(t_lane + kTmY, z);
                 if constexpr (PLO) {
-                    float y[32];
+                    f2 y[16];
                     tmem_ld32(t_lane + kTmY + 64, y);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) z[e] += y[e];
+                    for (int e = 0; e < 16; ++e) z[e] = add2(z[e], y[e]);
                 } else {
                     tmem_wait_ld();
                 }
@@ -907,16 +917,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (a.y && t < a.d.seqlen) {
                     TO* y = static_cast<TO*>(a.y) +
                             (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                    const float f = sp * s_r;
+                    const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         if (col0 + 8 * p >= a.d.dv) break;
-                        float o[8];
+                        f2 o[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float own = f * z[8 * p + e];
-                            o[e] = none ? own : fmaf(fs, x[8 * p + e], own);
-                        }
+                        for (int e = 0; e < 4; ++e) o[e] = fma2(q, x[4 * p + e], mul2(f, z[4 * p + e]));
                         store8(y + 8 * p, o);
                     }
                 }
@@ -924,8 +931,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         if (a.last && row < a.d.dk)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (col0 + e < a.d.dv) a.last[(bh * a.d.dv + col0 + e) * a.d.dk + row] = S[e];
+            for (int e = 0; e < 16; ++e)
+                if (col0 + 2 * e < a.d.dv) {
+                    float v0, v1;
+                    unpair(S[e], v0, v1);
+                    float* at = a.last + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
+                    at[0] = v0 * s_s;
+                    at[a.d.dk] = v1 * s_s;
+                }
     }
     tc_fence_before();
     __syncthreads();
@@ -955,9 +968,9 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     r.g = f.g; r.beta = f.beta; r.records = f.records; r.status = f.status; r.d = d;
     r.gates_bf16 = f.gate_dtype == SSM_BF16;
     r.keep_t = f.kept != nullptr;
-    r.count = (long long)f.batch * f.heads * d.chunks;
+    r.count = (unsigned)((long long)f.batch * f.heads * d.chunks);
     if (!allow_smem(records_kernel<DK>, RecSmem<DK>::bytes)) return SSM_ERR_CUDA;
-    records_kernel<DK><<<(unsigned)std::min<long long>(r.count, 2 * sms), kRecThreads,
+    records_kernel<DK><<<std::min<unsigned>(r.count, 2 * sms), kRecThreads,
                          RecSmem<DK>::bytes, s>>>(mq, mk, r);
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;

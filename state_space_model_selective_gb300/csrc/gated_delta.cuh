@@ -106,30 +106,47 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// n values times `scale` as hi + lo, pairs.
+// N pairs as hi + lo.
 template <int N>
-__device__ __forceinline__ void split(const float* v, float scale, uint32_t* hi, uint32_t* lo) {
-    const f2 s = pair(scale, scale);
+__device__ __forceinline__ void split(const f2* x, uint32_t* hi, uint32_t* lo) {
+    const f2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
+    for (int e = 0; e < N; ++e) {
         float a, b;
-        const f2 x = mul2(pair(v[2 * e], v[2 * e + 1]), s);
-        unpair(x, a, b);
+        unpair(x[e], a, b);
         hi[e] = pack_f16(a, b);
         const float2 h = unpack_f16(hi[e]);
-        unpair(add2(x, pair(-h.x, -h.y)), a, b);
+        unpair(fma2(pair(h.x, h.y), minus, x[e]), a, b);
         lo[e] = pack_f16(a, b);
     }
 }
 template <int N>
-__device__ __forceinline__ void round_to(const float* v, float scale, uint32_t* hi) {
-    const f2 s = pair(scale, scale);
+__device__ __forceinline__ void round_to(const f2* x, uint32_t* hi) {
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
+    for (int e = 0; e < N; ++e) {
         float a, b;
-        unpair(mul2(pair(v[2 * e], v[2 * e + 1]), s), a, b);
+        unpair(x[e], a, b);
         hi[e] = pack_f16(a, b);
     }
+}
+template <int N>
+__device__ __forceinline__ void scaled(const f2* x, float scale, f2* y) {
+    const f2 s = pair(scale, scale);
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = mul2(x[e], s);
+}
+// 16 or 32 columns of this thread's lane of tensor memory, as pairs.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, f2* v) {
+    float x[32];
+    ssm::tmem_ld32(taddr, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = pair(x[2 * e], x[2 * e + 1]);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, f2* v) {
+    float x[16];
+    ssm::tmem_ld16(taddr, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = pair(x[2 * e], x[2 * e + 1]);
 }
 
 // A tile's factor: a power of two that brings `most` (the largest magnitude, or a bound of
@@ -147,12 +164,19 @@ constexpr int kBoundTop = 14;  // of a bound
 // The largest stored magnitude of a tile scaled by its maximum.
 constexpr float kTopValue = 8192.0f;
 
-// The largest magnitude of n values over a warp (NaN aside).
+// The largest magnitude of N pairs over a warp (NaN aside).
 template <int N>
-__device__ __forceinline__ float warp_most(const float* v) {
+__device__ __forceinline__ float warp_most(const f2* v) {
     float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) m = fmaxf(m, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
+    for (int e = 0; e < N; ++e) {
+        float a, b;
+        unpair(v[e], a, b);
+        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+    }
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+__device__ __forceinline__ float warp_most(float m) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 template <int N>
@@ -176,30 +200,41 @@ __device__ __forceinline__ void put32(uint8_t* tile, int r, int c0, const uint32
         *reinterpret_cast<uint4*>(tile + piece(r, c0 + c)) =
             make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
-__device__ __forceinline__ void unpack8_bf16(uint4 w, float* f) {
+__device__ __forceinline__ void unpack8_bf16(uint4 w, f2* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        f[2 * e] = bf16lo(u[e]);
-        f[2 * e + 1] = bf16hi(u[e]);
-    }
+    for (int e = 0; e < 4; ++e) f[e] = pair(bf16lo(u[e]), bf16hi(u[e]));
 }
-__device__ __forceinline__ void unpack8_f16(uint4 w, float* f) {
+__device__ __forceinline__ void unpack8_f16(uint4 w, f2* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 h = unpack_f16(u[e]);
-        f[2 * e] = h.x;
-        f[2 * e + 1] = h.y;
+        f[e] = pair(h.x, h.y);
     }
 }
-__device__ __forceinline__ void store8(float* p, const float* o) {
-    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(o[4], o[5], o[6], o[7]);
+// The largest magnitude of 8 bf16.
+__device__ __forceinline__ float most8_bf16(uint4 w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t m = 0;  // magnitudes compare as integers
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
+    return __uint_as_float(m);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* o) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
-                                              pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+// 4 pairs to 8 consecutive elements.
+__device__ __forceinline__ void store8(float* p, const f2* o) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(o[0], o[1]);
+    *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(o[2], o[3]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f2* o) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a, b;
+        unpair(o[e], a, b);
+        w[e] = pack_bf16(a, b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
@@ -247,9 +282,26 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+// mbar_wait for what is due in a moment: looks without being put to sleep first (a woken
+// thread is some 200 cycles late, of the 2500 that a chunk takes).
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    const uint32_t addr = smem_u32(bar);
+    for (int i = 0; i < 256; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return mbar_wait(bar, parity, status);
+}
 // A wait that a whole warp takes together, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+    return __all_sync(0xffffffffu, mbar_poll(bar, parity, status));
 }
 
 struct Dims {

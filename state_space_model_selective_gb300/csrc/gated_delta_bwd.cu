@@ -9,9 +9,8 @@
 //   U = T' R;  F = [dR; dY] S0^T;  F2 = U L^T;  [dA'; dP'] = [-dR; dY] U^T
 //   dKK = dA' D (j < i),  dQK = dP' D (j <= i)          (beta cancels in dA A: dR = beta T^T dU)
 //   dQ = dQK K + e F_q;   dK = dKK K + dKK^T K + dQK^T Q - e F_k + w F2
-//   dbeta_i = (dR_i . R_i + sum_j dKK_ij KK_ij) / beta_i
-//   dg_t = sum_{i >= t} (sums of row i less sums of column i of M + e_i (q_i F_q,i - k_i F_k,i))
-//          + sum_{j < t} w_j k_j F2_j + e_63 <L, S0>,   M = dKK KK + dQK QK
+//   dbeta_i = (dR_i . R_i + k_i . (dKK K)_i) / beta_i
+//   dg_t = sum_{i >= t} dG_i + sum_{j < t} w_j k_j . F2_j + e_63 <L, S0>   (grads_kernel)
 #include <algorithm>
 #include <cstring>
 
@@ -194,12 +193,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int col0 = pan * kPan + 32 * part;
         const bool upper = row >= kC;   // these rows make dY and e dY
         const int i = row & 63;
-        float* xch = reinterpret_cast<float*>(smem + M::xch) + 32 * part * 64 + i;
-        float L[32];
+        f2* xch = reinterpret_cast<f2*>(smem + M::xch) + 16 * part * 64 + i;
+        f2 L[16];          // times its operand's factor; s_l undoes it
+        float s_l = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            L[e] = a.dlast && row < a.d.dk && col0 + e < a.d.dv
-                       ? a.dlast[(bh * a.d.dv + col0 + e) * a.d.dk + row] : 0.0f;
+        for (int e = 0; e < 16; ++e) {
+            const float* at = a.dlast + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
+            // (columns come in eights)
+            const bool in = a.dlast && row < a.d.dk && col0 + 2 * e < a.d.dv;
+            L[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
+        }
         auto kept_of = [&](int c) {
             return a.kept + ((bh * nc + c) * a.d.pans + pan) * adjoint_bytes(DK);
         };
@@ -216,19 +219,17 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             s_p = g->s_p;
             return in;
         };
-        float s_l = 0.0f;  // L's factor, undone
-        auto put_state = [&](int it, float bound) {
-            const float scale = tile_scale(bound, kBoundTop, s_l);
+        auto put_state = [&](int it) {
             uint32_t hw[16], lw[16];
             if (row < DK) {
-                split<32>(L, scale, hw, lw);
+                split<16>(L, hw, lw);
                 put32(smem + M::l_hi, row, 4 * part, hw);
                 put32(smem + M::l_lo, row, 4 * part, lw);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(bar_s);
-            const float m = warp_most<32>(L);
+            const float m = warp_most<16>(L) * s_l;
             if (lane == 0) s_most[12 * (it & 1) + warp] = m;
             warp_arrive(bar_m);
             uint8_t* k = kept_of(nc - 1 - it);
@@ -247,37 +248,42 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                             : make_uint4(0, 0, 0, 0);
         };
         // (upper warps) dY and e dY of step `it` as operands, dY kept
-        float s_dy = 0.0f, s_o = 0.0f;
         auto put_dy = [&](int it, float e) {
-            float x[32];
+            f2 x[16], y[16];
+            float m = 0.0f;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) unpack8_bf16(dy[p], x + 8 * p);
-            const float m = warp_most<32>(x);
+            for (int p = 0; p < 4; ++p) {
+                m = fmaxf(m, most8_bf16(dy[p]));
+                unpack8_bf16(dy[p], x + 4 * p);
+            }
+            m = warp_most(m);
             float* most = s_most + 12 * (it & 1) + 8;
             if (lane == 0) most[(quarter & 1) * 2 + part] = m;
             named_bar_sync(2, 128);
             const float all = most_of<4>(most);
+            float s_dy, s_o;
             uint32_t hw[16], lw[16];
-            round_to<32>(x, tile_scale(all, kTop, s_dy), hw);
+            scaled<16>(x, tile_scale(all, kTop, s_dy), y);
+            round_to<16>(y, hw);
             put32(smem + M::dy, i, 4 * part, hw);
             uint8_t* k = kept_of(nc - 1 - it);
             put32(k + kTile, i, 4 * part, hw);
             if (tid == 64) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[1] = s_dy;
-#pragma unroll
-            for (int n = 0; n < 32; ++n) x[n] *= e;
-            split<32>(x, tile_scale(all * e_max, kBoundTop, s_o), hw, lw);
+            scaled<16>(x, e * tile_scale(all * e_max, kBoundTop, s_o), x);
+            split<16>(x, hw, lw);
             put32(smem + M::o_hi, i, 4 * part, hw);
             put32(smem + M::o_lo, i, 4 * part, lw);
             fence_proxy_async_smem();
             warp_arrive(bar_o);
         };
         {   // the last chunk: its largest values are measured
-            const float m = warp_most<32>(L);
+            const float m = warp_most<16>(L);
             if (lane == 0) s_most[12 + warp] = m;
             named_bar_sync(1, 256);
             const float all = most_of<8>(s_most + 12);
             named_bar_sync(1, 256);
-            put_state(0, all);
+            scaled<16>(L, tile_scale(all, kBoundTop, s_l), L);
+            put_state(0);
         }
         bool ok = gates_of(0);  // the same for all lanes of a warp
         fetch(nc - 1);
@@ -285,51 +291,50 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
-            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h;
+            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p;
             if (c > 0) fetch(c - 1);
-            float x[32];
-            ok = ok && warp_wait(bar_m, ph, a.status) && warp_wait(bar_o, ph, a.status) &&
-                 warp_wait(bar_x, ph, a.status);
-            tc_fence_after();
-            // bounds: of L and dY measured, of dR from them
+            f2 x[16];
+            ok = ok && warp_wait(bar_m, ph, a.status) && warp_wait(bar_o, ph, a.status);
+            // bounds: of L and dY measured, of dR and the next L from them
             const float l_max = most_of<8>(s_most + 12 * ph);
             const float dy_max = most_of<4>(s_most + 12 * ph + 8);
-            const float dr_bound = kC * kTopValue * s_p * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
-            float s_od;  // e dY's factor, undone (the upper warps' own s_dy and s_o)
-            (void)tile_scale(dy_max * em, kBoundTop, s_od);
-            float s_dyd;
+            const float dr_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
+            float s_od, s_dyd, s_r, s_g, s_next;
+            (void)tile_scale(dy_max * em, kBoundTop, s_od);  // (put_dy's factors)
             (void)tile_scale(dy_max, kTop, s_dyd);
-            float s_r, s_g;
             const float r_scale = tile_scale(dr_bound, kBoundTop, s_r);
             const float g_scale = tile_scale(dr_bound * em, kBoundTop, s_g);
+            const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f * skq * em *
+                                                              (dy_max + dr_bound)), kBoundTop, s_next);
+            ok = ok && warp_wait(bar_x, ph, a.status);
+            tc_fence_after();
             if (ok) {
-                const float fp = s_p * s_dyd, fx = sh * s_l;
-                float z[32];
+                const f2 fp = pair(sp * s_dyd, sp * s_dyd), fx = pair(sh * s_l, sh * s_l);
+                f2 z[16];
                 tmem_ld32(t_lane + kTmP, x);
                 tmem_ld32(t_lane + kTmX, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = fmaf(fp, x[e], fx * z[e]);
+                for (int e = 0; e < 16; ++e) x[e] = fma2(fp, x[e], mul2(fx, z[e]));
                 if (upper) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) xch[64 * e] = x[e];
+                    for (int e = 0; e < 16; ++e) xch[64 * e] = x[e];
                 } else {
                     tmem_ld32(t_lane + kTmX + 64, z);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = fmaf(fx, z[e], x[e]);
+                    for (int e = 0; e < 16; ++e) x[e] = fma2(fx, z[e], x[e]);
                 }
             }
             tc_fence_before();
             if (!named_bar_and(1, 256, ok)) break;  // all eight warps leave together
             if (!upper) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] += xch[64 * e];
+                for (int e = 0; e < 16; ++e) x[e] = add2(x[e], xch[64 * e]);
                 uint32_t hw[16], lw[16];
-                float y[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = -er * x[e];
-                split<32>(y, g_scale, hw, lw);
+                f2 y[16];
+                scaled<16>(x, -er * g_scale, y);
+                split<16>(y, hw, lw);
                 put32(smem + M::r_hi, i, 4 * part, hw);
                 put32(smem + M::r_lo, i, 4 * part, lw);
                 fence_proxy_async_smem();
@@ -340,52 +345,54 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                              (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        if (col0 + 8 * p < a.d.dv) store8(dv + 8 * p, x + 8 * p);
+                        if (col0 + 8 * p < a.d.dv) store8(dv + 8 * p, x + 4 * p);
                 }
-                round_to<32>(x, r_scale, hw);
+                scaled<16>(x, r_scale, x);
+                round_to<16>(x, hw);
                 uint8_t* k = kept_of(c);
                 put32(k, i, 4 * part, hw);
                 if (tid == 0) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[0] = s_r;
             }
             // ---- L0 = e_63 L + Q^T e dY - K^T e dR
-            ok = warp_wait(bar_q, ph, a.status);
-            tc_fence_after();
-            if (ee == 0.0f)
+            scaled<16>(L, ee * s_l * next, L);
+            s_l = s_next;
+            auto add = [&](uint32_t at, float factor) {
+                const f2 f = pair(factor, factor);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) L[e] = 0.0f;
-            auto add = [&](uint32_t at, float factor, float keep) {
-                const f2 f = pair(factor, factor), k2 = pair(keep, keep);
-#pragma unroll
-                for (int e0 = 0; e0 < 32; e0 += 16) {
-                    float z[16], y[16];
-                    tmem_ld16(t_lane + at + e0, z);
-                    tmem_ld16(t_lane + at + 64 + e0, y);
+                for (int e0 = 0; e0 < 16; e0 += 8) {
+                    f2 z[8], y[8];
+                    tmem_ld16(t_lane + at + 2 * e0, z);
+                    tmem_ld16(t_lane + at + 64 + 2 * e0, y);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const f2 s = add2(pair(z[e], z[e + 1]), pair(y[e], y[e + 1]));
-                        unpair(fma2(k2, pair(L[e0 + e], L[e0 + e + 1]), mul2(f, s)), L[e0 + e], L[e0 + e + 1]);
-                    }
+                    for (int e = 0; e < 8; ++e) L[e0 + e] = fma2(f, add2(z[e], y[e]), L[e0 + e]);
                 }
             };
-            if (ok) add(kTmQ, skq * s_od, ee);
+            ok = warp_wait(bar_q, ph, a.status);
+            tc_fence_after();
+            if (ok) add(kTmQ, skq * s_od * next);
             if (c > 0) {
-                ok = ok && gates_of(it + 1);
+                ok = gates_of(it + 1) && ok;
                 // (the products that read dY and e dY are done: bar_q follows them)
                 if (upper) put_dy(it + 1, e_row);
             }
             ok = ok && warp_wait(bar_l, ph, a.status);
             tc_fence_after();
             if (ok) {
-                add(kTmK, skq * s_g, 1.0f);
-                const float qk = kC * kTopValue * 2.0f * skq;
-                if (c > 0) put_state(it + 1, fmaf(ee, l_max, qk * em * (dy_max + dr_bound)));
+                add(kTmK, skq * s_g * next);
+                if (c > 0) put_state(it + 1);
             }
         }
         if (a.dh0 && row < a.d.dk)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (col0 + e < a.d.dv) a.dh0[(bh * a.d.dv + col0 + e) * a.d.dk + row] = L[e];
+            for (int e = 0; e < 16; ++e)
+                if (col0 + 2 * e < a.d.dv) {
+                    float v0, v1;
+                    unpair(L[e], v0, v1);
+                    float* at = a.dh0 + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
+                    at[0] = v0 * s_l;
+                    at[a.d.dk] = v1 * s_l;
+                }
     }
     tc_fence_before();
     __syncthreads();
@@ -395,6 +402,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 // ------------------------------------------------------------------ grads
 
 constexpr int kGradThreads = 288;  // 8 warps on rows, one that loads
+constexpr int kMaxPans = 4;
 
 template <int DK> struct GradSmem {
     // of a head (two in turn): gates, panels of [K | Q], T' (64 rows; the 64 behind them in its
@@ -413,9 +421,9 @@ template <int DK> struct GradSmem {
     static constexpr uint32_t w = u + kTile;            // operand are not read)
     static constexpr uint32_t sums = w + 2 * kTile;     // (W^T's second block, not read either)
     static constexpr uint32_t misc = sums + 4096;
-    static constexpr uint32_t factors = misc + 256;     // [2][8] floats
+    static constexpr uint32_t factors = misc + 256;     // [2 heads][4 panels][8] floats
     static constexpr uint32_t bytes = w + 3 * kTile;
-    static_assert(factors + 64 <= bytes, "sums fit behind W");
+    static_assert(factors + 256 <= bytes, "sums fit behind W");
 };
 
 struct GradArgs {
@@ -426,35 +434,46 @@ struct GradArgs {
     void *dq, *dk, *dg, *dbeta;
     uint32_t* status;
     Dims d;
-    long long count;         // of chunks and groups
+    unsigned count;          // of chunks and groups
     int gates_bf16;
 };
 
-// Products of a row's 16-byte pieces of two tiles, summed.
-__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
-    float x[8], y[8], s = 0.0f;
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return a + b;
+}
+// Products of a row's 16-byte pieces of two tiles, added to `s`.
+__device__ __forceinline__ f2 dot8(uint4 a, uint4 b, f2 s) {
+    f2 x[4], y[4];
     unpack8_f16(a, x);
     unpack8_f16(b, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+    for (int e = 0; e < 4; ++e) s = fma2(x[e], y[e], s);
     return s;
 }
 
 // CTAs walk the chunks and groups of heads; a warp brings in what comes next.  Rows of
 // products are lanes: steps as k rows (0 to 63) and as q rows (64 to 127).
+//
+// The gates' gradients need no sums over D's rows and columns: scaling k_i as it reads by
+// e^{G_i}, as it writes by e^{-G_i} and q_i by e^{G_i} is what G does, so with dk split into
+// what comes from reading (dKK K - e F_k) and from writing (dKK^T K + dQK^T Q + w F2)
+//   dG_i = q_i . dq_i + k_i . dk_read,i - k_i . dk_write,i
+// where the parts of w F2 also belong to the chunk's end: they count before step t instead
+// of from it on.
 template <int DK, typename TG>
 __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = GradSmem<DK>;
-    constexpr int CW = DK / 2;  // columns of dstate a thread holds
-    // tensor memory: F, F2; [dA'; dP'], [K; Q] K^T and U until W is made, then W K and W^T [K; Q]
-    constexpr uint32_t kTmF = 0, kTmF2 = 128, kTmA = 256, kTmX = 320, kTmU = 384, kTmW = 384,
-                       kTmV = 256, kTmCols = 512;
+    constexpr int CP = DK / 4;  // pairs of columns of dstate a thread holds
+    // tensor memory: F, F2; [dA'; dP'] and U until W is made, then W K and W^T [K; Q]
+    constexpr uint32_t kTmF = 0, kTmF2 = 128, kTmA = 256, kTmU = 384, kTmW = 384, kTmV = 256,
+                       kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
-    float* s_row = reinterpret_cast<float*>(smem + M::sums);  // [128][2]
-    float* s_col = s_row + 256;                               // [4][64]
-    float* s_dec = s_col + 256;                               // [64][2]
-    float* s_db = s_dec + 128;                                // [64][2]
+    float* s_dot = reinterpret_cast<float*>(smem + M::sums);  // [128][2]: from step t on
+    float* s_end = s_dot + 256;                               // [64][2]: before step t
+    float* s_db = s_end + 128;                                // [64][2]
     float* s_c = s_db + 128;                                  // [8]
     float* s_most = s_c + 8;                                  // [8]
     float* s_scan = s_most + 8;                               // [2]
@@ -466,11 +485,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     uint64_t* bar_f = full + 9;
     uint64_t* bar_w = full + 10;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 11);
-    float* factors = reinterpret_cast<float*>(smem + M::factors);  // [2][8]: R, S0, dR, dY, L
+    float* factors = reinterpret_cast<float*>(smem + M::factors);  // R, S0, -, -, dR, dY, L
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nc = a.d.chunks, ratio = a.d.heads / a.d.groups, pans = a.d.pans;
-    const int steps = ratio * pans;  // of an item (a chunk and a group)
+    const unsigned nc = a.d.chunks, groups = a.d.groups;
+    const int ratio = a.d.heads / a.d.groups, pans = a.d.pans;
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
@@ -486,30 +505,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
         if (lane == 0) {
             int n = 0, hn = 0;  // columns and heads loaded
             bool ok = true;
-            for (long long item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
-                const long long bg = item / nc;
-                const long long head0 = (bg / a.d.groups) * a.d.heads + (bg % a.d.groups) * ratio;
+            for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+                const unsigned bg = item / nc, c = item - bg * nc;
+                const unsigned b = bg / groups, head0 = b * a.d.heads + (bg - b * groups) * ratio;
                 for (int hh = 0; hh < ratio && ok; ++hh, ++hn) {
-                    const long long ch = (head0 + hh) * nc + item % nc;
+                    const size_t ch = (size_t)(head0 + hh) * nc + c;
                     if (hn >= 2) ok = mbar_wait(empty_h + (hn & 1), ((hn >> 1) - 1) & 1, a.status);
                     if (!ok) break;
                     uint8_t* hd = smem + (hn & 1) * M::head;
+                    uint64_t* bh = full_h + (hn & 1);
                     const uint8_t* rec = a.records + ch * rec_bytes(DK);
-                    mbar_arrive_expect_tx(full_h + (hn & 1), M::head);
-                    bulk_load(hd, rec, kGateBytes + kq_bytes(DK), full_h + (hn & 1));
-                    bulk_load(hd + M::t, rec + rec_t(DK), kTile, full_h + (hn & 1));
+                    const uint8_t* kept0 = a.kept + ch * pans * kept_bytes(DK);
+                    const uint8_t* adj0 = a.adjoint + ch * pans * adjoint_bytes(DK);
+                    mbar_arrive_expect_tx(bh, M::head + 32 * pans);
+                    bulk_load(hd, rec, kGateBytes + kq_bytes(DK), bh);
+                    bulk_load(hd + M::t, rec + rec_t(DK), kTile, bh);
+                    for (int p = 0; p < pans; ++p) {
+                        float* f = factors + 8 * (kMaxPans * (hn & 1) + p);
+                        bulk_load(f, kept0 + p * kept_bytes(DK) + kTile + h_bytes(DK), 16, bh);
+                        bulk_load(f + 4, adj0 + p * adjoint_bytes(DK) + 2 * kTile + h_bytes(DK), 16, bh);
+                    }
                     for (int p = 0; p < pans; ++p, ++n) {
                         if (n >= 2) ok = mbar_wait(empty + (n & 1), ((n >> 1) - 1) & 1, a.status);
                         if (!ok) break;
                         uint8_t* st = smem + M::stages + (n & 1) * M::stage;
                         uint64_t* bar = full + (n & 1);
-                        const uint8_t* kept = a.kept + (ch * pans + p) * kept_bytes(DK);
-                        const uint8_t* adj = a.adjoint + (ch * pans + p) * adjoint_bytes(DK);
-                        mbar_arrive_expect_tx(bar, M::stage + 32);
-                        bulk_load(st + M::r, kept, kTile + h_bytes(DK), bar);
-                        bulk_load(st + M::rdo, adj, 2 * kTile + h_bytes(DK), bar);
-                        bulk_load(factors + 8 * (n & 1), kept + kTile + h_bytes(DK), 16, bar);
-                        bulk_load(factors + 8 * (n & 1) + 4, adj + 2 * kTile + h_bytes(DK), 16, bar);
+                        mbar_arrive_expect_tx(bar, M::stage);
+                        bulk_load(st + M::r, kept0 + p * kept_bytes(DK), kTile + h_bytes(DK), bar);
+                        bulk_load(st + M::rdo, adj0 + p * adjoint_bytes(DK), 2 * kTile + h_bytes(DK), bar);
                     }
                 }
             }
@@ -522,210 +545,181 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool is_q = row >= kC;
-        const int i = row & 63;
+        const int i = row & 63, col0 = (DK / 2) * part;  // first column of dstate
         int n = 0, hn = 0;
         bool ok = true;
-        for (long long item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
-            const int c = (int)(item % nc), t0 = c * kC;
-            const long long bg = item / nc;
-            const int b = (int)(bg / a.d.groups), group = (int)(bg % a.d.groups);
-            float acc[CW];  // of dK (rows 0 to 63) or dQ
+        for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+            const unsigned bg = item / nc;
+            const int c = (int)(item - bg * nc), t0 = c * kC;
+            const int b = (int)(bg / groups), group = (int)(bg - b * groups);
+            f2 acc[CP];  // of dK (rows 0 to 63) or dQ, summed over heads
 #pragma unroll
-            for (int e = 0; e < CW; ++e) acc[e] = 0.0f;
-            float own[32];  // of [dA'; dP']
-            float beta_sum = 0.0f, ls = 0.0f, into = 0.0f, outof = 0.0f;
-            float er = 0.0f, wr = 0.0f, skq = 0.0f, s_t = 0.0f;
-            for (int step = 0; step < steps; ++step, ++n) {
-                const int p = step % pans;
-                const uint32_t st = sb + M::stages + (n & 1) * M::stage;
-                const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
+            for (int e = 0; e < CP; ++e) acc[e] = 0;
+            for (int hh = 0; hh < ratio; ++hh, ++hn) {
                 const uint32_t hd = sb + (hn & 1) * M::head;
                 const uint8_t* hg = smem + (hn & 1) * M::head;
                 const Gates* gates = reinterpret_cast<const Gates*>(hg);
-                const float* fac = factors + 8 * (n & 1);
-                // ---- U = T' R, and with a head's first columns [K; Q] K^T
-                if (tid == 0) {
-                    bool in = true;
-                    if (p == 0) in = mbar_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
-                    in = mbar_wait(full + (n & 1), (n >> 1) & 1, a.status) && in;
-                    tc_fence_after();
-                    if (in) {
+                const float* fac = factors + 8 * kMaxPans * (hn & 1);
+                const int h = group * ratio + hh;
+                bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
+                const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
+                const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
+                const float skq = gates->s_kq;
+                // a step's row of K or Q, columns col0 + 16 n .. + 15
+                auto own_row = [&](int n16, f2* v) {
+                    const int c0 = col0 + 16 * n16;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        unpack8_f16(*reinterpret_cast<const uint4*>(
+                                        hg + M::kq + (c0 >> 6) * 2 * kTile + piece(row, ((c0 & 63) >> 3) + q)),
+                                    v + 4 * q);
+                };
+                // Products of U and L are summed over the panels where they are: U's factor is
+                // chosen so that all have the same, the largest of theirs.  A panel's own: U is at
+                // most 64 products of 2^13 and 2^15, brought down to 2^15
+                constexpr float kDown = 1.0f / 524288.0f;
+                float s_ul = 0.0f;
+                for (int p = 0; p < pans; ++p) s_ul = fmaxf(s_ul, fac[8 * p] * fac[8 * p + 6]);
+                // what the other heads have left in the sums does not belong to this one's dot
+                float before = 0.0f;
+                if (hh > 0) {
+                    f2 d = 0;
+#pragma unroll
+                    for (int n16 = 0; n16 < CP / 8; ++n16) {
+                        f2 v[8];
+                        own_row(n16, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d = fma2(v[e], acc[8 * n16 + e], d);
+                    }
+                    before = sum2(d);
+                }
+                f2 own[16];  // of [dA'; dP']
+#pragma unroll
+                for (int e = 0; e < 16; ++e) own[e] = 0;
+                float beta_sum = 0.0f, ls = 0.0f;
+                for (int p = 0; p < pans; ++p, ++n) {
+                    const uint32_t st = sb + M::stages + (n & 1) * M::stage;
+                    const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
+                    const float s_r = fac[8 * p], s_s = fac[8 * p + 1], s_dr = fac[8 * p + 4],
+                                s_dy = fac[8 * p + 5], s_l = fac[8 * p + 6];
+                    // ---- U = T' R
+                    if (tid == 0 && mbar_poll(full + (n & 1), (n >> 1) & 1, a.status)) {
+                        tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_f16(tmem + kTmU, kdesc<128>(hd + M::t, kk), mdesc(st + M::r, kk, kTile),
                                     idesc_f16(128, 64) | kIdescBMN, kk > 0);
                         mma_commit(bar_u);
-                        if (p == 0)
-#pragma unroll
-                            for (int kk = 0; kk < DK / 16; ++kk)
-                                mma_f16(tmem + kTmX, kdesc<128>(hd + M::kq, kk), kdesc<128>(hd + M::kq, kk),
-                                        idesc_f16(128, 64), kk > 0);
                     }
-                }
-                bool here = true;
-                if (p == 0) here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
-                here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
-                const float s_r = fac[0], s_s = fac[1], s_dr = fac[4], s_dy = fac[5], s_l = fac[6];
-                if (p == 0) {  // a head begins
-                    er = ex2_approx(gates->hi[i] + gates->lo[i]);
-                    wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
-                    skq = gates->s_kq;
-                    s_t = gates->s_t;
-                    beta_sum = ls = into = outof = 0.0f;
+                    here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
+                    // sums over these columns: dR . R, and L . S0
+                    {
+                        f2 dr = 0, dl = 0;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) own[e] = 0.0f;
-                }
-                // sums over these columns: dR . R, and L . S0
-                {
-                    float dr = 0.0f, dl = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t off4 = piece(row, 4 * part + q);
-                        if (!is_q)
-                            dr += dot8(*reinterpret_cast<const uint4*>(sg + M::rdo + off4),
-                                       *reinterpret_cast<const uint4*>(sg + M::r + off4));
-                        if (row < DK)
-                            dl += dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + off4),
-                                       *reinterpret_cast<const uint4*>(sg + M::l + off4));
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t at = piece(row, 4 * part + q);
+                            if (!is_q)
+                                dr = dot8(*reinterpret_cast<const uint4*>(sg + M::rdo + at),
+                                          *reinterpret_cast<const uint4*>(sg + M::r + at), dr);
+                            if (row < DK)
+                                dl = dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + at),
+                                          *reinterpret_cast<const uint4*>(sg + M::l + at), dl);
+                        }
+                        beta_sum = fmaf(s_dr * s_r, sum2(dr), beta_sum);
+                        ls = fmaf(s_s * s_l, sum2(dl), ls);
                     }
-                    beta_sum = fmaf(s_dr * s_r, dr, beta_sum);
-                    ls = fmaf(s_s * s_l, dl, ls);
-                }
-                here = warp_wait(bar_u, n & 1, a.status) && here;
-                tc_fence_after();
-                // U's factor: at most 64 products of 2^13 and 2^15, down to 2^15
-                constexpr float kDown = 1.0f / 524288.0f;
-                const float s_u = s_t * s_r / kDown;
-                if (here && !is_q) {
-                    float x[32];
-                    uint32_t hw[16];
-                    tmem_ld32(t_lane + kTmU + 32 * part, x);
-                    tmem_wait_ld();
-                    round_to<32>(x, kDown, hw);
-                    put32(smem + M::u, i, 4 * part, hw);
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                ok = named_bar_and(1, 256, here);
-                if (!ok) break;
-                if (tid == 0) {
+                    here = warp_wait(bar_u, n & 1, a.status) && here;
                     tc_fence_after();
-                    constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk, kk > 0);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
-                    mma_commit(bar_f);
-                }
-                here = warp_wait(bar_f, n & 1, a.status);
-                tc_fence_after();
-                if (here) {  // the state's parts, and these columns' part of [dA'; dP']
-                    const float f1 = (is_q ? s_dy : s_dr) * s_s, f2_ = s_u * s_l;
-                    const float fa = (is_q ? s_dy : -s_dr) * s_u;
-                    const float g1 = is_q ? er * f1 : -er * f1, g2 = wr * f2_;
-                    float in1 = 0.0f, out1 = 0.0f;
-#pragma unroll
-                    for (int b8 = 0; b8 < CW; b8 += 16) {
-                        const int c0 = CW * part + b8;
-                        float f[16], x[16];
-                        tmem_ld16(t_lane + kTmF + c0, f);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            unpack8_f16(*reinterpret_cast<const uint4*>(
-                                            hg + M::kq + (c0 >> 6) * 2 * kTile +
-                                            piece(row, ((c0 & 63) >> 3) + q)), x + 8 * q);
+                    const float s_u = s_ul / s_l * gates->s_t / kDown;
+                    if (here && !is_q) {
+                        f2 x[16];
+                        uint32_t hw[16];
+                        tmem_ld32(t_lane + kTmU + 32 * part, x);
                         tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            in1 = fmaf(x[e], f[e], in1);
-                            acc[b8 + e] = fmaf(g1, f[e], acc[b8 + e]);
-                        }
-                        if (!is_q) {
-                            tmem_ld16(t_lane + kTmF2 + c0, f);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                out1 = fmaf(x[e], f[e], out1);
-                                acc[b8 + e] = fmaf(g2, f[e], acc[b8 + e]);
-                            }
-                        }
+                        scaled<16>(x, kDown * (s_r * s_l / s_ul), x);
+                        round_to<16>(x, hw);
+                        put32(smem + M::u, i, 4 * part, hw);
                     }
-                    into = fmaf(g1 * skq, in1, into);
-                    outof = fmaf(g2 * skq, out1, outof);
-                    float x[32];
-                    tmem_ld32(t_lane + kTmA + 32 * part, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) own[e] = fmaf(fa, x[e], own[e]);
-                }
-                tc_fence_before();
-                if (p + 1 < pans) {
+                    fence_proxy_async_smem();
+                    tc_fence_before();
                     ok = named_bar_and(1, 256, here);
                     if (!ok) break;
-                    if (tid == 0) mbar_arrive(empty + (n & 1));
-                    continue;
+                    if (tid == 0) {
+                        tc_fence_after();
+                        constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
+                                    p > 0 || kk > 0);
+                        mma_commit(bar_f);
+                    }
+                    here = warp_wait(bar_f, n & 1, a.status);
+                    tc_fence_after();
+                    if (here) {
+                        const float f1 = (is_q ? er * s_dy : -er * s_dr) * s_s, fa = (is_q ? s_dy : -s_dr) * s_u;
+                        const f2 f1p = pair(f1, f1), fap = pair(fa, fa);
+#pragma unroll
+                        for (int e0 = 0; e0 < CP; e0 += 16) {
+                            f2 f[16];
+                            tmem_ld32(t_lane + kTmF + col0 + 2 * e0, f);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) acc[e0 + e] = fma2(f1p, f[e], acc[e0 + e]);
+                        }
+                        f2 x[16];
+                        tmem_ld32(t_lane + kTmA + 32 * part, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) own[e] = fma2(fap, x[e], own[e]);
+                    }
+                    tc_fence_before();
+                    ok = named_bar_and(1, 256, here);
+                    if (!ok) break;
+                    if (tid == 0) mbar_arrive(empty + (n & 1));  // these columns have been read
                 }
+                if (!ok) break;
 
-                // ---- the head's last columns are in: W = [dKK; dQK], and its sums with [KK; QK]
-                const int h = group * ratio + step / pans;
-                float rsum = 0.0f;
-                if (here) {
-                    const float hi = gates->hi[i], lo = gates->lo[i], kk2 = skq * skq;
+                // ---- W = [dKK; dQK]
+                {
+                    const float hi = gates->hi[i], lo = gates->lo[i];
                     const int last = is_q ? i : i - 1;
-                    float m[32];
-                    tmem_ld32(t_lane + kTmX + 32 * part, m);
-                    tmem_wait_ld();
+                    if (part == 1 && (quarter & 1) == 0) {  // rows to 31, columns from 32
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const int j = 32 * part + e;
-                        const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
-                        const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
-                        const float hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                        for (int e = 0; e < 16; ++e) own[e] = 0;
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const bool in = j + k <= last;
-                            own[e + k] = in ? own[e + k] * decay(hi, lo, hv[k], lv[k]) : 0.0f;
-                            m[e + k] = in ? kk2 * m[e + k] * own[e + k] : 0.0f;
-                            rsum += m[e + k];
+                        for (int e = 0; e < 16; e += 2) {
+                            const int j = 32 * part + 2 * e;
+                            const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
+                            const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
+                            const float d0 = j <= last ? decay(hi, lo, h4.x, l4.x) : 0.0f;
+                            const float d1 = j + 1 <= last ? decay(hi, lo, h4.y, l4.y) : 0.0f;
+                            const float d2 = j + 2 <= last ? decay(hi, lo, h4.z, l4.z) : 0.0f;
+                            const float d3 = j + 3 <= last ? decay(hi, lo, h4.w, l4.w) : 0.0f;
+                            own[e] = mul2(own[e], pair(d0, d1));
+                            own[e + 1] = mul2(own[e + 1], pair(d2, d3));
                         }
                     }
-                    // sums over the warp's 32 rows: lane l ends with column l
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-                        for (int k = 0; k < o; ++k) {
-                            const bool up = lane & o;
-                            const float send = up ? m[k] : m[k + o];
-                            m[k] = (up ? m[k + o] : m[k]) + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                    s_col[quarter * 64 + 32 * part + lane] = m[0];
-                }
-                const float most = warp_most<32>(own);
-                if (lane == 0) s_most[warp] = most;
-                tc_fence_before();
-                ok = named_bar_and(1, 256, here);
-                if (!ok) break;
-                if (tid == 0) mbar_arrive(empty + (n & 1));  // these columns have been read
-                float s_w;
-                const float w_scale = tile_scale(most_of<8>(s_most), kTop, s_w);
-                {
-                    uint32_t hw[16];
-                    round_to<32>(own, w_scale, hw);
-                    put32(smem + M::w, row, 4 * part, hw);
-                }
-                s_row[2 * row + part] = rsum + into;
-                if (!is_q) {
-                    s_dec[2 * i + part] = outof;
-                    s_db[2 * i + part] = beta_sum + rsum;
+                    const float most = warp_most<16>(own);
+                    if (lane == 0) s_most[warp] = most;
                 }
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
                 if (lane == 0) s_c[warp] = ls;
+                named_bar_sync(1, 256);
+                float s_w;
+                scaled<16>(own, tile_scale(most_of<8>(s_most), kTop, s_w), own);
+                {
+                    uint32_t hw[16];
+                    round_to<16>(own, hw);
+                    put32(smem + M::w, row, 4 * part, hw);
+                }
                 fence_proxy_async_smem();
                 named_bar_sync(1, 256);
                 if (tid == 0) {
@@ -743,13 +737,60 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                 idV, kk > 0);
                     mma_commit(bar_w);
                 }
+                here = warp_wait(bar_w, hn & 1, a.status);
+                tc_fence_after();
+                if (here) {
+                    const float f1 = s_w * skq, g2 = wr * s_ul * gates->s_t / kDown;
+                    const f2 f1p = pair(f1, f1), g2p = pair(g2, g2);
+                    f2 whole = 0, read = 0, end = 0, write = 0;  // dots with this row
+#pragma unroll
+                    for (int n16 = 0; n16 < CP / 8; ++n16) {
+                        f2 v[8], f[8];
+                        tmem_ld16(t_lane + kTmW + col0 + 16 * n16, f);
+                        own_row(n16, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            read = fma2(v[e], f[e], read);
+                            acc[8 * n16 + e] = fma2(f1p, f[e], acc[8 * n16 + e]);
+                        }
+                        if (!is_q) {
+                            tmem_ld16(t_lane + kTmV + col0 + 16 * n16, f);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                write = fma2(v[e], f[e], write);
+                                acc[8 * n16 + e] = fma2(f1p, f[e], acc[8 * n16 + e]);
+                            }
+                            tmem_ld16(t_lane + kTmF2 + col0 + 16 * n16, f);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                end = fma2(v[e], f[e], end);
+                                acc[8 * n16 + e] = fma2(g2p, f[e], acc[8 * n16 + e]);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) whole = fma2(v[e], acc[8 * n16 + e], whole);
+                    }
+                    const float own_dot = skq * (sum2(whole) - before);
+                    const float wk = skq * f1 * sum2(read), wv = skq * f1 * sum2(write),
+                                we = skq * g2 * sum2(end);
+                    s_dot[2 * row + part] = is_q ? own_dot : own_dot - 2.0f * wv - we;
+                    if (!is_q) {
+                        s_end[2 * i + part] = we;
+                        s_db[2 * i + part] = beta_sum + wk;
+                    }
+                }
+                tc_fence_before();
+                ok = named_bar_and(1, 256, here);
+                if (!ok) break;
                 // ---- the gates
                 if (tid < kC) {
                     const int t = t0 + i;
                     const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + h;
-                    float up = s_row[2 * i] + s_row[2 * i + 1] + s_row[128 + 2 * i] + s_row[129 + 2 * i];
-                    for (int q = 0; q < 4; ++q) up -= s_col[q * 64 + i];
-                    float down = s_dec[2 * i] + s_dec[2 * i + 1];
+                    float up = s_dot[2 * i] + s_dot[2 * i + 1] + s_dot[128 + 2 * i] + s_dot[129 + 2 * i];
+                    float down = s_end[2 * i] + s_end[2 * i + 1];
                     const float self = down;
                     // sums of `up` from here on, of `down` before here
 #pragma unroll
@@ -776,35 +817,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                  off ? 0.0f : (s_db[2 * i] + s_db[2 * i + 1]) / gate_at(a.beta, at, a.gates_bf16));
                     }
                 }
-                // ---- the products with W
-                here = warp_wait(bar_w, hn & 1, a.status);
-                tc_fence_after();
-                if (here) {
-                    const float f1 = s_w * skq;
-#pragma unroll
-                    for (int b8 = 0; b8 < CW; b8 += 16) {
-                        const int c0 = CW * part + b8;
-                        float f[16], f2_[16];
-                        tmem_ld16(t_lane + kTmW + c0, f);
-                        if (!is_q) tmem_ld16(t_lane + kTmV + c0, f2_);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            acc[b8 + e] = fmaf(f1, is_q ? f[e] : f[e] + f2_[e], acc[b8 + e]);
-                    }
-                }
-                tc_fence_before();
-                ok = named_bar_and(1, 256, here);  // sums and tensor memory are free for the next head
-                if (!ok) break;
+                named_bar_sync(1, 256);  // sums are free for the next head
                 if (tid == 0) mbar_arrive(empty_h + (hn & 1));
-                ++hn;
             }
             if (ok && t0 + i < a.d.seqlen) {
                 TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
-                          (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + CW * part;
+                          (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + col0;
 #pragma unroll
-                for (int e = 0; e < CW; e += 8)
-                    if (CW * part + e < a.d.dk) store8(out + e, acc + e);
+                for (int e = 0; e < CP; e += 4)
+                    if (col0 + 2 * e < a.d.dk) store8(out + 2 * e, acc + e);
             }
         }
     }
@@ -830,8 +851,8 @@ ssm_status_t run_backward(const ChainArgs& chain, GradArgs grads, cudaStream_t s
         return SSM_ERR_CUDA;
     chain_bwd_kernel<DK, TG><<<(unsigned)((long long)d.batch * d.heads * d.pans), kChainThreads,
                                ChainSmem<DK>::bytes, s>>>(chain);
-    grads.count = (long long)d.batch * d.groups * d.chunks;
-    grads_kernel<DK, TG><<<(unsigned)std::min<long long>(grads.count, sms), kGradThreads,
+    grads.count = (unsigned)((long long)d.batch * d.groups * d.chunks);
+    grads_kernel<DK, TG><<<std::min<unsigned>(grads.count, sms), kGradThreads,
                            GradSmem<DK>::bytes, s>>>(grads);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
