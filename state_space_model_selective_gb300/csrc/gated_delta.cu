@@ -161,42 +161,44 @@ struct RecArgs {
     int keep_t;       // T' is wanted (training)
 };
 
+template <int V> struct Vec;
+template <> struct Vec<1> { using T = float; };
+template <> struct Vec<2> { using T = float2; };
+template <> struct Vec<4> { using T = float4; };
+
 // Joins pairs of inverted blocks of N rows: of the lower left of [[X, 0], [L, Z]]^-1 =
 // -Z^-1 L X^-1, element (r, c .. c + V - 1) of the pair at (at, at).  In two steps, the
-// first product through `tmp` (rows of 36 floats; row `t` is this thread's).
+// first product through `tmp` (rows of 36 floats, from `t0` on).
 template <int N, int V>
 __device__ __forceinline__ void join_blocks(float* m, float* tmp, int at, int t0, int r, int c) {
+    using T = typename Vec<V>::T;
     const float* X = m + at * kPitch + at;
     const float* L = X + N * kPitch;
-    const float* Z = L + N;
-    float s[V];
+    // s = sum_j sign * left[r][j] right[j][c ..]
+    auto product = [&](const float* left, const float* right, int pitch, float sign) {
+        float s[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 0.0f;
+        for (int v = 0; v < V; ++v) s[v] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(L + r * kPitch + j);
-        const float lv[4] = {l.x, l.y, l.z, l.w};
+        for (int j = 0; j < N; j += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(left + r * kPitch + j);
+            const float lv[4] = {sign * l.x, sign * l.y, sign * l.z, sign * l.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
+                const T x = *reinterpret_cast<const T*>(right + (j + e) * pitch + c);
+                const float* xv = reinterpret_cast<const float*>(&x);
 #pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = fmaf(lv[e], X[(j + e) * kPitch + c + v], s[v]);
-    }
+                for (int v = 0; v < V; ++v) s[v] = fmaf(lv[e], xv[v], s[v]);
+            }
+        }
+        T out;
 #pragma unroll
-    for (int v = 0; v < V; ++v) tmp[(t0 + r) * 36 + c + v] = s[v];
+        for (int v = 0; v < V; ++v) reinterpret_cast<float*>(&out)[v] = s[v];
+        return out;
+    };
+    *reinterpret_cast<T*>(tmp + (t0 + r) * 36 + c) = product(L, X, kPitch, 1.0f);
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        const float4 z = *reinterpret_cast<const float4*>(Z + r * kPitch + j);
-        const float zv[4] = {-z.x, -z.y, -z.z, -z.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = fmaf(zv[e], tmp[(t0 + j + e) * 36 + c + v], s[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[(at + N + r) * kPitch + at + c + v] = s[v];
+    *reinterpret_cast<T*>(m + (at + N + r) * kPitch + at + c) = product(L + N, tmp + t0 * 36, 36, -1.0f);
     __syncthreads();
 }
 
@@ -601,20 +603,25 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 constexpr int kChainThreads = 288;  // 8 warps on rows, one that loads and multiplies
 
-// PLO: P's lo part is multiplied too (y in fp32)
-template <int DK, bool PLO> struct ChainSmem {
-    // of a stage: the record up to P, then the tile of v (one box)
-    static constexpr uint32_t kq = rec_kq(DK);
-    static constexpr uint32_t h = rec_h(DK);
-    static constexpr uint32_t p = rec_p(DK);
-    static constexpr uint32_t rec = p + (PLO ? 2 : 1) * kTile;
-    static constexpr uint32_t v = rec;
-    static constexpr uint32_t stage = v + kTile;
-    static constexpr uint32_t s_hi = 2 * stage;                    // S0, rows of dstate
-    static constexpr uint32_t s_lo = s_hi + h_bytes(DK);
-    static constexpr uint32_t r_hi = s_lo + h_bytes(DK);           // R, rows of steps
-    static constexpr uint32_t r_lo = r_hi + kTile;
-    static constexpr uint32_t misc = r_lo + kTile;
+// PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
+// products are taken too (y in fp32).
+template <int DK, int PW, bool PLO> struct ChainSmem {
+    // a stage (two in turn): gates, panels of K (twice: 128 rows), v (64 columns), panels of Q,
+    // P hi (| lo)
+    static constexpr uint32_t k = kGateBytes;
+    static constexpr uint32_t v = k + kq_bytes(DK);
+    static constexpr uint32_t q = v + kTile;
+    static constexpr uint32_t p = q + kq_bytes(DK) / 2;
+    static constexpr uint32_t p_bytes = (PLO ? 2 : 1) * kTile;
+    static constexpr uint32_t stage = p + p_bytes;
+    // one H hi | lo: the next comes in between its product and the next but one's
+    static constexpr uint32_t h = 2 * stage;
+    // S0, rows of dstate, and R, rows of steps: hi and lo tiles, or both in a tile's row
+    static constexpr uint32_t s = h + 2 * h_bytes(DK);
+    static constexpr uint32_t s_bytes = (PW / 32) * h_bytes(DK);
+    static constexpr uint32_t r = s + s_bytes;
+    static constexpr uint32_t r_bytes = (PW / 32) * kTile;
+    static constexpr uint32_t misc = r + r_bytes;
     static constexpr uint32_t bytes = misc + 512;
 };
 
@@ -625,39 +632,43 @@ struct ChainArgs {
     float* last;
     void* y;
     uint32_t* status;
-    Dims d;
+    Dims d;       // pans: panels of PW columns
 };
 
-// One head and 64 columns of headdim, chunk after chunk.  Rows of products are lanes of
-// tensor memory: of K S0 and Q S0 the steps (0 to 63 and 64 to 127), of H R the state's
-// rows, of P R the steps (64 to 127).  Two warpgroups take 32 columns each.  The state stays
-// in registers (a row of dstate to a lane) and goes through shared memory as hi + lo each
-// chunk, as R does.  Right operands are [hi | lo] side by side, 128 columns to an
-// instruction: it reads 4 KB of A either way, and at 64 columns that reading bounds it (55
-// cycles an instruction against 64 for twice the columns).
+// One head and PW columns of headdim, chunk after chunk.  Rows of products are lanes of
+// tensor memory: of K S0 the steps, twice over, so that all eight warps share the work on R (a
+// warp only reaches its quarter of the lanes); of H R the state's rows; of Q S0 and P R the
+// steps in lanes 64 to 127.  The state stays in registers (a row of dstate to a lane, half
+// the columns) and goes through shared memory as hi + lo each chunk, as R does.  Right
+// operands are [hi | lo] side by side, 2 PW columns to an instruction: at 64 columns an
+// instruction is bound by reading its 4 KB of A (55 cycles against 64 for twice the columns).
 //
 // The factors of S and R have to be known before they are written, and a reduction over
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
 // |S1| <= e_63 |S| + |H|_1 |R|, with the measured maxima of V and S, found while products
 // run.  A bound 2^20 too large would still leave 20 bits.
-template <int DK, typename TO>
+template <int DK, int PW, typename TO>
 __global__ void __launch_bounds__(kChainThreads, 1)
     chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr bool PLO = sizeof(TO) == 4;
-    using M = ChainSmem<DK, PLO>;
-    // tensor memory, hi and lo columns each: [K; Q] S0, H R, P R
-    constexpr uint32_t kTmX = 0, kTmH = 128, kTmY = 256, kTmCols = 512;
+    using M = ChainSmem<DK, PW, PLO>;
+    constexpr int NP = DK / 64;
+    constexpr int SC = PW / 2, RC = PW / 4;  // columns of S and of R to a thread
+    // tensor memory, hi and lo columns each: K S0, H R, Q S0, P R
+    constexpr uint32_t kTmX = 0, kTmH = 128, kTmQ = 256, kTmY = 384, kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // a stage has come in
-    uint64_t* bar_x = full + 2;   // [K; Q] S0 done
-    uint64_t* bar_h = full + 3;   // H R done
-    uint64_t* bar_y = full + 4;   // P R done: the stage and R are free
-    uint64_t* bar_s = full + 5;   // S0 is in shared memory
-    uint64_t* bar_r = full + 6;   // R is
-    uint64_t* bar_o = full + 7;   // P R has been read
-    uint64_t* bar_m = full + 8;   // the largest values of S0 and V are known
-    float* s_most = reinterpret_cast<float*>(full + 9);  // [2 chunks][8 warps of S, 4 of V]
+    uint64_t* full_h = full + 2;  // H has
+    uint64_t* bar_x = full + 3;   // K S0 done
+    uint64_t* bar_h = full + 4;   // H R done
+    uint64_t* bar_y = full + 5;   // Q S0 and P R done: the stage and R are free
+    uint64_t* bar_s = full + 6;   // S0 is in shared memory
+    uint64_t* bar_r = full + 7;   // R is
+    uint64_t* bar_o = full + 8;   // Q S0 and P R have been read
+    uint64_t* bar_m = full + 9;   // the largest values of S0 are known
+    uint64_t* bar_v = full + 10;  // and those of V
+    float* s_most = reinterpret_cast<float*>(full + 11);  // [2 chunks][8 warps of S, 4 of V]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -668,11 +679,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int n = 0; n < 5; ++n) mbar_init(full + n, 1);
+        for (int n = 0; n < 6; ++n) mbar_init(full + n, 1);
         mbar_init(bar_s, 8);
-        mbar_init(bar_r, 4);
+        mbar_init(bar_r, 8);
         mbar_init(bar_o, 4);
         mbar_init(bar_m, 8);
+        mbar_init(bar_v, 4);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -683,115 +695,143 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     if (warp == 8) {
         if (lane == 0) {
             const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
-            int loads = 0;
+            int loads = 0, h_loads = 0;
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
-                mbar_arrive_expect_tx(full + (c & 1), M::stage);
-                bulk_load(st, rec0 + (long long)c * rec_bytes(DK), M::rec, full + (c & 1));
-                tma_load_4d(st + M::v, &tm_v, full + (c & 1), pan * kPan, h, c * kC, b);
+                uint64_t* bar = full + (c & 1);
+                const uint8_t* rec = rec0 + (long long)c * rec_bytes(DK);
+                mbar_arrive_expect_tx(bar, M::stage);
+                bulk_load(st, rec, kGateBytes, bar);
+                for (int p = 0; p < NP; ++p) {
+                    const uint8_t* kq = rec + rec_kq(DK) + p * 2 * kTile;
+                    bulk_load(st + M::k + p * 2 * kTile, kq, kTile, bar);
+                    bulk_load(st + M::k + p * 2 * kTile + kTile, kq, kTile, bar);
+                    bulk_load(st + M::q + p * kTile, kq + kTile, kTile, bar);
+                }
+                tma_load_4d(st + M::v, &tm_v, bar, pan * PW, h, c * kC, b);
+                bulk_load(st + M::p, rec + rec_p(DK), M::p_bytes, bar);
                 ++loads;
             };
+            auto load_h = [&](int c) {
+                mbar_arrive_expect_tx(full_h, 2 * h_bytes(DK));
+                bulk_load(smem + M::h, rec0 + (long long)c * rec_bytes(DK) + rec_h(DK), 2 * h_bytes(DK), full_h);
+                ++h_loads;
+            };
             load(0);
+            load_h(0);
             if (nc > 1) load(1);
-            constexpr uint32_t id = idesc_f16(128, 128) | kIdescBMN;
-            constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescBMN;
-            int waited = 0;
+            // right operands: S0 and R with both parts, or the first of two tiles alone
+            constexpr uint32_t id2 = idesc_f16(128, 2 * PW) | kIdescBMN;
+            constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
+            constexpr uint32_t idy = PLO ? id2 : id1;
+            int waited = 0, h_waited = 0;
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
                 if (!mbar_wait(full + (c & 1), (c >> 1) & 1, a.status)) break;
                 ++waited;
-                if (!mbar_wait(bar_s, ph, a.status)) break;
+                if (!mbar_poll(bar_s, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmX, kdesc<128>(st + M::kq, kk), mdesc(sb + M::s_hi, kk, h_bytes(DK)),
-                            id, kk > 0);
+                    mma_f16(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                            id2, kk > 0);
                 mma_commit(bar_x);
-                if (!mbar_wait(bar_r, ph, a.status)) break;
+                if (c > 0 && !mbar_poll(bar_o, ph ^ 1, a.status)) break;
                 tc_fence_after();
-                const uint32_t hh = st + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
+                // Q in rows 64 to 127: its tiles of 128 rows start one tile early
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                            idy, kk > 0);
+                if (!mbar_wait(full_h, ph, a.status)) break;
+                ++h_waited;
+                if (!mbar_poll(bar_r, ph, a.status)) break;
+                tc_fence_after();
+                const uint32_t hh = sb + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
                 // (of 64 rows of H the 64 behind them are not read)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
+                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r_hi, kk, kTile), id64, 1);
+                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
                 mma_commit(bar_h);
-                if (c > 0 && !mbar_wait(bar_o, ph ^ 1, a.status)) break;
-                tc_fence_after();
-                // P in rows 64 to 127: its tile of 128 rows starts one tile early
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r_hi, kk, kTile),
-                            PLO ? id : id64, kk > 0);
+                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), idy, kk > 0);
                 if constexpr (PLO)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r_hi, kk, kTile), id64, 1);
+                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
                 mma_commit(bar_y);
-                if (c + 2 < nc) {
-                    if (!mbar_wait(bar_y, ph, a.status)) break;
-                    load(c + 2);
+                if (c + 1 < nc) {
+                    if (!mbar_poll(bar_h, ph, a.status)) break;
+                    load_h(c + 1);
+                    if (!mbar_poll(bar_y, ph, a.status)) break;
+                    if (c + 2 < nc) load(c + 2);
                 }
             }
             // never leave with a load still landing
             for (; waited < loads; ++waited)
                 (void)mbar_wait(full + (waited & 1), (waited >> 1) & 1, a.status);
+            if (h_waited < h_loads) (void)mbar_wait(full_h, h_waited & 1, a.status);
         }
     } else {
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
-        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * part;
-        const int col0 = pan * kPan + 32 * part;      // first column of headdim
-        const bool on_k = row < kC;                   // of [K; Q] S0
-        const int i = row & 63;
-        f2 S[16];          // times its operand's factor; s_s undoes it
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const bool upper = row >= kC;                 // these rows write y
+        const int i = row & 63;                       // the row's step
+        const int col0 = pan * PW + SC * part;        // first column of S and y
+        const int rc = RC * (2 * part + (upper ? 1 : 0));  // first column of R, in the panel
+        // pieces of a row's hi and lo part
+        constexpr uint32_t lo_s = PW == 64 ? h_bytes(DK) : 0, lo_r = PW == 64 ? kTile : 0;
+        constexpr int lo_c = PW == 64 ? 0 : 4;
+        f2 S[SC / 2];      // times its operand's factor; s_s undoes it
         float s_s = 0.0f;
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float f_row = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        float f_k = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
         bool off = true;
+        // the gates of chunk c, and the largest values of its V (upper warps)
         auto gates_of = [&](int c) {
             const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
-            f_row = ex2_approx(g->hi[i] + g->lo[i]) * g->s_kq;
+            f_k = ex2_approx(g->hi[i] + g->lo[i]) * g->s_kq;
             e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
             off = g->masked >> i & 1;
             s_h = g->s_h;
             s_p = g->s_p;
             // of e |K|_1 over a row, in units of the largest S
             k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
-            return in;
-        };
-        // the largest values of S (all warps) and of V (the warps on Q rows), for the
-        // factors of chunk c
-        auto maxima = [&](int c) {
-            const float m = warp_most<16>(S) * s_s;
-            if (lane == 0) s_most[12 * (c & 1) + warp] = m;
-            if (!on_k) {
+            if (upper) {
                 float v = 0.0f;
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    v = fmaxf(v, most8_bf16(*reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p))));
+                for (int p = 0; p < SC / 8; ++p)
+                    v = fmaxf(v, most8_bf16(*reinterpret_cast<const uint4*>(
+                                     tile + piece(i, (SC / 8) * part + p))));
                 v = warp_most(off ? 0.0f : v);
                 if (lane == 0) s_most[12 * (c & 1) + 8 + (quarter & 1) * 2 + part] = v;
+                warp_arrive(bar_v);
             }
-            warp_arrive(bar_m);
+            return in;
         };
-        // S0 of chunk c as an operand, and kept
+        // S0 of chunk c as an operand, kept, and its largest values
         auto put_state = [&](int c) {
-            uint32_t hw[16], lw[16];
+            uint32_t hw[SC / 2], lw[SC / 2];
             if (row < DK) {
-                split<16>(S, hw, lw);
-                put32(smem + M::s_hi, row, 4 * part, hw);
-                put32(smem + M::s_lo, row, 4 * part, lw);
+                split<SC / 2>(S, hw, lw);
+                put_pieces<SC / 8>(smem + M::s, row, (SC / 8) * part, hw);
+                put_pieces<SC / 8>(smem + M::s + lo_s, row, (SC / 8) * part + lo_c, lw);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(bar_s);
-            if (a.kept) {
+            const float m = warp_most<SC / 2>(S) * s_s;
+            if (lane == 0) s_most[12 * (c & 1) + warp] = m;
+            warp_arrive(bar_m);
+            if (PW == 64 && a.kept) {
                 uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
-                if (row < DK) put32(k + kTile, row, 4 * part, hw);
+                if (row < DK) put_pieces<SC / 8>(k + kTile, row, (SC / 8) * part, hw);
                 if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK) + 4) = s_s;
             }
         };
@@ -801,24 +841,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const Gates* g = reinterpret_cast<const Gates*>(smem);
             const bool given = a.h0 && row < a.d.dk && ex2_approx(g->hi[0] + g->lo[0]) != 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < SC / 2; ++e) {
                 const float* at = a.h0 + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
                 // (columns come in eights)
                 const bool in = given && col0 + 2 * e < a.d.dv;
                 S[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
             }
-            const float m = warp_most<16>(S);
+            const float m = warp_most<SC / 2>(S);
             if (lane == 0) s_most[12 + warp] = m;
             named_bar_sync(1, 256);
-            scaled<16>(S, tile_scale(most_of<8>(s_most + 12), kBoundTop, s_s), S);
-            put_state(0);
+            scaled<SC / 2>(S, tile_scale(most_of<8>(s_most + 12), kBoundTop, s_s), S);
+            named_bar_sync(1, 256);
+            if (ok) put_state(0);
         }
-        if (ok) maxima(0);
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
-            const float fs = f_row * s_s, ee = e_end, sp = s_p, sh = s_h;
-            f2 x[16];
-            ok = warp_wait(bar_m, ph, a.status);
+            const float fs = f_k * s_s, ee = e_end, sp = s_p, sh = s_h;
+            ok = warp_wait(bar_m, ph, a.status) && warp_wait(bar_v, ph, a.status);
             if (!ok) break;
             const float s_max = most_of<8>(s_most + 12 * ph);
             const float r_bound = fmaf(k_bound, s_max, most_of<4>(s_most + 12 * ph + 8));
@@ -826,112 +865,100 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
             // |H|_1 over a row is at most 64 times its largest value
             const float next = tile_scale(fmaf(ee, s_max, kC * 2 * kTopValue * sh * r_bound), kBoundTop, s_next);
-            ok = warp_wait(bar_x, ph, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_ld32(t_lane + kTmX, x);
-            if (on_k) {
-                // (the products that read R before are done: bar_x follows them)
-                f2 y[16];
-                tmem_ld32(t_lane + kTmX + 64, y);
+            // ---- R, times its factor
+            {
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
-                uint4 v[4];
+                f2 v[RC / 2];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    v[p] = make_uint4(0, 0, 0, 0);
+                for (int p = 0; p < RC / 8; ++p) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
                     // a masked step's value is not looked at (its row of K is 0)
-                    if (!off) v[p] = *reinterpret_cast<const uint4*>(tile + piece(i, 4 * part + p));
+                    if (!off) w = *reinterpret_cast<const uint4*>(tile + piece(i, rc / 8 + p));
+                    unpack8_bf16(w, v + 4 * p);
                 }
-                const f2 f = pair(-fs * r_scale, -fs * r_scale), rs = pair(r_scale, r_scale);
+                scaled<RC / 2>(v, r_scale, v);
+                const f2 f = pair(-fs * r_scale, -fs * r_scale);
+                f2 x[RC / 2], y[RC / 2];
+                ok = warp_wait(bar_x, ph, a.status);
+                if (!ok) break;
+                tc_fence_after();
+                tmem_cols<RC>(t_lane + kTmX + rc, x);
+                tmem_cols<RC>(t_lane + kTmX + PW + rc, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    f2 w[4];
-                    unpack8_bf16(v[p], w);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[4 * p + e] = fma2(f, add2(x[4 * p + e], y[4 * p + e]), mul2(w[e], rs));
-                }
-                uint32_t hw[16], lw[16];
-                split<16>(x, hw, lw);
-                put32(smem + M::r_hi, i, 4 * part, hw);
-                put32(smem + M::r_lo, i, 4 * part, lw);
+                for (int e = 0; e < RC / 2; ++e) x[e] = fma2(f, add2(x[e], y[e]), v[e]);
+                // (the products that read R before are done: bar_x follows them)
+                uint32_t hw[RC / 2], lw[RC / 2];
+                split<RC / 2>(x, hw, lw);
+                put_pieces<RC / 8>(smem + M::r, i, rc / 8, hw);
+                put_pieces<RC / 8>(smem + M::r + lo_r, i, rc / 8 + lo_c, lw);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(bar_r);
-                if (a.kept) {
+                if (PW == 64 && a.kept) {
                     uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
-                    put32(k, i, 4 * part, hw);
+                    put_pieces<RC / 8>(k, i, rc / 8, hw);
                     if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK)) = s_r;
                 }
-            } else {
-                if constexpr (PLO) {
-                    f2 y[16];
-                    tmem_ld32(t_lane + kTmX + 64, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = add2(x[e], y[e]);
-                } else {
-                    tmem_wait_ld();
-                }
             }
-            const float decayed = ee * s_s * next, added = sh * s_r * next;
-            const f2 a2 = pair(added, added);
-            scaled<16>(S, decayed, S);
-            ok = warp_wait(bar_h, ph, a.status);
+            // ---- the state, times its next factor; the next chunk's gates meanwhile
+            scaled<SC / 2>(S, ee * s_s * next, S);
+            const float added = sh * s_r * next;
+            if (c + 1 < nc) ok = gates_of(c + 1);
+            ok = warp_wait(bar_h, ph, a.status) && ok;
             if (!ok) break;
             tc_fence_after();
             {
-                f2 z[16], y[16];
-                tmem_ld32(t_lane + kTmH, z);
-                tmem_ld32(t_lane + kTmH + 64, y);
+                f2 z[SC / 2], y[SC / 2];
+                tmem_cols<SC>(t_lane + kTmH + SC * part, z);
+                tmem_cols<SC>(t_lane + kTmH + PW + SC * part, y);
                 tmem_wait_ld();
+                const f2 a2 = pair(added, added);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) S[e] = fma2(a2, add2(z[e], y[e]), S[e]);
+                for (int e = 0; e < SC / 2; ++e) S[e] = fma2(a2, add2(z[e], y[e]), S[e]);
             }
             s_s = s_next;
-            if (c + 1 < nc) {
-                put_state(c + 1);
-                ok = gates_of(c + 1);
-                if (!ok) break;
-                maxima(c + 1);
+            if (c + 1 < nc) put_state(c + 1);
+            if (!upper) continue;
+            // ---- y
+            ok = warp_wait(bar_y, ph, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            f2 x[SC / 2], z[SC / 2];
+            tmem_cols<SC>(t_lane + kTmQ + SC * part, x);
+            tmem_cols<SC>(t_lane + kTmY + SC * part, z);
+            tmem_wait_ld();
+            if constexpr (PLO) {
+                f2 w[SC / 2];
+                tmem_cols<SC>(t_lane + kTmQ + PW + SC * part, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < SC / 2; ++e) x[e] = add2(x[e], w[e]);
+                tmem_cols<SC>(t_lane + kTmY + PW + SC * part, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < SC / 2; ++e) z[e] = add2(z[e], w[e]);
             }
-            if (!on_k) {
-                ok = warp_wait(bar_y, ph, a.status);
-                if (!ok) break;
-                tc_fence_after();
-                f2 z[16];
-                tmem_ld32(t_lane + kTmY, z);
-                if constexpr (PLO) {
-                    f2 y[16];
-                    tmem_ld32(t_lane + kTmY + 64, y);
-                    tmem_wait_ld();
+            tc_fence_before();
+            warp_arrive(bar_o);
+            const int t = c * kC + i;
+            if (a.y && t < a.d.seqlen) {
+                TO* y = static_cast<TO*>(a.y) +
+                        (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
+                const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) z[e] = add2(z[e], y[e]);
-                } else {
-                    tmem_wait_ld();
-                }
-                tc_fence_before();
-                warp_arrive(bar_o);
-                const int t = c * kC + i;
-                if (a.y && t < a.d.seqlen) {
-                    TO* y = static_cast<TO*>(a.y) +
-                            (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                    const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
+                for (int p = 0; p < SC / 8; ++p) {
+                    if (col0 + 8 * p >= a.d.dv) break;
+                    f2 o[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        if (col0 + 8 * p >= a.d.dv) break;
-                        f2 o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = fma2(q, x[4 * p + e], mul2(f, z[4 * p + e]));
-                        store8(y + 8 * p, o);
-                    }
+                    for (int e = 0; e < 4; ++e) o[e] = fma2(q, x[4 * p + e], mul2(f, z[4 * p + e]));
+                    store8(y + 8 * p, o);
                 }
             }
         }
         if (a.last && row < a.d.dk)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < SC / 2; ++e)
                 if (col0 + 2 * e < a.d.dv) {
                     float v0, v1;
                     unpair(S[e], v0, v1);
@@ -975,14 +1002,25 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;
     a.y = f.y; a.status = f.status; a.d = d;
-    const unsigned grid = (unsigned)((long long)f.batch * f.heads * d.pans);
-    auto go = [&](auto kernel, uint32_t bytes) {
-        if (!allow_smem(kernel, bytes)) return false;
-        kernel<<<grid, kChainThreads, bytes, s>>>(mv, a);
+    // Panels of 32 columns take 0.7 of the time of 64 a chunk, on twice the CTAs (one to an
+    // SM): for heads so few that these run at once where the wider ones would leave SMs idle
+    const long long bh = (long long)f.batch * f.heads;
+    const long long wide = bh * d.pans, narrow = bh * ((f.dv + 31) / 32);
+    const bool half = !f.kept && 7 * ((narrow + sms - 1) / sms) < 10 * ((wide + sms - 1) / sms);
+    if (half) a.d.pans = (f.dv + 31) / 32;
+    const unsigned grid = (unsigned)(half ? narrow : wide);
+    auto go = [&](auto pw, auto to) {
+        constexpr int PW = decltype(pw)::value;
+        using TO = decltype(to);
+        constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
+        if (!allow_smem(chain_kernel<DK, PW, TO>, bytes)) return false;
+        chain_kernel<DK, PW, TO><<<grid, kChainThreads, bytes, s>>>(mv, a);
         return true;
     };
-    if (!(f.out_dtype == SSM_F32 ? go(chain_kernel<DK, float>, ChainSmem<DK, true>::bytes)
-                                 : go(chain_kernel<DK, __nv_bfloat16>, ChainSmem<DK, false>::bytes)))
+    auto by_out = [&](auto pw) {
+        return f.out_dtype == SSM_F32 ? go(pw, float{}) : go(pw, __nv_bfloat16{});
+    };
+    if (!(half ? by_out(std::integral_constant<int, 32>{}) : by_out(std::integral_constant<int, 64>{})))
         return SSM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

@@ -135,7 +135,18 @@ __device__ __forceinline__ void scaled(const f2* x, float scale, f2* y) {
 #pragma unroll
     for (int e = 0; e < N; ++e) y[e] = mul2(x[e], s);
 }
-// 16 or 32 columns of this thread's lane of tensor memory, as pairs.
+// 8, 16 or 32 columns of this thread's lane of tensor memory, as pairs.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, f2* v) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, f2* v) {
     float x[32];
     ssm::tmem_ld32(taddr, x);
@@ -192,6 +203,21 @@ __device__ __forceinline__ float most_of(const float* s) {
 // Byte offset of 16-byte piece c of row r of a tile of 128-byte rows.
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+}
+// N columns, 8, 16 or 32.
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, f2* v) {
+    if constexpr (N == 8) tmem_ld8(taddr, v);
+    else if constexpr (N == 16) tmem_ld16(taddr, v);
+    else tmem_ld32(taddr, v);
+}
+// 8 N values (4 N packed pairs) as pieces c0 .. c0 + N - 1 of row r.
+template <int N>
+__device__ __forceinline__ void put_pieces(uint8_t* tile, int r, int c0, const uint32_t* w) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        *reinterpret_cast<uint4*>(tile + piece(r, c0 + c)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 // 32 values (16 packed pairs) as pieces c0 .. c0 + 3 of row r.
 __device__ __forceinline__ void put32(uint8_t* tile, int r, int c0, const uint32_t* w) {
@@ -282,9 +308,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// mbar_wait for what is due in a moment: looks without being put to sleep first (a woken
-// thread is some 200 cycles late, of the 2500 that a chunk takes).
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint32_t* status) {
+// Looks for what is due in a moment without being put to sleep first (a woken thread is
+// some 200 cycles late, of the 3000 that a chunk takes).
+__device__ __forceinline__ bool mbar_look(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
     for (int i = 0; i < 256; ++i) {
         uint32_t done;
@@ -297,11 +323,15 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint32
             : "memory");
         if (done) return true;
     }
-    return mbar_wait(bar, parity, status);
+    return false;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint32_t* status) {
+    return mbar_look(bar, parity) || mbar_wait(bar, parity, status);
 }
 // A wait that a whole warp takes together, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-    return __all_sync(0xffffffffu, mbar_poll(bar, parity, status));
+    if (__all_sync(0xffffffffu, mbar_look(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
 struct Dims {

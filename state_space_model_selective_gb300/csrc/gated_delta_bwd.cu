@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
                 if (!mbar_wait(full_p, ph, a.status)) break;
                 ++p_seen;
-                if (!mbar_wait(bar_o, ph, a.status)) break;
+                if (!mbar_poll(bar_o, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                             id64, kk > 0);
                 if (!mbar_wait(full + (it & 1), (it >> 1) & 1, a.status)) break;
                 ++kh_seen;
-                if (!mbar_wait(bar_s, ph, a.status)) break;
+                if (!mbar_poll(bar_s, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f16(tmem + kTmQ, mdesc(sb + M::q, kk, kTile), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
                 mma_commit(bar_q);
-                if (!mbar_wait(bar_r, ph, a.status)) break;
+                if (!mbar_poll(bar_r, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
