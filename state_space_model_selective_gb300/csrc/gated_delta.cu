@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 // ------------------------------------------------------------------ chain
 
-constexpr int kChainThreads = 288;  // 8 warps on rows, one that loads and multiplies
+constexpr int kChainThreads = kSplitThreads;  // 8 warps on rows, one that loads and multiplies
 
 // PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
 // products are taken too (y in fp32).
@@ -692,9 +692,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 8) {
-        if (lane == 0) {
+    if (warp >= 8) {
+        give_registers();
+        if (warp == 8 && lane == 0) {
             const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
+            auto kept_of = [&](int c) {
+                return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
+            };
             int loads = 0, h_loads = 0;
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
@@ -730,12 +734,17 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (!mbar_wait(full + (c & 1), (c >> 1) & 1, a.status)) break;
                 ++waited;
                 if (!mbar_poll(bar_s, ph, a.status)) break;
+                if (PW == 64 && a.kept) bulk_wait_read_all();  // R's when K S0 is
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
                     mma_f16(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
                             id2, kk > 0);
                 mma_commit(bar_x);
+                if (PW == 64 && a.kept) {  // S0's hi part is what training keeps
+                    bulk_store(kept_of(c) + kTile, smem + M::s, h_bytes(DK));
+                    bulk_commit();
+                }
                 if (c > 0 && !mbar_poll(bar_o, ph ^ 1, a.status)) break;
                 tc_fence_after();
                 // Q in rows 64 to 127: its tiles of 128 rows start one tile early
@@ -747,6 +756,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 ++h_waited;
                 if (!mbar_poll(bar_r, ph, a.status)) break;
                 tc_fence_after();
+                if (PW == 64 && a.kept) {
+                    bulk_wait_read_all();  // S0's place is written when H R is done
+                    bulk_store(kept_of(c), smem + M::r, kTile);
+                    bulk_commit();
+                }
                 const uint32_t hh = sb + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
                 // (of 64 rows of H the 64 behind them are not read)
 #pragma unroll
@@ -771,12 +785,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     if (c + 2 < nc) load(c + 2);
                 }
             }
+            bulk_wait_all();
             // never leave with a load still landing
             for (; waited < loads; ++waited)
                 (void)mbar_wait(full + (waited & 1), (waited >> 1) & 1, a.status);
             if (h_waited < h_loads) (void)mbar_wait(full_h, h_waited & 1, a.status);
         }
     } else {
+        take_registers();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool upper = row >= kC;                 // these rows write y
@@ -815,7 +831,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             }
             return in;
         };
-        // S0 of chunk c as an operand, kept, and its largest values
+        auto factors_of = [&](int c) {
+            return reinterpret_cast<float*>(a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK) +
+                                            kTile + h_bytes(DK));
+        };
+        // S0 of chunk c as an operand, and its largest values
         auto put_state = [&](int c) {
             uint32_t hw[SC / 2], lw[SC / 2];
             if (row < DK) {
@@ -829,11 +849,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const float m = warp_most<SC / 2>(S) * s_s;
             if (lane == 0) s_most[12 * (c & 1) + warp] = m;
             warp_arrive(bar_m);
-            if (PW == 64 && a.kept) {
-                uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
-                if (row < DK) put_pieces<SC / 8>(k + kTile, row, (SC / 8) * part, hw);
-                if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK) + 4) = s_s;
-            }
+            if (PW == 64 && a.kept && tid == 0) factors_of(c)[1] = s_s;
         };
         bool ok = gates_of(0);
         {   // the first chunk: its largest values are measured.  A state that the first step
@@ -895,11 +911,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(bar_r);
-                if (PW == 64 && a.kept) {
-                    uint8_t* k = a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
-                    put_pieces<RC / 8>(k, i, rc / 8, hw);
-                    if (tid == 0) *reinterpret_cast<float*>(k + kTile + h_bytes(DK)) = s_r;
-                }
+                if (PW == 64 && a.kept && tid == 0) factors_of(c)[0] = s_r;
             }
             // ---- the state, times its next factor; the next chunk's gates meanwhile
             scaled<SC / 2>(S, ee * s_s * next, S);
@@ -947,13 +959,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                         (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
                 const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
 #pragma unroll
-                for (int p = 0; p < SC / 8; ++p) {
-                    if (col0 + 8 * p >= a.d.dv) break;
-                    f2 o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = fma2(q, x[4 * p + e], mul2(f, z[4 * p + e]));
-                    store8(y + 8 * p, o);
-                }
+                for (int e = 0; e < SC / 2; ++e) x[e] = fma2(q, x[e], mul2(f, z[e]));
+                store_row<SC / 2>(y, x, col0, a.d.dv, a.d.dv % 16 == 0);
             }
         }
         if (a.last && row < a.d.dk)

@@ -247,6 +247,20 @@ __device__ __forceinline__ float most8_bf16(uint4 w) {
     for (int e = 0; e < 4; ++e) m = max(m, max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
     return __uint_as_float(m);
 }
+// 8 pairs to 16 consecutive elements whose address is a multiple of 32 bytes (a whole sector
+// of bf16 to a lane).
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const f2* o) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float a, b;
+        unpair(o[e], a, b);
+        w[e] = pack_bf16(a, b);
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 // 4 pairs to 8 consecutive elements.
 __device__ __forceinline__ void store8(float* p, const f2* o) {
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(o[0], o[1]);
@@ -261,6 +275,21 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const f2* o) {
         w[e] = pack_bf16(a, b);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// N pairs as the columns col .. of a row of `cols` whose column col lies at p (cols a multiple
+// of 8); `wide`: rows are multiples of 32 bytes.
+template <int N, typename T>
+__device__ __forceinline__ void store_row(T* p, const f2* o, int col, int cols, bool wide) {
+    if (sizeof(T) == 2 && wide && N % 8 == 0) {
+        if constexpr (sizeof(T) == 2 && N % 8 == 0)
+#pragma unroll
+            for (int e = 0; e < N; e += 8)
+                if (col + 2 * e < cols) store16(p + 2 * e, o + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            if (col + 2 * e < cols) store8(p + 2 * e, o + e);
+    }
 }
 __device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
@@ -333,6 +362,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
     if (__all_sync(0xffffffffu, mbar_look(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
+
+// Registers move from the warps that load and multiply to those that compute: a kernel of 12
+// warps has 168 a thread at launch, 64512 in all; then 8 warps have 224 and 4 have 56.
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+}
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+}
+constexpr int kSplitThreads = 384;
 
 struct Dims {
     int batch, seqlen, heads, groups, dk, dv;

@@ -26,7 +26,7 @@ __device__ __forceinline__ void put_gate(void* p, long long i, int bf16, float v
 }
 // ------------------------------------------------------------------ chain
 
-constexpr int kChainThreads = 288;
+constexpr int kChainThreads = kSplitThreads;
 
 template <int DK> struct ChainSmem {
     static constexpr uint32_t k_bytes = (DK / 64) * kTile;
@@ -43,7 +43,8 @@ template <int DK> struct ChainSmem {
     static constexpr uint32_t o_lo = o_hi + kTile;
     static constexpr uint32_t r_hi = o_lo + kTile;           // -e dR
     static constexpr uint32_t r_lo = r_hi + kTile;
-    static constexpr uint32_t xch = r_lo + kTile;            // 64 x 64 fp32, columns first
+    static constexpr uint32_t dr = r_lo + kTile;             // dR, on its way out
+    static constexpr uint32_t xch = dr + kTile;              // 64 x 64 fp32, columns first
     static constexpr uint32_t misc = xch + 64 * 64 * 4;
     static constexpr uint32_t bytes = misc + 512;
 };
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_o = full + 8;    // dY and e dY are
     uint64_t* bar_r = full + 9;    // -e dR is
     uint64_t* bar_m = full + 10;   // the largest values of L are known
-    float* s_most = reinterpret_cast<float*>(full + 11);  // [2 chunks][8 warps of L, 4 of dY]
+    uint64_t* bar_d = full + 11;   // dR is in shared memory
+    float* s_most = reinterpret_cast<float*>(full + 12);  // [2 chunks][8 warps of L, 4 of dY]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -100,6 +102,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         mbar_init(bar_o, 4);
         mbar_init(bar_r, 4);
         mbar_init(bar_m, 8);
+        mbar_init(bar_d, 4);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -107,8 +110,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 8) {
-        if (lane == 0) {
+    if (warp >= 8) {
+        give_registers();
+        if (warp == 8 && lane == 0) {
+            auto kept_of = [&](int it) {
+                return a.kept + ((bh * nc + nc - 1 - it) * a.d.pans + pan) * adjoint_bytes(DK);
+            };
             int kh_loads = 0, q_loads = 0, p_loads = 0;
             auto rec_of = [&](int it) { return rec0 + (long long)(nc - 1 - it) * rec_bytes(DK); };
             auto load_kh = [&](int it) {
@@ -142,6 +149,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescAMN | kIdescBMN;
             for (int it = 0; it < nc; ++it) {
                 const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
+                bulk_wait_read_all();  // dR's place is written again when H^T L is done
                 if (!mbar_wait(full_p, ph, a.status)) break;
                 ++p_seen;
                 if (!mbar_poll(bar_o, ph, a.status)) break;
@@ -159,6 +167,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     mma_f16(tmem + kTmX, mdesc(st + M::h, kk, h_bytes(DK)),
                             mdesc(sb + M::l_hi, kk, h_bytes(DK)), id, kk > 0);
                 mma_commit(bar_x);
+                // dY and L's hi part are kept as they are
+                bulk_store(kept_of(it) + kTile, smem + M::dy, kTile);
+                bulk_store(kept_of(it) + 2 * kTile, smem + M::l_hi, h_bytes(DK));
+                bulk_commit();
                 if (!mbar_wait(full_q, ph, a.status)) break;
                 ++q_seen;
                 tc_fence_after();
@@ -166,6 +178,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f16(tmem + kTmQ, mdesc(sb + M::q, kk, kTile), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
+                bulk_wait_read_all();  // dY's place is written when this is done, L's later
                 mma_commit(bar_q);
                 if (!mbar_poll(bar_r, ph, a.status)) break;
                 tc_fence_after();
@@ -173,6 +186,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f16(tmem + kTmK, mdesc(st + M::k, kk, kTile), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
                 mma_commit(bar_l);
+                if (!mbar_poll(bar_d, ph, a.status)) break;
+                bulk_store(kept_of(it), smem + M::dr, kTile);
+                bulk_commit();
                 if (it + 1 < nc) {
                     if (!mbar_wait(bar_q, ph, a.status)) break;  // (it follows bar_x)
                     load_p(it + 1);
@@ -181,6 +197,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     if (it + 2 < nc) load_kh(it + 2);
                 }
             }
+            bulk_wait_all();
             // never leave with a load still landing
             for (; kh_seen < kh_loads; ++kh_seen)
                 (void)mbar_wait(full + (kh_seen & 1), (kh_seen >> 1) & 1, a.status);
@@ -188,6 +205,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             if (p_seen < p_loads) (void)mbar_wait(full_p, p_seen & 1, a.status);
         }
     } else {
+        take_registers();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * part;
         const int col0 = pan * kPan + 32 * part;
@@ -203,8 +221,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const bool in = a.dlast && row < a.d.dk && col0 + 2 * e < a.d.dv;
             L[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
         }
-        auto kept_of = [&](int c) {
-            return a.kept + ((bh * nc + c) * a.d.pans + pan) * adjoint_bytes(DK);
+        auto factors_of = [&](int c) {
+            return reinterpret_cast<float*>(a.kept + ((bh * nc + c) * a.d.pans + pan) * adjoint_bytes(DK) +
+                                            2 * kTile + h_bytes(DK));
         };
         // what a chunk's rows take from its gates, read before the stage can be refilled
         float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_kq = 0.0f, s_h = 0.0f, s_p = 0.0f;
@@ -232,9 +251,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const float m = warp_most<16>(L) * s_l;
             if (lane == 0) s_most[12 * (it & 1) + warp] = m;
             warp_arrive(bar_m);
-            uint8_t* k = kept_of(nc - 1 - it);
-            if (row < DK) put32(k + 2 * kTile, row, 4 * part, hw);
-            if (tid == 0) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[2] = s_l;
+            if (tid == 0) factors_of(nc - 1 - it)[2] = s_l;
         };
         uint4 dy[4];
         auto fetch = [&](int c) {
@@ -266,9 +283,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             scaled<16>(x, tile_scale(all, kTop, s_dy), y);
             round_to<16>(y, hw);
             put32(smem + M::dy, i, 4 * part, hw);
-            uint8_t* k = kept_of(nc - 1 - it);
-            put32(k + kTile, i, 4 * part, hw);
-            if (tid == 64) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[1] = s_dy;
+            if (tid == 64) factors_of(nc - 1 - it)[1] = s_dy;
             scaled<16>(x, e * tile_scale(all * e_max, kBoundTop, s_o), x);
             split<16>(x, hw, lw);
             put32(smem + M::o_hi, i, 4 * part, hw);
@@ -339,19 +354,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 put32(smem + M::r_lo, i, 4 * part, lw);
                 fence_proxy_async_smem();
                 warp_arrive(bar_r);
+                scaled<16>(x, r_scale, y);
+                round_to<16>(y, hw);
+                put32(smem + M::dr, i, 4 * part, hw);
+                fence_proxy_async_smem();
+                warp_arrive(bar_d);
+                if (tid == 0) factors_of(c)[0] = s_r;
                 const int t = c * kC + i;
                 if (t < a.d.seqlen) {
                     TG* dv = static_cast<TG*>(a.dv) +
                              (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        if (col0 + 8 * p < a.d.dv) store8(dv + 8 * p, x + 4 * p);
+                    store_row<16>(dv, x, col0, a.d.dv, a.d.dv % 16 == 0);
                 }
-                scaled<16>(x, r_scale, x);
-                round_to<16>(x, hw);
-                uint8_t* k = kept_of(c);
-                put32(k, i, 4 * part, hw);
-                if (tid == 0) reinterpret_cast<float*>(k + 2 * kTile + h_bytes(DK))[0] = s_r;
             }
             // ---- L0 = e_63 L + Q^T e dY - K^T e dR
             scaled<16>(L, ee * s_l * next, L);
@@ -401,7 +415,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
 // ------------------------------------------------------------------ grads
 
-constexpr int kGradThreads = 288;  // 8 warps on rows, one that loads
+constexpr int kGradThreads = kSplitThreads;  // 8 warps on rows, one that loads
 constexpr int kMaxPans = 4;
 
 template <int DK> struct GradSmem {
@@ -501,8 +515,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 8) {
-        if (lane == 0) {
+    if (warp >= 8) {
+        give_registers();
+        if (warp == 8 && lane == 0) {
             int n = 0, hn = 0;  // columns and heads loaded
             bool ok = true;
             for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
@@ -542,6 +557,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 (void)mbar_wait(full_h + (k & 1), (k >> 1) & 1, a.status);
         }
     } else {
+        take_registers();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool is_q = row >= kC;
@@ -823,9 +839,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             if (ok && t0 + i < a.d.seqlen) {
                 TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
                           (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + col0;
-#pragma unroll
-                for (int e = 0; e < CP; e += 4)
-                    if (col0 + 2 * e < a.d.dk) store8(out + 2 * e, acc + e);
+                store_row<CP>(out, acc, col0, a.d.dk, a.d.dk % 16 == 0);
             }
         }
     }
