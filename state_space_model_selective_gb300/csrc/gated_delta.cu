@@ -601,7 +601,9 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 // ------------------------------------------------------------------ chain
 
-constexpr int kChainThreads = kSplitThreads;  // 8 warps on rows, one that loads and multiplies
+// 8 warps on rows, one that multiplies and one that loads (a copy takes its issuer some 100
+// cycles, and a chunk has a dozen), two idle
+constexpr int kChainThreads = kSplitThreads;
 
 // PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
 // products are taken too (y in fp32).
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int n = 0; n < 6; ++n) mbar_init(full + n, 1);
+        for (int n = 0; n < 6; ++n) mbar_init(full + n, n == 2 ? 2 : 1);
         mbar_init(bar_s, 8);
         mbar_init(bar_r, 8);
         mbar_init(bar_o, 4);
@@ -695,10 +697,64 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     if (warp >= 8) {
         give_registers();
         if (warp == 8 && lane == 0) {
-            const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             auto kept_of = [&](int c) {
                 return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
             };
+            // right operands: S0 and R with both parts, or the first of two tiles alone
+            constexpr uint32_t id2 = idesc_f16(128, 2 * PW) | kIdescBMN;
+            constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
+            constexpr uint32_t idy = PLO ? id2 : id1;
+            for (int c = 0; c < nc; ++c) {
+                const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
+                if (!mbar_poll(full + (c & 1), (c >> 1) & 1, a.status)) break;
+                if (!mbar_poll(bar_s, ph, a.status)) break;
+                if (PW == 64 && a.kept) bulk_wait_read_all();  // R's when K S0 is
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                            id2, kk > 0);
+                mma_commit(bar_x);
+                if (PW == 64 && a.kept) {  // S0's hi part is what training keeps
+                    bulk_store(kept_of(c) + kTile, smem + M::s, h_bytes(DK));
+                    bulk_commit();
+                }
+                if (c > 0 && !mbar_poll(bar_o, ph ^ 1, a.status)) break;
+                tc_fence_after();
+                // Q in rows 64 to 127: its tiles of 128 rows start one tile early
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                            idy, kk > 0);
+                if (!mbar_poll(full_h, ph, a.status)) break;
+                if (!mbar_poll(bar_r, ph, a.status)) break;
+                tc_fence_after();
+                if (PW == 64 && a.kept) bulk_wait_read_all();  // S0's place is written when H R is done
+                const uint32_t hh = sb + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
+                // (of 64 rows of H the 64 behind them are not read)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                mma_commit(bar_h);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), idy, kk > 0);
+                if constexpr (PLO)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                mma_commit(bar_y);
+                if (PW == 64 && a.kept) {
+                    bulk_store(kept_of(c), smem + M::r, kTile);
+                    bulk_commit();
+                }
+            }
+            bulk_wait_all();
+        } else if (warp == 9 && lane == 0) {
+            const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             int loads = 0, h_loads = 0;
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
@@ -721,75 +777,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 bulk_load(smem + M::h, rec0 + (long long)c * rec_bytes(DK) + rec_h(DK), 2 * h_bytes(DK), full_h);
                 ++h_loads;
             };
+            // H counts as in once the chunk before is known to be done too, so that no barrier
+            // is ever a whole turn ahead of this thread
             load(0);
             load_h(0);
+            mbar_arrive(full_h);
             if (nc > 1) load(1);
-            // right operands: S0 and R with both parts, or the first of two tiles alone
-            constexpr uint32_t id2 = idesc_f16(128, 2 * PW) | kIdescBMN;
-            constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
-            constexpr uint32_t idy = PLO ? id2 : id1;
-            int waited = 0, h_waited = 0;
-            for (int c = 0; c < nc; ++c) {
-                const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
-                if (!mbar_wait(full + (c & 1), (c >> 1) & 1, a.status)) break;
-                ++waited;
-                if (!mbar_poll(bar_s, ph, a.status)) break;
-                if (PW == 64 && a.kept) bulk_wait_read_all();  // R's when K S0 is
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
-                            id2, kk > 0);
-                mma_commit(bar_x);
-                if (PW == 64 && a.kept) {  // S0's hi part is what training keeps
-                    bulk_store(kept_of(c) + kTile, smem + M::s, h_bytes(DK));
-                    bulk_commit();
-                }
-                if (c > 0 && !mbar_poll(bar_o, ph ^ 1, a.status)) break;
-                tc_fence_after();
-                // Q in rows 64 to 127: its tiles of 128 rows start one tile early
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
-                            idy, kk > 0);
-                if (!mbar_wait(full_h, ph, a.status)) break;
-                ++h_waited;
-                if (!mbar_poll(bar_r, ph, a.status)) break;
-                tc_fence_after();
-                if (PW == 64 && a.kept) {
-                    bulk_wait_read_all();  // S0's place is written when H R is done
-                    bulk_store(kept_of(c), smem + M::r, kTile);
-                    bulk_commit();
-                }
-                const uint32_t hh = sb + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
-                // (of 64 rows of H the 64 behind them are not read)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
-                mma_commit(bar_h);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), idy, kk > 0);
-                if constexpr (PLO)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
-                mma_commit(bar_y);
-                if (c + 1 < nc) {
-                    if (!mbar_poll(bar_h, ph, a.status)) break;
-                    load_h(c + 1);
-                    if (!mbar_poll(bar_y, ph, a.status)) break;
-                    if (c + 2 < nc) load(c + 2);
-                }
+            for (int c = 0; c + 1 < nc; ++c) {
+                if (!mbar_wait(bar_h, c & 1, a.status)) break;
+                load_h(c + 1);
+                if (!mbar_wait(bar_y, c & 1, a.status)) break;
+                mbar_arrive(full_h);
+                if (c + 2 < nc) load(c + 2);
             }
-            bulk_wait_all();
             // never leave with a load still landing
-            for (; waited < loads; ++waited)
-                (void)mbar_wait(full + (waited & 1), (waited >> 1) & 1, a.status);
-            if (h_waited < h_loads) (void)mbar_wait(full_h, h_waited & 1, a.status);
+            for (int c = max(0, loads - 2); c < loads; ++c)
+                (void)mbar_wait(full + (c & 1), (c >> 1) & 1, a.status);
+            (void)mbar_wait(full_h, (h_loads - 1) & 1, a.status);
         }
     } else {
         take_registers();

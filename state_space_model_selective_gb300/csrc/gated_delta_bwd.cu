@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < 7; ++i) mbar_init(full + i, i == 2 ? 2 : 1);
         mbar_init(bar_s, 8);
         mbar_init(bar_o, 4);
         mbar_init(bar_r, 4);
@@ -116,6 +116,50 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             auto kept_of = [&](int it) {
                 return a.kept + ((bh * nc + nc - 1 - it) * a.d.pans + pan) * adjoint_bytes(DK);
             };
+            constexpr uint32_t id = idesc_f16(128, 128) | kIdescAMN | kIdescBMN;
+            constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescAMN | kIdescBMN;
+            for (int it = 0; it < nc; ++it) {
+                const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
+                bulk_wait_read_all();  // dR's place is written again when H^T L is done
+                if (!mbar_poll(full_p, ph, a.status)) break;
+                if (!mbar_poll(bar_o, ph, a.status)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmP, mdesc(sb + M::p, kk, kTile), mdesc(sb + M::dy, kk, kTile),
+                            id64, kk > 0);
+                if (!mbar_poll(full + (it & 1), (it >> 1) & 1, a.status)) break;
+                if (!mbar_poll(bar_s, ph, a.status)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_f16(tmem + kTmX, mdesc(st + M::h, kk, h_bytes(DK)),
+                            mdesc(sb + M::l_hi, kk, h_bytes(DK)), id, kk > 0);
+                mma_commit(bar_x);
+                // dY and L's hi part are kept as they are
+                bulk_store(kept_of(it) + kTile, smem + M::dy, kTile);
+                bulk_store(kept_of(it) + 2 * kTile, smem + M::l_hi, h_bytes(DK));
+                bulk_commit();
+                if (!mbar_poll(full_q, ph, a.status)) break;
+                tc_fence_after();
+                // (of 64 columns of dstate the second block of rows is not read)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmQ, mdesc(sb + M::q, kk, kTile), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
+                bulk_wait_read_all();  // dY's place is written when this is done, L's later
+                mma_commit(bar_q);
+                if (!mbar_poll(bar_r, ph, a.status)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmK, mdesc(st + M::k, kk, kTile), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
+                mma_commit(bar_l);
+                if (!mbar_poll(bar_d, ph, a.status)) break;
+                bulk_store(kept_of(it), smem + M::dr, kTile);
+                bulk_commit();
+            }
+            bulk_wait_all();
+        } else if (warp == 9 && lane == 0) {
             int kh_loads = 0, q_loads = 0, p_loads = 0;
             auto rec_of = [&](int it) { return rec0 + (long long)(nc - 1 - it) * rec_bytes(DK); };
             auto load_kh = [&](int it) {
@@ -140,69 +184,26 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 bulk_load(smem + M::p, rec_of(it) + rec_p(DK), 2 * kTile, full_p);
                 ++p_loads;
             };
+            // Q counts as in once the chunk before is known to be done too, so that no barrier
+            // is ever a whole turn ahead of this thread
             load_kh(0);
             load_p(0);
             load_q(0);
+            mbar_arrive(full_q);
             if (nc > 1) load_kh(1);
-            int kh_seen = 0, q_seen = 0, p_seen = 0;
-            constexpr uint32_t id = idesc_f16(128, 128) | kIdescAMN | kIdescBMN;
-            constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescAMN | kIdescBMN;
-            for (int it = 0; it < nc; ++it) {
-                const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
-                bulk_wait_read_all();  // dR's place is written again when H^T L is done
-                if (!mbar_wait(full_p, ph, a.status)) break;
-                ++p_seen;
-                if (!mbar_poll(bar_o, ph, a.status)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmP, mdesc(sb + M::p, kk, kTile), mdesc(sb + M::dy, kk, kTile),
-                            id64, kk > 0);
-                if (!mbar_wait(full + (it & 1), (it >> 1) & 1, a.status)) break;
-                ++kh_seen;
-                if (!mbar_poll(bar_s, ph, a.status)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmX, mdesc(st + M::h, kk, h_bytes(DK)),
-                            mdesc(sb + M::l_hi, kk, h_bytes(DK)), id, kk > 0);
-                mma_commit(bar_x);
-                // dY and L's hi part are kept as they are
-                bulk_store(kept_of(it) + kTile, smem + M::dy, kTile);
-                bulk_store(kept_of(it) + 2 * kTile, smem + M::l_hi, h_bytes(DK));
-                bulk_commit();
-                if (!mbar_wait(full_q, ph, a.status)) break;
-                ++q_seen;
-                tc_fence_after();
-                // (of 64 columns of dstate the second block of rows is not read)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmQ, mdesc(sb + M::q, kk, kTile), mdesc(sb + M::o_hi, kk, kTile), id, kk > 0);
-                bulk_wait_read_all();  // dY's place is written when this is done, L's later
-                mma_commit(bar_q);
-                if (!mbar_poll(bar_r, ph, a.status)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmK, mdesc(st + M::k, kk, kTile), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
-                mma_commit(bar_l);
-                if (!mbar_poll(bar_d, ph, a.status)) break;
-                bulk_store(kept_of(it), smem + M::dr, kTile);
-                bulk_commit();
-                if (it + 1 < nc) {
-                    if (!mbar_wait(bar_q, ph, a.status)) break;  // (it follows bar_x)
-                    load_p(it + 1);
-                    load_q(it + 1);
-                    if (!mbar_wait(bar_l, ph, a.status)) break;
-                    if (it + 2 < nc) load_kh(it + 2);
-                }
+            for (int it = 0; it + 1 < nc; ++it) {
+                if (!mbar_wait(bar_q, it & 1, a.status)) break;  // (it follows bar_x)
+                load_p(it + 1);
+                load_q(it + 1);
+                if (!mbar_wait(bar_l, it & 1, a.status)) break;
+                mbar_arrive(full_q);
+                if (it + 2 < nc) load_kh(it + 2);
             }
-            bulk_wait_all();
             // never leave with a load still landing
-            for (; kh_seen < kh_loads; ++kh_seen)
-                (void)mbar_wait(full + (kh_seen & 1), (kh_seen >> 1) & 1, a.status);
-            if (q_seen < q_loads) (void)mbar_wait(full_q, q_seen & 1, a.status);
-            if (p_seen < p_loads) (void)mbar_wait(full_p, p_seen & 1, a.status);
+            for (int it = max(0, kh_loads - 2); it < kh_loads; ++it)
+                (void)mbar_wait(full + (it & 1), (it >> 1) & 1, a.status);
+            (void)mbar_wait(full_q, (q_loads - 1) & 1, a.status);
+            (void)mbar_wait(full_p, (p_loads - 1) & 1, a.status);
         }
     } else {
         take_registers();
