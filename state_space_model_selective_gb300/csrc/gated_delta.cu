@@ -668,10 +668,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_s = full + 6;   // S0 is in shared memory
     uint64_t* bar_r = full + 7;   // R is
     uint64_t* bar_o = full + 8;   // Q S0 and P R have been read
-    uint64_t* bar_m = full + 9;   // the largest values of S0 are known
-    uint64_t* bar_v = full + 10;  // and those of V
-    float* s_most = reinterpret_cast<float*>(full + 11);  // [2 chunks][8 warps of S, 4 of V]
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
+    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][8 warps of S0, 4 of V]
+    float* s_first = reinterpret_cast<float*>(s_most + 24);     // [8]: of the first S0
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + 8);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pan = blockIdx.x % a.d.pans;
@@ -685,8 +684,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         mbar_init(bar_s, 8);
         mbar_init(bar_r, 8);
         mbar_init(bar_o, 4);
-        mbar_init(bar_m, 8);
-        mbar_init(bar_v, 4);
+        for (int n = 0; n < 24; ++n) s_most[n] = 0;
         fence_mbar_init();
     }
     tc_fence_before();
@@ -830,8 +828,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     v = fmaxf(v, most8_bf16(*reinterpret_cast<const uint4*>(
                                      tile + piece(i, (SC / 8) * part + p))));
                 v = warp_most(off ? 0.0f : v);
-                if (lane == 0) s_most[12 * (c & 1) + 8 + (quarter & 1) * 2 + part] = v;
-                warp_arrive(bar_v);
+                if (lane == 0) post_most(s_most + 12 * (c & 1) + 8 + (quarter & 1) * 2 + part, v, c);
             }
             return in;
         };
@@ -851,8 +848,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             tc_fence_before();
             warp_arrive(bar_s);
             const float m = warp_most<SC / 2>(S) * s_s;
-            if (lane == 0) s_most[12 * (c & 1) + warp] = m;
-            warp_arrive(bar_m);
+            if (lane == 0) post_most(s_most + 12 * (c & 1) + warp, m, c);
             if (PW == 64 && a.kept && tid == 0) factors_of(c)[1] = s_s;
         };
         bool ok = gates_of(0);
@@ -868,19 +864,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 S[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
             }
             const float m = warp_most<SC / 2>(S);
-            if (lane == 0) s_most[12 + warp] = m;
+            if (lane == 0) s_first[warp] = m;
             named_bar_sync(1, 256);
-            scaled<SC / 2>(S, tile_scale(most_of<8>(s_most + 12), kBoundTop, s_s), S);
-            named_bar_sync(1, 256);
+            scaled<SC / 2>(S, tile_scale(most_of<8>(s_first), kBoundTop, s_s), S);
             if (ok) put_state(0);
         }
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
             const float fs = f_k * s_s, ee = e_end, sp = s_p, sh = s_h;
-            ok = warp_wait(bar_m, ph, a.status) && warp_wait(bar_v, ph, a.status);
+            float s_max, v_max;
+            ok = read_most<2>(s_most + 12 * ph, c, s_max, a.status) &&
+                 read_most<1>(s_most + 12 * ph + 8, c, v_max, a.status);
             if (!ok) break;
-            const float s_max = most_of<8>(s_most + 12 * ph);
-            const float r_bound = fmaf(k_bound, s_max, most_of<4>(s_most + 12 * ph + 8));
+            const float r_bound = fmaf(k_bound, s_max, v_max);
             float s_r, s_next;
             const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
             // |H|_1 over a row is at most 64 times its largest value

@@ -363,6 +363,41 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
+// Largest values that warps tell one another while products run, without a barrier: a word
+// of shared memory each, its last byte the chunk it belongs to, rounded up to the others (it
+// only enters bounds).  A word is written and read as a whole.
+__device__ __forceinline__ void post_most(uint32_t* slot, float most, int chunk) {
+    *reinterpret_cast<volatile uint32_t*>(slot) =
+        (__float_as_uint(most) & 0xffffff00u) | ((uint32_t)(chunk + 1) & 0xffu);
+}
+// The largest of 4 N words once they all belong to `chunk`; false when that takes too long.
+template <int N>
+__device__ __forceinline__ bool read_most(const uint32_t* slots, int chunk, float& most, uint32_t* status) {
+    const uint32_t tag = (uint32_t)(chunk + 1) & 0xffu, addr = smem_u32(slots);
+    for (uint32_t tries = 0; tries < (1u << 26); ++tries) {
+        uint32_t off = 0, m = 0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint32_t w[4];
+            asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(addr + 16 * n)
+                         : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                off |= w[e] ^ tag;
+                m = max(m, w[e]);
+            }
+        }
+        if (__all_sync(0xffffffffu, (off & 0xffu) == 0)) {
+            most = __uint_as_float(m | 0xffu);
+            return true;
+        }
+    }
+    record_status(status, SSM_ERR_TIMEOUT);
+    return false;
+}
+
 // Registers move from the warps that load and multiply to those that compute: a kernel of 12
 // warps has 168 a thread at launch, 64512 in all; then 8 warps have 224 and 4 have 56.
 __device__ __forceinline__ void take_registers() {

@@ -83,10 +83,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_s = full + 7;    // L is in shared memory
     uint64_t* bar_o = full + 8;    // dY and e dY are
     uint64_t* bar_r = full + 9;    // -e dR is
-    uint64_t* bar_m = full + 10;   // the largest values of L are known
-    uint64_t* bar_d = full + 11;   // dR is in shared memory
-    float* s_most = reinterpret_cast<float*>(full + 12);  // [2 chunks][8 warps of L, 4 of dY]
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_most + 24);
+    uint64_t* bar_d = full + 10;   // dR is in shared memory
+    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 12);  // [2 chunks][8 warps of L, 4 of dY]
+    float* s_first = reinterpret_cast<float*>(s_most + 24);     // [8]: of the first L
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + 8);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pan = blockIdx.x % a.d.pans;
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         mbar_init(bar_s, 8);
         mbar_init(bar_o, 4);
         mbar_init(bar_r, 4);
-        mbar_init(bar_m, 8);
         mbar_init(bar_d, 4);
+        for (int n = 0; n < 24; ++n) s_most[n] = 0;
         fence_mbar_init();
     }
     tc_fence_before();
@@ -250,8 +250,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             tc_fence_before();
             warp_arrive(bar_s);
             const float m = warp_most<16>(L) * s_l;
-            if (lane == 0) s_most[12 * (it & 1) + warp] = m;
-            warp_arrive(bar_m);
+            if (lane == 0) post_most(s_most + 12 * (it & 1) + warp, m, it);
             if (tid == 0) factors_of(nc - 1 - it)[2] = s_l;
         };
         uint4 dy[4];
@@ -275,10 +274,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 unpack8_bf16(dy[p], x + 4 * p);
             }
             m = warp_most(m);
-            float* most = s_most + 12 * (it & 1) + 8;
-            if (lane == 0) most[(quarter & 1) * 2 + part] = m;
-            named_bar_sync(2, 128);
-            const float all = most_of<4>(most);
+            uint32_t* most = s_most + 12 * (it & 1) + 8;
+            if (lane == 0) post_most(most + (quarter & 1) * 2 + part, m, it);
+            float all = 0.0f;
+            const bool told = read_most<1>(most, it, all, a.status);
             float s_dy, s_o;
             uint32_t hw[16], lw[16];
             scaled<16>(x, tile_scale(all, kTop, s_dy), y);
@@ -291,29 +290,28 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             put32(smem + M::o_lo, i, 4 * part, lw);
             fence_proxy_async_smem();
             warp_arrive(bar_o);
+            return told;
         };
         {   // the last chunk: its largest values are measured
             const float m = warp_most<16>(L);
-            if (lane == 0) s_most[12 + warp] = m;
+            if (lane == 0) s_first[warp] = m;
             named_bar_sync(1, 256);
-            const float all = most_of<8>(s_most + 12);
-            named_bar_sync(1, 256);
-            scaled<16>(L, tile_scale(all, kBoundTop, s_l), L);
+            scaled<16>(L, tile_scale(most_of<8>(s_first), kBoundTop, s_l), L);
             put_state(0);
         }
         bool ok = gates_of(0);  // the same for all lanes of a warp
         fetch(nc - 1);
-        if (upper) put_dy(0, e_row);
+        if (upper) ok = put_dy(0, e_row) && ok;
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
             const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p;
             if (c > 0) fetch(c - 1);
             f2 x[16];
-            ok = ok && warp_wait(bar_m, ph, a.status) && warp_wait(bar_o, ph, a.status);
             // bounds: of L and dY measured, of dR and the next L from them
-            const float l_max = most_of<8>(s_most + 12 * ph);
-            const float dy_max = most_of<4>(s_most + 12 * ph + 8);
+            float l_max = 0.0f, dy_max = 0.0f;
+            ok = ok && read_most<2>(s_most + 12 * ph, it, l_max, a.status) &&
+                 read_most<1>(s_most + 12 * ph + 8, it, dy_max, a.status);
             const float dr_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
             float s_od, s_dyd, s_r, s_g, s_next;
             (void)tile_scale(dy_max * em, kBoundTop, s_od);  // (put_dy's factors)
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             if (c > 0) {
                 ok = gates_of(it + 1) && ok;
                 // (the products that read dY and e dY are done: bar_q follows them)
-                if (upper) put_dy(it + 1, e_row);
+                if (upper) ok = put_dy(it + 1, e_row) && ok;
             }
             ok = ok && warp_wait(bar_l, ph, a.status);
             tc_fence_after();

@@ -7,11 +7,11 @@
 //   gradient: g = dy turned back, dx = r (g w - n mean(g w n)),
 //             dw = sum over tokens and heads of g n
 //
-// Bound by memory: 8 (gradient: 26) FP32 operations an element against 4 to 16 bytes,
-// so a head's row is read once into registers, reduced by shuffles, turned and
-// written.  What costs beside the bytes is the angles: a token's rot / 2 sines and
-// cosines are shared by its heads, so a CTA takes a few tokens with all their heads
-// and puts them into shared memory first.
+// Memory bounds it where the issue slots do not: an arithmetic instruction takes a
+// scheduler two cycles here, and a row of 128 bf16 leaves a lane 16 elements.  So two
+// floats go to an instruction where that is possible, rows are counted on without
+// divisions, and a token's rot / 2 sines and cosines are made once for all its heads: a CTA
+// takes a few tokens with all their heads and puts them into shared memory first.
 //
 // Angles of far positions: position * inv_freq is a phase in turns whose whole part
 // does not matter, so inv_freq / 2 pi is taken as a 64-bit binary fraction and
@@ -35,8 +35,9 @@ using namespace ssm;
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
 constexpr int kTable = 2048;      // sines and cosines a CTA holds (pairs x tokens)
-constexpr int kFwdCtas = 6;       // of the forward on an SM
-constexpr int kBwdMost = 152 * 3; // CTAs of the gradient, whose sums of dw are joined
+constexpr int kFwdCtas = 4;       // of the forward on an SM
+constexpr int kBwdCtas = 2;       // of the gradient
+constexpr int kBwdMost = 152 * kBwdCtas;  // its CTAs at most, whose sums of dw are joined
 
 // How a row's columns are paired.
 enum Pairs {
@@ -78,13 +79,30 @@ __device__ __forceinline__ void lane_columns(const QkArgs& a, int p, int& c0, in
     c1 = min(c1, a.dim);
 }
 
-__device__ __forceinline__ void unpack(uint4 v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16lo(w[i]);
-        f[2 * i + 1] = bf16hi(w[i]);
-    }
+// Two floats to an instruction.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return a + b;
 }
 
 // 8 consecutive elements as loaded: raw bits, converted when they are used, so that
@@ -103,22 +121,25 @@ template <> struct Raw<__nv_bfloat16> {
         v = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float* f) const { unpack(v, f); }
+    __device__ __forceinline__ void get(f2* f) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pair(bf16lo(w[i]), bf16hi(w[i]));
+    }
 };
 template <> struct Raw<float> {
-    float4 a, b;
+    ulonglong2 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        a = __ldcs(reinterpret_cast<const ulonglong2*>(p));
+        b = __ldcs(reinterpret_cast<const ulonglong2*>(p) + 1);
     }
     __device__ __forceinline__ void load_each(const float* p) {
-        a = make_float4(p[0], p[1], p[2], p[3]);
-        b = make_float4(p[4], p[5], p[6], p[7]);
+        a = make_ulonglong2(pair(p[0], p[1]), pair(p[2], p[3]));
+        b = make_ulonglong2(pair(p[4], p[5]), pair(p[6], p[7]));
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float* f) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void zero() { a = b = make_ulonglong2(0, 0); }
+    __device__ __forceinline__ void get(f2* f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
     }
 };
 
@@ -129,15 +150,17 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* row, int c, int dim, b
     else r.load_each(row + c);
 }
 
-__device__ __forceinline__ void store8(float* p, const float* f) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+__device__ __forceinline__ void store8(float* p, const f2* f) {
+    __stcs(reinterpret_cast<ulonglong2*>(p), make_ulonglong2(f[0], f[1]));
+    __stcs(reinterpret_cast<ulonglong2*>(p) + 1, make_ulonglong2(f[2], f[3]));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f2* f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        float a, b;
+        unpair(f[i], a, b);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         w[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
@@ -157,54 +180,62 @@ __device__ __forceinline__ unsigned long long turn_of(double freq) {
     return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
 }
 
-// Sines and cosines of the tile's tokens, [token][pair]; rot / 2 pairs.
-__device__ __forceinline__ void make_table(const QkArgs& a, long long t0, int n, float2* cs) {
-    const int half = a.rot / 2;
+// Cosines and sines of the tile's tokens, each [token][pair]; rot / 2 pairs a token,
+// `pitch` floats apart (a multiple of 4).
+struct Table {
+    float cos[kTable], sin[kTable];
+};
+__host__ __device__ __forceinline__ int table_pitch(int rot) { return (rot / 2 + 3) / 4 * 4; }
+__device__ __forceinline__ void make_table(const QkArgs& a, long long t0, int n, Table& cs) {
+    const int half = a.rot / 2, pitch = table_pitch(a.rot);
     if (half == 0) return;
-    // a thread keeps its pair where it can, and with it the pair's fraction
-    const int per = half <= kThreads ? kThreads / half : 1;
-    for (int e = threadIdx.x; e < half * per; e += kThreads) {
-        const int pair = e % half;
-        const unsigned long long f = turn_of(a.freq[pair]);
-        for (int t = e / half; t < n; t += per) {
-            const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * f;
-            // in half turns, -1 to 1
-            const float r = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
-            float s, c;
-            sincospif(r, &s, &c);
-            cs[t * half + pair] = make_float2(c, s);
-        }
+    // a thread keeps its pair, and with it the pair's fraction
+    const int per = kThreads / half;
+    const int pair = threadIdx.x % half;
+    if ((int)threadIdx.x >= half * per) return;
+    const unsigned long long f = turn_of(a.freq[pair]);
+    for (int t = threadIdx.x / half; t < n; t += per) {
+        const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * f;
+        // in half turns, -1 to 1
+        const float r = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
+        sincospif(r, &cs.sin[t * pitch + pair], &cs.cos[t * pitch + pair]);
     }
 }
 
-// t turned by the token's angles (BACK: turned back), in place.  `buf`: this row's dim
-// floats of shared memory (kShared).
+// u and v (8 elements each, pairs) turned by the token's angles (BACK: turned back), in
+// place.  `c`, `s`: the token's cosines and sines; `buf`: this row's floats of shared memory
+// (kShared).
 template <int MODE, bool BACK>
-__device__ __forceinline__ void turn(const QkArgs& a, const float2* cs, int p, int c0, int c1,
-                                     float* u, float* v, float* buf) {
+__device__ __forceinline__ void turn(const QkArgs& a, const float* c, const float* s, int p, int c0,
+                                     int c1, f2* u, f2* v, float* buf) {
     const int half = a.rot / 2;
     if constexpr (MODE == kHalves) {
         if (p < a.rot / 16) {
+            const f2 minus = ::pair(-1.0f, -1.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 k = cs[c0 + i];
-                const float s = BACK ? -k.y : k.y;
-                const float x = u[i], z = v[i];
-                u[i] = fmaf(x, k.x, -z * s);
-                v[i] = fmaf(x, s, z * k.x);
+            for (int i = 0; i < 4; i += 2) {
+                const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(c + c0 + 2 * i);
+                const ulonglong2 ss = *reinterpret_cast<const ulonglong2*>(s + c0 + 2 * i);
+                const f2 ce[2] = {cc.x, cc.y}, se[2] = {ss.x, ss.y};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const f2 n = mul2(se[e], minus);
+                    const f2 x = u[i + e], y = v[i + e];
+                    u[i + e] = fma2(x, ce[e], mul2(y, BACK ? se[e] : n));
+                    v[i + e] = fma2(x, BACK ? n : se[e], mul2(y, ce[e]));
+                }
             }
         }
     } else if constexpr (MODE == kNeighbours) {
-        auto both = [&](float* x, int c) {
+        auto both = [&](f2* x, int col) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const int pair = (c + i) >> 1;
-                if (pair < half) {
-                    const float2 k = cs[pair];
-                    const float s = BACK ? -k.y : k.y;
-                    const float e = x[i], o = x[i + 1];
-                    x[i] = fmaf(e, k.x, -o * s);
-                    x[i + 1] = fmaf(e, s, o * k.x);
+            for (int i = 0; i < 4; ++i) {
+                const int k = (col >> 1) + i;
+                if (k < half) {
+                    const float co = c[k], si = BACK ? -s[k] : s[k];
+                    float e, o;
+                    unpair(x[i], e, o);
+                    x[i] = ::pair(fmaf(e, co, -o * si), fmaf(e, si, o * co));
                 }
             }
         };
@@ -212,23 +243,30 @@ __device__ __forceinline__ void turn(const QkArgs& a, const float2* cs, int p, i
         both(v, c1);
     } else {
         __syncwarp();
+        if (c0 < a.dim)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c0 < a.dim) buf[c0 + i] = u[i];
-            if (c1 < a.dim) buf[c1 + i] = v[i];
-        }
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f2*>(buf + c0 + 2 * i) = u[i];
+        if (c1 < a.dim)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f2*>(buf + c1 + 2 * i) = v[i];
         __syncwarp();
-        auto each = [&](float* x, int c) {
-            if (c >= a.dim) return;
+        auto each = [&](f2* x, int from) {
+            if (from >= a.dim) return;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int col = c + i;
-                if (col >= a.rot) continue;
-                const bool first = col < half;
-                const float2 k = cs[first ? col : col - half];
-                const float s = BACK ? -k.y : k.y;
-                const float other = buf[first ? col + half : col - half];
-                x[i] = fmaf(x[i], k.x, first ? -other * s : other * s);
+            for (int i = 0; i < 4; ++i) {
+                float t[2];
+                unpair(x[i], t[0], t[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = from + 2 * i + e;
+                    if (col >= a.rot) continue;
+                    const bool first = col < half;
+                    const int k = first ? col : col - half;
+                    const float si = BACK ? -s[k] : s[k];
+                    const float other = buf[first ? col + half : col - half];
+                    t[e] = fmaf(t[e], c[k], first ? -other * si : other * si);
+                }
+                x[i] = ::pair(t[0], t[1]);
             }
         };
         each(u, c0);
@@ -236,80 +274,111 @@ __device__ __forceinline__ void turn(const QkArgs& a, const float2* cs, int p, i
     }
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int c0, int c1, int dim, float* f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[i] = w && c0 < dim ? w[c0 + i] : 1.0f;
-        f[8 + i] = w && c1 < dim ? w[c1 + i] : 1.0f;
+// Both weights in shared memory, ones where there is none.
+__device__ __forceinline__ void load_weights(const QkArgs& a, float* w) {
+    for (int e = threadIdx.x; e < 2 * kMaxDim; e += kThreads) {
+        const float* p = a.w[e / kMaxDim];
+        const int c = e % kMaxDim;
+        w[e] = p && c < a.dim ? p[c] : 1.0f;
     }
 }
+__device__ __forceinline__ void weights_of(const float* w, int c0, int c1, f2* u, f2* v) {
+    // (columns past the row: any of the 256)
+    const ulonglong2* p0 = reinterpret_cast<const ulonglong2*>(w + min(c0, kMaxDim - 8));
+    const ulonglong2* p1 = reinterpret_cast<const ulonglong2*>(w + min(c1, kMaxDim - 8));
+    const ulonglong2 a = p0[0], b = p0[1], c = p1[0], d = p1[1];
+    u[0] = a.x; u[1] = a.y; u[2] = b.x; u[3] = b.y;
+    v[0] = c.x; v[1] = c.y; v[2] = d.x; v[3] = d.y;
+}
+
+// The rows (token, head) of a tile that one group of lanes takes: every `groups`th.
+struct Walk {
+    int t, h, dt, dh, heads;
+    __device__ __forceinline__ Walk(int group, int groups, int n) : heads(n) {
+        t = group / n;
+        h = group - t * n;
+        dt = groups / n;
+        dh = groups - dt * n;
+    }
+    __device__ __forceinline__ void next() {
+        t += dt;
+        h += dh;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+    }
+};
 
 // A row group's shared memory for kShared.
-template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 1;
+template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 4;
 
 template <typename TI, typename TO, int MODE>
 __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
-    __shared__ float2 table[kTable];
-    __shared__ float bufs[kBufFloats<MODE>];
+    __shared__ __align__(16) Table table;
+    __shared__ __align__(16) float weights[2 * kMaxDim];
+    __shared__ __align__(16) float bufs[kBufFloats<MODE>];
     const int lanes = a.lanes, groups = kThreads / lanes;
     const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
     int c0, c1;
     lane_columns<MODE>(a, p, c0, c1);
     float* buf = MODE == kShared ? bufs + group * (16 * lanes) : nullptr;
-    const int half = a.rot / 2;
+    const int pitch = table_pitch(a.rot);
+    load_weights(a, weights);
 
     for (long long t0 = (long long)blockIdx.x * a.tile; t0 < a.tokens;
          t0 += (long long)gridDim.x * a.tile) {
         const int n = (int)min((long long)a.tile, a.tokens - t0);
-        make_table(a, t0, n, table);
         bool ready = false;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
-            const TI* x = static_cast<const TI*>(a.x[which]);
-            TO* y = static_cast<TO*>(a.y[which]);
-            const int heads = a.heads[which], rows = n * heads;
+            const int heads = a.heads[which];
+            if (heads == 0) continue;
+            const TI* x = static_cast<const TI*>(a.x[which]) + t0 * a.stride[which];
+            TO* y = static_cast<TO*>(a.y[which]) + t0 * heads * a.dim;
             const bool vec = a.vec[which] != 0;
-            float w[16];
-            load_weights(a.w[which], c0, c1, a.dim, w);
             // rows beyond the last are loaded as zeros and not stored: every lane of a
             // warp takes part in the shuffles
             Raw<TI> r0, r1;
-            auto fetch = [&](int row) {
-                if (row < rows) {
-                    const TI* src = x + (t0 + row / heads) * a.stride[which] +
-                                    (long long)(row % heads) * a.dim;
+            Walk in(group, groups, heads), at(group, groups, heads);
+            auto fetch = [&]() {
+                if (in.t < n) {
+                    const TI* src = x + in.t * a.stride[which] + in.h * a.dim;
                     load8(r0, src, c0, a.dim, vec);
                     load8(r1, src, c1, a.dim, vec);
                 } else {
                     r0.zero();
                     r1.zero();
                 }
+                in.next();
             };
-            fetch(group);
+            fetch();
             if (!ready) {
+                make_table(a, t0, n, table);
                 __syncthreads();
                 ready = true;
             }
-            for (int base = 0; base < rows; base += groups) {
-                const int row = base + group;
-                float u[8], v[8];
+            const int rows = n * heads;
+            for (int base = 0; base < rows; base += groups, at.next()) {
+                f2 u[4], v[4], wu[4], wv[4];
                 r0.get(u);
                 r1.get(v);
-                if (base + groups < rows) fetch(row + groups);
-                float s = 0.0f;
+                if (base + groups < rows) fetch();
+                f2 s = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s = fmaf(u[i], u[i], fmaf(v[i], v[i], s));
-                s = row_sum(s, lanes);
-                const float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));
+                for (int i = 0; i < 4; ++i) s = fma2(u[i], u[i], fma2(v[i], v[i], s));
+                const float r = rsqrtf(fmaf(row_sum(sum2(s), lanes), a.inv_dim, a.eps));
+                weights_of(weights + which * kMaxDim, c0, c1, wu, wv);
+                const f2 r2 = pair(r, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    u[i] *= r * w[i];
-                    v[i] *= r * w[8 + i];
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = mul2(u[i], mul2(wu[i], r2));
+                    v[i] = mul2(v[i], mul2(wv[i], r2));
                 }
-                const int t = min(row / heads, n - 1);
-                turn<MODE, false>(a, table + t * half, p, c0, c1, u, v, buf);
-                if (row < rows) {
-                    TO* dst = y + ((t0 + t) * heads + row % heads) * (long long)a.dim;
+                const int t = min(at.t, n - 1);
+                turn<MODE, false>(a, table.cos + t * pitch, table.sin + t * pitch, p, c0, c1, u, v, buf);
+                if (at.t < n) {
+                    TO* dst = y + ((long long)at.t * heads + at.h) * a.dim;
                     if (c0 < a.dim) store8(dst + c0, u);
                     if (c1 < a.dim) store8(dst + c1, v);
                 }
@@ -321,91 +390,105 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
 
 // TI: the type of x and dx, TO: of dy.
 template <typename TI, typename TO, int MODE>
-__global__ void __launch_bounds__(kThreads, 3) qk_bwd_kernel(const QkArgs a) {
-    __shared__ float2 table[kTable];
-    __shared__ float bufs[kBufFloats<MODE>];
-    __shared__ float sums[kThreads * 16];
+__global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs a) {
+    __shared__ __align__(16) Table table;
+    __shared__ __align__(16) float weights[2 * kMaxDim];
+    __shared__ __align__(16) float sums[kThreads * 16];  // rows' exchange, then the sums of dw
     const int lanes = a.lanes, groups = kThreads / lanes;
     const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
     int c0, c1;
     lane_columns<MODE>(a, p, c0, c1);
-    float* buf = MODE == kShared ? bufs + group * (16 * lanes) : nullptr;
-    const int half = a.rot / 2;
+    float* buf = sums + group * (16 * lanes);
+    const int pitch = table_pitch(a.rot);
+    load_weights(a, weights);
 
-    // q's rows over all tiles, then k's, so that one set of sums is kept at a time
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const TI* x = static_cast<const TI*>(a.x[which]);
-        const TO* dy = static_cast<const TO*>(a.dy[which]);
-        TI* dx = static_cast<TI*>(a.y[which]);
-        const int heads = a.heads[which];
-        const bool vec = a.vec[which] != 0;
-        float w[16], dw[16];
-        load_weights(a.w[which], c0, c1, a.dim, w);
+    f2 dw[2][8];  // of q and k
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
-        for (long long t0 = (long long)blockIdx.x * a.tile; heads > 0 && t0 < a.tokens;
-             t0 += (long long)gridDim.x * a.tile) {
-            const int n = (int)min((long long)a.tile, a.tokens - t0), rows = n * heads;
+    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0;
+    for (long long t0 = (long long)blockIdx.x * a.tile; t0 < a.tokens;
+         t0 += (long long)gridDim.x * a.tile) {
+        const int n = (int)min((long long)a.tile, a.tokens - t0);
+        bool ready = false;
+        auto rows_of = [&](int which, f2* sum) {
+            const int heads = a.heads[which];
+            if (heads == 0) return;
+            const TI* x = static_cast<const TI*>(a.x[which]) + t0 * a.stride[which];
+            const TO* dy = static_cast<const TO*>(a.dy[which]) + t0 * heads * a.dim;
+            TI* dx = static_cast<TI*>(a.y[which]) + t0 * heads * a.dim;
+            const bool vec = a.vec[which] != 0;
             Raw<TI> x0, x1;
             Raw<TO> d0, d1;
-            auto fetch = [&](int row) {
-                if (row < rows) {
-                    const int t = row / heads, h = row % heads;
-                    const TI* src = x + (t0 + t) * a.stride[which] + (long long)h * a.dim;
+            Walk in(group, groups, heads), at(group, groups, heads);
+            auto fetch = [&]() {
+                if (in.t < n) {
+                    const TI* src = x + in.t * a.stride[which] + in.h * a.dim;
                     load8(x0, src, c0, a.dim, vec);
                     load8(x1, src, c1, a.dim, vec);
-                    const TO* up = dy + ((t0 + t) * heads + h) * (long long)a.dim;
+                    const TO* up = dy + ((long long)in.t * heads + in.h) * a.dim;
                     load8(d0, up, c0, a.dim, true);
                     load8(d1, up, c1, a.dim, true);
                 } else {
                     x0.zero(); x1.zero(); d0.zero(); d1.zero();
                 }
+                in.next();
             };
-            fetch(group);
-            __syncthreads();  // the table's readers are done
-            make_table(a, t0, n, table);
-            __syncthreads();
-            for (int base = 0; base < rows; base += groups) {
-                const int row = base + group;
-                float u[8], v[8], g[8], q[8];
+            fetch();
+            if (!ready) {
+                __syncthreads();  // the table's readers are done
+                make_table(a, t0, n, table);
+                __syncthreads();
+                ready = true;
+            }
+            const int rows = n * heads;
+            for (int base = 0; base < rows; base += groups, at.next()) {
+                f2 u[4], v[4], g[4], q[4], wu[4], wv[4];
                 x0.get(u);
                 x1.get(v);
                 d0.get(g);
                 d1.get(q);
-                if (base + groups < rows) fetch(row + groups);
-                const int t = min(row / heads, n - 1);
-                turn<MODE, true>(a, table + t * half, p, c0, c1, g, q, buf);
-                float s = 0.0f, m = 0.0f;
+                if (base + groups < rows) fetch();
+                const int t = min(at.t, n - 1);
+                turn<MODE, true>(a, table.cos + t * pitch, table.sin + t * pitch, p, c0, c1, g, q, buf);
+                weights_of(weights + which * kMaxDim, c0, c1, wu, wv);
+                f2 s2 = 0, m2 = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s = fmaf(u[i], u[i], fmaf(v[i], v[i], s));
-                    m = fmaf(g[i] * w[i], u[i], fmaf(q[i] * w[8 + i], v[i], m));
+                for (int i = 0; i < 4; ++i) {
+                    s2 = fma2(u[i], u[i], fma2(v[i], v[i], s2));
+                    wu[i] = mul2(wu[i], g[i]);
+                    wv[i] = mul2(wv[i], q[i]);
+                    m2 = fma2(wu[i], u[i], fma2(wv[i], v[i], m2));
                 }
-                s = row_sum(s, lanes);
-                m = row_sum(m, lanes);
-                if (row >= rows) continue;  // uniform over a row; no shuffles behind this
-                const float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));
-                const float mr = m * a.inv_dim * r * r;  // mean(g w n) r, per x
+                const float s = row_sum(sum2(s2), lanes), m = row_sum(sum2(m2), lanes);
+                // (rows beyond the last add nothing to dw, with eps 0 either)
+                const float r = at.t < n ? rsqrtf(fmaf(s, a.inv_dim, a.eps)) : 0.0f;
+                const float mr = -m * a.inv_dim * r * r;  // of mean(g w n) r, per x
+                const f2 r2 = pair(r, r), mr2 = pair(mr, mr);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dw[i] = fmaf(g[i], u[i] * r, dw[i]);
-                    dw[8 + i] = fmaf(q[i], v[i] * r, dw[8 + i]);
-                    g[i] = r * fmaf(-mr, u[i], g[i] * w[i]);
-                    q[i] = r * fmaf(-mr, v[i], q[i] * w[8 + i]);
+                for (int i = 0; i < 4; ++i) {
+                    sum[i] = fma2(g[i], mul2(u[i], r2), sum[i]);
+                    sum[4 + i] = fma2(q[i], mul2(v[i], r2), sum[4 + i]);
+                    g[i] = mul2(r2, fma2(mr2, u[i], wu[i]));
+                    q[i] = mul2(r2, fma2(mr2, v[i], wv[i]));
                 }
-                TI* dst = dx + ((t0 + t) * heads + row % heads) * (long long)a.dim;
-                if (c0 < a.dim) store8(dst + c0, g);
-                if (c1 < a.dim) store8(dst + c1, q);
+                if (at.t < n) {
+                    TI* dst = dx + ((long long)at.t * heads + at.h) * a.dim;
+                    if (c0 < a.dim) store8(dst + c0, g);
+                    if (c1 < a.dim) store8(dst + c1, q);
+                }
             }
-        }
-        if (!a.join) continue;
+        };
+        rows_of(0, dw[0]);
+        rows_of(1, dw[1]);
+    }
+    if (!a.join) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
         // the CTA's sum over its groups, in their order
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c0 < a.dim) sums[group * a.dim + c0 + i] = dw[i];
-            if (c1 < a.dim) sums[group * a.dim + c1 + i] = dw[8 + i];
+        for (int i = 0; i < 4; ++i) {
+            if (c0 < a.dim) *reinterpret_cast<f2*>(sums + group * a.dim + c0 + 2 * i) = dw[which][i];
+            if (c1 < a.dim) *reinterpret_cast<f2*>(sums + group * a.dim + c1 + 2 * i) = dw[which][4 + i];
         }
         __syncthreads();
         for (int c = threadIdx.x; c < a.dim; c += kThreads) {
@@ -413,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 3) qk_bwd_kernel(const QkArgs a) {
             for (int j = 0; j < groups; ++j) s += sums[j * a.dim + c];
             a.partial[((long long)blockIdx.x * 2 + which) * a.dim + c] = s;
         }
-        __syncthreads();
     }
 }
 
@@ -426,6 +508,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* partial, int c
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < 2 * dim)
+#pragma unroll 8
         for (int j = warp; j < ctas; j += 32) s += partial[(long long)j * 2 * dim + c];
     part[warp][lane] = s;
     __syncthreads();
@@ -466,7 +549,7 @@ void plan(QkArgs& a, int mode, long long slots) {
     // few enough that all the CTAs have some
     const int groups = kThreads / a.lanes, heads = std::max(1, a.heads[0] + a.heads[1]);
     long long t = (4 * groups + heads - 1) / heads;
-    if (a.rot > 0) t = std::min<long long>(t, kTable / (a.rot / 2));
+    if (a.rot > 0) t = std::min<long long>(t, kTable / table_pitch(a.rot));
     t = std::min(t, (a.tokens + slots - 1) / slots);
     a.tile = (int)std::max(1LL, t);
 }
