@@ -34,7 +34,7 @@ using namespace ssm;
 
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
-constexpr int kTable = 2048;      // sines and cosines a CTA holds (pairs x tokens)
+constexpr int kTable = 1024;      // sines and cosines a CTA holds at a time (pairs x tokens)
 constexpr int kFwdCtas = 4;       // of the forward on an SM
 constexpr int kBwdCtas = 2;       // of the gradient
 constexpr int kBwdMost = 152 * kBwdCtas;  // its CTAs at most, whose sums of dw are joined
@@ -64,19 +64,21 @@ struct QkArgs {
     int join;                  // gradient: dw is wanted
 };
 
-// The first column of a lane's two chunks (dim where it has none).
+// The first column of a lane's two chunks (dim where it has none): lane p's are the pth of
+// the first and of the second half, of the rotated columns and then of the others, so that
+// neighbouring lanes read and write neighbouring chunks.
 template <int MODE>
 __device__ __forceinline__ void lane_columns(const QkArgs& a, int p, int& c0, int& c1) {
     const int half = MODE == kHalves ? a.rot / 16 : 0;
+    const int rest = a.dim / 8 - 2 * half, near = (rest + 1) / 2;
     if (p < half) {
         c0 = 8 * p;
         c1 = 8 * (p + half);
     } else {
-        c0 = 8 * (2 * p);  // behind 2 * half chunks: 2 half + 2 (p - half)
-        c1 = c0 + 8;
+        const int j = p - half;
+        c0 = j < near ? 8 * (2 * half + j) : a.dim;
+        c1 = near + j < rest ? 8 * (2 * half + near + j) : a.dim;
     }
-    c0 = min(c0, a.dim);
-    c1 = min(c1, a.dim);
 }
 
 // Two floats to an instruction.
@@ -143,11 +145,28 @@ template <> struct Raw<float> {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* row, int c, int dim, bool vec) {
-    if (c >= dim) r.zero();
-    else if (vec) r.load(row + c);
-    else r.load_each(row + c);
+// A lane's two chunks of a row.  A tile's rows are addressed by its base, the same for all
+// threads, and 32-bit byte offsets.  FULL: all lanes have both chunks, and rows are aligned.
+struct Chunks {
+    uint32_t o0, d1;     // the first chunk's offset in the row, and the second's from it
+    bool in0, in1;
+};
+template <bool FULL, typename T>
+__device__ __forceinline__ void load_row(Raw<T>& a, Raw<T>& b, const T* base, uint32_t at, const Chunks& c,
+                                         bool vec) {
+    const T* p0 = reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + (at + c.o0));
+    const T* p1 = reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + (at + c.o0 + c.d1));
+    if (FULL) {
+        a.load(p0);
+        b.load(p1);
+    } else {
+        if (!c.in0) a.zero();
+        else if (vec) a.load(p0);
+        else a.load_each(p0);
+        if (!c.in1) b.zero();
+        else if (vec) b.load(p1);
+        else b.load_each(p1);
+    }
 }
 
 __device__ __forceinline__ void store8(float* p, const f2* f) {
@@ -166,6 +185,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const f2* f) {
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_row(T* base, uint32_t at, const Chunks& c, const f2* u, const f2* v) {
+    char* p = reinterpret_cast<char*>(base);
+    if (FULL || c.in0) store8(reinterpret_cast<T*>(p + (at + c.o0)), u);
+    if (FULL || c.in1) store8(reinterpret_cast<T*>(p + (at + c.o0 + c.d1)), v);
+}
+
 // Sum over the `lanes` lanes of a row (all lanes of the warp take part).
 __device__ __forceinline__ float row_sum(float v, int lanes) {
 #pragma unroll
@@ -180,49 +206,65 @@ __device__ __forceinline__ unsigned long long turn_of(double freq) {
     return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
 }
 
-// Cosines and sines of the tile's tokens, each [token][pair]; rot / 2 pairs a token,
-// `pitch` floats apart (a multiple of 4).
+// Cosines, sines and negative sines of a tile's tokens, each [token][pair]; rot / 2 pairs a
+// token, `pitch` floats apart (a multiple of 4).
 struct Table {
-    float cos[kTable], sin[kTable];
+    float cos[kTable], sin[kTable], neg[kTable];
 };
 __host__ __device__ __forceinline__ int table_pitch(int rot) { return (rot / 2 + 3) / 4 * 4; }
-__device__ __forceinline__ void make_table(const QkArgs& a, long long t0, int n, Table& cs) {
-    const int half = a.rot / 2, pitch = table_pitch(a.rot);
-    if (half == 0) return;
-    // a thread keeps its pair, and with it the pair's fraction
-    const int per = kThreads / half;
-    const int pair = threadIdx.x % half;
-    if ((int)threadIdx.x >= half * per) return;
-    const unsigned long long f = turn_of(a.freq[pair]);
-    for (int t = threadIdx.x / half; t < n; t += per) {
-        const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * f;
-        // in half turns, -1 to 1
-        const float r = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
-        sincospif(r, &cs.sin[t * pitch + pair], &cs.cos[t * pitch + pair]);
+// A thread's pair and its fraction of a turn stay the same for all tiles.
+struct Angles {
+    unsigned long long turn;
+    int pair, first, per;   // threads of the same pair are `per` tokens apart
+    __device__ __forceinline__ Angles(const QkArgs& a) {
+        const int half = max(a.rot / 2, 1);
+        per = kThreads / half;
+        pair = threadIdx.x % half;
+        first = threadIdx.x / half;
+        if (a.rot == 0 || first >= per) first = 1 << 30;  // no part in it
+        turn = first < per ? turn_of(a.freq[pair]) : 0;
     }
-}
+    __device__ __forceinline__ void make(const QkArgs& a, long long t0, int n, Table& cs) const {
+        const int pitch = table_pitch(a.rot);
+        for (int t = first; t < n; t += per) {
+            const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * turn;
+            // in half turns, -1 to 1
+            const float r = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
+            float s, c;
+            sincospif(r, &s, &c);
+            const int at = t * pitch + pair;
+            cs.cos[at] = c;
+            cs.sin[at] = s;
+            cs.neg[at] = -s;
+        }
+    }
+};
 
 // u and v (8 elements each, pairs) turned by the token's angles (BACK: turned back), in
-// place.  `c`, `s`: the token's cosines and sines; `buf`: this row's floats of shared memory
-// (kShared).
+// place.  `c`, `s`, `m`: the token's cosines, sines and their negatives; `buf`: this row's
+// floats of shared memory (kShared).
 template <int MODE, bool BACK>
-__device__ __forceinline__ void turn(const QkArgs& a, const float* c, const float* s, int p, int c0,
-                                     int c1, f2* u, f2* v, float* buf) {
+__device__ __forceinline__ void turn(const QkArgs& a, const float* c, const float* s, const float* m,
+                                     int p, int c0, int c1, f2* u, f2* v, float* buf) {
     const int half = a.rot / 2;
     if constexpr (MODE == kHalves) {
         if (p < a.rot / 16) {
-            const f2 minus = ::pair(-1.0f, -1.0f);
+            if (BACK) {
+                const float* t = s;
+                s = m;
+                m = t;
+            }
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
                 const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(c + c0 + 2 * i);
                 const ulonglong2 ss = *reinterpret_cast<const ulonglong2*>(s + c0 + 2 * i);
-                const f2 ce[2] = {cc.x, cc.y}, se[2] = {ss.x, ss.y};
+                const ulonglong2 mm = *reinterpret_cast<const ulonglong2*>(m + c0 + 2 * i);
+                const f2 ce[2] = {cc.x, cc.y}, se[2] = {ss.x, ss.y}, me[2] = {mm.x, mm.y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const f2 n = mul2(se[e], minus);
                     const f2 x = u[i + e], y = v[i + e];
-                    u[i + e] = fma2(x, ce[e], mul2(y, BACK ? se[e] : n));
-                    v[i + e] = fma2(x, BACK ? n : se[e], mul2(y, ce[e]));
+                    u[i + e] = fma2(x, ce[e], mul2(y, me[e]));
+                    v[i + e] = fma2(x, se[e], mul2(y, ce[e]));
                 }
             }
         }
@@ -274,38 +316,46 @@ __device__ __forceinline__ void turn(const QkArgs& a, const float* c, const floa
     }
 }
 
-// Both weights in shared memory, ones where there is none.
+// Both weights in shared memory, ones where there is none and for a lane's missing columns.
+constexpr int kWeights = kMaxDim + 8;
 __device__ __forceinline__ void load_weights(const QkArgs& a, float* w) {
-    for (int e = threadIdx.x; e < 2 * kMaxDim; e += kThreads) {
-        const float* p = a.w[e / kMaxDim];
-        const int c = e % kMaxDim;
+    for (int e = threadIdx.x; e < 2 * kWeights; e += kThreads) {
+        const float* p = a.w[e / kWeights];
+        const int c = e % kWeights;
         w[e] = p && c < a.dim ? p[c] : 1.0f;
     }
 }
 __device__ __forceinline__ void weights_of(const float* w, int c0, int c1, f2* u, f2* v) {
-    // (columns past the row: any of the 256)
-    const ulonglong2* p0 = reinterpret_cast<const ulonglong2*>(w + min(c0, kMaxDim - 8));
-    const ulonglong2* p1 = reinterpret_cast<const ulonglong2*>(w + min(c1, kMaxDim - 8));
+    const ulonglong2* p0 = reinterpret_cast<const ulonglong2*>(w + c0);
+    const ulonglong2* p1 = reinterpret_cast<const ulonglong2*>(w + c1);
     const ulonglong2 a = p0[0], b = p0[1], c = p1[0], d = p1[1];
     u[0] = a.x; u[1] = a.y; u[2] = b.x; u[3] = b.y;
     v[0] = c.x; v[1] = c.y; v[2] = d.x; v[3] = d.y;
 }
 
-// The rows (token, head) of a tile that one group of lanes takes: every `groups`th.
+// The rows (token, head) of a tile that one group of lanes takes, every `groups`th, and
+// where they start in a tensor whose tokens are `stride` elements apart.
 struct Walk {
     int t, h, dt, dh, heads;
-    __device__ __forceinline__ Walk(int group, int groups, int n) : heads(n) {
+    uint32_t at, step, wrap;  // bytes; a tile has less than 2^31 of them
+    __device__ __forceinline__ Walk(int group, int groups, int n, int dim, long long stride, int size)
+        : heads(n) {
         t = group / n;
         h = group - t * n;
         dt = groups / n;
         dh = groups - dt * n;
+        at = (uint32_t)(t * stride + h * dim) * size;
+        step = (uint32_t)(dt * stride + dh * dim) * size;
+        wrap = (uint32_t)(stride - (long long)n * dim) * size;
     }
     __device__ __forceinline__ void next() {
         t += dt;
         h += dh;
+        at += step;
         if (h >= heads) {
             h -= heads;
             ++t;
+            at += wrap;
         }
     }
 };
@@ -313,23 +363,31 @@ struct Walk {
 // A row group's shared memory for kShared.
 template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 4;
 
-template <typename TI, typename TO, int MODE>
-__global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
-    __shared__ __align__(16) Table table;
-    __shared__ __align__(16) float weights[2 * kMaxDim];
+template <typename TI, typename TO, int MODE, bool FULL>
+__global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs a) {
+    __shared__ __align__(16) Table tables[2];
+    __shared__ __align__(16) float weights[2 * kWeights];
     __shared__ __align__(16) float bufs[kBufFloats<MODE>];
     const int lanes = a.lanes, groups = kThreads / lanes;
     const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
     int c0, c1;
     lane_columns<MODE>(a, p, c0, c1);
+    const Chunks in_x{c0 * (uint32_t)sizeof(TI), (c1 - c0) * (uint32_t)sizeof(TI), c0 < a.dim, c1 < a.dim};
+    const Chunks in_y{c0 * (uint32_t)sizeof(TO), (c1 - c0) * (uint32_t)sizeof(TO), c0 < a.dim, c1 < a.dim};
     float* buf = MODE == kShared ? bufs + group * (16 * lanes) : nullptr;
     const int pitch = table_pitch(a.rot);
+    const long long stride = (long long)gridDim.x * a.tile;
+    long long t0 = (long long)blockIdx.x * a.tile;
+    const Angles angles(a);
     load_weights(a, weights);
+    if (t0 < a.tokens) angles.make(a, t0, (int)min((long long)a.tile, a.tokens - t0), tables[0]);
+    __syncthreads();
 
-    for (long long t0 = (long long)blockIdx.x * a.tile; t0 < a.tokens;
-         t0 += (long long)gridDim.x * a.tile) {
+    for (int k = 0; t0 < a.tokens; t0 += stride, k ^= 1) {
         const int n = (int)min((long long)a.tile, a.tokens - t0);
-        bool ready = false;
+        const Table& table = tables[k];
+        if (t0 + stride < a.tokens)  // the next tile's
+            angles.make(a, t0 + stride, (int)min((long long)a.tile, a.tokens - t0 - stride), tables[k ^ 1]);
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             const int heads = a.heads[which];
@@ -337,15 +395,17 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
             const TI* x = static_cast<const TI*>(a.x[which]) + t0 * a.stride[which];
             TO* y = static_cast<TO*>(a.y[which]) + t0 * heads * a.dim;
             const bool vec = a.vec[which] != 0;
+            const int rows = n * heads;
             // rows beyond the last are loaded as zeros and not stored: every lane of a
             // warp takes part in the shuffles
             Raw<TI> r0, r1;
-            Walk in(group, groups, heads), at(group, groups, heads);
+            Walk in(group, groups, heads, a.dim, a.stride[which], sizeof(TI));
+            int t = 0, t_next = 0;  // the rows' tokens
+            uint32_t out = (uint32_t)(group * a.dim) * sizeof(TO);
             auto fetch = [&]() {
+                t_next = min(in.t, n - 1);
                 if (in.t < n) {
-                    const TI* src = x + in.t * a.stride[which] + in.h * a.dim;
-                    load8(r0, src, c0, a.dim, vec);
-                    load8(r1, src, c1, a.dim, vec);
+                    load_row<FULL>(r0, r1, x, in.at, in_x, vec);
                 } else {
                     r0.zero();
                     r1.zero();
@@ -353,62 +413,62 @@ __global__ void __launch_bounds__(kThreads, 4) qk_fwd_kernel(const QkArgs a) {
                 in.next();
             };
             fetch();
-            if (!ready) {
-                make_table(a, t0, n, table);
-                __syncthreads();
-                ready = true;
-            }
-            const int rows = n * heads;
-            for (int base = 0; base < rows; base += groups, at.next()) {
+            for (int row = group; row - group < rows;
+                 row += groups, out += (uint32_t)(groups * a.dim) * sizeof(TO)) {
                 f2 u[4], v[4], wu[4], wv[4];
                 r0.get(u);
                 r1.get(v);
-                if (base + groups < rows) fetch();
+                t = t_next;
+                if (row - group + groups < rows) fetch();
                 f2 s = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s = fma2(u[i], u[i], fma2(v[i], v[i], s));
                 const float r = rsqrtf(fmaf(row_sum(sum2(s), lanes), a.inv_dim, a.eps));
-                weights_of(weights + which * kMaxDim, c0, c1, wu, wv);
+                weights_of(weights + which * kWeights, c0, c1, wu, wv);
                 const f2 r2 = pair(r, r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     u[i] = mul2(u[i], mul2(wu[i], r2));
                     v[i] = mul2(v[i], mul2(wv[i], r2));
                 }
-                const int t = min(at.t, n - 1);
-                turn<MODE, false>(a, table.cos + t * pitch, table.sin + t * pitch, p, c0, c1, u, v, buf);
-                if (at.t < n) {
-                    TO* dst = y + ((long long)at.t * heads + at.h) * a.dim;
-                    if (c0 < a.dim) store8(dst + c0, u);
-                    if (c1 < a.dim) store8(dst + c1, v);
-                }
+                const int at = t * pitch;
+                turn<MODE, false>(a, table.cos + at, table.sin + at, table.neg + at, p, c0, c1, u, v, buf);
+                if (row < rows) store_row<FULL>(y, out, in_y, u, v);
             }
         }
-        __syncthreads();  // the table is read before it is made anew
+        __syncthreads();  // this table is read, the next one is made
     }
 }
 
 // TI: the type of x and dx, TO: of dy.
-template <typename TI, typename TO, int MODE>
+template <typename TI, typename TO, int MODE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs a) {
-    __shared__ __align__(16) Table table;
-    __shared__ __align__(16) float weights[2 * kMaxDim];
+    __shared__ __align__(16) Table tables[2];
+    __shared__ __align__(16) float weights[2 * kWeights];
     __shared__ __align__(16) float sums[kThreads * 16];  // rows' exchange, then the sums of dw
     const int lanes = a.lanes, groups = kThreads / lanes;
     const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
     int c0, c1;
     lane_columns<MODE>(a, p, c0, c1);
+    const Chunks in_x{c0 * (uint32_t)sizeof(TI), (c1 - c0) * (uint32_t)sizeof(TI), c0 < a.dim, c1 < a.dim};
+    const Chunks in_y{c0 * (uint32_t)sizeof(TO), (c1 - c0) * (uint32_t)sizeof(TO), c0 < a.dim, c1 < a.dim};
     float* buf = sums + group * (16 * lanes);
     const int pitch = table_pitch(a.rot);
+    const long long stride = (long long)gridDim.x * a.tile;
+    long long t0 = (long long)blockIdx.x * a.tile;
+    const Angles angles(a);
     load_weights(a, weights);
+    if (t0 < a.tokens) angles.make(a, t0, (int)min((long long)a.tile, a.tokens - t0), tables[0]);
+    __syncthreads();
 
     f2 dw[2][8];  // of q and k
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0;
-    for (long long t0 = (long long)blockIdx.x * a.tile; t0 < a.tokens;
-         t0 += (long long)gridDim.x * a.tile) {
+    for (int k = 0; t0 < a.tokens; t0 += stride, k ^= 1) {
         const int n = (int)min((long long)a.tile, a.tokens - t0);
-        bool ready = false;
+        const Table& table = tables[k];
+        if (t0 + stride < a.tokens)  // the next tile's
+            angles.make(a, t0 + stride, (int)min((long long)a.tile, a.tokens - t0 - stride), tables[k ^ 1]);
         auto rows_of = [&](int which, f2* sum) {
             const int heads = a.heads[which];
             if (heads == 0) return;
@@ -416,40 +476,36 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs
             const TO* dy = static_cast<const TO*>(a.dy[which]) + t0 * heads * a.dim;
             TI* dx = static_cast<TI*>(a.y[which]) + t0 * heads * a.dim;
             const bool vec = a.vec[which] != 0;
+            const int rows = n * heads;
             Raw<TI> x0, x1;
             Raw<TO> d0, d1;
-            Walk in(group, groups, heads), at(group, groups, heads);
+            Walk in(group, groups, heads, a.dim, a.stride[which], sizeof(TI));
+            int t = 0, t_next = 0;
+            uint32_t up = (uint32_t)(group * a.dim) * sizeof(TO), out = (uint32_t)(group * a.dim) * sizeof(TI);
             auto fetch = [&]() {
+                t_next = min(in.t, n - 1);
                 if (in.t < n) {
-                    const TI* src = x + in.t * a.stride[which] + in.h * a.dim;
-                    load8(x0, src, c0, a.dim, vec);
-                    load8(x1, src, c1, a.dim, vec);
-                    const TO* up = dy + ((long long)in.t * heads + in.h) * a.dim;
-                    load8(d0, up, c0, a.dim, true);
-                    load8(d1, up, c1, a.dim, true);
+                    load_row<FULL>(x0, x1, x, in.at, in_x, vec);
+                    load_row<FULL>(d0, d1, dy, up, in_y, true);
                 } else {
                     x0.zero(); x1.zero(); d0.zero(); d1.zero();
                 }
                 in.next();
+                up += (uint32_t)(groups * a.dim) * sizeof(TO);
             };
             fetch();
-            if (!ready) {
-                __syncthreads();  // the table's readers are done
-                make_table(a, t0, n, table);
-                __syncthreads();
-                ready = true;
-            }
-            const int rows = n * heads;
-            for (int base = 0; base < rows; base += groups, at.next()) {
+            for (int row = group; row - group < rows;
+                 row += groups, out += (uint32_t)(groups * a.dim) * sizeof(TI)) {
                 f2 u[4], v[4], g[4], q[4], wu[4], wv[4];
                 x0.get(u);
                 x1.get(v);
                 d0.get(g);
                 d1.get(q);
-                if (base + groups < rows) fetch();
-                const int t = min(at.t, n - 1);
-                turn<MODE, true>(a, table.cos + t * pitch, table.sin + t * pitch, p, c0, c1, g, q, buf);
-                weights_of(weights + which * kMaxDim, c0, c1, wu, wv);
+                t = t_next;
+                if (row - group + groups < rows) fetch();
+                const int at = t * pitch;
+                turn<MODE, true>(a, table.cos + at, table.sin + at, table.neg + at, p, c0, c1, g, q, buf);
+                weights_of(weights + which * kWeights, c0, c1, wu, wv);
                 f2 s2 = 0, m2 = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -460,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs
                 }
                 const float s = row_sum(sum2(s2), lanes), m = row_sum(sum2(m2), lanes);
                 // (rows beyond the last add nothing to dw, with eps 0 either)
-                const float r = at.t < n ? rsqrtf(fmaf(s, a.inv_dim, a.eps)) : 0.0f;
+                const float r = row < rows ? rsqrtf(fmaf(s, a.inv_dim, a.eps)) : 0.0f;
                 const float mr = -m * a.inv_dim * r * r;  // of mean(g w n) r, per x
                 const f2 r2 = pair(r, r), mr2 = pair(mr, mr);
 #pragma unroll
@@ -470,15 +526,12 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs
                     g[i] = mul2(r2, fma2(mr2, u[i], wu[i]));
                     q[i] = mul2(r2, fma2(mr2, v[i], wv[i]));
                 }
-                if (at.t < n) {
-                    TI* dst = dx + ((long long)at.t * heads + at.h) * a.dim;
-                    if (c0 < a.dim) store8(dst + c0, g);
-                    if (c1 < a.dim) store8(dst + c1, q);
-                }
+                if (row < rows) store_row<FULL>(dx, out, in_x, g, q);
             }
         };
         rows_of(0, dw[0]);
         rows_of(1, dw[1]);
+        __syncthreads();  // this table is read, the next one is made
     }
     if (!a.join) return;
 #pragma unroll
@@ -551,6 +604,9 @@ void plan(QkArgs& a, int mode, long long slots) {
     long long t = (4 * groups + heads - 1) / heads;
     if (a.rot > 0) t = std::min<long long>(t, kTable / table_pitch(a.rot));
     t = std::min(t, (a.tokens + slots - 1) / slots);
+    // what lies between its first and last element fits 31 bits (a single token's heads do)
+    t = std::min(t, (1LL << 29) / std::max(1LL, std::max(a.stride[0], a.stride[1])) - 1);
+    t = std::min(t, (1LL << 29) / ((long long)heads * a.dim));
     a.tile = (int)std::max(1LL, t);
 }
 
@@ -566,6 +622,13 @@ void by_mode(int mode, F&& f) {
     if (mode == kHalves) f(std::integral_constant<int, kHalves>{});
     else if (mode == kNeighbours) f(std::integral_constant<int, kNeighbours>{});
     else f(std::integral_constant<int, kShared>{});
+}
+
+// Rows of 16, 32, ... 256 columns that are aligned: no lane goes without
+bool whole(const QkArgs& a) {
+    for (int i = 0; i < 2; ++i)
+        if (a.heads[i] > 0 && !a.vec[i]) return false;
+    return a.dim == 16 * a.lanes;
 }
 
 ssm_status_t check_sizes(const QkArgs& a, int interleaved, ssm_dtype_t in, ssm_dtype_t out) {
@@ -638,14 +701,14 @@ extern "C" ssm_status_t ssm_qk_norm_rope_fwd(
     if (sms == 0) return SSM_ERR_CUDA;
     const int mode = mode_of(a, interleaved);
     plan(a, mode, (long long)sms * kFwdCtas);
-    // every CTA takes one tile where the grid allows
     const unsigned grid =
-        (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, 1 << 30);
+        (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, (long long)sms * kFwdCtas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
         by_mode(mode, [&](auto m) {
-            qk_fwd_kernel<decltype(ti), decltype(to), decltype(m)::value>
-                <<<grid, kThreads, 0, s>>>(a);
+            constexpr int MODE = decltype(m)::value;
+            if (whole(a)) qk_fwd_kernel<decltype(ti), decltype(to), MODE, true><<<grid, kThreads, 0, s>>>(a);
+            else qk_fwd_kernel<decltype(ti), decltype(to), MODE, false><<<grid, kThreads, 0, s>>>(a);
         });
         return true;
     });
@@ -716,8 +779,9 @@ extern "C" ssm_status_t ssm_qk_norm_rope_bwd(
     a.partial = static_cast<float*>(workspace);
     by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
         by_mode(mode, [&](auto m) {
-            qk_bwd_kernel<decltype(ti), decltype(to), decltype(m)::value>
-                <<<grid, kThreads, 0, s>>>(a);
+            constexpr int MODE = decltype(m)::value;
+            if (whole(a)) qk_bwd_kernel<decltype(ti), decltype(to), MODE, true><<<grid, kThreads, 0, s>>>(a);
+            else qk_bwd_kernel<decltype(ti), decltype(to), MODE, false><<<grid, kThreads, 0, s>>>(a);
         });
         return true;
     });
