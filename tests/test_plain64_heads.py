@@ -45,3 +45,47 @@ def test_rotation_is_one():
     assert np.allclose(np.sum(at(x, 77) ** 2), np.sum(x ** 2))
     assert np.allclose(H.turn(at(x, 77), H.angles(np.array([[77]]), f), 12, False, back=True), x)
     assert np.allclose(np.sum(at(x, 5) * at(y, 9)), np.sum(at(x, 1005) * at(y, 1009)))
+
+
+@pytest.mark.parametrize("groups,state", [(1, True), (2, True), (2, False)])
+def test_delta_gradient(groups, state):
+    rng = np.random.default_rng(groups)
+    b, n, h, dk, dv = 1, 4, 2, 3, 2
+    q, k = rng.standard_normal((2, b, n, groups, dk))
+    v, dy = rng.standard_normal((2, b, n, h, dv))
+    g, beta = -rng.random((b, n, h)), rng.random((b, n, h))
+    S, dS = rng.standard_normal((2, b, h, dv, dk))
+    if not state:
+        S = dS = None
+
+    def loss(**kw):
+        a = dict(q=q, k=k, v=v, g=g, beta=beta, state=S)
+        a.update(kw)
+        y, last, _ = H.delta_fwd(**a)
+        return np.sum(y * dy) + (np.sum(last * dS) if state else 0.0)
+
+    grads = H.delta_bwd(q, k, v, g, beta, dy, S, dS)
+    for name, x, got in zip(("q", "k", "v", "g", "beta", "state"), (q, k, v, g, beta, S), grads):
+        if x is not None:
+            ref = differences(lambda t: loss(**{name: t}), x)
+            np.testing.assert_allclose(got, ref, atol=2e-7, err_msg=name)
+
+
+def test_delta_masks():
+    """A step with beta 0 is not looked at; a gate of -inf forgets whatever there was."""
+    rng = np.random.default_rng(5)
+    q, k = rng.standard_normal((2, 1, 6, 1, 4))
+    v = rng.standard_normal((1, 6, 1, 3))
+    g, beta = -rng.random((1, 6, 1)), rng.random((1, 6, 1))
+    beta[0, 2] = 0
+    k[0, 2], v[0, 2] = np.nan, np.nan
+    y, last, _ = H.delta_fwd(q, k, v, g, beta)
+    assert np.isfinite(y).all()
+    grads = H.delta_bwd(q, k, v, g, beta, np.ones_like(v))
+    assert all(np.isfinite(t).all() for t in grads[:5])
+    assert not grads[1][0, 2].any() and not grads[2][0, 2].any() and not grads[4][0, 2].any()
+    g[0, 4] = -np.inf
+    y1, last1, _ = H.delta_fwd(q, k, v, g, beta)
+    y2, last2, _ = H.delta_fwd(q[:, 4:], k[:, 4:], v[:, 4:], g[:, 4:], beta[:, 4:])
+    assert np.array_equal(y1[:, 4:], y2) and np.array_equal(last1, last2)
+    assert not H.delta_bwd(q, k, v, g, beta, np.ones_like(v))[3][0, 4].any()

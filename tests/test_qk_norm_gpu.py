@@ -185,3 +185,15 @@ def test_guards_around_the_outputs():
                                                   ("dq", "dk", "dq_weight", "dk_weight")}, **args)
     for name, b in bufs.items():
         assert torch.all(b[:64] == 7) and torch.all(b[-64:] == 7), name
+
+
+def test_a_tile_of_tokens_far_apart():
+    """Rows of a wide projection: a tile is shortened so that its bytes count in 31 bits."""
+    wide = torch.zeros(1, 40, 1 << 24, dtype=BF16, device="cuda")
+    q, _, wq, _, pos, freq = inputs(1, 40, 2, 1, 64, 64, BF16, 6)
+    wide[..., 1 << 20:(1 << 20) + 128] = q.flatten(2).cuda()
+    part = wide[..., 1 << 20:(1 << 20) + 128].unflatten(-1, (2, 64))
+    args = dict(q_weight=wq.cuda(), positions=pos.cuda(), inv_freq=freq.cuda())
+    near_, _ = binding.ssm_qk_norm_rope_fwd(q.cuda(), **args)
+    far_, _ = binding.ssm_qk_norm_rope_fwd(part, **args)
+    assert torch.equal(near_, far_)
