@@ -469,10 +469,11 @@ __device__ __forceinline__ f2 dot8(uint4 a, uint4 b, f2 s) {
 // The exponent of a power of two, and back (0 for what is too small).
 __device__ __forceinline__ int exponent(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
-// Columns whose L is this far below others' (none, where no later step read them) have U
-// twice: rounded where its own values are for the products with dY and dR, and far below
-// for the sums with other columns' L.
-constexpr int kFar = -10;
+// U's products with L and those with dR and dY have one U, whose factor follows L's: columns
+// of headdim with this much less in L than others (with nothing, where no later step read
+// them) are left out of F2, so that their U never loses bits (2^7 or so at most, on fp16's
+// 2^-14 to 2^15).  Products below 2^kNone in all columns count as 0.
+constexpr int kFar = -16, kNone = -110;
 
 // CTAs walk the chunks and groups of heads; a warp brings in what comes next.  Rows of
 // products are lanes: steps as k rows (0 to 63) and as q rows (64 to 127).
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool is_q = row >= kC;
         const int i = row & 63, col0 = (DK / 2) * part;  // first column of dstate
-        int n = 0, hn = 0, fn = 0;
+        int n = 0, hn = 0;
         bool ok = true;
         for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
             const unsigned bg = item / nc;
@@ -586,8 +587,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 const int h = group * ratio + hh;
                 bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
                 const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
-                const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
-                const float skq = gates->s_kq;
                 // a step's row of K or Q, columns col0 + 16 n .. + 15
                 auto own_row = [&](int n16, f2* v) {
                     const int c0 = col0 + 16 * n16;
@@ -597,13 +596,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                         hg + M::kq + (c0 >> 6) * 2 * kTile + piece(row, ((c0 & 63) >> 3) + q)),
                                     v + 4 * q);
                 };
-                // Products of U and L are summed over the panels where they are: there U's factor
-                // is chosen so that all have the same, the largest of theirs.  A panel's own: U is
-                // at most 64 products of 2^13 and 2^15, brought down to 2^15
+                // Products of U and L are summed over the panels where they are: U's factor is
+                // chosen so that all have the same, the largest of theirs.  A panel's own: U is at
+                // most 64 products of 2^13 and 2^15, brought down to 2^15
                 constexpr float kDown = 1.0f / 524288.0f;
-                int e_ul = -100;
+                int e_ul = kNone;
                 for (int p = 0; p < pans; ++p) e_ul = max(e_ul, exponent(fac[8 * p]) + exponent(fac[8 * p + 6]));
-                const float s_ul = power(min(e_ul, 127));
                 // what the other heads have left in the sums does not belong to this one's dot
                 float before = 0.0f;
                 if (hh > 0) {
@@ -621,6 +619,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                 for (int e = 0; e < 16; ++e) own[e] = 0;
                 float beta_sum = 0.0f, ls = 0.0f;
+                bool begun = false;  // F2
                 for (int p = 0; p < pans; ++p, ++n) {
                     const uint32_t st = sb + M::stages + (n & 1) * M::stage;
                     const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
@@ -655,29 +654,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     here = warp_wait(bar_u, n & 1, a.status) && here;
                     tc_fence_after();
                     const int below = exponent(s_r) + exponent(s_l) - e_ul;
-                    const float down = below < kFar ? 1.0f : power(below);
-                    const float s_u = s_r * gates->s_t / (kDown * down);
-                    auto put_u = [&](float f) {
-                        if (here && !is_q) {
-                            f2 x[16];
-                            uint32_t hw[16];
-                            tmem_ld32(t_lane + kTmU + 32 * part, x);
-                            tmem_wait_ld();
-                            scaled<16>(x, kDown * f, x);
-                            round_to<16>(x, hw);
-                            put32(smem + M::u, i, 4 * part, hw);
-                        }
-                        fence_proxy_async_smem();
-                        tc_fence_before();
-                        return named_bar_and(1, 256, here);
-                    };
-                    auto mul_l = [&] {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk),
-                                    idesc_f16(128, DK), p > 0 || kk > 0);
-                    };
-                    ok = put_u(down);
+                    const float down = kDown * power(max(below, kFar)), s_u = s_r * gates->s_t / down;
+                    if (here && !is_q) {
+                        f2 x[16];
+                        uint32_t hw[16];
+                        tmem_ld32(t_lane + kTmU + 32 * part, x);
+                        tmem_wait_ld();
+                        scaled<16>(x, down, x);
+                        round_to<16>(x, hw);
+                        put32(smem + M::u, i, 4 * part, hw);
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    ok = named_bar_and(1, 256, here);
                     if (!ok) break;
                     if (tid == 0) {
                         tc_fence_after();
@@ -688,10 +677,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
-                        if (below >= kFar) mul_l();
+                        if (below >= kFar || e_ul == kNone) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
+                                        begun || kk > 0);
+                            begun = true;
+                        }
                         mma_commit(bar_f);
                     }
-                    here = warp_wait(bar_f, fn++ & 1, a.status);
+                    here = warp_wait(bar_f, n & 1, a.status);
                     tc_fence_after();
                     if (here) {
                         const float f1 = (is_q ? er * s_dy : -er * s_dr) * s_s, fa = (is_q ? s_dy : -s_dr) * s_u;
@@ -709,17 +704,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) own[e] = fma2(fap, x[e], own[e]);
-                    }
-                    if (below < kFar) {  // U once more, for L
-                        ok = put_u(power(below));
-                        if (!ok) break;
-                        if (tid == 0) {
-                            tc_fence_after();
-                            mul_l();
-                            mma_commit(bar_f);
-                        }
-                        here = warp_wait(bar_f, fn++ & 1, a.status);
-                        tc_fence_after();
                     }
                     tc_fence_before();
                     ok = named_bar_and(1, 256, here);
@@ -783,7 +767,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 here = warp_wait(bar_w, hn & 1, a.status);
                 tc_fence_after();
                 if (here) {
-                    const float f1 = s_w * skq, g2 = wr * s_ul * gates->s_t / kDown;
+                    const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
+                    const float skq = gates->s_kq, f1 = s_w * skq;
+                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_t / kDown : 0.0f;
                     const f2 f1p = pair(f1, f1), g2p = pair(g2, g2);
                     f2 whole = 0, read = 0, end = 0, write = 0;  // dots with this row
 #pragma unroll
