@@ -975,7 +975,7 @@ ssm_status_t ssm_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const 
 /*
  * Bytes of what ssm_gated_delta_fwd keeps for ssm_gated_delta_bwd (0 for sizes it does not
  * take): per 64 steps and head the chunk's products of q, k and the gates, its entering
- * state and its steps' errors (104 KB at dstate = headdim = 128).
+ * state and its steps' errors (137 KB at dstate = headdim = 128).
  */
 size_t ssm_gated_delta_checkpoint_bytes(int batch, int seqlen, int nheads, int dstate,
                                         int headdim);
@@ -1013,7 +1013,9 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * fp32 sequences, and bf16 ones of up to 16 steps without checkpoints (a decode step: one),
  * are walked step by step in fp32 and need no workspace.  Others are taken in chunks of
  * 64 steps on the tensor cores; what enters their products beside q and k is held as the
- * sum of two bf16, so y and the state are within about 1e-5 (2-norm) of the definition.
+ * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y and
+ * the state are within about 1e-6 (2-norm) of the definition; what is far below the largest
+ * value of its tile is off by up to 2^-32 of that.
  * Runs are bit-equal.  Bounded waits report through ssm_last_device_status.
  */
 ssm_status_t ssm_gated_delta_fwd(const void* q, const void* k, const void* v, long long q_stride,
@@ -1047,10 +1049,10 @@ size_t ssm_gated_delta_bwd_workspace_bytes(int batch, int seqlen, int nheads, in
  * same buffer; checkpoints: what the forward kept for the same inputs, or NULL (the forward
  * runs again, in a workspace that much larger).
  * The gradients of a masked step (beta 0) with respect to k, v and beta are 0, and so is
- * dg where g is -inf.  A key may only be NaN where all heads of its group mask the step.
+ * dg where g is -inf.
  * The adjoint of the state, dv and dinitial_state are as exact as the forward; dq, dk, dg
- * and dbeta come from products of operands rounded to bf16 (summed in fp32): within about
- * 3e-3 (2-norm), as far as their own rounding to bf16.
+ * and dbeta come from products of operands rounded to one fp16 (summed in fp32): within
+ * about 5e-4 (2-norm), less than their own rounding to bf16.
  * Supported as ssm_gated_delta_fwd, in_dtype SSM_BF16.  Runs are bit-equal: sums over
  * heads and steps have a fixed order.
  */
@@ -1066,7 +1068,8 @@ ssm_status_t ssm_gated_delta_bwd(const void* q, const void* k, const void* v, lo
 
 /*
  * Waits for `stream` to drain, then returns the device-side status the last
- * ssm_scan_fwd (or ssm_linrec or ssm_vocab_ce call) that used `workspace` recorded (SSM_OK or SSM_ERR_TIMEOUT),
+ * ssm_scan_fwd (or ssm_linrec, ssm_vocab_ce or ssm_gated_delta call) that used `workspace`
+ * recorded (SSM_OK or SSM_ERR_TIMEOUT),
  * or SSM_ERR_CUDA if the stream itself reports an error.
  */
 ssm_status_t ssm_last_device_status(const void* workspace, void* stream);

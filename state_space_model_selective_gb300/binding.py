@@ -1502,7 +1502,7 @@ def _delta_args(q, k, v, g, beta, initial_state):
             raise ValueError(f"{name} must have 4 dims, got {t.dim()}")
     batch, seqlen, ngroups, dstate = q.shape
     nheads, headdim = v.shape[2], v.shape[3]
-    if (nheads % ngroups if ngroups else nheads) != 0:
+    if (nheads % ngroups or not nheads if ngroups else nheads):
         raise ValueError(f"nheads {nheads} must be a multiple of ngroups {ngroups}")
     sq = _token_step(q, "q", q.dtype, q.shape)
     sk = _token_step(k, "k", q.dtype, q.shape)

@@ -438,7 +438,7 @@ inline bool make_map(CUtensorMap* map, const void* base, int batch, int seqlen, 
 // Sizes as the entry points check them.
 inline bool sizes_ok(int batch, int seqlen, int heads, int groups, int dk, int dv) {
     return batch >= 0 && seqlen >= 0 && heads >= 0 && groups >= 0 && dk >= 1 && dv >= 1 &&
-           (groups == 0 ? heads == 0 : heads % groups == 0);
+           (groups == 0 ? heads == 0 : heads > 0 && heads % groups == 0);
 }
 inline bool sizes_fit(int batch, int seqlen, int heads, int dk, int dv) {
     return dk % 8 == 0 && dv % 8 == 0 && dk <= 128 && dv <= 256 && seqlen < (1 << 30) &&
