@@ -166,39 +166,46 @@ template <> struct Vec<1> { using T = float; };
 template <> struct Vec<2> { using T = float2; };
 template <> struct Vec<4> { using T = float4; };
 
-// Joins pairs of inverted blocks of N rows: of the lower left of [[X, 0], [L, Z]]^-1 =
-// -Z^-1 L X^-1, element (r, c .. c + V - 1) of the pair at (at, at).  In two steps, the
-// first product through `tmp` (rows of 36 floats, from `t0` on).
-template <int N, int V>
-__device__ __forceinline__ void join_blocks(float* m, float* tmp, int at, int t0, int r, int c) {
+// Joins pairs of inverted blocks of N rows: the lower left of [[X, 0], [L, Z]]^-1 is
+// -Z^-1 L X^-1.  In two steps, the first product through `tmp` (rows of 36 floats).  Warps
+// take four columns of the first, then four rows of the second, so that what is zero in
+// the triangles is left out by whole warps.
+template <int N>
+__device__ __forceinline__ void join_blocks(float* m, float* tmp, int warp, int lane) {
+    constexpr int V = N / 8, W = N / 4;  // columns to a lane, warps to a pair
     using T = typename Vec<V>::T;
+    const int w = warp % W, at = (warp / W) * 2 * N;
     const float* X = m + at * kPitch + at;
     const float* L = X + N * kPitch;
-    // s = sum_j sign * left[r][j] right[j][c ..]
-    auto product = [&](const float* left, const float* right, int pitch, float sign) {
-        float s[V];
+    float* t = tmp + (warp / W) * N * 36;
+    auto add = [](float* s, const float* left, const float* right, int pitch) {
+        const float4 l = *reinterpret_cast<const float4*>(left);
+        const float lv[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            const T x = *reinterpret_cast<const T*>(right + e * pitch);
+            const float* xv = reinterpret_cast<const float*>(&x);
 #pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(left + r * kPitch + j);
-            const float lv[4] = {sign * l.x, sign * l.y, sign * l.z, sign * l.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const T x = *reinterpret_cast<const T*>(right + (j + e) * pitch + c);
-                const float* xv = reinterpret_cast<const float*>(&x);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s[v] = fmaf(lv[e], xv[v], s[v]);
-            }
+            for (int v = 0; v < V; ++v) s[v] = fmaf(lv[e], xv[v], s[v]);
         }
-        T out;
-#pragma unroll
-        for (int v = 0; v < V; ++v) reinterpret_cast<float*>(&out)[v] = s[v];
-        return out;
     };
-    *reinterpret_cast<T*>(tmp + (t0 + r) * 36 + c) = product(L, X, kPitch, 1.0f);
+    {
+        float s[V] = {};
+        const int r = lane % N, c = 4 * w + (lane / N) * V;
+#pragma unroll 2
+        for (int j = 4 * w; j < N; j += 4) add(s, L + r * kPitch + j, X + j * kPitch + c, kPitch);
+        *reinterpret_cast<T*>(t + r * 36 + c) = *reinterpret_cast<const T*>(s);
+    }
     __syncthreads();
-    *reinterpret_cast<T*>(m + (at + N + r) * kPitch + at + c) = product(L + N, tmp + t0 * 36, 36, -1.0f);
+    {
+        float s[V] = {};
+        const int r = 4 * w + lane / 8, c = (lane % 8) * V;
+#pragma unroll 2
+        for (int j = 0; j <= 4 * w; j += 4) add(s, L + N + r * kPitch + j, t + j * 36 + c, 36);
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = -s[v];
+        *reinterpret_cast<T*>(m + (at + N + r) * kPitch + at + c) = *reinterpret_cast<const T*>(s);
+    }
     __syncthreads();
 }
 
@@ -229,9 +236,9 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
         for (int r = 0; r < 8; ++r) m[(b + r) * kPitch + b + c] = x[r];
     }
     __syncthreads();
-    join_blocks<8, 1>(m, tmp, (tid >> 6) * 16, (tid >> 6) * 8, (tid >> 3) & 7, tid & 7);
-    join_blocks<16, 2>(m, tmp, (tid >> 7) * 32, (tid >> 7) * 16, (tid >> 3) & 15, (tid & 7) * 2);
-    join_blocks<32, 4>(m, tmp, 0, 0, tid >> 3, (tid & 7) * 4);
+    join_blocks<8>(m, tmp, tid >> 5, tid & 31);
+    join_blocks<16>(m, tmp, tid >> 5, tid & 31);
+    join_blocks<32>(m, tmp, tid >> 5, tid & 31);
 }
 
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
@@ -251,7 +258,9 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     Gates* gates = reinterpret_cast<Gates*>(smem + M::gates);
     float* s_beta = reinterpret_cast<float*>(smem + M::misc);
     float* s_dec = s_beta + kC;                                   // [32]: decays to step 31
-    float* s_most = s_dec + 32;                                   // [2][8]
+    float* s_inv = s_dec + 32;                                    // [64]: inverse ones from 0 or 32
+    float* s_span = s_inv + kC;                                   // [2]: their largest logarithm
+    float* s_most = s_span + 4;                                   // [2][8]
     long long* s_sum = reinterpret_cast<long long*>(s_most + 16);
     uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
@@ -350,15 +359,15 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         in_phase ^= 1;
         landing = false;
         uint4 raw[NP * 4];
-        float most = 0.0f;
+        MostBf16 seen;
 #pragma unroll
         for (int e = 0; e < NP * 4; ++e) {
             const int at = tid + kRecThreads * e, r = (at >> 3) & 127;
             raw[e] = *reinterpret_cast<const uint4*>(smem + M::kq + at * 16);
             if (r < kC && (masked >> r & 1)) raw[e] = make_uint4(0, 0, 0, 0);
-            most = fmaxf(most, most8_bf16(raw[e]));
+            seen.see(raw[e]);
         }
-        most = warp_most(most);
+        float most = warp_most(seen.value());
         if (lane == 0) s_most[warp] = most;
         ok = __syncthreads_and(ok);
         float s_kq;
@@ -374,6 +383,12 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                 make_uint4(w[0], w[1], w[2], w[3]);
         }
         if (tid < 32) s_dec[tid] = decay(gates->hi[31], gates->lo[31], gates->hi[tid], gates->lo[tid]);
+        if (tid < kC) {
+            const float d = (gates->hi[tid & 32] - gates->hi[tid]) + (gates->lo[tid & 32] - gates->lo[tid]);
+            s_inv[tid] = ex2_approx(d);
+            const float span = warp_most(fabsf(d));  // (NaN is above all)
+            if (lane == 0) s_span[warp] = span;
+        }
         if (tid == 0) {
             gates->s_kq = s_kq;
             gates->e_max = fmaxf(s_most[8], s_most[9]);
@@ -406,6 +421,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             const float hi = gates->hi[i], lo = gates->lo[i];
             const float f = s_kq * s_kq * (is_q ? 1.0f : s_beta[i]);
             const int j0 = 32 * part;
+            const int last = is_q ? i : i - 1;  // of the columns that count
             if (part == 0 && (quarter & 1) && !grows) {
                 // rows behind 32, columns before it: the decay from step 31 to the row times
                 // that from the column to step 31, neither above 1
@@ -417,8 +433,22 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                     x[e] = mul2(x[e], mul2(e2, pair(d4.x, d4.y)));
                     x[e + 1] = mul2(x[e + 1], mul2(e2, pair(d4.z, d4.w)));
                 }
+            } else if ((quarter & 1) == part && s_span[part] < 60.0f) {
+                // a block on the diagonal whose decay fp32 holds: from its first step to the
+                // row, and inversely to the column
+                const float e_i = f * decay(hi, lo, gates->hi[j0], gates->lo[j0]);
+                const f2 e2 = pair(e_i, e_i);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const int j = j0 + 2 * e;
+                    const float4 d4 = *reinterpret_cast<const float4*>(s_inv + j);
+                    float a0, a1, a2, a3;
+                    unpair(mul2(x[e], mul2(e2, pair(d4.x, d4.y))), a0, a1);
+                    unpair(mul2(x[e + 1], mul2(e2, pair(d4.z, d4.w))), a2, a3);
+                    x[e] = pair(j <= last ? a0 : 0.0f, j + 1 <= last ? a1 : 0.0f);
+                    x[e + 1] = pair(j + 2 <= last ? a2 : 0.0f, j + 3 <= last ? a3 : 0.0f);
+                }
             } else {
-                const int last = is_q ? i : i - 1;  // of the columns that count
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
                     const int j = j0 + 2 * e;
@@ -437,13 +467,13 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                 }
             }
         }
+        most = warp_most_or_nan<16>(x);
+        if (lane == 0 && is_q) s_most[(quarter & 1) * 2 + part] = most;
         if (!is_q)
 #pragma unroll
             for (int e = 0; e < 16; e += 2)
                 *reinterpret_cast<ulonglong2*>(tri + i * kPitch + 32 * part + 2 * e) =
                     make_ulonglong2(x[e], x[e + 1]);
-        most = warp_most<16>(x);
-        if (lane == 0 && is_q) s_most[(quarter & 1) * 2 + part] = most;
         tc_fence_before();
         ok = __syncthreads_and(ok);
         float s_p;  // of the operand (Q K^T) D
@@ -821,13 +851,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             // of e |K|_1 over a row, in units of the largest S
             k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
             if (upper) {
-                float v = 0.0f;
+                MostBf16 seen;
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
 #pragma unroll
                 for (int p = 0; p < SC / 8; ++p)
-                    v = fmaxf(v, most8_bf16(*reinterpret_cast<const uint4*>(
-                                     tile + piece(i, (SC / 8) * part + p))));
-                v = warp_most(off ? 0.0f : v);
+                    seen.see(*reinterpret_cast<const uint4*>(tile + piece(i, (SC / 8) * part + p)));
+                const float v = warp_most(off ? 0.0f : seen.value());
                 if (lane == 0) post_most(s_most + 12 * (c & 1) + 8 + (quarter & 1) * 2 + part, v, c);
             }
             return in;
@@ -863,6 +892,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 const bool in = given && col0 + 2 * e < a.d.dv;
                 S[e] = pair(in ? at[0] : 0.0f, in ? at[a.d.dk] : 0.0f);
             }
+            drop_infinities<SC / 2>(S);
             const float m = warp_most<SC / 2>(S);
             if (lane == 0) s_first[warp] = m;
             named_bar_sync(1, 256);

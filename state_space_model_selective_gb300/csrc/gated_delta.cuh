@@ -187,6 +187,22 @@ __device__ __forceinline__ float warp_most(const f2* v) {
     }
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
+// Infinities become NaN, which largest values do not see: what is not finite does not take
+// the others' bits.
+template <int N>
+__device__ __forceinline__ void drop_infinities(f2* v) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = fma2(v[e], 0, v[e]);
+}
+template <int N>
+__device__ __forceinline__ float warp_most_or_nan(f2* v) {
+    float m = warp_most<N>(v);
+    if (m == __int_as_float(0x7f800000)) {
+        drop_infinities<N>(v);
+        m = warp_most<N>(v);
+    }
+    return m;
+}
 __device__ __forceinline__ float warp_most(float m) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
@@ -239,14 +255,21 @@ __device__ __forceinline__ void unpack8_f16(uint4 w, f2* f) {
         f[e] = pair(h.x, h.y);
     }
 }
-// The largest magnitude of 8 bf16.
-__device__ __forceinline__ float most8_bf16(uint4 w) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t m = 0;  // magnitudes compare as integers
+// The largest finite magnitude of bf16, two at a time.  Magnitudes compare as integers, and
+// with the least exponent added infinities and NaN are negative ones: a value that is not
+// finite does not take the others' bits.
+struct MostBf16 {
+    uint32_t m = 0x00800080u;
+    __device__ __forceinline__ void see(uint4 w) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = max(m, max((u[e] & 0x7fffu) << 16, u[e] & 0x7fff0000u));
-    return __uint_as_float(m);
-}
+        for (int e = 0; e < 4; ++e)
+            asm("max.s16x2 %0, %0, %1;" : "+r"(m) : "r"((u[e] & 0x7fff7fffu) + 0x00800080u));
+    }
+    __device__ __forceinline__ float value() const {
+        return __uint_as_float((max(m >> 16, m & 0xffffu) - 0x80u) << 16);
+    }
+};
 // 8 pairs to 16 consecutive elements whose address is a multiple of 32 bytes (a whole sector
 // of bf16 to a lane).
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const f2* o) {

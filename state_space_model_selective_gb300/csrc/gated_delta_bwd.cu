@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         // (upper warps) dY and e dY of step `it` as operands, dY kept
         auto put_dy = [&](int it, float e) {
             f2 x[16], y[16];
-            float m = 0.0f;
+            MostBf16 seen;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                m = fmaxf(m, most8_bf16(dy[p]));
+                seen.see(dy[p]);
                 unpack8_bf16(dy[p], x + 4 * p);
             }
-            m = warp_most(m);
+            const float m = warp_most(seen.value());
             uint32_t* most = s_most + 12 * (it & 1) + 8;
             if (lane == 0) post_most(most + (quarter & 1) * 2 + part, m, it);
             float all = 0.0f;
@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             return told;
         };
         {   // the last chunk: its largest values are measured
+            drop_infinities<16>(L);
             const float m = warp_most<16>(L);
             if (lane == 0) s_first[warp] = m;
             named_bar_sync(1, 256);
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                             own[e + 1] = mul2(own[e + 1], pair(d2, d3));
                         }
                     }
-                    const float most = warp_most<16>(own);
+                    const float most = warp_most_or_nan<16>(own);
                     if (lane == 0) s_most[warp] = most;
                 }
 #pragma unroll

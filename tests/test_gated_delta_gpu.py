@@ -444,3 +444,39 @@ def test_columns_that_later_steps_do_not_read(dv):
         t["dy"][:, 64:, :, dv // 2:] *= far
         t["dfinal"][:, :, dv // 2:] *= far
         check_grads(backward(cuda(t), grad_dtype=F32), reference_grads(t), F32, F32)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_reach_their_own_columns(bad):
+    """A v that is not finite spoils its column of headdim from its chunk on, a state's or a
+    gradient's its column, a q its own y: nothing else, to the same tolerances."""
+    t = inputs(1, 200, 2, 2, 64, 128, seed=19)
+    y_ref, last_ref = reference(t)
+    ref = reference_grads(t)
+    keep = [c for c in range(128) if c not in (5, 77)]
+
+    s = {k: None if v is None else v.clone() for k, v in t.items()}
+    s["beta"][0, 70] = t["beta"][0, 70] = 0.5
+    y_ref, last_ref = reference(t)
+    ref = reference_grads(t)
+    s["v"][0, 70, 0, 5] = bad
+    s["state"][0, 1, 77, 3] = bad
+    s["q"][0, 130, 1, 2] = bad
+    s["q"][0, 199, 0] = bad
+    y, last = forward(cuda(s), out_dtype=F32)
+    rows = [i for i in range(200) if i not in (130, 199)]
+    assert off(y[:, rows][..., keep], y_ref[:, rows][..., keep]) < FWD
+    assert off(last[:, :, keep], last_ref[:, :, keep]) < FWD
+    assert off(y[:, :64, 0], y_ref[:, :64, 0]) < FWD  # the chunk before
+    assert not torch.isfinite(y[0, 70:, 0, 5]).any() and not torch.isfinite(last[0, 0, 5]).any()
+    assert not torch.isfinite(y[0, 130, 1]).any() and not torch.isfinite(y[0, 199, 0]).any()
+
+    s = {k: None if v is None else v.clone() for k, v in t.items()}
+    s["dy"][0, 100, 0, 5] = bad
+    s["dfinal"][0, 1, 77, 3] = bad
+    g = backward(cuda(s), grad_dtype=F32)
+    assert off(g["dv"][..., keep], ref["dv"][..., keep]) < FWD
+    assert off(g["dinitial_state"][:, :, keep], ref["dinitial_state"][:, :, keep]) < FWD
+    assert off(g["dq"][:, 128:, 0], ref["dq"][:, 128:, 0]) < BWD  # the chunks behind
+    assert not torch.isfinite(g["dq"][0, 100, 0]).any()
+    assert not torch.isfinite(g["dk"][0, 60, 0]).any()
