@@ -155,6 +155,7 @@ struct RecArgs {
     const void *g, *beta;
     uint8_t* records;
     uint32_t* status;
+    uint32_t* flags;  // of chunks and heads whose records are in memory, or NULL
     Dims d;
     unsigned count;   // of chunks and heads
     int gates_bf16;
@@ -196,7 +197,7 @@ __device__ __forceinline__ void join_blocks(float* m, float* tmp, int warp, int 
         for (int j = 4 * w; j < N; j += 4) add(s, L + r * kPitch + j, X + j * kPitch + c, kPitch);
         *reinterpret_cast<T*>(t + r * 36 + c) = *reinterpret_cast<const T*>(s);
     }
-    __syncthreads();
+    named_bar_sync(1, kRecThreads);
     {
         float s[V] = {};
         const int r = 4 * w + lane / 8, c = (lane % 8) * V;
@@ -206,7 +207,7 @@ __device__ __forceinline__ void join_blocks(float* m, float* tmp, int warp, int 
         for (int v = 0; v < V; ++v) s[v] = -s[v];
         *reinterpret_cast<T*>(m + (at + N + r) * kPitch + at + c) = *reinterpret_cast<const T*>(s);
     }
-    __syncthreads();
+    named_bar_sync(1, kRecThreads);
 }
 
 // T = (1 + A)^-1 in place, A strictly lower 64 x 64 (zeros above).  The eight 8 x 8
@@ -235,7 +236,7 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
 #pragma unroll
         for (int r = 0; r < 8; ++r) m[(b + r) * kPitch + b + c] = x[r];
     }
-    __syncthreads();
+    named_bar_sync(1, kRecThreads);
     join_blocks<8>(m, tmp, tid >> 5, tid & 31);
     join_blocks<16>(m, tmp, tid >> 5, tid & 31);
     join_blocks<32>(m, tmp, tid >> 5, tid & 31);
@@ -243,15 +244,20 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
 
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
 // this one's H and P leave.
-template <int DK>
-__global__ void __launch_bounds__(kRecThreads, 2)
-    records_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const RecArgs a) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+//
+// LO: P's lo part is wanted, and T' for it as hi + lo (y in fp32, or a gradient will read it).
+// For y in bf16, whose own rounding is 2^-9, P only enters as one fp16, as do then its factors.
+//
+// The work of eight warps: the items `first`, first + step, ...  With flags they are told one
+// by one, and go through the chunks of all heads side by side.
+template <int DK, bool LO, bool FLAGS>
+__device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                             const RecArgs& a, uint8_t* smem, uint32_t tmem,
+                                             unsigned first, unsigned step) {
     using M = RecSmem<DK>;
     constexpr int NP = DK / 64;
     // tensor memory: [K; Q] K^T, then H (hi and lo columns); P (hi and lo columns)
-    constexpr uint32_t kTmX = 0, kTmH = 0, kTmP = 128, kTmCols = 256;
+    constexpr uint32_t kTmX = 0, kTmH = 0, kTmP = 128;
     const uint32_t sb = smem_u32(smem);
     float* tri = reinterpret_cast<float*>(smem + M::tri);
     float* tmp = reinterpret_cast<float*>(smem + M::tmp);
@@ -265,13 +271,16 @@ __global__ void __launch_bounds__(kRecThreads, 2)
     uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
     uint64_t* bar_mma = bar_in + 1;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bar_mma + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane, i = row & 63;
     const bool is_q = row >= kC;
 
     const unsigned chunks = a.d.chunks, heads = a.d.heads, ratio = heads / a.d.groups;
+    const unsigned all_heads = heads * a.d.batch;
+    auto chunk_of = [&](unsigned item) {
+        return FLAGS ? (item % all_heads) * chunks + item / all_heads : item;
+    };
     auto load = [&](unsigned ch) {  // K and Q of a chunk (one thread)
         const unsigned bh = ch / chunks, b = bh / heads;
         const int t0 = (int)(ch - bh * chunks) * kC, group = (int)((bh - b * heads) / ratio);
@@ -291,26 +300,30 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
         beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
     };
-    if (blockIdx.x < a.count) fetch(blockIdx.x);
-    if (warp == 0) tmem_alloc(s_tmem, kTmCols);
+    if (first < a.count) fetch(chunk_of(first));
     if (tid == 0) {
         mbar_init(bar_in, 1);
         mbar_init(bar_mma, 1);
         fence_mbar_init();
-        if (blockIdx.x < a.count) load(blockIdx.x);
+        if (first < a.count) load(chunk_of(first));
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    named_bar_sync(1, kRecThreads);
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     bool ok = true;
     bool landing = false;  // (thread 0) a load is on its way
     uint32_t mma_phase = 0, in_phase = 0;
 
-    for (unsigned ch = blockIdx.x; ch < a.count && ok; ch += gridDim.x) {
+    // (thread 0) what went out before is in memory: told to the chains
+    auto tell = [&](unsigned ch) {
+        bulk_wait_all();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        st_release_gpu(a.flags + ch, 1u);
+    };
+    unsigned before = 0;
+    for (unsigned item = first; item < a.count && ok; item += step) {
+        const unsigned ch = chunk_of(item);
         uint8_t* rec = a.records + (size_t)ch * rec_bytes(DK);
-        const bool more = ch + gridDim.x < a.count;
+        const bool more = step < a.count - item;
         // ---- the gates: base-2 logarithms summed as integers of 2^-32, so that differences
         // of far sums are as exact as near ones (a decay of 2^-300 and less is 0 all the same)
         long long sum = 0;
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             if (tid == 31) *s_sum = sum;
         }
         if (tid == 0) bulk_wait_read_all();  // the last chunk's stores have left shared memory
-        __syncthreads();
+        named_bar_sync(1, kRecThreads);
         const unsigned long long masked = (unsigned long long)s_flags[1] << 32 | s_flags[0];
         const bool grows = s_flags[4] | s_flags[5];
         if (tid < kC) {
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             const float m = warp_most(e);
             if (lane == 0) s_most[8 + warp] = m;
         }
-        if (more) fetch(ch + gridDim.x);
+        if (more) fetch(chunk_of(item + step));
 
         // ---- K and Q to fp16, in place, under one factor.  Steps that learn nothing: their
         // keys are not looked at
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         }
         float most = warp_most(seen.value());
         if (lane == 0) s_most[warp] = most;
-        ok = __syncthreads_and(ok);
+        ok = named_bar_and(1, kRecThreads, ok);
         float s_kq;
         const float kq_scale = tile_scale(most_of<8>(s_most), kTop, s_kq);
 #pragma unroll
@@ -394,10 +407,12 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             gates->e_max = fmaxf(s_most[8], s_most[9]);
         }
         fence_proxy_async_smem();
-        __syncthreads();
+        named_bar_sync(1, kRecThreads);
 
         // ---- [K; Q] K^T
         if (tid == 0 && ok) {
+            if (FLAGS && item != first) tell(before);
+            before = ch;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < DK / 16; ++kk)
@@ -475,15 +490,19 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                 *reinterpret_cast<ulonglong2*>(tri + i * kPitch + 32 * part + 2 * e) =
                     make_ulonglong2(x[e], x[e + 1]);
         tc_fence_before();
-        ok = __syncthreads_and(ok);
+        ok = named_bar_and(1, kRecThreads, ok);
         float s_p;  // of the operand (Q K^T) D
         const float p_scale = tile_scale(most_of<4>(s_most), kTop, s_p);
         uint32_t hw[16], lw[16];
         if (is_q) {
             scaled<16>(x, p_scale, x);
-            split<16>(x, hw, lw);
+            if constexpr (LO) {
+                split<16>(x, hw, lw);
+                put32(smem + M::p_lo, i, 4 * part, lw);
+            } else {
+                round_to<16>(x, hw);
+            }
             put32(smem + M::p_hi, i, 4 * part, hw);
-            put32(smem + M::p_lo, i, 4 * part, lw);
         }
         invert_unit_lower(tri, tmp, tid);
 
@@ -506,13 +525,14 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                 s_most[warp] = mt;
                 s_most[8 + warp] = mw;
             }
-            __syncthreads();  // (the triangle has been read)
+            named_bar_sync(1, kRecThreads);  // (the triangle has been read)
             const float t_scale = tile_scale(most_of<8>(s_most), kTop, s_t);
             const float w_scale = tile_scale(most_of<8>(s_most + 8), kTop, s_w);
             uint32_t th[8], tl[8], wh[8], wl[8];
             scaled<8>(t, t_scale, t);
             scaled<8>(wt, w_scale, wt);
-            split<8>(t, th, tl);
+            if constexpr (LO) split<8>(t, th, tl);
+            else round_to<8>(t, th);
             split<8>(wt, wh, wl);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -522,14 +542,14 @@ __global__ void __launch_bounds__(kRecThreads, 2)
                         make_uint4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
                 };
                 put(M::t_hi, th);
-                put(M::t_lo, tl);
+                if constexpr (LO) put(M::t_lo, tl);
                 put(M::w_hi, wh);
                 put(M::w_lo, wl);
             }
             if (tid == 0) gates->s_t = s_t;
         }
         fence_proxy_async_smem();
-        __syncthreads();
+        named_bar_sync(1, kRecThreads);
 
         // ---- H = K^T diag(w) T' (rows of dstate) and P T' (rows 64 to 127: the tile of 128
         // rows starts one tile early, its first half is not read); columns 64 to 127: the
@@ -547,11 +567,12 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_hi - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
-                        idP, kk > 0);
+                        LO ? idP : idP64, kk > 0);
+            if constexpr (LO)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
-                        idP64, 1);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
+                            idP64, 1);
             mma_commit(bar_mma);
             if (a.keep_t) {
                 bulk_store(rec + rec_t(DK), smem + M::t_hi, kTile);
@@ -563,34 +584,43 @@ __global__ void __launch_bounds__(kRecThreads, 2)
         tc_fence_after();
         if (tid == 0 && ok) {
             bulk_wait_read_all();   // K, Q and T' have left
-            if (more) load(ch + gridDim.x);
+            if (more) load(chunk_of(item + step));
             landing = more;
         }
-        f2 hx[16], px[16];
+        auto both = [&](uint32_t at, f2* v) {  // columns of the hi and the lo part
+#pragma unroll
+            for (int e0 = 0; e0 < 16; e0 += 8) {
+                f2 y[8];
+                tmem_ld16(t_lane + at + 2 * e0, v + e0);
+                tmem_ld16(t_lane + at + 64 + 2 * e0, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e0 + e] = add2(v[e0 + e], y[e]);
+            }
+        };
+        // (P is read once more for its operand: with both parts of it and of H a thread has no
+        // registers to keep it)
+        auto p_row = [&](f2* v) {
+            if constexpr (LO) {
+                both(kTmP + 32 * part, v);
+            } else {
+                tmem_ld32(t_lane + kTmP + 32 * part, v);
+                tmem_wait_ld();
+            }
+        };
+        f2 px[16], hx[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) hx[e] = px[e] = 0;
-        if (ok) {
-            auto both = [&](uint32_t at, f2* v) {  // columns of the hi and the lo part
-#pragma unroll
-                for (int e0 = 0; e0 < 16; e0 += 8) {
-                    f2 y[8];
-                    tmem_ld16(t_lane + at + 2 * e0, v + e0);
-                    tmem_ld16(t_lane + at + 64 + 2 * e0, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e0 + e] = add2(v[e0 + e], y[e]);
-                }
-            };
-            if (row < DK) both(kTmH + 32 * part, hx);
-            if (is_q) both(kTmP + 32 * part, px);
-        }
-        const float mh = warp_most<16>(hx), mp = warp_most<16>(px);
+        if (ok && is_q) p_row(px);
+        const float mp = warp_most<16>(px);
+        if (ok && row < DK) both(kTmH + 32 * part, hx);
+        const float mh = warp_most<16>(hx);
         if (lane == 0) {
             s_most[warp] = mh;
             s_most[8 + warp] = mp;
         }
         tc_fence_before();
-        ok = __syncthreads_and(ok);
+        ok = named_bar_and(1, kRecThreads, ok);
         if (!ok) break;
         float s_h2, s_p2;
         const float h_scale = tile_scale(most_of<8>(s_most), kTop, s_h2);
@@ -602,37 +632,65 @@ __global__ void __launch_bounds__(kRecThreads, 2)
             put32(smem + M::t_hi + h_bytes(DK), row, 4 * part, lw);
         }
         if (is_q) {
+            if constexpr (LO) p_row(px);
             scaled<16>(px, p2_scale, px);
-            split<16>(px, hw, lw);
+            if constexpr (LO) {
+                split<16>(px, hw, lw);
+                put32(smem + M::p_lo, i, 4 * part, lw);
+            } else {
+                round_to<16>(px, hw);
+            }
             put32(smem + M::p_hi, i, 4 * part, hw);
-            put32(smem + M::p_lo, i, 4 * part, lw);
         }
+        if constexpr (LO) tc_fence_before();
         if (tid == 0) {
             gates->s_h = s_h2 * s_kq * s_w;
             gates->s_p = s_p2 * s_p * s_t;
         }
         fence_proxy_async_smem();
-        __syncthreads();
+        named_bar_sync(1, kRecThreads);
         if (tid == 0) {
             bulk_store(rec, smem + M::gates, kGateBytes);
             bulk_store(rec + rec_h(DK), smem + M::t_hi, 2 * h_bytes(DK));
-            bulk_store(rec + rec_p(DK), smem + M::p_hi, 2 * kTile);
+            bulk_store(rec + rec_p(DK), smem + M::p_hi, (LO ? 2 : 1) * kTile);
             bulk_commit();
         }
     }
     if (tid == 0) {
         bulk_wait_all();
+        if (FLAGS && ok && first < a.count) tell(before);
         if (landing) (void)mbar_wait(bar_in, in_phase, a.status);  // never leave with one landing
     }
+}
+
+// The eight warps' tensor memory, allocated and given back around `work`.
+template <uint32_t COLS, typename F>
+__device__ __forceinline__ void with_tmem(uint32_t* place, int warp, F&& work) {
+    if ((threadIdx.x >> 5) == warp) tmem_alloc(place, COLS);
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, kTmCols);
+    tc_fence_after();
+    const uint32_t tmem = *place;
+    work(tmem);
+    tc_fence_before();
+    __syncthreads();
+    if ((threadIdx.x >> 5) == warp) tmem_dealloc(tmem, COLS);
+}
+
+template <int DK, bool LO>
+__global__ void __launch_bounds__(kRecThreads, 2)
+    records_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const RecArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    with_tmem<256>(reinterpret_cast<uint32_t*>(smem + RecSmem<DK>::bytes - 8), 0, [&](uint32_t tmem) {
+        make_records<DK, LO, false>(tm_q, tm_k, a, smem, tmem, blockIdx.x, gridDim.x);
+    });
 }
 
 // ------------------------------------------------------------------ chain
 
-// 8 warps on rows, one that multiplies and one that loads (a copy takes its issuer some 100
-// cycles, and a chunk has a dozen), two idle
+// 8 warps on rows, one that multiplies, one that loads (a copy takes its issuer some 100
+// cycles, and a chunk has a dozen), one that looks for records, one idle
 constexpr int kChainThreads = kSplitThreads;
 
 // PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
@@ -664,6 +722,7 @@ struct ChainArgs {
     float* last;
     void* y;
     uint32_t* status;
+    const uint32_t* flags;  // of records that are being made meanwhile, or NULL
     Dims d;       // pans: panels of PW columns
 };
 
@@ -679,16 +738,15 @@ struct ChainArgs {
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
 // |S1| <= e_63 |S| + |H|_1 |R|, with the measured maxima of V and S, found while products
 // run.  A bound 2^20 too large would still leave 20 bits.
-template <int DK, int PW, typename TO>
-__global__ void __launch_bounds__(kChainThreads, 1)
-    chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+template <int DK, int PW, typename TO, bool FLAGS>
+__device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainArgs& a, uint8_t* smem,
+                                          uint32_t tmem, unsigned index) {
     constexpr bool PLO = sizeof(TO) == 4;
     using M = ChainSmem<DK, PW, PLO>;
     constexpr int NP = DK / 64;
     constexpr int SC = PW / 2, RC = PW / 4;  // columns of S and of R to a thread
     // tensor memory, hi and lo columns each: K S0, H R, Q S0, P R
-    constexpr uint32_t kTmX = 0, kTmH = 128, kTmQ = 256, kTmY = 384, kTmCols = 512;
+    constexpr uint32_t kTmX = 0, kTmH = 128, kTmQ = 256, kTmY = 384;
     const uint32_t sb = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // a stage has come in
     uint64_t* full_h = full + 2;  // H has
@@ -700,27 +758,25 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_o = full + 8;   // Q S0 and P R have been read
     uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][8 warps of S0, 4 of V]
     float* s_first = reinterpret_cast<float*>(s_most + 24);     // [8]: of the first S0
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + 8);
+    uint32_t* s_made = reinterpret_cast<uint32_t*>(s_first + 8);  // records known to be in memory
+    constexpr uint32_t kNotMade = 0xffffffffu;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int pan = blockIdx.x % a.d.pans;
-    const long long bh = blockIdx.x / a.d.pans;
+    const int pan = index % a.d.pans;
+    const long long bh = index / a.d.pans;
     const int b = (int)(bh / a.d.heads), h = (int)(bh % a.d.heads);
     const int nc = a.d.chunks;
 
-    if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
         for (int n = 0; n < 6; ++n) mbar_init(full + n, n == 2 ? 2 : 1);
         mbar_init(bar_s, 8);
         mbar_init(bar_r, 8);
         mbar_init(bar_o, 4);
         for (int n = 0; n < 24; ++n) s_most[n] = 0;
+        *s_made = 0;
         fence_mbar_init();
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
 
     if (warp >= 8) {
         give_registers();
@@ -784,6 +840,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         } else if (warp == 9 && lane == 0) {
             const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             int loads = 0, h_loads = 0;
+            // a record that is being made at the same time: false when that takes too long
+            auto made = [&](int c) {
+                if constexpr (FLAGS) {
+                    const uint32_t addr = smem_u32(s_made);
+                    for (uint32_t tries = 0; tries < (1u << 27); ++tries) {
+                        uint32_t n;
+                        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(addr) : "memory");
+                        if (n == kNotMade) return false;
+                        if (n > (uint32_t)c) return true;
+                    }
+                    record_status(a.status, SSM_ERR_TIMEOUT);
+                    return false;
+                }
+                return true;
+            };
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
                 uint64_t* bar = full + (c & 1);
@@ -807,21 +878,43 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             };
             // H counts as in once the chunk before is known to be done too, so that no barrier
             // is ever a whole turn ahead of this thread
-            load(0);
-            load_h(0);
-            mbar_arrive(full_h);
-            if (nc > 1) load(1);
-            for (int c = 0; c + 1 < nc; ++c) {
+            bool here = made(0);
+            if (here) {
+                load(0);
+                load_h(0);
+                mbar_arrive(full_h);
+                here = nc == 1 || made(1);
+                if (here && nc > 1) load(1);
+            }
+            for (int c = 0; c + 1 < nc && here; ++c) {
                 if (!mbar_wait(bar_h, c & 1, a.status)) break;
                 load_h(c + 1);
                 if (!mbar_wait(bar_y, c & 1, a.status)) break;
                 mbar_arrive(full_h);
-                if (c + 2 < nc) load(c + 2);
+                if (c + 2 < nc) {
+                    here = made(c + 2);
+                    if (here) load(c + 2);
+                }
             }
             // never leave with a load still landing
             for (int c = max(0, loads - 2); c < loads; ++c)
                 (void)mbar_wait(full + (c & 1), (c >> 1) & 1, a.status);
-            (void)mbar_wait(full_h, (h_loads - 1) & 1, a.status);
+            if (h_loads > 0) (void)mbar_wait(full_h, (h_loads - 1) & 1, a.status);
+        } else if (FLAGS && warp == 10 && lane == 0) {
+            // Looks for records that are being made, ahead of the loads: a look takes most of a
+            // microsecond
+            const uint32_t addr = smem_u32(s_made);
+            for (int c = 0; c < nc; ++c) {
+                uint32_t tries = 0;
+                while (ld_acquire_gpu(a.flags + bh * nc + c) == 0 && ++tries < kFlagSpinLimit) {}
+                const bool there = tries < kFlagSpinLimit;
+                if (!there) record_status(a.status, SSM_ERR_TIMEOUT);
+                asm volatile("fence.proxy.async;" ::: "memory");
+                asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr),
+                             "r"(there ? (uint32_t)c + 1 : kNotMade)
+                             : "memory");
+                if (!there) break;
+            }
         }
     } else {
         take_registers();
@@ -1004,9 +1097,43 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                     at[a.d.dk] = v1 * s_s;
                 }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, kTmCols);
+}
+
+template <int DK, int PW, typename TO>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
+    with_tmem<512>(reinterpret_cast<uint32_t*>(smem + bytes - 8), 8, [&](uint32_t tmem) {
+        run_chain<DK, PW, TO, false>(tm_v, a, smem, tmem, blockIdx.x);
+    });
+}
+
+// Records and chains at once, for chains so few that they leave SMs idle: CTAs take numbers,
+// the first `makers` make records, chunk by chunk of all heads, and tell the others, which
+// follow.  A chain only waits for CTAs with lower numbers, which have started and wait for
+// nothing.
+template <int DK, typename TO>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    both_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const RecArgs r, const ChainArgs a,
+                uint32_t* ticket, unsigned makers) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t bytes = ChainSmem<DK, 32, sizeof(TO) == 4>::bytes;
+    static_assert(RecSmem<DK>::bytes <= bytes, "records' place");
+    uint32_t* place = reinterpret_cast<uint32_t*>(smem + bytes - 8);
+    if (threadIdx.x == 0) place[1] = atomicAdd(ticket, 1u);
+    with_tmem<512>(place, 8, [&](uint32_t tmem) {
+        const unsigned number = place[1];
+        if (number >= makers) {
+            run_chain<DK, 32, TO, true>(tm_v, a, smem, tmem, number - makers);
+        } else if (threadIdx.x < kRecThreads) {
+            take_registers();
+            make_records<DK, sizeof(TO) == 4, true>(tm_q, tm_k, r, smem, tmem, number, makers);
+        } else {
+            give_registers();
+        }
+    });
 }
 
 // ------------------------------------------------------------------- host
@@ -1033,9 +1160,6 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     r.gates_bf16 = f.gate_dtype == SSM_BF16;
     r.keep_t = f.kept != nullptr;
     r.count = (unsigned)((long long)f.batch * f.heads * d.chunks);
-    if (!allow_smem(records_kernel<DK>, RecSmem<DK>::bytes)) return SSM_ERR_CUDA;
-    records_kernel<DK><<<std::min<unsigned>(r.count, 2 * sms), kRecThreads,
-                         RecSmem<DK>::bytes, s>>>(mq, mk, r);
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;
     a.y = f.y; a.status = f.status; a.d = d;
@@ -1045,6 +1169,34 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     const long long wide = bh * d.pans, narrow = bh * ((f.dv + 31) / 32);
     const bool half = !f.kept && 7 * ((narrow + sms - 1) / sms) < 10 * ((wide + sms - 1) / sms);
     if (half) a.d.pans = (f.dv + 31) / 32;
+    // Where these leave SMs idle, the records are made on those meanwhile: 3.5 SMs to a head keep
+    // up with its chains (8192 steps at headdim 128, one after the other against at once: 16
+    // heads 295 and 260 us, 20 heads, 3.6 SMs to each, 305 and 290 us, 22, 2.9 to each, 314 and 361 us)
+    const long long makers = sms - narrow;
+    if (half && f.flags && 2 * makers >= 7 * bh) {
+        if (cudaMemsetAsync(f.flags, 0, (r.count + 1) * 4ull, s) != cudaSuccess) return SSM_ERR_CUDA;
+        r.flags = f.flags + 1;
+        a.flags = f.flags + 1;
+        auto both = [&](auto to) {
+            using TO = decltype(to);
+            constexpr uint32_t bytes = ChainSmem<DK, 32, sizeof(TO) == 4>::bytes;
+            if (!allow_smem(both_kernel<DK, TO>, bytes)) return false;
+            both_kernel<DK, TO><<<(unsigned)sms, kChainThreads, bytes, s>>>(mq, mk, mv, r, a, f.flags,
+                                                                         (unsigned)makers);
+            return true;
+        };
+        if (!(f.out_dtype == SSM_F32 ? both(float{}) : both(__nv_bfloat16{}))) return SSM_ERR_CUDA;
+        return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+    }
+    auto make = [&](auto lo) {
+        constexpr bool LO = decltype(lo)::value;
+        if (!allow_smem(records_kernel<DK, LO>, RecSmem<DK>::bytes)) return false;
+        records_kernel<DK, LO><<<std::min<unsigned>(r.count, 2 * sms), kRecThreads,
+                                 RecSmem<DK>::bytes, s>>>(mq, mk, r);
+        return true;
+    };
+    if (!(f.kept || f.out_dtype == SSM_F32 ? make(std::true_type{}) : make(std::false_type{})))
+        return SSM_ERR_CUDA;
     const unsigned grid = (unsigned)(half ? narrow : wide);
     auto go = [&](auto pw, auto to) {
         constexpr int PW = decltype(pw)::value;
@@ -1109,7 +1261,7 @@ extern "C" size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nhe
     if (!sizes_ok(batch, seqlen, nheads, nheads, dstate, headdim) ||
         !sizes_fit(batch, seqlen, nheads, dstate, headdim))
         return 0;
-    return 1024 + records_bytes(batch, seqlen, nheads, dstate);
+    return 1024 + flags_bytes(batch, seqlen, nheads) + records_bytes(batch, seqlen, nheads, dstate);
 }
 
 extern "C" ssm_status_t ssm_gated_delta_fwd(
@@ -1183,7 +1335,9 @@ extern "C" ssm_status_t ssm_gated_delta_fwd(
     f.y = y; f.out_dtype = out_dtype; f.final_state = final_state;
     f.status = reinterpret_cast<uint32_t*>(ws) + 1;
     f.batch = batch; f.seqlen = seqlen; f.heads = nheads; f.groups = ngroups; f.dk = dstate; f.dv = headdim;
-    f.records = checkpoints ? static_cast<uint8_t*>(checkpoints) : ws + 1024;
+    f.flags = checkpoints ? nullptr : reinterpret_cast<uint32_t*>(ws + 1024);
+    f.records = checkpoints ? static_cast<uint8_t*>(checkpoints)
+                            : ws + 1024 + gdn_host::flags_bytes(batch, seqlen, nheads);
     f.kept = checkpoints ? f.records + gdn_host::records_bytes(batch, seqlen, nheads, dstate) : nullptr;
     return gdn_internal::chunked_forward(f, s);
 }

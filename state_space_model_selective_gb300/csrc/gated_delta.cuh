@@ -472,6 +472,10 @@ inline int dk_tile(int dk) { return dk <= 64 ? 64 : 128; }
 inline size_t chunk_count(int batch, int seqlen, int heads) {
     return (size_t)batch * heads * (((size_t)seqlen + gdn::kC - 1) / gdn::kC);
 }
+// A word for each record, and one more
+inline size_t flags_bytes(int batch, int seqlen, int heads) {
+    return ((chunk_count(batch, seqlen, heads) + 1) * 4 + 1023) / 1024 * 1024;
+}
 inline size_t records_bytes(int batch, int seqlen, int heads, int dk) {
     return chunk_count(batch, seqlen, heads) * gdn::rec_bytes(dk_tile(dk));
 }
@@ -507,6 +511,7 @@ struct Forward {
     uint8_t* records;
     uint8_t* kept;       // NULL: nothing is kept
     uint32_t* status;
+    uint32_t* flags;     // flags_bytes, or NULL
     int batch, seqlen, heads, groups, dk, dv;
 };
 ssm_status_t chunked_forward(const Forward& f, cudaStream_t stream);
