@@ -109,14 +109,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // N pairs as hi + lo.
 template <int N>
 __device__ __forceinline__ void split(const f2* x, uint32_t* hi, uint32_t* lo) {
-    const f2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         float a, b;
         unpair(x[e], a, b);
         hi[e] = pack_f16(a, b);
-        const float2 h = unpack_f16(hi[e]);
-        unpair(fma2(pair(h.x, h.y), minus, x[e]), a, b);
+        asm("{\n\t.reg .b16 p, q, m;\n\t"
+            "mov.b32 {p, q}, %2;\n\t"
+            "mov.b16 m, 0xbc00;\n\t"  // -1
+            "fma.rn.f32.f16 %0, p, m, %0;\n\t"
+            "fma.rn.f32.f16 %1, q, m, %1;\n\t}"
+            : "+f"(a), "+f"(b)
+            : "r"(hi[e]));
         lo[e] = pack_f16(a, b);
     }
 }
@@ -183,7 +187,7 @@ __device__ __forceinline__ float warp_most(const f2* v) {
     for (int e = 0; e < N; ++e) {
         float a, b;
         unpair(v[e], a, b);
-        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+        asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
     }
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
