@@ -713,6 +713,7 @@ template <int DK, int PW, bool PLO> struct ChainSmem {
     static constexpr uint32_t r_bytes = (PW / 32) * kTile;
     static constexpr uint32_t misc = r + r_bytes;
     static constexpr uint32_t bytes = misc + 512;
+    static_assert(bytes <= 227 * 1024, "shared memory");
 };
 
 struct ChainArgs {
@@ -1043,7 +1044,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             ok = warp_wait(bar_h, ph, a.status) && ok;
             if (!ok) break;
             tc_fence_after();
-            {
+            if (DK == 128 || !upper) {  // (with 64 rows, what is in the other lanes is no state)
                 f2 z[SC / 2], y[SC / 2];
                 tmem_cols<SC>(t_lane + kTmH + SC * part, z);
                 tmem_cols<SC>(t_lane + kTmH + PW + SC * part, y);

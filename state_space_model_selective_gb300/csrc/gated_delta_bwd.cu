@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             scaled<16>(L, ee * s_l * next, L);
             s_l = s_next;
             auto add = [&](uint32_t at, float factor) {
+                // (with 64 rows, what is in the other lanes is no adjoint)
+                if (DK == 64 && upper) return;
                 const f2 f = pair(factor, factor);
 #pragma unroll
                 for (int e0 = 0; e0 < 16; e0 += 8) {

@@ -480,3 +480,18 @@ def test_values_that_are_not_finite_reach_their_own_columns(bad):
     assert off(g["dq"][:, 128:, 0], ref["dq"][:, 128:, 0]) < BWD  # the chunks behind
     assert not torch.isfinite(g["dq"][0, 100, 0]).any()
     assert not torch.isfinite(g["dk"][0, 60, 0]).any()
+
+
+def test_status_of_many_calls():
+    """No wait runs out, in either arrangement of the kernels, and results do not change from call
+    to call."""
+    for h, n, dk, dv, dt in ((1, 200, 64, 40, F32), (6, 150, 16, 40, F32), (6, 400, 128, 64, BF16),
+                             (30, 300, 64, 128, BF16), (200, 130, 64, 64, BF16)):
+        c = cuda(inputs(1, n, h, h, dk, dv, seed=h))
+        ws = torch.empty(binding.ssm_gated_delta_workspace_bytes(1, n, h, dk, dv), dtype=torch.uint8,
+                         device="cuda")
+        first = forward(c, out_dtype=dt, workspace=ws)
+        for _ in range(20):
+            again = forward(c, out_dtype=dt, workspace=ws)
+            assert binding.ssm_last_device_status(ws) == 0
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
