@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
 // ------------------------------------------------------------------ grads
 
-constexpr int kGradThreads = kSplitThreads;  // 8 warps on rows, one that loads
+// 8 warps on rows, one that loads, one that multiplies, two for the gates' gradients
+constexpr int kGradThreads = kSplitThreads;
 constexpr int kMaxPans = 4;
 
 template <int DK> struct GradSmem {
@@ -436,7 +437,7 @@ template <int DK> struct GradSmem {
     static constexpr uint32_t u = stages + 2 * stage;   // U, then W (rows 64 to 127 of U's
     static constexpr uint32_t w = u + kTile;            // operand are not read)
     static constexpr uint32_t sums = w + 2 * kTile;     // (W^T's second block, not read either)
-    static constexpr uint32_t misc = sums + 4096;
+    static constexpr uint32_t misc = sums + 4608;
     static constexpr uint32_t factors = misc + 256;     // [2 heads][4 panels][8] floats
     static constexpr uint32_t bytes = w + 3 * kTile;
     static_assert(factors + 256 <= bytes, "sums fit behind W");
@@ -478,8 +479,26 @@ __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t
 // 2^-14 to 2^15).  Products below 2^kNone in all columns count as 0.
 constexpr int kFar = -16, kNone = -110;
 
-// CTAs walk the chunks and groups of heads; a warp brings in what comes next.  Rows of
-// products are lanes: steps as k rows (0 to 63) and as q rows (64 to 127).
+// What the warps on rows leave for those of a head's gates.
+struct Sums {
+    float dot[2 * kC][2];  // of what counts from step t on
+    float end[kC][2];      // before step t
+    float db[kC][2];
+    float ls[8];           // <L, S0>
+};
+
+// The largest product of R's and L's factors over the panels of a head.
+__device__ __forceinline__ int largest_ul(const float* fac, int pans) {
+    int e = kNone;
+    for (int p = 0; p < pans; ++p) e = max(e, exponent(fac[8 * p]) + exponent(fac[8 * p + 6]));
+    return e;
+}
+
+// CTAs walk the chunks and groups of heads; one warp brings in what comes next, one issues the
+// products, U's of the next columns ahead of time.  Rows of products are lanes: steps as k
+// rows (0 to 63) and as q rows (64 to 127).  All wait for one another by mbarriers, so that no
+// step of one warp holds up the others' (242 us for 8 x 2048 steps of 16 heads when the warps on
+// rows met at barriers and did the rest themselves, TIME_NOW now).
 //
 // The gates' gradients need no sums over D's rows and columns: scaling k_i as it reads by
 // e^{G_i}, as it writes by e^{-G_i} and q_i by e^{G_i} is what G does, so with dk split into
@@ -492,24 +511,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = GradSmem<DK>;
     constexpr int CP = DK / 4;  // pairs of columns of dstate a thread holds
-    // tensor memory: F, F2; [dA'; dP'] and U until W is made, then W K and W^T [K; Q]
-    constexpr uint32_t kTmF = 0, kTmF2 = 128, kTmA = 256, kTmU = 384, kTmW = 384, kTmV = 256,
+    // tensor memory: F, then W K; F2; [dA'; dP'], then W^T [K; Q]; U
+    constexpr uint32_t kTmF = 0, kTmW = 0, kTmF2 = 128, kTmA = 256, kTmV = 256, kTmU = 384,
                        kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
-    float* s_dot = reinterpret_cast<float*>(smem + M::sums);  // [128][2]: from step t on
-    float* s_end = s_dot + 256;                               // [64][2]: before step t
-    float* s_db = s_end + 128;                                // [64][2]
-    float* s_c = s_db + 128;                                  // [8]
-    float* s_most = s_c + 8;                                  // [8]
-    float* s_scan = s_most + 8;                               // [2]
+    Sums* sums = reinterpret_cast<Sums*>(smem + M::sums);             // [2 heads]
+    uint32_t* s_most = reinterpret_cast<uint32_t*>(sums + 2);         // [2 heads][8 warps]: of W
+    float* s_scan = reinterpret_cast<float*>(s_most + 16);            // [2]
+    static_assert(2 * sizeof(Sums) + 72 <= M::misc - M::sums, "sums fit");
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // [2] columns are in
     uint64_t* empty = full + 2;                                    // [2] and have been read
     uint64_t* full_h = full + 4;                                   // [2] a head is in
     uint64_t* empty_h = full + 6;                                  // [2]
-    uint64_t* bar_u = full + 8;
-    uint64_t* bar_f = full + 9;
-    uint64_t* bar_w = full + 10;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 11);
+    uint64_t* dots_in = full + 8;                                  // [2] a head's sums are there
+    uint64_t* dots_out = full + 10;                                // [2]
+    uint64_t* bar_u = full + 12;   // products done: U; F; A and F2; W's two
+    uint64_t* bar_f = full + 13;
+    uint64_t* bar_a = full + 14;
+    uint64_t* bar_w = full + 15;
+    uint64_t* u_in = full + 16;    // U is in shared memory, the last A has been read
+    uint64_t* f_out = full + 17;   // F has been read
+    uint64_t* w_in = full + 18;    // W is in shared memory
+    uint64_t* w_out = full + 19;   // W's products and F2 have been read
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 20);
     float* factors = reinterpret_cast<float*>(smem + M::factors);  // R, S0, -, -, dR, dY, L
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -518,7 +542,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
-        for (int n = 0; n < 11; ++n) mbar_init(full + n, 1);
+        for (int n = 0; n < 2; ++n) {
+            mbar_init(full + n, 1);
+            mbar_init(empty + n, 8);
+            mbar_init(full_h + n, 1);
+            mbar_init(empty_h + n, 10);
+            mbar_init(dots_in + n, 8);
+            mbar_init(dots_out + n, 2);
+        }
+        for (int n = 12; n < 16; ++n) mbar_init(full + n, 1);
+        for (int n = 16; n < 20; ++n) mbar_init(full + n, 8);
+        for (int n = 0; n < 16; ++n) s_most[n] = 0;
         fence_mbar_init();
     }
     tc_fence_before();
@@ -566,6 +600,125 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             for (int k = max(0, n - 2); k < n; ++k) (void)mbar_wait(full + (k & 1), (k >> 1) & 1, a.status);
             for (int k = max(0, hn - 2); k < hn; ++k)
                 (void)mbar_wait(full_h + (k & 1), (k >> 1) & 1, a.status);
+        } else if (warp == 9 && lane == 0) {
+            constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
+            constexpr uint32_t idW = idesc_f16(128, DK) | kIdescBMN;
+            constexpr uint32_t idV = idesc_f16(128, DK) | kIdescAMN | kIdescBMN;
+            // U = T' R
+            auto multiply_u = [&](int n, int hn) {
+                if (!mbar_poll(full + (n & 1), (n >> 1) & 1, a.status)) return false;
+                const uint32_t st = sb + M::stages + (n & 1) * M::stage, hd = sb + (hn & 1) * M::head;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmU, kdesc<128>(hd + M::t, kk), mdesc(st + M::r, kk, kTile), id64 | kIdescBMN,
+                            kk > 0);
+                mma_commit(bar_u);
+                return true;
+            };
+            // F = [dR; dY] S0^T, of columns that are in
+            auto multiply_f = [&](int n) {
+                const uint32_t st = sb + M::stages + (n & 1) * M::stage;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
+                mma_commit(bar_f);
+                return true;
+            };
+            const int heads = blockIdx.x < a.count ? (int)((a.count - 1 - blockIdx.x) / gridDim.x + 1) * ratio : 0;
+            bool ok = heads > 0 && mbar_poll(full_h, 0, a.status) && multiply_u(0, 0) && multiply_f(0);
+            for (int hn = 0, n = 0; hn < heads && ok; ++hn) {
+                const float* fac = factors + 8 * kMaxPans * (hn & 1);
+                const uint32_t hd = sb + (hn & 1) * M::head;
+                const int e_ul = largest_ul(fac, pans);
+                bool begun = false;  // F2
+                for (int p = 0; p < pans && ok; ++p, ++n) {
+                    const uint32_t st = sb + M::stages + (n & 1) * M::stage;
+                    const bool near = exponent(fac[8 * p]) + exponent(fac[8 * p + 6]) - e_ul >= kFar || e_ul == kNone;
+                    ok = mbar_poll(u_in, n & 1, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
+                    if (near) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
+                                    begun || kk > 0);
+                        begun = true;
+                    }
+                    mma_commit(bar_a);
+                    if (p + 1 < pans)
+                        ok = multiply_u(n + 1, hn) && mbar_poll(f_out, n & 1, a.status) && multiply_f(n + 1);
+                }
+                ok = ok && mbar_poll(w_in, hn & 1, a.status);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(hd + M::kq, kk, 2 * kTile), idW, kk > 0);
+                // (rows 64 to 127 of W^T [K; Q] are not read)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_f16(tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(hd + M::kq, kk, 2 * kTile), idV, kk > 0);
+                mma_commit(bar_w);
+                if (hn + 1 < heads)
+                    ok = mbar_poll(full_h + ((hn + 1) & 1), ((hn + 1) >> 1) & 1, a.status) &&
+                         multiply_u(n, hn + 1) && mbar_poll(w_out, hn & 1, a.status) && multiply_f(n);
+            }
+        } else if (warp >= 10) {
+            // ---- the gates: step i
+            const int i = tid - 10 * 32;
+            int hn = 0;
+            bool ok = true;
+            for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+                const unsigned bg = item / nc;
+                const int t = (int)(item - bg * nc) * kC + i;
+                const int b = (int)(bg / groups), group = (int)(bg - b * groups);
+                const bool in = t < a.d.seqlen;
+                for (int hh = 0; hh < ratio && ok; ++hh, ++hn) {
+                    const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + group * ratio + hh;
+                    const float g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
+                    const float beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
+                    const Gates* gates = reinterpret_cast<const Gates*>(smem + (hn & 1) * M::head);
+                    const Sums& s = sums[hn & 1];
+                    ok = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status) &&
+                         warp_wait(dots_in + (hn & 1), (hn >> 1) & 1, a.status);
+                    ok = named_bar_and(2, 64, ok);
+                    if (!ok) break;
+                    float up = s.dot[i][0] + s.dot[i][1] + s.dot[kC + i][0] + s.dot[kC + i][1];
+                    float down = s.end[i][0] + s.end[i][1];
+                    const float self = down, db = s.db[i][0] + s.db[i][1];
+                    float all = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) all += s.ls[q];
+                    const float e_end = ex2_approx(gates->hi[kC - 1] + gates->lo[kC - 1]);
+                    const bool off = gates->masked >> i & 1;
+                    // sums of `up` from here on, of `down` before here
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float u = __shfl_down_sync(0xffffffffu, up, o);
+                        const float d = __shfl_up_sync(0xffffffffu, down, o);
+                        if (lane + o < 32) up += u;
+                        if (lane >= o) down += d;
+                    }
+                    if (i == 32) s_scan[0] = up;
+                    if (i == 31) s_scan[1] = down;
+                    warp_arrive(dots_out + (hn & 1));
+                    warp_arrive(empty_h + (hn & 1));
+                    named_bar_sync(2, 64);
+                    if (warp == 10) up += s_scan[0];
+                    else down += s_scan[1];
+                    if (in) {
+                        // a gate of -inf cuts the past off: its gradient is 0
+                        const bool cut = ex2_approx(g * kLog2e) == 0.0f;
+                        put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - self) + e_end * all);
+                        put_gate(a.dbeta, at, a.gates_bf16, off ? 0.0f : db / beta);
+                    }
+                }
+            }
         }
     } else {
         take_registers();
@@ -587,7 +740,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 const uint8_t* hg = smem + (hn & 1) * M::head;
                 const Gates* gates = reinterpret_cast<const Gates*>(hg);
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
-                const int h = group * ratio + hh;
                 bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
                 const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
                 // a step's row of K or Q, columns col0 + 16 n .. + 15
@@ -603,8 +755,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 // chosen so that all have the same, the largest of theirs.  A panel's own: U is at
                 // most 64 products of 2^13 and 2^15, brought down to 2^15
                 constexpr float kDown = 1.0f / 524288.0f;
-                int e_ul = kNone;
-                for (int p = 0; p < pans; ++p) e_ul = max(e_ul, exponent(fac[8 * p]) + exponent(fac[8 * p + 6]));
+                const int e_ul = largest_ul(fac, pans);
                 // what the other heads have left in the sums does not belong to this one's dot
                 float before = 0.0f;
                 if (hh > 0) {
@@ -622,22 +773,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                 for (int e = 0; e < 16; ++e) own[e] = 0;
                 float beta_sum = 0.0f, ls = 0.0f;
-                bool begun = false;  // F2
                 for (int p = 0; p < pans; ++p, ++n) {
-                    const uint32_t st = sb + M::stages + (n & 1) * M::stage;
                     const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
                     const float s_r = fac[8 * p], s_s = fac[8 * p + 1], s_dr = fac[8 * p + 4],
                                 s_dy = fac[8 * p + 5], s_l = fac[8 * p + 6];
-                    // ---- U = T' R
-                    if (tid == 0 && mbar_poll(full + (n & 1), (n >> 1) & 1, a.status)) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kTmU, kdesc<128>(hd + M::t, kk), mdesc(st + M::r, kk, kTile),
-                                    idesc_f16(128, 64) | kIdescBMN, kk > 0);
-                        mma_commit(bar_u);
-                    }
                     here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
+                    const int below = exponent(s_r) + exponent(s_l) - e_ul;
+                    const float down = kDown * power(max(below, kFar)), s_u = s_r * gates->s_t / down;
+                    if (!is_q) {
+                        here = warp_wait(bar_u, n & 1, a.status) && here;
+                        tc_fence_after();
+                        f2 x[16];
+                        uint32_t hw[16];
+                        tmem_ld32(t_lane + kTmU + 32 * part, x);
+                        tmem_wait_ld();
+                        scaled<16>(x, down, x);
+                        round_to<16>(x, hw);
+                        put32(smem + M::u, i, 4 * part, hw);
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                    } else {
+                        tc_fence_before();
+                    }
+                    if (here) warp_arrive(u_in);
                     // sums over these columns: dR . R, and L . S0
                     {
                         f2 dr = 0, dl = 0;
@@ -654,46 +812,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         beta_sum = fmaf(s_dr * s_r, sum2(dr), beta_sum);
                         ls = fmaf(s_s * s_l, sum2(dl), ls);
                     }
-                    here = warp_wait(bar_u, n & 1, a.status) && here;
-                    tc_fence_after();
-                    const int below = exponent(s_r) + exponent(s_l) - e_ul;
-                    const float down = kDown * power(max(below, kFar)), s_u = s_r * gates->s_t / down;
-                    if (here && !is_q) {
-                        f2 x[16];
-                        uint32_t hw[16];
-                        tmem_ld32(t_lane + kTmU + 32 * part, x);
-                        tmem_wait_ld();
-                        scaled<16>(x, down, x);
-                        round_to<16>(x, hw);
-                        put32(smem + M::u, i, 4 * part, hw);
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    ok = named_bar_and(1, 256, here);
+                    ok = here && warp_wait(bar_f, n & 1, a.status);
                     if (!ok) break;
-                    if (tid == 0) {
-                        tc_fence_after();
-                        constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
-                        if (below >= kFar || e_ul == kNone) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
-                                        begun || kk > 0);
-                            begun = true;
-                        }
-                        mma_commit(bar_f);
-                    }
-                    here = warp_wait(bar_f, n & 1, a.status);
                     tc_fence_after();
-                    if (here) {
-                        const float f1 = (is_q ? er * s_dy : -er * s_dr) * s_s, fa = (is_q ? s_dy : -s_dr) * s_u;
-                        const f2 f1p = pair(f1, f1), fap = pair(fa, fa);
+                    {
+                        const float f1 = (is_q ? er * s_dy : -er * s_dr) * s_s;
+                        const f2 f1p = pair(f1, f1);
 #pragma unroll
                         for (int e0 = 0; e0 < CP; e0 += 16) {
                             f2 f[16];
@@ -702,16 +826,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                             for (int e = 0; e < 16; ++e) acc[e0 + e] = fma2(f1p, f[e], acc[e0 + e]);
                         }
+                        tc_fence_before();
+                        warp_arrive(f_out);
+                    }
+                    ok = warp_wait(bar_a, n & 1, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    {
+                        const float fa = (is_q ? s_dy : -s_dr) * s_u;
+                        const f2 fap = pair(fa, fa);
                         f2 x[16];
                         tmem_ld32(t_lane + kTmA + 32 * part, x);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) own[e] = fma2(fap, x[e], own[e]);
                     }
-                    tc_fence_before();
-                    ok = named_bar_and(1, 256, here);
-                    if (!ok) break;
-                    if (tid == 0) mbar_arrive(empty + (n & 1));  // these columns have been read
+                    warp_arrive(empty + (n & 1));  // these columns have been read
                 }
                 if (!ok) break;
 
@@ -737,39 +867,28 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         }
                     }
                     const float most = warp_most_or_nan<16>(own);
-                    if (lane == 0) s_most[warp] = most;
+                    if (lane == 0) post_most(s_most + 8 * (hn & 1) + warp, most, hn);
                 }
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-                if (lane == 0) s_c[warp] = ls;
-                named_bar_sync(1, 256);
-                float s_w;
-                scaled<16>(own, tile_scale(most_of<8>(s_most), kTop, s_w), own);
+                float s_w, w_most;
+                ok = read_most<2>(s_most + 8 * (hn & 1), hn, w_most, a.status);
+                if (!ok) break;
+                scaled<16>(own, tile_scale(w_most, kTop, s_w), own);
                 {
                     uint32_t hw[16];
                     round_to<16>(own, hw);
                     put32(smem + M::w, row, 4 * part, hw);
                 }
                 fence_proxy_async_smem();
-                named_bar_sync(1, 256);
-                if (tid == 0) {
-                    tc_fence_after();
-                    constexpr uint32_t idW = idesc_f16(128, DK) | kIdescBMN;
-                    constexpr uint32_t idV = idesc_f16(128, DK) | kIdescAMN | kIdescBMN;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(hd + M::kq, kk, 2 * kTile),
-                                idW, kk > 0);
-                    // (rows 64 to 127 of W^T [K; Q] are not read)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_f16(tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(hd + M::kq, kk, 2 * kTile),
-                                idV, kk > 0);
-                    mma_commit(bar_w);
-                }
-                here = warp_wait(bar_w, hn & 1, a.status);
+                tc_fence_before();
+                warp_arrive(w_in);
+                Sums& s = sums[hn & 1];
+                ok = (hn < 2 || warp_wait(dots_out + (hn & 1), ((hn >> 1) - 1) & 1, a.status)) &&
+                     warp_wait(bar_w, hn & 1, a.status);
+                if (!ok) break;
                 tc_fence_after();
-                if (here) {
+                {
                     const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
                     const float skq = gates->s_kq, f1 = s_w * skq;
                     const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_t / kDown : 0.0f;
@@ -808,49 +927,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     const float own_dot = skq * (sum2(whole) - before);
                     const float wk = skq * f1 * sum2(read), wv = skq * f1 * sum2(write),
                                 we = skq * g2 * sum2(end);
-                    s_dot[2 * row + part] = is_q ? own_dot : own_dot - 2.0f * wv - we;
+                    s.dot[row][part] = is_q ? own_dot : own_dot - 2.0f * wv - we;
                     if (!is_q) {
-                        s_end[2 * i + part] = we;
-                        s_db[2 * i + part] = beta_sum + wk;
+                        s.end[i][part] = we;
+                        s.db[i][part] = beta_sum + wk;
                     }
+                    if (lane == 0) s.ls[warp] = ls;
                 }
                 tc_fence_before();
-                ok = named_bar_and(1, 256, here);
-                if (!ok) break;
-                // ---- the gates
-                if (tid < kC) {
-                    const int t = t0 + i;
-                    const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + h;
-                    float up = s_dot[2 * i] + s_dot[2 * i + 1] + s_dot[128 + 2 * i] + s_dot[129 + 2 * i];
-                    float down = s_end[2 * i] + s_end[2 * i + 1];
-                    const float self = down;
-                    // sums of `up` from here on, of `down` before here
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float u = __shfl_down_sync(0xffffffffu, up, o);
-                        const float d = __shfl_up_sync(0xffffffffu, down, o);
-                        if (lane + o < 32) up += u;
-                        if (lane >= o) down += d;
-                    }
-                    if (tid == 32) s_scan[0] = up;
-                    if (tid == 31) s_scan[1] = down;
-                    named_bar_sync(2, 64);
-                    if (warp == 0) up += s_scan[0];
-                    if (warp == 1) down += s_scan[1];
-                    float all = 0.0f;
-                    for (int q = 0; q < 8; ++q) all += s_c[q];
-                    if (t < a.d.seqlen) {
-                        const float e_end = ex2_approx(gates->hi[kC - 1] + gates->lo[kC - 1]);
-                        // a gate of -inf cuts the past off: its gradient is 0
-                        const bool cut = ex2_approx(gate_at(a.g, at, a.gates_bf16) * kLog2e) == 0.0f;
-                        const bool off = gates->masked >> i & 1;
-                        put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - self) + e_end * all);
-                        put_gate(a.dbeta, at, a.gates_bf16,
-                                 off ? 0.0f : (s_db[2 * i] + s_db[2 * i + 1]) / gate_at(a.beta, at, a.gates_bf16));
-                    }
-                }
-                named_bar_sync(1, 256);  // sums are free for the next head
-                if (tid == 0) mbar_arrive(empty_h + (hn & 1));
+                warp_arrive(w_out);
+                warp_arrive(dots_in + (hn & 1));
+                warp_arrive(empty_h + (hn & 1));
             }
             if (ok && t0 + i < a.d.seqlen) {
                 TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
