@@ -1010,7 +1010,7 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * Supported: dstate a multiple of 8 up to 128, headdim a multiple of 8 up to 256, nheads a
  * multiple of ngroups, seqlen < 2^30, batch * nheads * ceil(seqlen / 64) < 2^30; in_dtype
  * SSM_BF16, or SSM_F32 without checkpoints.  seqlen == 0 hands the state on.
- * fp32 sequences, and bf16 ones of up to 16 steps without checkpoints (a decode step: one),
+ * fp32 sequences, and bf16 ones of up to 10 steps without checkpoints (a decode step: one),
  * are walked step by step in fp32 and need no workspace.  Others are taken in chunks of
  * 64 steps on the tensor cores; what enters their products beside q and k is held as the
  * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y and

@@ -1490,7 +1490,7 @@ def ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim) -> i
     return int(lib().ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim))
 
 
-_WALKED = 16  # steps a bf16 sequence is walked up to, without a workspace
+_WALKED = 10  # steps a bf16 sequence is walked up to, without a workspace
 
 
 def _delta_args(q, k, v, g, beta, initial_state):

