@@ -10,6 +10,7 @@ kernels.  There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -1371,9 +1372,31 @@ def _token_step(t, name, dtype, shape):
 
 
 def _one_device(first, *others):
+    if _devices() == 1:
+        return
+    device = first.get_device()
     for t in others:
-        if t is not None and t.get_device() != first.get_device():
+        if t is not None and t.get_device() != device:
             raise ValueError("all tensors must be on one device")
+
+
+@functools.lru_cache(None)
+def _devices():
+    return torch.cuda.device_count()
+
+
+def _outputs(given, wants, stream):
+    """The tensors of ``wants`` (name: what it is shaped like, shape, dtype), given or new."""
+    if given:
+        for name in given:
+            if name not in wants:
+                raise ValueError(f"out[{name!r}] is not an output of this call")
+    g = {}
+    for name, (like, shape, dtype) in wants.items():
+        t = given.get(name) if given else None
+        g[name] = (_new(like, shape, dtype, stream) if t is None else
+                   _like(t, f"out[{name!r}]", shape, dtype))
+    return g
 
 
 def _qk_args(q, k, q_weight, k_weight, positions, inv_freq):
@@ -1422,7 +1445,7 @@ def ssm_qk_norm_rope_fwd(q, k=None, q_weight=None, k_weight=None, positions=None
     code = _dt_code(out_dt, "out_dtype")
     q_out = _out(q_out, "q_out", q, q.shape, out_dt, stream)
     if k is not None:
-        k_out = _out(k_out, "k_out", q, k.shape, out_dt, stream)
+        k_out = _out(k_out, "k_out", k, k.shape, out_dt, stream)
         _one_device(q, q_out, k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -1452,21 +1475,16 @@ def ssm_qk_norm_rope_bwd(dq_out, dk_out, q, k=None, q_weight=None, k_weight=None
     _req(dq_out, "dq_out")
     code = _dt_code(dq_out.dtype, "dq_out")
     _like(dq_out, "dq_out", q.shape, dq_out.dtype)
-    wants = {"dq": (q.shape, q.dtype)}
+    wants = {"dq": (q, q.shape, q.dtype)}
     if k is not None:
         _like(dk_out, "dk_out", k.shape, dq_out.dtype)
-        wants["dk"] = (k.shape, q.dtype)
+        wants["dk"] = (k, k.shape, q.dtype)
     if q_weight is not None:
-        wants["dq_weight"] = ((dim,), torch.float32)
+        wants["dq_weight"] = (q_weight, q_weight.shape, torch.float32)
     if k is not None and k_weight is not None:
-        wants["dk_weight"] = ((dim,), torch.float32)
-    out = out or {}
-    for name in out:
-        if name not in wants:
-            raise ValueError(f"out[{name!r}] is not an output of this call")
+        wants["dk_weight"] = (k_weight, k_weight.shape, torch.float32)
     g = dict.fromkeys(("dq", "dk", "dq_weight", "dk_weight"))
-    for name, (shape, dt) in wants.items():
-        g[name] = _out(out.get(name), f"out[{name!r}]", q, shape, dt, stream)
+    g.update(_outputs(out, wants, stream))
     if g["dq_weight"] is not None or g["dk_weight"] is not None or workspace is not None:
         workspace = _work(workspace, q, ssm_qk_norm_rope_bwd_workspace_bytes(tokens, qheads, kheads,
                                                                              dim), stream)
@@ -1540,8 +1558,8 @@ def ssm_gated_delta_fwd(q, k, v, g, beta, initial_state=None, out_dtype=None, y=
     code = _dt_code(out_dt, "out_dtype")
     y = _out(y, "y", v, v.shape, out_dt, stream)
     if final_state is not None or return_final_state:
-        final_state = _out(final_state, "final_state", v, (batch, nheads, headdim, dstate),
-                           torch.float32, stream)
+        final_state = _out(final_state, "final_state", v if initial_state is None else initial_state,
+                           (batch, nheads, headdim, dstate), torch.float32, stream)
     five = batch, seqlen, nheads, dstate, headdim
     _delta_kept(checkpoints, *five)
     if workspace is not None or (q.dtype == torch.bfloat16 and
@@ -1578,17 +1596,12 @@ def ssm_gated_delta_bwd(q, k, v, g, beta, dy, initial_state=None, dfinal_state=N
     _delta_kept(checkpoints, *five)
     gd = q.dtype if grad_dtype is None else grad_dtype
     code = _dt_code(gd, "grad_dtype")
-    out = out or {}
-    wants = {"dq": (q.shape, gd), "dk": (q.shape, gd), "dv": (v.shape, gd),
-             "dg": (g.shape, g.dtype), "dbeta": (g.shape, g.dtype)}
-    if want_dinitial_state or "dinitial_state" in out:
-        wants["dinitial_state"] = ((batch, nheads, headdim, dstate), torch.float32)
-    for name in out:
-        if name not in wants:
-            raise ValueError(f"out[{name!r}] is not an output of this call")
+    wants = {"dq": (q, q.shape, gd), "dk": (q, q.shape, gd), "dv": (v, v.shape, gd),
+             "dg": (g, g.shape, g.dtype), "dbeta": (g, g.shape, g.dtype)}
+    if want_dinitial_state or (out and "dinitial_state" in out):
+        wants["dinitial_state"] = (v, (batch, nheads, headdim, dstate), torch.float32)
     grads = {"dinitial_state": None}
-    for name, (shape, dt) in wants.items():
-        grads[name] = _out(out.get(name), f"out[{name!r}]", q, shape, dt, stream)
+    grads.update(_outputs(out, wants, stream))
     need = ssm_gated_delta_bwd_workspace_bytes(*five)
     if checkpoints is None:
         need += ssm_gated_delta_checkpoint_bytes(*five)
