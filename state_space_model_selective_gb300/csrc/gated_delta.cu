@@ -43,7 +43,9 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 
 // A warp holds kWalkRows rows of one head's state, 8 lanes to a row, 4 rows at a time:
 // lane s of a row has the columns 4 (8 j + s) .. + 3, so that a load is 128 contiguous
-// bytes a row and a dot product takes 3 shuffles.  NJ = ceil(dstate / 32).
+// bytes a row and a dot product takes 3 shuffles.  NJ = ceil(dstate / 32).  Bound by reading
+// and writing the state: one token of 128 x 32 heads of 128 x 128 92 us, 5.8 TB/s (with 4 rows
+// to a warp 104 us).
 template <typename T, typename TO, int NJ>
 __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const WalkArgs a) {
     constexpr int SETS = kWalkRows / 4;
@@ -245,6 +247,9 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
     join_blocks<32>(m, tmp, tid >> 5, tid & 31);
 }
 
+// Bound by the issue of some 15000 warp instructions a chunk and head (14000 without LO): 4096 of
+// them at dstate 128 take 128 us (118 us), two CTAs' phases filling each other's waits.
+//
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
 // this one's H and P leave.
 //
@@ -733,6 +738,10 @@ struct ChainArgs {
 // the columns) and goes through shared memory as hi + lo each chunk, as R does.  Right
 // operands are [hi | lo] side by side, 2 PW columns to an instruction: at 64 columns an
 // instruction is bound by reading its 4 KB of A (55 cycles against 64 for twice the columns).
+//
+// A chunk of 64 columns takes some 2.5 us (128 heads of 128 x 128, 32 chunks, 256 CTAs: 156 us), of
+// 32 columns 1.6 us: instructions of the five passes through registers, their fetch (straight
+// code that two warps of a scheduler share) and the products' latency, one after the other.
 //
 // The factors of S and R have to be known before they are written, and a reduction over
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,

@@ -363,6 +363,10 @@ struct Walk {
 // A row group's shared memory for kShared.
 template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 4;
 
+// CTAs walk the tokens, the next tile's sines and cosines made while this one's rows are on their
+// way.  FULL: aligned rows of 16, 32, ... 256 columns, without checks.  16384 tokens of 32 + 8 heads
+// of 128 bf16 take 68 us, 4.9 TB/s: instructions (293 a warp and 4 rows) beside HBM.  (Three CTAs
+// an SM and checked rows: 77 us; a CTA for every tile: 72 us.)
 template <typename TI, typename TO, int MODE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs a) {
     __shared__ __align__(16) Table tables[2];
@@ -440,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs
     }
 }
 
-// TI: the type of x and dx, TO: of dy.
+// TI: the type of x and dx, TO: of dy.  16384 tokens of 32 heads of 128 bf16 take 99 us, 4 TB/s:
+// 386 instructions a warp and 4 rows on two CTAs an SM (135 us one float to an instruction).
 template <typename TI, typename TO, int MODE, bool FULL>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs a) {
     __shared__ __align__(16) Table tables[2];
