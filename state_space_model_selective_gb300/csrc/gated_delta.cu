@@ -693,9 +693,11 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 // ------------------------------------------------------------------ chain
 
-// 8 warps on rows, one that multiplies, one that loads (a copy takes its issuer some 100
-// cycles, and a chunk has a dozen), one that looks for records, one idle
-constexpr int kChainThreads = kSplitThreads;
+// Warps on rows (16 for 64 columns of headdim: 150 us where 8 took 156 us; 8 for 32), one that
+// multiplies, one that loads (a copy takes its issuer some 100 cycles, and a chunk has a dozen),
+// one that looks for records, one idle
+template <int PW> constexpr int kRowWarps = PW / 4;
+template <int PW> constexpr int kChainThreads = 32 * (kRowWarps<PW> + 4);
 
 // PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
 // products are taken too (y in fp32).
@@ -732,14 +734,14 @@ struct ChainArgs {
 };
 
 // One head and PW columns of headdim, chunk after chunk.  Rows of products are lanes of
-// tensor memory: of K S0 the steps, twice over, so that all eight warps share the work on R (a
+// tensor memory: of K S0 the steps, twice over, so that all warps share the work on R (a
 // warp only reaches its quarter of the lanes); of H R the state's rows; of Q S0 and P R the
-// steps in lanes 64 to 127.  The state stays in registers (a row of dstate to a lane, half
-// the columns) and goes through shared memory as hi + lo each chunk, as R does.  Right
+// steps in lanes 64 to 127.  The state stays in registers (a row of dstate to a lane, 16
+// columns) and goes through shared memory as hi + lo each chunk, as R does.  Right
 // operands are [hi | lo] side by side, 2 PW columns to an instruction: at 64 columns an
 // instruction is bound by reading its 4 KB of A (55 cycles against 64 for twice the columns).
 //
-// A chunk of 64 columns takes some 2.5 us (128 heads of 128 x 128, 32 chunks, 256 CTAs: 156 us), of
+// A chunk of 64 columns takes some 2.3 us (128 heads of 128 x 128, 32 chunks, 256 CTAs: 150 us), of
 // 32 columns 1.6 us: instructions of the five passes through registers, their fetch (straight
 // code that two warps of a scheduler share) and the products' latency, one after the other.
 //
@@ -753,7 +755,10 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
     constexpr bool PLO = sizeof(TO) == 4;
     using M = ChainSmem<DK, PW, PLO>;
     constexpr int NP = DK / 64;
-    constexpr int SC = PW / 2, RC = PW / 4;  // columns of S and of R to a thread
+    constexpr int NW = kRowWarps<PW>;             // warps on rows
+    constexpr int PARTS = NW / 4;                 // of the columns
+    constexpr int SC = PW / PARTS, RC = SC / 2;   // columns of S and of R to a thread
+    constexpr int kMosts = NW + NW / 2;           // largest values of a chunk
     // tensor memory, hi and lo columns each: K S0, H R, Q S0, P R
     constexpr uint32_t kTmX = 0, kTmH = 128, kTmQ = 256, kTmY = 384;
     const uint32_t sb = smem_u32(smem);
@@ -765,9 +770,9 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
     uint64_t* bar_s = full + 6;   // S0 is in shared memory
     uint64_t* bar_r = full + 7;   // R is
     uint64_t* bar_o = full + 8;   // Q S0 and P R have been read
-    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][8 warps of S0, 4 of V]
-    float* s_first = reinterpret_cast<float*>(s_most + 24);     // [8]: of the first S0
-    uint32_t* s_made = reinterpret_cast<uint32_t*>(s_first + 8);  // records known to be in memory
+    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][NW warps of S0, NW / 2 of V]
+    float* s_first = reinterpret_cast<float*>(s_most + 2 * kMosts);  // [NW]: of the first S0
+    uint32_t* s_made = reinterpret_cast<uint32_t*>(s_first + NW);  // records known to be in memory
     constexpr uint32_t kNotMade = 0xffffffffu;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -778,18 +783,18 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
 
     if (tid == 0) {
         for (int n = 0; n < 6; ++n) mbar_init(full + n, n == 2 ? 2 : 1);
-        mbar_init(bar_s, 8);
-        mbar_init(bar_r, 8);
-        mbar_init(bar_o, 4);
-        for (int n = 0; n < 24; ++n) s_most[n] = 0;
+        mbar_init(bar_s, NW);
+        mbar_init(bar_r, NW);
+        mbar_init(bar_o, NW / 2);
+        for (int n = 0; n < 2 * kMosts; ++n) s_most[n] = 0;
         *s_made = 0;
         fence_mbar_init();
     }
     __syncthreads();
 
-    if (warp >= 8) {
-        give_registers();
-        if (warp == 8 && lane == 0) {
+    if (warp >= NW) {
+        give_registers<NW>();
+        if (warp == NW && lane == 0) {
             auto kept_of = [&](int c) {
                 return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
             };
@@ -846,7 +851,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 }
             }
             bulk_wait_all();
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == NW + 1 && lane == 0) {
             const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             int loads = 0, h_loads = 0;
             // a record that is being made at the same time: false when that takes too long
@@ -909,7 +914,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             for (int c = max(0, loads - 2); c < loads; ++c)
                 (void)mbar_wait(full + (c & 1), (c >> 1) & 1, a.status);
             if (h_loads > 0) (void)mbar_wait(full_h, (h_loads - 1) & 1, a.status);
-        } else if (FLAGS && warp == 10 && lane == 0) {
+        } else if (FLAGS && warp == NW + 2 && lane == 0) {
             // Looks for records that are being made, ahead of the loads: a look takes most of a
             // microsecond
             const uint32_t addr = smem_u32(s_made);
@@ -926,7 +931,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             }
         }
     } else {
-        take_registers();
+        take_registers<NW>();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool upper = row >= kC;                 // these rows write y
@@ -959,7 +964,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 for (int p = 0; p < SC / 8; ++p)
                     seen.see(*reinterpret_cast<const uint4*>(tile + piece(i, (SC / 8) * part + p)));
                 const float v = warp_most(off ? 0.0f : seen.value());
-                if (lane == 0) post_most(s_most + 12 * (c & 1) + 8 + (quarter & 1) * 2 + part, v, c);
+                if (lane == 0) post_most(s_most + kMosts * (c & 1) + NW + (quarter & 1) * PARTS + part, v, c);
             }
             return in;
         };
@@ -979,7 +984,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             tc_fence_before();
             warp_arrive(bar_s);
             const float m = warp_most<SC / 2>(S) * s_s;
-            if (lane == 0) post_most(s_most + 12 * (c & 1) + warp, m, c);
+            if (lane == 0) post_most(s_most + kMosts * (c & 1) + warp, m, c);
             if (PW == 64 && a.kept && tid == 0) factors_of(c)[1] = s_s;
         };
         bool ok = gates_of(0);
@@ -997,16 +1002,16 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             drop_infinities<SC / 2>(S);
             const float m = warp_most<SC / 2>(S);
             if (lane == 0) s_first[warp] = m;
-            named_bar_sync(1, 256);
-            scaled<SC / 2>(S, tile_scale(most_of<8>(s_first), kBoundTop, s_s), S);
+            named_bar_sync(1, 32 * NW);
+            scaled<SC / 2>(S, tile_scale(most_of<NW>(s_first), kBoundTop, s_s), S);
             if (ok) put_state(0);
         }
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
             const float fs = f_k * s_s, ee = e_end, sp = s_p, sh = s_h;
             float s_max, v_max;
-            ok = read_most<2>(s_most + 12 * ph, c, s_max, a.status) &&
-                 read_most<1>(s_most + 12 * ph + 8, c, v_max, a.status);
+            ok = read_most<NW / 4>(s_most + kMosts * ph, c, s_max, a.status) &&
+                 read_most<NW / 8>(s_most + kMosts * ph + NW, c, v_max, a.status);
             if (!ok) break;
             const float r_bound = fmaf(k_bound, s_max, v_max);
             float s_r, s_next;
@@ -1109,11 +1114,11 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
 }
 
 template <int DK, int PW, typename TO>
-__global__ void __launch_bounds__(kChainThreads, 1)
+__global__ void __launch_bounds__(kChainThreads<PW>, 1)
     chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
-    with_tmem<512>(reinterpret_cast<uint32_t*>(smem + bytes - 8), 8, [&](uint32_t tmem) {
+    with_tmem<512>(reinterpret_cast<uint32_t*>(smem + bytes - 8), kRowWarps<PW>, [&](uint32_t tmem) {
         run_chain<DK, PW, TO, false>(tm_v, a, smem, tmem, blockIdx.x);
     });
 }
@@ -1123,7 +1128,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 // follow.  A chain only waits for CTAs with lower numbers, which have started and wait for
 // nothing.
 template <int DK, typename TO>
-__global__ void __launch_bounds__(kChainThreads, 1)
+__global__ void __launch_bounds__(kChainThreads<32>, 1)
     both_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const RecArgs r, const ChainArgs a,
                 uint32_t* ticket, unsigned makers) {
@@ -1137,10 +1142,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (number >= makers) {
             run_chain<DK, 32, TO, true>(tm_v, a, smem, tmem, number - makers);
         } else if (threadIdx.x < kRecThreads) {
-            take_registers();
+            take_registers<8>();
             make_records<DK, sizeof(TO) == 4, true>(tm_q, tm_k, r, smem, tmem, number, makers);
         } else {
-            give_registers();
+            give_registers<8>();
         }
     });
 }
@@ -1190,7 +1195,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
             using TO = decltype(to);
             constexpr uint32_t bytes = ChainSmem<DK, 32, sizeof(TO) == 4>::bytes;
             if (!allow_smem(both_kernel<DK, TO>, bytes)) return false;
-            both_kernel<DK, TO><<<(unsigned)sms, kChainThreads, bytes, s>>>(mq, mk, mv, r, a, f.flags,
+            both_kernel<DK, TO><<<(unsigned)sms, kChainThreads<32>, bytes, s>>>(mq, mk, mv, r, a, f.flags,
                                                                          (unsigned)makers);
             return true;
         };
@@ -1212,7 +1217,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
         using TO = decltype(to);
         constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
         if (!allow_smem(chain_kernel<DK, PW, TO>, bytes)) return false;
-        chain_kernel<DK, PW, TO><<<grid, kChainThreads, bytes, s>>>(mv, a);
+        chain_kernel<DK, PW, TO><<<grid, kChainThreads<PW>, bytes, s>>>(mv, a);
         return true;
     };
     auto by_out = [&](auto pw) {

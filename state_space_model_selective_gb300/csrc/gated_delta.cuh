@@ -436,13 +436,18 @@ __device__ __forceinline__ bool read_most(const uint32_t* slots, int chunk, floa
     return false;
 }
 
-// Registers move from the warps that load and multiply to those that compute: a kernel of 12
-// warps has 168 a thread at launch, 64512 in all; then 8 warps have 224 and 4 have 56.
+// Registers move from the warps that load and multiply to the NW that compute: a kernel of 12
+// warps has 168 a thread at launch, 64512 in all; then 8 warps have 224 and 4 have 56.  One of 20
+// has 96, 61440 in all; then 16 have 104 and 4 have 64.
+template <int NW>
 __device__ __forceinline__ void take_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (NW == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
 }
+template <int NW>
 __device__ __forceinline__ void give_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (NW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 constexpr int kSplitThreads = 384;
 

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const uint32_t tmem = *s_tmem;
 
     if (warp >= 8) {
-        give_registers();
+        give_registers<8>();
         if (warp == 8 && lane == 0) {
             auto kept_of = [&](int it) {
                 return a.kept + ((bh * nc + nc - 1 - it) * a.d.pans + pan) * adjoint_bytes(DK);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             (void)mbar_wait(full_p, (p_loads - 1) & 1, a.status);
         }
     } else {
-        take_registers();
+        take_registers<8>();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * part;
         const int col0 = pan * kPan + 32 * part;
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     const uint32_t tmem = *s_tmem;
 
     if (warp >= 8) {
-        give_registers();
+        give_registers<8>();
         if (warp == 8 && lane == 0) {
             int n = 0, hn = 0;  // columns and heads loaded
             bool ok = true;
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             }
         }
     } else {
-        take_registers();
+        take_registers<8>();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const bool is_q = row >= kC;
