@@ -1016,7 +1016,10 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y and
  * the state are within about 1e-6 (2-norm) of the definition; what is far below the largest
  * value of its tile is off by up to 2^-32 of that.
+ * The workspace must not be used by another call that may run concurrently.
  * Runs are bit-equal.  Bounded waits report through ssm_last_device_status.
+ * A v, state or q that is not finite spoils its column of headdim from its 64 steps on, its
+ * column, or its own step's y; a k that is not finite its head from its 64 steps on.
  */
 ssm_status_t ssm_gated_delta_fwd(const void* q, const void* k, const void* v, long long q_stride,
                                  long long k_stride, long long v_stride, const void* g,

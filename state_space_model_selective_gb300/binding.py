@@ -1378,6 +1378,8 @@ def _one_device(first, *others):
     for t in others:
         if t is not None and t.get_device() != device:
             raise ValueError("all tensors must be on one device")
+    if device != torch.cuda.current_device():  # where the kernels would run
+        raise ValueError(f"the tensors are on device {device}, which is not the current one")
 
 
 @functools.lru_cache(None)

@@ -207,3 +207,20 @@ def test_steps_between_tokens():
             step(bad)
     with pytest.raises(ValueError, match="shape"):
         step(z(3, 5, 2, 8), (3, 5, 4, 8))
+
+
+def test_another_device_is_refused(monkeypatch):
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    monkeypatch.setattr(binding, "_devices", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    binding._one_device(On(0), On(0), None)
+    with pytest.raises(ValueError, match="one device"):
+        binding._one_device(On(0), None, On(1))
+    with pytest.raises(ValueError, match="not the current one"):
+        binding._one_device(On(1), On(1))
