@@ -26,7 +26,8 @@ __device__ __forceinline__ void put_gate(void* p, long long i, int bf16, float v
 }
 // ------------------------------------------------------------------ chain
 
-constexpr int kChainThreads = kSplitThreads;
+constexpr int kRowWarps = 16;
+constexpr int kChainThreads = 32 * (kRowWarps + 4);
 
 template <int DK> struct ChainSmem {
     static constexpr uint32_t k_bytes = (DK / 64) * kTile;
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = ChainSmem<DK>;
     constexpr int NP = DK / 64;
+    constexpr int kMosts = kRowWarps + kRowWarps / 2;  // largest values of a chunk
     // tensor memory: P^T dY; hi and lo columns of H^T L, of Q^T e dY and of -K^T e dR
     constexpr uint32_t kTmP = 0, kTmX = 64, kTmQ = 192, kTmK = 320, kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
@@ -85,9 +87,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_o = full + 8;    // dY and e dY are
     uint64_t* bar_r = full + 9;    // -e dR is
     uint64_t* bar_d = full + 10;   // dR is in shared memory
-    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 12);  // [2 chunks][8 warps of L, 4 of dY]
-    float* s_first = reinterpret_cast<float*>(s_most + 24);     // [8]: of the first L
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + 8);
+    uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 12);  // [2 chunks][16 warps of L, 8 of dY]
+    float* s_first = reinterpret_cast<float*>(s_most + 2 * kMosts);  // [16]: of the first L
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + kRowWarps);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pan = blockIdx.x % a.d.pans;
@@ -96,14 +98,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const int nc = a.d.chunks;
     const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
 
-    if (warp == 8) tmem_alloc(s_tmem, kTmCols);
+    if (warp == kRowWarps) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
         for (int i = 0; i < 7; ++i) mbar_init(full + i, i == 2 ? 2 : 1);
-        mbar_init(bar_s, 8);
-        mbar_init(bar_o, 4);
-        mbar_init(bar_r, 4);
-        mbar_init(bar_d, 4);
-        for (int n = 0; n < 24; ++n) s_most[n] = 0;
+        mbar_init(bar_s, kRowWarps);
+        mbar_init(bar_o, kRowWarps / 2);
+        mbar_init(bar_r, kRowWarps / 2);
+        mbar_init(bar_d, kRowWarps / 2);
+        for (int n = 0; n < 2 * kMosts; ++n) s_most[n] = 0;
         fence_mbar_init();
     }
     tc_fence_before();
@@ -111,9 +113,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp >= 8) {
-        give_registers<8>();
-        if (warp == 8 && lane == 0) {
+    if (warp >= kRowWarps) {
+        give_registers<kRowWarps>();
+        if (warp == kRowWarps && lane == 0) {
             auto kept_of = [&](int it) {
                 return a.kept + ((bh * nc + nc - 1 - it) * a.d.pans + pan) * adjoint_bytes(DK);
             };
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 bulk_commit();
             }
             bulk_wait_all();
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == kRowWarps + 1 && lane == 0) {
             int kh_loads = 0, q_loads = 0, p_loads = 0;
             auto rec_of = [&](int it) { return rec0 + (long long)(nc - 1 - it) * rec_bytes(DK); };
             auto load_kh = [&](int it) {
@@ -207,17 +209,17 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             (void)mbar_wait(full_p, (p_loads - 1) & 1, a.status);
         }
     } else {
-        take_registers<8>();
+        take_registers<kRowWarps>();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
-        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 32 * part;
-        const int col0 = pan * kPan + 32 * part;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + 16 * part;
+        const int col0 = pan * kPan + 16 * part;
         const bool upper = row >= kC;   // these rows make dY and e dY
         const int i = row & 63;
-        f2* xch = reinterpret_cast<f2*>(smem + M::xch) + 16 * part * 64 + i;
-        f2 L[16];          // times its operand's factor; s_l undoes it
+        f2* xch = reinterpret_cast<f2*>(smem + M::xch) + 8 * part * 64 + i;
+        f2 L[8];          // times its operand's factor; s_l undoes it
         float s_l = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 8; ++e) {
             const float* at = a.dlast + (bh * a.d.dv + col0 + 2 * e) * a.d.dk + row;
             // (columns come in eights)
             const bool in = a.dlast && row < a.d.dk && col0 + 2 * e < a.d.dv;
@@ -241,24 +243,24 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             return in;
         };
         auto put_state = [&](int it) {
-            uint32_t hw[16], lw[16];
+            uint32_t hw[8], lw[8];
             if (row < DK) {
-                split<16>(L, hw, lw);
-                put32(smem + M::l_hi, row, 4 * part, hw);
-                put32(smem + M::l_lo, row, 4 * part, lw);
+                split<8>(L, hw, lw);
+                put_pieces<2>(smem + M::l_hi, row, 2 * part, hw);
+                put_pieces<2>(smem + M::l_lo, row, 2 * part, lw);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(bar_s);
-            const float m = warp_most<16>(L) * s_l;
-            if (lane == 0) post_most(s_most + 12 * (it & 1) + warp, m, it);
+            const float m = warp_most<8>(L) * s_l;
+            if (lane == 0) post_most(s_most + kMosts * (it & 1) + warp, m, it);
             if (tid == 0) factors_of(nc - 1 - it)[2] = s_l;
         };
-        uint4 dy[4];
+        uint4 dy[2];
         auto fetch = [&](int c) {
             const int t = c * kC + i;
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 2; ++p)
                 dy[p] = upper && t < a.d.seqlen && col0 + 8 * p < a.d.dv
                             ? *reinterpret_cast<const uint4*>(
                                   a.dy + (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv +
@@ -267,38 +269,38 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         };
         // (upper warps) dY and e dY of step `it` as operands, dY kept
         auto put_dy = [&](int it, float e) {
-            f2 x[16], y[16];
+            f2 x[8], y[8];
             MostBf16 seen;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < 2; ++p) {
                 seen.see(dy[p]);
                 unpack8_bf16(dy[p], x + 4 * p);
             }
             const float m = warp_most(seen.value());
-            uint32_t* most = s_most + 12 * (it & 1) + 8;
-            if (lane == 0) post_most(most + (quarter & 1) * 2 + part, m, it);
+            uint32_t* most = s_most + kMosts * (it & 1) + kRowWarps;
+            if (lane == 0) post_most(most + (quarter & 1) * 4 + part, m, it);
             float all = 0.0f;
-            const bool told = read_most<1>(most, it, all, a.status);
+            const bool told = read_most<2>(most, it, all, a.status);
             float s_dy, s_o;
-            uint32_t hw[16], lw[16];
-            scaled<16>(x, tile_scale(all, kTop, s_dy), y);
-            round_to<16>(y, hw);
-            put32(smem + M::dy, i, 4 * part, hw);
+            uint32_t hw[8], lw[8];
+            scaled<8>(x, tile_scale(all, kTop, s_dy), y);
+            round_to<8>(y, hw);
+            put_pieces<2>(smem + M::dy, i, 2 * part, hw);
             if (tid == 64) factors_of(nc - 1 - it)[1] = s_dy;
-            scaled<16>(x, e * tile_scale(all * e_max, kBoundTop, s_o), x);
-            split<16>(x, hw, lw);
-            put32(smem + M::o_hi, i, 4 * part, hw);
-            put32(smem + M::o_lo, i, 4 * part, lw);
+            scaled<8>(x, e * tile_scale(all * e_max, kBoundTop, s_o), x);
+            split<8>(x, hw, lw);
+            put_pieces<2>(smem + M::o_hi, i, 2 * part, hw);
+            put_pieces<2>(smem + M::o_lo, i, 2 * part, lw);
             fence_proxy_async_smem();
             warp_arrive(bar_o);
             return told;
         };
         {   // the last chunk: its largest values are measured
-            drop_infinities<16>(L);
-            const float m = warp_most<16>(L);
+            drop_infinities<8>(L);
+            const float m = warp_most<8>(L);
             if (lane == 0) s_first[warp] = m;
-            named_bar_sync(1, 256);
-            scaled<16>(L, tile_scale(most_of<8>(s_first), kBoundTop, s_l), L);
+            named_bar_sync(1, 32 * kRowWarps);
+            scaled<8>(L, tile_scale(most_of<kRowWarps>(s_first), kBoundTop, s_l), L);
             put_state(0);
         }
         bool ok = gates_of(0);  // the same for all lanes of a warp
@@ -309,11 +311,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const uint32_t ph = it & 1;
             const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p;
             if (c > 0) fetch(c - 1);
-            f2 x[16];
+            f2 x[8];
             // bounds: of L and dY measured, of dR and the next L from them
             float l_max = 0.0f, dy_max = 0.0f;
-            ok = ok && read_most<2>(s_most + 12 * ph, it, l_max, a.status) &&
-                 read_most<1>(s_most + 12 * ph + 8, it, dy_max, a.status);
+            ok = ok && read_most<4>(s_most + kMosts * ph, it, l_max, a.status) &&
+                 read_most<2>(s_most + kMosts * ph + kRowWarps, it, dy_max, a.status);
             const float dr_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
             float s_od, s_dyd, s_r, s_g, s_next;
             (void)tile_scale(dy_max * em, kBoundTop, s_od);  // (put_dy's factors)
@@ -326,38 +328,38 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             tc_fence_after();
             if (ok) {
                 const f2 fp = pair(sp * s_dyd, sp * s_dyd), fx = pair(sh * s_l, sh * s_l);
-                f2 z[16];
-                tmem_ld32(t_lane + kTmP, x);
-                tmem_ld32(t_lane + kTmX, z);
+                f2 z[8];
+                tmem_ld16(t_lane + kTmP, x);
+                tmem_ld16(t_lane + kTmX, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fma2(fp, x[e], mul2(fx, z[e]));
+                for (int e = 0; e < 8; ++e) x[e] = fma2(fp, x[e], mul2(fx, z[e]));
                 if (upper) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) xch[64 * e] = x[e];
+                    for (int e = 0; e < 8; ++e) xch[64 * e] = x[e];
                 } else {
-                    tmem_ld32(t_lane + kTmX + 64, z);
+                    tmem_ld16(t_lane + kTmX + 64, z);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = fma2(fx, z[e], x[e]);
+                    for (int e = 0; e < 8; ++e) x[e] = fma2(fx, z[e], x[e]);
                 }
             }
             tc_fence_before();
-            if (!named_bar_and(1, 256, ok)) break;  // all eight warps leave together
+            if (!named_bar_and(1, 32 * kRowWarps, ok)) break;  // all warps on rows leave together
             if (!upper) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = add2(x[e], xch[64 * e]);
-                uint32_t hw[16], lw[16];
-                f2 y[16];
-                scaled<16>(x, -er * g_scale, y);
-                split<16>(y, hw, lw);
-                put32(smem + M::r_hi, i, 4 * part, hw);
-                put32(smem + M::r_lo, i, 4 * part, lw);
+                for (int e = 0; e < 8; ++e) x[e] = add2(x[e], xch[64 * e]);
+                uint32_t hw[8], lw[8];
+                f2 y[8];
+                scaled<8>(x, -er * g_scale, y);
+                split<8>(y, hw, lw);
+                put_pieces<2>(smem + M::r_hi, i, 2 * part, hw);
+                put_pieces<2>(smem + M::r_lo, i, 2 * part, lw);
                 fence_proxy_async_smem();
                 warp_arrive(bar_r);
-                scaled<16>(x, r_scale, y);
-                round_to<16>(y, hw);
-                put32(smem + M::dr, i, 4 * part, hw);
+                scaled<8>(x, r_scale, y);
+                round_to<8>(y, hw);
+                put_pieces<2>(smem + M::dr, i, 2 * part, hw);
                 fence_proxy_async_smem();
                 warp_arrive(bar_d);
                 if (tid == 0) factors_of(c)[0] = s_r;
@@ -365,25 +367,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (t < a.d.seqlen) {
                     TG* dv = static_cast<TG*>(a.dv) +
                              (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                    store_row<16>(dv, x, col0, a.d.dv, a.d.dv % 16 == 0);
+                    store_row<8>(dv, x, col0, a.d.dv, a.d.dv % 16 == 0);
                 }
             }
             // ---- L0 = e_63 L + Q^T e dY - K^T e dR
-            scaled<16>(L, ee * s_l * next, L);
+            scaled<8>(L, ee * s_l * next, L);
             s_l = s_next;
             auto add = [&](uint32_t at, float factor) {
                 // (with 64 rows, what is in the other lanes is no adjoint)
                 if (DK == 64 && upper) return;
                 const f2 f = pair(factor, factor);
+                f2 z[8], y[8];
+                tmem_ld16(t_lane + at, z);
+                tmem_ld16(t_lane + at + 64, y);
+                tmem_wait_ld();
 #pragma unroll
-                for (int e0 = 0; e0 < 16; e0 += 8) {
-                    f2 z[8], y[8];
-                    tmem_ld16(t_lane + at + 2 * e0, z);
-                    tmem_ld16(t_lane + at + 64 + 2 * e0, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) L[e0 + e] = fma2(f, add2(z[e], y[e]), L[e0 + e]);
-                }
+                for (int e = 0; e < 8; ++e) L[e] = fma2(f, add2(z[e], y[e]), L[e]);
             };
             ok = warp_wait(bar_q, ph, a.status);
             tc_fence_after();
@@ -402,7 +401,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         if (a.dh0 && row < a.d.dk)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
                 if (col0 + 2 * e < a.d.dv) {
                     float v0, v1;
                     unpair(L[e], v0, v1);
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, kTmCols);
+    if (warp == kRowWarps) tmem_dealloc(tmem, kTmCols);
 }
 
 // ------------------------------------------------------------------ grads
