@@ -35,7 +35,9 @@ using namespace ssm;
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 256;
 constexpr int kTable = 1024;      // sines and cosines a CTA holds at a time (pairs x tokens)
+constexpr int kHeldTable = 512;   // the same where lanes hold them
 constexpr int kFwdCtas = 4;       // of the forward on an SM
+constexpr int kHeldCtas = 3;      // of the forward with held angles
 constexpr int kBwdCtas = 2;       // of the gradient
 constexpr int kBwdMost = 152 * kBwdCtas;  // its CTAs at most, whose sums of dw are joined
 
@@ -208,8 +210,8 @@ __device__ __forceinline__ unsigned long long turn_of(double freq) {
 
 // Cosines, sines and negative sines of a tile's tokens, each [token][pair]; rot / 2 pairs a
 // token, `pitch` floats apart (a multiple of 4).
-struct Table {
-    float cos[kTable], sin[kTable], neg[kTable];
+template <int N> struct Table {
+    float cos[N], sin[N], neg[N];
 };
 __host__ __device__ __forceinline__ int table_pitch(int rot) { return (rot / 2 + 3) / 4 * 4; }
 // A thread's pair and its fraction of a turn stay the same for all tiles.
@@ -224,7 +226,8 @@ struct Angles {
         if (a.rot == 0 || first >= per) first = 1 << 30;  // no part in it
         turn = first < per ? turn_of(a.freq[pair]) : 0;
     }
-    __device__ __forceinline__ void make(const QkArgs& a, long long t0, int n, Table& cs) const {
+    template <int N>
+    __device__ __forceinline__ void make(const QkArgs& a, long long t0, int n, Table<N>& cs) const {
         const int pitch = table_pitch(a.rot);
         for (int t = first; t < n; t += per) {
             const unsigned long long phase = (unsigned long long)a.pos[t0 + t] * turn;
@@ -360,6 +363,49 @@ struct Walk {
     }
 };
 
+// Held angles: a lane keeps its pairs' angles in registers while it goes through its part of one
+// token's heads.
+struct Held {
+    f2 c[4], s[4];         // cosines and sines
+    bool turned;
+    // pairs col .. col + 7 of the token at `at`; BACK: turned back
+    template <bool BACK, int N>
+    __device__ __forceinline__ void take(const Table<N>& table, int at, int col, bool on) {
+        turned = on;
+        if (!on) return;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(table.cos + at + col + 2 * i);
+            const ulonglong2 ss = *reinterpret_cast<const ulonglong2*>((BACK ? table.neg : table.sin) + at + col + 2 * i);
+            c[i] = cc.x; c[i + 1] = cc.y;
+            s[i] = ss.x; s[i + 1] = ss.y;
+        }
+    }
+    __device__ __forceinline__ void turn(f2* u, f2* v) const {
+        if (turned)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f2 x = u[i], y = v[i];
+                u[i] = fma2(x, c[i], mul2(y, s[i] ^ 0x8000000080000000ull));
+                v[i] = fma2(x, s[i], mul2(y, c[i]));
+            }
+    }
+};
+// The rows that a warp takes with held angles: one token's heads, q's and then k's, a group of
+// lanes to each of as many neighbouring heads as it has groups.
+constexpr int kHeldTokens = kThreads / 32;   // of a tile, one to a warp
+struct Share {
+    int group, groups, rows_q, rows;
+    __device__ __forceinline__ Share(const QkArgs& a, int lanes) {
+        groups = 32 / lanes;
+        group = (threadIdx.x & 31) / lanes;
+        rows_q = a.heads[0] / groups;
+        rows = rows_q + a.heads[1] / groups;
+    }
+    __device__ __forceinline__ bool starts(int r) const { return r == 0 || r == rows_q; }
+    __device__ __forceinline__ int of(int r) const { return r >= rows_q; }  // q or k
+};
+
 // A row group's shared memory for kShared.
 template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 4;
 
@@ -367,9 +413,9 @@ template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 :
 // way.  FULL: aligned rows of 16, 32, ... 256 columns, without checks.  16384 tokens of 32 + 8 heads
 // of 128 bf16 take 68 us, 4.9 TB/s: instructions (293 a warp and 4 rows) beside HBM.  (Three CTAs
 // an SM and checked rows: 77 us; a CTA for every tile: 72 us.)
-template <typename TI, typename TO, int MODE, bool FULL>
-__global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs a) {
-    __shared__ __align__(16) Table tables[2];
+template <typename TI, typename TO, int MODE, bool FULL, bool HELD>
+__global__ void __launch_bounds__(kThreads, HELD ? kHeldCtas : kFwdCtas) qk_fwd_kernel(const QkArgs a) {
+    __shared__ __align__(16) Table<HELD ? kHeldTable : kTable> tables[2];
     __shared__ __align__(16) float weights[2 * kWeights];
     __shared__ __align__(16) float bufs[kBufFloats<MODE>];
     const int lanes = a.lanes, groups = kThreads / lanes;
@@ -385,13 +431,54 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs
     const Angles angles(a);
     load_weights(a, weights);
     if (t0 < a.tokens) angles.make(a, t0, (int)min((long long)a.tile, a.tokens - t0), tables[0]);
+    // held: the next row is on its way, the next tile's first one too
+    const Share share(a, HELD ? lanes : 1);
+    Raw<TI> r0, r1;
+    const TI* x = nullptr;
+    auto ahead = [&](int row, long long t) {
+        const int which = share.of(row);
+        if (share.starts(row)) x = static_cast<const TI*>(a.x[which]) + t * a.stride[which] + share.group * a.dim;
+        else x += share.groups * a.dim;
+        load_row<true>(r0, r1, x, 0, in_x, true);
+    };
+    if (HELD && t0 + (threadIdx.x >> 5) < a.tokens) ahead(0, t0 + (threadIdx.x >> 5));
     __syncthreads();
 
     for (int k = 0; t0 < a.tokens; t0 += stride, k ^= 1) {
         const int n = (int)min((long long)a.tile, a.tokens - t0);
-        const Table& table = tables[k];
+        const auto& table = tables[k];
         if (t0 + stride < a.tokens)  // the next tile's
             angles.make(a, t0 + stride, (int)min((long long)a.tile, a.tokens - t0 - stride), tables[k ^ 1]);
+        if constexpr (HELD) {
+            const int t = threadIdx.x >> 5;
+            Held held;
+            held.template take<false>(table, t * pitch, c0, p < a.rot / 16);
+            TO* y = nullptr;
+#pragma unroll 1
+            for (int row = 0; row < (t < n ? share.rows : 0); ++row, y += share.groups * a.dim) {
+                const int which = share.of(row);
+                if (share.starts(row))
+                    y = static_cast<TO*>(a.y[which]) + ((t0 + t) * a.heads[which] + share.group) * a.dim;
+                f2 u[4], v[4], wu[4], wv[4];
+                r0.get(u);
+                r1.get(v);
+                if (row + 1 < share.rows) ahead(row + 1, t0 + t);
+                else if (t0 + stride + t < a.tokens) ahead(0, t0 + stride + t);
+                f2 s = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s = fma2(u[i], u[i], fma2(v[i], v[i], s));
+                const float r = rsqrtf(fmaf(row_sum(sum2(s), lanes), a.inv_dim, a.eps));
+                weights_of(weights + which * kWeights, c0, c1, wu, wv);
+                const f2 r2 = pair(r, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = mul2(u[i], mul2(wu[i], r2));
+                    v[i] = mul2(v[i], mul2(wv[i], r2));
+                }
+                held.turn(u, v);
+                store_row<true>(y, 0, in_y, u, v);
+            }
+        } else
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
             const int heads = a.heads[which];
@@ -444,13 +531,39 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs
     }
 }
 
+// A row's gradient in place of dy (g, q), already turned back, and its part of dw (none where the
+// row is not there, with eps 0 either).
+__device__ __forceinline__ void row_gradient(const QkArgs& a, int lanes, bool there, const f2* u, const f2* v,
+                                             f2* g, f2* q, f2* wu, f2* wv, f2* sum) {
+    f2 s2 = 0, m2 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s2 = fma2(u[i], u[i], fma2(v[i], v[i], s2));
+        wu[i] = mul2(wu[i], g[i]);
+        wv[i] = mul2(wv[i], q[i]);
+        m2 = fma2(wu[i], u[i], fma2(wv[i], v[i], m2));
+    }
+    const float s = row_sum(sum2(s2), lanes), m = row_sum(sum2(m2), lanes);
+    const float r = there ? rsqrtf(fmaf(s, a.inv_dim, a.eps)) : 0.0f;
+    const float mr = -m * a.inv_dim * r * r;  // of mean(g w n) r, per x
+    const f2 r2 = pair(r, r), mr2 = pair(mr, mr);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum[i] = fma2(g[i], mul2(u[i], r2), sum[i]);
+        sum[4 + i] = fma2(q[i], mul2(v[i], r2), sum[4 + i]);
+        g[i] = mul2(r2, fma2(mr2, u[i], wu[i]));
+        q[i] = mul2(r2, fma2(mr2, v[i], wv[i]));
+    }
+}
+
 // TI: the type of x and dx, TO: of dy.  16384 tokens of 32 heads of 128 bf16 take 99 us, 4 TB/s:
 // 386 instructions a warp and 4 rows on two CTAs an SM (135 us one float to an instruction).
-template <typename TI, typename TO, int MODE, bool FULL>
+template <typename TI, typename TO, int MODE, bool FULL, bool HELD>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs a) {
-    __shared__ __align__(16) Table tables[2];
+    __shared__ __align__(16) Table<HELD ? kHeldTable : kTable> tables[2];
     __shared__ __align__(16) float weights[2 * kWeights];
-    __shared__ __align__(16) float sums[kThreads * 16];  // rows' exchange, then the sums of dw
+    // rows' exchange, then the sums of dw; held: a thread's dw of q and k
+    __shared__ __align__(16) float sums[kThreads * 16 * (HELD ? 2 : 1)];
     const int lanes = a.lanes, groups = kThreads / lanes;
     const int group = threadIdx.x / lanes, p = threadIdx.x % lanes;
     int c0, c1;
@@ -464,16 +577,71 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs
     const Angles angles(a);
     load_weights(a, weights);
     if (t0 < a.tokens) angles.make(a, t0, (int)min((long long)a.tile, a.tokens - t0), tables[0]);
+    // held: the next row is on its way, the next tile's first one too
+    const Share share(a, HELD ? lanes : 1);
+    Raw<TI> x0, x1;
+    Raw<TO> d0, d1;
+    const TI* x = nullptr;
+    const TO* dy = nullptr;
+    auto ahead = [&](int row, long long t) {
+        const int which = share.of(row);
+        if (share.starts(row)) {
+            x = static_cast<const TI*>(a.x[which]) + t * a.stride[which] + share.group * a.dim;
+            dy = static_cast<const TO*>(a.dy[which]) + (t * a.heads[which] + share.group) * a.dim;
+        } else {
+            x += share.groups * a.dim;
+            dy += share.groups * a.dim;
+        }
+        load_row<true>(x0, x1, x, 0, in_x, true);
+        load_row<true>(d0, d1, dy, 0, in_y, true);
+    };
+    if (HELD && t0 + (threadIdx.x >> 5) < a.tokens) ahead(0, t0 + (threadIdx.x >> 5));
     __syncthreads();
 
-    f2 dw[2][8];  // of q and k
+    f2 dw[2][8];  // of q and k (held: not in registers all along)
+    f2* own = reinterpret_cast<f2*>(sums) + threadIdx.x;  // [2][8], kThreads apart
+    if constexpr (HELD)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) own[i * kThreads] = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0;
     for (int k = 0; t0 < a.tokens; t0 += stride, k ^= 1) {
         const int n = (int)min((long long)a.tile, a.tokens - t0);
-        const Table& table = tables[k];
+        const auto& table = tables[k];
         if (t0 + stride < a.tokens)  // the next tile's
             angles.make(a, t0 + stride, (int)min((long long)a.tile, a.tokens - t0 - stride), tables[k ^ 1]);
+        if constexpr (HELD) {
+            const int t = threadIdx.x >> 5;
+            Held held;
+            held.template take<true>(table, t * pitch, c0, p < a.rot / 16);
+            int row = 0;
+#pragma unroll 1
+            for (int which = 0; which < (t < n ? 2 : 0); ++which) {
+                const int end = which ? share.rows : share.rows_q;
+                if (row == end) continue;
+                TI* dx = static_cast<TI*>(a.y[which]) + ((t0 + t) * a.heads[which] + share.group) * a.dim;
+                f2 sum[8];
+                f2* at = own + which * 8 * kThreads;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = at[i * kThreads];
+#pragma unroll 1
+                for (; row < end; ++row, dx += share.groups * a.dim) {
+                    f2 u[4], v[4], g[4], q[4], wu[4], wv[4];
+                    x0.get(u);
+                    x1.get(v);
+                    d0.get(g);
+                    d1.get(q);
+                    if (row + 1 < share.rows) ahead(row + 1, t0 + t);
+                    else if (t0 + stride + t < a.tokens) ahead(0, t0 + stride + t);
+                    held.turn(g, q);
+                    weights_of(weights + which * kWeights, c0, c1, wu, wv);
+                    row_gradient(a, lanes, true, u, v, g, q, wu, wv, sum);
+                    store_row<true>(dx, 0, in_x, g, q);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) at[i * kThreads] = sum[i];
+            }
+        } else {
         auto rows_of = [&](int which, f2* sum) {
             const int heads = a.heads[which];
             if (heads == 0) return;
@@ -511,34 +679,21 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs
                 const int at = t * pitch;
                 turn<MODE, true>(a, table.cos + at, table.sin + at, table.neg + at, p, c0, c1, g, q, buf);
                 weights_of(weights + which * kWeights, c0, c1, wu, wv);
-                f2 s2 = 0, m2 = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s2 = fma2(u[i], u[i], fma2(v[i], v[i], s2));
-                    wu[i] = mul2(wu[i], g[i]);
-                    wv[i] = mul2(wv[i], q[i]);
-                    m2 = fma2(wu[i], u[i], fma2(wv[i], v[i], m2));
-                }
-                const float s = row_sum(sum2(s2), lanes), m = row_sum(sum2(m2), lanes);
-                // (rows beyond the last add nothing to dw, with eps 0 either)
-                const float r = row < rows ? rsqrtf(fmaf(s, a.inv_dim, a.eps)) : 0.0f;
-                const float mr = -m * a.inv_dim * r * r;  // of mean(g w n) r, per x
-                const f2 r2 = pair(r, r), mr2 = pair(mr, mr);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sum[i] = fma2(g[i], mul2(u[i], r2), sum[i]);
-                    sum[4 + i] = fma2(q[i], mul2(v[i], r2), sum[4 + i]);
-                    g[i] = mul2(r2, fma2(mr2, u[i], wu[i]));
-                    q[i] = mul2(r2, fma2(mr2, v[i], wv[i]));
-                }
+                row_gradient(a, lanes, row < rows, u, v, g, q, wu, wv, sum);
                 if (row < rows) store_row<FULL>(dx, out, in_x, g, q);
             }
         };
         rows_of(0, dw[0]);
         rows_of(1, dw[1]);
+        }
         __syncthreads();  // this table is read, the next one is made
     }
     if (!a.join) return;
+    if constexpr (HELD) {
+        // (own words only, before they are written over)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = own[i * kThreads];
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         // the CTA's sum over its groups, in their order
@@ -636,6 +791,17 @@ bool whole(const QkArgs& a) {
     return a.dim == 16 * a.lanes;
 }
 
+// Whether angles are held: with heads for all of a warp's groups of lanes, and whole tiles for every
+// CTA.  With fewer tokens or other heads rows are spread over all lanes instead.
+bool hold(QkArgs& a, int mode, long long slots) {
+    const int groups = 32 / a.lanes;
+    if (mode != kHalves || !whole(a) || a.heads[0] % groups || a.heads[1] % groups ||
+        kHeldTokens * table_pitch(a.rot) > kHeldTable || a.tokens < slots * kHeldTokens)
+        return false;
+    a.tile = kHeldTokens;
+    return true;
+}
+
 ssm_status_t check_sizes(const QkArgs& a, int interleaved, ssm_dtype_t in, ssm_dtype_t out) {
     using namespace ssm_host;
     if (!sizes_ok(a.tokens, a.heads[0], a.heads[1], a.dim) || a.rot < 0 || a.rot > a.dim ||
@@ -706,14 +872,22 @@ extern "C" ssm_status_t ssm_qk_norm_rope_fwd(
     if (sms == 0) return SSM_ERR_CUDA;
     const int mode = mode_of(a, interleaved);
     plan(a, mode, (long long)sms * kFwdCtas);
-    const unsigned grid =
-        (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, (long long)sms * kFwdCtas);
+    const bool held = hold(a, mode, (long long)sms * kHeldCtas);
+    const unsigned grid = (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile,
+                                                        (long long)sms * (held ? kHeldCtas : kFwdCtas));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
         by_mode(mode, [&](auto m) {
             constexpr int MODE = decltype(m)::value;
-            if (whole(a)) qk_fwd_kernel<decltype(ti), decltype(to), MODE, true><<<grid, kThreads, 0, s>>>(a);
-            else qk_fwd_kernel<decltype(ti), decltype(to), MODE, false><<<grid, kThreads, 0, s>>>(a);
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            if constexpr (MODE == kHalves)
+                if (held) {
+                    qk_fwd_kernel<TI, TO, MODE, true, true><<<grid, kThreads, 0, s>>>(a);
+                    return;
+                }
+            if (whole(a)) qk_fwd_kernel<TI, TO, MODE, true, false><<<grid, kThreads, 0, s>>>(a);
+            else qk_fwd_kernel<TI, TO, MODE, false, false><<<grid, kThreads, 0, s>>>(a);
         });
         return true;
     });
@@ -780,13 +954,21 @@ extern "C" ssm_status_t ssm_qk_norm_rope_bwd(
 
     const int mode = mode_of(a, interleaved);
     plan(a, mode, kBwdMost);
+    const bool held = hold(a, mode, kBwdMost);
     const unsigned grid = (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, kBwdMost);
     a.partial = static_cast<float*>(workspace);
     by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
         by_mode(mode, [&](auto m) {
             constexpr int MODE = decltype(m)::value;
-            if (whole(a)) qk_bwd_kernel<decltype(ti), decltype(to), MODE, true><<<grid, kThreads, 0, s>>>(a);
-            else qk_bwd_kernel<decltype(ti), decltype(to), MODE, false><<<grid, kThreads, 0, s>>>(a);
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            if constexpr (MODE == kHalves)
+                if (held) {
+                    qk_bwd_kernel<TI, TO, MODE, true, true><<<grid, kThreads, 0, s>>>(a);
+                    return;
+                }
+            if (whole(a)) qk_bwd_kernel<TI, TO, MODE, true, false><<<grid, kThreads, 0, s>>>(a);
+            else qk_bwd_kernel<TI, TO, MODE, false, false><<<grid, kThreads, 0, s>>>(a);
         });
         return true;
     });

@@ -197,3 +197,22 @@ def test_a_tile_of_tokens_far_apart():
     near_, _ = binding.ssm_qk_norm_rope_fwd(q.cuda(), **args)
     far_, _ = binding.ssm_qk_norm_rope_fwd(part, **args)
     assert torch.equal(near_, far_)
+
+
+@pytest.mark.parametrize("n,hq,hk,d,rot", [(4099, 32, 8, 128, 64), (5003, 5, 3, 128, 128), (8133, 4, 1, 64, 0),
+                                           (8133, 7, 0, 64, 48), (4003, 1, 4, 256, 256), (30001, 3, 1, 16, 16),
+                                           (30001, 3, 2, 32, 16), (4099, 4, 12, 128, 128), (4097, 0, 8, 128, 32),
+                                           (5003, 8, 16, 64, 64), (4003, 6, 2, 256, 128), (3700, 64, 32, 16, 16)])
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, F32), (BF16, F32)])
+def test_many_tokens(n, hq, hk, d, rot, xt, yt):
+    """Enough tokens for whole tiles in all CTAs: lanes hold their angles over the heads."""
+    q, k, wq, wk, pos, freq = inputs(1, n, hq, max(hk, 1), d, rot, xt, n + d)
+    check(q, k if hk else None, wq, wk if hk else None, pos, freq, False, yt)
+    if (xt, yt) == (BF16, BF16) and hk and hq:  # ranges of a projection give the same, bit for bit
+        wide = torch.cat((q.flatten(2), k.flatten(2)), -1).cuda()
+        qr = wide[..., :hq * d].unflatten(-1, (hq, d))
+        kr = wide[..., hq * d:].unflatten(-1, (hk, d))
+        args = dict(q_weight=wq.cuda(), positions=pos.cuda(), inv_freq=None if freq is None else freq.cuda())
+        for a, b in zip(binding.ssm_qk_norm_rope_fwd(q.cuda(), k.cuda(), **args),
+                        binding.ssm_qk_norm_rope_fwd(qr, kr, **args)):
+            assert torch.equal(a, b)
