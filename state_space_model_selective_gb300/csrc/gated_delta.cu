@@ -44,7 +44,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // A warp holds kWalkRows rows of one head's state, 8 lanes to a row, 4 rows at a time:
 // lane s of a row has the columns 4 (8 j + s) .. + 3, so that a load is 128 contiguous
 // bytes a row and a dot product takes 3 shuffles.  NJ = ceil(dstate / 32).  Bound by reading
-// and writing the state: one token of 128 x 32 heads of 128 x 128 92 us, 5.8 TB/s (with 4 rows
+// and writing the state: one token of 256 x 32 heads of 128 x 64 92 us, 5.8 TB/s (with 4 rows
 // to a warp 104 us).
 template <typename T, typename TO, int NJ>
 __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const WalkArgs a) {

@@ -66,7 +66,8 @@ struct ChainArgs {
 // instruction: rows 64 to 127 are their lo part, added through shared memory.  The warps on
 // those rows also make dY and e dY of the chunk before, while the others work on dR.  The
 // factors come from bounds as the forward's do, with the largest values of L and dY measured.
-// Bound as the forward's chain: 8 x 16 heads of 128 x 128, 32 chunks, 202 us, 3.1 us a chunk.
+// Bound as the forward's chain: 8 x 16 heads of 128 x 128, 32 chunks, 196 us, 3 us a chunk (203 us with
+// 8 warps on rows).
 template <int DK, typename TG>
 __global__ void __launch_bounds__(kChainThreads, 1)
     chain_bwd_kernel(const ChainArgs a) {

@@ -37,7 +37,6 @@ constexpr int kMaxDim = 256;
 constexpr int kTable = 1024;      // sines and cosines a CTA holds at a time (pairs x tokens)
 constexpr int kHeldTable = 512;   // the same where lanes hold them
 constexpr int kFwdCtas = 4;       // of the forward on an SM
-constexpr int kHeldCtas = 3;      // of the forward with held angles
 constexpr int kBwdCtas = 2;       // of the gradient
 constexpr int kBwdMost = 152 * kBwdCtas;  // its CTAs at most, whose sums of dw are joined
 
@@ -410,11 +409,12 @@ struct Share {
 template <int MODE> constexpr int kBufFloats = MODE == kShared ? kThreads * 16 : 4;
 
 // CTAs walk the tokens, the next tile's sines and cosines made while this one's rows are on their
-// way.  FULL: aligned rows of 16, 32, ... 256 columns, without checks.  16384 tokens of 32 + 8 heads
-// of 128 bf16 take 68 us, 4.9 TB/s: instructions (293 a warp and 4 rows) beside HBM.  (Three CTAs
-// an SM and checked rows: 77 us; a CTA for every tile: 72 us.)
+// way.  FULL: aligned rows of 16, 32, ... 256 columns, without checks.  HELD: as described above.
+// 16384 tokens of 32 + 8 heads of 128 bf16 take 64 us, 5.2 TB/s, bound by HBM and 190 instructions a
+// warp and 4 rows (not held 68 us, 293; held by three CTAs an SM 68 us; lanes of a warp on four
+// tokens, 256 bytes of each at a time, 75 us).
 template <typename TI, typename TO, int MODE, bool FULL, bool HELD>
-__global__ void __launch_bounds__(kThreads, HELD ? kHeldCtas : kFwdCtas) qk_fwd_kernel(const QkArgs a) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas) qk_fwd_kernel(const QkArgs a) {
     __shared__ __align__(16) Table<HELD ? kHeldTable : kTable> tables[2];
     __shared__ __align__(16) float weights[2 * kWeights];
     __shared__ __align__(16) float bufs[kBufFloats<MODE>];
@@ -556,8 +556,9 @@ __device__ __forceinline__ void row_gradient(const QkArgs& a, int lanes, bool th
     }
 }
 
-// TI: the type of x and dx, TO: of dy.  16384 tokens of 32 heads of 128 bf16 take 99 us, 4 TB/s:
-// 386 instructions a warp and 4 rows on two CTAs an SM (135 us one float to an instruction).
+// TI: the type of x and dx, TO: of dy.  16384 tokens of 32 heads of 128 bf16 take 77 us, 5.2 TB/s:
+// 284 instructions a warp and 4 rows on two CTAs an SM (not held 99 us, 386; one float to an
+// instruction 135 us).
 template <typename TI, typename TO, int MODE, bool FULL, bool HELD>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_bwd_kernel(const QkArgs a) {
     __shared__ __align__(16) Table<HELD ? kHeldTable : kTable> tables[2];
@@ -872,9 +873,9 @@ extern "C" ssm_status_t ssm_qk_norm_rope_fwd(
     if (sms == 0) return SSM_ERR_CUDA;
     const int mode = mode_of(a, interleaved);
     plan(a, mode, (long long)sms * kFwdCtas);
-    const bool held = hold(a, mode, (long long)sms * kHeldCtas);
-    const unsigned grid = (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile,
-                                                        (long long)sms * (held ? kHeldCtas : kFwdCtas));
+    const bool held = hold(a, mode, (long long)sms * kFwdCtas);
+    const unsigned grid =
+        (unsigned)std::min<long long>((tokens + a.tile - 1) / a.tile, (long long)sms * kFwdCtas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     by_types(in_dtype, out_dtype, [&](auto ti, auto to) {
         by_mode(mode, [&](auto m) {
