@@ -1,12 +1,13 @@
 // gated_delta.cu -- the gated delta rule, forward: S = exp(g) S; u = beta (v - S k);
 // S += u k^T; y = S q.
 //
-// Three kernels:
+// Four kernels:
 //  * walk: the steps as they are defined, for a few tokens (one: a decode step).  Bound by
 //    reading and writing the states.
 //  * records: P, H and the gates of every chunk of 64 steps (gated_delta.cuh), all chunks at
 //    once: three products on the tensor cores around the inverse of a unit triangle in fp32.
-//  * chain: the chunks of one head and 64 columns of headdim in order.
+//  * chain: the chunks of one head and 64 (or 32) columns of headdim in order.
+//  * both: records and chains at once, where chains are few.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>

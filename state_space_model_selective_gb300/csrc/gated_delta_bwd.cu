@@ -453,6 +453,7 @@ struct GradArgs {
     uint32_t* status;
     Dims d;
     unsigned count;          // of chunks and groups
+    int splits, per;         // CTAs that share an item's heads (a cluster), and heads of one
     int gates_bf16;
     int fresh;               // there was no initial state
 };
@@ -480,6 +481,21 @@ __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t
 // them) are left out of F2, so that their U never loses bits (2^7 or so at most, on fp16's
 // 2^-14 to 2^15).  Products below 2^kNone in all columns count as 0.
 constexpr int kFar = -16, kNone = -110;
+
+// All threads of a cluster's CTAs meet here, what they wrote to shared memory is seen.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t own, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(own), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ f2 cluster_load(uint32_t at) {
+    f2 v;
+    asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
 
 // What the warps on rows leave for those of a head's gates.
 struct Sums {
@@ -541,6 +557,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned nc = a.d.chunks, groups = a.d.groups;
     const int ratio = a.d.heads / a.d.groups, pans = a.d.pans;
+    // this CTA's items, and its heads of them
+    const unsigned first = blockIdx.x / a.splits, step = gridDim.x / a.splits, rank = blockIdx.x % a.splits;
+    const int head_lo = (int)rank * a.per, mine = min(a.per, ratio - head_lo);
 
     if (warp == 8) tmem_alloc(s_tmem, kTmCols);
     if (tid == 0) {
@@ -567,10 +586,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
         if (warp == 8 && lane == 0) {
             int n = 0, hn = 0;  // columns and heads loaded
             bool ok = true;
-            for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+            for (unsigned item = first; item < a.count && ok; item += step) {
                 const unsigned bg = item / nc, c = item - bg * nc;
-                const unsigned b = bg / groups, head0 = b * a.d.heads + (bg - b * groups) * ratio;
-                for (int hh = 0; hh < ratio && ok; ++hh, ++hn) {
+                const unsigned b = bg / groups, head0 = b * a.d.heads + (bg - b * groups) * ratio + head_lo;
+                for (int hh = 0; hh < mine && ok; ++hh, ++hn) {
                     const size_t ch = (size_t)(head0 + hh) * nc + c;
                     if (hn >= 2) ok = mbar_wait(empty_h + (hn & 1), ((hn >> 1) - 1) & 1, a.status);
                     if (!ok) break;
@@ -628,7 +647,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 mma_commit(bar_f);
                 return true;
             };
-            const int heads = blockIdx.x < a.count ? (int)((a.count - 1 - blockIdx.x) / gridDim.x + 1) * ratio : 0;
+            const int heads = first < a.count ? (int)((a.count - 1 - first) / step + 1) * mine : 0;
             bool ok = heads > 0 && mbar_poll(full_h, 0, a.status) && multiply_u(0, 0) && multiply_f(0);
             for (int hn = 0, n = 0; hn < heads && ok; ++hn) {
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
@@ -675,13 +694,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             const int i = tid - 10 * 32;
             int hn = 0;
             bool ok = true;
-            for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+            for (unsigned item = first; item < a.count && ok; item += step) {
                 const unsigned bg = item / nc;
                 const int t = (int)(item - bg * nc) * kC + i;
                 const int b = (int)(bg / groups), group = (int)(bg - b * groups);
                 const bool in = t < a.d.seqlen;
-                for (int hh = 0; hh < ratio && ok; ++hh, ++hn) {
-                    const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + group * ratio + hh;
+                for (int hh = 0; hh < mine && ok; ++hh, ++hn) {
+                    const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + group * ratio + head_lo + hh;
                     const float g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
                     const float beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
                     const Gates* gates = reinterpret_cast<const Gates*>(smem + (hn & 1) * M::head);
@@ -723,6 +742,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 }
             }
         }
+        if (a.splits > 1) {  // (as the warps on rows do)
+            __syncwarp();
+            cluster_meet();
+            cluster_meet();
+        }
     } else {
         take_registers<8>();
         const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
@@ -731,14 +755,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
         const int i = row & 63, col0 = (DK / 2) * part;  // first column of dstate
         int n = 0, hn = 0;
         bool ok = true;
-        for (unsigned item = blockIdx.x; item < a.count && ok; item += gridDim.x) {
+        for (unsigned item = first; item < a.count && ok; item += step) {
             const unsigned bg = item / nc;
             const int c = (int)(item - bg * nc), t0 = c * kC;
             const int b = (int)(bg / groups), group = (int)(bg - b * groups);
             f2 acc[CP];  // of dK (rows 0 to 63) or dQ, summed over heads
 #pragma unroll
             for (int e = 0; e < CP; ++e) acc[e] = 0;
-            for (int hh = 0; hh < ratio; ++hh, ++hn) {
+            for (int hh = 0; hh < mine; ++hh, ++hn) {
                 const uint32_t hd = sb + (hn & 1) * M::head;
                 const uint8_t* hg = smem + (hn & 1) * M::head;
                 const Gates* gates = reinterpret_cast<const Gates*>(hg);
@@ -939,6 +963,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 warp_arrive(dots_in + (hn & 1));
                 warp_arrive(empty_h + (hn & 1));
             }
+            // With few items the CTAs of a cluster have some heads each of one, the only one they
+            // have: the first adds the others' sums to its own, from where the columns were (all
+            // of them have been read)
+            if (a.splits > 1) {
+                f2* left = reinterpret_cast<f2*>(smem + M::stages) + tid;
+                static_assert(CP * 256 * 8 <= 2 * M::stage, "sums fit");
+                named_bar_sync(1, 256);  // no warp on rows reads columns any more
+                if (rank > 0)
+#pragma unroll
+                    for (int e = 0; e < CP; ++e) left[e * 256] = acc[e];
+                cluster_meet();
+                if (rank == 0)
+                    for (int r = 1; r < a.splits; ++r) {
+                        const uint32_t there = cluster_address(smem_u32(left), r);
+#pragma unroll
+                        for (int e = 0; e < CP; ++e) acc[e] = add2(acc[e], cluster_load(there + e * 256 * 8));
+                    }
+                cluster_meet();  // (the others' memory has been read)
+                if (rank > 0) break;
+            }
             if (ok && t0 + i < a.d.seqlen) {
                 TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
                           (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + col0;
@@ -969,8 +1013,34 @@ ssm_status_t run_backward(const ChainArgs& chain, GradArgs grads, cudaStream_t s
     chain_bwd_kernel<DK, TG><<<(unsigned)((long long)d.batch * d.heads * d.pans), kChainThreads,
                                ChainSmem<DK>::bytes, s>>>(chain);
     grads.count = (unsigned)((long long)d.batch * d.groups * d.chunks);
-    grads_kernel<DK, TG><<<std::min<unsigned>(grads.count, sms), kGradThreads,
-                           GradSmem<DK>::bytes, s>>>(grads);
+    // CTAs walk the items with all their heads, or up to 8 share one item's (each then has just the
+    // one): whichever takes fewer rounds of heads, with half a head's time for the start and the
+    // sum.  (The whole gradient, unshared and shared: one chunk of 21 heads 144 and 44 us, 8 chunks of
+    // 24 heads in 3 groups 75 and 46 us.)
+    const int ratio = d.heads / d.groups;
+    auto rounds = [&](long long ctas) { return (ctas + sms - 1) / sms; };
+    long long best = rounds(grads.count) * ratio * 2;
+    grads.per = ratio;
+    for (int n = 2; n <= std::min(ratio, 8); ++n) {
+        const int per = (ratio + n - 1) / n, used = (ratio + per - 1) / per;
+        const long long cost = rounds((long long)grads.count * used) * (per * 2 + 1);
+        if (cost < best) {
+            best = cost;
+            grads.per = per;
+        }
+    }
+    grads.splits = (ratio + grads.per - 1) / grads.per;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(grads.splits > 1 ? grads.count * grads.splits : std::min<unsigned>(grads.count, sms));
+    config.blockDim = dim3(kGradThreads);
+    config.dynamicSmemBytes = GradSmem<DK>::bytes;
+    config.stream = s;
+    cudaLaunchAttribute cluster[1];
+    cluster[0].id = cudaLaunchAttributeClusterDimension;
+    cluster[0].val.clusterDim = {(unsigned)grads.splits, 1, 1};
+    config.attrs = cluster;
+    config.numAttrs = grads.splits > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&config, grads_kernel<DK, TG>, grads) != cudaSuccess) return SSM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 

@@ -503,3 +503,16 @@ def test_a_first_gate_without_a_state_has_no_gradient(n):
     g = backward(cuda(t), grad_dtype=F32)
     assert not g["dg"][:, 0].any()
     assert off(g["dg"], reference_grads(t)["dg"]) < GATES
+
+
+@pytest.mark.parametrize("b,n,h,groups,dk,dv", [(1, 1, 21, 1, 128, 128), (1, 70, 9, 1, 64, 64), (2, 200, 24, 3, 128, 72),
+                                                (3, 1021, 6, 2, 72, 40), (1, 300, 32, 2, 40, 200)])
+def test_few_chunks_and_many_heads_of_a_group(b, n, h, groups, dk, dv):
+    """A group's heads are shared by CTAs that add up dq and dk."""
+    t = inputs(b, n, h, groups, dk, dv, seed=h + n)
+    c = cuda(t)
+    g = backward(c, grad_dtype=F32)
+    check_grads(g, reference_grads(t), F32, F32)
+    for _ in range(3):
+        again = backward(c, grad_dtype=F32)
+        assert all(torch.equal(g[k], again[k]) for k in g)
