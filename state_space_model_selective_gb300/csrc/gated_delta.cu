@@ -1098,7 +1098,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
 #pragma unroll
                 for (int e = 0; e < SC / 2; ++e) x[e] = fma2(q, x[e], mul2(f, z[e]));
-                store_row<SC / 2>(y, x, col0, a.d.dv, a.d.dv % 16 == 0);
+                store_row<SC / 2>(y, x, col0, a.d.dv, rows_of_sectors(a.y, a.d.dv));
             }
         }
         if (a.last && row < a.d.dk)

@@ -314,8 +314,12 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const f2* o) {
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Whether all rows of `cols` bf16 lie at multiples of 32 bytes (tensors start at any of 16).
+__device__ __forceinline__ bool rows_of_sectors(const void* base, int cols) {
+    return cols % 16 == 0 && (reinterpret_cast<uintptr_t>(base) & 31) == 0;
+}
 // N pairs as the columns col .. of a row of `cols` whose column col lies at p (cols a multiple
-// of 8); `wide`: rows are multiples of 32 bytes.
+// of 8); `wide`: rows_of_sectors (col is a multiple of 16).
 template <int N, typename T>
 __device__ __forceinline__ void store_row(T* p, const f2* o, int col, int cols, bool wide) {
     if (sizeof(T) == 2 && wide && N % 8 == 0) {

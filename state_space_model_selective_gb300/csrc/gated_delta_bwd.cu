@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 if (t < a.d.seqlen) {
                     TG* dv = static_cast<TG*>(a.dv) +
                              (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                    store_row<8>(dv, x, col0, a.d.dv, a.d.dv % 16 == 0);
+                    store_row<8>(dv, x, col0, a.d.dv, rows_of_sectors(a.dv, a.d.dv));
                 }
             }
             // ---- L0 = e_63 L + Q^T e dY - K^T e dR
@@ -984,9 +984,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 if (rank > 0) break;
             }
             if (ok && t0 + i < a.d.seqlen) {
-                TG* out = static_cast<TG*>(is_q ? a.dq : a.dk) +
+                void* base = is_q ? a.dq : a.dk;
+                TG* out = static_cast<TG*>(base) +
                           (((long long)b * a.d.seqlen + t0 + i) * a.d.groups + group) * a.d.dk + col0;
-                store_row<CP>(out, acc, col0, a.d.dk, a.d.dk % 16 == 0);
+                store_row<CP>(out, acc, col0, a.d.dk, rows_of_sectors(base, a.d.dk));
             }
         }
     }
