@@ -1013,9 +1013,9 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * fp32 sequences, and bf16 ones of up to 10 steps without checkpoints (a decode step: one),
  * are walked step by step in fp32 and need no workspace.  Others are taken in chunks of
  * 64 steps on the tensor cores; what enters their products beside q and k is held as the
- * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y and
- * the state are within about 1e-6 (2-norm) of the definition; what is far below the largest
- * value of its tile is off by up to 2^-32 of that.
+ * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y (then
+ * rounded once to out_dtype) and the state are within about 1e-6 (2-norm) of the definition; what
+ * is far below the largest value of its tile is off by up to 2^-32 of that.
  * The workspace must not be used by another call that may run concurrently.
  * Runs are bit-equal.  Bounded waits report through ssm_last_device_status.
  * A v, state or q that is not finite spoils its column of headdim from its 64 steps on, its

@@ -248,18 +248,15 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
     join_blocks<32>(m, tmp, tid >> 5, tid & 31);
 }
 
-// Bound by the issue of some 15000 warp instructions a chunk and head (14000 without LO): 4096 of
-// them at dstate 128 take 128 us (118 us), two CTAs' phases filling each other's waits.
+// Bound by the issue of some 15000 warp instructions a chunk and head: 4096 of them at dstate
+// 128 take 128 us, two CTAs' phases filling each other's waits.
 //
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
 // this one's H and P leave.
 //
-// LO: P's lo part is wanted, and T' for it as hi + lo (y in fp32, or a gradient will read it).
-// For y in bf16, whose own rounding is 2^-9, P only enters as one fp16, as do then its factors.
-//
 // The work of eight warps: the items `first`, first + step, ...  With flags they are told one
 // by one, and go through the chunks of all heads side by side.
-template <int DK, bool LO, bool FLAGS>
+template <int DK, bool FLAGS>
 __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                              const RecArgs& a, uint8_t* smem, uint32_t tmem,
                                              unsigned first, unsigned step) {
@@ -501,13 +498,9 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         uint32_t hw[16], lw[16];
         if (is_q) {
             scaled<16>(x, p_scale, x);
-            if constexpr (LO) {
-                split<16>(x, hw, lw);
-                put32(smem + M::p_lo, i, 4 * part, lw);
-            } else {
-                round_to<16>(x, hw);
-            }
+            split<16>(x, hw, lw);
             put32(smem + M::p_hi, i, 4 * part, hw);
+            put32(smem + M::p_lo, i, 4 * part, lw);
         }
         invert_unit_lower(tri, tmp, tid);
 
@@ -536,8 +529,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             uint32_t th[8], tl[8], wh[8], wl[8];
             scaled<8>(t, t_scale, t);
             scaled<8>(wt, w_scale, wt);
-            if constexpr (LO) split<8>(t, th, tl);
-            else round_to<8>(t, th);
+            split<8>(t, th, tl);
             split<8>(wt, wh, wl);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -547,7 +539,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
                         make_uint4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
                 };
                 put(M::t_hi, th);
-                if constexpr (LO) put(M::t_lo, tl);
+                put(M::t_lo, tl);
                 put(M::w_hi, wh);
                 put(M::w_lo, wl);
             }
@@ -572,12 +564,11 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_hi - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
-                        LO ? idP : idP64, kk > 0);
-            if constexpr (LO)
+                        idP, kk > 0);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
-                            idP64, 1);
+            for (int kk = 0; kk < 4; ++kk)
+                mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
+                        idP64, 1);
             mma_commit(bar_mma);
             if (a.keep_t) {
                 bulk_store(rec + rec_t(DK), smem + M::t_hi, kTile);
@@ -605,18 +596,10 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         };
         // (P is read once more for its operand: with both parts of it and of H a thread has no
         // registers to keep it)
-        auto p_row = [&](f2* v) {
-            if constexpr (LO) {
-                both(kTmP + 32 * part, v);
-            } else {
-                tmem_ld32(t_lane + kTmP + 32 * part, v);
-                tmem_wait_ld();
-            }
-        };
         f2 px[16], hx[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) hx[e] = px[e] = 0;
-        if (ok && is_q) p_row(px);
+        if (ok && is_q) both(kTmP + 32 * part, px);
         const float mp = warp_most<16>(px);
         if (ok && row < DK) both(kTmH + 32 * part, hx);
         const float mh = warp_most<16>(hx);
@@ -637,17 +620,13 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             put32(smem + M::t_hi + h_bytes(DK), row, 4 * part, lw);
         }
         if (is_q) {
-            if constexpr (LO) p_row(px);
+            both(kTmP + 32 * part, px);
             scaled<16>(px, p2_scale, px);
-            if constexpr (LO) {
-                split<16>(px, hw, lw);
-                put32(smem + M::p_lo, i, 4 * part, lw);
-            } else {
-                round_to<16>(px, hw);
-            }
+            split<16>(px, hw, lw);
             put32(smem + M::p_hi, i, 4 * part, hw);
+            put32(smem + M::p_lo, i, 4 * part, lw);
         }
-        if constexpr (LO) tc_fence_before();
+        tc_fence_before();
         if (tid == 0) {
             gates->s_h = s_h2 * s_kq * s_w;
             gates->s_p = s_p2 * s_p * s_t;
@@ -657,7 +636,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         if (tid == 0) {
             bulk_store(rec, smem + M::gates, kGateBytes);
             bulk_store(rec + rec_h(DK), smem + M::t_hi, 2 * h_bytes(DK));
-            bulk_store(rec + rec_p(DK), smem + M::p_hi, (LO ? 2 : 1) * kTile);
+            bulk_store(rec + rec_p(DK), smem + M::p_hi, 2 * kTile);
             bulk_commit();
         }
     }
@@ -682,13 +661,13 @@ __device__ __forceinline__ void with_tmem(uint32_t* place, int warp, F&& work) {
     if ((threadIdx.x >> 5) == warp) tmem_dealloc(tmem, COLS);
 }
 
-template <int DK, bool LO>
+template <int DK>
 __global__ void __launch_bounds__(kRecThreads, 2)
     records_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const RecArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     with_tmem<256>(reinterpret_cast<uint32_t*>(smem + RecSmem<DK>::bytes - 8), 0, [&](uint32_t tmem) {
-        make_records<DK, LO, false>(tm_q, tm_k, a, smem, tmem, blockIdx.x, gridDim.x);
+        make_records<DK, false>(tm_q, tm_k, a, smem, tmem, blockIdx.x, gridDim.x);
     });
 }
 
@@ -700,17 +679,15 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 template <int PW> constexpr int kRowWarps = PW / 4;
 template <int PW> constexpr int kChainThreads = 32 * (kRowWarps<PW> + 4);
 
-// PW: columns of headdim a CTA takes (64, or 32 where heads are few); PLO: P's and Q's lo
-// products are taken too (y in fp32).
-template <int DK, int PW, bool PLO> struct ChainSmem {
+// PW: columns of headdim a CTA takes (64, or 32 where heads are few).
+template <int DK, int PW> struct ChainSmem {
     // a stage (two in turn): gates, panels of K (twice: 128 rows), v (64 columns), panels of Q,
-    // P hi (| lo)
+    // P hi | lo
     static constexpr uint32_t k = kGateBytes;
     static constexpr uint32_t v = k + kq_bytes(DK);
     static constexpr uint32_t q = v + kTile;
     static constexpr uint32_t p = q + kq_bytes(DK) / 2;
-    static constexpr uint32_t p_bytes = (PLO ? 2 : 1) * kTile;
-    static constexpr uint32_t stage = p + p_bytes;
+    static constexpr uint32_t stage = p + 2 * kTile;
     // one H hi | lo: the next comes in between its product and the next but one's
     static constexpr uint32_t h = 2 * stage;
     // S0, rows of dstate, and R, rows of steps: hi and lo tiles, or both in a tile's row
@@ -753,8 +730,7 @@ struct ChainArgs {
 template <int DK, int PW, typename TO, bool FLAGS>
 __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainArgs& a, uint8_t* smem,
                                           uint32_t tmem, unsigned index) {
-    constexpr bool PLO = sizeof(TO) == 4;
-    using M = ChainSmem<DK, PW, PLO>;
+    using M = ChainSmem<DK, PW>;
     constexpr int NP = DK / 64;
     constexpr int NW = kRowWarps<PW>;             // warps on rows
     constexpr int PARTS = NW / 4;                 // of the columns
@@ -799,10 +775,9 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             auto kept_of = [&](int c) {
                 return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
             };
-            // right operands: S0 and R with both parts, or the first of two tiles alone
+            // right operands: S0 and R with both parts, or R's hi part alone
             constexpr uint32_t id2 = idesc_f16(128, 2 * PW) | kIdescBMN;
             constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
-            constexpr uint32_t idy = PLO ? id2 : id1;
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
                 if (!mbar_poll(full + (c & 1), (c >> 1) & 1, a.status)) break;
@@ -824,7 +799,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
                     mma_f16(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
-                            idy, kk > 0);
+                            id2, kk > 0);
                 if (!mbar_poll(full_h, ph, a.status)) break;
                 if (!mbar_poll(bar_r, ph, a.status)) break;
                 tc_fence_after();
@@ -840,11 +815,10 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 mma_commit(bar_h);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), idy, kk > 0);
-                if constexpr (PLO)
+                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
                 mma_commit(bar_y);
                 if (PW == 64 && a.kept) {
                     bulk_store(kept_of(c), smem + M::r, kTile);
@@ -883,7 +857,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                     bulk_load(st + M::q + p * kTile, kq + kTile, kTile, bar);
                 }
                 tma_load_4d(st + M::v, &tm_v, bar, pan * PW, h, c * kC, b);
-                bulk_load(st + M::p, rec + rec_p(DK), M::p_bytes, bar);
+                bulk_load(st + M::p, rec + rec_p(DK), 2 * kTile, bar);
                 ++loads;
             };
             auto load_h = [&](int c) {
@@ -1078,17 +1052,15 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             tmem_cols<SC>(t_lane + kTmQ + SC * part, x);
             tmem_cols<SC>(t_lane + kTmY + SC * part, z);
             tmem_wait_ld();
-            if constexpr (PLO) {
-                f2 w[SC / 2];
-                tmem_cols<SC>(t_lane + kTmQ + PW + SC * part, w);
-                tmem_wait_ld();
+            f2 w[SC / 2];
+            tmem_cols<SC>(t_lane + kTmQ + PW + SC * part, w);
+            tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < SC / 2; ++e) x[e] = add2(x[e], w[e]);
-                tmem_cols<SC>(t_lane + kTmY + PW + SC * part, w);
-                tmem_wait_ld();
+            for (int e = 0; e < SC / 2; ++e) x[e] = add2(x[e], w[e]);
+            tmem_cols<SC>(t_lane + kTmY + PW + SC * part, w);
+            tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < SC / 2; ++e) z[e] = add2(z[e], w[e]);
-            }
+            for (int e = 0; e < SC / 2; ++e) z[e] = add2(z[e], w[e]);
             tc_fence_before();
             warp_arrive(bar_o);
             const int t = c * kC + i;
@@ -1118,7 +1090,7 @@ template <int DK, int PW, typename TO>
 __global__ void __launch_bounds__(kChainThreads<PW>, 1)
     chain_kernel(const __grid_constant__ CUtensorMap tm_v, const ChainArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
+    constexpr uint32_t bytes = ChainSmem<DK, PW>::bytes;
     with_tmem<512>(reinterpret_cast<uint32_t*>(smem + bytes - 8), kRowWarps<PW>, [&](uint32_t tmem) {
         run_chain<DK, PW, TO, false>(tm_v, a, smem, tmem, blockIdx.x);
     });
@@ -1134,7 +1106,7 @@ __global__ void __launch_bounds__(kChainThreads<32>, 1)
                 const __grid_constant__ CUtensorMap tm_v, const RecArgs r, const ChainArgs a,
                 uint32_t* ticket, unsigned makers) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr uint32_t bytes = ChainSmem<DK, 32, sizeof(TO) == 4>::bytes;
+    constexpr uint32_t bytes = ChainSmem<DK, 32>::bytes;
     static_assert(RecSmem<DK>::bytes <= bytes, "records' place");
     uint32_t* place = reinterpret_cast<uint32_t*>(smem + bytes - 8);
     if (threadIdx.x == 0) place[1] = atomicAdd(ticket, 1u);
@@ -1144,7 +1116,7 @@ __global__ void __launch_bounds__(kChainThreads<32>, 1)
             run_chain<DK, 32, TO, true>(tm_v, a, smem, tmem, number - makers);
         } else if (threadIdx.x < kRecThreads) {
             take_registers<8>();
-            make_records<DK, sizeof(TO) == 4, true>(tm_q, tm_k, r, smem, tmem, number, makers);
+            make_records<DK, true>(tm_q, tm_k, r, smem, tmem, number, makers);
         } else {
             give_registers<8>();
         }
@@ -1194,7 +1166,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
         a.flags = f.flags + 1;
         auto both = [&](auto to) {
             using TO = decltype(to);
-            constexpr uint32_t bytes = ChainSmem<DK, 32, sizeof(TO) == 4>::bytes;
+            constexpr uint32_t bytes = ChainSmem<DK, 32>::bytes;
             if (!allow_smem(both_kernel<DK, TO>, bytes)) return false;
             both_kernel<DK, TO><<<(unsigned)sms, kChainThreads<32>, bytes, s>>>(mq, mk, mv, r, a, f.flags,
                                                                          (unsigned)makers);
@@ -1203,20 +1175,13 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
         if (!(f.out_dtype == SSM_F32 ? both(float{}) : both(__nv_bfloat16{}))) return SSM_ERR_CUDA;
         return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
     }
-    auto make = [&](auto lo) {
-        constexpr bool LO = decltype(lo)::value;
-        if (!allow_smem(records_kernel<DK, LO>, RecSmem<DK>::bytes)) return false;
-        records_kernel<DK, LO><<<std::min<unsigned>(r.count, 2 * sms), kRecThreads,
-                                 RecSmem<DK>::bytes, s>>>(mq, mk, r);
-        return true;
-    };
-    if (!(f.kept || f.out_dtype == SSM_F32 ? make(std::true_type{}) : make(std::false_type{})))
-        return SSM_ERR_CUDA;
+    if (!allow_smem(records_kernel<DK>, RecSmem<DK>::bytes)) return SSM_ERR_CUDA;
+    records_kernel<DK><<<std::min<unsigned>(r.count, 2 * sms), kRecThreads, RecSmem<DK>::bytes, s>>>(mq, mk, r);
     const unsigned grid = (unsigned)(half ? narrow : wide);
     auto go = [&](auto pw, auto to) {
         constexpr int PW = decltype(pw)::value;
         using TO = decltype(to);
-        constexpr uint32_t bytes = ChainSmem<DK, PW, sizeof(TO) == 4>::bytes;
+        constexpr uint32_t bytes = ChainSmem<DK, PW>::bytes;
         if (!allow_smem(chain_kernel<DK, PW, TO>, bytes)) return false;
         chain_kernel<DK, PW, TO><<<grid, kChainThreads<PW>, bytes, s>>>(mv, a);
         return true;
