@@ -1054,8 +1054,10 @@ size_t ssm_gated_delta_bwd_workspace_bytes(int batch, int seqlen, int nheads, in
  * The gradients of a masked step (beta 0) with respect to k, v and beta are 0, and so is
  * dg where g is -inf.
  * The adjoint of the state, dv and dinitial_state are as exact as the forward; dq, dk, dg
- * and dbeta come from products of operands rounded to one fp16 (summed in fp32): within
- * about 5e-4 (2-norm), less than their own rounding to bf16.
+ * and dbeta come from products of operands rounded to one fp16 (summed in fp32): dq, dk and
+ * dbeta are within about 4e-4 and dg, a sum of terms of either sign, within about 1e-3
+ * (2-norm).  That is less than their own rounding to bf16, and what is left in fp32.
+ * dbeta does not lose by a small beta, the step's own or another's.
  * Supported as ssm_gated_delta_fwd, in_dtype SSM_BF16.  Runs are bit-equal: sums over
  * heads and steps have a fixed order.
  */

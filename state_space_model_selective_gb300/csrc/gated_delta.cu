@@ -143,16 +143,17 @@ constexpr int kPitch = 68;  // floats between the rows of the triangle
 
 template <int DK> struct RecSmem {
     static constexpr uint32_t kq = 0;                    // panels of [K 64 rows | Q 64 rows]
-    static constexpr uint32_t t_hi = kq_bytes(DK);       // T', rows i, columns j
+    static constexpr uint32_t t_hi = kq_bytes(DK);       // T, rows i, columns j
     static constexpr uint32_t t_lo = t_hi + kTile;
-    static constexpr uint32_t w_hi = t_lo + kTile;       // diag(w) T'
+    static constexpr uint32_t w_hi = t_lo + kTile;       // diag(w) T
     static constexpr uint32_t w_lo = w_hi + kTile;
     static constexpr uint32_t p_hi = w_lo + kTile;       // (Q K^T) D
     static constexpr uint32_t p_lo = p_hi + kTile;
-    static constexpr uint32_t gates = p_lo + kTile;      // as the record has them
+    static constexpr uint32_t n = p_lo + kTile;          // b^-1 T b
+    static constexpr uint32_t gates = n + kTile;         // as the record has them
     static constexpr uint32_t misc = gates + kGateBytes;
     static constexpr uint32_t bytes = misc + 1024;
-    // A, then T (fp32), in the place of T' and its w's first tile; H and P leave from there too
+    // A, then T (fp32), in the place of T's and its w's first tile; H and P leave from there too
     static constexpr uint32_t tri = t_hi;
     static constexpr uint32_t tmp = w_lo;
 };
@@ -165,7 +166,7 @@ struct RecArgs {
     Dims d;
     unsigned count;   // of chunks and heads
     int gates_bf16;
-    int keep_t;       // T' is wanted (training)
+    int keep_n;       // N is wanted (training)
 };
 
 template <int V> struct Vec;
@@ -254,6 +255,14 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
 // this one's H and P leave.
 //
+// The beta of a row of the triangle: N divides the row by it, so that it must not be too small for
+// the row to be held.  A smaller one is taken for this, which changes T by as much and N not at
+// all (masked rows are 0 in either).
+__device__ __forceinline__ float row_beta(float b) {
+    constexpr float least = 8.673617379884035e-19f;  // 2^-60
+    return fabsf(b) < least ? copysignf(least, b) : b;
+}
+
 // The work of eight warps: the items `first`, first + step, ...  With flags they are told one
 // by one, and go through the chunks of all heads side by side.
 template <int DK, bool FLAGS>
@@ -272,8 +281,8 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
     float* s_dec = s_beta + kC;                                   // [32]: decays to step 31
     float* s_inv = s_dec + 32;                                    // [64]: inverse ones from 0 or 32
     float* s_span = s_inv + kC;                                   // [2]: their largest logarithm
-    float* s_most = s_span + 4;                                   // [2][8]
-    long long* s_sum = reinterpret_cast<long long*>(s_most + 16);
+    float* s_most = s_span + 4;                                   // [3][8]
+    long long* s_sum = reinterpret_cast<long long*>(s_most + 24);
     uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
     uint64_t* bar_mma = bar_in + 1;
@@ -366,9 +375,14 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             gates->hi[tid] = hi;
             gates->lo[tid] = lo;
             if (tid == 0) gates->masked = masked;
+            gates->beta[tid] = beta;
             const float e = ex2_approx(hi + lo);
-            const float m = warp_most(e);
-            if (lane == 0) s_most[8 + warp] = m;
+            // (a beta that is not finite spoils its chunk whatever it is held under)
+            const float m = warp_most(e), mb = warp_most(fabsf(beta) < 1e38f ? fabsf(beta) : 0.0f);
+            if (lane == 0) {
+                s_most[8 + warp] = m;
+                s_most[16 + warp] = mb;
+            }
         }
         if (more) fetch(chunk_of(item + step));
 
@@ -411,6 +425,10 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         if (tid == 0) {
             gates->s_kq = s_kq;
             gates->e_max = fmaxf(s_most[8], s_most[9]);
+            const float b = fmaxf(fmaxf(s_most[16], s_most[17]), 1.0f);
+            const uint32_t top = (__float_as_uint(b) + 0x7fffffu) & 0xff800000u;
+            gates->b_top = __uint_as_float(top);
+            gates->b_down = __uint_as_float((254u << 23) - top);
         }
         fence_proxy_async_smem();
         named_bar_sync(1, kRecThreads);
@@ -440,7 +458,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             tmem_ld32(t_lane + kTmX + 32 * part, x);
             tmem_wait_ld();
             const float hi = gates->hi[i], lo = gates->lo[i];
-            const float f = s_kq * s_kq * (is_q ? 1.0f : s_beta[i]);
+            const float f = s_kq * s_kq * (is_q ? 1.0f : row_beta(s_beta[i]));
             const int j0 = 32 * part;
             const int last = is_q ? i : i - 1;  // of the columns that count
             if (part == 0 && (quarter & 1) && !grows) {
@@ -504,24 +522,41 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         }
         invert_unit_lower(tri, tmp, tid);
 
-        // ---- T' and diag(w) T' as operands: row r = tid / 4, 16 columns
+        // ---- T and diag(w) T as operands, N to be kept: row r = tid / 4, 16 columns
         float s_t, s_w;
         {
             const int r = tid >> 2, j0 = (tid & 3) * 16;
             const float w = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[r], gates->lo[r]);
-            f2 t[8], wt[8];
+            f2 t[8], wt[8], nt[8];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const ulonglong2 m2 = *reinterpret_cast<const ulonglong2*>(tri + r * kPitch + j0 + 2 * e);
-                const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(s_beta + j0 + 2 * e);
-                t[e] = mul2(m2.x, b2.x);
-                t[e + 1] = mul2(m2.y, b2.y);
+                t[e] = m2.x;
+                t[e + 1] = m2.y;
             }
             scaled<8>(t, w, wt);
             const float mt = warp_most<8>(t), mw = warp_most<8>(wt);
             if (lane == 0) {
                 s_most[warp] = mt;
                 s_most[8 + warp] = mw;
+            }
+            if (a.keep_n) {
+                const float inv = 1.0f / row_beta(s_beta[r]);
+                const f2 inv2 = pair(inv, inv);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(s_beta + j0 + 2 * e);
+                    nt[e] = mul2(t[e], mul2(inv2, b2.x));
+                    nt[e + 1] = mul2(t[e + 1], mul2(inv2, b2.y));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {  // the diagonal is 1
+                    float n0, n1;
+                    unpair(nt[e], n0, n1);
+                    nt[e] = pair(j0 + 2 * e == r ? 1.0f : n0, j0 + 2 * e + 1 == r ? 1.0f : n1);
+                }
+                const float mn = warp_most<8>(nt);
+                if (lane == 0) s_most[16 + warp] = mn;
             }
             named_bar_sync(1, kRecThreads);  // (the triangle has been read)
             const float t_scale = tile_scale(most_of<8>(s_most), kTop, s_t);
@@ -543,12 +578,21 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
                 put(M::w_hi, wh);
                 put(M::w_lo, wl);
             }
-            if (tid == 0) gates->s_t = s_t;
+            if (a.keep_n) {
+                float s_n;
+                scaled<8>(nt, tile_scale(most_of<8>(s_most + 16), kTop, s_n), nt);
+                round_to<8>(nt, th);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    *reinterpret_cast<uint4*>(smem + M::n + piece(r, (j0 >> 3) + s)) =
+                        make_uint4(th[4 * s], th[4 * s + 1], th[4 * s + 2], th[4 * s + 3]);
+                if (tid == 0) gates->s_n = s_n;
+            }
         }
         fence_proxy_async_smem();
         named_bar_sync(1, kRecThreads);
 
-        // ---- H = K^T diag(w) T' (rows of dstate) and P T' (rows 64 to 127: the tile of 128
+        // ---- H = K^T diag(w) T (rows of dstate) and P T (rows 64 to 127: the tile of 128
         // rows starts one tile early, its first half is not read); columns 64 to 127: the
         // right operand's lo part
         if (tid == 0 && ok) {
@@ -570,8 +614,8 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
                 mma_f16(tmem + kTmP, kdesc<128>(sb + M::p_lo - kTile, kk), mdesc(sb + M::t_hi, kk, kTile),
                         idP64, 1);
             mma_commit(bar_mma);
-            if (a.keep_t) {
-                bulk_store(rec + rec_t(DK), smem + M::t_hi, kTile);
+            if (a.keep_n) {
+                bulk_store(rec + rec_n(DK), smem + M::n, kTile);
                 bulk_commit();
             }
         }
@@ -579,7 +623,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         mma_phase ^= 1;
         tc_fence_after();
         if (tid == 0 && ok) {
-            bulk_wait_read_all();   // K, Q and T' have left
+            bulk_wait_read_all();   // K, Q and N have left
             if (more) load(chunk_of(item + step));
             landing = more;
         }
@@ -690,7 +734,7 @@ template <int DK, int PW> struct ChainSmem {
     static constexpr uint32_t stage = p + 2 * kTile;
     // one H hi | lo: the next comes in between its product and the next but one's
     static constexpr uint32_t h = 2 * stage;
-    // S0, rows of dstate, and R, rows of steps: hi and lo tiles, or both in a tile's row
+    // S0, rows of dstate, and b R, rows of steps: hi and lo tiles, or both in a tile's row
     static constexpr uint32_t s = h + 2 * h_bytes(DK);
     static constexpr uint32_t s_bytes = (PW / 32) * h_bytes(DK);
     static constexpr uint32_t r = s + s_bytes;
@@ -713,9 +757,9 @@ struct ChainArgs {
 
 // One head and PW columns of headdim, chunk after chunk.  Rows of products are lanes of
 // tensor memory: of K S0 the steps, twice over, so that all warps share the work on R (a
-// warp only reaches its quarter of the lanes); of H R the state's rows; of Q S0 and P R the
+// warp only reaches its quarter of the lanes); of H b R the state's rows; of Q S0 and P b R the
 // steps in lanes 64 to 127.  The state stays in registers (a row of dstate to a lane, 16
-// columns) and goes through shared memory as hi + lo each chunk, as R does.  Right
+// columns) and goes through shared memory as hi + lo each chunk, as b R does.  Right
 // operands are [hi | lo] side by side, 2 PW columns to an instruction: at 64 columns an
 // instruction is bound by reading its 4 KB of A (55 cycles against 64 for twice the columns).
 //
@@ -725,7 +769,7 @@ struct ChainArgs {
 //
 // The factors of S and R have to be known before they are written, and a reduction over
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
-// |S1| <= e_63 |S| + |H|_1 |R|, with the measured maxima of V and S, found while products
+// |S1| <= e_63 |S| + |H|_1 |b| |R|, with the measured maxima of V and S, found while products
 // run.  A bound 2^20 too large would still leave 20 bits.
 template <int DK, int PW, typename TO, bool FLAGS>
 __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainArgs& a, uint8_t* smem,
@@ -736,17 +780,17 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
     constexpr int PARTS = NW / 4;                 // of the columns
     constexpr int SC = PW / PARTS, RC = SC / 2;   // columns of S and of R to a thread
     constexpr int kMosts = NW + NW / 2;           // largest values of a chunk
-    // tensor memory, hi and lo columns each: K S0, H R, Q S0, P R
+    // tensor memory, hi and lo columns each: K S0, H b R, Q S0, P b R
     constexpr uint32_t kTmX = 0, kTmH = 128, kTmQ = 256, kTmY = 384;
     const uint32_t sb = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + M::misc);  // a stage has come in
     uint64_t* full_h = full + 2;  // H has
     uint64_t* bar_x = full + 3;   // K S0 done
-    uint64_t* bar_h = full + 4;   // H R done
-    uint64_t* bar_y = full + 5;   // Q S0 and P R done: the stage and R are free
+    uint64_t* bar_h = full + 4;   // H b R done
+    uint64_t* bar_y = full + 5;   // Q S0 and P b R done: the stage and b R are free
     uint64_t* bar_s = full + 6;   // S0 is in shared memory
-    uint64_t* bar_r = full + 7;   // R is
-    uint64_t* bar_o = full + 8;   // Q S0 and P R have been read
+    uint64_t* bar_r = full + 7;   // b R is
+    uint64_t* bar_o = full + 8;   // Q S0 and P b R have been read
     uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][NW warps of S0, NW / 2 of V]
     float* s_first = reinterpret_cast<float*>(s_most + 2 * kMosts);  // [NW]: of the first S0
     uint32_t* s_made = reinterpret_cast<uint32_t*>(s_first + NW);  // records known to be in memory
@@ -775,14 +819,13 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             auto kept_of = [&](int c) {
                 return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
             };
-            // right operands: S0 and R with both parts, or R's hi part alone
+            // right operands: S0 and b R with both parts, or b R's hi part alone
             constexpr uint32_t id2 = idesc_f16(128, 2 * PW) | kIdescBMN;
             constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
                 if (!mbar_poll(full + (c & 1), (c >> 1) & 1, a.status)) break;
                 if (!mbar_poll(bar_s, ph, a.status)) break;
-                if (PW == 64 && a.kept) bulk_wait_read_all();  // R's when K S0 is
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
@@ -803,7 +846,12 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 if (!mbar_poll(full_h, ph, a.status)) break;
                 if (!mbar_poll(bar_r, ph, a.status)) break;
                 tc_fence_after();
-                if (PW == 64 && a.kept) bulk_wait_read_all();  // S0's place is written when H R is done
+                if (PW == 64 && a.kept) {
+                    bulk_wait_read_all();  // S0's place is written when H b R is done
+                    // R is in the place of V
+                    bulk_store(kept_of(c), smem + (c & 1) * M::stage + M::v, kTile);
+                    bulk_commit();
+                }
                 const uint32_t hh = sb + M::h, hl = hh + h_bytes(DK), pp = st + M::p;
                 // (of 64 rows of H the 64 behind them are not read)
 #pragma unroll
@@ -819,11 +867,8 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                if (PW == 64 && a.kept) bulk_wait_read_all();  // the stage is loaded again
                 mma_commit(bar_y);
-                if (PW == 64 && a.kept) {
-                    bulk_store(kept_of(c), smem + M::r, kTile);
-                    bulk_commit();
-                }
             }
             bulk_wait_all();
         } else if (warp == NW + 1 && lane == 0) {
@@ -919,7 +964,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         f2 S[SC / 2];      // times its operand's factor; s_s undoes it
         float s_s = 0.0f;
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float f_k = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        float f_k = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f, b_part = 0.0f, b_top = 1.0f;
         bool off = true;
         // the gates of chunk c, and the largest values of its V (upper warps)
         auto gates_of = [&](int c) {
@@ -930,6 +975,8 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             off = g->masked >> i & 1;
             s_h = g->s_h;
             s_p = g->s_p;
+            b_part = g->beta[i] * g->b_down;
+            b_top = g->b_top;
             // of e |K|_1 over a row, in units of the largest S
             k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
             if (upper) {
@@ -989,13 +1036,14 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                  read_most<NW / 8>(s_most + kMosts * ph + NW, c, v_max, a.status);
             if (!ok) break;
             const float r_bound = fmaf(k_bound, s_max, v_max);
-            float s_r, s_next;
+            float s_r, s_next;   // of R, and of the next S
             const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
+            const float s_br = s_r * b_top;
             // |H|_1 over a row is at most 64 times its largest value
-            const float next = tile_scale(fmaf(ee, s_max, kC * 2 * kTopValue * sh * r_bound), kBoundTop, s_next);
-            // ---- R, times its factor
+            const float next = tile_scale(fmaf(ee, s_max, kC * 2 * kTopValue * sh * b_top * r_bound), kBoundTop, s_next);
+            // ---- R, times its factor, and b R, times b_top less
             {
-                const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
+                uint8_t* tile = smem + (c & 1) * M::stage + M::v;
                 f2 v[RC / 2];
 #pragma unroll
                 for (int p = 0; p < RC / 8; ++p) {
@@ -1015,8 +1063,13 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < RC / 2; ++e) x[e] = fma2(f, add2(x[e], y[e]), v[e]);
-                // (the products that read R before are done: bar_x follows them)
                 uint32_t hw[RC / 2], lw[RC / 2];
+                if (PW == 64 && a.kept) {  // V is done with: its largest values are known
+                    round_to<RC / 2>(x, hw);
+                    put_pieces<RC / 8>(tile, i, rc / 8, hw);
+                }
+                scaled<RC / 2>(x, b_part, x);
+                // (the products that read b R before are done: bar_x follows them)
                 split<RC / 2>(x, hw, lw);
                 put_pieces<RC / 8>(smem + M::r, i, rc / 8, hw);
                 put_pieces<RC / 8>(smem + M::r + lo_r, i, rc / 8 + lo_c, lw);
@@ -1027,7 +1080,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             }
             // ---- the state, times its next factor; the next chunk's gates meanwhile
             scaled<SC / 2>(S, ee * s_s * next, S);
-            const float added = sh * s_r * next;
+            const float added = sh * s_br * next;
             if (c + 1 < nc) ok = gates_of(c + 1);
             ok = warp_wait(bar_h, ph, a.status) && ok;
             if (!ok) break;
@@ -1067,7 +1120,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             if (a.y && t < a.d.seqlen) {
                 TO* y = static_cast<TO*>(a.y) +
                         (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                const f2 f = pair(sp * s_r, sp * s_r), q = pair(fs, fs);
+                const f2 f = pair(sp * s_br, sp * s_br), q = pair(fs, fs);
 #pragma unroll
                 for (int e = 0; e < SC / 2; ++e) x[e] = fma2(q, x[e], mul2(f, z[e]));
                 store_row<SC / 2>(y, x, col0, a.d.dv, rows_of_sectors(a.y, a.d.dv));
@@ -1145,7 +1198,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     RecArgs r{};
     r.g = f.g; r.beta = f.beta; r.records = f.records; r.status = f.status; r.d = d;
     r.gates_bf16 = f.gate_dtype == SSM_BF16;
-    r.keep_t = f.kept != nullptr;
+    r.keep_n = f.kept != nullptr;
     r.count = (unsigned)((long long)f.batch * f.heads * d.chunks);
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;

@@ -5,13 +5,16 @@
 // Per head, with the state S (dstate x headdim here), for chunks of 64 steps that start
 // from S0 (G_i = sum of g up to step i, everything inside the chunk):
 //   D_ij = exp(G_i - G_j), j <= i;   e_i = exp(G_i);   w_j = exp(G_63 - G_j)
-//   A_ij = beta_i (k_i . k_j) D_ij, j < i;   T = (1 + A)^-1;   T' = T diag(beta)
+//   A_ij = beta_i (k_i . k_j) D_ij, j < i;   T = (1 + A)^-1;   b = diag(beta)
 //   R = V - e K S0                      what each step's value is off the carried state
-//   U = T' R                            the steps' updates
-//   Y = e Q S0 + P R,    P = ((Q K^T) D) T'
-//   S1 = e_63 S0 + H R,  H = K^T diag(w) T'
+//   U = T b R                           the steps' updates
+//   Y = e Q S0 + P b R,    P = ((Q K^T) D) T
+//   S1 = e_63 S0 + H b R,  H = K^T diag(w) T
 // P and H depend on q, k and the gates alone, so one kernel makes them for all chunks at
-// once, and the chain over the chunks is two products deep: K S0 and H R.
+// once, and the chain over the chunks is two products deep: K S0 and H b R.
+// b goes with R, not into P and H, for the gradient's sake: theirs with respect to b R is z, of
+// which dR = b z and dbeta_i = z_i . E_i, with the steps' errors E = N R, N = b^-1 T b, U = b E.
+// No step's small beta is ever rounded beside other steps' larger ones and divided by.
 //
 // Operands are fp16 under one power of two per tile, chosen from the tile's largest value
 // or a bound of it: bf16 inputs are exact in it down to 2^-30 of that, a value as the sum
@@ -37,15 +40,17 @@ constexpr uint32_t kTile = 8192;  // a 64 x 64 fp16 tile: 64 rows of 128 bytes
 // be multiplied with.
 struct Gates {
     float hi[kC], lo[kC];
+    float beta[kC];
     unsigned long long masked;
-    float s_kq, s_h, s_p, s_t;
+    float s_kq, s_h, s_p, s_n;
     float e_max;   // the largest decay from the chunk's start to a step
+    float b_top, b_down;  // a power of two that no beta is above, 1 at least, and its inverse
 };
 constexpr uint32_t kGateBytes = 1024;
 static_assert(sizeof(Gates) <= kGateBytes, "gates fit their place");
 
 // The record of one chunk and head (bytes): gates | panels of K and Q (64 columns of
-// dstate: 64 rows each) | H hi | H lo (dstate rows) | P hi | P lo | T'.  Tiles are stored as
+// dstate: 64 rows each) | H hi | H lo (dstate rows) | P hi | P lo | N.  Tiles are stored as
 // they lie in shared memory: rows of 128 bytes whose 16-byte pieces are XORed with (row mod
 // 8), so that one bulk copy brings in what the chain needs.
 __host__ __device__ constexpr uint32_t h_bytes(int dk) { return (uint32_t)dk * 128u; }
@@ -53,11 +58,11 @@ __host__ __device__ constexpr uint32_t kq_bytes(int dk) { return (uint32_t)(dk /
 __host__ __device__ constexpr uint32_t rec_kq(int) { return kGateBytes; }
 __host__ __device__ constexpr uint32_t rec_h(int dk) { return kGateBytes + kq_bytes(dk); }
 __host__ __device__ constexpr uint32_t rec_p(int dk) { return rec_h(dk) + 2 * h_bytes(dk); }
-__host__ __device__ constexpr uint32_t rec_t(int dk) { return rec_p(dk) + 2 * kTile; }
-__host__ __device__ constexpr uint32_t rec_bytes(int dk) { return rec_t(dk) + kTile; }
+__host__ __device__ constexpr uint32_t rec_n(int dk) { return rec_p(dk) + 2 * kTile; }
+__host__ __device__ constexpr uint32_t rec_bytes(int dk) { return rec_n(dk) + kTile; }
 // What training keeps for each chunk, head and 64 columns of headdim, rounded to one fp16:
-// R | S0 | their factors (forward), dR | dY | L | their factors (gradient).  Only products
-// whose results are rounded to bf16 read them.
+// R | S0 | their factors (forward), z | dY | L | their factors (gradient).  Only dq, dk, dg and
+// dbeta come from them.
 constexpr uint32_t kFactorBytes = 128;
 __host__ __device__ constexpr uint32_t kept_bytes(int dk) { return kTile + h_bytes(dk) + kFactorBytes; }
 __host__ __device__ constexpr uint32_t adjoint_bytes(int dk) { return 2 * kTile + h_bytes(dk) + kFactorBytes; }

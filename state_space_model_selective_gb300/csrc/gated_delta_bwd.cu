@@ -2,14 +2,15 @@
 // (gated_delta.cuh has the chunked form and its names).
 //
 // With L the adjoint of the state behind a chunk, per chunk, backwards:
-//   dR = P^T dY + H^T L                 (also V's gradient)
+//   z = P^T dY + H^T L,  dR = b z       (dR is also V's gradient)
 //   L0 = e_63 L + Q^T (e dY) - K^T (e dR)
 // is a chain two products deep again (chain_bwd_kernel, one head and 64 columns of headdim
-// a CTA).  With dR and L kept, everything else is one kernel over all chunks at once:
-//   U = T' R;  F = [dR; dY] S0^T;  F2 = U L^T;  [dA'; dP'] = [-dR; dY] U^T
-//   dKK = dA' D (j < i),  dQK = dP' D (j <= i)          (beta cancels in dA A: dR = beta T^T dU)
+// a CTA).  With z and L kept, everything else is one kernel over all chunks at once:
+//   E = N R;  U = b E;  F = [dR; dY] S0^T;  F2 = U L^T;  [dA'; dP'] = [-dR; dY] U^T
+//   dKK = dA' D (j < i),  dQK = dP' D (j <= i)          (beta cancels in dA A: dR = b T^T dU)
 //   dQ = dQK K + e F_q;   dK = dKK K + dKK^T K + dQK^T Q - e F_k + w F2
-//   dbeta_i = (dR_i . R_i + k_i . (dKK K)_i) / beta_i
+//   dbeta_i = z_i . E_i
+// z is the operand of F and dA'; b enters their rows afterwards.
 //   dg_t = sum_{i >= t} dG_i + sum_{j < t} w_j k_j . F2_j + e_63 <L, S0>   (grads_kernel)
 #include <algorithm>
 #include <cstring>
@@ -44,8 +45,8 @@ template <int DK> struct ChainSmem {
     static constexpr uint32_t o_lo = o_hi + kTile;
     static constexpr uint32_t r_hi = o_lo + kTile;           // -e dR
     static constexpr uint32_t r_lo = r_hi + kTile;
-    static constexpr uint32_t dr = r_lo + kTile;             // dR, on its way out
-    static constexpr uint32_t xch = dr + kTile;              // 64 x 64 fp32, columns first
+    static constexpr uint32_t z = r_lo + kTile;              // z, on its way out
+    static constexpr uint32_t xch = z + kTile;               // 64 x 64 fp32, columns first
     static constexpr uint32_t misc = xch + 64 * 64 * 4;
     static constexpr uint32_t bytes = misc + 512;
 };
@@ -53,7 +54,7 @@ template <int DK> struct ChainSmem {
 struct ChainArgs {
     const __nv_bfloat16* dy;
     const uint8_t* records;
-    uint8_t* kept;          // dR | dY | L
+    uint8_t* kept;          // z | dY | L
     const float* dlast;
     float* dh0;
     void* dv;
@@ -64,7 +65,7 @@ struct ChainArgs {
 // One head and 64 columns of headdim, backwards; laid out as the forward's chain.  H^T L and
 // P^T dY have 64 rows, so both parts of the left operand go into the 128 rows of one
 // instruction: rows 64 to 127 are their lo part, added through shared memory.  The warps on
-// those rows also make dY and e dY of the chunk before, while the others work on dR.  The
+// those rows also make dY and e dY of the chunk before, while the others work on z.  The
 // factors come from bounds as the forward's do, with the largest values of L and dY measured.
 // Bound as the forward's chain: 8 x 16 heads of 128 x 128, 32 chunks, 196 us, 3 us a chunk (203 us with
 // 8 warps on rows).
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* bar_s = full + 7;    // L is in shared memory
     uint64_t* bar_o = full + 8;    // dY and e dY are
     uint64_t* bar_r = full + 9;    // -e dR is
-    uint64_t* bar_d = full + 10;   // dR is in shared memory
+    uint64_t* bar_z = full + 10;   // z is
     uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 12);  // [2 chunks][16 warps of L, 8 of dY]
     float* s_first = reinterpret_cast<float*>(s_most + 2 * kMosts);  // [16]: of the first L
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_first + kRowWarps);
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         mbar_init(bar_s, kRowWarps);
         mbar_init(bar_o, kRowWarps / 2);
         mbar_init(bar_r, kRowWarps / 2);
-        mbar_init(bar_d, kRowWarps / 2);
+        mbar_init(bar_z, kRowWarps / 2);
         for (int n = 0; n < 2 * kMosts; ++n) s_most[n] = 0;
         fence_mbar_init();
     }
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             constexpr uint32_t id64 = idesc_f16(128, 64) | kIdescAMN | kIdescBMN;
             for (int it = 0; it < nc; ++it) {
                 const uint32_t ph = it & 1, st = sb + (it & 1) * M::stage;
-                bulk_wait_read_all();  // dR's place is written again when H^T L is done
+                bulk_wait_read_all();  // z's place is written again when H^T L is done
                 if (!mbar_poll(full_p, ph, a.status)) break;
                 if (!mbar_poll(bar_o, ph, a.status)) break;
                 tc_fence_after();
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 for (int kk = 0; kk < 4; ++kk)
                     mma_f16(tmem + kTmK, mdesc(st + M::k, kk, kTile), mdesc(sb + M::r_hi, kk, kTile), id, kk > 0);
                 mma_commit(bar_l);
-                if (!mbar_poll(bar_d, ph, a.status)) break;
-                bulk_store(kept_of(it), smem + M::dr, kTile);
+                if (!mbar_poll(bar_z, ph, a.status)) break;
+                bulk_store(kept_of(it), smem + M::z, kTile);
                 bulk_commit();
             }
             bulk_wait_all();
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                             2 * kTile + h_bytes(DK));
         };
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_kq = 0.0f, s_h = 0.0f, s_p = 0.0f;
+        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_kq = 0.0f, s_h = 0.0f, s_p = 0.0f, b_row = 0.0f,
+              b_top = 1.0f;
         auto gates_of = [&](int it) {
             const bool in = warp_wait(full + (it & 1), (it >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (it & 1) * M::stage);
@@ -241,6 +243,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             s_kq = g->s_kq;
             s_h = g->s_h;
             s_p = g->s_p;
+            b_row = g->beta[i];
+            b_top = g->b_top;
             return in;
         };
         auto put_state = [&](int it) {
@@ -310,18 +314,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
-            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p;
+            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p, br = b_row;
             if (c > 0) fetch(c - 1);
             f2 x[8];
-            // bounds: of L and dY measured, of dR and the next L from them
+            // bounds: of L and dY measured, of z, dR and the next L from them
             float l_max = 0.0f, dy_max = 0.0f;
             ok = ok && read_most<4>(s_most + kMosts * ph, it, l_max, a.status) &&
                  read_most<2>(s_most + kMosts * ph + kRowWarps, it, dy_max, a.status);
-            const float dr_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
-            float s_od, s_dyd, s_r, s_g, s_next;
+            const float z_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
+            const float dr_bound = z_bound * b_top;
+            float s_od, s_dyd, s_z, s_g, s_next;
             (void)tile_scale(dy_max * em, kBoundTop, s_od);  // (put_dy's factors)
             (void)tile_scale(dy_max, kTop, s_dyd);
-            const float r_scale = tile_scale(dr_bound, kBoundTop, s_r);
+            const float z_scale = tile_scale(z_bound, kBoundTop, s_z);
             const float g_scale = tile_scale(dr_bound * em, kBoundTop, s_g);
             const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f * skq * em *
                                                               (dy_max + dr_bound)), kBoundTop, s_next);
@@ -352,18 +357,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 for (int e = 0; e < 8; ++e) x[e] = add2(x[e], xch[64 * e]);
                 uint32_t hw[8], lw[8];
                 f2 y[8];
-                scaled<8>(x, -er * g_scale, y);
+                scaled<8>(x, -er * br * g_scale, y);
                 split<8>(y, hw, lw);
                 put_pieces<2>(smem + M::r_hi, i, 2 * part, hw);
                 put_pieces<2>(smem + M::r_lo, i, 2 * part, lw);
                 fence_proxy_async_smem();
                 warp_arrive(bar_r);
-                scaled<8>(x, r_scale, y);
+                scaled<8>(x, z_scale, y);
                 round_to<8>(y, hw);
-                put_pieces<2>(smem + M::dr, i, 2 * part, hw);
+                put_pieces<2>(smem + M::z, i, 2 * part, hw);
                 fence_proxy_async_smem();
-                warp_arrive(bar_d);
-                if (tid == 0) factors_of(c)[0] = s_r;
+                warp_arrive(bar_z);
+                if (tid == 0) factors_of(c)[0] = s_z;
+                scaled<8>(x, br, x);
                 const int t = c * kC + i;
                 if (t < a.d.seqlen) {
                     TG* dv = static_cast<TG*>(a.dv) +
@@ -423,16 +429,16 @@ constexpr int kGradThreads = kSplitThreads;
 constexpr int kMaxPans = 4;
 
 template <int DK> struct GradSmem {
-    // of a head (two in turn): gates, panels of [K | Q], T' (64 rows; the 64 behind them in its
+    // of a head (two in turn): gates, panels of [K | Q], N (64 rows; the 64 behind them in its
     // operand are not read)
     static constexpr uint32_t kq = kGateBytes;
-    static constexpr uint32_t t = kq + kq_bytes(DK);
-    static constexpr uint32_t head = t + kTile;
-    // of a head's 64 columns of headdim (two in turn): R, S0, then [dR; dY], L
+    static constexpr uint32_t nn = kq + kq_bytes(DK);
+    static constexpr uint32_t head = nn + kTile;
+    // of a head's 64 columns of headdim (two in turn): R, S0, then [z; dY], L
     static constexpr uint32_t r = 0;
     static constexpr uint32_t s0 = kTile;
-    static constexpr uint32_t rdo = s0 + h_bytes(DK);
-    static constexpr uint32_t l = rdo + 2 * kTile;
+    static constexpr uint32_t zdy = s0 + h_bytes(DK);
+    static constexpr uint32_t l = zdy + 2 * kTile;
     static constexpr uint32_t stage = l + h_bytes(DK);
     static constexpr uint32_t stages = 2 * head;
     static constexpr uint32_t u = stages + 2 * stage;   // U, then W (rows 64 to 127 of U's
@@ -447,8 +453,8 @@ template <int DK> struct GradSmem {
 struct GradArgs {
     const uint8_t* records;
     const uint8_t* kept;     // R | S0
-    const uint8_t* adjoint;  // dR | dY | L
-    const void *g, *beta;
+    const uint8_t* adjoint;  // z | dY | L
+    const void* g;
     void *dq, *dk, *dg, *dbeta;
     uint32_t* status;
     Dims d;
@@ -476,7 +482,7 @@ __device__ __forceinline__ f2 dot8(uint4 a, uint4 b, f2 s) {
 // The exponent of a power of two, and back (0 for what is too small).
 __device__ __forceinline__ int exponent(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
-// U's products with L and those with dR and dY have one U, whose factor follows L's: columns
+// U's products with L and those with z and dY have one U, whose factor follows L's: columns
 // of headdim with this much less in L than others (with nothing, where no later step read
 // them) are left out of F2, so that their U never loses bits (2^7 or so at most, on fp16's
 // 2^-14 to 2^15).  Products below 2^kNone in all columns count as 0.
@@ -513,7 +519,7 @@ __device__ __forceinline__ int largest_ul(const float* fac, int pans) {
 }
 
 // CTAs walk the chunks and groups of heads; one warp brings in what comes next, one issues the
-// products, U's of the next columns ahead of time.  Rows of products are lanes: steps as k
+// products, E's of the next columns ahead of time.  Rows of products are lanes: steps as k
 // rows (0 to 63) and as q rows (64 to 127).  All wait for one another by mbarriers, so that no
 // step of one warp holds up the others' (242 us for 8 x 2048 steps of 16 heads when the warps on
 // rows met at barriers and did the rest themselves, 220 us now).
@@ -529,8 +535,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     extern __shared__ __align__(1024) uint8_t smem[];
     using M = GradSmem<DK>;
     constexpr int CP = DK / 4;  // pairs of columns of dstate a thread holds
-    // tensor memory: F, then W K; F2; [dA'; dP'], then W^T [K; Q]; U
-    constexpr uint32_t kTmF = 0, kTmW = 0, kTmF2 = 128, kTmA = 256, kTmV = 256, kTmU = 384,
+    // tensor memory: F, then W K; F2; [dA'; dP'], then W^T [K; Q]; E
+    constexpr uint32_t kTmF = 0, kTmW = 0, kTmF2 = 128, kTmA = 256, kTmV = 256, kTmE = 384,
                        kTmCols = 512;
     const uint32_t sb = smem_u32(smem);
     Sums* sums = reinterpret_cast<Sums*>(smem + M::sums);             // [2 heads]
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     uint64_t* empty_h = full + 6;                                  // [2]
     uint64_t* dots_in = full + 8;                                  // [2] a head's sums are there
     uint64_t* dots_out = full + 10;                                // [2]
-    uint64_t* bar_u = full + 12;   // products done: U; F; A and F2; W's two
+    uint64_t* bar_e = full + 12;   // products done: E; F; A and F2; W's two
     uint64_t* bar_f = full + 13;
     uint64_t* bar_a = full + 14;
     uint64_t* bar_w = full + 15;
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     uint64_t* w_in = full + 18;    // W is in shared memory
     uint64_t* w_out = full + 19;   // W's products and F2 have been read
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 20);
-    float* factors = reinterpret_cast<float*>(smem + M::factors);  // R, S0, -, -, dR, dY, L
+    float* factors = reinterpret_cast<float*>(smem + M::factors);  // R, S0, -, -, z, dY, L
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned nc = a.d.chunks, groups = a.d.groups;
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     const uint8_t* adj0 = a.adjoint + ch * pans * adjoint_bytes(DK);
                     mbar_arrive_expect_tx(bh, M::head + 32 * pans);
                     bulk_load(hd, rec, kGateBytes + kq_bytes(DK), bh);
-                    bulk_load(hd + M::t, rec + rec_t(DK), kTile, bh);
+                    bulk_load(hd + M::nn, rec + rec_n(DK), kTile, bh);
                     for (int p = 0; p < pans; ++p) {
                         float* f = factors + 8 * (kMaxPans * (hn & 1) + p);
                         bulk_load(f, kept0 + p * kept_bytes(DK) + kTile + h_bytes(DK), 16, bh);
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         uint64_t* bar = full + (n & 1);
                         mbar_arrive_expect_tx(bar, M::stage);
                         bulk_load(st + M::r, kept0 + p * kept_bytes(DK), kTile + h_bytes(DK), bar);
-                        bulk_load(st + M::rdo, adj0 + p * adjoint_bytes(DK), 2 * kTile + h_bytes(DK), bar);
+                        bulk_load(st + M::zdy, adj0 + p * adjoint_bytes(DK), 2 * kTile + h_bytes(DK), bar);
                     }
                 }
             }
@@ -625,30 +631,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
             constexpr uint32_t idW = idesc_f16(128, DK) | kIdescBMN;
             constexpr uint32_t idV = idesc_f16(128, DK) | kIdescAMN | kIdescBMN;
-            // U = T' R
-            auto multiply_u = [&](int n, int hn) {
+            // E = N R
+            auto multiply_e = [&](int n, int hn) {
                 if (!mbar_poll(full + (n & 1), (n >> 1) & 1, a.status)) return false;
                 const uint32_t st = sb + M::stages + (n & 1) * M::stage, hd = sb + (hn & 1) * M::head;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmU, kdesc<128>(hd + M::t, kk), mdesc(st + M::r, kk, kTile), id64 | kIdescBMN,
+                    mma_f16(tmem + kTmE, kdesc<128>(hd + M::nn, kk), mdesc(st + M::r, kk, kTile), id64 | kIdescBMN,
                             kk > 0);
-                mma_commit(bar_u);
+                mma_commit(bar_e);
                 return true;
             };
-            // F = [dR; dY] S0^T, of columns that are in
+            // F = [z; dY] S0^T, of columns that are in
             auto multiply_f = [&](int n) {
                 const uint32_t st = sb + M::stages + (n & 1) * M::stage;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmF, kdesc<128>(st + M::rdo, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
+                    mma_f16(tmem + kTmF, kdesc<128>(st + M::zdy, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
                 mma_commit(bar_f);
                 return true;
             };
             const int heads = first < a.count ? (int)((a.count - 1 - first) / step + 1) * mine : 0;
-            bool ok = heads > 0 && mbar_poll(full_h, 0, a.status) && multiply_u(0, 0) && multiply_f(0);
+            bool ok = heads > 0 && mbar_poll(full_h, 0, a.status) && multiply_e(0, 0) && multiply_f(0);
             for (int hn = 0, n = 0; hn < heads && ok; ++hn) {
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
                 const uint32_t hd = sb + (hn & 1) * M::head;
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmA, kdesc<128>(st + M::rdo, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
+                        mma_f16(tmem + kTmA, kdesc<128>(st + M::zdy, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
                     if (near) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -672,7 +678,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     }
                     mma_commit(bar_a);
                     if (p + 1 < pans)
-                        ok = multiply_u(n + 1, hn) && mbar_poll(f_out, n & 1, a.status) && multiply_f(n + 1);
+                        ok = multiply_e(n + 1, hn) && mbar_poll(f_out, n & 1, a.status) && multiply_f(n + 1);
                 }
                 ok = ok && mbar_poll(w_in, hn & 1, a.status);
                 if (!ok) break;
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 mma_commit(bar_w);
                 if (hn + 1 < heads)
                     ok = mbar_poll(full_h + ((hn + 1) & 1), ((hn + 1) >> 1) & 1, a.status) &&
-                         multiply_u(n, hn + 1) && mbar_poll(w_out, hn & 1, a.status) && multiply_f(n);
+                         multiply_e(n, hn + 1) && mbar_poll(w_out, hn & 1, a.status) && multiply_f(n);
             }
         } else if (warp >= 10) {
             // ---- the gates: step i
@@ -702,7 +708,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 for (int hh = 0; hh < mine && ok; ++hh, ++hn) {
                     const long long at = ((long long)b * a.d.seqlen + t) * a.d.heads + group * ratio + head_lo + hh;
                     const float g = in ? gate_at(a.g, at, a.gates_bf16) : 0.0f;
-                    const float beta = in ? gate_at(a.beta, at, a.gates_bf16) : 0.0f;
                     const Gates* gates = reinterpret_cast<const Gates*>(smem + (hn & 1) * M::head);
                     const Sums& s = sums[hn & 1];
                     ok = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status) &&
@@ -737,7 +742,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         // none: their gradients are 0
                         const bool cut = ex2_approx(g * kLog2e) == 0.0f || (t == 0 && a.fresh);
                         put_gate(a.dg, at, a.gates_bf16, cut ? 0.0f : up + (down - self) + e_end * all);
-                        put_gate(a.dbeta, at, a.gates_bf16, off ? 0.0f : db / beta);
+                        put_gate(a.dbeta, at, a.gates_bf16, off ? 0.0f : db);
                     }
                 }
             }
@@ -769,6 +774,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
                 bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
                 const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
+                const float b_row = gates->beta[i], b_top = gates->b_top, b_part = b_row * gates->b_down;
                 // a step's row of K or Q, columns col0 + 16 n .. + 15
                 auto own_row = [&](int n16, f2* v) {
                     const int c0 = col0 + 16 * n16;
@@ -779,8 +785,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                     v + 4 * q);
                 };
                 // Products of U and L are summed over the panels where they are: U's factor is
-                // chosen so that all have the same, the largest of theirs.  A panel's own: U is at
-                // most 64 products of 2^13 and 2^15, brought down to 2^15
+                // chosen so that all have the same, the largest of theirs.  A panel's own: E is at
+                // most 64 products of 2^13 and 2^15, and beta at most b_top: brought down to 2^15
                 constexpr float kDown = 1.0f / 524288.0f;
                 const int e_ul = largest_ul(fac, pans);
                 // what the other heads have left in the sums does not belong to this one's dot
@@ -802,19 +808,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 float beta_sum = 0.0f, ls = 0.0f;
                 for (int p = 0; p < pans; ++p, ++n) {
                     const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
-                    const float s_r = fac[8 * p], s_s = fac[8 * p + 1], s_dr = fac[8 * p + 4],
+                    const float s_r = fac[8 * p], s_s = fac[8 * p + 1], s_z = fac[8 * p + 4],
                                 s_dy = fac[8 * p + 5], s_l = fac[8 * p + 6];
                     here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
                     const int below = exponent(s_r) + exponent(s_l) - e_ul;
-                    const float down = kDown * power(max(below, kFar)), s_u = s_r * gates->s_t / down;
+                    const float s_e = s_r * gates->s_n, down = kDown * power(max(below, kFar)),
+                                s_u = s_e * b_top / down;
+                    f2 e_row[16];
                     if (!is_q) {
-                        here = warp_wait(bar_u, n & 1, a.status) && here;
+                        here = warp_wait(bar_e, n & 1, a.status) && here;
                         tc_fence_after();
                         f2 x[16];
                         uint32_t hw[16];
-                        tmem_ld32(t_lane + kTmU + 32 * part, x);
+                        tmem_ld32(t_lane + kTmE + 32 * part, e_row);
                         tmem_wait_ld();
-                        scaled<16>(x, down, x);
+                        scaled<16>(e_row, down * b_part, x);
                         round_to<16>(x, hw);
                         put32(smem + M::u, i, 4 * part, hw);
                         fence_proxy_async_smem();
@@ -823,27 +831,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         tc_fence_before();
                     }
                     if (here) warp_arrive(u_in);
-                    // sums over these columns: dR . R, and L . S0
+                    // sums over these columns: z . E, and L . S0
                     {
-                        f2 dr = 0, dl = 0;
+                        f2 ze = 0, dl = 0;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t at = piece(row, 4 * part + q);
-                            if (!is_q)
-                                dr = dot8(*reinterpret_cast<const uint4*>(sg + M::rdo + at),
-                                          *reinterpret_cast<const uint4*>(sg + M::r + at), dr);
+                            if (!is_q) {
+                                f2 z[4];
+                                unpack8_f16(*reinterpret_cast<const uint4*>(sg + M::zdy + at), z);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) ze = fma2(z[e], e_row[4 * q + e], ze);
+                            }
                             if (row < DK)
                                 dl = dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + at),
                                           *reinterpret_cast<const uint4*>(sg + M::l + at), dl);
                         }
-                        beta_sum = fmaf(s_dr * s_r, sum2(dr), beta_sum);
+                        beta_sum = fmaf(s_z * s_e, sum2(ze), beta_sum);
                         ls = fmaf(s_s * s_l, sum2(dl), ls);
                     }
                     ok = here && warp_wait(bar_f, n & 1, a.status);
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float f1 = (is_q ? er * s_dy : -er * s_dr) * s_s;
+                        const float f1 = (is_q ? er * s_dy : -er * b_row * s_z) * s_s;
                         const f2 f1p = pair(f1, f1);
 #pragma unroll
                         for (int e0 = 0; e0 < CP; e0 += 16) {
@@ -860,7 +871,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float fa = (is_q ? s_dy : -s_dr) * s_u;
+                        const float fa = (is_q ? s_dy : -b_row * s_z) * s_u;
                         const f2 fap = pair(fa, fa);
                         f2 x[16];
                         tmem_ld32(t_lane + kTmA + 32 * part, x);
@@ -915,9 +926,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 {
                     const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
                     const float skq = gates->s_kq, f1 = s_w * skq;
-                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_t / kDown : 0.0f;
+                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_n * b_top / kDown : 0.0f;
                     const f2 f1p = pair(f1, f1), g2p = pair(g2, g2);
-                    f2 whole = 0, read = 0, end = 0, write = 0;  // dots with this row
+                    f2 whole = 0, end = 0, write = 0;  // dots with this row
 #pragma unroll
                     for (int n16 = 0; n16 < CP / 8; ++n16) {
                         f2 v[8], f[8];
@@ -925,10 +936,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         own_row(n16, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            read = fma2(v[e], f[e], read);
-                            acc[8 * n16 + e] = fma2(f1p, f[e], acc[8 * n16 + e]);
-                        }
+                        for (int e = 0; e < 8; ++e) acc[8 * n16 + e] = fma2(f1p, f[e], acc[8 * n16 + e]);
                         if (!is_q) {
                             tmem_ld16(t_lane + kTmV + col0 + 16 * n16, f);
                             tmem_wait_ld();
@@ -949,12 +957,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         for (int e = 0; e < 8; ++e) whole = fma2(v[e], acc[8 * n16 + e], whole);
                     }
                     const float own_dot = skq * (sum2(whole) - before);
-                    const float wk = skq * f1 * sum2(read), wv = skq * f1 * sum2(write),
-                                we = skq * g2 * sum2(end);
+                    const float wv = skq * f1 * sum2(write), we = skq * g2 * sum2(end);
                     s.dot[row][part] = is_q ? own_dot : own_dot - 2.0f * wv - we;
                     if (!is_q) {
                         s.end[i][part] = we;
-                        s.db[i][part] = beta_sum + wk;
+                        s.db[i][part] = beta_sum;
                     }
                     if (lane == 0) s.ls[warp] = ls;
                 }
@@ -1138,7 +1145,7 @@ extern "C" ssm_status_t ssm_gated_delta_bwd(
     c.records = records; c.kept = ws + 1024; c.dlast = dfinal_state; c.dh0 = dinitial_state;
     c.dv = dv; c.status = status; c.d = d;
     GradArgs w{};
-    w.records = records; w.kept = records + rb; w.adjoint = ws + 1024; w.g = g; w.beta = beta;
+    w.records = records; w.kept = records + rb; w.adjoint = ws + 1024; w.g = g;
     w.dq = dq; w.dk = dk; w.dg = dg; w.dbeta = dbeta; w.status = status; w.d = d;
     w.gates_bf16 = gate_dtype == SSM_BF16;
     w.fresh = !initial_state;

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from tests.helpers import to64
-from tests.test_gated_delta_gpu import BF16, F32, cuda, forward, inputs, kept_for, reference
+from tests.test_gated_delta_gpu import (BF16, BWD, F32, FWD, GATES, ROUND, backward, check_grads, cuda, forward, inputs,
+                                        kept_for, off, reference, reference_grads)
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +25,59 @@ def test_y_in_bf16_is_rounded_once(n, h, dk, dv, keep):
     # sums) of up to 192 terms of either sign, in sum below 8 times the largest result
     ref = reference(t)[0]
     assert (np.abs(to64(y) - ref) <= np.abs(ref) * 2.0 ** -8 + np.abs(ref).max() * 2.0 ** -17).all()
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("small", [1e-3, 1e-6, 1e-9, 1e-12, 1e-20, 1e-30])
+@pytest.mark.parametrize("n,h,dk,dv", [(150, 4, 64, 64), (200, 2, 128, 128), (70, 6, 72, 136)])
+def test_small_betas_beside_others(small, gt, n, h, dk, dv):
+    """A step that learns next to nothing has a gradient of beta as large as the others': (L k) . e,
+    which is not a difference of anything rounded with beta in it.  Its own steps are held to what
+    all are: sums of products of either sign of operands rounded to fp16."""
+    t = inputs(1, n, h, h // 2, dk, dv, seed=n, gt=gt)
+    at = torch.arange(n) % 8 == 3
+    t["beta"][:, at] = (small * (0.5 + torch.rand(1, int(at.sum()), h))).to(gt)
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    assert off(y, y_ref) < FWD and off(last, last_ref) < FWD
+    kept = kept_for(c)
+    forward(c, checkpoints=kept)
+    for kw in ({}, {"checkpoints": kept}):
+        g, ref = backward(c, grad_dtype=F32, **kw), reference_grads(t)
+        check_grads(g, ref, gt, F32)
+        rounding = ROUND if gt == BF16 else 0
+        assert off(g["dbeta"][:, at], ref["dbeta"][:, at.numpy()]) < GATES + rounding
+        assert off(g["dv"][:, at], ref["dv"][:, at.numpy()]) < FWD
+
+
+def test_betas_from_0_to_1_alone():
+    """Every step's beta another power of two, down to 2^-100, in no order."""
+    t = inputs(1, 320, 2, 2, 64, 64, seed=21, masked=0)
+    t["beta"] = 2.0 ** -torch.randint(0, 101, (1, 320, 2)).float()
+    g, ref = backward(cuda(t), grad_dtype=F32), reference_grads(t)
+    check_grads(g, ref, F32, F32)
+    for lo, hi in ((1.0, 2.0 ** -9), (2.0 ** -10, 2.0 ** -40), (2.0 ** -41, 2.0 ** -100)):
+        at = ((t["beta"] <= lo) & (t["beta"] >= hi))[0].numpy()
+        assert off(g["dbeta"].cpu()[0][torch.from_numpy(at)], ref["dbeta"][0][at]) < GATES
+
+
+@pytest.mark.parametrize("top", [1.9, 100.0, -1.0])
+def test_betas_above_1_and_below_0(top):
+    """Short keys: beta k . k stays below 1 (or above -1), so that no state grows faster than its
+    gates let it shrink."""
+    t = inputs(1, 150, 4, 2, 64, 72, seed=22)
+    t["k"] = (t["k"].float() * abs(top) ** -0.5).to(BF16)
+    t["beta"] = t["beta"] * top
+    if top < 0:
+        t["g"] -= 0.7
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    # (below 0 the triangle's inverse grows: 1 + k . k a step, in whose span the gates halve it)
+    wide = 2 if top < 0 else 1
+    assert off(y, y_ref) < wide * FWD and off(last, last_ref) < wide * FWD
+    got, ref = backward(c, grad_dtype=F32), reference_grads(t)
+    for name, tol in (("dq", BWD), ("dk", BWD), ("dv", FWD), ("dinitial_state", FWD), ("dg", GATES),
+                      ("dbeta", GATES)):
+        assert off(got[name], ref[name]) < wide * tol, name
