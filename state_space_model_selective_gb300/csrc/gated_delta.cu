@@ -281,8 +281,8 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
     float* s_dec = s_beta + kC;                                   // [32]: decays to step 31
     float* s_inv = s_dec + 32;                                    // [64]: inverse ones from 0 or 32
     float* s_span = s_inv + kC;                                   // [2]: their largest logarithm
-    float* s_most = s_span + 4;                                   // [3][8]
-    long long* s_sum = reinterpret_cast<long long*>(s_most + 24);
+    float* s_most = s_span + 4;                                   // [4][8]
+    long long* s_sum = reinterpret_cast<long long*>(s_most + 32);
     uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
     uint64_t* bar_mma = bar_in + 1;
@@ -386,31 +386,61 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         }
         if (more) fetch(chunk_of(item + step));
 
-        // ---- K and Q to fp16, in place, under one factor.  Steps that learn nothing: their
-        // keys are not looked at
+        // ---- K and Q to fp16, in place.  Steps that learn nothing: their keys are not looked at
         ok = warp_wait(bar_in, in_phase, a.status);
         in_phase ^= 1;
         landing = false;
         uint4 raw[NP * 4];
-        MostBf16 seen;
+        MostBf16 seen, seen_q[2];  // K, and two steps of Q (8 lanes to a step)
+        const int r0 = tid >> 3;   // this thread's steps are r0 and r0 + 32
 #pragma unroll
         for (int e = 0; e < NP * 4; ++e) {
-            const int at = tid + kRecThreads * e, r = (at >> 3) & 127;
-            raw[e] = *reinterpret_cast<const uint4*>(smem + M::kq + at * 16);
-            if (r < kC && (masked >> r & 1)) raw[e] = make_uint4(0, 0, 0, 0);
-            seen.see(raw[e]);
+            raw[e] = *reinterpret_cast<const uint4*>(smem + M::kq + (tid + kRecThreads * e) * 16);
+            if (e & 2) {
+                seen_q[e & 1].see(raw[e]);
+            } else {
+                if (masked >> (r0 + 32 * (e & 1)) & 1) raw[e] = make_uint4(0, 0, 0, 0);
+                seen.see(raw[e]);
+            }
         }
-        float most = warp_most(seen.value());
-        if (lane == 0) s_most[warp] = most;
+        float most = warp_most(seen.value()), most_q = 0.0f;
+        // the steps whose q a common factor is for: those that learn, or all if none does
+        const unsigned long long apart = ~masked == 0 ? 0 : masked;
+        float own_q[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float m = seen_q[n].value();
+            if (apart >> (r0 + 32 * n) & 1) {
+                own_q[n] = m;
+            } else {
+                own_q[n] = 0.0f;
+                most_q = fmaxf(most_q, m);
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) own_q[n] = fmaxf(own_q[n], __shfl_xor_sync(0xffffffffu, own_q[n], o));
+        }
+        most_q = warp_most(most_q);
+        if (lane == 0) {
+            s_most[warp] = most;
+            s_most[24 + warp] = most_q;
+        }
         ok = named_bar_and(1, kRecThreads, ok);
-        float s_kq;
-        const float kq_scale = tile_scale(most_of<8>(s_most), kTop, s_kq);
+        float s_k, s_q[2], q_scale[2];
+        most = most_of<8>(s_most);
+        const float k_scale = tile_scale(most, kTop, s_k);
+        most_q = most_of<8>(s_most + 24);
+        if (most_q > 0.0f) most = most_q;  // (steps that do not ask: the keys' does as well)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            q_scale[n] = tile_scale(fmaxf(most, own_q[n]), kTop, s_q[n]);
+            if ((tid & 7) == 0) gates->s_q[r0 + 32 * n] = (uint16_t)(__float_as_uint(s_q[n]) >> 16);
+        }
 #pragma unroll
         for (int e = 0; e < NP * 4; ++e) {
             f2 x[4];
             uint32_t w[4];
             unpack8_bf16(raw[e], x);
-            scaled<4>(x, kq_scale, x);
+            scaled<4>(x, e & 2 ? q_scale[e & 1] : k_scale, x);
             round_to<4>(x, w);
             *reinterpret_cast<uint4*>(smem + M::kq + (tid + kRecThreads * e) * 16) =
                 make_uint4(w[0], w[1], w[2], w[3]);
@@ -423,7 +453,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             if (lane == 0) s_span[warp] = span;
         }
         if (tid == 0) {
-            gates->s_kq = s_kq;
+            gates->s_k = s_k;
             gates->e_max = fmaxf(s_most[8], s_most[9]);
             const float b = fmaxf(fmaxf(s_most[16], s_most[17]), 1.0f);
             const uint32_t top = (__float_as_uint(b) + 0x7fffffu) & 0xff800000u;
@@ -458,7 +488,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             tmem_ld32(t_lane + kTmX + 32 * part, x);
             tmem_wait_ld();
             const float hi = gates->hi[i], lo = gates->lo[i];
-            const float f = s_kq * s_kq * (is_q ? 1.0f : row_beta(s_beta[i]));
+            const float f = is_q ? s_k : s_k * s_k * row_beta(s_beta[i]);
             const int j0 = 32 * part;
             const int last = is_q ? i : i - 1;  // of the columns that count
             if (part == 0 && (quarter & 1) && !grows) {
@@ -672,7 +702,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         }
         tc_fence_before();
         if (tid == 0) {
-            gates->s_h = s_h2 * s_kq * s_w;
+            gates->s_h = s_h2 * s_k * s_w;
             gates->s_p = s_p2 * s_p * s_t;
         }
         fence_proxy_async_smem();
@@ -964,21 +994,24 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         f2 S[SC / 2];      // times its operand's factor; s_s undoes it
         float s_s = 0.0f;
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float f_k = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f, b_part = 0.0f, b_top = 1.0f;
+        float f_k = 0.0f, f_q = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f, b_part = 0.0f,
+              b_top = 1.0f;
         bool off = true;
         // the gates of chunk c, and the largest values of its V (upper warps)
         auto gates_of = [&](int c) {
             const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
-            f_k = ex2_approx(g->hi[i] + g->lo[i]) * g->s_kq;
+            const float e_row = ex2_approx(g->hi[i] + g->lo[i]);
+            f_k = e_row * g->s_k;
+            f_q = e_row * g->q_factor(i);
             e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
             off = g->masked >> i & 1;
             s_h = g->s_h;
-            s_p = g->s_p;
+            s_p = g->s_p * g->q_factor(i);
             b_part = g->beta[i] * g->b_down;
             b_top = g->b_top;
             // of e |K|_1 over a row, in units of the largest S
-            k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_kq;
+            k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_k;
             if (upper) {
                 MostBf16 seen;
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
@@ -1030,7 +1063,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         }
         for (int c = 0; c < nc && ok; ++c) {
             const uint32_t ph = c & 1;
-            const float fs = f_k * s_s, ee = e_end, sp = s_p, sh = s_h;
+            const float fs = f_k * s_s, fq = f_q * s_s, ee = e_end, sp = s_p, sh = s_h;
             float s_max, v_max;
             ok = read_most<NW / 4>(s_most + kMosts * ph, c, s_max, a.status) &&
                  read_most<NW / 8>(s_most + kMosts * ph + NW, c, v_max, a.status);
@@ -1120,7 +1153,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             if (a.y && t < a.d.seqlen) {
                 TO* y = static_cast<TO*>(a.y) +
                         (((long long)b * a.d.seqlen + t) * a.d.heads + h) * a.d.dv + col0;
-                const f2 f = pair(sp * s_br, sp * s_br), q = pair(fs, fs);
+                const f2 f = pair(sp * s_br, sp * s_br), q = pair(fq, fq);
 #pragma unroll
                 for (int e = 0; e < SC / 2; ++e) x[e] = fma2(q, x[e], mul2(f, z[e]));
                 store_row<SC / 2>(y, x, col0, a.d.dv, rows_of_sectors(a.y, a.d.dv));

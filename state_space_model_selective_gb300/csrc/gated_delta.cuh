@@ -42,10 +42,15 @@ struct Gates {
     float hi[kC], lo[kC];
     float beta[kC];
     unsigned long long masked;
-    float s_kq, s_h, s_p, s_n;
+    float s_k, s_h, s_p, s_n;
     float e_max;   // the largest decay from the chunk's start to a step
     float b_top, b_down;  // a power of two that no beta is above, 1 at least, and its inverse
+    uint16_t s_q[kC];        // in bf16
+    __device__ __forceinline__ float q_factor(int i) const { return __uint_as_float((uint32_t)s_q[i] << 16); }
 };
+// Q has a factor of its own, s_q, for each step: the same for all that learn, so that dY may enter
+// products with P (held without s_q) and Q under s_q; a masked step whose q is larger than theirs (it may
+// be padding) has its own and takes none of their bits.
 constexpr uint32_t kGateBytes = 1024;
 static_assert(sizeof(Gates) <= kGateBytes, "gates fit their place");
 
@@ -190,6 +195,9 @@ __device__ __forceinline__ float tile_scale(float most, int top, float& back) {
     back = __uint_as_float((254u - g) << 23);
     return __uint_as_float(g << 23);
 }
+// A product of a tile's factor with others: it overflows where the tile's values are 0, or so small
+// that they count as 0, and must leave them that.
+__device__ __forceinline__ float finite_factor(float f) { return f > 1.7e38f ? 1.7e38f : f; }
 constexpr int kTop = 12;    // of a measured maximum
 constexpr int kBoundTop = 14;  // of a bound
 // The largest stored magnitude of a tile scaled by its maximum.

@@ -232,15 +232,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                             2 * kTile + h_bytes(DK));
         };
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_kq = 0.0f, s_h = 0.0f, s_p = 0.0f, b_row = 0.0f,
-              b_top = 1.0f;
+        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_k = 0.0f, s_h = 0.0f, s_p = 0.0f, b_row = 0.0f,
+              b_top = 1.0f, s_q = 0.0f;
         auto gates_of = [&](int it) {
             const bool in = warp_wait(full + (it & 1), (it >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (it & 1) * M::stage);
             e_row = ex2_approx(g->hi[i] + g->lo[i]);
             e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
             e_max = fmaxf(g->e_max, 1.0f);
-            s_kq = g->s_kq;
+            s_k = g->s_k;
+            s_q = g->q_factor(i);
             s_h = g->s_h;
             s_p = g->s_p;
             b_row = g->beta[i];
@@ -272,8 +273,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                   col0 + 8 * p)
                             : make_uint4(0, 0, 0, 0);
         };
-        // (upper warps) dY and e dY of step `it` as operands, dY kept
-        auto put_dy = [&](int it, float e) {
+        // (upper warps) dY and e dY, times Q's factors, of step `it` as operands, dY kept
+        auto put_dy = [&](int it, float e, float sq) {
             f2 x[8], y[8];
             MostBf16 seen;
 #pragma unroll
@@ -281,18 +282,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 seen.see(dy[p]);
                 unpack8_bf16(dy[p], x + 4 * p);
             }
-            const float m = warp_most(seen.value());
+            const float m = warp_most(seen.value() * sq);
             uint32_t* most = s_most + kMosts * (it & 1) + kRowWarps;
             if (lane == 0) post_most(most + (quarter & 1) * 4 + part, m, it);
             float all = 0.0f;
             const bool told = read_most<2>(most, it, all, a.status);
             float s_dy, s_o;
             uint32_t hw[8], lw[8];
-            scaled<8>(x, tile_scale(all, kTop, s_dy), y);
+            scaled<8>(x, finite_factor(sq * tile_scale(all, kTop, s_dy)), y);
             round_to<8>(y, hw);
             put_pieces<2>(smem + M::dy, i, 2 * part, hw);
             if (tid == 64) factors_of(nc - 1 - it)[1] = s_dy;
-            scaled<8>(x, e * tile_scale(all * e_max, kBoundTop, s_o), x);
+            scaled<8>(x, finite_factor(e * finite_factor(sq * tile_scale(all * e_max, kBoundTop, s_o))), x);
             split<8>(x, hw, lw);
             put_pieces<2>(smem + M::o_hi, i, 2 * part, hw);
             put_pieces<2>(smem + M::o_lo, i, 2 * part, lw);
@@ -310,14 +311,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         bool ok = gates_of(0);  // the same for all lanes of a warp
         fetch(nc - 1);
-        if (upper) ok = put_dy(0, e_row) && ok;
+        if (upper) ok = put_dy(0, e_row, s_q) && ok;
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
-            const float er = e_row, ee = e_end, em = e_max, skq = s_kq, sh = s_h, sp = s_p, br = b_row;
+            const float er = e_row, ee = e_end, em = e_max, sk = s_k, sh = s_h, sp = s_p, br = b_row;
             if (c > 0) fetch(c - 1);
             f2 x[8];
-            // bounds: of L and dY measured, of z, dR and the next L from them
+            // bounds: of L and dY (times Q's factors) measured, of z, dR and the next L from them
             float l_max = 0.0f, dy_max = 0.0f;
             ok = ok && read_most<4>(s_most + kMosts * ph, it, l_max, a.status) &&
                  read_most<2>(s_most + kMosts * ph + kRowWarps, it, dy_max, a.status);
@@ -328,8 +329,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             (void)tile_scale(dy_max, kTop, s_dyd);
             const float z_scale = tile_scale(z_bound, kBoundTop, s_z);
             const float g_scale = tile_scale(dr_bound * em, kBoundTop, s_g);
-            const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f * skq * em *
-                                                              (dy_max + dr_bound)), kBoundTop, s_next);
+            const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f * em *
+                                                              (dy_max + sk * dr_bound)), kBoundTop, s_next);
             ok = ok && warp_wait(bar_x, ph, a.status);
             tc_fence_after();
             if (ok) {
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                 for (int e = 0; e < 8; ++e) x[e] = add2(x[e], xch[64 * e]);
                 uint32_t hw[8], lw[8];
                 f2 y[8];
-                scaled<8>(x, -er * br * g_scale, y);
+                scaled<8>(x, -finite_factor(er * br * g_scale), y);
                 split<8>(y, hw, lw);
                 put_pieces<2>(smem + M::r_hi, i, 2 * part, hw);
                 put_pieces<2>(smem + M::r_lo, i, 2 * part, lw);
@@ -393,16 +394,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             };
             ok = warp_wait(bar_q, ph, a.status);
             tc_fence_after();
-            if (ok) add(kTmQ, skq * s_od * next);
+            if (ok) add(kTmQ, s_od * next);
             if (c > 0) {
                 ok = gates_of(it + 1) && ok;
                 // (the products that read dY and e dY are done: bar_q follows them)
-                if (upper) ok = put_dy(it + 1, e_row) && ok;
+                if (upper) ok = put_dy(it + 1, e_row, s_q) && ok;
             }
             ok = ok && warp_wait(bar_l, ph, a.status);
             tc_fence_after();
             if (ok) {
-                add(kTmK, skq * s_g * next);
+                add(kTmK, sk * s_g * next);
                 if (c > 0) put_state(it + 1);
             }
         }
@@ -774,7 +775,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
                 bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
                 const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
-                const float b_row = gates->beta[i], b_top = gates->b_top, b_part = b_row * gates->b_down;
+                // dY's rows are kept times Q's factors (powers of two): what undoes it
+                auto inv_q = [&]() { return __uint_as_float((254u << 23) - __float_as_uint(gates->q_factor(i))); };
                 // a step's row of K or Q, columns col0 + 16 n .. + 15
                 auto own_row = [&](int n16, f2* v) {
                     const int c0 = col0 + 16 * n16;
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
                     const int below = exponent(s_r) + exponent(s_l) - e_ul;
                     const float s_e = s_r * gates->s_n, down = kDown * power(max(below, kFar)),
-                                s_u = s_e * b_top / down;
+                                s_u = s_e * gates->b_top / down;
                     f2 e_row[16];
                     if (!is_q) {
                         here = warp_wait(bar_e, n & 1, a.status) && here;
@@ -822,7 +824,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         uint32_t hw[16];
                         tmem_ld32(t_lane + kTmE + 32 * part, e_row);
                         tmem_wait_ld();
-                        scaled<16>(e_row, down * b_part, x);
+                        scaled<16>(e_row, down * gates->b_down * gates->beta[i], x);
                         round_to<16>(x, hw);
                         put32(smem + M::u, i, 4 * part, hw);
                         fence_proxy_async_smem();
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float f1 = (is_q ? er * s_dy : -er * b_row * s_z) * s_s;
+                        const float f1 = (is_q ? er * (s_dy * inv_q()) : -er * gates->beta[i] * s_z) * s_s;
                         const f2 f1p = pair(f1, f1);
 #pragma unroll
                         for (int e0 = 0; e0 < CP; e0 += 16) {
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float fa = (is_q ? s_dy : -b_row * s_z) * s_u;
+                        const float fa = (is_q ? s_dy : -gates->beta[i] * s_z * gates->s_k) * s_u;
                         const f2 fap = pair(fa, fa);
                         f2 x[16];
                         tmem_ld32(t_lane + kTmA + 32 * part, x);
@@ -883,7 +885,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 }
                 if (!ok) break;
 
-                // ---- W = [dKK; dQK]
+                // ---- W = [dKK; dQK], rows times K's and Q's factors: as W^T [K; Q] needs them
                 {
                     const float hi = -gates->hi[i], lo = -gates->lo[i];
                     const f2 mh = pair(hi, hi), ml = pair(lo, lo);
@@ -925,8 +927,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 tc_fence_after();
                 {
                     const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
-                    const float skq = gates->s_kq, f1 = s_w * skq;
-                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_n * b_top / kDown : 0.0f;
+                    const float f1 = is_q ? s_w * (gates->s_k * inv_q()) : s_w;
+                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_n * gates->b_top / kDown : 0.0f;
                     const f2 f1p = pair(f1, f1), g2p = pair(g2, g2);
                     f2 whole = 0, end = 0, write = 0;  // dots with this row
 #pragma unroll
@@ -956,8 +958,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
 #pragma unroll
                         for (int e = 0; e < 8; ++e) whole = fma2(v[e], acc[8 * n16 + e], whole);
                     }
-                    const float own_dot = skq * (sum2(whole) - before);
-                    const float wv = skq * f1 * sum2(write), we = skq * g2 * sum2(end);
+                    const float s_row = is_q ? gates->q_factor(i) : gates->s_k;
+                    const float own_dot = s_row * (sum2(whole) - before);
+                    const float wv = s_row * f1 * sum2(write), we = s_row * g2 * sum2(end);
                     s.dot[row][part] = is_q ? own_dot : own_dot - 2.0f * wv - we;
                     if (!is_q) {
                         s.end[i][part] = we;

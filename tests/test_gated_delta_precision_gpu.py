@@ -81,3 +81,69 @@ def test_betas_above_1_and_below_0(top):
     for name, tol in (("dq", BWD), ("dk", BWD), ("dv", FWD), ("dinitial_state", FWD), ("dg", GATES),
                       ("dbeta", GATES)):
         assert off(got[name], ref[name]) < wide * tol, name
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -20, 2.0 ** 12, 2.0 ** 30, 2.0 ** 90])
+def test_queries_of_any_size(scale):
+    """Keys do not lose bits by large queries: y scales with q, the state is untouched."""
+    t = inputs(2, 150, 4, 2, 64, 64, seed=23)
+    t["q"] = t["q"] * scale
+    y_ref, last_ref = reference(t)
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    assert off(y, y_ref) < FWD and off(last, last_ref) < FWD
+    t["dy"], t["dfinal"] = t["dy"] / scale, t["dfinal"]
+    check_grads(backward(cuda(t), grad_dtype=F32), reference_grads(t), F32, F32)
+
+
+@pytest.mark.parametrize("n,h,dk,dv", [(150, 4, 64, 64), (200, 2, 128, 72), (130, 160, 64, 64)])
+@pytest.mark.parametrize("huge", [1e3, 1e10, 3e38])
+def test_queries_of_padding_take_no_bits(huge, n, h, dk, dv):
+    """A padded batch whose masked steps hold any finite q (memory that nobody wrote): all other
+    steps are as exact as without them, forward and gradient (theirs has dy 0)."""
+    t = inputs(1, n, h, h // 2, dk, dv, seed=24)
+    pad = torch.zeros(1, n, dtype=torch.bool)
+    pad[:, n // 2 + 7:] = True
+    pad[:, 20:23] = True
+    t["beta"], t["g"] = (t[k].masked_fill(pad[..., None], 0.0) for k in ("beta", "g"))
+    t["dy"] = t["dy"].masked_fill(pad[..., None, None], 0.0)
+    y_ref, last_ref = reference(t)
+    ref = reference_grads(t)
+    t["q"] = torch.where(pad[..., None, None], (torch.randn(t["q"].shape) * huge).clamp(-3e38, 3e38).to(BF16), t["q"])
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    valid = (~pad[0]).nonzero()[:, 0]
+    assert off(y[:, valid], y_ref[:, valid.numpy()]) < FWD and off(last, last_ref) < FWD
+    g = backward(c, grad_dtype=F32)
+    check_grads(g, ref, F32, F32)
+
+
+@pytest.mark.parametrize("learners", [0.0, 2.0 ** -9, 1.0])
+def test_masked_steps_that_ask(learners):
+    """Steps that learn nothing but read: their q, larger or smaller than the others' (whose is small
+    or 0 where they only learn), counts; which they are differs from head to head."""
+    t = inputs(1, 200, 4, 2, 64, 64, seed=25, masked=0.4)
+    t["beta"][:, 64:128] = 0         # a chunk that learns nothing
+    t["q"] = torch.where((t["beta"] > 0).any(-1)[..., None, None], t["q"] * learners, t["q"])
+    t["q"][:, 1::3] *= 64
+    t["q"][:, 2::7] *= 2.0 ** -9
+    t["q"][:, 5] = 0
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    assert off(y, y_ref) < FWD and off(last, last_ref) < FWD
+    g, ref = backward(c, grad_dtype=F32), reference_grads(t)
+    check_grads(g, ref, F32, F32)
+    for i in (5, 60, 150):
+        assert off(g["dq"][:, i], ref["dq"][:, i]) < 2 * BWD  # (one step, not the mean of many)
+
+
+def test_growth_without_gradients():
+    """Chunks that grow by e^12 and hold no gradient: they are 0, not 0 times infinity."""
+    t = inputs(1, 256, 2, 2, 64, 64, seed=26, restart=0)
+    t["g"][:, 64:128, 0], t["g"][:, 192:256, 0] = 0.19, 0.19
+    t["g"][:, 128:192, 0] -= 0.2
+    t["dy"][:, 64:, 0], t["dfinal"][:, 0] = 0, 0
+    g, ref = backward(cuda(t), grad_dtype=F32), reference_grads(t)
+    check_grads(g, ref, F32, F32)
+    assert not g["dv"][:, 64:, 0].any() and not g["dq"][:, 64:, 0].any()
