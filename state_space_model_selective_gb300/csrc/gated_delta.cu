@@ -152,7 +152,7 @@ template <int DK> struct RecSmem {
     static constexpr uint32_t n = p_lo + kTile;          // b^-1 T b
     static constexpr uint32_t gates = n + kTile;         // as the record has them
     static constexpr uint32_t misc = gates + kGateBytes;
-    static constexpr uint32_t bytes = misc + 1024;
+    static constexpr uint32_t bytes = misc + 1536;
     // A, then T (fp32), in the place of T's and its w's first tile; H and P leave from there too
     static constexpr uint32_t tri = t_hi;
     static constexpr uint32_t tmp = w_lo;
@@ -286,6 +286,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
     uint32_t* s_flags = reinterpret_cast<uint32_t*>(s_sum + 1);   // masked, NaN, growing: two words each
     uint64_t* bar_in = reinterpret_cast<uint64_t*>(s_flags + 6);
     uint64_t* bar_mma = bar_in + 1;
+    float* s_e = reinterpret_cast<float*>(smem + M::misc + 1024);  // [64]: decays from the chunk's start; [3][8]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane, i = row & 63;
@@ -377,6 +378,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             if (tid == 0) gates->masked = masked;
             gates->beta[tid] = beta;
             const float e = ex2_approx(hi + lo);
+            s_e[tid] = e;
             // (a beta that is not finite spoils its chunk whatever it is held under)
             const float m = warp_most(e), mb = warp_most(fabsf(beta) < 1e38f ? fabsf(beta) : 0.0f);
             if (lane == 0) {
@@ -458,7 +460,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
             const float b = fmaxf(fmaxf(s_most[16], s_most[17]), 1.0f);
             const uint32_t top = (__float_as_uint(b) + 0x7fffffu) & 0xff800000u;
             gates->b_top = __uint_as_float(top);
-            gates->b_down = __uint_as_float((254u << 23) - top);
+            gates->b_down = inverse(gates->b_top);
         }
         fence_proxy_async_smem();
         named_bar_sync(1, kRecThreads);
@@ -704,6 +706,37 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         if (tid == 0) {
             gates->s_h = s_h2 * s_k * s_w;
             gates->s_p = s_p2 * s_p * s_t;
+            gates->h_e = kTopValue * gates->s_h * gates->b_top;  // (without growth a step's decay is 1 at most)
+            gates->p_e = kC * kTopValue * gates->s_p * gates->b_top;
+            gates->n_e = kTopValue * gates->s_n;
+        }
+        if (grows) {  // from the operands' hi parts as they lie there, a thread's own
+            auto most_e = [&](uint32_t tile, int r, int c0, int n, bool in) {
+                float m = 0.0f;
+#pragma unroll 1
+                for (int c = c0; in && c < c0 + n; ++c) {
+                    f2 y[4];
+                    unpack8_f16(*reinterpret_cast<const uint4*>(smem + tile + piece(r, c)), y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a0, a1;
+                        unpair(mul2(y[e], *reinterpret_cast<const f2*>(s_e + 8 * c + 2 * e)), a0, a1);
+                        m = fmaxf(m, fmaxf(fabsf(a0), fabsf(a1)));
+                    }
+                }
+                return warp_most(m);
+            };
+            const float me[3] = {most_e(M::t_hi, row, 4 * part, 4, row < DK), most_e(M::p_hi, i, 4 * part, 4, is_q),
+                                 most_e(M::n, tid >> 2, (tid & 3) * 2, 2, a.keep_n)};
+            if (lane == 0)
+                for (int n = 0; n < 3; ++n) s_e[kC + 8 * n + warp] = me[n];
+            named_bar_sync(1, kRecThreads);
+            if (tid == 0) {
+                // (an operand's rounding is 2^-11)
+                gates->h_e = 1.001f * most_of<8>(s_e + kC) * gates->s_h * gates->b_top;
+                gates->p_e = kC * 1.001f * most_of<8>(s_e + kC + 8) * gates->s_p * gates->b_top;
+                gates->n_e = 1.001f * most_of<8>(s_e + kC + 16) * gates->s_n;
+            }
         }
         fence_proxy_async_smem();
         named_bar_sync(1, kRecThreads);
@@ -799,8 +832,8 @@ struct ChainArgs {
 //
 // The factors of S and R have to be known before they are written, and a reduction over
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
-// |S1| <= e_63 |S| + |H|_1 |b| |R|, with the measured maxima of V and S, found while products
-// run.  A bound 2^20 too large would still leave 20 bits.
+// |S1| <= e_63 |S| + |b| (|H|_1 |V| + |H e|_1 |K|_1 |S|), with the measured maxima of V and S,
+// found while products run.  A bound 2^20 too large would still leave 20 bits.
 template <int DK, int PW, typename TO, bool FLAGS>
 __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainArgs& a, uint8_t* smem,
                                           uint32_t tmem, unsigned index) {
@@ -994,7 +1027,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         f2 S[SC / 2];      // times its operand's factor; s_s undoes it
         float s_s = 0.0f;
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float f_k = 0.0f, f_q = 0.0f, e_end = 0.0f, k_bound = 0.0f, s_h = 0.0f, s_p = 0.0f, b_part = 0.0f,
+        float f_k = 0.0f, f_q = 0.0f, e_end = 0.0f, k_bound = 0.0f, h_bound = 0.0f, s_h = 0.0f, s_p = 0.0f, b_part = 0.0f,
               b_top = 1.0f;
         bool off = true;
         // the gates of chunk c, and the largest values of its V (upper warps)
@@ -1010,8 +1043,10 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             s_p = g->s_p * g->q_factor(i);
             b_part = g->beta[i] * g->b_down;
             b_top = g->b_top;
-            // of e |K|_1 over a row, in units of the largest S
-            k_bound = fmaxf(g->e_max, 1.0f) * (DK * kTopValue) * g->s_k;
+            // of |K|_1 over a row, in units of the largest S; of what H takes from that
+            k_bound = (DK * kTopValue) * g->s_k;
+            h_bound = kC * g->h_e * k_bound;
+            k_bound *= fmaxf(g->e_max, 1.0f);
             if (upper) {
                 MostBf16 seen;
                 const uint8_t* tile = smem + (c & 1) * M::stage + M::v;
@@ -1073,7 +1108,8 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             const float r_scale = tile_scale(r_bound, kBoundTop, s_r);
             const float s_br = s_r * b_top;
             // |H|_1 over a row is at most 64 times its largest value
-            const float next = tile_scale(fmaf(ee, s_max, kC * 2 * kTopValue * sh * b_top * r_bound), kBoundTop, s_next);
+            const float next = tile_scale(fmaf(h_bound + ee, s_max, kC * 2 * kTopValue * sh * b_top * v_max),
+                                          kBoundTop, s_next);
             // ---- R, times its factor, and b R, times b_top less
             {
                 uint8_t* tile = smem + (c & 1) * M::stage + M::v;
@@ -1109,7 +1145,16 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(bar_r);
-                if (PW == 64 && a.kept && tid == 0) factors_of(c)[0] = s_r;
+                if (PW == 64 && a.kept && tid == 0) {
+                    const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
+                    float s_u;
+                    (void)tile_scale(kC * b_top * fmaf(kTopValue * g->s_n, v_max, g->n_e * (DK * kTopValue * g->s_k) * s_max),
+                                     kBoundTop, s_u);
+                    float* f = factors_of(c);
+                    f[0] = s_r * g->s_n;
+                    f[2] = s_u;
+                    f[3] = f[0] * inverse(s_u);
+                }
             }
             // ---- the state, times its next factor; the next chunk's gates meanwhile
             scaled<SC / 2>(S, ee * s_s * next, S);

@@ -45,6 +45,9 @@ struct Gates {
     float s_k, s_h, s_p, s_n;
     float e_max;   // the largest decay from the chunk's start to a step
     float b_top, b_down;  // a power of two that no beta is above, 1 at least, and its inverse
+    // no |H e b|, 64 |P e b| or |N e| is above these, e and b of the column's step: of products with
+    // what has decayed (or grown) since the chunk's start
+    float h_e, p_e, n_e;
     uint16_t s_q[kC];        // in bf16
     __device__ __forceinline__ float q_factor(int i) const { return __uint_as_float((uint32_t)s_q[i] << 16); }
 };
@@ -66,8 +69,9 @@ __host__ __device__ constexpr uint32_t rec_p(int dk) { return rec_h(dk) + 2 * h_
 __host__ __device__ constexpr uint32_t rec_n(int dk) { return rec_p(dk) + 2 * kTile; }
 __host__ __device__ constexpr uint32_t rec_bytes(int dk) { return rec_n(dk) + kTile; }
 // What training keeps for each chunk, head and 64 columns of headdim, rounded to one fp16:
-// R | S0 | their factors (forward), z | dY | L | their factors (gradient).  Only dq, dk, dg and
-// dbeta come from them.
+// R | S0 | factors (forward), z | dY | L | their factors (gradient).  Only dq, dk, dg and dbeta come
+// from them.  The forward's factors: of E = N R (the products of the tiles), of S0, of U (from a
+// bound), and what takes E to U's.
 constexpr uint32_t kFactorBytes = 128;
 __host__ __device__ constexpr uint32_t kept_bytes(int dk) { return kTile + h_bytes(dk) + kFactorBytes; }
 __host__ __device__ constexpr uint32_t adjoint_bytes(int dk) { return 2 * kTile + h_bytes(dk) + kFactorBytes; }
@@ -195,6 +199,8 @@ __device__ __forceinline__ float tile_scale(float most, int top, float& back) {
     back = __uint_as_float((254u - g) << 23);
     return __uint_as_float(g << 23);
 }
+// The inverse of a power of two.
+__device__ __forceinline__ float inverse(float v) { return __uint_as_float((254u << 23) - __float_as_uint(v)); }
 // A product of a tile's factor with others: it overflows where the tile's values are 0, or so small
 // that they count as 0, and must leave them that.
 __device__ __forceinline__ float finite_factor(float f) { return f > 1.7e38f ? 1.7e38f : f; }

@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                                             2 * kTile + h_bytes(DK));
         };
         // what a chunk's rows take from its gates, read before the stage can be refilled
-        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_k = 0.0f, s_h = 0.0f, s_p = 0.0f, b_row = 0.0f,
-              b_top = 1.0f, s_q = 0.0f;
+        float e_row = 0.0f, e_end = 0.0f, e_max = 1.0f, s_k = 0.0f, s_h = 0.0f, s_p = 0.0f, h_e = 0.0f,
+              p_e = 0.0f, own = 0.0f;  // own: of dY's rows Q's factor, of z's beta
         auto gates_of = [&](int it) {
             const bool in = warp_wait(full + (it & 1), (it >> 1) & 1, a.status);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (it & 1) * M::stage);
@@ -241,11 +241,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             e_end = ex2_approx(g->hi[kC - 1] + g->lo[kC - 1]);
             e_max = fmaxf(g->e_max, 1.0f);
             s_k = g->s_k;
-            s_q = g->q_factor(i);
             s_h = g->s_h;
             s_p = g->s_p;
-            b_row = g->beta[i];
-            b_top = g->b_top;
+            own = upper ? g->q_factor(i) : g->beta[i];
+            h_e = g->h_e;
+            p_e = g->p_e;
             return in;
         };
         auto put_state = [&](int it) {
@@ -311,26 +311,26 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         bool ok = gates_of(0);  // the same for all lanes of a warp
         fetch(nc - 1);
-        if (upper) ok = put_dy(0, e_row, s_q) && ok;
+        if (upper) ok = put_dy(0, e_row, own) && ok;
         for (int it = 0; it < nc; ++it) {
             const int c = nc - 1 - it;
             const uint32_t ph = it & 1;
-            const float er = e_row, ee = e_end, em = e_max, sk = s_k, sh = s_h, sp = s_p, br = b_row;
+            const float er = e_row, ee = e_end, em = e_max, sk = s_k, sh = s_h, sp = s_p, br = own;
             if (c > 0) fetch(c - 1);
             f2 x[8];
-            // bounds: of L and dY (times Q's factors) measured, of z, dR and the next L from them
+            // bounds: of L and dY (times Q's factors) measured, of z, e dR and the next L from them
             float l_max = 0.0f, dy_max = 0.0f;
             ok = ok && read_most<4>(s_most + kMosts * ph, it, l_max, a.status) &&
                  read_most<2>(s_most + kMosts * ph + kRowWarps, it, dy_max, a.status);
             const float z_bound = kC * kTopValue * sp * 2.0f * dy_max + DK * kTopValue * sh * 2.0f * l_max;
-            const float dr_bound = z_bound * b_top;
+            const float edr_bound = p_e * dy_max + h_e * (DK * l_max);
             float s_od, s_dyd, s_z, s_g, s_next;
             (void)tile_scale(dy_max * em, kBoundTop, s_od);  // (put_dy's factors)
             (void)tile_scale(dy_max, kTop, s_dyd);
             const float z_scale = tile_scale(z_bound, kBoundTop, s_z);
-            const float g_scale = tile_scale(dr_bound * em, kBoundTop, s_g);
-            const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f * em *
-                                                              (dy_max + sk * dr_bound)), kBoundTop, s_next);
+            const float g_scale = tile_scale(edr_bound, kBoundTop, s_g);
+            const float next = tile_scale(fmaf(ee, l_max, kC * kTopValue * 2.0f *
+                                                              (em * dy_max + sk * edr_bound)), kBoundTop, s_next);
             ok = ok && warp_wait(bar_x, ph, a.status);
             tc_fence_after();
             if (ok) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             if (c > 0) {
                 ok = gates_of(it + 1) && ok;
                 // (the products that read dY and e dY are done: bar_q follows them)
-                if (upper) ok = put_dy(it + 1, e_row, s_q) && ok;
+                if (upper) ok = put_dy(it + 1, e_row, own) && ok;
             }
             ok = ok && warp_wait(bar_l, ph, a.status);
             tc_fence_after();
@@ -512,10 +512,10 @@ struct Sums {
     float ls[8];           // <L, S0>
 };
 
-// The largest product of R's and L's factors over the panels of a head.
+// The largest product of U's and L's factors over the panels of a head.
 __device__ __forceinline__ int largest_ul(const float* fac, int pans) {
     int e = kNone;
-    for (int p = 0; p < pans; ++p) e = max(e, exponent(fac[8 * p]) + exponent(fac[8 * p + 6]));
+    for (int p = 0; p < pans; ++p) e = max(e, exponent(fac[8 * p + 2]) + exponent(fac[8 * p + 6]));
     return e;
 }
 
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
     uint64_t* w_in = full + 18;    // W is in shared memory
     uint64_t* w_out = full + 19;   // W's products and F2 have been read
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 20);
-    float* factors = reinterpret_cast<float*>(smem + M::factors);  // R, S0, -, -, z, dY, L
+    float* factors = reinterpret_cast<float*>(smem + M::factors);  // E, S0, U, E's to U's, z, dY, L
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned nc = a.d.chunks, groups = a.d.groups;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 bool begun = false;  // F2
                 for (int p = 0; p < pans && ok; ++p, ++n) {
                     const uint32_t st = sb + M::stages + (n & 1) * M::stage;
-                    const bool near = exponent(fac[8 * p]) + exponent(fac[8 * p + 6]) - e_ul >= kFar || e_ul == kNone;
+                    const bool near = exponent(fac[8 * p + 2]) + exponent(fac[8 * p + 6]) - e_ul >= kFar || e_ul == kNone;
                     ok = mbar_poll(u_in, n & 1, a.status);
                     if (!ok) break;
                     tc_fence_after();
@@ -774,9 +774,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 const Gates* gates = reinterpret_cast<const Gates*>(hg);
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
                 bool here = warp_wait(full_h + (hn & 1), (hn >> 1) & 1, a.status);
-                const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
                 // dY's rows are kept times Q's factors (powers of two): what undoes it
-                auto inv_q = [&]() { return __uint_as_float((254u << 23) - __float_as_uint(gates->q_factor(i))); };
+                const float inv_q = inverse(gates->q_factor(i));
+                // of this row in F and in A: as a q row for dY, as a k row for -dR = -b z
+                const float er = ex2_approx(gates->hi[i] + gates->lo[i]);
+                const float f_row = is_q ? er * inv_q : -er * gates->beta[i];
+                const float a_row = is_q ? 1.0f : -gates->beta[i] * gates->s_k;
                 // a step's row of K or Q, columns col0 + 16 n .. + 15
                 auto own_row = [&](int n16, f2* v) {
                     const int c0 = col0 + 16 * n16;
@@ -787,9 +790,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                     v + 4 * q);
                 };
                 // Products of U and L are summed over the panels where they are: U's factor is
-                // chosen so that all have the same, the largest of theirs.  A panel's own: E is at
-                // most 64 products of 2^13 and 2^15, and beta at most b_top: brought down to 2^15
-                constexpr float kDown = 1.0f / 524288.0f;
+                // chosen so that all have the same, the largest of theirs
                 const int e_ul = largest_ul(fac, pans);
                 // what the other heads have left in the sums does not belong to this one's dot
                 float before = 0.0f;
@@ -810,12 +811,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 float beta_sum = 0.0f, ls = 0.0f;
                 for (int p = 0; p < pans; ++p, ++n) {
                     const uint8_t* sg = smem + M::stages + (n & 1) * M::stage;
-                    const float s_r = fac[8 * p], s_s = fac[8 * p + 1], s_z = fac[8 * p + 4],
-                                s_dy = fac[8 * p + 5], s_l = fac[8 * p + 6];
+                    const float s_s = fac[8 * p + 1], s_row = fac[8 * p + (is_q ? 5 : 4)], s_l = fac[8 * p + 6];
                     here = warp_wait(full + (n & 1), (n >> 1) & 1, a.status) && here;
-                    const int below = exponent(s_r) + exponent(s_l) - e_ul;
-                    const float s_e = s_r * gates->s_n, down = kDown * power(max(below, kFar)),
-                                s_u = s_e * gates->b_top / down;
+                    const int below = max(exponent(fac[8 * p + 2]) + exponent(s_l) - e_ul, kFar);
                     f2 e_row[16];
                     if (!is_q) {
                         here = warp_wait(bar_e, n & 1, a.status) && here;
@@ -824,7 +822,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                         uint32_t hw[16];
                         tmem_ld32(t_lane + kTmE + 32 * part, e_row);
                         tmem_wait_ld();
-                        scaled<16>(e_row, down * gates->b_down * gates->beta[i], x);
+                        scaled<16>(e_row, fac[8 * p + 3] * power(below) * gates->beta[i], x);
                         round_to<16>(x, hw);
                         put32(smem + M::u, i, 4 * part, hw);
                         fence_proxy_async_smem();
@@ -849,14 +847,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                                 dl = dot8(*reinterpret_cast<const uint4*>(sg + M::s0 + at),
                                           *reinterpret_cast<const uint4*>(sg + M::l + at), dl);
                         }
-                        beta_sum = fmaf(s_z * s_e, sum2(ze), beta_sum);
+                        beta_sum = fmaf(s_row * fac[8 * p], sum2(ze), beta_sum);
                         ls = fmaf(s_s * s_l, sum2(dl), ls);
                     }
                     ok = here && warp_wait(bar_f, n & 1, a.status);
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float f1 = (is_q ? er * (s_dy * inv_q()) : -er * gates->beta[i] * s_z) * s_s;
+                        const float f1 = f_row * s_row * s_s;
                         const f2 f1p = pair(f1, f1);
 #pragma unroll
                         for (int e0 = 0; e0 < CP; e0 += 16) {
@@ -873,7 +871,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                     if (!ok) break;
                     tc_fence_after();
                     {
-                        const float fa = (is_q ? s_dy : -gates->beta[i] * s_z * gates->s_k) * s_u;
+                        const float fa = a_row * s_row * (fac[8 * p + 2] * power(-below));
                         const f2 fap = pair(fa, fa);
                         f2 x[16];
                         tmem_ld32(t_lane + kTmA + 32 * part, x);
@@ -927,8 +925,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 tc_fence_after();
                 {
                     const float wr = decay(gates->hi[kC - 1], gates->lo[kC - 1], gates->hi[i], gates->lo[i]);
-                    const float f1 = is_q ? s_w * (gates->s_k * inv_q()) : s_w;
-                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) * gates->s_n * gates->b_top / kDown : 0.0f;
+                    const float f1 = is_q ? s_w * (gates->s_k * inv_q) : s_w;
+                    const float g2 = e_ul > kNone ? wr * power(min(e_ul, 127)) : 0.0f;
                     const f2 f1p = pair(f1, f1), g2p = pair(g2, g2);
                     f2 whole = 0, end = 0, write = 0;  // dots with this row
 #pragma unroll

@@ -147,3 +147,21 @@ def test_growth_without_gradients():
     g, ref = backward(cuda(t), grad_dtype=F32), reference_grads(t)
     check_grads(g, ref, F32, F32)
     assert not g["dv"][:, 64:, 0].any() and not g["dq"][:, 64:, 0].any()
+
+
+@pytest.mark.parametrize("nats", [6, 10, 12])
+def test_growth_within_a_chunk(nats):
+    """Gates above 0: e^nats in 64 steps, whose operands' rows lie as far apart.  Two fp16 hold
+    2^-39 of the bound above a tile's largest value, which is up to 2^14 too large here: rows e^12 =
+    2^17 smaller are off by 2^-8 of theirs times what they are multiplied with, which is 2^17
+    larger than others' but counts once in 64: 2^-17 at most, in the mean of all rows 2 * FWD."""
+    t = inputs(1, 192, 2, 2, 64, 64, seed=27, restart=0)
+    t["g"][:, 64:128], t["g"][:, 128:] = nats / 64, -nats / 64
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    assert off(y, y_ref) < 2 * FWD and off(last, last_ref) < 2 * FWD
+    got, ref = backward(c, grad_dtype=F32), reference_grads(t)
+    for name, tol in (("dq", BWD), ("dk", BWD), ("dv", 2 * FWD), ("dinitial_state", 2 * FWD), ("dg", GATES),
+                      ("dbeta", GATES)):
+        assert off(got[name], ref[name]) < tol, name
