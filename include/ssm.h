@@ -984,6 +984,10 @@ size_t ssm_gated_delta_checkpoint_bytes(int batch, int seqlen, int nheads, int d
  * enough with checkpoints, and none are needed for a sequence that is walked. */
 size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int dstate, int headdim);
 
+/* The longest bf16 sequence that ssm_gated_delta_fwd walks step by step where no checkpoints are
+ * kept (10). */
+int ssm_gated_delta_walked_steps(void);
+
 /*
  * Gated delta rule.
  *   The scalar-decay state of ssd_chunked_fwd ("Mamba-3 NKI Kernels for AWS Neuron",
@@ -1010,8 +1014,9 @@ size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int ds
  * Supported: dstate a multiple of 8 up to 128, headdim a multiple of 8 up to 256, nheads a
  * multiple of ngroups, seqlen < 2^30, batch * nheads * ceil(seqlen / 64) < 2^30; in_dtype
  * SSM_BF16, or SSM_F32 without checkpoints.  seqlen == 0 hands the state on.
- * fp32 sequences, and bf16 ones of up to 10 steps without checkpoints (a decode step: one),
- * are walked step by step in fp32 and need no workspace.  Others are taken in chunks of
+ * fp32 sequences, and bf16 ones of up to ssm_gated_delta_walked_steps() steps without
+ * checkpoints (a decode step: one), are walked step by step in fp32 and need no workspace; an
+ * fp32 step takes some 3 us whatever the batch, until all SMs have states to work on.  Others are taken in chunks of
  * 64 steps on the tensor cores; what enters their products beside q and k is held as the
  * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y (then
  * rounded once to out_dtype) and the state are within about 1e-6 (2-norm) of the definition; what

@@ -25,7 +25,7 @@ from .binding import (EXPORTS, SSMError, lib, ssd_chunked_bwd,  # noqa: F401
                       ssm_decode_step_mamba3, ssm_decode_step_mamba3_mimo,
                       ssm_gated_delta_bwd, ssm_gated_delta_bwd_workspace_bytes,
                       ssm_gated_delta_checkpoint_bytes, ssm_gated_delta_fwd,
-                      ssm_gated_delta_workspace_bytes,
+                      ssm_gated_delta_walked_steps, ssm_gated_delta_workspace_bytes,
                       ssm_last_device_status, ssm_qk_norm_rope_bwd,
                       ssm_qk_norm_rope_bwd_workspace_bytes, ssm_qk_norm_rope_fwd, ssm_scan_bwd, ssm_scan_bwd_workspace_bytes,
                       ssm_scan_checkpoint_bytes, ssm_scan_fwd, ssm_scan_fwd_host,

@@ -43,7 +43,7 @@ EXPORTS = ["ssm_abi_version", "ssm_status_string", "ssm_scan_workspace_bytes", "
            "ssm_vocab_ce_workspace_bytes", "ssm_vocab_ce_fwd", "ssm_vocab_ce_bwd_workspace_bytes",
            "ssm_vocab_ce_bwd", "ssm_qk_norm_rope_fwd", "ssm_qk_norm_rope_bwd_workspace_bytes",
            "ssm_qk_norm_rope_bwd", "ssm_gated_delta_checkpoint_bytes",
-           "ssm_gated_delta_workspace_bytes", "ssm_gated_delta_fwd",
+           "ssm_gated_delta_workspace_bytes", "ssm_gated_delta_walked_steps", "ssm_gated_delta_fwd",
            "ssm_gated_delta_bwd_workspace_bytes", "ssm_gated_delta_bwd"]
 
 
@@ -163,6 +163,8 @@ def lib() -> ctypes.CDLL:
                   L.ssm_gated_delta_bwd_workspace_bytes):
             f.restype = sz
             f.argtypes = [i] * 5
+        L.ssm_gated_delta_walked_steps.restype = i
+        L.ssm_gated_delta_walked_steps.argtypes = []
         L.ssm_gated_delta_fwd.restype = i
         L.ssm_gated_delta_fwd.argtypes = ([vp] * 3 + [ll] * 3 + [vp] * 6 + [i] * 9 +
                                           [vp, sz, vp])
@@ -1510,7 +1512,10 @@ def ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim) -> i
     return int(lib().ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, dstate, headdim))
 
 
-_WALKED = 10  # steps a bf16 sequence is walked up to, without a workspace
+@functools.lru_cache(None)
+def ssm_gated_delta_walked_steps() -> int:
+    """Steps a bf16 sequence is walked up to, without a workspace, where nothing is kept."""
+    return int(lib().ssm_gated_delta_walked_steps())
 
 
 def _delta_args(q, k, v, g, beta, initial_state):
@@ -1565,7 +1570,8 @@ def ssm_gated_delta_fwd(q, k, v, g, beta, initial_state=None, out_dtype=None, y=
     five = batch, seqlen, nheads, dstate, headdim
     _delta_kept(checkpoints, *five)
     if workspace is not None or (q.dtype == torch.bfloat16 and
-                                 (checkpoints is not None or seqlen > _WALKED)):
+                                 (checkpoints is not None or
+                                  seqlen > ssm_gated_delta_walked_steps())):
         need = 1024 if checkpoints is not None else ssm_gated_delta_workspace_bytes(*five)
         workspace = _work(workspace, q, need, stream)
     _one_device(q, k, v, g, beta, initial_state, y, final_state, checkpoints, workspace)

@@ -22,9 +22,11 @@ using namespace gdn;
 
 constexpr int kWalkThreads = 128;
 constexpr int kWalkRows = 8;       // rows of the state (of headdim) a warp holds
-// The longest bf16 sequence that is walked.  At headdim = dstate = 128 walked and in chunks: 128 x
-// 32 heads, 8 steps 349 and 505 us, 12 steps 634 and 505 us; 32 x 32 heads, 12 steps 124 and 147 us;
-// 16 heads, 12 steps 19 us both.
+// The longest bf16 sequence that is walked.  A step costs the same again, a chunk costs what it
+// costs however few of its steps there are; inputs not in the caches, at headdim = dstate = 128,
+// 8, 10 and 12 steps walked, and in chunks: 128 x 32 heads 467, 569, 653 and 533 us; 32 x 32 heads
+// 137, 160, 186 and 155 us; 8 x 16 heads 29, 35, 39 and 39 us.  Smaller states could be walked
+// for longer (32 x 32 heads of 64 x 64, 16 steps: 68 and 87 us).
 constexpr int kWalkSteps = 10;
 
 struct WalkArgs {
@@ -1365,6 +1367,8 @@ extern "C" size_t ssm_gated_delta_checkpoint_bytes(int batch, int seqlen, int nh
     return records_bytes(batch, seqlen, nheads, dstate) +
            keep_bytes(batch, seqlen, nheads, dstate, headdim);
 }
+
+extern "C" int ssm_gated_delta_walked_steps(void) { return kWalkSteps; }
 
 extern "C" size_t ssm_gated_delta_workspace_bytes(int batch, int seqlen, int nheads, int dstate,
                                                   int headdim) {
