@@ -1102,6 +1102,8 @@ ssm_status_t ssm_last_device_status(const void* workspace, void* stream);
  *    publish of its final (inclusive) state, so chunk 1 waits until its
  *    limit: a wait on a flag that nothing sets, with no fault.  The scan's
  *    outputs are then undefined.
+ *  - ssm_gated_delta_fwd where records and chains run at once (few heads): the limit is that of
+ *    the wait for a record, and the first record made is not told of.
  *  - Process-wide setting, read when each scan is enqueued; not for use while
  *    other threads enqueue scans.  Always returns SSM_OK.
  */

@@ -763,7 +763,8 @@ def ssm_last_device_status(workspace, stream=None) -> int:
 def ssm_debug_set_lookback(drop_first_publish: bool = False, spin_limit: int = 0) -> None:
     """Test hook of the scan's chained L-chunks: chunk 0 withholds its publish
     (so chunk 1's bounded wait runs out and records SSM_ERR_TIMEOUT) and the
-    wait gives up after ``spin_limit`` polls (0: the default).  Process-wide;
+    wait gives up after ``spin_limit`` polls (0: the default).  In the gated delta rule, where
+    records and chains run at once, the first record is not told of.  Process-wide;
     call with no arguments to restore the defaults."""
     _check(lib().ssm_debug_set_lookback(1 if drop_first_publish else 0, int(spin_limit)),
            "ssm_debug_set_lookback")

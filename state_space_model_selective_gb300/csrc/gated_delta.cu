@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "gated_delta.cuh"
+#include "scan_internal.h"
 
 namespace {
 
@@ -169,6 +170,7 @@ struct RecArgs {
     unsigned count;   // of chunks and heads
     int gates_bf16;
     int keep_n;       // N is wanted (training)
+    int drop_first;   // (a test's) the first record is not told
 };
 
 template <int V> struct Vec;
@@ -335,7 +337,7 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
     auto tell = [&](unsigned ch) {
         bulk_wait_all();
         asm volatile("fence.proxy.async;" ::: "memory");
-        st_release_gpu(a.flags + ch, 1u);
+        if (!(a.drop_first && ch == 0)) st_release_gpu(a.flags + ch, 1u);
     };
     unsigned before = 0;
     for (unsigned item = first; item < a.count && ok; item += step) {
@@ -817,6 +819,7 @@ struct ChainArgs {
     void* y;
     uint32_t* status;
     const uint32_t* flags;  // of records that are being made meanwhile, or NULL
+    uint32_t spin_limit;    // looks at one of them before giving up
     Dims d;       // pans: panels of PW columns
 };
 
@@ -859,6 +862,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
     uint32_t* s_most = reinterpret_cast<uint32_t*>(full + 10);  // [2 chunks][NW warps of S0, NW / 2 of V]
     float* s_first = reinterpret_cast<float*>(s_most + 2 * kMosts);  // [NW]: of the first S0
     uint32_t* s_made = reinterpret_cast<uint32_t*>(s_first + NW);  // records known to be in memory
+    uint32_t* s_stop = s_made + 1;  // the chunk whose record never came: all leave when it is due
     constexpr uint32_t kNotMade = 0xffffffffu;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -874,6 +878,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         mbar_init(bar_o, NW / 2);
         for (int n = 0; n < 2 * kMosts; ++n) s_most[n] = 0;
         *s_made = 0;
+        *s_stop = kNotMade;
         fence_mbar_init();
     }
     __syncthreads();
@@ -890,6 +895,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
                 if (!mbar_poll(full + (c & 1), (c >> 1) & 1, a.status)) break;
+                if (FLAGS && *s_stop == (uint32_t)c) break;
                 if (!mbar_poll(bar_s, ph, a.status)) break;
                 tc_fence_after();
 #pragma unroll
@@ -957,6 +963,11 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             auto load = [&](int c) {
                 uint8_t* st = smem + (c & 1) * M::stage;
                 uint64_t* bar = full + (c & 1);
+                if (FLAGS && !made(c)) {
+                    *s_stop = (uint32_t)c;
+                    mbar_arrive(bar);
+                    return false;
+                }
                 const uint8_t* rec = rec0 + (long long)c * rec_bytes(DK);
                 mbar_arrive_expect_tx(bar, M::stage);
                 bulk_load(st, rec, kGateBytes, bar);
@@ -969,6 +980,7 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 tma_load_4d(st + M::v, &tm_v, bar, pan * PW, h, c * kC, b);
                 bulk_load(st + M::p, rec + rec_p(DK), 2 * kTile, bar);
                 ++loads;
+                return true;
             };
             auto load_h = [&](int c) {
                 mbar_arrive_expect_tx(full_h, 2 * h_bytes(DK));
@@ -977,23 +989,18 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             };
             // H counts as in once the chunk before is known to be done too, so that no barrier
             // is ever a whole turn ahead of this thread
-            bool here = made(0);
+            bool here = load(0);
             if (here) {
-                load(0);
                 load_h(0);
                 mbar_arrive(full_h);
-                here = nc == 1 || made(1);
-                if (here && nc > 1) load(1);
+                if (nc > 1) here = load(1);
             }
             for (int c = 0; c + 1 < nc && here; ++c) {
                 if (!mbar_wait(bar_h, c & 1, a.status)) break;
                 load_h(c + 1);
                 if (!mbar_wait(bar_y, c & 1, a.status)) break;
                 mbar_arrive(full_h);
-                if (c + 2 < nc) {
-                    here = made(c + 2);
-                    if (here) load(c + 2);
-                }
+                if (c + 2 < nc) here = load(c + 2);
             }
             // never leave with a load still landing
             for (int c = max(0, loads - 2); c < loads; ++c)
@@ -1005,8 +1012,8 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             const uint32_t addr = smem_u32(s_made);
             for (int c = 0; c < nc; ++c) {
                 uint32_t tries = 0;
-                while (ld_acquire_gpu(a.flags + bh * nc + c) == 0 && ++tries < kFlagSpinLimit) {}
-                const bool there = tries < kFlagSpinLimit;
+                while (ld_acquire_gpu(a.flags + bh * nc + c) == 0 && ++tries < a.spin_limit) {}
+                const bool there = tries < a.spin_limit;
                 if (!there) record_status(a.status, SSM_ERR_TIMEOUT);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr),
@@ -1034,7 +1041,8 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
         bool off = true;
         // the gates of chunk c, and the largest values of its V (upper warps)
         auto gates_of = [&](int c) {
-            const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status);
+            const bool in = warp_wait(full + (c & 1), (c >> 1) & 1, a.status) &&
+                            !(FLAGS && *s_stop == (uint32_t)c);
             const Gates* g = reinterpret_cast<const Gates*>(smem + (c & 1) * M::stage);
             const float e_row = ex2_approx(g->hi[i] + g->lo[i]);
             f_k = e_row * g->s_k;
@@ -1297,6 +1305,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
         if (cudaMemsetAsync(f.flags, 0, (r.count + 1) * 4ull, s) != cudaSuccess) return SSM_ERR_CUDA;
         r.flags = f.flags + 1;
         a.flags = f.flags + 1;
+        ssm_internal::lookback_setting(&a.spin_limit, &r.drop_first);
         auto both = [&](auto to) {
             using TO = decltype(to);
             constexpr uint32_t bytes = ChainSmem<DK, 32>::bytes;
