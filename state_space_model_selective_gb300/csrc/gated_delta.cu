@@ -435,7 +435,10 @@ __device__ __forceinline__ void make_records(const CUtensorMap& tm_q, const CUte
         most = most_of<8>(s_most);
         const float k_scale = tile_scale(most, kTop, s_k);
         most_q = most_of<8>(s_most + 24);
-        if (most_q > 0.0f) most = most_q;  // (steps that do not ask: the keys' does as well)
+        if (most == 0.0f) most = 1.0f;
+        // (dY and the gradient's W enter products under it, beside rows under the keys': not below a
+        // 2^10th of theirs.  For a q that is next to nothing beside the keys, 2^-24, theirs does)
+        if (most_q > most * 5.9604645e-8f) most = fmaxf(most_q, most * 0.0009765625f);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             q_scale[n] = tile_scale(fmaxf(most, own_q[n]), kTop, s_q[n]);

@@ -165,3 +165,25 @@ def test_growth_within_a_chunk(nats):
     for name, tol in (("dq", BWD), ("dk", BWD), ("dv", 2 * FWD), ("dinitial_state", 2 * FWD), ("dg", GATES),
                       ("dbeta", GATES)):
         assert off(got[name], ref[name]) < tol, name
+
+
+@pytest.mark.parametrize("size", [0.0, 1e-30, 1e-12])
+def test_queries_of_next_to_nothing(size):
+    """dq does not depend on q: it is right where q is 0 or nearly, in steps that learn and in a
+    chunk that does not, with gradients of y of any size."""
+    t = inputs(1, 200, 4, 2, 64, 64, seed=28)
+    t["beta"][:, 64:128] = 0
+    t["q"] = t["q"] * size
+    t["dy"][:, 128:] *= 1e-6
+    ref = reference_grads(t)
+    g = backward(cuda(t), grad_dtype=F32)
+    for at in (slice(0, 64), slice(64, 128), slice(128, 200)):
+        assert off(g["dq"][:, at], ref["dq"][:, at]) < BWD
+    for name, tol in (("dk", BWD), ("dv", FWD), ("dbeta", GATES)):
+        assert off(g[name], ref[name]) < tol, name
+    # what restarts leave of it is sum(dy q^T) alone, some 1e-30 or 1e-12.  Such a q is held under the
+    # keys' factor, at most 2^13 / max|k|, in fp16, 2^-24 apart: off by 2^-25 / 2^12 max|k| at most
+    # each, so the sum over 200 steps of dy (and what is carried on does not grow) by 200 times that
+    least = 200 * 2.0 ** -37 * float(t["k"].abs().max() * t["dy"].abs().max()) * ref["dinitial_state"].size ** 0.5
+    diff = np.linalg.norm(to64(g["dinitial_state"]) - ref["dinitial_state"])
+    assert diff < FWD * np.linalg.norm(ref["dinitial_state"]) + least
