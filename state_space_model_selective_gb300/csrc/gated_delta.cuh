@@ -366,15 +366,20 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
     mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);  // the types are the descriptor's
 }
 
+// A tile's descriptor moved on by `bytes`: its address is the low word's first bits.  One addition, where
+// a descriptor made anew takes five instructions of the one thread that issues all products.
+__device__ __forceinline__ uint64_t moved(uint64_t desc, uint32_t bytes) {
+    return (desc & 0xffffffff00000000ull) | ((uint32_t)desc + (bytes >> 4));
+}
 // K-major operand (rows of 64 values along the contraction) of R rows, k-step kk.
 template <int R>
 __device__ __forceinline__ uint64_t kdesc(uint32_t tile, int kk) {
-    return smem_desc_k128(tile + (uint32_t)((kk >> 2) * (R * 128) + (kk & 3) * 32));
+    return moved(smem_desc_k128(tile), (uint32_t)((kk >> 2) * (R * 128) + (kk & 3) * 32));
 }
 // MN-major operand (one row of 64 values per step of the contraction), k-step kk;
 // further blocks of 64 `lbo` bytes apart.
 __device__ __forceinline__ uint64_t mdesc(uint32_t tile, int kk, uint32_t lbo) {
-    return smem_desc_mn128(tile + (uint32_t)kk * 2048u, lbo);
+    return moved(smem_desc_mn128(tile, lbo), (uint32_t)kk * 2048u);
 }
 
 // `bytes` (a multiple of 16) of global memory to shared memory, counted on `bar`.
