@@ -888,7 +888,19 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
 
     if (warp >= NW) {
         give_registers<NW>();
-        if (warp == NW && lane == 0) {
+        // Products are issued by one thread.  With 32 columns they are so short that its instructions
+        // are what they wait for: there the warp makes the operands together (8192 steps of 16 heads
+        // 274 us -> 255 us); with 64, where the votes of its waits cost more, the thread by itself.
+        constexpr bool kWarp = PW == 32;
+        if (warp == NW && (kWarp || lane == 0)) {
+            const int one = kWarp ? elect_one() : 1;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return kWarp ? warp_wait(bar, parity, a.status) : mbar_poll(bar, parity, a.status);
+            };
+            auto multiply = [&](uint32_t d, uint64_t left, uint64_t right, uint32_t id, uint32_t add) {
+                if constexpr (kWarp) mma_f16_warp(one, d, left, right, id, add);
+                else mma_f16(d, left, right, id, add);
+            };
             auto kept_of = [&](int c) {
                 return a.kept + ((bh * nc + c) * a.d.pans + pan) * kept_bytes(DK);
             };
@@ -897,28 +909,28 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
             constexpr uint32_t id1 = idesc_f16(128, 64) | kIdescBMN;
             for (int c = 0; c < nc; ++c) {
                 const uint32_t ph = c & 1, st = sb + (c & 1) * M::stage;
-                if (!mbar_poll(full + (c & 1), (c >> 1) & 1, a.status)) break;
+                if (!wait(full + (c & 1), (c >> 1) & 1)) break;
                 if (FLAGS && *s_stop == (uint32_t)c) break;
-                if (!mbar_poll(bar_s, ph, a.status)) break;
+                if (!wait(bar_s, ph)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
-                            id2, kk > 0);
-                mma_commit(bar_x);
+                    multiply(tmem + kTmX, kdesc<128>(st + M::k, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                             id2, kk > 0);
+                if (one) mma_commit(bar_x);
                 if (PW == 64 && a.kept) {  // S0's hi part is what training keeps
                     bulk_store(kept_of(c) + kTile, smem + M::s, h_bytes(DK));
                     bulk_commit();
                 }
-                if (c > 0 && !mbar_poll(bar_o, ph ^ 1, a.status)) break;
+                if (c > 0 && !wait(bar_o, ph ^ 1)) break;
                 tc_fence_after();
                 // Q in rows 64 to 127: its tiles of 128 rows start one tile early
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk)
-                    mma_f16(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
-                            id2, kk > 0);
-                if (!mbar_poll(full_h, ph, a.status)) break;
-                if (!mbar_poll(bar_r, ph, a.status)) break;
+                    multiply(tmem + kTmQ, kdesc<64>(st + M::q - kTile, kk), mdesc(sb + M::s, kk, h_bytes(DK)),
+                             id2, kk > 0);
+                if (!wait(full_h, ph)) break;
+                if (!wait(bar_r, ph)) break;
                 tc_fence_after();
                 if (PW == 64 && a.kept) {
                     bulk_wait_read_all();  // S0's place is written when H b R is done
@@ -930,21 +942,21 @@ __device__ __forceinline__ void run_chain(const CUtensorMap& tm_v, const ChainAr
                 // (of 64 rows of H the 64 behind them are not read)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
+                    multiply(tmem + kTmH, kdesc<DK>(hh, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
-                mma_commit(bar_h);
+                    multiply(tmem + kTmH, kdesc<DK>(hl, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                if (one) mma_commit(bar_h);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
+                    multiply(tmem + kTmY, kdesc<128>(pp - kTile, kk), mdesc(sb + M::r, kk, kTile), id2, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
+                    multiply(tmem + kTmY, kdesc<128>(pp, kk), mdesc(sb + M::r, kk, kTile), id1, 1);
                 if (PW == 64 && a.kept) bulk_wait_read_all();  // the stage is loaded again
-                mma_commit(bar_y);
+                if (one) mma_commit(bar_y);
             }
-            bulk_wait_all();
+            if (one) bulk_wait_all();
         } else if (warp == NW + 1 && lane == 0) {
             const uint8_t* rec0 = a.records + bh * nc * rec_bytes(DK);
             int loads = 0, h_loads = 0;
@@ -1294,17 +1306,20 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;
     a.y = f.y; a.status = f.status; a.d = d;
-    // Panels of 32 columns take 0.7 of the time of 64 a chunk, on twice the CTAs (one to an
-    // SM): for heads so few that these run at once where the wider ones would leave SMs idle
+    // Panels of 32 columns take 0.7 of the time of 64 a chunk (1.7 and 2.5 us), on twice the CTAs (one
+    // to an SM): for heads so few that these run at once where the wider ones would leave SMs idle
     const long long bh = (long long)f.batch * f.heads;
     const long long wide = bh * d.pans, narrow = bh * ((f.dv + 31) / 32);
     const bool half = !f.kept && 7 * ((narrow + sms - 1) / sms) < 10 * ((wide + sms - 1) / sms);
     if (half) a.d.pans = (f.dv + 31) / 32;
-    // Where these leave SMs idle, the records are made on those meanwhile: 3.5 SMs to a head keep
-    // up with its chains (8192 steps at headdim 128, one after the other against at once: 16
-    // heads 295 and 260 us, 20 heads, 3.6 SMs to each, 305 and 290 us, 22, 2.9 to each, 314 and 361 us)
+    // Where these leave SMs idle, the records may be made on those meanwhile.  That costs some 9 us and
+    // 0.13 us for each chunk of a chain (its records come one by one), and saves the records' own
+    // launch, 0.03 us for each chunk and head; four SMs to a head keep up with its chains.  One
+    // after the other and at once, headdim 128: 8192 steps, 1 head 222 and 240 us, 8 heads 257 and
+    // 248 us, 18 heads (4.4 SMs to each) 294 and 255 us, 20 heads (3.6) 301 and 308 to 330 us; 2048 steps,
+    // 16 heads 89 and 89 us; 512 steps, 16 heads 40 and 49 us.
     const long long makers = sms - narrow;
-    if (half && f.flags && 2 * makers >= 7 * bh) {
+    if (half && f.flags && makers >= 4 * bh && r.count > 300u + 5u * d.chunks) {
         if (cudaMemsetAsync(f.flags, 0, (r.count + 1) * 4ull, s) != cudaSuccess) return SSM_ERR_CUDA;
         r.flags = f.flags + 1;
         a.flags = f.flags + 1;

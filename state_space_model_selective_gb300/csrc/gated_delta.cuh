@@ -366,6 +366,27 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
     mma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);  // the types are the descriptor's
 }
 
+// The same from a whole warp, whose operands are then the same for all its lanes (they need not be
+// taken from vector to uniform registers one by one): the lane with `one` set issues it.
+__device__ __forceinline__ void mma_f16_warp(int one, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ int elect_one() {
+    int one;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, e;\n\t}"
+        : "=r"(one));
+    return one;
+}
 // A tile's descriptor moved on by `bytes`: its address is the low word's first bits.  One addition, where
 // a descriptor made anew takes five instructions of the one thread that issues all products.
 __device__ __forceinline__ uint64_t moved(uint64_t desc, uint32_t bytes) {

@@ -628,20 +628,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
             for (int k = max(0, n - 2); k < n; ++k) (void)mbar_wait(full + (k & 1), (k >> 1) & 1, a.status);
             for (int k = max(0, hn - 2); k < hn; ++k)
                 (void)mbar_wait(full_h + (k & 1), (k >> 1) & 1, a.status);
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9) {
+            const int one = elect_one();
             constexpr uint32_t id64 = idesc_f16(128, 64), idk = idesc_f16(128, DK);
             constexpr uint32_t idW = idesc_f16(128, DK) | kIdescBMN;
             constexpr uint32_t idV = idesc_f16(128, DK) | kIdescAMN | kIdescBMN;
             // E = N R
             auto multiply_e = [&](int n, int hn) {
-                if (!mbar_poll(full + (n & 1), (n >> 1) & 1, a.status)) return false;
+                if (!warp_wait(full + (n & 1), (n >> 1) & 1, a.status)) return false;
                 const uint32_t st = sb + M::stages + (n & 1) * M::stage, hd = sb + (hn & 1) * M::head;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmE, kdesc<128>(hd + M::nn, kk), mdesc(st + M::r, kk, kTile), id64 | kIdescBMN,
+                    mma_f16_warp(one, tmem + kTmE, kdesc<128>(hd + M::nn, kk), mdesc(st + M::r, kk, kTile), id64 | kIdescBMN,
                             kk > 0);
-                mma_commit(bar_e);
+                if (one) mma_commit(bar_e);
                 return true;
             };
             // F = [z; dY] S0^T, of columns that are in
@@ -650,12 +651,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmF, kdesc<128>(st + M::zdy, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
-                mma_commit(bar_f);
+                    mma_f16_warp(one, tmem + kTmF, kdesc<128>(st + M::zdy, kk), kdesc<DK>(st + M::s0, kk), idk, kk > 0);
+                if (one) mma_commit(bar_f);
                 return true;
             };
             const int heads = first < a.count ? (int)((a.count - 1 - first) / step + 1) * mine : 0;
-            bool ok = heads > 0 && mbar_poll(full_h, 0, a.status) && multiply_e(0, 0) && multiply_f(0);
+            bool ok = heads > 0 && warp_wait(full_h, 0, a.status) && multiply_e(0, 0) && multiply_f(0);
             for (int hn = 0, n = 0; hn < heads && ok; ++hn) {
                 const float* fac = factors + 8 * kMaxPans * (hn & 1);
                 const uint32_t hd = sb + (hn & 1) * M::head;
@@ -664,37 +665,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) grads_kernel(const GradArgs a
                 for (int p = 0; p < pans && ok; ++p, ++n) {
                     const uint32_t st = sb + M::stages + (n & 1) * M::stage;
                     const bool near = exponent(fac[8 * p + 2]) + exponent(fac[8 * p + 6]) - e_ul >= kFar || e_ul == kNone;
-                    ok = mbar_poll(u_in, n & 1, a.status);
+                    ok = warp_wait(u_in, n & 1, a.status);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + kTmA, kdesc<128>(st + M::zdy, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
+                        mma_f16_warp(one, tmem + kTmA, kdesc<128>(st + M::zdy, kk), kdesc<64>(sb + M::u, kk), id64, kk > 0);
                     if (near) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
+                            mma_f16_warp(one, tmem + kTmF2, kdesc<128>(sb + M::u, kk), kdesc<DK>(st + M::l, kk), idk,
                                     begun || kk > 0);
                         begun = true;
                     }
-                    mma_commit(bar_a);
+                    if (one) mma_commit(bar_a);
                     if (p + 1 < pans)
-                        ok = multiply_e(n + 1, hn) && mbar_poll(f_out, n & 1, a.status) && multiply_f(n + 1);
+                        ok = multiply_e(n + 1, hn) && warp_wait(f_out, n & 1, a.status) && multiply_f(n + 1);
                 }
-                ok = ok && mbar_poll(w_in, hn & 1, a.status);
+                ok = ok && warp_wait(w_in, hn & 1, a.status);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16(tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(hd + M::kq, kk, 2 * kTile), idW, kk > 0);
+                    mma_f16_warp(one, tmem + kTmW, kdesc<128>(sb + M::w, kk), mdesc(hd + M::kq, kk, 2 * kTile), idW, kk > 0);
                 // (rows 64 to 127 of W^T [K; Q] are not read)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_f16(tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(hd + M::kq, kk, 2 * kTile), idV, kk > 0);
-                mma_commit(bar_w);
+                    mma_f16_warp(one, tmem + kTmV, mdesc(sb + M::w, kk, kTile), mdesc(hd + M::kq, kk, 2 * kTile), idV, kk > 0);
+                if (one) mma_commit(bar_w);
                 if (hn + 1 < heads)
-                    ok = mbar_poll(full_h + ((hn + 1) & 1), ((hn + 1) >> 1) & 1, a.status) &&
-                         multiply_e(n, hn + 1) && mbar_poll(w_out, hn & 1, a.status) && multiply_f(n);
+                    ok = warp_wait(full_h + ((hn + 1) & 1), ((hn + 1) >> 1) & 1, a.status) &&
+                         multiply_e(n, hn + 1) && warp_wait(w_out, hn & 1, a.status) && multiply_f(n);
             }
         } else if (warp >= 10) {
             // ---- the gates: step i

@@ -17,7 +17,7 @@ OK, TIMEOUT = 0, 7
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 40)])
 def test_a_record_that_is_never_told_of(dk, dv):
-    n, h = 400, 3
+    n, h = 8192, 8   # so many that records are made beside the chains
     c = cuda(inputs(1, n, h, h, dk, dv, seed=31))
     ws = torch.empty(binding.ssm_gated_delta_workspace_bytes(1, n, h, dk, dv), dtype=torch.uint8,
                      device="cuda")
@@ -40,8 +40,8 @@ def test_a_record_that_is_never_told_of(dk, dv):
 
 
 def test_a_limit_of_looks_alone_changes_nothing():
-    c = cuda(inputs(1, 400, 2, 2, 64, 64, seed=32))
-    ws = torch.empty(binding.ssm_gated_delta_workspace_bytes(1, 400, 2, 64, 64), dtype=torch.uint8,
+    c = cuda(inputs(1, 8192, 8, 8, 64, 64, seed=32))
+    ws = torch.empty(binding.ssm_gated_delta_workspace_bytes(1, 8192, 8, 64, 64), dtype=torch.uint8,
                      device="cuda")
     want = forward(c, workspace=ws)
     try:
