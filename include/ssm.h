@@ -1019,8 +1019,11 @@ int ssm_gated_delta_walked_steps(void);
  * fp32 step takes some 3 us whatever the batch, until all SMs have states to work on.  Others are taken in chunks of
  * 64 steps on the tensor cores; what enters their products beside q and k is held as the
  * sum of two fp16 under a power-of-two factor for each tile of 64 steps or columns, so y (then
- * rounded once to out_dtype) and the state are within about 1e-6 (2-norm) of the definition; what
- * is far below the largest value of its tile is off by up to 2^-32 of that.
+ * rounded once to out_dtype) and the state are within about 1e-6 (2-norm) of the definition.
+ * What is far below the largest value of its tile is off by up to 2^-22 of that (the factors come
+ * from bounds; some 2^-28 for keys of many columns).  q may be of any size, in masked steps too (a
+ * q 2^24 times smaller than the keys of its 64 steps loses bits to them).  Gates above 0 cost
+ * nothing up to a growth by e^10 within 64 steps; with e^12 y is 4e-6 off, with e^16 2e-4.
  * The workspace must not be used by another call that may run concurrently.
  * Runs are bit-equal.  Bounded waits report through ssm_last_device_status.
  * A v, state or q that is not finite spoils its column of headdim from its 64 steps on, its
@@ -1058,10 +1061,10 @@ size_t ssm_gated_delta_bwd_workspace_bytes(int batch, int seqlen, int nheads, in
  * runs again, in a workspace that much larger).
  * The gradients of a masked step (beta 0) with respect to k, v and beta are 0, and so is
  * dg where g is -inf.
- * The adjoint of the state, dv and dinitial_state are as exact as the forward; dq, dk, dg
- * and dbeta come from products of operands rounded to one fp16 (summed in fp32): dq, dk and
- * dbeta are within about 4e-4 and dg, a sum of terms of either sign, within about 1e-3
- * (2-norm).  That is less than their own rounding to bf16, and what is left in fp32.
+ * The adjoint of the state, dv and dinitial_state are as exact as the forward; dq, dk, dg and
+ * dbeta come from products of operands rounded to one fp16 (summed in fp32): dq, dk and dbeta
+ * are within about 4e-4 and dg, a sum of terms of either sign, within about 1e-3 (2-norm; 2e-2
+ * with growth by e^16).  That is less than their own rounding to bf16, and what is left in fp32.
  * dbeta does not lose by a small beta, the step's own or another's.
  * Supported as ssm_gated_delta_fwd, in_dtype SSM_BF16.  Runs are bit-equal: sums over
  * heads and steps have a fixed order.

@@ -253,8 +253,8 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
     join_blocks<32>(m, tmp, tid >> 5, tid & 31);
 }
 
-// Bound by the issue of some 15000 warp instructions a chunk and head: 4096 of them at dstate
-// 128 take 128 us, two CTAs' phases filling each other's waits.
+// Bound by the issue of some 15400 warp instructions a chunk and head (16700 with N): 4096 of them at
+// dstate 128 take 125 us (137 us), two CTAs' phases filling each other's waits.
 //
 // CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
 // this one's H and P leave.
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kRecThreads, 2)
 
 // ------------------------------------------------------------------ chain
 
-// Warps on rows (16 for 64 columns of headdim: 150 us where 8 took 156 us; 8 for 32), one that
+// Warps on rows (16 for 64 columns of headdim, 4 % faster than 8; 8 for 32), one that
 // multiplies, one that loads (a copy takes its issuer some 100 cycles, and a chunk has a dozen),
 // one that looks for records, one idle
 template <int PW> constexpr int kRowWarps = PW / 4;
@@ -834,9 +834,10 @@ struct ChainArgs {
 // operands are [hi | lo] side by side, 2 PW columns to an instruction: at 64 columns an
 // instruction is bound by reading its 4 KB of A (55 cycles against 64 for twice the columns).
 //
-// A chunk of 64 columns takes some 2.3 us (128 heads of 128 x 128, 32 chunks, 256 CTAs: 150 us), of
-// 32 columns 1.6 us: instructions of the five passes through registers, their fetch (straight
-// code that two warps of a scheduler share) and the products' latency, one after the other.
+// A chunk of 64 columns takes some 2.6 us (128 heads of 128 x 128, 32 chunks, 256 CTAs: 169 us with what
+// training keeps), of 32 columns 1.65 us: instructions of the five passes through registers, their
+// fetch (straight code that two warps of a scheduler share), the products' issue and their latency,
+// one after the other.
 //
 // The factors of S and R have to be known before they are written, and a reduction over
 // the CTA there would lie on the chain.  So they come from bounds: |R| <= |V| + e |K|_1 |S|,
@@ -1306,7 +1307,7 @@ ssm_status_t run_chunked(const gdn_internal::Forward& f, cudaStream_t s) {
     ChainArgs a{};
     a.records = f.records; a.kept = f.kept; a.h0 = f.initial_state; a.last = f.final_state;
     a.y = f.y; a.status = f.status; a.d = d;
-    // Panels of 32 columns take 0.7 of the time of 64 a chunk (1.7 and 2.5 us), on twice the CTAs (one
+    // Panels of 32 columns take 0.65 of the time of 64 a chunk (1.65 and 2.6 us), on twice the CTAs (one
     // to an SM): for heads so few that these run at once where the wider ones would leave SMs idle
     const long long bh = (long long)f.batch * f.heads;
     const long long wide = bh * d.pans, narrow = bh * ((f.dv + 31) / 32);

@@ -18,8 +18,8 @@
 //
 // Operands are fp16 under one power of two per tile, chosen from the tile's largest value
 // or a bound of it: bf16 inputs are exact in it down to 2^-30 of that, a value as the sum
-// of two fp16 (hi + lo) is to 2^-22, where two bf16 leave 2^-17 and cost the same products.
-// (With bf16 the state of 1000 steps was 5e-6 off, 2-norm.)
+// of two fp16 (hi + lo) is to 2^-22 or 2^-39 of the bound, where two bf16 leave 2^-17 and cost the
+// same products.  (With bf16 the state of 1000 steps was 5e-6 off, 2-norm.)
 #pragma once
 
 #include <cuda_fp16.h>

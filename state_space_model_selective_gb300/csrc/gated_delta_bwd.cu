@@ -67,8 +67,8 @@ struct ChainArgs {
 // instruction: rows 64 to 127 are their lo part, added through shared memory.  The warps on
 // those rows also make dY and e dY of the chunk before, while the others work on z.  The
 // factors come from bounds as the forward's do, with the largest values of L and dY measured.
-// Bound as the forward's chain: 8 x 16 heads of 128 x 128, 32 chunks, 196 us, 3 us a chunk (203 us with
-// 8 warps on rows).
+// Bound as the forward's chain: 8 x 16 heads of 128 x 128, 32 chunks, 200 us, 3.1 us a chunk (3 % more
+// with 8 warps on rows).
 template <int DK, typename TG>
 __global__ void __launch_bounds__(kChainThreads, 1)
     chain_bwd_kernel(const ChainArgs a) {
@@ -523,7 +523,7 @@ __device__ __forceinline__ int largest_ul(const float* fac, int pans) {
 // products, E's of the next columns ahead of time.  Rows of products are lanes: steps as k
 // rows (0 to 63) and as q rows (64 to 127).  All wait for one another by mbarriers, so that no
 // step of one warp holds up the others' (242 us for 8 x 2048 steps of 16 heads when the warps on
-// rows met at barriers and did the rest themselves, 220 us now).
+// rows met at barriers and did the rest themselves, 217 us now).
 //
 // The gates' gradients need no sums over D's rows and columns: scaling k_i as it reads by
 // e^{G_i}, as it writes by e^{-G_i} and q_i by e^{G_i} is what G does, so with dk split into

@@ -187,3 +187,23 @@ def test_queries_of_next_to_nothing(size):
     least = 200 * 2.0 ** -37 * float(t["k"].abs().max() * t["dy"].abs().max()) * ref["dinitial_state"].size ** 0.5
     diff = np.linalg.norm(to64(g["dinitial_state"]) - ref["dinitial_state"])
     assert diff < FWD * np.linalg.norm(ref["dinitial_state"]) + least
+
+
+@pytest.mark.parametrize("onehot", [False, True])
+@pytest.mark.parametrize("big", [300.0, 3e4, 3e6])
+def test_a_large_column_beside_others(big, onehot):
+    """Two fp16 hold 2^-39 of the bound that a tile's factor comes from.  Of the next state it is at
+    most s + 64 * 2 h (v + 128 * 2 k s), with s, v, h, k the largest |S|, |V|, |H|, |K|: 2^16 s for
+    one-hot keys (h, k = 1), where no sum is larger than one term: 2^-23 of the largest a chunk, 2^-22
+    for two."""
+    t = inputs(1, 128, 2, 2, 128, 128, seed=30, masked=0, restart=0)
+    if onehot:
+        t["k"] = torch.nn.functional.one_hot(torch.randint(0, 128, (1, 128, 2)), 128).to(BF16)
+    t["v"][..., 3], t["state"][:, :, 3] = t["v"][..., 3] * big, t["state"][:, :, 3] * big
+    y, last = forward(cuda(t), out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    assert off(y, y_ref) < FWD and off(last, last_ref) < FWD
+    most = max(float(t["v"].abs().max()), float(t["state"].abs().max()), np.abs(last_ref).max())
+    others = [c for c in range(128) if c != 3]
+    assert np.abs(to64(last) - last_ref)[:, :, others].max() < most * 2.0 ** -22
+    assert np.abs(to64(y) - y_ref)[..., others].max() < most * 2.0 ** -22
