@@ -253,12 +253,6 @@ __device__ __forceinline__ void invert_unit_lower(float* m, float* tmp, int tid)
     join_blocks<32>(m, tmp, tid >> 5, tid & 31);
 }
 
-// Bound by the issue of some 15400 warp instructions a chunk and head (16700 with N): 4096 of them at
-// dstate 128 take 125 us (137 us), two CTAs' phases filling each other's waits.
-//
-// CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
-// this one's H and P leave.
-//
 // The beta of a row of the triangle: N divides the row by it, so that it must not be too small for
 // the row to be held.  A smaller one is taken for this, which changes T by as much and N not at
 // all (masked rows are 0 in either).
@@ -267,6 +261,12 @@ __device__ __forceinline__ float row_beta(float b) {
     return fabsf(b) < least ? copysignf(least, b) : b;
 }
 
+// Bound by the issue of some 15400 warp instructions a chunk and head (16700 with N): 4096 of them at
+// dstate 128 take 125 us (137 us), two CTAs' phases filling each other's waits.
+//
+// CTAs walk the chunks and heads, two CTAs to an SM; the next chunk's K and Q come in while
+// this one's H and P leave.
+//
 // The work of eight warps: the items `first`, first + step, ...  With flags they are told one
 // by one, and go through the chunks of all heads side by side.
 template <int DK, bool FLAGS>

@@ -203,7 +203,7 @@ __device__ __forceinline__ float tile_scale(float most, int top, float& back) {
 __device__ __forceinline__ float inverse(float v) { return __uint_as_float((254u << 23) - __float_as_uint(v)); }
 // A product of a tile's factor with others: it overflows where the tile's values are 0, or so small
 // that they count as 0, and must leave them that.
-__device__ __forceinline__ float finite_factor(float f) { return f > 1.7e38f ? 1.7e38f : f; }
+__device__ __forceinline__ float finite_factor(float f) { return fabsf(f) > 1.7e38f ? copysignf(1.7e38f, f) : f; }
 constexpr int kTop = 12;    // of a measured maximum
 constexpr int kBoundTop = 14;  // of a bound
 // The largest stored magnitude of a tile scaled by its maximum.

@@ -138,12 +138,14 @@ def test_masked_steps_that_ask(learners):
         assert off(g["dq"][:, i], ref["dq"][:, i]) < 2 * BWD  # (one step, not the mean of many)
 
 
-def test_growth_without_gradients():
+@pytest.mark.parametrize("sign", [1, -1])
+def test_growth_without_gradients(sign):
     """Chunks that grow by e^12 and hold no gradient: they are 0, not 0 times infinity."""
     t = inputs(1, 256, 2, 2, 64, 64, seed=26, restart=0)
     t["g"][:, 64:128, 0], t["g"][:, 192:256, 0] = 0.19, 0.19
     t["g"][:, 128:192, 0] -= 0.2
     t["dy"][:, 64:, 0], t["dfinal"][:, 0] = 0, 0
+    t["beta"][:, 64:, 0] *= sign
     g, ref = backward(cuda(t), grad_dtype=F32), reference_grads(t)
     check_grads(g, ref, F32, F32)
     assert not g["dv"][:, 64:, 0].any() and not g["dq"][:, 64:, 0].any()
@@ -207,3 +209,19 @@ def test_a_large_column_beside_others(big, onehot):
     others = [c for c in range(128) if c != 3]
     assert np.abs(to64(last) - last_ref)[:, :, others].max() < most * 2.0 ** -22
     assert np.abs(to64(y) - y_ref)[..., others].max() < most * 2.0 ** -22
+
+
+@pytest.mark.parametrize("n,h,groups,dk,dv", [(1000, 4, 4, 128, 128), (320, 6, 2, 64, 64), (150, 4, 2, 72, 200)])
+def test_what_the_header_says(n, h, groups, dk, dv):
+    """y and the state 1e-6; dq, dk and dbeta up to six operands rounded to one fp16 (N, R, U, z or S0,
+    L, W), each 2^-11 / sqrt(12) = 1.4e-4 in the mean: 3.5e-4, and a fifth more where roundings of one
+    tile add up in a column; dg a sum of such terms of which up to two thirds cancel."""
+    t = inputs(2, n, h, groups, dk, dv, seed=n + 1)
+    c = cuda(t)
+    y, last = forward(c, out_dtype=F32)
+    y_ref, last_ref = reference(t)
+    assert off(y, y_ref) < 1e-6 and off(last, last_ref) < 1e-6
+    g, ref = backward(c, grad_dtype=F32), reference_grads(t)
+    for name, tol in (("dv", 1e-6), ("dinitial_state", 1e-6), ("dq", 4.2e-4), ("dk", 4.2e-4), ("dbeta", 4.2e-4),
+                      ("dg", 1.2e-3)):
+        assert off(g[name], ref[name]) < tol, name
